@@ -377,6 +377,61 @@ MOE_API int moe_backward(const moe_config_t* cfg, const void* x, const void* W_g
                  float* dW_g, float* dbias, float* dW1, float* dW2, void* ws,
                  size_t ws_bytes, void* stream);
 
+/* ---- norms around a block -----------------------------------------------
+ * (No counterpart on the source pages: the expert layer's neighbours in a
+ * transformer block.) Root-mean-square norms before and after a block, fused
+ * with the block's gate and the residual scale. With rstd(v) = 1 /
+ * sqrt(mean(v^2) + eps) over a row's d values, b the block's output:
+ *   out = alpha x + beta g * (b rstd(b) w_post)    (post half)
+ *   n   = out rstd(out) w_pre                      (pre half: the next
+ *                                                   block's input)
+ * Either half may be left out: b = NULL leaves out the post half (out is x;
+ * alpha, beta and the gate are not used), w_pre = NULL the pre half. n is
+ * taken from the fp32 out, before its rounding; sums are fp32. A row whose
+ * sum of squares passes the fp32 range has rstd 0. */
+enum {
+  MOE_GATE_NONE = 0,    /* g = 1 */
+  MOE_GATE_TOKEN = 1,   /* gate [T] fp32 */
+  MOE_GATE_CHANNEL = 2, /* gate [d] fp32 */
+  MOE_GATE_ELEMENT = 3  /* gate [T, d] (dtype) */
+};
+
+typedef struct moe_norm_config {
+  int32_t T;     /* rows, >= 0 */
+  int32_t d;     /* row length, multiple of 64, at most 65536 */
+  int32_t dtype; /* MOE_DTYPE_*: x, b, out, n, dout, dx, db, an element gate */
+  int32_t gate;  /* MOE_GATE_* */
+  float eps;     /* finite, > 0 */
+  float alpha;   /* residual scale, finite */
+  float beta;    /* branch scale, finite */
+} moe_norm_config_t;
+
+/* x, b [T, d]; w_post, w_pre [d] fp32; gate as cfg->gate says. Outputs:
+ * out [T, d] (NULL without the post half), n [T, d] (NULL without the pre
+ * half), rstd_post, rstd_pre [T] fp32 (what the backward reads; nullable).
+ * Outputs may not overlap inputs or one another. Every tensor pointer but
+ * the [T] ones is 16-byte aligned. */
+MOE_API int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b,
+                   const float* w_post, const void* gate, const float* w_pre, void* out,
+                   void* n, float* rstd_post, float* rstd_pre, void* stream);
+
+/* Gradients of moe_block_norm's inputs, given dout [T, d] (the gradient that
+ * reaches out by other ways than n: the next residual's) and dn [T, d] fp32
+ * (moe_backward's dx; NULL without the pre half). y [T, d]: the forward's
+ * out (x without the post half); b, weights, gate and rstd_* as there.
+ * Outputs, overwritten: dx [T, d] (of x, through the residual), db [T, d],
+ * dw_post, dw_pre [d] fp32, dgate (gate's shape; fp32, or dtype for an
+ * element gate); those of a half left out, and dgate without a gate, are
+ * NULL. ws: >= moe_block_norm_backward_workspace_size bytes (0 for an
+ * invalid configuration), 256-byte aligned; no zeroing. Two kernels, no
+ * atomics: bitwise reproducible. T = 0 zeroes the weights' gradients. */
+MOE_API size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg);
+MOE_API int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout,
+                   const float* dn, const void* y, const void* b, const float* w_post,
+                   const void* gate, const float* w_pre, const float* rstd_post,
+                   const float* rstd_pre, void* dx, void* db, float* dw_post, void* dgate,
+                   float* dw_pre, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- errors --------------------------------------------------------------
  * moe_get_device_error synchronises `stream`, reads the workspace error
  * word, clears it, and returns MOE_OK, MOE_ERR_BAD_INDEX or MOE_ERR_TIMEOUT

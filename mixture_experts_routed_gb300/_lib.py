@@ -25,6 +25,10 @@ MOE_NUM_EVENTS = 8
 MOE_XPERM_AUTO = 0
 MOE_XPERM_PACKED = 1
 MOE_XPERM_GATHERED = 2
+MOE_GATE_NONE = 0
+MOE_GATE_TOKEN = 1
+MOE_GATE_CHANNEL = 2
+MOE_GATE_ELEMENT = 3
 
 
 class MoeConfig(ctypes.Structure):
@@ -36,6 +40,11 @@ class MoeConfig(ctypes.Structure):
                                              ("gemm_tile_n", ctypes.c_int32),
                                              ("x_perm_mode", ctypes.c_int32),
                                              ("keep_z", ctypes.c_int32)]
+
+
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "dtype", "gate")] + \
+               [(n, ctypes.c_float) for n in ("eps", "alpha", "beta")]
 
 
 class MoeForwardViews(ctypes.Structure):
@@ -77,6 +86,9 @@ PROTOTYPES = {
     "moe_backward_workspace_size": (_SZ, [_CFG]),
     "moe_backward": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P, _P,
                           _SZ, _P]),
+    "moe_block_norm": (_I, [_P] * 11),
+    "moe_block_norm_backward_workspace_size": (_SZ, [_P]),
+    "moe_block_norm_backward": (_I, [_P] * 16 + [_SZ, _P]),
 }
 
 _lib = None

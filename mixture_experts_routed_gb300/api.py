@@ -17,7 +17,8 @@ from . import _lib as L
 __all__ = ["MoEError", "make_config", "config_from", "workspace_size", "scratch_size",
            "alloc_workspace", "route", "dispatch", "expert_ffn", "combine", "forward",
            "forward_views", "get_device_error", "clear_device_error", "kernel_count",
-           "check_config", "backward", "backward_workspace_size"]
+           "check_config", "backward", "backward_workspace_size", "norm_config", "block_norm",
+           "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace"]
 
 
 class MoEError(RuntimeError):
@@ -27,12 +28,14 @@ class MoEError(RuntimeError):
         super().__init__(f"{what}: {msg} (status {status})" if what else msg)
 
 
+_DTYPES = {"f32": L.MOE_DTYPE_F32, "fp32": L.MOE_DTYPE_F32, "bf16": L.MOE_DTYPE_BF16,
+           torch.float32: L.MOE_DTYPE_F32, torch.bfloat16: L.MOE_DTYPE_BF16}
+
+
 def make_config(T, d, E, k, f, dtype="bf16", router=L.MOE_ROUTER_RENORM, pre_k=8,
                 payload_fp8=0, n_group=1, topk_group=1, payload_scale=0.0,
                 output_fp8=0, tau=1.0, gemm_tile_n=0, x_perm_mode=0, keep_z=0) -> L.MoeConfig:
-    dt = {"f32": L.MOE_DTYPE_F32, "fp32": L.MOE_DTYPE_F32, "bf16": L.MOE_DTYPE_BF16,
-          torch.float32: L.MOE_DTYPE_F32, torch.bfloat16: L.MOE_DTYPE_BF16}[dtype]
-    return L.MoeConfig(int(T), int(d), int(E), int(k), int(f), dt, int(router), int(pre_k),
+    return L.MoeConfig(int(T), int(d), int(E), int(k), int(f), _DTYPES[dtype], int(router), int(pre_k),
                        int(payload_fp8), int(n_group), int(topk_group), float(payload_scale),
                        int(output_fp8), float(tau), int(gemm_tile_n), int(x_perm_mode),
                        int(keep_z))
@@ -294,3 +297,96 @@ def get_device_error(ws, stream=None) -> int:
 
 def clear_device_error(ws, stream=None) -> None:
     _check(L.load().moe_clear_device_error(_p(ws), _s(stream)), "moe_clear_device_error")
+
+
+# ---------------------------------------------------------------- norms around a block
+_GATES = {"none": L.MOE_GATE_NONE, "token": L.MOE_GATE_TOKEN, "channel": L.MOE_GATE_CHANNEL,
+          "element": L.MOE_GATE_ELEMENT}
+
+
+def norm_config(T, d, dtype="bf16", gate="none", eps=1e-6, alpha=1.0, beta=1.0) -> L.MoeNormConfig:
+    """gate: "none", "token", "channel", "element" or a MOE_GATE_* value."""
+    return L.MoeNormConfig(int(T), int(d), _DTYPES[dtype], int(_GATES.get(gate, gate)),
+                           float(eps), float(alpha), float(beta))
+
+
+def _ndt(c):
+    return torch.float32 if c.dtype == L.MOE_DTYPE_F32 else torch.bfloat16
+
+
+def block_norm_workspace_size(c) -> int:
+    return int(L.load().moe_block_norm_backward_workspace_size(ctypes.byref(c)))
+
+
+def alloc_norm_workspace(c, device=None) -> torch.Tensor:
+    n = block_norm_workspace_size(c)
+    if n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "workspace size")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _shaped(name, t, shape, dtype):
+    """A tensor of the call's shape and type, or None."""
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {tuple(t.shape)} {t.dtype}, not "
+                                              f"{tuple(shape)} {dtype}")
+    return _p(t)
+
+
+def _gate_form(c):
+    return {L.MOE_GATE_TOKEN: ((c.T,), torch.float32), L.MOE_GATE_CHANNEL: ((c.d,), torch.float32),
+            L.MOE_GATE_ELEMENT: ((c.T, c.d), _ndt(c))}.get(c.gate)
+
+
+def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=None,
+               rstd_post=None, rstd_pre=None, want_rstd=False, stream=None) -> dict:
+    """out = alpha x + beta gate * norm(b) w_post and n = norm(out) w_pre; without ``b``
+    out is x, without ``w_pre`` there is no n. ``want_rstd``: keep the statistics the
+    backward reads."""
+    dt, td, f32 = _ndt(c), (c.T, c.d), torch.float32
+    post, pre = b is not None, w_pre is not None
+    if post and out is None:
+        out = torch.empty(td, dtype=dt, device=x.device)
+    if pre and n is None:
+        n = torch.empty(td, dtype=dt, device=x.device)
+    if want_rstd and post and rstd_post is None:
+        rstd_post = torch.empty(c.T, dtype=f32, device=x.device)
+    if want_rstd and pre and rstd_pre is None:
+        rstd_pre = torch.empty(c.T, dtype=f32, device=x.device)
+    form = _gate_form(c) if post else None
+    st = L.load().moe_block_norm(
+        ctypes.byref(c), _shaped("x", x, td, dt), _shaped("b", b, td, dt),
+        _shaped("w_post", w_post, (c.d,), f32),
+        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (c.d,), f32),
+        _shaped("out", out, td, dt), _shaped("n", n, td, dt),
+        _shaped("rstd_post", rstd_post, (c.T,), f32), _shaped("rstd_pre", rstd_pre, (c.T,), f32),
+        _s(stream))
+    _check(st, "moe_block_norm")
+    return {"out": out, "n": n, "rstd_post": rstd_post, "rstd_pre": rstd_pre}
+
+
+def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_pre, *, ws,
+                        stream=None) -> dict:
+    """Gradients after a ``block_norm`` of the same inputs: ``y`` is its out (x without
+    ``b``), ``dout`` the gradient that reaches y by the residual, ``dn`` (fp32) the one of
+    n. dx, db, an element gate's dgate in the config's type; dw_post, dw_pre and the other
+    dgate fp32; None for what the forward left out."""
+    dt, td, f32, dev = _ndt(c), (c.T, c.d), torch.float32, dout.device
+    post, pre = w_post is not None, w_pre is not None
+    form = _gate_form(c) if post else None
+
+    def new(on, shape, dtype):
+        return torch.empty(shape, dtype=dtype, device=dev) if on else None
+
+    g = {"dx": new(True, td, dt), "db": new(post, td, dt), "dw_post": new(post, (c.d,), f32),
+         "dgate": new(True, *form) if form else None, "dw_pre": new(pre, (c.d,), f32)}
+    st = L.load().moe_block_norm_backward(
+        ctypes.byref(c), _shaped("dout", dout, td, dt), _shaped("dn", dn, td, f32),
+        _shaped("y", y, td, dt), _shaped("b", b, td, dt), _shaped("w_post", w_post, (c.d,), f32),
+        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (c.d,), f32),
+        _shaped("rstd_post", rstd_post, (c.T,), f32) if post else None,
+        _shaped("rstd_pre", rstd_pre, (c.T,), f32) if pre else None, _p(g["dx"]), _p(g["db"]),
+        _p(g["dw_post"]), _p(g["dgate"]), _p(g["dw_pre"]), _p(ws),
+        ws.numel() * ws.element_size(), _s(stream))
+    _check(st, "moe_block_norm_backward")
+    return g

@@ -273,4 +273,22 @@ cudaError_t launch_gemm_simt(int epi, const float* A, int a_shared, int R, const
                              int K, int N, const int32_t* offsets, float* out, uint32_t* err,
                              cudaStream_t s, float* zout = nullptr);
 
+// ---------------------------------------------------------------- norm.cu
+// Up to this many rows take the widest row groups (one wave of the SMs).
+constexpr int kNormFewRows = 152;
+// The norms around a block (b null: no post half; w_pre null: no pre half);
+// gate_kind as MOE_GATE_*.
+cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, float beta, int T,
+                              int d, const void* x, const void* b, const float* w_post,
+                              const void* gate, const float* w_pre, void* out, void* n,
+                              float* rstd_post, float* rstd_pre, int num_sms, cudaStream_t s);
+// Bytes of `part` the backward's column sums take.
+size_t block_norm_bwd_ws(int dtype, int T, int d);
+cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
+                                  int T, int d, const void* dout, const float* dn, const void* yo,
+                                  const void* b, const float* w_post, const void* gate,
+                                  const float* w_pre, const float* rstd_post,
+                                  const float* rstd_pre, void* dx, void* db, float* dw_post,
+                                  void* dgate, float* dw_pre, float* part, cudaStream_t s);
+
 }  // namespace moe

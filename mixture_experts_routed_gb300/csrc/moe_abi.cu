@@ -3,6 +3,7 @@
 // allocates, frees or synchronises (except moe_get_device_error).
 #include <cfloat>
 #include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 
@@ -538,6 +539,28 @@ int backward_impl(const moe_config_t* cfg, const void* x, const void* Wg, const 
   return status_of(e);
 }
 
+// ---------------------------------------------------------------- block norms
+int check_norm(const moe_norm_config_t* c) {
+  if (c == nullptr || c->T < 0 || c->d <= 0 || c->d % 64 != 0) return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->gate < MOE_GATE_NONE || c->gate > MOE_GATE_ELEMENT) return MOE_ERR_INVALID_ARG;
+  if (!(c->eps > 0.f && c->eps <= FLT_MAX) || !(fabsf(c->alpha) <= FLT_MAX) ||
+      !(fabsf(c->beta) <= FLT_MAX))
+    return MOE_ERR_INVALID_ARG;
+  return c->d > 65536 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+// The halves' tensors go together.
+bool norm_args_ok(const moe_norm_config_t& c, const void* x, const void* b, const float* w_post,
+                  const void* gate, const float* w_pre) {
+  if (b == nullptr && w_pre == nullptr) return false;
+  if ((b == nullptr) != (w_post == nullptr)) return false;
+  if (!ok_ptr(x) || (b != nullptr && (!ok_ptr(b) || !ok_ptr(w_post)))) return false;
+  if (w_pre != nullptr && !ok_ptr(w_pre)) return false;
+  if (b == nullptr || c.gate == MOE_GATE_NONE) return true;
+  return gate != nullptr && aligned(gate, c.gate == MOE_GATE_TOKEN ? 4 : 16);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -733,6 +756,60 @@ int moe_backward(const moe_config_t* cfg, const void* x, const void* W_g, const 
                  float* dW1, float* dW2, void* ws, size_t ws_bytes, void* stream) {
   return backward_impl(cfg, x, W_g, bias, noise, W1, W2, fwd_ws, fwd_ws_bytes, dout, dx, dW_g,
                        dbias, dW1, dW2, ws, ws_bytes, stream);
+}
+
+int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b, const float* w_post,
+                   const void* gate, const float* w_pre, void* out, void* n, float* rstd_post,
+                   float* rstd_pre, void* stream) {
+  const int st = check_norm(cfg);
+  if (st != MOE_OK) return st;
+  const moe_norm_config_t& c = *cfg;
+  if (c.T == 0) return MOE_OK;
+  if (!norm_args_ok(c, x, b, w_post, gate, w_pre) || (b != nullptr ? !ok_ptr(out) : out != nullptr) ||
+      (w_pre != nullptr ? !ok_ptr(n) : n != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_block_norm(c.dtype, c.gate, c.eps, c.alpha, c.beta, c.T, c.d, x, b,
+                                     w_post, gate, w_pre, out, n, rstd_post, rstd_pre, sms,
+                                     as_stream(stream)));
+}
+
+size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg) {
+  if (check_norm(cfg) != MOE_OK) return 0;
+  return align_up(block_norm_bwd_ws(cfg->dtype, cfg->T > 0 ? cfg->T : 1, cfg->d), kAlign);
+}
+
+int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, const float* dn,
+                            const void* y, const void* b, const float* w_post, const void* gate,
+                            const float* w_pre, const float* rstd_post, const float* rstd_pre,
+                            void* dx, void* db, float* dw_post, void* dgate, float* dw_pre,
+                            void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_norm(cfg);
+  if (st != MOE_OK) return st;
+  const moe_norm_config_t& c = *cfg;
+  const bool post = b != nullptr || w_post != nullptr, pre = w_pre != nullptr;
+  const bool gated = post && c.gate != MOE_GATE_NONE;
+  if (ws == nullptr || !aligned(ws, kAlign) || (!post && !pre)) return MOE_ERR_INVALID_ARG;
+  if ((pre ? !ok_ptr(dw_pre) : dw_pre != nullptr) || (post ? !ok_ptr(dw_post) : dw_post != nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (gated ? (dgate == nullptr || !aligned(dgate, c.gate == MOE_GATE_TOKEN ? 4 : 16))
+            : dgate != nullptr)
+    return MOE_ERR_INVALID_ARG;
+  if (c.T > 0) {
+    if (!norm_args_ok(c, y, b, w_post, gate, w_pre) || !ok_ptr(dout) || !ok_ptr(dx))
+      return MOE_ERR_INVALID_ARG;
+    if ((pre ? !ok_ptr(dn) || rstd_pre == nullptr : dn != nullptr) ||
+        (post ? !ok_ptr(db) || rstd_post == nullptr : db != nullptr))
+      return MOE_ERR_INVALID_ARG;
+  }
+  if (ws_bytes < moe_block_norm_backward_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  // (with no rows b may be null: what is left out goes by the weights)
+  const void* bp = post && b == nullptr ? static_cast<const void*>(w_post) : b;
+  return status_of(launch_block_norm_bwd(c.dtype, c.gate, c.eps, c.alpha, c.beta, c.T, c.d, dout,
+                                         dn, y, bp, w_post, gate, w_pre, rstd_post, rstd_pre, dx,
+                                         db, dw_post, dgate, dw_pre, static_cast<float*>(ws),
+                                         as_stream(stream)));
 }
 
 int moe_forward_kernel_count(const moe_config_t* cfg) {

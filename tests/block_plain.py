@@ -1,0 +1,83 @@
+"""Plain 64-bit forms of the operators around the expert layer, on the CPU, each with the sum
+of absolute terms its rounding errors scale with."""
+import torch
+
+F64 = torch.float64
+U32 = 2.0 ** -24  # half a step of fp32, relative
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def norm_forward(x, b, w_post, gate, w_pre, kind, eps, alpha, beta):
+    """dict of (value, absolute terms)."""
+    r = {}
+    y, ay = x, x.abs()
+    if b is not None:
+        rb = 1 / torch.sqrt((b * b).mean(1, keepdim=True) + eps)
+        g = 1.0 if kind == "none" else (gate[:, None] if kind == "token" else gate)
+        branch = beta * g * (b * rb * w_post)
+        ay = (alpha * x).abs() + branch.abs()
+        y = alpha * x + branch
+        r["out"] = (y, ay)
+        r["rstd_post"] = (rb[:, 0], rb[:, 0])
+    if w_pre is not None:
+        ro = 1 / torch.sqrt((y * y).mean(1, keepdim=True) + eps)
+        r["rstd_pre"] = (ro[:, 0], ro[:, 0])
+        # a relative error e of rstd and the errors of y both reach n
+        r["n"] = (y * ro * w_pre, (ay * ro * w_pre).abs()
+                  + (y * ro * w_pre).abs() * (ay * ay).mean(1, keepdim=True) * ro * ro)
+    return r
+
+
+def norm_backward(dout, dn, y, b, w_post, gate, w_pre, rb, ro, kind, alpha, beta):
+    """Of (dx, db, dw_post, dgate, dw_pre): (value, absolute terms); rb, ro [T] as kept."""
+    r = {}
+    D, aD = dout, dout.abs()
+    if w_pre is not None:
+        yh, v = y * ro[:, None], dn * w_pre
+        r["dw_pre"] = ((dn * yh).sum(0), (dn * yh).abs().sum(0))
+        D = D + ro[:, None] * (v - yh * (v * yh).mean(1, keepdim=True))
+        aD = aD + ro[:, None] * (v.abs() + yh.abs() * (v * yh).abs().mean(1, keepdim=True))
+    if b is None:
+        r["dx"] = (D, aD)
+        return r
+    r["dx"] = (alpha * D, abs(alpha) * aD)
+    G, aG = beta * D, abs(beta) * aD
+    bh = b * rb[:, None]
+    u = bh * w_post
+    if kind == "token":
+        r["dgate"] = ((G * u).sum(1), (aG * u.abs()).sum(1))
+    elif kind == "channel":
+        r["dgate"] = ((G * u).sum(0), (aG * u.abs()).sum(0))
+    elif kind == "element":
+        r["dgate"] = (G * u, aG * u.abs())
+    g = 1.0 if kind == "none" else (gate[:, None] if kind == "token" else gate)
+    G = G * g
+    aG = aG * abs(g)
+    r["dw_post"] = ((G * bh).sum(0), (aG * bh.abs()).sum(0))
+    v, av = G * w_post, aG * w_post.abs()
+    r["db"] = (rb[:, None] * (v - bh * (v * bh).mean(1, keepdim=True)),
+               rb[:, None] * (av + bh.abs() * (av * bh.abs()).mean(1, keepdim=True)))
+    return r
+
+
+def norm_problem(T, d, dtype, kind, post, pre, seed, device="cpu"):
+    """Inputs of a norm call (fp32 draws on the CPU, rounded to dtype where the call takes it)."""
+    g = torch.Generator().manual_seed(seed)
+
+    def draw(*shape):
+        return torch.randn(shape, generator=g)
+
+    i = {"x": (1.5 * draw(T, d)).to(dtype), "b": (0.7 * draw(T, d)).to(dtype),
+         "w_post": 1 + 0.2 * draw(d), "w_pre": 1 + 0.2 * draw(d), "gate": None,
+         "dout": draw(T, d).to(dtype), "dn": draw(T, d)}
+    if kind != "none":
+        v = torch.sigmoid(draw(*{"token": (T,), "channel": (d,), "element": (T, d)}[kind]))
+        i["gate"] = v.to(dtype) if kind == "element" else v
+    if not post:
+        i["b"] = i["w_post"] = i["gate"] = None
+    if not pre:
+        i["w_pre"] = i["dn"] = None
+    return {k: None if v is None else v.to(device) for k, v in i.items()}

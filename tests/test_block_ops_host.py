@@ -1,0 +1,107 @@
+"""Refusals of the operators around the expert layer: status codes found on the host, before
+any CUDA call (no GPU needed)."""
+import ctypes
+
+import pytest
+
+from mixture_experts_routed_gb300 import _lib as L
+from mixture_experts_routed_gb300 import build as B
+
+P = ctypes.c_void_p(4096)    # aligned, never read: every call here is refused first
+ODD = ctypes.c_void_p(4100)  # 4-byte aligned only
+
+
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return L.load()
+
+
+def norm(**kw):
+    base = dict(T=8, d=128, dtype=1, gate=0, eps=1e-6, alpha=1.0, beta=1.0)
+    base.update(kw)
+    return L.MoeNormConfig(*[base[n] for n, _ in L.MoeNormConfig._fields_])
+
+
+def norm_forward(lib, c, x=P, b=P, w_post=P, gate=None, w_pre=P, out=P, n=P):
+    return lib.moe_block_norm(ctypes.byref(c), x, b, w_post, gate, w_pre, out, n, None, None, None)
+
+
+def norm_backward(lib, c, dout=P, dn=P, y=P, b=P, w_post=P, gate=None, w_pre=P, rb=P, ro=P, dx=P,
+                  db=P, dw_post=P, dgate=None, dw_pre=P, ws=P, ws_bytes=1 << 40):
+    return lib.moe_block_norm_backward(ctypes.byref(c), dout, dn, y, b, w_post, gate, w_pre, rb, ro,
+                                       dx, db, dw_post, dgate, dw_pre, ws, ws_bytes, None)
+
+
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), L.MOE_ERR_INVALID_ARG), (dict(d=0), L.MOE_ERR_INVALID_ARG),
+    (dict(d=96), L.MOE_ERR_INVALID_ARG), (dict(dtype=2), L.MOE_ERR_INVALID_ARG),
+    (dict(gate=-1), L.MOE_ERR_INVALID_ARG), (dict(gate=4), L.MOE_ERR_INVALID_ARG),
+    (dict(eps=0.0), L.MOE_ERR_INVALID_ARG), (dict(eps=NAN), L.MOE_ERR_INVALID_ARG),
+    (dict(eps=INF), L.MOE_ERR_INVALID_ARG), (dict(alpha=NAN), L.MOE_ERR_INVALID_ARG),
+    (dict(alpha=INF), L.MOE_ERR_INVALID_ARG), (dict(beta=-INF), L.MOE_ERR_INVALID_ARG),
+    (dict(d=65600), L.MOE_ERR_UNSUPPORTED)])
+def test_norm_configs(lib, kw, status):
+    c = norm(**kw)
+    assert norm_forward(lib, c) == status
+    assert norm_backward(lib, c) == status
+    assert lib.moe_block_norm_backward_workspace_size(ctypes.byref(c)) == 0
+
+
+def test_norm_null_config(lib):
+    assert lib.moe_block_norm(None, *[P] * 9, None) == L.MOE_ERR_INVALID_ARG
+    assert lib.moe_block_norm_backward_workspace_size(None) == 0
+
+
+@pytest.mark.parametrize("gate,kw", [
+    (0, dict(x=None)), (0, dict(x=ODD)), (0, dict(b=ODD)), (0, dict(w_post=None)),
+    (0, dict(w_post=ODD)), (0, dict(b=None)), (0, dict(w_pre=ODD)), (0, dict(out=None)),
+    (0, dict(out=ODD)), (0, dict(n=None)), (0, dict(n=ODD)), (0, dict(w_pre=None)),
+    (0, dict(b=None, w_post=None)), (0, dict(b=None, w_post=None, out=None, w_pre=None, n=None)),
+    (1, dict()), (2, dict()), (2, dict(gate=ODD)), (3, dict(gate=ODD)),
+    (1, dict(gate=ctypes.c_void_p(4098)))])
+def test_norm_forward_arguments(lib, gate, kw):
+    assert norm_forward(lib, norm(gate=gate), **kw) == L.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("gate,kw", [
+    (0, dict(dout=None)), (0, dict(dout=ODD)), (0, dict(dn=None)), (0, dict(dn=ODD)),
+    (0, dict(y=None)), (0, dict(y=ODD)), (0, dict(b=None)), (0, dict(b=ODD)),
+    (0, dict(w_post=None)), (0, dict(w_pre=None)), (0, dict(rb=None)), (0, dict(ro=None)),
+    (0, dict(dx=None)), (0, dict(dx=ODD)), (0, dict(db=None)), (0, dict(db=ODD)),
+    (0, dict(dw_post=None)), (0, dict(dw_pre=None)), (0, dict(dw_pre=ODD)), (0, dict(dgate=P)),
+    (1, dict(gate=P)), (2, dict(gate=P, dgate=ODD)), (3, dict(dgate=P)), (0, dict(ws=None)),
+    (0, dict(ws=ctypes.c_void_p(4096 + 128))),
+    (0, dict(b=None, w_post=None, db=None, dw_post=None, w_pre=None, dn=None, dw_pre=None))])
+def test_norm_backward_arguments(lib, gate, kw):
+    assert norm_backward(lib, norm(gate=gate), **kw) == L.MOE_ERR_INVALID_ARG
+
+
+def test_norm_backward_workspace(lib):
+    c = norm()
+    need = lib.moe_block_norm_backward_workspace_size(ctypes.byref(c))
+    assert need > 0 and need % 256 == 0
+    assert norm_backward(lib, c, ws_bytes=need - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_norm_config_matches_the_header():
+    from test_abi_host import struct_fields
+    fields = struct_fields("moe_norm_config")
+    ctypes_of = {"int32_t": ctypes.c_int32, "float": ctypes.c_float}
+    assert [(n, ctypes_of[t]) for n, t in fields] == list(L.MoeNormConfig._fields_)
+
+
+def test_norm_binding_refuses_wrong_shapes_and_types():
+    import torch
+    import mixture_experts_routed_gb300 as moe
+    B.build()
+    c = moe.norm_config(4, 64, "bf16")
+    w = torch.ones(64)
+    for x in (torch.zeros((4, 128), dtype=torch.bfloat16), torch.zeros((4, 64))):
+        with pytest.raises(moe.MoEError, match="not"):
+            moe.block_norm(c, x, w_pre=w)
+    with pytest.raises(moe.MoEError, match="not contiguous"):
+        moe.block_norm(c, torch.zeros((64, 4), dtype=torch.bfloat16).t(), w_pre=w)
