@@ -305,6 +305,25 @@ MOE_API int moe_forward(const moe_config_t* cfg, const void* x, const void* W_g,
                 const float* bias, const float* noise, const void* W1, const void* W2,
                 void* out, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- whole layer for a few tokens ------------------------------------------
+ * moe_forward's layer for at most MOE_FEW_MAX_TOKENS tokens (a decode step),
+ * gate to combine in one kernel: the routing rules of moe_route, the experts
+ * as in moe_expert_ffn, the weighted sum as in moe_combine, with every sum
+ * in fp32 and h carried as two bf16 parts, so only out is rounded to bf16
+ * (moe_forward rounds h too, and adds in another order). bf16 layers without
+ * payloads (payload_fp8, output_fp8) or keep_z, T <= MOE_FEW_MAX_TOKENS;
+ * else MOE_ERR_UNSUPPORTED. gemm_tile_n and x_perm_mode have no effect.
+ * Arguments as moe_forward. ws: >= moe_forward_few_workspace_size bytes (0
+ * for a configuration it refuses), 256-byte aligned, zeroed once before its
+ * first use; calls that share one must not overlap. No atomics on values:
+ * bitwise reproducible. The kernel's blocks wait on one another (a
+ * cooperative launch, one block per SM). It can be captured into a graph. */
+#define MOE_FEW_MAX_TOKENS 32
+MOE_API size_t moe_forward_few_workspace_size(const moe_config_t* cfg);
+MOE_API int moe_forward_few(const moe_config_t* cfg, const void* x, const void* W_g,
+                const float* bias, const float* noise, const void* W1, const void* W2,
+                void* out, void* ws, size_t ws_bytes, void* stream);
+
 /* (No counterpart on the source pages: timing instrumentation.)
  * moe_forward that also records CUDA events (cudaEvent_t, passed as void*)
  * at the kernel boundaries, for per-kernel timing on the launching stream:

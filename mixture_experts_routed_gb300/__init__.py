@@ -11,6 +11,7 @@ from .api import (  # noqa: F401
     dispatch, expert_ffn, combine, quantize_output, combine_fp8, forward, forward_views,
     get_device_error,
     clear_device_error, kernel_count, check_config, backward, backward_workspace_size,
+    forward_few, few_workspace_size,
     norm_config, block_norm, block_norm_backward, block_norm_workspace_size, alloc_norm_workspace,
 )
 from ._lib import (  # noqa: F401
@@ -18,5 +19,5 @@ from ._lib import (  # noqa: F401
     MOE_ERR_LAUNCH, MOE_ERR_BAD_INDEX, MOE_ERR_TIMEOUT, MOE_DTYPE_F32, MOE_DTYPE_BF16,
     MOE_ROUTER_RENORM, MOE_ROUTER_PREK_SOFTMAX, MOE_ROUTER_GROUP_LIMITED,
     MOE_ROUTER_SOFT_GUMBEL, MOE_NUM_EVENTS, MOE_XPERM_AUTO, MOE_XPERM_PACKED, MOE_XPERM_GATHERED,
-    MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_ELEMENT,
+    MOE_FEW_MAX_TOKENS, MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL, MOE_GATE_ELEMENT,
 )

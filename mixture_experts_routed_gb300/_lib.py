@@ -25,6 +25,7 @@ MOE_NUM_EVENTS = 8
 MOE_XPERM_AUTO = 0
 MOE_XPERM_PACKED = 1
 MOE_XPERM_GATHERED = 2
+MOE_FEW_MAX_TOKENS = 32
 MOE_GATE_NONE = 0
 MOE_GATE_TOKEN = 1
 MOE_GATE_CHANNEL = 2
@@ -86,6 +87,8 @@ PROTOTYPES = {
     "moe_backward_workspace_size": (_SZ, [_CFG]),
     "moe_backward": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P, _P, _P,
                           _SZ, _P]),
+    "moe_forward_few_workspace_size": (_SZ, [_CFG]),
+    "moe_forward_few": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_block_norm": (_I, [_P] * 11),
     "moe_block_norm_backward_workspace_size": (_SZ, [_P]),
     "moe_block_norm_backward": (_I, [_P] * 16 + [_SZ, _P]),

@@ -17,7 +17,8 @@ from . import _lib as L
 __all__ = ["MoEError", "make_config", "config_from", "workspace_size", "scratch_size",
            "alloc_workspace", "route", "dispatch", "expert_ffn", "combine", "forward",
            "forward_views", "get_device_error", "clear_device_error", "kernel_count",
-           "check_config", "backward", "backward_workspace_size", "norm_config", "block_norm",
+           "check_config", "backward", "backward_workspace_size", "forward_few",
+           "few_workspace_size", "norm_config", "block_norm",
            "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace"]
 
 
@@ -105,11 +106,15 @@ def backward_workspace_size(c) -> int:
     return int(L.load().moe_backward_workspace_size(_cfg(c)))
 
 
+def few_workspace_size(c) -> int:
+    return int(L.load().moe_forward_few_workspace_size(_cfg(c)))
+
+
 def alloc_workspace(c, kind: str = "forward", device=None) -> torch.Tensor:
     """Zeroed workspace (so the device error word starts clear); kind is
-    "forward", "scratch" or "backward"."""
+    "forward", "scratch", "backward" or "few"."""
     n = {"forward": workspace_size, "scratch": scratch_size,
-         "backward": backward_workspace_size}[kind](c)
+         "backward": backward_workspace_size, "few": few_workspace_size}[kind](c)
     if n == 0:
         raise MoEError(L.MOE_ERR_INVALID_ARG, "workspace size")
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
@@ -232,6 +237,19 @@ def forward(c, x, Wg, bias, W1, W2, *, ws, out=None, events=None, noise=None, st
                                          _p(W1), _p(W2), _p(out), _p(ws), nbytes, arr,
                                          len(events), _s(stream))
     _check(st, "moe_forward")
+    return out
+
+
+def forward_few(c, x, Wg, bias, W1, W2, *, ws, out=None, noise=None, stream=None):
+    """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one kernel. ``ws``: a
+    "few" workspace."""
+    cc = config_from(c)
+    if out is None:
+        out = torch.empty((cc.T, cc.d), dtype=torch.bfloat16, device=x.device)
+    st = L.load().moe_forward_few(ctypes.byref(cc), _p(x), _p(Wg), _p(bias), _p(noise), _p(W1),
+                                  _p(W2), _p(out), _p(ws), ws.numel() * ws.element_size(),
+                                  _s(stream))
+    _check(st, "moe_forward_few")
     return out
 
 

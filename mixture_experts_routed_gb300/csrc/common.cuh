@@ -291,4 +291,19 @@ cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alp
                                   const float* rstd_pre, void* dx, void* db, float* dw_post,
                                   void* dgate, float* dw_pre, float* part, cudaStream_t s);
 
+// ---------------------------------------------------------------- few.cu
+// The whole layer for a few tokens (T <= kFewMaxTokens, bf16) in one
+// cooperative kernel. Its four counters live in the workspace's first block
+// at kFewSyncOffset and are zero between launches.
+constexpr int kFewMaxTokens = 32;
+constexpr int kFewMaxCtas = 160;  // the grid the partial sums are sized for
+constexpr size_t kFewSyncOffset = 128;
+struct FewLayout {
+  size_t idx, w, gpart, tiles, ntiles, h, h_rows, part, total;
+};
+FewLayout few_layout(int T, int d, int E, int k, int f);
+cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const void* W1,
+                       const void* W2, int T, int d, int E, int f, RouterSpec rs, void* out,
+                       void* ws, int num_sms, cudaStream_t s);
+
 }  // namespace moe

@@ -539,6 +539,18 @@ int backward_impl(const moe_config_t* cfg, const void* x, const void* Wg, const 
   return status_of(e);
 }
 
+// ---------------------------------------------------------------- few tokens
+static_assert(kFewMaxTokens == MOE_FEW_MAX_TOKENS, "the header's limit");
+
+int check_few(const moe_config_t* c) {
+  const int st = check_cfg(c);
+  if (st != MOE_OK) return st;
+  if (c->dtype != MOE_DTYPE_BF16 || c->payload_fp8 || c->output_fp8 || c->keep_z ||
+      c->T > kFewMaxTokens)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
 // ---------------------------------------------------------------- block norms
 int check_norm(const moe_norm_config_t* c) {
   if (c == nullptr || c->T < 0 || c->d <= 0 || c->d % 64 != 0) return MOE_ERR_INVALID_ARG;
@@ -756,6 +768,30 @@ int moe_backward(const moe_config_t* cfg, const void* x, const void* W_g, const 
                  float* dW1, float* dW2, void* ws, size_t ws_bytes, void* stream) {
   return backward_impl(cfg, x, W_g, bias, noise, W1, W2, fwd_ws, fwd_ws_bytes, dout, dx, dW_g,
                        dbias, dW1, dW2, ws, ws_bytes, stream);
+}
+
+size_t moe_forward_few_workspace_size(const moe_config_t* cfg) {
+  if (check_few(cfg) != MOE_OK) return 0;
+  return few_layout(cfg->T, cfg->d, cfg->E, cfg->k, cfg->f).total;
+}
+
+int moe_forward_few(const moe_config_t* cfg, const void* x, const void* W_g, const float* bias,
+                    const float* noise, const void* W1, const void* W2, void* out, void* ws,
+                    size_t ws_bytes, void* stream) {
+  const int st = check_few(cfg);
+  if (st != MOE_OK) return st;
+  const moe_config_t& c = *cfg;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (c.T > 0 && (!ok_ptr(x) || W_g == nullptr || !ok_ptr(W1) || !ok_ptr(W2) || !ok_ptr(out) ||
+                  (soft(c) && noise == nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_forward_few_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.T == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  const RouterSpec rs{c.k, c.pre_k, c.router, c.n_group, c.topk_group, c.tau, noise};
+  return status_of(launch_few(x, W_g, bias, W1, W2, c.T, c.d, c.E, c.f, rs, out, ws, sms,
+                              as_stream(stream)));
 }
 
 int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b, const float* w_post,

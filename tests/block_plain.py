@@ -81,3 +81,54 @@ def norm_problem(T, d, dtype, kind, post, pre, seed, device="cpu"):
     if not pre:
         i["w_pre"] = i["dn"] = None
     return {k: None if v is None else v.to(device) for k, v in i.items()}
+
+
+# ---------------------------------------------------------------- the layer for a few tokens
+def choose(L, router, k, pre_k, n_group, topk_group, noise=None, tau=1.0):
+    """ids [T, k] and weights of 64-bit logits, and each token's distance to another choice."""
+    T, E = L.shape
+    if router == 3:
+        w = torch.softmax((L + noise) / tau, 1)
+        return torch.arange(E, device=L.device).expand(T, E), w, torch.full((T,), 1.0)
+    gap = torch.full((T,), float("inf"), dtype=F64, device=L.device)
+    if router == 2:
+        score = torch.softmax(L, 1).view(T, n_group, -1).sum(2)
+        s, order = torch.sort(score, dim=1, descending=True, stable=True)
+        keep = torch.zeros_like(score, dtype=torch.bool).scatter_(1, order[:, :topk_group], True)
+        if topk_group < n_group:
+            gap = (s[:, topk_group - 1] - s[:, topk_group]) / s[:, 0]
+        L = L.masked_fill(~keep.repeat_interleave(E // n_group, 1), -float("inf"))
+    v, i = torch.sort(L, dim=1, descending=True, stable=True)
+    if k < E:
+        gap = torch.minimum(gap, (v[:, k - 1] - v[:, k]).abs())
+    if k > 1:
+        gap = torch.minimum(gap, (v[:, :k - 1] - v[:, 1:k]).min(1).values)
+    ex = torch.exp(v[:, :pre_k if router == 1 else k] - v[:, :1])
+    return i[:, :k], ex[:, :k] / ex.sum(1, keepdim=True), gap.cpu()
+
+
+def few_layer(c, i):
+    """(out, its tolerance without the last rounding, gap) of the layer: c a config, i its
+    inputs. Sums of n products on the tensor cores add 16 at a time in fp32: n / 8 + 64 half
+    steps of the absolute terms cover the additions and the joining of partial sums; h is
+    carried to 2^-17; the logits' errors reach the routing weights twice."""
+    x = i["x"].to(F64)
+    Wg = i["Wg"].to(F64)
+    noise = i.get("gumbel")
+    L = x @ Wg + i["bias"].to(F64)
+    idx, w, gap = choose(L, c.router, c.k, c.pre_k, c.n_group, c.topk_group,
+                         None if noise is None else noise.to(F64), c.tau)
+    e_l = ((c.d / 64 + 128) * U32 * (x.abs() @ Wg.abs()).max(1).values / c.tau)[:, None]
+    c1, c2 = (c.d / 8 + 64) * U32, (c.f / 8 + 64) * U32
+    out, tol = torch.zeros_like(x), torch.zeros_like(x)
+    for e in sorted(set(idx.flatten().tolist())):
+        t, j = (idx == e).nonzero(as_tuple=True)
+        W1, W2 = i["W1"][e].to(F64), i["W2"][e].to(F64)
+        z = x[t] @ W1
+        h = z * torch.sigmoid(z)
+        dh = 1.1 * c1 * (x[t].abs() @ W1.abs()) + (2.0 ** -17 + 8 * U32) * h.abs()
+        y, ya = h @ W2, h.abs() @ W2.abs()
+        we = w[t, j][:, None]
+        out[t] += we * y
+        tol[t] += we * (c2 * ya + dh @ W2.abs() + (2 * e_l[t] + 64 * U32) * y.abs())
+    return out, tol, gap

@@ -105,3 +105,44 @@ def test_norm_binding_refuses_wrong_shapes_and_types():
             moe.block_norm(c, x, w_pre=w)
     with pytest.raises(moe.MoEError, match="not contiguous"):
         moe.block_norm(c, torch.zeros((64, 4), dtype=torch.bfloat16).t(), w_pre=w)
+
+
+def moe_cfg(**kw):
+    from test_abi_host import cfg
+    return cfg(**{"T": 8, **kw})
+
+
+def few(lib, c, x=P, Wg=P, noise=None, W1=P, W2=P, out=P, ws=P, ws_bytes=1 << 40):
+    return lib.moe_forward_few(ctypes.byref(c), x, Wg, None, noise, W1, W2, out, ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), L.MOE_ERR_INVALID_ARG), (dict(d=100), L.MOE_ERR_INVALID_ARG),
+    (dict(k=9), L.MOE_ERR_INVALID_ARG), (dict(T=33), L.MOE_ERR_UNSUPPORTED),
+    (dict(dtype=0), L.MOE_ERR_UNSUPPORTED), (dict(payload_fp8=1), L.MOE_ERR_UNSUPPORTED),
+    (dict(output_fp8=1), L.MOE_ERR_UNSUPPORTED), (dict(keep_z=1), L.MOE_ERR_UNSUPPORTED)])
+def test_few_configs(lib, kw, status):
+    c = moe_cfg(**kw)
+    assert few(lib, c) == status
+    assert lib.moe_forward_few_workspace_size(ctypes.byref(c)) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(x=None), dict(x=ODD), dict(Wg=None), dict(W1=None), dict(W1=ODD), dict(W2=None),
+    dict(W2=ODD), dict(out=None), dict(out=ODD), dict(ws=None),
+    dict(ws=ctypes.c_void_p(4096 + 128))])
+def test_few_arguments(lib, kw):
+    assert few(lib, moe_cfg(), **kw) == L.MOE_ERR_INVALID_ARG
+
+
+def test_few_soft_gating_wants_its_samples(lib):
+    assert few(lib, moe_cfg(router=3, E=8, k=8, tau=1.0)) == L.MOE_ERR_INVALID_ARG
+
+
+def test_few_workspace(lib):
+    assert L.MOE_FEW_MAX_TOKENS == 32
+    for kw in (dict(T=1), dict(T=32, E=256, k=8, d=7168, f=2048), dict(T=0)):
+        c = moe_cfg(**kw)
+        need = lib.moe_forward_few_workspace_size(ctypes.byref(c))
+        assert need > 0 and need % 256 == 0
+        assert few(lib, c, ws_bytes=need - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
