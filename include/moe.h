@@ -451,6 +451,69 @@ MOE_API int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* do
                    const float* rstd_pre, void* dx, void* db, float* dw_post, void* dgate,
                    float* dw_pre, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- microscaled 4-bit expert products --------------------------------------
+ * (No counterpart on the source pages, whose payloads stop at 8 bits.) The
+ * expert products of moe_expert_ffn with both operands in 4 bits: OCP
+ * microscaling, MXFP4. Blocks of 32 values along the contraction share one
+ * power-of-two scale, a byte s (E8M0: 2^(s - 127)); each value is E2M1:
+ *   s - 127 = max(floor(log2(amax)) - 2, -127); s = 127 for a block of zeros,
+ *   255 (which stands for NaN) for a block with an infinity or a NaN;
+ *   code = E2M1(v / 2^(s - 127)), to nearest even, saturating at +-6.
+ * Codes lie two to a byte, the even k in the low half: rows [R, K / 2],
+ * weights [E, N, K / 2] (transposed: k innermost). Scales lie as the tensor
+ * cores read them, in chunks of 128 rows (or columns n) x 4 blocks, 512
+ * bytes: row i, block j at (i % 32) * 16 + (i / 32) * 4 + j. Weights:
+ * [E][ceil(N / 128)][ceil(K / 128)] chunks. Rows: [tile][ceil(K / 128)]
+ * chunks, where the tiles are each expert's segment cut into 128 rows, one
+ * expert after the other, so they go with the offsets they were made for.
+ * Every code and scale pointer is 16-byte aligned. */
+typedef struct moe_mx4_config {
+  int32_t R;         /* routed rows, 0..2^24 */
+  int32_t K;         /* contraction, multiple of 64, at most 65536 */
+  int32_t N;         /* output features, multiple of 64, at most 65536 */
+  int32_t E;         /* experts, 1..256 (1: a plain linear layer, offsets {0, R}) */
+  int32_t dtype;     /* MOE_DTYPE_*: x, W and what the dequantisers write */
+  int32_t out_dtype; /* MOE_DTYPE_*: the product's output */
+  int32_t silu;      /* 1: the product ends in SiLU (the W1 pass); else 0 */
+  int32_t x_rows;    /* rows of x where quantised rows are gathered, >= 0 */
+} moe_mx4_config_t;
+
+/* Sizes in bytes (0 for an invalid configuration): the rows' scales, the
+ * weights' scales, and the workspace of the two calls that take one (an
+ * error word and the product's split sums; zero it once before first use). */
+MOE_API size_t moe_mx4_row_scale_size(const moe_mx4_config_t* cfg);
+MOE_API size_t moe_mx4_weight_scale_size(const moe_mx4_config_t* cfg);
+MOE_API size_t moe_mx4_workspace_size(const moe_mx4_config_t* cfg);
+
+/* Expert weights W [E, K, N] (dtype) -> wq [E, N, K / 2], w_scale; done once
+ * where the weights are loaded. */
+MOE_API int moe_mx4_quantize_weights(const moe_mx4_config_t* cfg, const void* W, uint8_t* wq,
+                   uint8_t* w_scale, void* stream);
+
+/* Rows of x (dtype) -> q [R, K / 2], scale: row r of the layout is x[r], or
+ * x[src[r]] with src (the dispatch's; x then has x_rows rows), so the packed
+ * bf16 rows need not exist. Rows outside [offsets[0], offsets[E]) are not
+ * touched. A src outside [0, x_rows) gives a row of zeros, offsets that fall
+ * or leave [0, R] give nothing, and both flag MOE_ERR_BAD_INDEX. */
+MOE_API int moe_mx4_quantize_rows(const moe_mx4_config_t* cfg, const void* x,
+                   const int32_t* src, const int32_t* offsets, uint8_t* q, uint8_t* scale,
+                   void* ws, size_t ws_bytes, void* stream);
+
+/* out[r] = q[r] . wq[e] (fp32 sums, then SiLU with cfg->silu, then rounded
+ * to out_dtype) for the rows r of each expert e's segment [offsets[e],
+ * offsets[e + 1]); out [R, N]. Offsets that fall or leave [0, R] write
+ * nothing and flag MOE_ERR_BAD_INDEX. Bitwise reproducible. */
+MOE_API int moe_mx4_product(const moe_mx4_config_t* cfg, const uint8_t* q, const uint8_t* scale,
+                   const uint8_t* wq, const uint8_t* w_scale, const int32_t* offsets,
+                   void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The values codes and scales stand for (exact in both types): W [E, K, N],
+ * rows [R, K]. */
+MOE_API int moe_mx4_dequantize_weights(const moe_mx4_config_t* cfg, const uint8_t* wq,
+                   const uint8_t* w_scale, void* W, void* stream);
+MOE_API int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* q,
+                   const uint8_t* scale, const int32_t* offsets, void* x, void* stream);
+
 /* ---- errors --------------------------------------------------------------
  * moe_get_device_error synchronises `stream`, reads the workspace error
  * word, clears it, and returns MOE_OK, MOE_ERR_BAD_INDEX or MOE_ERR_TIMEOUT

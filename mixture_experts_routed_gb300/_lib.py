@@ -48,6 +48,11 @@ class MoeNormConfig(ctypes.Structure):
                [(n, ctypes.c_float) for n in ("eps", "alpha", "beta")]
 
 
+class MoeMx4Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("R", "K", "N", "E", "dtype", "out_dtype", "silu", "x_rows")]
+
+
 class MoeForwardViews(ctypes.Structure):
     _fields_ = [("topk_idx", ctypes.c_void_p), ("topk_w", ctypes.c_void_p),
                 ("counts", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
@@ -89,6 +94,14 @@ PROTOTYPES = {
                           _SZ, _P]),
     "moe_forward_few_workspace_size": (_SZ, [_CFG]),
     "moe_forward_few": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_mx4_row_scale_size": (_SZ, [_P]),
+    "moe_mx4_weight_scale_size": (_SZ, [_P]),
+    "moe_mx4_workspace_size": (_SZ, [_P]),
+    "moe_mx4_quantize_weights": (_I, [_P] * 5),
+    "moe_mx4_quantize_rows": (_I, [_P] * 7 + [_SZ, _P]),
+    "moe_mx4_product": (_I, [_P] * 8 + [_SZ, _P]),
+    "moe_mx4_dequantize_weights": (_I, [_P] * 5),
+    "moe_mx4_dequantize_rows": (_I, [_P] * 6),
     "moe_block_norm": (_I, [_P] * 11),
     "moe_block_norm_backward_workspace_size": (_SZ, [_P]),
     "moe_block_norm_backward": (_I, [_P] * 16 + [_SZ, _P]),

@@ -19,7 +19,9 @@ __all__ = ["MoEError", "make_config", "config_from", "workspace_size", "scratch_
            "forward_views", "get_device_error", "clear_device_error", "kernel_count",
            "check_config", "backward", "backward_workspace_size", "forward_few",
            "few_workspace_size", "norm_config", "block_norm",
-           "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace"]
+           "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace",
+           "mx4_config", "mx4_quantize_weights", "mx4_quantize_rows", "mx4_product",
+           "mx4_dequantize_weights", "mx4_dequantize_rows", "alloc_mx4_workspace"]
 
 
 class MoEError(RuntimeError):
@@ -408,3 +410,112 @@ def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_
         ws.numel() * ws.element_size(), _s(stream))
     _check(st, "moe_block_norm_backward")
     return g
+
+
+# ---------------------------------------------------------------- 4-bit expert products
+def mx4_config(R, K, N, E, dtype="bf16", out_dtype="bf16", silu=0, x_rows=0) -> L.MoeMx4Config:
+    return L.MoeMx4Config(int(R), int(K), int(N), int(E), _DTYPES[dtype], _DTYPES[out_dtype],
+                          int(silu), int(x_rows))
+
+
+def alloc_mx4_workspace(c, device=None) -> torch.Tensor:
+    """Zeroed workspace of the 4-bit calls (one serves any configuration)."""
+    n = int(L.load().moe_mx4_workspace_size(ctypes.byref(c)))
+    if n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _scales(size, c, device):
+    n = int(size(ctypes.byref(c)))
+    if n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "mx4 config")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _scale_p(name, size, c, t):
+    if t.dtype != torch.uint8 or t.numel() < int(size(ctypes.byref(c))):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {t.numel()} {t.dtype}")
+    return _p(t)
+
+
+def _indices(name, t, n):
+    if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {t.numel()} {t.dtype}, not {n} int32")
+    return _p(t)
+
+
+def mx4_quantize_weights(c, W, *, q=None, scale=None, stream=None):
+    """W [E, K, N] -> (codes uint8 [E, N, K / 2], scales uint8 in the product's layout)."""
+    lib = L.load()
+    if q is None:
+        q = torch.empty((c.E, c.N, c.K // 2), dtype=torch.uint8, device=W.device)
+    if scale is None:
+        scale = _scales(lib.moe_mx4_weight_scale_size, c, W.device)
+    st = lib.moe_mx4_quantize_weights(
+        ctypes.byref(c), _shaped("W", W, (c.E, c.K, c.N), _ndt(c)),
+        _shaped("q", q, (c.E, c.N, c.K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_weight_scale_size, c, scale), _s(stream))
+    _check(st, "moe_mx4_quantize_weights")
+    return q, scale
+
+
+def mx4_quantize_rows(c, x, offsets, *, ws, src=None, q=None, scale=None, stream=None):
+    """Rows x [R, K], or with ``src`` [R] the rows x[src] of x [x_rows, K] -> (codes uint8
+    [R, K / 2], scales uint8 laid out for ``offsets``)."""
+    lib = L.load()
+    if q is None:
+        q = torch.empty((c.R, c.K // 2), dtype=torch.uint8, device=x.device)
+    if scale is None:
+        scale = _scales(lib.moe_mx4_row_scale_size, c, x.device)
+    st = lib.moe_mx4_quantize_rows(
+        ctypes.byref(c), _shaped("x", x, (c.R if src is None else c.x_rows, c.K), _ndt(c)),
+        _indices("src", src, c.R), _indices("offsets", offsets, c.E + 1),
+        _shaped("q", q, (c.R, c.K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale), _p(ws),
+        ws.numel() * ws.element_size(), _s(stream))
+    _check(st, "moe_mx4_quantize_rows")
+    return q, scale
+
+
+def mx4_product(c, q, scale, wq, w_scale, offsets, *, ws, out=None, stream=None):
+    """out[r] = rows q[r] . weights wq[e] over each expert's segment, [R, N]."""
+    lib = L.load()
+    odt = torch.float32 if c.out_dtype == L.MOE_DTYPE_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((c.R, c.N), dtype=odt, device=q.device)
+    st = lib.moe_mx4_product(
+        ctypes.byref(c), _shaped("q", q, (c.R, c.K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale),
+        _shaped("wq", wq, (c.E, c.N, c.K // 2), torch.uint8),
+        _scale_p("w_scale", lib.moe_mx4_weight_scale_size, c, w_scale),
+        _indices("offsets", offsets, c.E + 1), _shaped("out", out, (c.R, c.N), odt), _p(ws),
+        ws.numel() * ws.element_size(), _s(stream))
+    _check(st, "moe_mx4_product")
+    return out
+
+
+def mx4_dequantize_weights(c, wq, w_scale, *, W=None, stream=None):
+    """The values of quantised weights, [E, K, N]."""
+    lib = L.load()
+    if W is None:
+        W = torch.empty((c.E, c.K, c.N), dtype=_ndt(c), device=wq.device)
+    st = lib.moe_mx4_dequantize_weights(
+        ctypes.byref(c), _shaped("wq", wq, (c.E, c.N, c.K // 2), torch.uint8),
+        _scale_p("w_scale", lib.moe_mx4_weight_scale_size, c, w_scale),
+        _shaped("W", W, (c.E, c.K, c.N), _ndt(c)), _s(stream))
+    _check(st, "moe_mx4_dequantize_weights")
+    return W
+
+
+def mx4_dequantize_rows(c, q, scale, offsets, *, x=None, stream=None):
+    """The values of quantised rows, [R, K] (rows outside the segments are not written)."""
+    lib = L.load()
+    if x is None:
+        x = torch.empty((c.R, c.K), dtype=_ndt(c), device=q.device)
+    st = lib.moe_mx4_dequantize_rows(
+        ctypes.byref(c), _shaped("q", q, (c.R, c.K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale),
+        _indices("offsets", offsets, c.E + 1), _shaped("x", x, (c.R, c.K), _ndt(c)), _s(stream))
+    _check(st, "moe_mx4_dequantize_rows")
+    return x

@@ -306,4 +306,27 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
                        const void* W2, int T, int d, int E, int f, RouterSpec rs, void* out,
                        void* ws, int num_sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- mx4.cu
+// Microscaled 4-bit rows and expert weights, and their grouped product.
+constexpr int kMx4MaxCtas = 160;    // the grid the product's partial sums are sized for
+constexpr int kMx4SplitRows = 32;   // a split launch's rows per expert, at most
+// Row tiles (128 rows of one expert) that R rows of E experts can make.
+size_t mx4_row_tiles(int R, int E);
+cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,
+                            const int32_t* offsets, int E, int R, int K, uint8_t* q, uint8_t* sc,
+                            uint32_t* err, int num_sms, cudaStream_t s);
+cudaError_t launch_mx4_rows_back(int dtype, const uint8_t* q, const uint8_t* sc,
+                                 const int32_t* offsets, int E, int R, int K, void* out,
+                                 int num_sms, cudaStream_t s);
+cudaError_t launch_mx4_weights(int dtype, const void* W, int E, int K, int N, uint8_t* q,
+                               uint8_t* sc, cudaStream_t s);
+cudaError_t launch_mx4_weights_back(int dtype, const uint8_t* q, const uint8_t* sc, int E, int K,
+                                    int N, void* W, cudaStream_t s);
+// `ctr`: kMx4MaxCtas words, zero between launches; `part`: [kMx4MaxCtas][2]
+// [kMx4SplitRows][256] fp32.
+cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8_t* wq,
+                               const uint8_t* wsc, const int32_t* offsets, int E, int R, int K,
+                               int N, int out_f32, int silu, void* out, uint32_t* err,
+                               uint32_t* ctr, float* part, int num_sms, cudaStream_t s);
+
 }  // namespace moe

@@ -551,6 +551,27 @@ int check_few(const moe_config_t* c) {
   return MOE_OK;
 }
 
+// ---------------------------------------------------------------- 4-bit products
+int check_mx4(const moe_mx4_config_t* c) {
+  if (c == nullptr || c->R < 0 || c->K <= 0 || c->N <= 0 || c->K % 64 != 0 || c->N % 64 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (c->E < 1 || c->E > kMaxExperts || c->x_rows < 0) return MOE_ERR_INVALID_ARG;
+  for (int dt : {c->dtype, c->out_dtype})
+    if (dt != MOE_DTYPE_F32 && dt != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->silu != 0 && c->silu != 1) return MOE_ERR_INVALID_ARG;
+  if (c->K > 65536 || c->N > 65536 || c->R > 1 << 24) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The workspace: the error word, the product's tile arrivals, its split sums.
+constexpr size_t kMx4CtrOffset = kAlign;
+constexpr size_t kMx4PartOffset = kMx4CtrOffset + 1024;
+static_assert(kMx4MaxCtas * sizeof(uint32_t) <= 1024, "arrivals");
+
+size_t mx4_row_scales(const moe_mx4_config_t& c) {
+  return mx4_row_tiles(c.R, c.E) * ceil_div(c.K, 128) * 512;
+}
+
 // ---------------------------------------------------------------- block norms
 int check_norm(const moe_norm_config_t* c) {
   if (c == nullptr || c->T < 0 || c->d <= 0 || c->d % 64 != 0) return MOE_ERR_INVALID_ARG;
@@ -792,6 +813,90 @@ int moe_forward_few(const moe_config_t* cfg, const void* x, const void* W_g, con
   const RouterSpec rs{c.k, c.pre_k, c.router, c.n_group, c.topk_group, c.tau, noise};
   return status_of(launch_few(x, W_g, bias, W1, W2, c.T, c.d, c.E, c.f, rs, out, ws, sms,
                               as_stream(stream)));
+}
+
+size_t moe_mx4_row_scale_size(const moe_mx4_config_t* cfg) {
+  if (check_mx4(cfg) != MOE_OK) return 0;
+  return cfg->R > 0 ? mx4_row_scales(*cfg) : 512;
+}
+
+size_t moe_mx4_weight_scale_size(const moe_mx4_config_t* cfg) {
+  if (check_mx4(cfg) != MOE_OK) return 0;
+  return static_cast<size_t>(cfg->E) * ceil_div(cfg->N, 128) * ceil_div(cfg->K, 128) * 512;
+}
+
+size_t moe_mx4_workspace_size(const moe_mx4_config_t* cfg) {
+  if (check_mx4(cfg) != MOE_OK) return 0;
+  return kMx4PartOffset + static_cast<size_t>(kMx4MaxCtas) * 2 * kMx4SplitRows * 256 * 4;
+}
+
+int moe_mx4_quantize_weights(const moe_mx4_config_t* cfg, const void* W, uint8_t* wq,
+                             uint8_t* w_scale, void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  if (!ok_ptr(W) || !ok_ptr(wq) || !ok_ptr(w_scale)) return MOE_ERR_INVALID_ARG;
+  return status_of(launch_mx4_weights(cfg->dtype, W, cfg->E, cfg->K, cfg->N, wq, w_scale,
+                                      as_stream(stream)));
+}
+
+int moe_mx4_quantize_rows(const moe_mx4_config_t* cfg, const void* x, const int32_t* src,
+                          const int32_t* offsets, uint8_t* q, uint8_t* scale, void* ws,
+                          size_t ws_bytes, void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  const moe_mx4_config_t& c = *cfg;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (c.R > 0 && (!ok_ptr(x) || offsets == nullptr || !ok_ptr(q) || !ok_ptr(scale)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_mx4_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.R == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_mx4_rows(c.dtype, x, src, src != nullptr ? c.x_rows : c.R, offsets, c.E,
+                                   c.R, c.K, q, scale, static_cast<uint32_t*>(ws), sms,
+                                   as_stream(stream)));
+}
+
+int moe_mx4_product(const moe_mx4_config_t* cfg, const uint8_t* q, const uint8_t* scale,
+                    const uint8_t* wq, const uint8_t* w_scale, const int32_t* offsets, void* out,
+                    void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  const moe_mx4_config_t& c = *cfg;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (c.R > 0 && (!ok_ptr(q) || !ok_ptr(scale) || !ok_ptr(wq) || !ok_ptr(w_scale) ||
+                  offsets == nullptr || !ok_ptr(out)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_mx4_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.R == 0) return MOE_OK;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_mx4_product(q, scale, wq, w_scale, offsets, c.E, c.R, c.K, c.N,
+                                      c.out_dtype == MOE_DTYPE_F32 ? 1 : 0, c.silu, out,
+                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kMx4CtrOffset),
+                                      at<float>(ws, kMx4PartOffset), sms, as_stream(stream)));
+}
+
+int moe_mx4_dequantize_weights(const moe_mx4_config_t* cfg, const uint8_t* wq,
+                               const uint8_t* w_scale, void* W, void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  if (!ok_ptr(W) || !ok_ptr(wq) || !ok_ptr(w_scale)) return MOE_ERR_INVALID_ARG;
+  return status_of(launch_mx4_weights_back(cfg->dtype, wq, w_scale, cfg->E, cfg->K, cfg->N, W,
+                                           as_stream(stream)));
+}
+
+int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* q, const uint8_t* scale,
+                            const int32_t* offsets, void* x, void* stream) {
+  const int st = check_mx4(cfg);
+  if (st != MOE_OK) return st;
+  const moe_mx4_config_t& c = *cfg;
+  if (c.R == 0) return MOE_OK;
+  if (!ok_ptr(q) || !ok_ptr(scale) || offsets == nullptr || !ok_ptr(x)) return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_mx4_rows_back(c.dtype, q, scale, offsets, c.E, c.R, c.K, x, sms,
+                                        as_stream(stream)));
 }
 
 int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b, const float* w_post,

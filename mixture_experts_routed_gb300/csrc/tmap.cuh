@@ -14,6 +14,11 @@ namespace moe {
 bool make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_cols,
                  uint32_t box_rows);
 
+// 2-D map over row-major [rows, cols] bytes (cols a multiple of 16), box
+// [box_rows][128 bytes], 128-byte swizzle, zero fill outside the matrix.
+bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                       uint32_t box_rows);
+
 // 2-D map over a row-major [rows, cols] output, box [32 rows][32 cols]: fp32
 // with the 128-byte swizzle, or bf16 with the 64-byte swizzle. Stores
 // outside the matrix are clipped.

@@ -132,3 +132,47 @@ def few_layer(c, i):
         out[t] += we * y
         tol[t] += we * (c2 * ya + dh @ W2.abs() + (2 * e_l[t] + 64 * U32) * y.abs())
     return out, tol, gap
+
+
+# ---------------------------------------------------------------- microscaled 4-bit values
+GRID = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=F64)
+
+
+def mx4_quantize(v):
+    """[n, K] in 64 bits -> codes [n, K] and scale bytes [n, K / 32], by nearest grid value."""
+    b = v.reshape(v.shape[0], -1, 32)
+    amax = b.abs().amax(2)
+    fin = torch.isfinite(b).all(2)
+    s = torch.frexp(torch.where(fin & (amax > 0), amax, torch.ones_like(amax))).exponent - 1 - 2
+    s = s.clamp(min=-127) + 127
+    s = torch.where(amax == 0, torch.full_like(s, 127), s)
+    s = torch.where(fin, s, torch.full_like(s, 255))
+    m = torch.where(fin[..., None], b.abs(), torch.zeros_like(b)) * torch.exp2(
+        127.0 - s[..., None].to(F64))
+    dist = (m.clamp(max=6.0)[..., None] - GRID.to(v.device)).abs()
+    near = dist == dist.amin(-1, keepdim=True)
+    # of two equally near codes the even one
+    code = torch.arange(8, device=v.device)
+    pick = torch.where(near, 8 * (code % 2) + code, torch.full_like(code, 99)).amin(-1) % 8
+    pick = pick + 8 * torch.signbit(b).long()
+    return pick.reshape(v.shape), s.to(torch.uint8)
+
+
+def mx4_values(code, s):
+    code = code.long()
+    v = GRID.to(code.device)[code & 7] * (1 - 2 * (code >> 3))
+    sc = torch.where(s == 255, torch.full(s.shape, float("nan"), dtype=F64, device=s.device),
+                     torch.exp2(s.to(F64) - 127))
+    return (v.reshape(code.shape[0], -1, 32) * sc[..., None]).reshape(code.shape)
+
+
+def unpack_codes(q):
+    """[..., K / 2] bytes -> [..., K] codes, the even k in the low half."""
+    return torch.stack([q & 15, q >> 4], -1).flatten(-2)
+
+
+def scales_of_tiles(scale, tiles, K):
+    """Chunk bytes -> [tiles * 128, K / 32] scale bytes."""
+    kc = -(-K // 128)
+    c = scale[:tiles * kc * 512].reshape(tiles, kc, 32, 4, 4)   # i % 32, i / 32, block
+    return c.permute(0, 3, 2, 1, 4).reshape(tiles * 128, kc * 4)[:, :K // 32]

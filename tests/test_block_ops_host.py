@@ -146,3 +146,75 @@ def test_few_workspace(lib):
         need = lib.moe_forward_few_workspace_size(ctypes.byref(c))
         assert need > 0 and need % 256 == 0
         assert few(lib, c, ws_bytes=need - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def mx4(**kw):
+    base = dict(R=8, K=128, N=64, E=2, dtype=1, out_dtype=1, silu=0, x_rows=8)
+    base.update(kw)
+    return L.MoeMx4Config(*[base[n] for n, _ in L.MoeMx4Config._fields_])
+
+
+def mx4_calls(lib, c, bad=None, ws_bytes=1 << 40):
+    """The five calls, each argument that `bad` = (call, position, value) names replaced."""
+    r = ctypes.byref(c)
+    calls = {"quantize_weights": [r, P, P, P, None],
+             "quantize_rows": [r, P, None, P, P, P, P, ws_bytes, None],
+             "product": [r, P, P, P, P, P, P, P, ws_bytes, None],
+             "dequantize_weights": [r, P, P, P, None],
+             "dequantize_rows": [r, P, P, P, P, None]}
+    if bad is None:
+        return [getattr(lib, "moe_mx4_" + n)(*a) for n, a in calls.items()]
+    calls[bad[0]][bad[1]] = bad[2]
+    return getattr(lib, "moe_mx4_" + bad[0])(*calls[bad[0]])
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(R=-1), L.MOE_ERR_INVALID_ARG), (dict(K=0), L.MOE_ERR_INVALID_ARG),
+    (dict(K=96), L.MOE_ERR_INVALID_ARG), (dict(N=32), L.MOE_ERR_INVALID_ARG),
+    (dict(N=0), L.MOE_ERR_INVALID_ARG), (dict(E=0), L.MOE_ERR_INVALID_ARG),
+    (dict(E=257), L.MOE_ERR_INVALID_ARG), (dict(dtype=2), L.MOE_ERR_INVALID_ARG),
+    (dict(out_dtype=-1), L.MOE_ERR_INVALID_ARG), (dict(silu=2), L.MOE_ERR_INVALID_ARG),
+    (dict(x_rows=-1), L.MOE_ERR_INVALID_ARG), (dict(K=65600), L.MOE_ERR_UNSUPPORTED),
+    (dict(N=65600), L.MOE_ERR_UNSUPPORTED), (dict(R=(1 << 24) + 1), L.MOE_ERR_UNSUPPORTED)])
+def test_mx4_configs(lib, kw, status):
+    c = mx4(**kw)
+    assert set(mx4_calls(lib, c)) == {status}
+    for size in ("row_scale_size", "weight_scale_size", "workspace_size"):
+        assert getattr(lib, "moe_mx4_" + size)(ctypes.byref(c)) == 0
+
+
+@pytest.mark.parametrize("call,positions", [
+    ("quantize_weights", (1, 2, 3)), ("quantize_rows", (1, 4, 5, 6)),
+    ("product", (1, 2, 3, 4, 6, 7)), ("dequantize_weights", (1, 2, 3)),
+    ("dequantize_rows", (1, 2, 4))])
+def test_mx4_arguments(lib, call, positions):
+    for i in positions:
+        for v in (None, ODD):
+            assert mx4_calls(lib, mx4(), (call, i, v)) == L.MOE_ERR_INVALID_ARG, (i, v)
+
+
+def test_mx4_null_offsets_and_small_workspaces(lib):
+    for call, i in (("quantize_rows", 3), ("product", 5), ("dequantize_rows", 3)):
+        assert mx4_calls(lib, mx4(), (call, i, None)) == L.MOE_ERR_INVALID_ARG
+    need = lib.moe_mx4_workspace_size(ctypes.byref(mx4()))
+    for call, i in (("quantize_rows", 7), ("product", 8)):
+        assert mx4_calls(lib, mx4(), (call, i, need - 1)) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+def test_mx4_scale_sizes_hold_every_split_of_the_rows(lib):
+    # the row tiles of any segments: at most one partial tile per expert with rows
+    import random
+    rng = random.Random(0)
+    for _ in range(200):
+        E = rng.randint(1, 40)
+        n = [rng.choice([0, 1, 127, 128, 129, rng.randint(0, 600)]) for _ in range(E)]
+        c = mx4(R=sum(n), E=E, K=192)
+        tiles = sum(-(-v // 128) for v in n)
+        assert lib.moe_mx4_row_scale_size(ctypes.byref(c)) >= max(1, tiles) * 2 * 512 * (sum(n) > 0)
+    assert lib.moe_mx4_weight_scale_size(ctypes.byref(mx4(K=192, N=192, E=3))) == 3 * 2 * 2 * 512
+
+
+def test_mx4_config_matches_the_header():
+    from test_abi_host import struct_fields
+    assert [(n, ctypes.c_int32) for n, t in struct_fields("moe_mx4_config")] == \
+        list(L.MoeMx4Config._fields_)
