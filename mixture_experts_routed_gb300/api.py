@@ -71,12 +71,20 @@ def _p(t):
         raise MoEError(L.MOE_ERR_INVALID_ARG, "tensor is not contiguous")
     if not t.is_cuda:
         raise MoEError(L.MOE_ERR_INVALID_ARG, "tensor is not in GPU memory")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
+
+
+# The current stream's handle without a Stream object in between (a call costs microseconds
+# where a decode step's kernels do), where torch has the query.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _s(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and torch.cuda.is_initialized():
+        return _raw_stream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(st, what):
@@ -347,7 +355,9 @@ def alloc_norm_workspace(c, device=None) -> torch.Tensor:
 
 def _shaped(name, t, shape, dtype):
     """A tensor of the call's shape and type, or None."""
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype:
         raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {tuple(t.shape)} {t.dtype}, not "
                                               f"{tuple(shape)} {dtype}")
     return _p(t)

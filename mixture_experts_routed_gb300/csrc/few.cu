@@ -55,23 +55,30 @@ constexpr int BM = 128, BK = 64;            // features, contraction rows of a s
 constexpr int BOX_BYTES = BK * 64 * 2;      // [64 k][64 features] bf16
 constexpr int A_BYTES = 2 * BOX_BYTES;
 constexpr int GATE_E = 64;                  // experts of a gate CTA
-constexpr int GATE_ROWS = 64;               // x rows staged at a time
-constexpr int MAX_CHUNKS = 64;              // partial sums of a logit
+constexpr int GATE_ROWS = 256;              // contraction rows staged at a time
+constexpr int MAX_LOADS = 32;               // partial sums of a logit a thread adds up
 constexpr int TMEM_COLS = 128;              // two accumulators of 64 columns
 constexpr int MAX_ROWS = kFewMaxTokens * kMaxFanout;
 
+// TP: the tokens a launch is compiled for
 template <int TP>
 struct Cfg {
-  static constexpr int N1 = TP < 16 ? 16 : TP;  // x rows of phase 1's products
-  static constexpr int N2 = 2 * TP;             // h rows (hi, lo) of phase 2's
+  static constexpr int N1 = TP < 16 ? 16 : TP;  // columns of phase 1's products: x rows
+  static constexpr int HR = 2 * TP;             // h rows of an expert: hi, lo
+  static constexpr int N2 = HR < 16 ? 16 : HR;  // columns of phase 2's (past HR: unused)
+  // gate: experts a thread takes, lanes to a row of W_g, rows side by side
+  static constexpr int VE = TP <= 8 ? 8 : 64 / TP;
+  static constexpr int LPR = GATE_E / VE, RG = THREADS / LPR;
+  static constexpr int CB = 32 / TP;            // partial sums joined at a time
   static constexpr int B_BYTES = (N1 > N2 ? N1 : N2) * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 200 * 1024 / STAGE;
   static constexpr int OFF_BAR = STAGES * STAGE;
   static constexpr int OFF_TAB = OFF_BAR + (2 * STAGES + 5) * 8;
-  static constexpr int SMEM = OFF_TAB + 256 * 4 + 256 * 2 + MAX_ROWS * 2 + MAX_ROWS * 4 + 64 + 1024;
+  static constexpr int SMEM = OFF_TAB + 256 * 4 + 256 * 2 + MAX_ROWS * 4 + MAX_ROWS * 4 + 64 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(GATE_ROWS * TP * 4 + 4 * TP * GATE_E * 4 + kMaxExperts * 4 <= OFF_BAR, "scratch");
+  static_assert(GATE_ROWS * TP * 4 + RG * TP * GATE_E * 4 + GATE_ROWS * GATE_E * 2 <= OFF_BAR,
+                "scratch");
 };
 
 struct Params {
@@ -81,6 +88,7 @@ struct Params {
   RouterSpec rs;
   int T, d, E, f, k;
   int gate_groups, gate_chunks, gate_len;  // expert groups x chunks of gate_len rows
+  int gate_vec;                            // W_g rows can be read a vector at a time
   int32_t* idx;
   float* w;
   float* gpart;      // [chunks][T][E]
@@ -117,21 +125,99 @@ __device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t target, u
     if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
+// Threads side by side that add up E logits.
+__host__ __device__ constexpr int expert_lanes(int E) {
+  return E <= 32 ? 32 : (E <= 64 ? 64 : (E <= 128 ? 128 : 256));
+}
+
+// One warp: token t's choice from its logits row (NJ logits a lane), ranked
+// and weighted as topk::warp_select_and_weigh does it, in a loop: this code
+// runs once a launch, and unrolled its instructions arrive more slowly than
+// they run (4 us at 8 rounds). The argmax of a round is one reduction of
+// order-preserving integer keys and one of the ids that have the best key.
+template <int NJ>
+__device__ __forceinline__ void choose(const float* row, int E, const RouterSpec& rs, int t,
+                                       int32_t* idx, float* w) {
+  constexpr uint32_t ALL = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  float v[NJ];
+  int id[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    id[j] = lane + 32 * j;
+    v[j] = id[j] < E ? row[id[j]] : -INFINITY;
+  }
+  if (rs.mode == topk::kRouterGroup) topk::warp_group_limit<NJ>(v, id, E, rs);
+  uint32_t key[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+    // -0 as +0; a NaN, like the padding, is never chosen (key 0)
+    const uint32_t b = __float_as_uint(v[j] + 0.f);
+    key[j] = id[j] >= E || isnan(v[j]) ? 0u : (b & 0x80000000u ? ~b : b | 0x80000000u);
+  }
+  const int rounds = topk::rounds_of(rs);
+  float mine = -INFINITY, m = 0.f;  // lane s: round s's logit
+  int mine_id = 0x7fffffff;
+#pragma unroll 1
+  for (int s = 0; s < rounds; ++s) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) best = max(best, key[j]);
+    best = __reduce_max_sync(ALL, best);
+    int bi = 0x7fffffff;
+#pragma unroll
+    for (int j = NJ - 1; j >= 0; --j) bi = best != 0 && key[j] == best ? id[j] : bi;
+    bi = __reduce_min_sync(ALL, bi);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j)
+      if (id[j] == bi) key[j] = 0;
+    const float bv = best == 0 ? -INFINITY
+                               : __uint_as_float(best & 0x80000000u ? best & 0x7fffffffu : ~best);
+    if (s == 0) m = bv;
+    if (lane == s) {
+      mine = bv;
+      mine_id = bi;
+    }
+  }
+  const float ex = lane < rounds ? expf(mine - m) : 0.f;
+  float den = 0.f;
+#pragma unroll 1
+  for (int s = 0; s < rounds; ++s) den += __shfl_sync(ALL, ex, s);
+  if (lane < rs.k) {
+    idx[t * rs.k + lane] = mine_id;
+    w[t * rs.k + lane] = ex / den;
+  }
+}
+// Soft gating (E <= 16): every expert, weighted.
+__device__ __forceinline__ void weigh_all(const float* row, int E, const RouterSpec& rs, int t,
+                                          int32_t* idx, float* w) {
+  const int lane = threadIdx.x & 31;
+  const int id[1] = {lane};
+  const float v[1] = {lane < E ? row[lane] : -INFINITY};
+  topk::warp_soft_weigh<1>(v, id, E, rs, t, idx, w);
+}
 __device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
-// The steps of one phase (`units` accumulators of `len` steps) and each
-// CTA's range of them.
+// The steps of one phase (`units` accumulators of `len` steps, fewer than
+// 2^28 in all) and each CTA's range of them: start(c) = floor(total c / G).
 struct Range {
-  int len;
-  long long total;
-  int G;
+  int len, total, G, q, r;
   __device__ Range(int units, int len_, int grid) : len(len_) {
-    total = static_cast<long long>(units) * len;
-    G = total < grid ? static_cast<int>(total) : grid;  // every range holds a step
+    total = units * len;
+    G = total < grid ? total : grid;  // every range holds a step
+    q = G > 0 ? total / G : 0;
+    r = total - q * G;
   }
-  __device__ long long start(int c) const { return c >= G ? total : total * c / G; }
-  // the CTA whose range holds step i
-  __device__ int owner(long long i) const { return static_cast<int>(((i + 1) * G - 1) / total); }
+  __device__ int start(int c) const { return c >= G ? total : q * c + r * c / G; }
+  // the CTA whose range holds step i: an estimate, put right
+  __device__ int owner(int i) const {
+    int c = static_cast<int>((static_cast<float>(i) + 1.f) * static_cast<float>(G) /
+                             static_cast<float>(total));
+    c = c < G ? c : G - 1;
+    while (c > 0 && start(c) > i) --c;
+    while (c + 1 < G && start(c + 1) <= i) ++c;
+    return c;
+  }
 };
 }  // namespace fw
 
@@ -152,8 +238,8 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   uint64_t* drain = tempty + 2;
   uint32_t* smask = reinterpret_cast<uint32_t*>(smem + C::OFF_TAB);  // slot -> its tokens
   float* rw = reinterpret_cast<float*>(smask + kMaxExperts);         // [T][k] weights
-  int16_t* ridx = reinterpret_cast<int16_t*>(rw + MAX_ROWS);         // [T][k] experts, -1: none
-  int16_t* sexp = ridx + MAX_ROWS;                                   // slot -> expert
+  int32_t* ridx = reinterpret_cast<int32_t*>(rw + MAX_ROWS);         // [T][k] experts, -1: none
+  int16_t* sexp = reinterpret_cast<int16_t*>(ridx + MAX_ROWS);       // slot -> expert
   uint32_t* misc = reinterpret_cast<uint32_t*>(sexp + kMaxExperts);
   uint32_t* tmem_slot = misc;
   int* s_nslots = reinterpret_cast<int*>(misc + 1);
@@ -183,54 +269,91 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   for (int i = cta * THREADS + tid; i < p.ntiles; i += grid * THREADS) p.tiles[i] = 0;
   {
     float* xs = reinterpret_cast<float*>(smem);  // [GATE_ROWS][TP]
-    float* red = xs + GATE_ROWS * TP;            // [4][TP][GATE_E]
+    float* red = xs + GATE_ROWS * TP;            // [RG][TP][GATE_E]
+    __nv_bfloat16* wg = reinterpret_cast<__nv_bfloat16*>(red + C::RG * TP * GATE_E);
     const int chunk = cta / p.gate_groups, e0 = (cta % p.gate_groups) * GATE_E;
     if (chunk < p.gate_chunks) {
       const int r0 = chunk * p.gate_len, r1 = min(d, r0 + p.gate_len);
-      const int e = e0 + (tid & 63), rg = tid >> 6;
-      float acc[TP];
+      const int ec = tid % C::LPR * C::VE, rg = tid / C::LPR;
+      float acc[TP][C::VE];
 #pragma unroll
-      for (int t = 0; t < TP; ++t) acc[t] = 0.f;
+      for (int t = 0; t < TP; ++t)
+#pragma unroll
+        for (int i = 0; i < C::VE; ++i) acc[t][i] = 0.f;
       for (int rb = r0; rb < r1; rb += GATE_ROWS) {
-        const int n = min(GATE_ROWS, r1 - rb);
+        const int n = min(GATE_ROWS, r1 - rb);  // a multiple of 8
         __syncthreads();
-        for (int i = tid; i < GATE_ROWS * TP; i += THREADS) {
-          const int t = i / GATE_ROWS, r = i % GATE_ROWS;
-          xs[r * TP + t] =
-              t < T && r < n ? __bfloat162float(p.x[static_cast<size_t>(t) * d + rb + r]) : 0.f;
+        // the weights of all rows in flight at once
+        const __nv_bfloat16* g = p.Wg + static_cast<size_t>(rb) * E + e0;
+        if (p.gate_vec != 0) {
+#pragma unroll 4
+          for (int i = tid; i < n * (GATE_E / 8); i += THREADS) {
+            const int r = i / (GATE_E / 8), c = i % (GATE_E / 8) * 8;
+            if (e0 + c < E) cp_async16(smem_u32(wg + r * GATE_E + c), g + r * E + c);
+          }
+        } else {
+#pragma unroll 4
+          for (int i = tid; i < n * GATE_E; i += THREADS) {
+            const int r = i / GATE_E, c = i % GATE_E;
+            if (e0 + c < E) wg[i] = g[r * E + c];
+          }
         }
-        // this thread's weights: rows rg, rg + 4, ...
-        float wv[GATE_ROWS / 4];
+        cp_async_commit();
+        for (int i = tid; i < T * (GATE_ROWS / 8); i += THREADS) {
+          const int t = i / (GATE_ROWS / 8), r = i % (GATE_ROWS / 8) * 8;
+          if (r >= n) continue;
+          const uint4 v =
+              __ldg(reinterpret_cast<const uint4*>(p.x + static_cast<size_t>(t) * d + rb + r));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < GATE_ROWS / 4; ++j) {
-          const int r = rg + 4 * j;
-          wv[j] = e < E && r < n
-                      ? __bfloat162float(p.Wg[static_cast<size_t>(rb + r) * E + e])
-                      : 0.f;
+          for (int q = 0; q < 4; ++q) {
+            xs[(r + 2 * q) * TP + t] = __uint_as_float(w[q] << 16);
+            xs[(r + 2 * q + 1) * TP + t] = __uint_as_float(w[q] & 0xffff0000u);
+          }
         }
+        cp_async_wait<0>();
         __syncthreads();
+        // (tokens past T and experts past E: sums of stale values, not stored)
+#pragma unroll 1
+        for (int r = rg; r < n; r += C::RG) {
+          float xv[TP];
+          if constexpr (TP >= 4) {
 #pragma unroll
-        for (int j = 0; j < GATE_ROWS / 4; ++j) {
-          const float4* xr = reinterpret_cast<const float4*>(xs + (rg + 4 * j) * TP);
+            for (int t = 0; t < TP; t += 4) {
+              const float4 v = *reinterpret_cast<const float4*>(xs + r * TP + t);
+              xv[t] = v.x;
+              xv[t + 1] = v.y;
+              xv[t + 2] = v.z;
+              xv[t + 3] = v.w;
+            }
+          } else {
+            xv[0] = xs[r];
+          }
+          const uint32_t* wr = reinterpret_cast<const uint32_t*>(wg + r * GATE_E + ec);
 #pragma unroll
-          for (int t = 0; t < TP; t += 4) {
-            const float4 v = xr[t / 4];
-            acc[t] = fmaf(v.x, wv[j], acc[t]);
-            acc[t + 1] = fmaf(v.y, wv[j], acc[t + 1]);
-            acc[t + 2] = fmaf(v.z, wv[j], acc[t + 2]);
-            acc[t + 3] = fmaf(v.w, wv[j], acc[t + 3]);
+          for (int i = 0; i < C::VE; i += 2) {
+            const uint32_t w2 = wr[i / 2];
+            const float lo = __uint_as_float(w2 << 16), hi = __uint_as_float(w2 & 0xffff0000u);
+#pragma unroll
+            for (int t = 0; t < TP; ++t) {
+              acc[t][i] = fmaf(xv[t], lo, acc[t][i]);
+              acc[t][i + 1] = fmaf(xv[t], hi, acc[t][i + 1]);
+            }
           }
         }
       }
 #pragma unroll
-      for (int t = 0; t < TP; ++t) red[(rg * TP + t) * GATE_E + (tid & 63)] = acc[t];
+      for (int t = 0; t < TP; ++t)
+        if (t < T)
+#pragma unroll
+          for (int i = 0; i < C::VE; ++i) red[(rg * TP + t) * GATE_E + ec + i] = acc[t][i];
       __syncthreads();
       for (int i = tid; i < T * GATE_E; i += THREADS) {
         const int t = i / GATE_E, c = i % GATE_E;
         if (e0 + c < E) {
           float s = 0.f;
 #pragma unroll
-          for (int g = 0; g < 4; ++g) s += red[(g * TP + t) * GATE_E + c];
+          for (int g = 0; g < C::RG; ++g) s += red[(g * TP + t) * GATE_E + c];
           p.gpart[(static_cast<size_t>(chunk) * T + t) * E + e0 + c] = s;
         }
       }
@@ -242,55 +365,68 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   if (tid == 0) add_acq_rel(p.sync + SYNC_GATE, 1);
 
   // ---------------------------------------------------------------- router
-  for (int t = cta; t < T; t += grid) {
-    float* logits = reinterpret_cast<float*>(smem);  // [kMaxExperts]
-    if (tid == 0 && !lost) lost = !wait_count(p.sync + SYNC_GATE, grid, kWaitLimitNs);
+  // One token: every CTA adds up its sums (at most 32 KB) and routes it
+  // itself, which saves a trip through L2 (about 1 us). Several: CTA t routes
+  // token t and the others wait (7 tokens routed by every CTA took 10 us,
+  // shared out 4.6).
+  const bool local = T == 1;
+  if (local || cta < T) {
+    float* logits = reinterpret_cast<float*>(smem);  // [E]
+    float* sums = logits + kMaxExperts;              // [THREADS]
+    if (tid == 0) lost = !wait_count(p.sync + SYNC_GATE, grid, kWaitLimitNs);
     __syncthreads();
-    if (tid < E) {
-      // the chunks' sums, compensated
-      float s = p.bias != nullptr ? __ldg(p.bias + tid) : 0.f, comp = 0.f;
-      const float* g = p.gpart + static_cast<size_t>(t) * E + tid;
-#pragma unroll 16
-      for (int c = 0; c < p.gate_chunks; ++c) {
-        const float yv = __fsub_rn(__ldcg(g + static_cast<size_t>(c) * T * E), comp);
-        const float sum = __fadd_rn(s, yv);
-        comp = __fsub_rn(__fsub_rn(sum, s), yv);
-        s = sum;
-      }
-      logits[tid] = s;
+    // a logit's sums are shared by 256 / EP threads
+    const int EP = expert_lanes(E), parts = THREADS / EP;
+    const int e = tid % EP, part = tid / EP;
+    const int t = cta < T ? cta : 0;
+    // all loads in flight, then a tree
+    float v[MAX_LOADS];
+    const float* g = p.gpart + (static_cast<size_t>(part) * T + t) * E + e;
+    const int n = e < E ? p.gate_chunks - part : 0, step = parts * T * E;
+#pragma unroll
+    for (int j = 0; j < MAX_LOADS; ++j) v[j] = j * parts < n ? __ldcg(g + j * step) : 0.f;
+#pragma unroll
+    for (int w = MAX_LOADS / 2; w > 0; w >>= 1)
+#pragma unroll
+      for (int j = 0; j < w; ++j) v[j] += v[j + w];
+    sums[tid] = v[0] + (part == 0 && e < E && p.bias != nullptr ? __ldg(p.bias + e) : 0.f);
+    __syncthreads();
+    if (part == 0 && e < E) {
+      float s = sums[tid];
+      for (int q = 1; q < parts; ++q) s += sums[tid + q * EP];
+      logits[e] = s;
     }
     __syncthreads();
     if (warp == 0) {
-      float v[8];
-      int id[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        id[j] = lane + 32 * j;
-        v[j] = id[j] < E ? logits[id[j]] : -INFINITY;
+      int32_t* oi = local ? ridx : p.idx;
+      float* ow = local ? rw : p.w;
+      if (p.rs.mode == topk::kRouterSoft)
+        weigh_all(logits, E, p.rs, t, oi, ow);
+      else if (E <= 64)
+        choose<2>(logits, E, p.rs, t, oi, ow);
+      else
+        choose<8>(logits, E, p.rs, t, oi, ow);
+      if (!local) {
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) add_acq_rel(p.sync + SYNC_ROUTE, 1);
       }
-      if (p.rs.mode == topk::kRouterSoft) {
-        topk::warp_soft_weigh<8>(v, id, E, p.rs, t, p.idx, p.w);
-      } else {
-        if (p.rs.mode == topk::kRouterGroup) topk::warp_group_limit<8>(v, id, E, p.rs);
-        topk::warp_select_and_weigh<8>(v, id, p.rs, t, p.idx, p.w);
-      }
-      __threadfence();
-      __syncwarp();
-      if (lane == 0) add_acq_rel(p.sync + SYNC_ROUTE, 1);
     }
-    __syncthreads();
   }
-  if (tid == 0 && !lost) lost = !wait_count(p.sync + SYNC_ROUTE, T, kWaitLimitNs);
+  if (!local) {
+    if (tid == 0 && !lost) lost = !wait_count(p.sync + SYNC_ROUTE, T, kWaitLimitNs);
+  }
   for (int e = tid; e < kMaxExperts; e += THREADS) smask[e] = 0;
   __syncthreads();
 
   // ---------------------------------------------------------------- slots
   // the chosen experts in id order, and each one's tokens as a bit mask
   for (int i = tid; i < T * k; i += THREADS) {
-    const int e = __ldcg(p.idx + i);
+    const int e = local ? ridx[i] : __ldcg(p.idx + i);
+    const float w = local ? rw[i] : __ldcg(p.w + i);
     const bool ok = e >= 0 && e < E;
-    ridx[i] = static_cast<int16_t>(ok ? e : -1);
-    rw[i] = ok ? __ldcg(p.w + i) : 0.f;
+    ridx[i] = ok ? e : -1;
+    rw[i] = ok ? w : 0.f;
     if (ok)
       atomicOr(&smask[e], 1u << (i / k));
     else
@@ -300,7 +436,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   if (warp == 0) {
     // in place: slot <= expert, and a round's masks are read before it writes
     int n = 0;
-    for (int j = 0; j < kMaxExperts / 32; ++j) {
+    for (int j = 0; j < (E + 31) / 32; ++j) {
       const uint32_t m = smask[j * 32 + lane];
       const uint32_t have = __ballot_sync(0xffffffffu, m != 0);
       const int at = n + __popc(have & ((1u << lane) - 1));
@@ -361,10 +497,9 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         return true;
       };
       {
-        const long long end = r1.start(cta + 1);
-        for (long long i = r1.start(cta); i < end && !dead;) {
-          const int u = static_cast<int>(i / r1.len), k0 = static_cast<int>(i - static_cast<long long>(u) * r1.len);
-          const int n = static_cast<int>(min(static_cast<long long>(r1.len - k0), end - i));
+        const int end = r1.start(cta + 1);
+        for (int i = r1.start(cta); i < end && !dead;) {
+          const int u = i / r1.len, k0 = i - u * r1.len, n = min(r1.len - k0, end - i);
           const int slot = u / FB, c0 = (u - slot * FB) * BM, row = sexp[slot] * d;
           for (int j = k0; j < k0 + n; ++j) {
             if (!claim()) break;
@@ -378,17 +513,17 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       if (!dead) {
         // the first W2 tiles go out before h is known to be there; their h
         // rows follow once every h tile has been counted
-        const long long first = r2.start(cta), end = r2.start(cta + 1);
-        auto w2_step = [&](long long i, bool a, bool b) {
-          const int u = static_cast<int>(i / r2.len), j = static_cast<int>(i - static_cast<long long>(u) * r2.len);
+        const int first = r2.start(cta), end = r2.start(cta + 1);
+        auto w2_step = [&](int i, bool a, bool b) {
+          const int u = i / r2.len, j = i - u * r2.len;
           const int db = u / nslots, slot = u - db * nslots;
-          if (a) load_a(&tmW2, sexp[slot] * f + j * BK, db * BM, d, C::N2 * 128);
+          if (a) load_a(&tmW2, sexp[slot] * f + j * BK, db * BM, d, C::HR * 128);
           if (b)
-            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::N2);
+            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::HR);
         };
         const int s0 = s;
         const uint32_t ph0 = ph;
-        long long ahead = first;
+        int ahead = first;
         for (; ahead < end && ahead < first + C::STAGES; ++ahead) {
           if (!claim()) break;
           w2_step(ahead, true, false);
@@ -400,21 +535,20 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         const uint32_t ph1 = ph;
         s = s0;
         ph = ph0;
-        for (long long i = first; i < ahead; ++i) {
+        for (int i = first; i < ahead; ++i) {
           w2_step(i, false, true);
           next();
         }
         s = s1;
         ph = ph1;
-        for (long long i = ahead; i < end && !dead;) {
-          const int u = static_cast<int>(i / r2.len), k0 = static_cast<int>(i - static_cast<long long>(u) * r2.len);
-          const int n = static_cast<int>(min(static_cast<long long>(r2.len - k0), end - i));
+        for (int i = ahead; i < end && !dead;) {
+          const int u = i / r2.len, k0 = i - u * r2.len, n = min(r2.len - k0, end - i);
           const int db = u / nslots, slot = u - db * nslots;
           const int row = sexp[slot] * f;
           for (int j = k0; j < k0 + n; ++j) {
             if (!claim()) break;
-            load_a(&tmW2, row + j * BK, db * BM, d, C::N2 * 128);
-            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::N2);
+            load_a(&tmW2, row + j * BK, db * BM, d, C::HR * 128);
+            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::HR);
             next();
           }
           i += n;
@@ -442,10 +576,9 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       uint32_t ph = 0, aph = 0;
       bool dead = false;
       auto phase = [&](const Range& r, uint32_t idesc) {
-        const long long end = r.start(cta + 1);
-        for (long long i = r.start(cta); i < end && !dead;) {
-          const int k0 = static_cast<int>(i % r.len);
-          const int n = static_cast<int>(min(static_cast<long long>(r.len - k0), end - i));
+        const int end = r.start(cta + 1);
+        for (int i = r.start(cta); i < end && !dead;) {
+          const int n = min(r.len - i % r.len, end - i);
           if (!mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs)) {
             dead = true;
             break;
@@ -525,16 +658,15 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     // Joins block `blk` of range r (steps [a, b)) that this CTA holds a part
     // v of: true for the last CTA to arrive, with the sum in v.
     float* part = p.part;
-    auto join = [&](const Range& r, long long a, long long b, uint32_t* ctr, uint32_t mask,
-                    float (&v)[TP]) {
-      auto slice = [&](int c) {
-        return part + (static_cast<size_t>(c) * 2 + (r.start(c) > a ? 0 : 1)) * TP * BM + col;
-      };
+    auto join = [&](const Range& r, int a, int b, uint32_t* ctr, uint32_t mask, float (&v)[TP]) {
+      const int c0 = r.owner(a), c1 = r.owner(b - 1);
+      // a CTA's part of the block its range starts in comes first, of the one
+      // it ends in second
+      auto slice = [&](int c) { return part + (c * 2 + (c > c0 ? 0 : 1)) * TP * BM + col; };
       float* mine = slice(cta);
 #pragma unroll
       for (int t = 0; t < TP; ++t)
         if ((mask >> t) & 1u) __stcg(mine + t * BM, v[t]);
-      const int c0 = r.owner(a), c1 = r.owner(b - 1);
       __threadfence();
       bar_epi();
       if (tid == 128) *s_last = add_acq_rel(ctr, 1) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
@@ -544,21 +676,25 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         __threadfence();
 #pragma unroll
         for (int t = 0; t < TP; ++t) v[t] = 0.f;
-        for (int c = c0; c <= c1; ++c) {
-          const float* o = slice(c);
+        for (int cb = c0; cb <= c1; cb += C::CB) {
+          float o[C::CB][TP];
 #pragma unroll
-          for (int t = 0; t < TP; ++t)
-            if ((mask >> t) & 1u) v[t] += __ldcg(o + t * BM);
+          for (int q = 0; q < C::CB; ++q)
+#pragma unroll
+            for (int t = 0; t < TP; ++t)
+              o[q][t] = cb + q <= c1 && ((mask >> t) & 1u) ? __ldcg(slice(cb + q) + t * BM) : 0.f;
+#pragma unroll
+          for (int q = 0; q < C::CB; ++q)
+#pragma unroll
+            for (int t = 0; t < TP; ++t) v[t] += o[q][t];
         }
       }
       return last;
     };
     {
-      const long long end = r1.start(cta + 1);
-      for (long long i = r1.start(cta); i < end;) {
-        const int u = static_cast<int>(i / r1.len);
-        const long long a = static_cast<long long>(u) * r1.len, b = a + r1.len;
-        const long long stop = min(b, end);
+      const int end = r1.start(cta + 1);
+      for (int i = r1.start(cta); i < end;) {
+        const int u = i / r1.len, a = u * r1.len, b = a + r1.len, stop = min(b, end);
         const int slot = u / FB, fb = u - slot * FB;
         const uint32_t mask = smask[slot];
         float v[TP];
@@ -566,7 +702,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         if ((i == a && stop == b) || join(r1, a, b, p.tiles + u, mask, v)) {
           const int c = fb * BM + col;
           if (c < f) {
-            __nv_bfloat16* hr = p.h + static_cast<size_t>(slot) * C::N2 * f + c;
+            __nv_bfloat16* hr = p.h + static_cast<size_t>(slot) * C::HR * f + c;
 #pragma unroll
             for (int t = 0; t < TP; ++t)
               if ((mask >> t) & 1u) {
@@ -588,16 +724,14 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     }
     part += static_cast<size_t>(grid) * 2 * TP * BM;
     {
-      const long long end = r2.start(cta + 1), blk = static_cast<long long>(nslots) * r2.len;
-      for (long long i = r2.start(cta); i < end;) {
-        const int db = static_cast<int>(i / blk);
-        const long long a = db * blk, b = a + blk, begin = i, stop = min(b, end);
+      const int end = r2.start(cta + 1), blk = nslots * r2.len;
+      for (int i = r2.start(cta); i < end;) {
+        const int db = i / blk, a = db * blk, b = a + blk, begin = i, stop = min(b, end);
         float o[TP];
 #pragma unroll
         for (int t = 0; t < TP; ++t) o[t] = 0.f;
         while (i < stop) {
-          const int u = static_cast<int>(i / r2.len);
-          const int slot = u - db * nslots, e = sexp[slot];
+          const int u = i / r2.len, slot = u - db * nslots, e = sexp[slot];
           // lane t holds token t's weight for this expert
           float wt = 0.f;
           if (lane < T)
@@ -611,9 +745,9 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
             const float w = __shfl_sync(0xffffffffu, wt, t);
             if ((mask >> t) & 1u) o[t] = fmaf(w, v[t], o[t]);
           }
-          i = min(static_cast<long long>(u + 1) * r2.len, stop);
+          i = min((u + 1) * r2.len, stop);
         }
-        const uint32_t all = T == 32 ? 0xffffffffu : (1u << T) - 1u;
+        const uint32_t all = T >= 32 ? 0xffffffffu : (1u << T) - 1u;
         if ((begin == a && stop == b) || join(r2, a, b, p.tiles + nslots * FB + db, all, o)) {
           const int c = db * BM + col;
           if (c < d) {
@@ -664,7 +798,14 @@ cudaError_t launch_tp(const CUtensorMap& mX, const CUtensorMap& mW1, const CUten
   return cudaLaunchKernelEx(&lc, few_kernel<TP>, mX, mW1, mW2, mH, p);
 }
 
-int padded_tokens(int T) { return T <= 8 ? 8 : (T <= 16 ? 16 : 32); }
+// Chunks of the gate's contraction, at most: what the threads that share a
+// logit add up, and one per CTA.
+int max_chunks(int E) {
+  const int n = fw::MAX_LOADS * (fw::THREADS / fw::expert_lanes(E));
+  return n < kFewMaxCtas ? n : kFewMaxCtas;
+}
+
+int padded_tokens(int T) { return T <= 1 ? 1 : (T <= 8 ? 8 : (T <= 16 ? 16 : 32)); }
 
 }  // namespace
 
@@ -680,7 +821,7 @@ FewLayout few_layout(int T, int d, int E, int k, int f) {
   };
   L.idx = take(R * 4);
   L.w = take(R * 4);
-  L.gpart = take(static_cast<size_t>(fw::MAX_CHUNKS) * T * E * 4);
+  L.gpart = take(static_cast<size_t>(max_chunks(E)) * T * E * 4);
   L.ntiles = slots * ceil_div(f, fw::BM) + ceil_div(d, fw::BM);
   L.tiles = take(L.ntiles * 4);
   L.h_rows = slots * 2 * TP;
@@ -708,14 +849,16 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
   p.f = f;
   p.k = rs.k;
   p.gate_groups = ceil_div(E, fw::GATE_E);
-  // chunks of the contraction: at least 32 rows each, at most one per CTA of
-  // an expert group
+  // chunks of the contraction: at least 32 rows each (a multiple of 8), at
+  // most one per CTA of an expert group, and every token's router on a CTA
   int chunks = grid / p.gate_groups;
-  if (chunks > fw::MAX_CHUNKS) chunks = fw::MAX_CHUNKS;
+  const int most = max_chunks(E);
+  if (chunks > most) chunks = most;
   if (chunks > d / 32) chunks = d / 32;
-  if (chunks < 1) return cudaErrorInvalidConfiguration;  // fewer SMs than expert groups
-  p.gate_len = ceil_div(d, chunks);
+  if (chunks < 1 || grid < T) return cudaErrorInvalidConfiguration;
+  p.gate_len = ceil_div(ceil_div(d, chunks), 8) * 8;
   p.gate_chunks = ceil_div(d, p.gate_len);
+  p.gate_vec = E % 8 == 0 && reinterpret_cast<uintptr_t>(Wg) % 16 == 0 ? 1 : 0;
   p.idx = reinterpret_cast<int32_t*>(base + L.idx);
   p.w = reinterpret_cast<float*>(base + L.w);
   p.gpart = reinterpret_cast<float*>(base + L.gpart);
@@ -734,6 +877,7 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
       !make_map_2d(&mH, p.h, L.h_rows, f, 64, 2 * TP))
     return cudaErrorInvalidValue;
   switch (TP) {
+    case 1: return launch_tp<1>(mX, mW1, mW2, mH, p, grid, s);
     case 8: return launch_tp<8>(mX, mW1, mW2, mH, p, grid, s);
     case 16: return launch_tp<16>(mX, mW1, mW2, mH, p, grid, s);
     default: return launch_tp<32>(mX, mW1, mW2, mH, p, grid, s);
