@@ -310,6 +310,7 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
 // Microscaled 4-bit rows and expert weights, and their grouped product.
 constexpr int kMx4MaxCtas = 160;    // the grid the product's partial sums are sized for
 constexpr int kMx4SplitRows = 32;   // a split launch's rows per expert, at most
+constexpr int kMx4PairRows = 128;   // rows per expert, on average, from which pairs of CTAs work
 // Row tiles (128 rows of one expert) that R rows of E experts can make.
 size_t mx4_row_tiles(int R, int E);
 cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,

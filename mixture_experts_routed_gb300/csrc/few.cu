@@ -41,6 +41,7 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "range.cuh"
 #include "tmap.cuh"
 #include "topk.cuh"
 
@@ -197,28 +198,6 @@ __device__ __forceinline__ void weigh_all(const float* row, int E, const RouterS
   topk::warp_soft_weigh<1>(v, id, E, rs, t, idx, w);
 }
 __device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
-
-// The steps of one phase (`units` accumulators of `len` steps, fewer than
-// 2^28 in all) and each CTA's range of them: start(c) = floor(total c / G).
-struct Range {
-  int len, total, G, q, r;
-  __device__ Range(int units, int len_, int grid) : len(len_) {
-    total = units * len;
-    G = total < grid ? total : grid;  // every range holds a step
-    q = G > 0 ? total / G : 0;
-    r = total - q * G;
-  }
-  __device__ int start(int c) const { return c >= G ? total : q * c + r * c / G; }
-  // the CTA whose range holds step i: an estimate, put right
-  __device__ int owner(int i) const {
-    int c = static_cast<int>((static_cast<float>(i) + 1.f) * static_cast<float>(G) /
-                             static_cast<float>(total));
-    c = c < G ? c : G - 1;
-    while (c > 0 && start(c) > i) --c;
-    while (c + 1 < G && start(c + 1) <= i) ++c;
-    return c;
-  }
-};
 }  // namespace fw
 
 template <int TP>
@@ -571,51 +550,53 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
-    if (lane == 0) {
-      int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
-      bool dead = false;
-      auto phase = [&](const Range& r, uint32_t idesc) {
-        const int end = r.start(cta + 1);
-        for (int i = r.start(cta); i < end && !dead;) {
-          const int n = min(r.len - i % r.len, end - i);
-          if (!mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs)) {
+    // (the whole warp, converged: tc_mma_f16_lead says why)
+    const uint32_t lead = lane == 0 ? 1u : 0u;
+    int s = 0, acc = 0;
+    uint32_t ph = 0, aph = 0;
+    bool dead = false;
+    const uint64_t ad0 = make_sdesc_sw128(smem_u32(smem), BOX_BYTES, 1024),
+                   bd0 = make_sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
+    auto phase = [&](const Range& r, uint32_t idesc) {
+      const int end = r.start(cta + 1);
+      for (int i = r.start(cta); i < end && !dead;) {
+        const int n = min(r.len - i % r.len, end - i);
+        if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs))) {
+          dead = true;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t dt = tmem_base + acc * 64;
+        for (int j = 0; j < n; ++j) {
+          if (!__all_sync(0xffffffffu, mbar_wait_spin(&full[s], ph, kWaitLimitNs))) {
             dead = true;
             break;
           }
           tc_fence_after();
-          const uint32_t dt = tmem_base + acc * 64;
-          for (int j = 0; j < n; ++j) {
-            if (!mbar_wait_spin(&full[s], ph, kWaitLimitNs)) {
-              dead = true;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + A_BYTES;
+          const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              tc_mma_f16(dt, make_sdesc_sw128(a + kk * 2048, BOX_BYTES, 1024),
-                         make_sdesc_sw128(b + kk * 32, 16, 1024), idesc, (j | kk) != 0 ? 1u : 0u);
-            tc_commit(&empty[s]);
-            if (++s == C::STAGES) {
-              s = 0;
-              ph ^= 1u;
-            }
+          for (int kk = 0; kk < BK / 16; ++kk)
+            tc_mma_f16_lead(lead, dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
+                            kk > 0 || j > 0 ? 1u : 0u);
+          tc_commit_lead(lead, &empty[s]);
+          if (++s == C::STAGES) {
+            s = 0;
+            ph ^= 1u;
           }
-          tc_commit(&tfull[acc]);
-          if (++acc == 2) {
-            acc = 0;
-            aph ^= 1u;
-          }
-          i += n;
         }
-      };
-      phase(r1, make_idesc_bf16_f32(BM, C::N1, true, false));
-      if (!dead) phase(r2, make_idesc_bf16_f32(BM, C::N2, true, false));
-      // nothing this thread issued may still run when tensor memory is freed
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0, kWaitLimitNs) || dead) atomicOr(p.err, kErrTimeout);
-    }
+        tc_commit_lead(lead, &tfull[acc]);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+        i += n;
+      }
+    };
+    phase(r1, make_idesc_bf16_f32(BM, C::N1, true, false));
+    if (!dead) phase(r2, make_idesc_bf16_f32(BM, C::N2, true, false));
+    // nothing this thread issued may still run when tensor memory is freed
+    tc_commit_lead(lead, drain);
+    if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue
     const int col = (warp & 3) * 32 + lane;  // feature of the block = TMEM lane

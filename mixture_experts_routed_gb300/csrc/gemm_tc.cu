@@ -1300,6 +1300,21 @@ bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t
   return r == CUDA_SUCCESS;
 }
 
+// 2-D map over chunks of 512 bytes, box [2 chunks].
+bool make_map_2d_chunks(CUtensorMap* m, const void* base, uint64_t chunks) {
+  auto enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {128, chunks};
+  const cuuint64_t strides[1] = {512};
+  const cuuint32_t box[2] = {128, 2};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // 2-D map over the row-major [rows, cols] output, box [32 rows][32 cols]:
 // fp32 (128-byte rows, 128-byte swizzle) for the fp32 pass, bf16 (64-byte
 // rows, 64-byte swizzle) for the SiLU pass, matching the staging blocks.

@@ -25,9 +25,11 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "ptx.cuh"
+#include "range.cuh"
 #include "tmap.cuh"
 
 namespace moe {
@@ -56,6 +58,15 @@ __device__ __forceinline__ float scale_value(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7fc00000u : (s == 0u ? 0x00400000u : s << 23));
 }
 
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_once(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 // 8 scaled values to 8 codes, v[0] lowest
 __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
   uint32_t r;
@@ -69,11 +80,14 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-__device__ __forceinline__ float code_value(uint32_t c) {
-  // magnitudes 0, .5 and (1 + m / 2) 2^(e - 1)
-  const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-  const float v = e == 0 ? 0.5f * m : __uint_as_float(((e + 126u) << 23) | (m << 22));
-  return c & 8u ? -v : v;
+// the values of the two codes in the low byte of c
+__device__ __forceinline__ float2 code_pair(uint32_t c) {
+  uint32_t h;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
+      : "=r"(h)
+      : "r"(c));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
 // The segments' row tiles: seg[e] = offsets[e], base[e] = row tiles before
@@ -131,72 +145,78 @@ __device__ __forceinline__ size_t row_scale_at(int r, const int* seg, const int*
 }
 
 // ---------------------------------------------------------------- rows
-// A warp quantises 256 (bf16) or 128 (fp32) consecutive values of a row: a
-// lane loads 16 bytes, a block's 4 (8) lanes agree on its amax, and a lane
-// stores 4 (2) bytes of codes. Bound by HBM: the row is read once.
+// A warp quantises `per` spans (256 bf16 or 128 fp32 values each) of a row: a
+// lane loads 16 bytes of a span, a block's 4 (8) lanes agree on its amax, and
+// a lane stores 4 (2) bytes of codes. Four spans are in flight at a time.
+// Bound by HBM: the row is read once.
 template <typename T>
 __global__ void __launch_bounds__(256)
     mx4_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
-                    const int32_t* __restrict__ offsets, int E, int R, int K,
+                    const int32_t* __restrict__ offsets, int E, int R, int K, int per,
                     uint8_t* __restrict__ q, uint8_t* __restrict__ sc, uint32_t* err) {
-  constexpr int V = 16 / sizeof(T), LPB = 32 / V, SPAN = 32 * V;
+  constexpr int V = 16 / sizeof(T), LPB = 32 / V, SPAN = 32 * V, F = 4;
   __shared__ int seg[kMaxExperts + 1], base[kMaxExperts + 1], ok;
   pdl_wait();
   pdl_trigger();
   if (!load_segments(offsets, E, R, seg, base, &ok, err)) return;
   const int lane = threadIdx.x & 31;
-  const int kc = up_div(K, 128), spans = up_div(K, SPAN);
-  const long long total = static_cast<long long>(seg[E] - seg[0]) * spans;
-  const long long step = static_cast<long long>(gridDim.x) * 8;
-  for (long long i = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); i < total;
-       i += step) {
-    const int r = seg[0] + static_cast<int>(i / spans), k = static_cast<int>(i % spans) * SPAN + lane * V;
-    int xr = src != nullptr ? __ldg(src + r) : r;
+  const int kc = up_div(K, 128);
+  const int k0 = blockIdx.y * per * SPAN, k1 = min(K, k0 + per * SPAN);
+  const int last = seg[E];
+  for (int r = seg[0] + blockIdx.x * 8 + (threadIdx.x >> 5); r < last; r += gridDim.x * 8) {
+    const int xr = src != nullptr ? __ldg(src + r) : r;
     const bool in = xr >= 0 && xr < x_rows;
     if (!in && lane == 0) atomicOr(err, kErrBadIndex);
-    uint4 raw = {0, 0, 0, 0};
-    if (in && k < K)
-      raw = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(xr) * K + k));
-    float v[8] = {};
-    if constexpr (V == 4) {
-      v[0] = __uint_as_float(raw.x);
-      v[1] = __uint_as_float(raw.y);
-      v[2] = __uint_as_float(raw.z);
-      v[3] = __uint_as_float(raw.w);
-    } else {
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+    const T* row = x + static_cast<size_t>(in ? xr : 0) * K;
+    uint8_t* qr = q + static_cast<size_t>(r) * (K / 2);
+    uint8_t* sr = sc + row_scale_at(r, seg, base, E, kc);
+    for (int kb = k0 + lane * V; kb - lane * V < k1; kb += F * SPAN) {
+      uint4 raw[F];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      for (int f = 0; f < F; ++f)
+        raw[f] = in && kb + f * SPAN < k1 ? ld_once(row + kb + f * SPAN) : uint4{0, 0, 0, 0};
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int k = kb + f * SPAN;
+        const uint32_t w[4] = {raw[f].x, raw[f].y, raw[f].z, raw[f].w};
+        // |v| orders as its bits do, infinities and NaN above every number
+        uint32_t m;
+        if constexpr (V == 8) {
+          m = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                       __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+#pragma unroll
+          for (int o = 1; o < LPB; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = max(m << 16, m & 0xffff0000u);
+        } else {
+          m = max(max(w[0] & 0x7fffffffu, w[1] & 0x7fffffffu),
+                  max(w[2] & 0x7fffffffu, w[3] & 0x7fffffffu));
+#pragma unroll
+          for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        }
+        const uint32_t s = scale_code(m);
+        const float inv = inv_scale(s);
+        float v[8] = {};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+          if constexpr (V == 8)
+            v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16) * inv;
+          else
+            v[j] = __uint_as_float(w[j]) * inv;
+        }
+        const uint32_t codes = pack8(v);
+        // the four blocks of a 128-value group, as one word from its first lane
+        uint32_t word = s | __shfl_down_sync(0xffffffffu, s, LPB) << 8;
+        word |= __shfl_down_sync(0xffffffffu, word, 2 * LPB) << 16;
+        if (k < k1) {
+          if constexpr (V == 8)
+            *reinterpret_cast<uint32_t*>(qr + k / 2) = codes;
+          else
+            *reinterpret_cast<uint16_t*>(qr + k / 2) = static_cast<uint16_t>(codes);
+          if (lane % (4 * LPB) == 0)
+            *reinterpret_cast<uint32_t*>(sr + static_cast<size_t>(k >> 7) * CHUNK) = word;
+        }
       }
     }
-    // |v| orders as its bits do, infinities and NaN above every number
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-#pragma unroll
-    for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const uint32_t s = scale_code(m);
-    const float inv = inv_scale(s);
-#pragma unroll
-    for (int j = 0; j < V; ++j) v[j] *= inv;
-    const uint32_t codes = pack8(v);
-    uint8_t* qr = q + static_cast<size_t>(r) * (K / 2) + k / 2;
-    if (k < K) {
-      if constexpr (V == 8)
-        *reinterpret_cast<uint32_t*>(qr) = codes;
-      else
-        *reinterpret_cast<uint16_t*>(qr) = static_cast<uint16_t>(codes);
-    }
-    // the four blocks of a 128-value group, as one word from its first lane
-    uint32_t word = s;
-#pragma unroll
-    for (int j = 1; j < 4; ++j)
-      word |= __shfl_down_sync(0xffffffffu, s, j * LPB) << (8 * j);
-    if (lane % (4 * LPB) == 0 && k < K)
-      *reinterpret_cast<uint32_t*>(sc + row_scale_at(r, seg, base, E, kc) +
-                                   static_cast<size_t>(k >> 7) * CHUNK) = word;
   }
 }
 
@@ -218,91 +238,131 @@ __global__ void __launch_bounds__(256)
     const float s = scale_value(__ldg(sc + row_scale_at(r, seg, base, E, kc) +
                                       static_cast<size_t>(k >> 7) * CHUNK + ((k >> 5) & 3)));
     T* o = out + static_cast<size_t>(r) * K + k;
+    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<T>(code_value((c >> (4 * j)) & 15u) * s);
+    for (int j = 0; j < 8; j += 2) {
+      const float2 f = code_pair(c >> (4 * j));
+      v[j] = f.x * s;
+      v[j + 1] = f.y * s;
+    }
+    if constexpr (sizeof(T) == 4) {
+      reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+      reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+      *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
 // ---------------------------------------------------------------- weights
 // W [E][K][N] -> codes [E][N][K / 2]: a block takes 256 (fp32: 128) values of
-// k x 64 of n through shared memory, so that both the rows of W and the runs
-// of codes are read and written in whole sectors; a thread quantises one
-// block of 32.
+// k x 64 of n through shared memory; a thread quantises two blocks of 32 of
+// one n, so that the rows of W and the runs of codes (32 bytes) are read and
+// written in whole sectors. Bound by HBM.
 template <typename T>
 constexpr int kWeightK = 512 / sizeof(T);
 template <typename T>
-constexpr int kWeightThreads = kWeightK<T> / 32 * 64;
+constexpr int kWeightThreads = kWeightK<T>;  // 64 n x (k / 64)
+
+// byte of the scale of column n, block k / 32 of expert e
+__device__ __forceinline__ size_t weight_scale_at(int e, int n, int k, int K, int N) {
+  return ((static_cast<size_t>(e) * up_div(N, 128) + (n >> 7)) * up_div(K, 128) + (k >> 7)) *
+             CHUNK +
+         (n & 31) * 16 + ((n & 127) >> 5) * 4 + ((k >> 5) & 3);
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kWeightThreads<T>)
     mx4_weights_kernel(const T* __restrict__ W, int K, int N, uint8_t* __restrict__ q,
                        uint8_t* __restrict__ sc) {
-  __shared__ __align__(16) T tile[kWeightK<T>][64];
+  constexpr int KT = kWeightK<T>, TH = kWeightThreads<T>, V = 16 / sizeof(T), PER = 64 / V;
+  __shared__ __align__(16) T tile[KT][64];
   pdl_wait();
   pdl_trigger();
-  const int n0 = blockIdx.x * 64, k0 = blockIdx.y * kWeightK<T>, e = blockIdx.z;
+  const int n0 = blockIdx.x * 64, k0 = blockIdx.y * KT, e = blockIdx.z;
   const T* We = W + static_cast<size_t>(e) * K * N;
-  constexpr int V = 16 / sizeof(T), PER = 64 / V;
-  for (int i = threadIdx.x; i < kWeightK<T> * PER; i += kWeightThreads<T>) {
-    const int k = i / PER, c = (i % PER) * V;
+#pragma unroll
+  for (int j = 0; j < KT * PER / TH; ++j) {
+    const int i = threadIdx.x + j * TH, k = i / PER, c = (i % PER) * V;
     if (k0 + k < K)
-      *reinterpret_cast<uint4*>(&tile[k][c]) =
-          __ldg(reinterpret_cast<const uint4*>(We + static_cast<size_t>(k0 + k) * N + n0 + c));
+      ptx::cp_async16(ptx::smem_u32(&tile[k][c]), We + static_cast<size_t>(k0 + k) * N + n0 + c);
   }
+  ptx::cp_async_commit();
+  ptx::cp_async_wait<0>();
   __syncthreads();
-  const int n = threadIdx.x & 63, kb = threadIdx.x >> 6;
-  if (k0 + kb * 32 >= K) return;
-  float v[32];
-  uint32_t m = 0;
+  const int n = threadIdx.x & 63, kt = (threadIdx.x >> 6) * 64;
+  if (k0 + kt >= K) return;  // (K is a multiple of 64)
+  uint32_t s2[2];
+  uint4 w4[2];
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
-    v[j] = static_cast<float>(tile[kb * 32 + j][n]);
-    m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  for (int h = 0; h < 2; ++h) {
+    float v[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      v[j] = static_cast<float>(tile[kt + h * 32 + j][n]);
+      m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+    s2[h] = scale_code(m);
+    const float inv = inv_scale(s2[h]);
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = v[8 * j + i] * inv;
+      w[j] = pack8(u);
+    }
+    w4[h] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  const uint32_t s = scale_code(m);
-  const float inv = inv_scale(s);
-  uint32_t w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = v[8 * j + i] * inv;
-    w[j] = pack8(u);
-  }
-  const size_t row = static_cast<size_t>(e) * N + n0 + n;
-  *reinterpret_cast<uint4*>(q + row * (K / 2) + (k0 + kb * 32) / 2) =
-      make_uint4(w[0], w[1], w[2], w[3]);
-  const int kc = up_div(K, 128), nt = up_div(N, 128), ni = n0 + n;
-  sc[((static_cast<size_t>(e) * nt + (ni >> 7)) * kc + ((k0 + kb * 32) >> 7)) * CHUNK +
-     (ni & 31) * 16 + ((ni & 127) >> 5) * 4 + (kb & 3)] = static_cast<uint8_t>(s);
+  uint4* o = reinterpret_cast<uint4*>(q + (static_cast<size_t>(e) * N + n0 + n) * (K / 2) +
+                                      (k0 + kt) / 2);
+  o[0] = w4[0];
+  o[1] = w4[1];
+  *reinterpret_cast<uint16_t*>(sc + weight_scale_at(e, n0 + n, k0 + kt, K, N)) =
+      static_cast<uint16_t>(s2[0] | s2[1] << 8);
 }
 
 template <typename T>
 __global__ void __launch_bounds__(kWeightThreads<T>)
     mx4_weights_back_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc, int K,
                             int N, T* __restrict__ W) {
-  __shared__ __align__(16) T tile[kWeightK<T>][64];
+  constexpr int KT = kWeightK<T>, TH = kWeightThreads<T>, V = 16 / sizeof(T), PER = 64 / V;
+  __shared__ __align__(16) T tile[KT][64];
   pdl_wait();
   pdl_trigger();
-  const int n0 = blockIdx.x * 64, k0 = blockIdx.y * kWeightK<T>, e = blockIdx.z;
-  const int n = threadIdx.x & 63, kb = threadIdx.x >> 6;
-  if (k0 + kb * 32 < K) {
-    const size_t row = static_cast<size_t>(e) * N + n0 + n;
-    const int kc = up_div(K, 128), nt = up_div(N, 128), ni = n0 + n;
-    const float s = scale_value(__ldg(
-        sc + ((static_cast<size_t>(e) * nt + (ni >> 7)) * kc + ((k0 + kb * 32) >> 7)) * CHUNK +
-        (ni & 31) * 16 + ((ni & 127) >> 5) * 4 + (kb & 3)));
-    const uint4 c = __ldg(reinterpret_cast<const uint4*>(q + row * (K / 2) + (k0 + kb * 32) / 2));
-    const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  const int n0 = blockIdx.x * 64, k0 = blockIdx.y * KT, e = blockIdx.z;
+  const int n = threadIdx.x & 63, kt = (threadIdx.x >> 6) * 64;
+  if (k0 + kt < K) {
+    const uint32_t s2 =
+        __ldg(reinterpret_cast<const uint16_t*>(sc + weight_scale_at(e, n0 + n, k0 + kt, K, N)));
+    const uint4* c = reinterpret_cast<const uint4*>(
+        q + (static_cast<size_t>(e) * N + n0 + n) * (K / 2) + (k0 + kt) / 2);
+    const uint4 both[2] = {ld_once(c), ld_once(c + 1)};
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      tile[kb * 32 + j][n] = static_cast<T>(code_value((w[j >> 3] >> (4 * (j & 7))) & 15u) * s);
+    for (int h = 0; h < 2; ++h) {
+      const uint4 c4 = both[h];
+      const float s = scale_value((s2 >> (8 * h)) & 255u);
+      const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float2 f = code_pair(w[j >> 3] >> (4 * (j & 7)));
+        tile[kt + h * 32 + j][n] = static_cast<T>(f.x * s);
+        tile[kt + h * 32 + j + 1][n] = static_cast<T>(f.y * s);
+      }
+    }
   }
   __syncthreads();
   T* We = W + static_cast<size_t>(e) * K * N;
-  constexpr int V = 16 / sizeof(T), PER = 64 / V;
-  for (int i = threadIdx.x; i < kWeightK<T> * PER; i += kWeightThreads<T>) {
-    const int k = i / PER, c0 = (i % PER) * V;
+#pragma unroll
+  for (int j = 0; j < KT * PER / TH; ++j) {
+    const int i = threadIdx.x + j * TH, k = i / PER, c0 = (i % PER) * V;
     if (k0 + k < K)
       *reinterpret_cast<uint4*>(We + static_cast<size_t>(k0 + k) * N + n0 + c0) =
           *reinterpret_cast<const uint4*>(&tile[k][c0]);
@@ -310,32 +370,42 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
 }
 
 // ---------------------------------------------------------------- product
-// Tiles of 128 rows of one expert x up to 256 columns, one CTA each,
+// Tiles of 128 rows of one expert x up to 256 columns on one CTA, or of 256
+// rows x 256 columns on a pair of CTAs (cta_group::2: each stages its own 128
+// rows and half of the columns, so a byte staged feeds twice the products);
 // persistent. A stage of the TMA ring holds 256 values of k: the rows' and
 // the weights' codes (128-byte rows, 128-byte swizzle, both k-major) and
-// their scale chunks. One thread copies a stage's scales to tensor memory
-// (tcgen05.cp, the 512 bytes of a chunk to 4 columns of each of the four
-// lane quarters) and issues the M128 N256 K64 products that read them; the
-// scales have columns of their own per stage, so a stage's copy never meets
-// a product still reading.
+// their scale chunks (of a pair's columns: all of them, on both sides). One
+// thread copies a stage's scales to tensor memory (tcgen05.cp, the 512 bytes
+// of a chunk to 4 columns of each of the four lane quarters) and issues the
+// products of 128 columns x K 64 that read them; the scales have columns of
+// their own per stage, so a stage's copy never meets a product still reading.
+// Three accumulators of 128 columns: a tile takes two, and the next tile
+// starts once the epilogue has drained one of them.
 namespace mx {
-constexpr int BM = 128, BN = 256, KS = 256;  // a stage's rows, columns, values of k
-constexpr int A_BYTES = BM * 128, B_BOX = 64 * 128, B_BYTES = BN / 64 * B_BOX;
-constexpr int SFA_BYTES = 2 * CHUNK, SFB_BYTES = 4 * CHUNK;
-constexpr int OFF_B = A_BYTES, OFF_SFA = OFF_B + B_BYTES, OFF_SFB = OFF_SFA + SFA_BYTES;
-constexpr int STAGE = OFF_SFB + SFB_BYTES;
-constexpr int STAGES = 4;
-constexpr int OFF_STG = STAGES * STAGE;  // 4 KB an epilogue warp
-constexpr int OFF_BAR = OFF_STG + 4 * 4096;
-constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 3) * 8 + 24;
-constexpr int SMEM = OFF_SEG + 2 * (kMaxExperts + 1) * 4 + 1024;
-constexpr int TMEM_COLS = 512, SF_COL = 256, SF_STAGE = 24;
+constexpr int BN = 256, HN = 128, KS = 256;  // a tile's columns, an accumulator's, a stage's k
+constexpr int A_BOX = 32 * 128, B_BOX = 64 * 128;  // boxes of 32 rows, 64 columns
+constexpr int A_BYTES = 128 * 128;
+constexpr int SF_COL = 384, SF_STAGE = 24;  // tensor memory columns: 3 x 128, then scales
+constexpr int TMEM_COLS = 512, ACCS = 3;
 constexpr int THREADS = 256;
-static_assert(STAGE % 1024 == 0 && OFF_BAR % 8 == 0 && SMEM <= 227 * 1024, "shared memory");
+
+template <bool PAIR>
+struct Cfg {
+  static constexpr int BM = PAIR ? 256 : 128;
+  static constexpr int B_BYTES = (PAIR ? 128 : 256) * 128;
+  static constexpr int OFF_B = A_BYTES, OFF_SFA = OFF_B + B_BYTES, OFF_SFB = OFF_SFA + 2 * CHUNK;
+  static constexpr int STAGE = OFF_SFB + 4 * CHUNK;
+  static constexpr int STAGES = PAIR ? 5 : 4;
+  static constexpr int OFF_STG = STAGES * STAGE;  // 4 KB an epilogue warp
+  static constexpr int OFF_BAR = OFF_STG + 4 * 4096;
+  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
+  static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
+  static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
+  static_assert(SF_COL + STAGES * SF_STAGE <= TMEM_COLS, "tensor memory");
+};
 
 struct Params {
-  const uint8_t* as;
-  const uint8_t* ws;
   const int32_t* offsets;
   void* out;
   uint32_t* err;
@@ -346,28 +416,63 @@ struct Params {
 };
 
 // kind::mxf4, E2M1 both sides, E8M0 scales, fp32 accumulator, both K-major,
-// M = 128, K = 64; sf: which half of a scale column's four bytes
-__device__ __forceinline__ uint32_t idesc_mxf4(int n, uint32_t sf) {
+// K = 64; sf: which half of a scale column's four bytes
+__device__ __forceinline__ uint32_t idesc_mxf4(int m, int n, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
-         (1u << 27) | (sf << 29);
+         (static_cast<uint32_t>(m >> 7) << 27) | (sf << 29);
 }
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+// (lead: as tc_mma_f16_lead)
+template <bool PAIR>
+__device__ __forceinline__ void mma_mxf4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                         uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.ne.b32 q, %7, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+        : "memory");
 }
 // 32 rows of 16 bytes, contiguous, to 4 columns of all four lane quarters
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t saddr) {
-  // no swizzle; 8-row groups 128 bytes apart; descriptor version 1
-  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-                        (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-               : "memory");
+// (of a pair: in each CTA from its own shared memory). The descriptor: no
+// swizzle, 8-row groups 128 bytes apart, version 1.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
+}
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t lead, uint32_t taddr, uint64_t desc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
+        "l"(desc), "r"(lead)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
+        "l"(desc), "r"(lead)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+  if constexpr (PAIR)
+    tc_commit_pair_mc_lead(lead, bar, 0x3);
+  else
+    tc_commit_lead(lead, bar);
 }
 __device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
@@ -375,14 +480,17 @@ struct Tile {
   int e, row0, rows, mt, n0, n;
 };
 // Tile t: expert by expert, column blocks outside, row tiles inside, so that
-// the CTAs at work side by side share a column block's weights.
-__device__ __forceinline__ Tile tile_at(int t, const int* seg, const int* base, int E, int N) {
+// the CTAs at work side by side share a column block's weights. tb: tiles of
+// BM rows before each expert; base: tiles of 128 rows (scale chunks).
+template <int BM>
+__device__ __forceinline__ Tile tile_at(int t, const int* seg, const int* base, const int* tb,
+                                        int E, int N) {
   const int nt = up_div(N, BN);
   Tile r;
-  r.e = last_at_most(base, E - 1, t / nt);
-  const int l = t - base[r.e] * nt, m = base[r.e + 1] - base[r.e];
+  r.e = last_at_most(tb, E - 1, t / nt);
+  const int l = t - tb[r.e] * nt, m = tb[r.e + 1] - tb[r.e];
   const int nb = l / m, mt = l - nb * m;
-  r.mt = base[r.e] + mt;
+  r.mt = base[r.e] + mt * (BM / 128);
   r.row0 = seg[r.e] + mt * BM;
   r.rows = min(BM, seg[r.e + 1] - r.row0);
   r.n0 = nb * BN;
@@ -394,27 +502,33 @@ __device__ __forceinline__ Tile tile_at(int t, const int* seg, const int* base, 
 __device__ __forceinline__ float mx_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
 // TO: the output type
-template <typename TO>
+template <bool PAIR, typename TO>
 __global__ void __launch_bounds__(mx::THREADS, 1)
     mx4_product_kernel(const __grid_constant__ CUtensorMap tmA,
-                       const __grid_constant__ CUtensorMap tmB, const mx::Params p) {
+                       const __grid_constant__ CUtensorMap tmB,
+                       const __grid_constant__ CUtensorMap tmSA,
+                       const __grid_constant__ CUtensorMap tmSB, const mx::Params p) {
   using namespace mx;
+  using C = Cfg<PAIR>;
+  constexpr int STAGES = C::STAGES, BM = C::BM;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // pair: the even CTA's
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + 1;
-  uint64_t* drain = tempty + 1;
+  uint64_t* tempty = tfull + ACCS;  // pair: the even CTA's
+  uint64_t* drain = tempty + ACCS;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* s_ok = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* s_last = tmem_slot + 2;
   int* s_wide = reinterpret_cast<int*>(tmem_slot + 3);
-  int* seg = reinterpret_cast<int*>(smem + OFF_SEG);
+  int* seg = reinterpret_cast<int*>(smem + C::OFF_SEG);
   int* base = seg + kMaxExperts + 1;
+  int* tb = PAIR ? base + kMaxExperts + 1 : base;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int cta = blockIdx.x, grid = gridDim.x;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const int cta = PAIR ? blockIdx.x >> 1 : blockIdx.x, grid = PAIR ? gridDim.x >> 1 : gridDim.x;
   const int E = p.E, K = p.K, N = p.N;
 
   if (tid == 0) {
@@ -422,40 +536,61 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    mbar_init(tfull, 1);
-    mbar_init(tempty, 4);
+    for (int i = 0; i < ACCS; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], PAIR ? 8 : 4);
+    }
     mbar_init(drain, 1);
     *s_wide = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, TMEM_COLS);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
   }
   pdl_wait();
   pdl_trigger();
   const bool ok = load_segments(p.offsets, E, p.R, seg, base, s_ok, p.err);
   for (int e = tid; ok && e < E; e += THREADS)
     if (seg[e + 1] - seg[e] > kMx4SplitRows) *s_wide = 1;
+  if (PAIR && warp == 0) {
+    // tiles of 256 rows before each expert
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane, n = e < E ? (base[e + 1] - base[e] + 1) / 2 : 0;
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < E) tb[e] = run + inc - n;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) tb[E] = run;
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers exist before anyone signals them
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const int kst = up_div(K, KS), kc = up_div(K, 128);
-  const int tiles = ok ? base[E] * up_div(N, BN) : 0;
+  const int tiles = ok ? tb[E] * up_div(N, BN) : 0;
   // Few rows everywhere and fewer tiles than CTAs: the tiles' stages are one
   // sequence cut into equal ranges, and a tile's partial sums are joined by
   // the last CTA to arrive, in CTA order. Otherwise whole tiles in turn.
-  const bool split = tiles < grid && *s_wide == 0;
-  const int total = split ? tiles * kst : 0, G = min(grid, total);
-  auto start = [&](int c) {
-    return c >= G ? total : static_cast<int>(static_cast<long long>(total) * c / G);
-  };
+  const bool split = !PAIR && tiles < grid && *s_wide == 0;
+  const Range rg(split ? tiles : 0, kst, grid);
   // Walk this CTA's pieces: f(tile, first stage, end stage)
   auto walk = [&](auto f) {
     if (split) {
-      const int end = start(cta + 1);
-      for (int i = start(cta); i < end;) {
+      const int end = rg.start(cta + 1);
+      for (int i = rg.start(cta); i < end;) {
         const int t = i / kst, k0 = i - t * kst, k1 = min(kst, k0 + end - i);
         if (!f(t, k0, k1)) return;
         i += k1 - k0;
@@ -470,31 +605,52 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     if (lane == 0) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmB);
+      prefetch_tmap(&tmSA);
+      prefetch_tmap(&tmSB);
       int s = 0, used = 0;
       uint32_t ph = 0;
       bool dead = false;
+      const uint32_t leader_full = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
       walk([&](int t, int k0, int k1) {
-        const Tile tl = tile_at(t, seg, base, E, N);
-        const int nb = tl.n / 64, nj = up_div(tl.n, 128), nt = up_div(N, 128);
-        const uint8_t* as = p.as + static_cast<size_t>(tl.mt) * kc * CHUNK;
-        const uint8_t* ws = p.ws + (static_cast<size_t>(tl.e) * nt + tl.n0 / 128) * kc * CHUNK;
+        const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
+        const int nt = up_div(N, HN), nj = up_div(tl.n, HN);
+        // boxes of 32 rows and of 64 columns of CTA r; a box that is not
+        // loaded feeds only sums that are not stored
+        auto a_boxes = [&](int r) { return min(4, max(0, up_div(tl.rows - r * 128, 32))); };
+        auto b_boxes = [&](int r) {
+          if (!PAIR) return tl.n / 64;
+          const int left = tl.n - r * 64;
+          return (left > 0) + (left > HN);
+        };
+        auto bytes = [&](int r) {
+          const int na = a_boxes(r);
+          return na * A_BOX + b_boxes(r) * B_BOX + ((na > 0 ? 1 : 0) + nj) * 2 * CHUNK;
+        };
+        const int na = a_boxes(rank), nb = b_boxes(rank);
+        const uint32_t expect = PAIR ? bytes(0) + bytes(1) : bytes(0);
+        const int mt = tl.mt + rank, row0 = tl.row0 + rank * 128;
         for (int kb = k0; kb < k1; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs)) {
             dead = true;
             return false;
           }
           if (used < STAGES) ++used;
-          uint8_t* st = smem + s * STAGE;
-          const uint32_t sf = static_cast<uint32_t>(min(2, kc - 2 * kb)) * CHUNK;
-          mbar_arrive_expect_tx(&full[s], A_BYTES + nb * B_BOX + (1 + nj) * sf);
-          tma_load_2d(st, &tmA, &full[s], kb * 128, tl.row0);
+          uint8_t* st = smem + s * C::STAGE;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
+          auto load = [&](int off, const CUtensorMap* m, int c0, int c1) {
+            if constexpr (PAIR)
+              tma_load_2d_pair(st + off, m, leader_full + s * 8, c0, c1);
+            else
+              tma_load_2d(st + off, m, &full[s], c0, c1);
+          };
           for (int b = 0; b < nb; ++b)
-            tma_load_2d(st + OFF_B + b * B_BOX, &tmB, &full[s], kb * 128,
-                        tl.e * N + tl.n0 + b * 64);
-          bulk_load(st + OFF_SFA, as + static_cast<size_t>(kb) * 2 * CHUNK, sf, &full[s]);
+            load(C::OFF_B + b * B_BOX, &tmB, kb * 128,
+                 tl.e * N + tl.n0 + (PAIR ? b * HN + static_cast<int>(rank) * 64 : b * 64));
+          for (int b = 0; b < na; ++b) load(b * A_BOX, &tmA, kb * 128, row0 + b * 32);
+          if (na > 0) load(C::OFF_SFA, &tmSA, 0, mt * kc + kb * 2);
           for (int j = 0; j < nj; ++j)
-            bulk_load(st + OFF_SFB + j * 2 * CHUNK,
-                      ws + (static_cast<size_t>(j) * kc + kb * 2) * CHUNK, sf, &full[s]);
+            load(C::OFF_SFB + j * 2 * CHUNK, &tmSB, 0,
+                 (tl.e * nt + tl.n0 / HN + j) * kc + kb * 2);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
@@ -502,8 +658,9 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         }
         return true;
       });
-      // the latest use of each stage has landed before this CTA may exit
-      for (int j = 0; j < used; ++j) {
+      // the latest use of each stage has landed before this CTA may exit (a
+      // pair: the even CTA's barrier counts both, and both exit together)
+      for (int j = 0; rank == 0 && j < used; ++j) {
         if (s == 0) {
           s = STAGES;
           ph ^= 1u;
@@ -517,115 +674,171 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
       if (dead) atomicOr(p.err, kErrTimeout);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int s = 0;
+    // (the whole warp, converged: tc_mma_f16_lead says why)
+    if (rank == 0) {
+      const uint32_t lead = lane == 0 ? 1u : 0u;
+      int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool dead = false;
+      const uint32_t base0 = smem_u32(smem);
+      const uint64_t ad0 = make_sdesc_sw128(base0, 16, 1024),
+                     bd0 = make_sdesc_sw128(base0 + C::OFF_B, 16, 1024),
+                     sa0 = scales_desc(base0 + C::OFF_SFA), sb0 = scales_desc(base0 + C::OFF_SFB);
+      constexpr int B_HALF = (PAIR ? 1 : 2) * B_BOX;
+      const uint32_t id0 = idesc_mxf4(BM, HN, 0), id2 = idesc_mxf4(BM, HN, 2);
+      // one stage's scales and products (inlined with constants for a whole one)
+      auto stage = [&](int chunks, int steps, int nj, uint32_t d0, uint32_t d1, uint32_t more) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
+#pragma unroll
+        for (int c = 0; c < chunks; ++c) {
+          cp_scales<PAIR>(lead, sf + c * 4, sa0 + off + c * (CHUNK / 16));
+#pragma unroll
+          for (int j = 0; j < nj; ++j)
+            cp_scales<PAIR>(lead, sf + 8 + c * 8 + j * 4,
+                            sb0 + off + (2 * j + c) * (CHUNK / 16));
+        }
+#pragma unroll
+        for (int kk = 0; kk < steps; ++kk)
+#pragma unroll
+          for (int j = 0; j < nj; ++j)
+            mma_mxf4<PAIR>(lead, j == 0 ? d0 : d1, ad0 + off + kk * 2,
+                           bd0 + off + j * (B_HALF / 16) + kk * 2, (kk & 1) ? id2 : id0,
+                           sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8 + j * 4,
+                           kk > 0 ? 1u : more);
+      };
       walk([&](int t, int k0, int k1) {
-        const Tile tl = tile_at(t, seg, base, E, N);
-        const int nj = up_div(tl.n, 128);
-        if (!mbar_wait(tempty, aph ^ 1u, kWaitLimitNs)) {
+        const int n = tile_at<BM>(t, seg, base, tb, E, N).n;
+        const int nj = n > HN ? 2 : 1;
+        const int acc1 = acc + 1 == ACCS ? 0 : acc + 1;
+        const uint32_t aph1 = acc + 1 == ACCS ? aph ^ 1u : aph;
+        bool ready = mbar_wait_spin_cluster(&tempty[acc], aph ^ 1u, kWaitLimitNs);
+        if (nj == 2 && ready)
+          ready = mbar_wait_spin_cluster(&tempty[acc1], aph1 ^ 1u, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, ready)) {
           dead = true;
           return false;
         }
         tc_fence_after();
+        const uint32_t d0 = tmem_base + acc * HN, d1 = tmem_base + acc1 * HN;
         for (int kb = k0; kb < k1; ++kb) {
-          if (!mbar_wait_spin(&full[s], ph, kWaitLimitNs)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_spin(&full[s], ph, kWaitLimitNs))) {
             dead = true;
             break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem + s * STAGE), b = a + OFF_B;
-          const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
-          const int chunks = min(2, kc - 2 * kb), steps = min(4, (K - kb * KS) / 64);
-          for (int c = 0; c < chunks; ++c) {
-            cp_scales(sf + c * 4, a + OFF_SFA + c * CHUNK);
-            for (int j = 0; j < nj; ++j)
-              cp_scales(sf + 8 + c * 8 + j * 4, a + OFF_SFB + (2 * j + c) * CHUNK);
-          }
-          for (int kk = 0; kk < steps; ++kk)
-            mma_mxf4(tmem_base, make_sdesc_sw128(a + kk * 32, 16, 1024),
-                     make_sdesc_sw128(b + kk * 32, 16, 1024), idesc_mxf4(tl.n, (kk & 1) * 2),
-                     sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8, (kb > k0 || kk > 0) ? 1u : 0u);
-          tc_commit(&empty[s]);
+          const uint32_t more = kb > k0 ? 1u : 0u;
+          const int left = K - kb * KS;
+          if (left >= KS && nj == 2)
+            stage(2, 4, 2, d0, d1, more);
+          else
+            stage(left > 128 ? 2 : 1, min(4, left / 64), nj, d0, d1, more);
+          commit<PAIR>(lead, &empty[s]);
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        tc_commit(tfull);
-        aph ^= 1u;
+        for (int j = 0; j < nj; ++j) {
+          commit<PAIR>(lead, &tfull[acc]);
+          if (++acc == ACCS) {
+            acc = 0;
+            aph ^= 1u;
+          }
+        }
         return !dead;
       });
-      tc_commit(drain);
-      if (!mbar_wait(drain, 0, kWaitLimitNs) || dead) atomicOr(p.err, kErrTimeout);
+      if constexpr (PAIR)
+        tc_commit_pair_mc_lead(lead, drain, 0x1);
+      else
+        tc_commit_lead(lead, drain);
+      if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
     }
   } else if (warp >= 4) {
     const int w = warp & 3;
-    uint8_t* stg = smem + OFF_STG + w * 4096;
+    uint8_t* stg = smem + C::OFF_STG + w * 4096;
+    int acc = 0;
     uint32_t aph = 0;
     bool dead = false;
     TO* out = static_cast<TO*>(p.out);
+    const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
     auto put = [&](size_t row, int col, float4 v) {
       if (p.silu) v = make_float4(mx_silu(v.x), mx_silu(v.y), mx_silu(v.z), mx_silu(v.w));
       TO* o = out + row * N + col;
       if constexpr (sizeof(TO) == 4) {
         *reinterpret_cast<float4*>(o) = v;
       } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y),
+                             hi = __floats2bfloat162_rn(v.z, v.w);
         *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
                                                   *reinterpret_cast<const uint32_t*>(&hi));
       }
     };
     walk([&](int t, int k0, int k1) {
-      const Tile tl = tile_at(t, seg, base, E, N);
+      const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
       const bool whole = k0 == 0 && k1 == kst;
-      const int a = t * kst;
+      // rows of this warp's 32 lanes
+      const int r0 = static_cast<int>(rank) * 128 + w * 32, rows = min(32, tl.rows - r0);
+      const int first = split ? rg.owner(t * kst) : 0;
+      // a CTA's part of the tile its range starts in comes first, of the one
+      // it ends in second
       auto slice = [&](int c) {
-        return p.part + (static_cast<size_t>(c) * 2 + (start(c) > a ? 0 : 1)) * kMx4SplitRows * BN;
+        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * BN;
       };
-      // after a wait that ran out the loops go on, so that the four warps
-      // still meet at every barrier
-      if (!dead && !mbar_wait(tfull, aph, kWaitLimitNs)) dead = true;
-      dead = __any_sync(0xffffffffu, dead);
-      aph ^= 1u;
-      tc_fence_after();
-      for (int c0 = 0; c0 < tl.n; c0 += 32) {
-        if (w * 32 < tl.rows) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(w * 32) << 16) + c0, r);
-          tmem_ld_wait();
-          // 32 x 32 through shared memory, 16-byte pieces swizzled by row
-          __syncwarp();
+      for (int h = 0; h < tl.n; h += HN) {
+        // after a wait that ran out the loops go on, so that the four warps
+        // still meet at every barrier
+        if (!dead && !mbar_wait(&tfull[acc], aph, kWaitLimitNs)) dead = true;
+        dead = __any_sync(0xffffffffu, dead);
+        tc_fence_after();
+        if (rows > 0) {
+#pragma unroll 1
+          for (int c0 = 0; c0 < min(HN, tl.n - h); c0 += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(
+                tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN + c0, r);
+            tmem_ld_wait();
+            // 32 x 32 through shared memory, 16-byte pieces swizzled by row
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-          __syncwarp();
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+                  make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+            __syncwarp();
+            const int c4 = lane & 7, col = h + c0 + c4 * 4;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int row = j * 4 + (lane >> 3), c4 = lane & 7;
-            const float4 v =
-                *reinterpret_cast<const float4*>(stg + row * 128 + ((c4 ^ (row & 7)) * 16));
-            if (w * 32 + row < tl.rows) {
-              if (whole)
-                put(tl.row0 + w * 32 + row, tl.n0 + c0 + c4 * 4, v);
-              else  // (at most kMx4SplitRows rows: warp 0's)
-                __stcg(reinterpret_cast<float4*>(slice(cta) + row * BN + c0 + c4 * 4), v);
+            for (int j = 0; j < 8; ++j) {
+              const int row = j * 4 + (lane >> 3);
+              const float4 v =
+                  *reinterpret_cast<const float4*>(stg + row * 128 + ((c4 ^ (row & 7)) * 16));
+              if (row < rows) {
+                if (whole)
+                  put(static_cast<size_t>(tl.row0 + r0 + row), tl.n0 + col, v);
+                else  // (at most kMx4SplitRows rows: warp 0's)
+                  __stcg(reinterpret_cast<float4*>(slice(cta) + row * BN + col), v);
+              }
             }
           }
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_remote(leader_tempty + acc * 8);
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+        if (++acc == ACCS) {
+          acc = 0;
+          aph ^= 1u;
+        }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(tempty);
       if (!whole) {
-        const int c0 = static_cast<int>((static_cast<long long>(a + 1) * G - 1) / total);
-        const int c1 = static_cast<int>((static_cast<long long>(a + kst) * G - 1) / total);
+        const int last_cta = rg.owner((t + 1) * kst - 1);
         __threadfence();
         bar_epi();
         if (tid == 128) {
-          const bool last = atomicAdd(p.ctr + t, 1u) == static_cast<uint32_t>(c1 - c0);
+          const bool last = atomicAdd(p.ctr + t, 1u) == static_cast<uint32_t>(last_cta - first);
           if (last) p.ctr[t] = 0;
           *s_last = last ? 1u : 0u;
         }
@@ -636,14 +849,22 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
           for (int i = tid - 128; i < tl.rows * quads; i += 128) {
             const int row = i / quads, col = (i - row * quads) * 4;
             float4 v = {0.f, 0.f, 0.f, 0.f};
-            for (int c = c0; c <= c1; ++c) {
-              const float4 o = __ldcg(reinterpret_cast<const float4*>(slice(c) + row * BN + col));
-              v.x += o.x;
-              v.y += o.y;
-              v.z += o.z;
-              v.w += o.w;
+            for (int cb = first; cb <= last_cta; cb += 8) {
+              float4 o[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                o[j] = cb + j <= last_cta
+                           ? __ldcg(reinterpret_cast<const float4*>(slice(cb + j) + row * BN + col))
+                           : float4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                v.x += o[j].x;
+                v.y += o[j].y;
+                v.z += o[j].z;
+                v.w += o[j].w;
+              }
             }
-            put(tl.row0 + row, tl.n0 + col, v);
+            put(static_cast<size_t>(tl.row0 + row), tl.n0 + col, v);
           }
         }
       }
@@ -653,8 +874,39 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+template <bool PAIR, typename TO>
+cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mSA,
+                           const CUtensorMap& mSB, const mx::Params& p, int grid, cudaStream_t s) {
+  using C = mx::Cfg<PAIR>;
+  auto* kernel = mx4_product_kernel<PAIR, TO>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(PAIR ? grid / 2 * 2 : grid);
+  lc.blockDim = dim3(mx::THREADS);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&lc, kernel, mA, mB, mSA, mSB, p);
 }
 
 int blocks_for(long long items, int per_block, int most) {
@@ -669,13 +921,19 @@ size_t mx4_row_tiles(int R, int E) { return static_cast<size_t>(R / 128) + (R < 
 cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,
                             const int32_t* offsets, int E, int R, int K, uint8_t* q, uint8_t* sc,
                             uint32_t* err, int num_sms, cudaStream_t s) {
-  const int span = dtype == 0 ? 128 : 256;
-  const dim3 grid(blocks_for(static_cast<long long>(R) * up_div(K, span), 8, num_sms * 8));
-  return dtype == 0 ? launch_pdl(mx4_rows_kernel<float>, grid, dim3(256), 0, s,
-                                 static_cast<const float*>(x), src, x_rows, offsets, E, R, K, q, sc, err)
-                    : launch_pdl(mx4_rows_kernel<__nv_bfloat16>, grid, dim3(256), 0, s,
-                                 static_cast<const __nv_bfloat16*>(x), src, x_rows, offsets, E, R, K, q,
-                                 sc, err);
+  // whole rows to a warp where there are enough rows, else a few spans
+  const int span = dtype == 0 ? 128 : 256, spans = up_div(K, span), warps = num_sms * 32;
+  int cuts = R >= warps ? 1 : (warps + R - 1) / R;
+  if (cuts > up_div(spans, 4)) cuts = up_div(spans, 4);
+  const int per = up_div(up_div(spans, cuts), 4) * 4;
+  const dim3 grid(blocks_for(R, 8, num_sms * 8), up_div(spans, per));
+  return dtype == 0
+             ? launch_pdl(mx4_rows_kernel<float>, grid, dim3(256), 0, s,
+                          static_cast<const float*>(x), src, x_rows, offsets, E, R, K, per, q, sc,
+                          err)
+             : launch_pdl(mx4_rows_kernel<__nv_bfloat16>, grid, dim3(256), 0, s,
+                          static_cast<const __nv_bfloat16*>(x), src, x_rows, offsets, E, R, K, per,
+                          q, sc, err);
 }
 
 cudaError_t launch_mx4_rows_back(int dtype, const uint8_t* q, const uint8_t* sc,
@@ -710,18 +968,21 @@ cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8
                                const uint8_t* wsc, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,
                                uint32_t* ctr, float* part, int num_sms, cudaStream_t s) {
-  using namespace mx;
-  CUtensorMap mA, mB;
-  if (!make_map_2d_bytes(&mA, aq, R, K / 2, 128) ||
-      !make_map_2d_bytes(&mB, wq, static_cast<uint64_t>(E) * N, K / 2, 64))
+  CUtensorMap mA, mB, mSA, mSB;
+  const uint64_t kc = up_div(K, 128);
+  if (!make_map_2d_bytes(&mA, aq, R, K / 2, 32) ||
+      !make_map_2d_bytes(&mB, wq, static_cast<uint64_t>(E) * N, K / 2, 64) ||
+      !make_map_2d_chunks(&mSA, as, mx4_row_tiles(R, E) * kc) ||
+      !make_map_2d_chunks(&mSB, wsc, static_cast<uint64_t>(E) * up_div(N, 128) * kc))
     return cudaErrorInvalidValue;
-  const Params p{as, wsc, offsets, out, err, ctr, part, E, R, K, N, silu};
+  const mx::Params p{offsets, out, err, ctr, part, E, R, K, N, silu};
   const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
-  auto go = [&](auto kernel) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    return e != cudaSuccess ? e : launch_pdl(kernel, dim3(grid), dim3(THREADS), SMEM, s, mA, mB, p);
-  };
-  return out_f32 ? go(mx4_product_kernel<float>) : go(mx4_product_kernel<__nv_bfloat16>);
+  const bool pair = R >= kMx4PairRows * E;
+  if (pair)
+    return out_f32 ? launch_product<true, float>(mA, mB, mSA, mSB, p, grid, s)
+                   : launch_product<true, __nv_bfloat16>(mA, mB, mSA, mSB, p, grid, s);
+  return out_f32 ? launch_product<false, float>(mA, mB, mSA, mSB, p, grid, s)
+                 : launch_product<false, __nv_bfloat16>(mA, mB, mSA, mSB, p, grid, s);
 }
 
 }  // namespace moe

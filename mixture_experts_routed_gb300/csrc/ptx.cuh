@@ -215,6 +215,42 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint
       : "memory");
 }
 
+// The two above for a warp that runs its issue loop converged: every lane
+// executes the call and the one with `lead` != 0 (always the same) issues.
+// The operands are then uniform values of a converged warp; issued from a
+// one-lane branch instead, each product cost about 130 clocks of moving them
+// to uniform registers.
+__device__ __forceinline__ void tc_mma_f16_lead(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
+                                                uint64_t bdesc, uint32_t idesc,
+                                                uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
+          smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_mc_lead(uint32_t lead, uint64_t* bar,
+                                                       uint16_t cta_mask) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;\n\t}\n" ::"r"(smem_u32(bar)),
+      "h"(cta_mask), "r"(lead)
+      : "memory");
+}
+
 // Warp reads 32 TMEM lanes x 32 consecutive 32-bit columns: thread i gets
 // lane (base lane + i), columns [col, col + 32).
 __device__ __forceinline__ void tmem_ld_32x32b_x32(uint32_t taddr, uint32_t (&r)[32]) {

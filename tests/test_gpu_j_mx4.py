@@ -176,7 +176,15 @@ def test_products(cuda_ok, counts, K, N):
     product(counts, K, N, seed=K + N + len(counts))
 
 
-@pytest.mark.parametrize("counts", [[2, 1], [200, 100]])
+# many rows per expert: pairs of blocks, 256 rows a tile; the second block's rows none, one,
+# some or all
+@pytest.mark.parametrize("counts", [[128], [257], [513, 0], [300, 129, 1, 600], [1500, 0, 2, 40]])
+@pytest.mark.parametrize("K,N", [(64, 64), (192, 128), (256, 320), (1408, 192), (2048, 1472)])
+def test_pairs(cuda_ok, counts, K, N):
+    product(counts, K, N, seed=K + N + len(counts))
+
+
+@pytest.mark.parametrize("counts", [[2, 1], [200, 100], [400, 130]])
 @pytest.mark.parametrize("silu", [0, 1])
 def test_bf16_and_silu(cuda_ok, counts, silu):
     product(counts, 512, 384, "bf16", silu, seed=silu)
@@ -185,15 +193,17 @@ def test_bf16_and_silu(cuda_ok, counts, silu):
 def test_many_experts_and_more_tiles_than_blocks(cuda_ok):
     product([i % 5 for i in range(256)], 256, 320, seed=1)
     product([i * 9 % 140 for i in range(64)], 320, 1408, "bf16", seed=2)
+    product([i * 97 % 700 for i in range(32)], 320, 1408, "bf16", seed=3)
 
 
 def test_long_contraction(cuda_ok):
     product([1, 1], 4096, 1408, seed=5)
     product([140], 7168, 576, seed=6)
+    product([300], 7168, 320, seed=7)
 
 
 def test_nan_blocks_reach_their_rows_and_columns_only(cuda_ok):
-    for counts in ([3, 2], [100, 60]):
+    for counts in ([3, 2], [100, 60], [300, 290]):
         c, q, sc, wq, wsc, off, ws, out = product(counts, 256, 192, seed=7)
         x = moe.mx4_dequantize_rows(c, q, sc, off)
         x[1, 70] = float("nan")
@@ -210,7 +220,7 @@ def test_nan_blocks_reach_their_rows_and_columns_only(cuda_ok):
 
 
 def test_same_bits_again_and_in_a_graph(cuda_ok):
-    for counts in ([2, 0, 1], [150, 3, 99]):
+    for counts in ([2, 0, 1], [150, 3, 99], [700, 300, 90]):
         c, q, sc, wq, wsc, off, ws, out = product(counts, 2048, 320, seed=8)
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
