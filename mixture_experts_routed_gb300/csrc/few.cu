@@ -445,109 +445,108 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       p.out[i] = __float2bfloat16(0.f);
   } else if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
+    // (the whole warp, converged: tc_mma_f16_lead says why)
+    const uint32_t lead = lane == 0 ? 1u : 0u;
     if (lane == 0) {
       prefetch_tmap(&tmX);
       prefetch_tmap(&tmW1);
       prefetch_tmap(&tmW2);
       prefetch_tmap(&tmH);
-      int s = 0;
-      uint32_t ph = 0;
-      int used = 0;  // stages filled at least once
-      bool dead = false;
-      // the weight boxes of a step: expert e's rows [k0, k0 + 64), features [c0, c0 + 128)
-      auto load_a = [&](const CUtensorMap* m, int row, int c0, int cols, uint32_t b_bytes) {
-        const int nb = min(2, (cols - c0) / 64);
-        mbar_arrive_expect_tx(&full[s], nb * BOX_BYTES + b_bytes);
-        uint8_t* st = smem + s * C::STAGE;
-        for (int b = 0; b < nb; ++b) tma_load_2d(st + b * BOX_BYTES, m, &full[s], c0 + b * 64, row);
-      };
-      auto next = [&]() {
-        if (++s == C::STAGES) {
-          s = 0;
-          ph ^= 1u;
+    }
+    __syncwarp();
+    int s = 0;
+    uint32_t ph = 0;
+    int used = 0;  // stages filled at least once
+    bool dead = false;
+    const uint32_t smem0 = smem_u32(smem), bar0 = smem_u32(full);
+    // a step's weight boxes, rows [row, row + 64) x features [c0, c0 + 64 nb),
+    // and the byte count of all it loads
+    auto load_a = [&](const CUtensorMap* m, int row, int c0, int nb, uint32_t b_bytes) {
+      const uint32_t st = smem0 + s * C::STAGE, bar = bar0 + s * 8;
+      mbar_arrive_expect_tx_lead(lead, &full[s], nb * BOX_BYTES + b_bytes);
+      tma_load_2d_lead(lead, st, m, bar, c0, row);
+      if (nb == 2) tma_load_2d_lead(lead, st + BOX_BYTES, m, bar, c0 + 64, row);
+    };
+    auto load_b = [&](const CUtensorMap* m, int k, int row) {
+      tma_load_2d_lead(lead, smem0 + s * C::STAGE + A_BYTES, m, bar0 + s * 8, k, row);
+    };
+    auto next = [&]() {
+      if (++s == C::STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
+    };
+    auto claim = [&]() {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
+        dead = true;
+        return false;
+      }
+      if (used < C::STAGES) ++used;
+      return true;
+    };
+    {
+      const int end = r1.start(cta + 1);
+      for (int i = r1.start(cta); i < end && !dead;) {
+        const int u = i / r1.len, k0 = i - u * r1.len, n = min(r1.len - k0, end - i);
+        const int slot = u / FB, c0 = (u - slot * FB) * BM, row = sexp[slot] * d;
+        const int nb = min(2, (f - c0) / 64);
+        for (int j = k0; j < k0 + n; ++j) {
+          if (!claim()) break;
+          load_a(&tmW1, row + j * BK, c0, nb, C::N1 * 128);
+          load_b(&tmX, j * BK, 0);
+          next();
         }
-      };
-      auto claim = [&]() {
-        if (!mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs)) {
-          dead = true;
-          return false;
-        }
-        if (used < C::STAGES) ++used;
-        return true;
-      };
-      {
-        const int end = r1.start(cta + 1);
-        for (int i = r1.start(cta); i < end && !dead;) {
-          const int u = i / r1.len, k0 = i - u * r1.len, n = min(r1.len - k0, end - i);
-          const int slot = u / FB, c0 = (u - slot * FB) * BM, row = sexp[slot] * d;
+        i += n;
+      }
+    }
+    if (!dead) {
+      // the first W2 tiles go out before h is known to be there; their h
+      // rows follow once every h tile has been counted
+      const int first = r2.start(cta), end = r2.start(cta + 1);
+      const int ahead = min(end, first + C::STAGES);
+      const int s0 = s;
+      const uint32_t ph0 = ph;
+      auto w2_steps = [&](int from, int to, bool a, bool b) {
+        for (int i = from; i < to && !dead;) {
+          const int u = i / r2.len, k0 = i - u * r2.len, n = min(r2.len - k0, to - i);
+          const int db = u / nslots, slot = u - db * nslots;
+          const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
           for (int j = k0; j < k0 + n; ++j) {
-            if (!claim()) break;
-            load_a(&tmW1, row + j * BK, c0, f, C::N1 * 128);
-            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmX, &full[s], j * BK, 0);
+            if (a) {
+              if (!claim()) break;
+              load_a(&tmW2, row + j * BK, db * BM, nb, C::HR * 128);
+            }
+            if (b) load_b(&tmH, j * BK, slot * C::HR);
             next();
           }
           i += n;
         }
-      }
+      };
+      w2_steps(first, ahead, true, false);
+      if (lane == 0 && !lost) lost = !wait_count(p.sync + SYNC_H, nslots * FB, kWaitLimitNs);
+      __syncwarp();
+      asm volatile("fence.proxy.async;" ::: "memory");
       if (!dead) {
-        // the first W2 tiles go out before h is known to be there; their h
-        // rows follow once every h tile has been counted
-        const int first = r2.start(cta), end = r2.start(cta + 1);
-        auto w2_step = [&](int i, bool a, bool b) {
-          const int u = i / r2.len, j = i - u * r2.len;
-          const int db = u / nslots, slot = u - db * nslots;
-          if (a) load_a(&tmW2, sexp[slot] * f + j * BK, db * BM, d, C::HR * 128);
-          if (b)
-            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::HR);
-        };
-        const int s0 = s;
-        const uint32_t ph0 = ph;
-        int ahead = first;
-        for (; ahead < end && ahead < first + C::STAGES; ++ahead) {
-          if (!claim()) break;
-          w2_step(ahead, true, false);
-          next();
-        }
-        if (!lost) lost = !wait_count(p.sync + SYNC_H, nslots * FB, kWaitLimitNs);
-        asm volatile("fence.proxy.async;" ::: "memory");
-        const int s1 = s;
-        const uint32_t ph1 = ph;
         s = s0;
         ph = ph0;
-        for (int i = first; i < ahead; ++i) {
-          w2_step(i, false, true);
-          next();
-        }
-        s = s1;
-        ph = ph1;
-        for (int i = ahead; i < end && !dead;) {
-          const int u = i / r2.len, k0 = i - u * r2.len, n = min(r2.len - k0, end - i);
-          const int db = u / nslots, slot = u - db * nslots;
-          const int row = sexp[slot] * f;
-          for (int j = k0; j < k0 + n; ++j) {
-            if (!claim()) break;
-            load_a(&tmW2, row + j * BK, db * BM, d, C::HR * 128);
-            tma_load_2d(smem + s * C::STAGE + A_BYTES, &tmH, &full[s], j * BK, slot * C::HR);
-            next();
-          }
-          i += n;
-        }
+        w2_steps(first, ahead, false, true);
+        w2_steps(ahead, end, true, true);
       }
-      // no copy may still be on its way into this CTA when it exits: the
-      // latest use of each stage has landed (its phase is the one before s, ph)
-      for (int j = 0; j < used; ++j) {
-        if (s == 0) {
-          s = C::STAGES;
-          ph ^= 1u;
-        }
-        --s;
-        if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
-          dead = true;
-          break;
-        }
-      }
-      if (dead || lost) atomicOr(p.err, kErrTimeout);
     }
+    // no copy may still be on its way into this CTA when it exits: the
+    // latest use of each stage has landed (its phase is the one before s, ph)
+    for (int j = 0; j < used; ++j) {
+      if (s == 0) {
+        s = C::STAGES;
+        ph ^= 1u;
+      }
+      --s;
+      if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
+        dead = true;
+        break;
+      }
+    }
+    if (lane == 0 && (dead || lost)) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
     // (the whole warp, converged: tc_mma_f16_lead says why)

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
 // starts once the epilogue has drained one of them.
 namespace mx {
 constexpr int BN = 256, HN = 128, KS = 256;  // a tile's columns, an accumulator's, a stage's k
-constexpr int A_BOX = 32 * 128, B_BOX = 64 * 128;  // boxes of 32 rows, 64 columns
+constexpr int B_BOX = 64 * 128;             // a box of 64 columns
 constexpr int A_BYTES = 128 * 128;
 constexpr int SF_COL = 384, SF_STAGE = 24;  // tensor memory columns: 3 x 128, then scales
 constexpr int TMEM_COLS = 512, ACCS = 3;
@@ -505,6 +505,7 @@ __device__ __forceinline__ float mx_silu(float z) { return __fdividef(z, 1.f + _
 template <bool PAIR, typename TO>
 __global__ void __launch_bounds__(mx::THREADS, 1)
     mx4_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmA32,
                        const __grid_constant__ CUtensorMap tmB,
                        const __grid_constant__ CUtensorMap tmSA,
                        const __grid_constant__ CUtensorMap tmSB, const mx::Params p) {
@@ -602,77 +603,95 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
   };
 
   if (warp == 0) {
+    // (the whole warp, converged: tc_mma_f16_lead says why)
+    const uint32_t lead = lane == 0 ? 1u : 0u;
     if (lane == 0) {
       prefetch_tmap(&tmA);
+      prefetch_tmap(&tmA32);
       prefetch_tmap(&tmB);
       prefetch_tmap(&tmSA);
       prefetch_tmap(&tmSB);
-      int s = 0, used = 0;
-      uint32_t ph = 0;
-      bool dead = false;
-      const uint32_t leader_full = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
-      walk([&](int t, int k0, int k1) {
-        const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
-        const int nt = up_div(N, HN), nj = up_div(tl.n, HN);
-        // boxes of 32 rows and of 64 columns of CTA r; a box that is not
-        // loaded feeds only sums that are not stored
-        auto a_boxes = [&](int r) { return min(4, max(0, up_div(tl.rows - r * 128, 32))); };
-        auto b_boxes = [&](int r) {
-          if (!PAIR) return tl.n / 64;
-          const int left = tl.n - r * 64;
-          return (left > 0) + (left > HN);
-        };
-        auto bytes = [&](int r) {
-          const int na = a_boxes(r);
-          return na * A_BOX + b_boxes(r) * B_BOX + ((na > 0 ? 1 : 0) + nj) * 2 * CHUNK;
-        };
-        const int na = a_boxes(rank), nb = b_boxes(rank);
-        const uint32_t expect = PAIR ? bytes(0) + bytes(1) : bytes(0);
-        const int mt = tl.mt + rank, row0 = tl.row0 + rank * 128;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs)) {
-            dead = true;
-            return false;
-          }
-          if (used < STAGES) ++used;
-          uint8_t* st = smem + s * C::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
-          auto load = [&](int off, const CUtensorMap* m, int c0, int c1) {
-            if constexpr (PAIR)
-              tma_load_2d_pair(st + off, m, leader_full + s * 8, c0, c1);
-            else
-              tma_load_2d(st + off, m, &full[s], c0, c1);
-          };
-          for (int b = 0; b < nb; ++b)
-            load(C::OFF_B + b * B_BOX, &tmB, kb * 128,
-                 tl.e * N + tl.n0 + (PAIR ? b * HN + static_cast<int>(rank) * 64 : b * 64));
-          for (int b = 0; b < na; ++b) load(b * A_BOX, &tmA, kb * 128, row0 + b * 32);
-          if (na > 0) load(C::OFF_SFA, &tmSA, 0, mt * kc + kb * 2);
-          for (int j = 0; j < nj; ++j)
-            load(C::OFF_SFB + j * 2 * CHUNK, &tmSB, 0,
-                 (tl.e * nt + tl.n0 / HN + j) * kc + kb * 2);
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+    }
+    __syncwarp();
+    int s = 0, used = 0;
+    uint32_t ph = 0;
+    bool dead = false;
+    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
+    auto load2 = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+      if constexpr (PAIR)
+        tma_load_2d_pair_lead(lead, dst, m, bar, c0, c1);
+      else
+        tma_load_2d_lead(lead, dst, m, bar, c0, c1);
+    };
+    auto load3 = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+      if constexpr (PAIR)
+        tma_load_3d_pair_lead(lead, dst, m, bar, c0, c1, c2);
+      else
+        tma_load_3d_lead(lead, dst, m, bar, c0, c1, c2);
+    };
+    walk([&](int t, int k0, int k1) {
+      const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
+      const int nt = up_div(N, HN);
+      // CTA r's rows come in one box of 128 or, few, of 32, and its columns
+      // in boxes of 64; what is not loaded feeds only sums that are not stored
+      auto a_bytes = [&](int r) {
+        const int left = tl.rows - r * 128;
+        return left <= 0 ? 0 : (left <= 32 ? A_BYTES / 4 : A_BYTES);
+      };
+      auto b_boxes = [&](int r) {
+        if (!PAIR) return tl.n / 64;
+        const int left = tl.n - r * 64;
+        return (left > 0) + (left > HN);
+      };
+      auto bytes = [&](int r) {
+        const int na = a_bytes(r);
+        return na + b_boxes(r) * B_BOX + (na > 0 ? 2 * CHUNK : 0) + 4 * CHUNK;
+      };
+      const int na = a_bytes(rank), nb = b_boxes(rank);
+      const uint32_t expect = PAIR ? bytes(0) + bytes(1) : bytes(0);
+      const CUtensorMap* ma = na == A_BYTES ? &tmA : &tmA32;
+      const int mt = tl.mt + rank, row0 = tl.row0 + rank * 128;
+      const int col0 = tl.e * N + tl.n0 + (PAIR ? static_cast<int>(rank) * 64 : 0);
+      const int sbt = tl.e * nt + tl.n0 / HN;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
+          dead = true;
+          return false;
         }
-        return true;
-      });
-      // the latest use of each stage has landed before this CTA may exit (a
-      // pair: the even CTA's barrier counts both, and both exit together)
-      for (int j = 0; rank == 0 && j < used; ++j) {
-        if (s == 0) {
-          s = STAGES;
+        if (used < STAGES) ++used;
+        const uint32_t st = smem0 + s * C::STAGE, bar = bar0 + s * 8;
+        if (rank == 0) mbar_arrive_expect_tx_lead(lead, &full[s], expect);
+#pragma unroll
+        for (int b = 0; b < (PAIR ? 2 : 4); ++b)
+          if (b < nb)
+            load2(st + C::OFF_B + b * B_BOX, &tmB, bar, kb * 128, col0 + b * (PAIR ? HN : 64));
+        if (na > 0) {
+          load2(st, ma, bar, kb * 128, row0);
+          load3(st + C::OFF_SFA, &tmSA, bar, 0, kb * 2, mt);
+        }
+        load3(st + C::OFF_SFB, &tmSB, bar, 0, kb * 2, sbt);
+        if (++s == STAGES) {
+          s = 0;
           ph ^= 1u;
         }
-        --s;
-        if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
-          dead = true;
-          break;
-        }
       }
-      if (dead) atomicOr(p.err, kErrTimeout);
+      return true;
+    });
+    // the latest use of each stage has landed before this CTA may exit (a
+    // pair: the even CTA's barrier counts both, and both exit together)
+    for (int j = 0; rank == 0 && j < used; ++j) {
+      if (s == 0) {
+        s = STAGES;
+        ph ^= 1u;
+      }
+      --s;
+      if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
+        dead = true;
+        break;
+      }
     }
+    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
     // (the whole warp, converged: tc_mma_f16_lead says why)
     if (rank == 0) {
@@ -885,7 +904,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
 }
 
 template <bool PAIR, typename TO>
-cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mSA,
+cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mA32, const CUtensorMap& mB, const CUtensorMap& mSA,
                            const CUtensorMap& mSB, const mx::Params& p, int grid, cudaStream_t s) {
   using C = mx::Cfg<PAIR>;
   auto* kernel = mx4_product_kernel<PAIR, TO>;
@@ -906,7 +925,7 @@ cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mB, const C
   attr[1].val.clusterDim.z = 1;
   lc.attrs = attr;
   lc.numAttrs = PAIR ? 2 : 1;
-  return cudaLaunchKernelEx(&lc, kernel, mA, mB, mSA, mSB, p);
+  return cudaLaunchKernelEx(&lc, kernel, mA, mA32, mB, mSA, mSB, p);
 }
 
 int blocks_for(long long items, int per_block, int most) {
@@ -968,21 +987,21 @@ cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8
                                const uint8_t* wsc, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,
                                uint32_t* ctr, float* part, int num_sms, cudaStream_t s) {
-  CUtensorMap mA, mB, mSA, mSB;
+  CUtensorMap mA, mA32, mB, mSA, mSB;
   const uint64_t kc = up_div(K, 128);
-  if (!make_map_2d_bytes(&mA, aq, R, K / 2, 32) ||
+  if (!make_map_2d_bytes(&mA, aq, R, K / 2, 128) || !make_map_2d_bytes(&mA32, aq, R, K / 2, 32) ||
       !make_map_2d_bytes(&mB, wq, static_cast<uint64_t>(E) * N, K / 2, 64) ||
-      !make_map_2d_chunks(&mSA, as, mx4_row_tiles(R, E) * kc) ||
-      !make_map_2d_chunks(&mSB, wsc, static_cast<uint64_t>(E) * up_div(N, 128) * kc))
+      !make_map_3d_chunks(&mSA, as, mx4_row_tiles(R, E), kc, 1) ||
+      !make_map_3d_chunks(&mSB, wsc, static_cast<uint64_t>(E) * up_div(N, 128), kc, 2))
     return cudaErrorInvalidValue;
   const mx::Params p{offsets, out, err, ctr, part, E, R, K, N, silu};
   const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
   const bool pair = R >= kMx4PairRows * E;
   if (pair)
-    return out_f32 ? launch_product<true, float>(mA, mB, mSA, mSB, p, grid, s)
-                   : launch_product<true, __nv_bfloat16>(mA, mB, mSA, mSB, p, grid, s);
-  return out_f32 ? launch_product<false, float>(mA, mB, mSA, mSB, p, grid, s)
-                 : launch_product<false, __nv_bfloat16>(mA, mB, mSA, mSB, p, grid, s);
+    return out_f32 ? launch_product<true, float>(mA, mA32, mB, mSA, mSB, p, grid, s)
+                   : launch_product<true, __nv_bfloat16>(mA, mA32, mB, mSA, mSB, p, grid, s);
+  return out_f32 ? launch_product<false, float>(mA, mA32, mB, mSA, mSB, p, grid, s)
+                 : launch_product<false, __nv_bfloat16>(mA, mA32, mB, mSA, mSB, p, grid, s);
 }
 
 }  // namespace moe

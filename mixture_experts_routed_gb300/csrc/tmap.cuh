@@ -19,9 +19,10 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows);
 
-// 2-D map over chunks of 512 bytes (128 words a row), box of two chunks, no
-// swizzle, zero fill past the last.
-bool make_map_2d_chunks(CUtensorMap* m, const void* base, uint64_t chunks);
+// 3-D map over [tiles][groups] chunks of 512 bytes (128 words), box of
+// box_tiles x two chunks, no swizzle, zero fill outside.
+bool make_map_3d_chunks(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t groups,
+                        uint32_t box_tiles);
 
 // 2-D map over a row-major [rows, cols] output, box [32 rows][32 cols]: fp32
 // with the 128-byte swizzle, or bf16 with the 64-byte swizzle. Stores
