@@ -445,8 +445,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       p.out[i] = __float2bfloat16(0.f);
   } else if (warp == 0) {
     // -------------------------------------------------------------- TMA producer
-    // (the whole warp, converged: tc_mma_f16_lead says why)
-    const uint32_t lead = lane == 0 ? 1u : 0u;
+    // (the whole warp, converged: elect_one says why)
     if (lane == 0) {
       prefetch_tmap(&tmX);
       prefetch_tmap(&tmW1);
@@ -458,17 +457,16 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     uint32_t ph = 0;
     int used = 0;  // stages filled at least once
     bool dead = false;
-    const uint32_t smem0 = smem_u32(smem), bar0 = smem_u32(full);
     // a step's weight boxes, rows [row, row + 64) x features [c0, c0 + 64 nb),
     // and the byte count of all it loads
     auto load_a = [&](const CUtensorMap* m, int row, int c0, int nb, uint32_t b_bytes) {
-      const uint32_t st = smem0 + s * C::STAGE, bar = bar0 + s * 8;
-      mbar_arrive_expect_tx_lead(lead, &full[s], nb * BOX_BYTES + b_bytes);
-      tma_load_2d_lead(lead, st, m, bar, c0, row);
-      if (nb == 2) tma_load_2d_lead(lead, st + BOX_BYTES, m, bar, c0 + 64, row);
+      uint8_t* st = smem + s * C::STAGE;
+      mbar_arrive_expect_tx(&full[s], nb * BOX_BYTES + b_bytes);
+      tma_load_2d(st, m, &full[s], c0, row);
+      if (nb == 2) tma_load_2d(st + BOX_BYTES, m, &full[s], c0 + 64, row);
     };
     auto load_b = [&](const CUtensorMap* m, int k, int row) {
-      tma_load_2d_lead(lead, smem0 + s * C::STAGE + A_BYTES, m, bar0 + s * 8, k, row);
+      tma_load_2d(smem + s * C::STAGE + A_BYTES, m, &full[s], k, row);
     };
     auto next = [&]() {
       if (++s == C::STAGES) {
@@ -492,8 +490,11 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         const int nb = min(2, (f - c0) / 64);
         for (int j = k0; j < k0 + n; ++j) {
           if (!claim()) break;
-          load_a(&tmW1, row + j * BK, c0, nb, C::N1 * 128);
-          load_b(&tmX, j * BK, 0);
+          if (elect_one()) {
+            load_a(&tmW1, row + j * BK, c0, nb, C::N1 * 128);
+            load_b(&tmX, j * BK, 0);
+          }
+          __syncwarp();
           next();
         }
         i += n;
@@ -512,11 +513,12 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           const int db = u / nslots, slot = u - db * nslots;
           const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
           for (int j = k0; j < k0 + n; ++j) {
-            if (a) {
-              if (!claim()) break;
-              load_a(&tmW2, row + j * BK, db * BM, nb, C::HR * 128);
+            if (a && !claim()) break;
+            if (elect_one()) {
+              if (a) load_a(&tmW2, row + j * BK, db * BM, nb, C::HR * 128);
+              if (b) load_b(&tmH, j * BK, slot * C::HR);
             }
-            if (b) load_b(&tmH, j * BK, slot * C::HR);
+            __syncwarp();
             next();
           }
           i += n;
@@ -549,8 +551,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     if (lane == 0 && (dead || lost)) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issue
-    // (the whole warp, converged: tc_mma_f16_lead says why)
-    const uint32_t lead = lane == 0 ? 1u : 0u;
+    // (the whole warp, converged: elect_one says why)
     int s = 0, acc = 0;
     uint32_t ph = 0, aph = 0;
     bool dead = false;
@@ -573,17 +574,22 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           }
           tc_fence_after();
           const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+          const uint32_t more = j > 0 ? 1u : 0u;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk)
-            tc_mma_f16_lead(lead, dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
-                            kk > 0 || j > 0 ? 1u : 0u);
-          tc_commit_lead(lead, &empty[s]);
+            for (int kk = 0; kk < BK / 16; ++kk)
+              tc_mma_f16(dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
+                         kk > 0 ? 1u : more);
+            tc_commit(&empty[s]);
+          }
+          __syncwarp();
           if (++s == C::STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        tc_commit_lead(lead, &tfull[acc]);
+        if (elect_one()) tc_commit(&tfull[acc]);
+        __syncwarp();
         if (++acc == 2) {
           acc = 0;
           aph ^= 1u;
@@ -594,7 +600,8 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     phase(r1, make_idesc_bf16_f32(BM, C::N1, true, false));
     if (!dead) phase(r2, make_idesc_bf16_f32(BM, C::N2, true, false));
     // nothing this thread issued may still run when tensor memory is freed
-    tc_commit_lead(lead, drain);
+    if (elect_one()) tc_commit(drain);
+    __syncwarp();
     if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue

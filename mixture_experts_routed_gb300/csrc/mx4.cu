@@ -396,9 +396,8 @@ struct Cfg {
   static constexpr int B_BYTES = (PAIR ? 128 : 256) * 128;
   static constexpr int OFF_B = A_BYTES, OFF_SFA = OFF_B + B_BYTES, OFF_SFB = OFF_SFA + 2 * CHUNK;
   static constexpr int STAGE = OFF_SFB + 4 * CHUNK;
-  static constexpr int STAGES = PAIR ? 5 : 4;
-  static constexpr int OFF_STG = STAGES * STAGE;  // 4 KB an epilogue warp
-  static constexpr int OFF_BAR = OFF_STG + 4 * 4096;
+  static constexpr int STAGES = PAIR ? 5 : 4;  // (tensor memory's and shared memory's most)
+  static constexpr int OFF_BAR = STAGES * STAGE;
   static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
   static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
@@ -421,28 +420,25 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int m, int n, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
          (static_cast<uint32_t>(m >> 7) << 27) | (sf << 29);
 }
-// (lead: as tc_mma_f16_lead)
 template <bool PAIR>
-__device__ __forceinline__ void mma_mxf4(uint32_t lead, uint32_t d, uint64_t a, uint64_t b,
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b,
                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t accumulate) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
         "[%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
+        "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "setp.ne.b32 q, %7, 0;\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
         "[%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lead)
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 // 32 rows of 16 bytes, contiguous, to 4 columns of all four lane quarters
@@ -453,26 +449,20 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
          (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
 }
 template <bool PAIR>
-__device__ __forceinline__ void cp_scales(uint32_t lead, uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
   if constexpr (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
-        "l"(desc), "r"(lead)
-        : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
   else
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-        "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}\n" ::"r"(taddr),
-        "l"(desc), "r"(lead)
-        : "memory");
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
 }
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+__device__ __forceinline__ void commit(uint64_t* bar) {
   if constexpr (PAIR)
-    tc_commit_pair_mc_lead(lead, bar, 0x3);
+    tc_commit_pair_mc(bar, 0x3);
   else
-    tc_commit_lead(lead, bar);
+    tc_commit(bar);
 }
 __device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 
@@ -499,6 +489,17 @@ __device__ __forceinline__ Tile tile_at(int t, const int* seg, const int* base, 
 }
 }  // namespace mx
 
+// 32 bytes: one store where they are 32-byte aligned, else two of 16
+__device__ __forceinline__ void st_sector(bool whole, void* p, const uint32_t (&v)[8]) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
 __device__ __forceinline__ float mx_silu(float z) { return __fdividef(z, 1.f + __expf(-z)); }
 
 // TO: the output type
@@ -603,8 +604,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
   };
 
   if (warp == 0) {
-    // (the whole warp, converged: tc_mma_f16_lead says why)
-    const uint32_t lead = lane == 0 ? 1u : 0u;
+    // (the whole warp, converged: elect_one says why)
     if (lane == 0) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmA32);
@@ -616,19 +616,18 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     int s = 0, used = 0;
     uint32_t ph = 0;
     bool dead = false;
-    const uint32_t smem0 = smem_u32(smem);
-    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : smem_u32(full);
-    auto load2 = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1) {
+    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
+    auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
       if constexpr (PAIR)
-        tma_load_2d_pair_lead(lead, dst, m, bar, c0, c1);
+        tma_load_2d_pair(dst, m, bar0 + s * 8, c0, c1);
       else
-        tma_load_2d_lead(lead, dst, m, bar, c0, c1);
+        tma_load_2d(dst, m, &full[s], c0, c1);
     };
-    auto load3 = [&](uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2) {
+    auto load3 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1, int c2) {
       if constexpr (PAIR)
-        tma_load_3d_pair_lead(lead, dst, m, bar, c0, c1, c2);
+        tma_load_3d_pair(dst, m, bar0 + s * 8, c0, c1, c2);
       else
-        tma_load_3d_lead(lead, dst, m, bar, c0, c1, c2);
+        tma_load_3d(dst, m, &full[s], c0, c1, c2);
     };
     walk([&](int t, int k0, int k1) {
       const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
@@ -660,17 +659,20 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
           return false;
         }
         if (used < STAGES) ++used;
-        const uint32_t st = smem0 + s * C::STAGE, bar = bar0 + s * 8;
-        if (rank == 0) mbar_arrive_expect_tx_lead(lead, &full[s], expect);
+        if (elect_one()) {
+          uint8_t* st = smem + s * C::STAGE;
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
 #pragma unroll
-        for (int b = 0; b < (PAIR ? 2 : 4); ++b)
-          if (b < nb)
-            load2(st + C::OFF_B + b * B_BOX, &tmB, bar, kb * 128, col0 + b * (PAIR ? HN : 64));
-        if (na > 0) {
-          load2(st, ma, bar, kb * 128, row0);
-          load3(st + C::OFF_SFA, &tmSA, bar, 0, kb * 2, mt);
+          for (int b = 0; b < (PAIR ? 2 : 4); ++b)
+            if (b < nb)
+              load2(st + C::OFF_B + b * B_BOX, &tmB, kb * 128, col0 + b * (PAIR ? HN : 64));
+          if (na > 0) {
+            load2(st, ma, kb * 128, row0);
+            load3(st + C::OFF_SFA, &tmSA, 0, kb * 2, mt);
+          }
+          load3(st + C::OFF_SFB, &tmSB, 0, kb * 2, sbt);
         }
-        load3(st + C::OFF_SFB, &tmSB, bar, 0, kb * 2, sbt);
+        __syncwarp();
         if (++s == STAGES) {
           s = 0;
           ph ^= 1u;
@@ -693,9 +695,8 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     }
     if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
-    // (the whole warp, converged: tc_mma_f16_lead says why)
+    // (the whole warp, converged: elect_one says why)
     if (rank == 0) {
-      const uint32_t lead = lane == 0 ? 1u : 0u;
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool dead = false;
@@ -711,17 +712,17 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
 #pragma unroll
         for (int c = 0; c < chunks; ++c) {
-          cp_scales<PAIR>(lead, sf + c * 4, sa0 + off + c * (CHUNK / 16));
+          cp_scales<PAIR>(sf + c * 4, sa0 + off + c * (CHUNK / 16));
 #pragma unroll
           for (int j = 0; j < nj; ++j)
-            cp_scales<PAIR>(lead, sf + 8 + c * 8 + j * 4,
+            cp_scales<PAIR>(sf + 8 + c * 8 + j * 4,
                             sb0 + off + (2 * j + c) * (CHUNK / 16));
         }
 #pragma unroll
         for (int kk = 0; kk < steps; ++kk)
 #pragma unroll
           for (int j = 0; j < nj; ++j)
-            mma_mxf4<PAIR>(lead, j == 0 ? d0 : d1, ad0 + off + kk * 2,
+            mma_mxf4<PAIR>(j == 0 ? d0 : d1, ad0 + off + kk * 2,
                            bd0 + off + j * (B_HALF / 16) + kk * 2, (kk & 1) ? id2 : id0,
                            sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8 + j * 4,
                            kk > 0 ? 1u : more);
@@ -748,18 +749,22 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
           tc_fence_after();
           const uint32_t more = kb > k0 ? 1u : 0u;
           const int left = K - kb * KS;
-          if (left >= KS && nj == 2)
-            stage(2, 4, 2, d0, d1, more);
-          else
-            stage(left > 128 ? 2 : 1, min(4, left / 64), nj, d0, d1, more);
-          commit<PAIR>(lead, &empty[s]);
+          if (elect_one()) {
+            if (left >= KS && nj == 2)
+              stage(2, 4, 2, d0, d1, more);
+            else
+              stage(left > 128 ? 2 : 1, min(4, left / 64), nj, d0, d1, more);
+            commit<PAIR>(&empty[s]);
+          }
+          __syncwarp();
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
         for (int j = 0; j < nj; ++j) {
-          commit<PAIR>(lead, &tfull[acc]);
+          if (elect_one()) commit<PAIR>(&tfull[acc]);
+          __syncwarp();
           if (++acc == ACCS) {
             acc = 0;
             aph ^= 1u;
@@ -767,30 +772,42 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         }
         return !dead;
       });
-      if constexpr (PAIR)
-        tc_commit_pair_mc_lead(lead, drain, 0x1);
-      else
-        tc_commit_lead(lead, drain);
+      if (elect_one()) {
+        if constexpr (PAIR)
+          tc_commit_pair_mc(drain, 0x1);
+        else
+          tc_commit(drain);
+      }
+      __syncwarp();
       if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
     }
   } else if (warp >= 4) {
     const int w = warp & 3;
-    uint8_t* stg = smem + C::OFF_STG + w * 4096;
     int acc = 0;
     uint32_t aph = 0;
     bool dead = false;
     TO* out = static_cast<TO*>(p.out);
     const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
-    auto put = [&](size_t row, int col, float4 v) {
-      if (p.silu) v = make_float4(mx_silu(v.x), mx_silu(v.y), mx_silu(v.z), mx_silu(v.w));
+    auto finish = [&](float v) { return p.silu ? mx_silu(v) : v; };
+    // 32 columns of a row from a lane's registers, whole sectors a store
+    const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
+    auto put32 = [&](size_t row, int col, const uint32_t (&r)[32]) {
       TO* o = out + row * N + col;
-      if constexpr (sizeof(TO) == 4) {
-        *reinterpret_cast<float4*>(o) = v;
-      } else {
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y),
-                             hi = __floats2bfloat162_rn(v.z, v.w);
-        *reinterpret_cast<uint2*>(o) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                  *reinterpret_cast<const uint32_t*>(&hi));
+      constexpr int PER = 32 / sizeof(TO);
+#pragma unroll
+      for (int j = 0; j < 32; j += PER) {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if constexpr (sizeof(TO) == 4) {
+            v[i] = __float_as_uint(finish(__uint_as_float(r[j + i])));
+          } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(
+                finish(__uint_as_float(r[j + 2 * i])), finish(__uint_as_float(r[j + 2 * i + 1])));
+            v[i] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+        st_sector(sectors, o + j, v);
       }
     };
     walk([&](int t, int k0, int k1) {
@@ -817,24 +834,18 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
             tmem_ld_32x32b_x32(
                 tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN + c0, r);
             tmem_ld_wait();
-            // 32 x 32 through shared memory, 16-byte pieces swizzled by row
-            __syncwarp();
+            if (lane < rows) {
+              if (whole) {
+                put32(static_cast<size_t>(tl.row0 + r0 + lane), tl.n0 + h + c0, r);
+              } else {
+                // (at most kMx4SplitRows rows: the first warp's)
+                uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * BN + h + c0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-                  make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
-            __syncwarp();
-            const int c4 = lane & 7, col = h + c0 + c4 * 4;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int row = j * 4 + (lane >> 3);
-              const float4 v =
-                  *reinterpret_cast<const float4*>(stg + row * 128 + ((c4 ^ (row & 7)) * 16));
-              if (row < rows) {
-                if (whole)
-                  put(static_cast<size_t>(tl.row0 + r0 + row), tl.n0 + col, v);
-                else  // (at most kMx4SplitRows rows: warp 0's)
-                  __stcg(reinterpret_cast<float4*>(slice(cta) + row * BN + col), v);
+                for (int j = 0; j < 32; j += 8) {
+                  const uint32_t v[8] = {r[j],     r[j + 1], r[j + 2], r[j + 3],
+                                         r[j + 4], r[j + 5], r[j + 6], r[j + 7]};
+                  st_sector(true, o + j, v);
+                }
               }
             }
           }
@@ -883,7 +894,11 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
                 v.w += o[j].w;
               }
             }
-            put(static_cast<size_t>(tl.row0 + row), tl.n0 + col, v);
+            TO* o = out + static_cast<size_t>(tl.row0 + row) * N + tl.n0 + col;
+            o[0] = static_cast<TO>(finish(v.x));
+            o[1] = static_cast<TO>(finish(v.y));
+            o[2] = static_cast<TO>(finish(v.z));
+            o[3] = static_cast<TO>(finish(v.w));
           }
         }
       }

@@ -215,89 +215,36 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint
       : "memory");
 }
 
-// The two above for a warp that runs its issue loop converged: every lane
-// executes the call and the one with `lead` != 0 (always the same) issues.
-// The operands are then uniform values of a converged warp; issued from a
-// one-lane branch instead, each product cost about 130 clocks of moving them
-// to uniform registers.
-__device__ __forceinline__ void tc_mma_f16_lead(uint32_t lead, uint32_t d_tmem, uint64_t adesc,
-                                                uint64_t bdesc, uint32_t idesc,
-                                                uint32_t accumulate) {
+// One lane of a converged warp (always the same): true for it alone. A loop
+// that issues tensor-core products or TMA copies runs converged and enters
+// the issuing branch by this election: their operands then are values of the
+// whole warp. From a loop inside a one-lane branch each product took about
+// 130 clocks to issue (the 4-bit product of 8192^3: 534 us so, 349 us with
+// lane-predicated instructions, 209 us elected).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit_lead(uint32_t lead, uint64_t* bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(
-          smem_u32(bar)),
-      "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void tc_commit_pair_mc_lead(uint32_t lead, uint64_t* bar,
-                                                       uint16_t cta_mask) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %2, 0;\n\t"
-      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;\n\t}\n" ::"r"(smem_u32(bar)),
-      "h"(cta_mask), "r"(lead)
-      : "memory");
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
-// TMA loads and their barrier's byte count likewise, from a converged warp.
-__device__ __forceinline__ void mbar_arrive_expect_tx_lead(uint32_t lead, uint64_t* bar,
-                                                           uint32_t bytes) {
+// 3-D tiled load; c2 the outermost coordinate.
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                            int32_t c0, int32_t c1, int32_t c2) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
-      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}\n" ::"r"(smem_u32(bar)),
-      "r"(bytes), "r"(lead)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-__device__ __forceinline__ void tma_load_2d_lead(uint32_t lead, uint32_t dst,
-                                                 const CUtensorMap* map, uint32_t bar, int32_t c0,
-                                                 int32_t c1) {
+__device__ __forceinline__ void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
+                                                 int32_t c2) {
   asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];\n\t}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_2d_pair_lead(uint32_t lead, uint32_t dst,
-                                                      const CUtensorMap* map, uint32_t bar_cluster,
-                                                      int32_t c0, int32_t c1) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-      "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];\n\t}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_lead(uint32_t lead, uint32_t dst,
-                                                 const CUtensorMap* map, uint32_t bar, int32_t c0,
-                                                 int32_t c1, int32_t c2) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(lead)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair_lead(uint32_t lead, uint32_t dst,
-                                                      const CUtensorMap* map, uint32_t bar_cluster,
-                                                      int32_t c0, int32_t c1, int32_t c2) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %6, 0;\n\t"
-      "@q cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];\n\t}\n" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(lead)
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
 

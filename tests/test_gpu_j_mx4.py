@@ -276,3 +276,15 @@ def test_no_rows(cuda_ok):
     wq, wsc = moe.mx4_quantize_weights(c, torch.ones((2, 128, 64), dtype=torch.bfloat16,
                                                      device="cuda"))
     assert moe.mx4_product(c, q, sc, wq, wsc, off, ws=ws).shape == (0, 64)
+
+
+def test_an_output_aligned_to_16_bytes_only(cuda_ok):
+    for counts in ([3], [200], [300, 300]):
+        for dt in ("f32", "bf16"):
+            c, q, sc, wq, wsc, off, ws, out = product(counts, 256, 192, dt, seed=9)
+            buf = torch.zeros(out.numel() + 64, dtype=out.dtype, device="cuda")
+            view = buf[16 // out.element_size():][:out.numel()].view(out.shape)
+            assert view.data_ptr() % 32 == 16
+            moe.mx4_product(c, q, sc, wq, wsc, off, ws=ws, out=view)
+            assert torch.equal(view, out)
+            assert not bool(buf[:16 // out.element_size()].any())
