@@ -937,6 +937,9 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
   if (gated ? (dgate == nullptr || !aligned(dgate, c.gate == MOE_GATE_TOKEN ? 4 : 16))
             : dgate != nullptr)
     return MOE_ERR_INVALID_ARG;
+  // (a channel gate's gradients read the weight and the gate, rows or none)
+  if ((post && !ok_ptr(w_post)) || (post && c.gate == MOE_GATE_CHANNEL && !ok_ptr(gate)))
+    return MOE_ERR_INVALID_ARG;
   if (c.T > 0) {
     if (!norm_args_ok(c, y, b, w_post, gate, w_pre) || !ok_ptr(dout) || !ok_ptr(dx))
       return MOE_ERR_INVALID_ARG;

@@ -18,19 +18,28 @@
 //   dw_post = sum_t G g bh
 //   v' = G g w_post     db = rstd_post (v' - bh mean(v' bh))
 //
-// Both directions are bound by HBM: every tensor is read or written once,
-// a row held in registers between the two reductions it needs.
+// A channel gate keeps one sum, A = sum_t G bh: dw_post = g A, dg = w_post A.
+//
+// Both directions are bound by HBM: every tensor is read or written once.
+// A row is shared by a warp or by a block of up to 512 threads; each copies
+// the two vectors of its own columns into a ring of rows in shared memory (cp.async: a thread
+// waits for its own copies only, so the ring needs no barrier) and reads
+// them as often as the sums in between require, while the next rows are on
+// their way. Loads into registers instead left too little in flight beside
+// the column sums and weights (16384 x 5120 forward: 173 us; 8191 x 7168
+// backward: 250 us).
 #include <cstdint>
 #include <type_traits>
 
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateElement = 3;
+constexpr int kGateToken = 1, kGateChannel = 2, kGateElement = 3;  // (0: none)
 
 // 16 bytes of a row: VEC elements, widened to fp32.
 template <typename T>
@@ -108,23 +117,82 @@ __device__ __forceinline__ void ld_f32_stream(const float* p, float (&v)[N]) {
   }
 }
 
-// Sum over the TPR threads of a row, in a fixed order; every thread gets it.
-// `buf`: the row's 2 x 32 floats, `turn` alternates so that one barrier per
-// sum is enough.
-template <int TPR>
+// Two fp32 values in one 64-bit register, and the packed operations on them:
+// half the instructions of a row's arithmetic, which with them no longer
+// outlasts its bytes.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 mk2(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ f2 dup2(float a) { return mk2(a, a); }
+__device__ __forceinline__ float2 un2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen2(const uint4& r, f2 (&v)[Vec<T>::N / 2]) {
+  if constexpr (std::is_same<T, float>::value) {
+    v[0] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+    v[1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+  } else {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = mk2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store2(T* p, const f2 (&v)[Vec<T>::N / 2]) {
+  constexpr int N = Vec<T>::N;
+  float u[N];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    const float2 f = un2(v[i]);
+    u[2 * i] = f.x;
+    u[2 * i + 1] = f.y;
+  }
+  store<T>(p, u);
+}
+
+template <int N>
+__device__ __forceinline__ void store2f(float* p, const f2 (&v)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; i += 2) {
+    const float2 a = un2(v[i]), b = un2(v[i + 1]);
+    reinterpret_cast<float4*>(p)[i / 2] = make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+
+// Sum over the threads of a row (a warp, or the block), in a fixed order;
+// every thread gets it. `buf`: 2 x 32 floats, `turn` alternates so that one
+// barrier per sum is enough.
+template <bool WARP>
 __device__ __forceinline__ float row_sum(float v, float* buf, int& turn) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (TPR > 32) {
-    constexpr int W = TPR / 32;
+  if constexpr (!WARP) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* b = buf + turn * 32;
     turn ^= 1;
     if (lane == 0) b[w] = v;
     __syncthreads();
-    v = lane < W ? b[lane] : 0.f;
+    v = lane < (blockDim.x >> 5) ? b[lane] : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    v = __shfl_sync(0xffffffffu, v, 0);
   }
   return v;
 }
@@ -148,456 +216,695 @@ __device__ __forceinline__ void gate_at(const void* gate, int kind, float gt, si
   }
 }
 
-constexpr int block_of(int tpr) { return tpr < 128 ? 128 : tpr; }
+// The weight of the branch at column c: w_post, times a channel gate.
+template <int N>
+__device__ __forceinline__ void branch_weight(const float* w_post, const void* gate, int kind,
+                                              int c, float (&w)[N]) {
+  ld_f32<N>(w_post + c, w);
+  if (kind == kGateChannel) {
+    float g[N];
+    ld_f32<N>(static_cast<const float*>(gate) + c, g);
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] *= g[i];
+  }
+}
+template <int N>
+__device__ __forceinline__ void pack2(const float (&w)[N], f2 (&v)[N / 2]) {
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) v[i] = mk2(w[2 * i], w[2 * i + 1]);
+}
 
-// A row is shared by TPR threads, each holding up to NV vectors of it.
-// NV = 0: rows too wide for registers; the row is read again (from L2) after
-// each sum.
-template <typename T, int TPR, int NV, bool POST, bool PRE>
-__global__ void __launch_bounds__(block_of(TPR))
-    block_norm_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ b,
-                      const float* __restrict__ w_post, const void* __restrict__ gate,
-                      const float* __restrict__ w_pre, T* __restrict__ out, T* __restrict__ n,
-                      float* __restrict__ rstd_post, float* __restrict__ rstd_pre) {
-  constexpr int N = Vec<T>::N;
-  constexpr int RPB = block_of(TPR) / TPR;
+// Threads of a block that takes rows by the warp; other blocks are one row's
+// threads, two vectors each.
+constexpr int kWarpBlock = 128;
+constexpr int kRowThreads = 512;  // at most
+
+// This thread's copies of one tensor's row.
+template <typename T>
+__device__ __forceinline__ void ring_fill(uint4* dst, const T* row, int nvec, int tid, int tpr) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = tid + j * tpr;
+    if (i < nvec)
+      ptx::cp_async16(ptx::smem_u32(dst + i), row + static_cast<size_t>(i) * Vec<T>::N);
+  }
+}
+
+// Forward: S rows in flight.
+template <typename T, bool WARP, int S, bool POST, bool PRE>
+__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
+    norm_ring_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ b,
+                     const float* __restrict__ w_post, const void* __restrict__ gate,
+                     const float* __restrict__ w_pre, T* __restrict__ out, T* __restrict__ n,
+                     float* __restrict__ rstd_post, float* __restrict__ rstd_pre) {
+  constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
-  const int tid = RPB == 1 ? threadIdx.x : threadIdx.x % TPR;
+  const int tpr = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int sub = WARP ? threadIdx.x >> 5 : 0;  // the block's row group
   const int d = a.d, nvec = d / N;
   const float inv_d = 1.f / static_cast<float>(d);
-  for (size_t t = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR; t < a.T;
-       t += static_cast<size_t>(gridDim.x) * RPB) {
-    const T* xr = x + t * d;
-    const T* br = POST ? b + t * d : nullptr;
-    constexpr int M = NV > 0 ? NV : 1;
-    uint4 xv[M], bv[M];
-    if constexpr (NV > 0) {
+  const bool elem = POST && a.gate == kGateElement;
+  const int size = nvec * (1 + (POST ? 1 : 0) + (elem ? 1 : 0));  // a ring slot: x, b, gate
+  uint4* mine = ring + static_cast<size_t>(sub) * S * size;
+  const int step = gridDim.x * RPB, t0 = blockIdx.x * RPB + sub;
+  auto fill = [&](int t, int slot) {
+    if (t < a.T) {
+      uint4* dst = mine + slot * size;
+      const size_t at = static_cast<size_t>(t) * d;
+      ring_fill<T>(dst, x + at, nvec, tid, tpr);
+      if (POST) ring_fill<T>(dst + nvec, b + at, nvec, tid, tpr);
+      if (elem) ring_fill<T>(dst + 2 * nvec, static_cast<const T*>(gate) + at, nvec, tid, tpr);
+    }
+    ptx::cp_async_commit();
+  };
+  f2 wb[2][H], wn[2][H];
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * TPR;
-        if (i < nvec) {
-          if (POST) bv[j] = ld_stream(br + i * N);
-          xv[j] = ld_stream(xr + i * N);
-        }
+  for (int s = 0; s < S - 1; ++s) fill(t0 + s * step, s);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = (tid + j * tpr) * N;
+    if (c < d) {
+      float w[N];
+      if constexpr (POST) {
+        branch_weight<N>(w_post, gate, a.gate, c, w);
+        pack2<N>(w, wb[j]);
+      }
+      if constexpr (PRE) {
+        ld_f32<N>(w_pre + c, w);
+        pack2<N>(w, wn[j]);
       }
     }
-    float rb = 0.f, gt = 1.f;
+  }
+  const f2 alpha = dup2(a.alpha);
+  const bool token = POST && a.gate == kGateToken;
+  float gt_next = token && t0 < a.T ? __ldg(static_cast<const float*>(gate) + t0) : 1.f;
+  int slot = 0;
+  for (int t = t0; t < a.T; t += step) {
+    // the slot that the row before this one was read from is filled again
+    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    ptx::cp_async_wait<S - 1>();
+    const uint4* in = mine + slot * size;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    float rb = 0.f;
+    const float gt = gt_next;
+    if (token && t + step < a.T) gt_next = __ldg(static_cast<const float*>(gate) + t + step);
     if constexpr (POST) {
-      if (a.gate == kGateToken) gt = __ldg(static_cast<const float*>(gate) + t);
-      float ss = 0.f;
-      auto square = [&](const uint4& raw) {
-        float v[N];
-        widen<T>(raw, v);
+      f2 ss = 0;
 #pragma unroll
-        for (int i = 0; i < N; ++i) ss = fmaf(v[i], v[i], ss);
-      };
-      if constexpr (NV > 0) {
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * tpr;
+        if (i < nvec) {
+          f2 v[H];
+          widen2<T>(in[nvec + i], v);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (tid + j * TPR < nvec) square(bv[j]);
-      } else {
-        for (int i = tid; i < nvec; i += TPR) square(ld_stream(br + static_cast<size_t>(i) * N));
+          for (int q = 0; q < H; ++q) ss = fma2(v[q], v[q], ss);
+        }
       }
-      ss = row_sum<TPR>(ss, buf, turn);
-      rb = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      const float2 h = un2(ss);
+      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
+      rb = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
       if (rstd_post != nullptr && tid == 0) rstd_post[t] = rb;
     }
-    // y = alpha x + beta g (b rb w_post) at vector i
-    auto row_y = [&](int i, const uint4& xraw, const uint4& braw, float (&y)[N]) {
-      widen<T>(xraw, y);
-      if constexpr (POST) {
-        float bb[N], w[N], g[N];
-        widen<T>(braw, bb);
-        ld_f32<N>(w_post + i * N, w);
-        gate_at<T, N>(gate, a.gate, gt, t, d, i * N, g);
+    const size_t at = static_cast<size_t>(t) * d;
+    const f2 scale = dup2(a.beta * gt * rb);
+    f2 ss = 0;
+    f2 y[2][H];
 #pragma unroll
-        for (int q = 0; q < N; ++q)
-          y[q] = fmaf(a.alpha, y[q], a.beta * g[q] * (bb[q] * rb * w[q]));
-      }
-    };
-    float ss = 0.f;
-    float y[M][N];
-    if constexpr (NV > 0) {
+    for (int j = 0; j < 2; ++j) {
+      const int i = tid + j * tpr;
+      if (i < nvec) {
+        widen2<T>(in[i], y[j]);
+        if constexpr (POST) {
+          f2 v[H];
+          widen2<T>(in[nvec + i], v);
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * TPR;
-        if (i < nvec) {
-          row_y(i, xv[j], bv[j], y[j]);
-          if (POST) store<T>(out + t * d + i * N, y[j]);
-          if (PRE) {
+          for (int q = 0; q < H; ++q) v[q] = mul2(v[q], wb[j][q]);
+          if (elem) {
+            f2 g[H];
+            widen2<T>(in[2 * nvec + i], g);
 #pragma unroll
-            for (int q = 0; q < N; ++q) ss = fmaf(y[j][q], y[j][q], ss);
+            for (int q = 0; q < H; ++q) v[q] = mul2(v[q], g[q]);
           }
-        }
-      }
-    } else {
-      for (int i = tid; i < nvec; i += TPR) {
-        row_y(i, ld_stream(xr + static_cast<size_t>(i) * N),
-              POST ? ld_stream(br + static_cast<size_t>(i) * N) : uint4{}, y[0]);
-        if (POST) store<T>(out + t * d + static_cast<size_t>(i) * N, y[0]);
-        if (PRE) {
 #pragma unroll
-          for (int q = 0; q < N; ++q) ss = fmaf(y[0][q], y[0][q], ss);
+          for (int q = 0; q < H; ++q) y[j][q] = fma2(scale, v[q], mul2(alpha, y[j][q]));
+          store2<T>(out + at + i * N, y[j]);
+        }
+        if constexpr (PRE) {
+#pragma unroll
+          for (int q = 0; q < H; ++q) ss = fma2(y[j][q], y[j][q], ss);
         }
       }
     }
     if constexpr (PRE) {
-      ss = row_sum<TPR>(ss, buf, turn);
-      const float ro = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      const float2 h = un2(ss);
+      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
+      const float ro = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
       if (rstd_pre != nullptr && tid == 0) rstd_pre[t] = ro;
-      auto put = [&](int i, float (&v)[N]) {
-        float w[N];
-        ld_f32<N>(w_pre + i * N, w);
+      const f2 r2 = dup2(ro);
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = v[q] * ro * w[q];
-        store<T>(n + t * d + static_cast<size_t>(i) * N, v);
-      };
-      if constexpr (NV > 0) {
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * tpr;
+        if (i < nvec) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (tid + j * TPR < nvec) put(tid + j * TPR, y[j]);
-      } else {
-        for (int i = tid; i < nvec; i += TPR) {
-          row_y(i, ld_stream(xr + static_cast<size_t>(i) * N),
-                POST ? ld_stream(br + static_cast<size_t>(i) * N) : uint4{}, y[0]);
-          put(i, y[0]);
+          for (int q = 0; q < H; ++q) y[j][q] = mul2(mul2(y[j][q], r2), wn[j][q]);
+          store2<T>(n + at + i * N, y[j]);
         }
       }
     }
   }
+  ptx::cp_async_wait<0>();
 }
 
-// Backward. Each group of TPR threads walks rows g, g + groups, ... and keeps
-// its rows' column sums (dw_pre, dw_post, a channel gate's dgate) in
-// registers, written once to part[group][3][d]; reduce_columns adds the
-// groups in order. NV = 0: the sums live in part itself.
-template <typename T, int TPR, int NV, bool POST, bool PRE>
-__global__ void __launch_bounds__(block_of(TPR))
-    block_norm_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
-                          const float* __restrict__ dn, const T* __restrict__ yo,
-                          const T* __restrict__ b, const float* __restrict__ w_post,
-                          const void* __restrict__ gate, const float* __restrict__ w_pre,
-                          const float* __restrict__ rstd_post,
-                          const float* __restrict__ rstd_pre, T* __restrict__ dx,
-                          T* __restrict__ db, void* __restrict__ dgate,
-                          float* __restrict__ part) {
-  constexpr int N = Vec<T>::N;
-  constexpr int RPB = block_of(TPR) / TPR;
+// Backward. Each row group walks rows g, g + groups, ... and keeps its rows'
+// column sums (of dw_pre; of dw_post, or A of a channel gate) in registers,
+// written once to part[group][2][d]; reduce_columns adds the groups in
+// order. Factors that a row shares (rstd, beta, a token gate) are taken out
+// of the per-element terms.
+template <typename T, bool WARP, int S, bool POST, bool PRE>
+__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
+    norm_ring_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
+                         const float* __restrict__ dn, const T* __restrict__ yo,
+                         const T* __restrict__ b, const float* __restrict__ w_post,
+                         const void* __restrict__ gate, const float* __restrict__ w_pre,
+                         const float* __restrict__ rstd_post, const float* __restrict__ rstd_pre,
+                         T* __restrict__ dx, T* __restrict__ db, void* __restrict__ dgate,
+                         float* __restrict__ part) {
+  constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
+  constexpr int P = N / 4;  // 16-byte pieces of dn to a vector
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
-  const int tid = RPB == 1 ? threadIdx.x : threadIdx.x % TPR;
+  const int tpr = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int sub = WARP ? threadIdx.x >> 5 : 0;
   const int d = a.d, nvec = d / N;
   const float inv_d = 1.f / static_cast<float>(d);
-  const size_t group = static_cast<size_t>(blockIdx.x) * RPB + threadIdx.x / TPR;
-  float* part_pre = part + group * 3 * d;
-  float* part_post = part_pre + d;
-  float* part_gate = part_post + d;
-  const bool chan = POST && a.gate == kGateChannel;
-  constexpr int M = NV > 0 ? NV : 1;
-  float apre[M][N] = {}, apost[M][N] = {}, agate[M][N] = {};
-  if constexpr (NV == 0) {
-    for (int c = tid; c < 3 * d; c += TPR) part_pre[c] = 0.f;
-    __syncthreads();
-  }
-  for (size_t t = group; t < a.T; t += static_cast<size_t>(gridDim.x) * RPB) {
-    const size_t row = t * d;
-    const float ro = PRE ? __ldg(rstd_pre + t) : 0.f;
-    const float rb = POST ? __ldg(rstd_post + t) : 0.f;
-    const float gt = POST && a.gate == kGateToken ? __ldg(static_cast<const float*>(gate) + t)
-                                                  : 1.f;
-    // D (in place of dout) and, first, sum of v yh
-    float s1 = 0.f;
-    float D[M][N], yh[M][N], v[M][N], bh[M][N];
-    auto load = [&](int i, float (&D_)[N], float (&yh_)[N], float (&v_)[N]) {
-      widen<T>(ld_stream(dout + row + static_cast<size_t>(i) * N), D_);
+  const bool elem = POST && a.gate == kGateElement, token = POST && a.gate == kGateToken;
+  // a ring slot: dout, then y and dn, then b, then an element gate
+  const int off_y = nvec, off_n = 2 * nvec, off_b = PRE ? (2 + P) * nvec : nvec;
+  const int off_g = off_b + nvec;
+  const int size = off_b + (POST ? nvec : 0) + (elem ? nvec : 0);
+  uint4* mine = ring + static_cast<size_t>(sub) * S * size;
+  const int group = blockIdx.x * RPB + sub, step = gridDim.x * RPB;
+  auto fill = [&](int t, int slot) {
+    if (t < a.T) {
+      uint4* dst = mine + slot * size;
+      const size_t at = static_cast<size_t>(t) * d;
+      ring_fill<T>(dst, dout + at, nvec, tid, tpr);
       if constexpr (PRE) {
-        float w[N];
-        widen<T>(ld_stream(yo + row + static_cast<size_t>(i) * N), yh_);
-        ld_f32_stream<N>(dn + row + static_cast<size_t>(i) * N, v_);
-        ld_f32<N>(w_pre + i * N, w);
+        ring_fill<T>(dst + off_y, yo + at, nvec, tid, tpr);
 #pragma unroll
-        for (int q = 0; q < N; ++q) yh_[q] *= ro;
-      }
-    };
-    auto first = [&](int i, float (&yh_)[N], float (&v_)[N], float (&acc)[N]) {
-      float w[N];
-      ld_f32<N>(w_pre + i * N, w);
+        for (int j = 0; j < 2; ++j) {
+          const int i = tid + j * tpr;
+          if (i < nvec)
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        acc[q] = fmaf(v_[q], yh_[q], acc[q]);
-        v_[q] *= w[q];
-        s1 = fmaf(v_[q], yh_[q], s1);
-      }
-    };
-    if constexpr (NV > 0) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int i = tid + j * TPR;
-        if (i < nvec) {
-          load(i, D[j], yh[j], v[j]);
-          if constexpr (POST) widen<T>(ld_stream(b + row + static_cast<size_t>(i) * N), bh[j]);
+            for (int q = 0; q < P; ++q)
+              ptx::cp_async16(ptx::smem_u32(dst + off_n + q * nvec + i), dn + at + i * N + q * 4);
         }
       }
-      if constexpr (PRE) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (tid + j * TPR < nvec) first(tid + j * TPR, yh[j], v[j], apre[j]);
-      }
-    } else if constexpr (PRE) {
-      for (int i = tid; i < nvec; i += TPR) {
-        load(i, D[0], yh[0], v[0]);
-        float acc[N];
-#pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = part_pre[i * N + q];
-        first(i, yh[0], v[0], acc);
-#pragma unroll
-        for (int q = 0; q < N; ++q) part_pre[i * N + q] = acc[q];
+      if constexpr (POST) {
+        ring_fill<T>(dst + off_b, b + at, nvec, tid, tpr);
+        if (elem) ring_fill<T>(dst + off_g, static_cast<const T*>(gate) + at, nvec, tid, tpr);
       }
     }
-    if constexpr (PRE) s1 = row_sum<TPR>(s1, buf, turn) * inv_d;
-    // dx = alpha D (D itself without the post half); then the branch: G = beta D
-    float s2 = 0.f, sg = 0.f;
-    const float al = POST ? a.alpha : 1.f;
-    auto second = [&](int i, float (&D_)[N], float (&yh_)[N], float (&v_)[N], float (&bh_)[N],
-                      float (&ap)[N], float (&ag)[N], bool put) {
-      float o[N];
+    ptx::cp_async_commit();
+  };
+  auto load_dn = [&](const uint4* in, int i, f2 (&v)[H]) {
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        if constexpr (PRE) D_[q] += ro * (v_[q] - yh_[q] * s1);
-        o[q] = al * D_[q];
-      }
-      if (put) store<T>(dx + row + static_cast<size_t>(i) * N, o);
+    for (int q = 0; q < P; ++q) {
+      const uint4 r = in[off_n + q * nvec + i];
+      v[2 * q] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+      v[2 * q + 1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+  };
+  f2 wb[2][H], wn[2][H], apre[2][H] = {}, apost[2][H] = {};
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) fill(group + s * step, s);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int c = (tid + j * tpr) * N;
+    if (c < d) {
+      float w[N];
       if constexpr (POST) {
-        float w[N], g[N], e[N];
-        ld_f32<N>(w_post + i * N, w);
-        gate_at<T, N>(gate, a.gate, gt, t, d, i * N, g);
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-          const float G = a.beta * D_[q];
-          bh_[q] *= rb;
-          const float gu = G * (bh_[q] * w[q]);
-          const float gg = G * g[q];
-          e[q] = gu;
-          sg += gu;
-          ap[q] = fmaf(gg, bh_[q], ap[q]);
-          ag[q] += gu;
-          D_[q] = gg * w[q];  // v'
-          s2 = fmaf(D_[q], bh_[q], s2);
-        }
-        if (a.gate == kGateElement && put)
-          store<T>(static_cast<T*>(dgate) + row + static_cast<size_t>(i) * N, e);
+        branch_weight<N>(w_post, gate, a.gate, c, w);
+        pack2<N>(w, wb[j]);
       }
-    };
-    if constexpr (NV > 0) {
+      if constexpr (PRE) {
+        ld_f32<N>(w_pre + c, w);
+        pack2<N>(w, wn[j]);
+      }
+    }
+  }
+  const f2 al = dup2(POST ? a.alpha : 1.f);
+  // a row's statistics and token gate, loaded while the row before is at work
+  float ro_next = 0.f, rb_next = 0.f, gt_next = 1.f;
+  auto fetch = [&](int t) {
+    if (t >= a.T) return;
+    if (PRE) ro_next = __ldg(rstd_pre + t);
+    if (POST) rb_next = __ldg(rstd_post + t);
+    if (token) gt_next = __ldg(static_cast<const float*>(gate) + t);
+  };
+  fetch(group);
+  int slot = 0;
+  for (int t = group; t < a.T; t += step) {
+    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    ptx::cp_async_wait<S - 1>();
+    const uint4* in = mine + slot * size;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    const size_t at = static_cast<size_t>(t) * d;
+    const float ro = ro_next, rb = rb_next, gt = gt_next;
+    fetch(t + step);
+    float s1 = 0.f;  // ro mean(v y)
+    if constexpr (PRE) {
+      const f2 r2 = dup2(ro);
+      f2 ss = 0;
 #pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (tid + j * TPR < nvec)
-          second(tid + j * TPR, D[j], yh[j], v[j], bh[j], apost[j], agate[j], true);
-    } else {
-      for (int i = tid; i < nvec; i += TPR) {
-        load(i, D[0], yh[0], v[0]);
-        if constexpr (PRE) {
-          float none[N] = {}, keep = s1;
-          first(i, yh[0], v[0], none);
-          s1 = keep;
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * tpr;
+        if (i < nvec) {
+          f2 y[H], v[H];
+          widen2<T>(in[off_y + i], y);
+          load_dn(in, i, v);
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            const f2 p = mul2(mul2(v[q], r2), y[q]);
+            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(apre[j][q]) : "l"(p));
+            ss = fma2(p, wn[j][q], ss);
+          }
         }
-        float ap[N] = {}, ag[N] = {};
-        if constexpr (POST) widen<T>(ld_stream(b + row + static_cast<size_t>(i) * N), bh[0]);
-        second(i, D[0], yh[0], v[0], bh[0], ap, ag, true);
-        if constexpr (POST) {
+      }
+      const float2 h = un2(ss);
+      s1 = row_sum<WARP>(h.x + h.y, buf, turn) * inv_d;
+    }
+    // D = dout + ro v - ro yh mean(v yh), dx = alpha D and, of the branch, D w
+    const f2 r2 = dup2(ro), c2 = dup2(-ro * ro * s1), k2 = dup2(gt * a.beta * rb);
+    f2 v2[2][H], ss = 0;
 #pragma unroll
-          for (int q = 0; q < N; ++q) {
-            part_post[i * N + q] += ap[q];
-            if (chan) part_gate[i * N + q] += ag[q];
+    for (int j = 0; j < 2; ++j) {
+      const int i = tid + j * tpr;
+      if (i < nvec) {
+        f2 D[H], o[H];
+        widen2<T>(in[i], D);
+        if constexpr (PRE) {
+          f2 y[H], v[H];
+          widen2<T>(in[off_y + i], y);
+          load_dn(in, i, v);
+#pragma unroll
+          for (int q = 0; q < H; ++q)
+            D[q] = fma2(mul2(v[q], wn[j][q]), r2, fma2(y[q], c2, D[q]));
+        }
+#pragma unroll
+        for (int q = 0; q < H; ++q) o[q] = mul2(al, D[q]);
+        store2<T>(dx + at + i * N, o);
+        if constexpr (POST) {
+          f2 bb[H];
+          widen2<T>(in[off_b + i], bb);
+          if (elem) {
+            f2 g[H];
+            widen2<T>(in[off_g + i], g);
+#pragma unroll
+            for (int q = 0; q < H; ++q) {
+              o[q] = mul2(mul2(D[q], k2), mul2(bb[q], wb[j][q]));
+              D[q] = mul2(D[q], g[q]);
+            }
+            store2<T>(static_cast<T*>(dgate) + at + i * N, o);
+          }
+#pragma unroll
+          for (int q = 0; q < H; ++q) {
+            apost[j][q] = fma2(mul2(D[q], k2), bb[q], apost[j][q]);
+            v2[j][q] = mul2(D[q], wb[j][q]);
+            ss = fma2(v2[j][q], bb[q], ss);
           }
         }
       }
     }
     if constexpr (POST) {
-      s2 = row_sum<TPR>(s2, buf, turn) * inv_d;
-      if (a.gate == kGateToken) {
-        sg = row_sum<TPR>(sg, buf, turn);
-        if (tid == 0) static_cast<float*>(dgate)[t] = sg;
-      }
-      auto third = [&](int i, float (&v2)[N], float (&bh_)[N]) {
-        float o[N];
+      // sum of D w b: beta rb of it is a token gate's gradient
+      const float2 h = un2(ss);
+      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
+      if (token && tid == 0) static_cast<float*>(dgate)[t] = a.beta * rb * sum;
+      const float k = gt * a.beta * rb;
+      const f2 kv = dup2(k), kb = dup2(-k * rb * rb * sum * inv_d);
 #pragma unroll
-        for (int q = 0; q < N; ++q) o[q] = rb * (v2[q] - bh_[q] * s2);
-        store<T>(db + row + static_cast<size_t>(i) * N, o);
-      };
-      if constexpr (NV > 0) {
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + j * tpr;
+        if (i < nvec) {
+          f2 bb[H];
+          widen2<T>(in[off_b + i], bb);
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-          if (tid + j * TPR < nvec) third(tid + j * TPR, D[j], bh[j]);
-      } else {
-        for (int i = tid; i < nvec; i += TPR) {
-          load(i, D[0], yh[0], v[0]);
-          if constexpr (PRE) {
-            float none[N] = {}, keep = s1;
-            first(i, yh[0], v[0], none);
-            s1 = keep;
-          }
-          float ap[N] = {}, ag[N] = {};
-          widen<T>(ld_stream(b + row + static_cast<size_t>(i) * N), bh[0]);
-          const float mean = s2;
-          second(i, D[0], yh[0], v[0], bh[0], ap, ag, false);
-          s2 = mean;
-          third(i, D[0], bh[0]);
+          for (int q = 0; q < H; ++q) v2[j][q] = fma2(kv, v2[j][q], mul2(kb, bb[q]));
+          store2<T>(db + at + i * N, v2[j]);
         }
       }
     }
   }
-  if constexpr (NV > 0) {
+  ptx::cp_async_wait<0>();
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int i = tid + j * TPR;
-      if (i >= nvec) continue;
+  for (int j = 0; j < 2; ++j) {
+    const int i = tid + j * tpr;
+    if (i >= nvec) continue;
+    float* o = part + static_cast<size_t>(group) * 2 * d + i * N;
+    if (PRE) store2f<N>(o, apre[j]);
+    if (POST) store2f<N>(o + d, apost[j]);
+  }
+}
+
+// Rows too wide for the ring (more than 1024 vectors): 512 threads a row,
+// which is read again (from L2) after each sum.
+constexpr int kWideThreads = 512;
+
+template <typename T, bool POST, bool PRE>
+__global__ void __launch_bounds__(kWideThreads)
+    norm_wide_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ b,
+                     const float* __restrict__ w_post, const void* __restrict__ gate,
+                     const float* __restrict__ w_pre, T* __restrict__ out, T* __restrict__ n,
+                     float* __restrict__ rstd_post, float* __restrict__ rstd_pre) {
+  constexpr int N = Vec<T>::N, TPR = kWideThreads;
+  __shared__ float buf[64];
+  int turn = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, d = a.d, nvec = d / N;
+  const float inv_d = 1.f / static_cast<float>(d);
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t at = static_cast<size_t>(t) * d;
+    float rb = 0.f, gt = 1.f, ss = 0.f;
+    if constexpr (POST) {
+      if (a.gate == kGateToken) gt = __ldg(static_cast<const float*>(gate) + t);
+      for (int i = tid; i < nvec; i += TPR) {
+        float v[N];
+        widen<T>(ld_stream(b + at + i * N), v);
 #pragma unroll
-      for (int q = 0; q < N; q += 4) {
-        if (PRE)
-          *reinterpret_cast<float4*>(part_pre + i * N + q) =
-              make_float4(apre[j][q], apre[j][q + 1], apre[j][q + 2], apre[j][q + 3]);
-        if (POST)
-          *reinterpret_cast<float4*>(part_post + i * N + q) =
-              make_float4(apost[j][q], apost[j][q + 1], apost[j][q + 2], apost[j][q + 3]);
-        if (chan)
-          *reinterpret_cast<float4*>(part_gate + i * N + q) =
-              make_float4(agate[j][q], agate[j][q + 1], agate[j][q + 2], agate[j][q + 3]);
+        for (int q = 0; q < N; ++q) ss = fmaf(v[q], v[q], ss);
+      }
+      ss = row_sum<false>(ss, buf, turn);
+      rb = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      if (rstd_post != nullptr && tid == 0) rstd_post[t] = rb;
+    }
+    auto row_y = [&](int i, float (&y)[N]) {
+      widen<T>(ld_stream(x + at + i * N), y);
+      if constexpr (POST) {
+        float v[N], w[N], g[N];
+        widen<T>(ld_stream(b + at + i * N), v);
+        ld_f32<N>(w_post + i * N, w);
+        gate_at<T, N>(gate, a.gate, gt, t, d, i * N, g);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          y[q] = fmaf(a.alpha, y[q], a.beta * g[q] * (v[q] * rb * w[q]));
+      }
+    };
+    ss = 0.f;
+    for (int i = tid; i < nvec; i += TPR) {
+      float y[N];
+      row_y(i, y);
+      if (POST) store<T>(out + at + i * N, y);
+#pragma unroll
+      for (int q = 0; q < N; ++q) ss = fmaf(y[q], y[q], ss);
+    }
+    if constexpr (PRE) {
+      ss = row_sum<false>(ss, buf, turn);
+      const float ro = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
+      if (rstd_pre != nullptr && tid == 0) rstd_pre[t] = ro;
+      for (int i = tid; i < nvec; i += TPR) {
+        float y[N], w[N];
+        row_y(i, y);
+        ld_f32<N>(w_pre + i * N, w);
+#pragma unroll
+        for (int q = 0; q < N; ++q) y[q] = y[q] * ro * w[q];
+        store<T>(n + at + i * N, y);
       }
     }
   }
 }
 
-// o[c] = sum over groups p of part[p][which][c], in order: 8 slices of the
-// groups, each added in order, then the slices in order.
+// The column sums of a block live in its part[block][2][d].
+template <typename T, bool POST, bool PRE>
+__global__ void __launch_bounds__(kWideThreads)
+    norm_wide_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
+                         const float* __restrict__ dn, const T* __restrict__ yo,
+                         const T* __restrict__ b, const float* __restrict__ w_post,
+                         const void* __restrict__ gate, const float* __restrict__ w_pre,
+                         const float* __restrict__ rstd_post, const float* __restrict__ rstd_pre,
+                         T* __restrict__ dx, T* __restrict__ db, void* __restrict__ dgate,
+                         float* __restrict__ part) {
+  constexpr int N = Vec<T>::N, TPR = kWideThreads;
+  __shared__ float buf[64];
+  int turn = 0;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, d = a.d, nvec = d / N;
+  const float inv_d = 1.f / static_cast<float>(d);
+  float* part_pre = part + static_cast<size_t>(blockIdx.x) * 2 * d;
+  float* part_post = part_pre + d;
+  const bool elem = POST && a.gate == kGateElement;
+  bool fresh = true;  // this block's first row: the sums start
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x, fresh = false) {
+    const size_t at = static_cast<size_t>(t) * d;
+    const float ro = PRE ? __ldg(rstd_pre + t) : 0.f;
+    const float rb = POST ? __ldg(rstd_post + t) : 0.f;
+    const bool token = POST && a.gate == kGateToken;
+    const float gt = token ? __ldg(static_cast<const float*>(gate) + t) : 1.f;
+    auto pre_at = [&](int i, float (&yh)[N], float (&v)[N], float (&w)[N]) {
+      widen<T>(ld_stream(yo + at + i * N), yh);
+      ld_f32_stream<N>(dn + at + i * N, v);
+      ld_f32<N>(w_pre + i * N, w);
+#pragma unroll
+      for (int q = 0; q < N; ++q) yh[q] *= ro;
+    };
+    float s1 = 0.f;
+    if constexpr (PRE) {
+      for (int i = tid; i < nvec; i += TPR) {
+        float yh[N], v[N], w[N];
+        pre_at(i, yh, v, w);
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          float* o = part_pre + i * N + q;
+          *o = fmaf(v[q], yh[q], fresh ? 0.f : *o);
+          s1 = fmaf(v[q] * w[q], yh[q], s1);
+        }
+      }
+      s1 = row_sum<false>(s1, buf, turn) * inv_d;
+    }
+    auto d_at = [&](int i, float (&D)[N]) {
+      widen<T>(ld_stream(dout + at + i * N), D);
+      if constexpr (PRE) {
+        float yh[N], v[N], w[N];
+        pre_at(i, yh, v, w);
+#pragma unroll
+        for (int q = 0; q < N; ++q) D[q] += ro * (v[q] * w[q] - yh[q] * s1);
+      }
+    };
+    // of the branch: G, the element gate's part of it, bh and the weight
+    auto branch_at = [&](int i, float (&D)[N], float (&bh)[N], float (&w)[N], float (&g)[N]) {
+      widen<T>(ld_stream(b + at + i * N), bh);
+      branch_weight<N>(w_post, gate, a.gate, i * N, w);
+#pragma unroll
+      for (int q = 0; q < N; ++q) g[q] = 1.f;
+      if (elem) widen<T>(ld_stream(static_cast<const T*>(gate) + at + i * N), g);
+#pragma unroll
+      for (int q = 0; q < N; ++q) {
+        bh[q] *= rb;
+        D[q] *= a.beta;
+      }
+    };
+    const float al = POST ? a.alpha : 1.f;
+    float s2 = 0.f;
+    for (int i = tid; i < nvec; i += TPR) {
+      float D[N], o[N];
+      d_at(i, D);
+#pragma unroll
+      for (int q = 0; q < N; ++q) o[q] = al * D[q];
+      store<T>(dx + at + i * N, o);
+      if constexpr (POST) {
+        float bh[N], w[N], g[N];
+        branch_at(i, D, bh, w, g);
+        if (elem) {
+#pragma unroll
+          for (int q = 0; q < N; ++q) o[q] = D[q] * (bh[q] * w[q]);
+          store<T>(static_cast<T*>(dgate) + at + i * N, o);
+        }
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+          float* s = part_post + i * N + q;
+          *s = fmaf(gt * g[q] * D[q], bh[q], fresh ? 0.f : *s);
+          s2 = fmaf(D[q] * g[q] * w[q], bh[q], s2);
+        }
+      }
+    }
+    if constexpr (POST) {
+      s2 = row_sum<false>(s2, buf, turn);
+      if (token && tid == 0) static_cast<float*>(dgate)[t] = s2;
+      s2 *= inv_d;
+      for (int i = tid; i < nvec; i += TPR) {
+        float D[N], bh[N], w[N], g[N], o[N];
+        d_at(i, D);
+        branch_at(i, D, bh, w, g);
+#pragma unroll
+        for (int q = 0; q < N; ++q) o[q] = rb * gt * (D[q] * g[q] * w[q] - bh[q] * s2);
+        store<T>(db + at + i * N, o);
+      }
+    }
+  }
+}
+
+// The groups' column sums, in order: 8 slices of the groups, each added in
+// order, then the slices in order. z 0: dw_pre; 1: dw_post, or with a channel
+// gate A, whence dw_post = g A and dgate = w_post A.
 __global__ void __launch_bounds__(256)
-    reduce_columns_kernel(const float* __restrict__ part, int groups, int d,
-                          float* __restrict__ o_pre, float* __restrict__ o_post,
-                          float* __restrict__ o_gate) {
+    reduce_columns_kernel(const float* __restrict__ part, int groups, int d, int which0,
+                          const float* __restrict__ w_post, const float* __restrict__ gate,
+                          float* __restrict__ dw_pre, float* __restrict__ dw_post,
+                          float* __restrict__ dgate) {
   __shared__ float sm[8][32];
   pdl_wait();
   pdl_trigger();
-  float* outs[3] = {o_pre, o_post, o_gate};
-  float* o = outs[blockIdx.y];
-  if (o == nullptr) return;
+  const int which = which0 + blockIdx.y;
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
   const int per = (groups + 7) / 8;
   const int p1 = min(groups, (sl + 1) * per);
   float s = 0.f;
-  const float* src = part + static_cast<size_t>(blockIdx.y) * d + c;
+  const float* src = part + static_cast<size_t>(which) * d + c;
 #pragma unroll 8
-  for (int p = sl * per; p < p1; ++p) s += src[static_cast<size_t>(p) * 3 * d];
+  for (int p = sl * per; p < p1; ++p) s += src[static_cast<size_t>(p) * 2 * d];
   sm[sl][threadIdx.x & 31] = s;
   __syncthreads();
   if (sl == 0) {
     float r = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) r += sm[i][threadIdx.x];
-    o[c] = r;
+    if (which == 0) {
+      dw_pre[c] = r;
+    } else if (dgate != nullptr) {
+      dw_post[c] = __ldg(gate + c) * r;
+      dgate[c] = __ldg(w_post + c) * r;
+    } else {
+      dw_post[c] = r;
+    }
   }
 }
 
-// How a row of nvec vectors is shared: the narrowest group that holds it
-// with at most `most` vectors a thread; few rows take wider groups, so that
-// the one wave they are runs with as much memory in flight as it can.
-struct Shape {
-  int tpr, nv;
-};
-Shape shape_of(int nvec, int T, int most) {
-  static const int widths[4] = {32, 128, 256, 512};
-  if (T <= kNormFewRows) {
-    for (int w : {32, 128, 256, 512})
-      if (nvec <= w) return {w, 1};
-    if (nvec <= 1024) return {512, 2};
+// Threads to a row of nvec vectors (0: too wide for the ring): a warp for
+// short rows, else two vectors a thread, or one where the rows do not fill
+// the SMs, so that a row is as short as it can be.
+int threads_of(int nvec, int T) {
+  if (nvec > 2 * kRowThreads) return 0;
+  const int per = T <= kNormFewRows ? 1 : 2;
+  const int n = ceil_div(ceil_div(nvec, per), 32) * 32;
+  return nvec <= 32 * per ? 32 : (n < kRowThreads ? n : kRowThreads);
+}
+// Blocks an SM is to hold, at 128 registers a thread.
+int blocks_per_sm(int tpr) { return tpr == 32 ? 4 : 512 / tpr; }
+
+// Bytes of a row's tensors in the ring.
+size_t fwd_slot(int dtype, int d, bool post, bool elem) {
+  return static_cast<size_t>(d) * (dtype == 0 ? 4 : 2) * (1 + (post ? 1 : 0) + (elem ? 1 : 0));
+}
+size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
+  return static_cast<size_t>(d) *
+         ((dtype == 0 ? 4 : 2) * (1 + (pre ? 1 : 0) + (post ? 1 : 0) + (post && elem ? 1 : 0)) +
+          (pre ? 4 : 0));
+}
+constexpr size_t kRingMost = 220 * 1024;  // shared memory a block may take
+constexpr int kFwdStages = 3;
+
+// Backward row groups (each writes its column sums): one wave of blocks, each
+// group with a row of its own where T allows.
+int bwd_groups(int tpr, int T) {
+  if (tpr == 0) return T < 152 ? T : 152;
+  const int rpb = tpr == 32 ? kWarpBlock / 32 : 1, most = 152 * blocks_per_sm(tpr) * rpb;
+  return ceil_div(T < most ? T : most, rpb) * rpb;
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_ring(K kernel, int blocks, int threads, size_t smem, cudaStream_t s,
+                        Args... args) {
+  if (smem > 47 * 1024) {  // (the default limit is 48 KB, of which the sums take some)
+    const cudaError_t e = cudaFuncSetAttribute(
+        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
   }
-  for (int w : widths)
-    if (nvec <= w * most) {
-      const int nv = ceil_div(nvec, w);
-      return {w, nv > 2 ? 4 : nv};
-    }
-  return {512, 0};
+  return launch_pdl(kernel, dim3(blocks), dim3(threads), smem, s, args...);
 }
 
 template <typename T, bool POST, bool PRE>
 struct Fwd {
-  static constexpr int kMost = 4;  // vectors a thread holds
-  template <int TPR, int NV>
-  static cudaError_t go(const NormArgs& a, int groups, const void* x, const void* b,
-                        const float* w_post, const void* gate, const float* w_pre, void* out,
-                        void* n, float* rstd_post, float* rstd_pre, cudaStream_t s) {
-    constexpr int RPB = block_of(TPR) / TPR;
-    return launch_pdl(block_norm_kernel<T, TPR, NV, POST, PRE>, dim3(ceil_div(groups, RPB)),
-                      dim3(block_of(TPR)), 0, s, a, static_cast<const T*>(x),
-                      static_cast<const T*>(b), w_post, gate, w_pre, static_cast<T*>(out),
-                      static_cast<T*>(n), rstd_post, rstd_pre);
+  template <typename... Args>
+  static cudaError_t go(const NormArgs& a, int num_sms, cudaStream_t s, Args... args) {
+    const int nvec = a.d / Vec<T>::N, tpr = threads_of(nvec, a.T);
+    if (tpr == 0)
+      return launch_pdl(norm_wide_kernel<T, POST, PRE>, dim3(a.T < num_sms * 4 ? a.T : num_sms * 4),
+                        dim3(kWideThreads), 0, s, a, args...);
+    const bool elem = POST && a.gate == kGateElement;
+    const size_t slot = fwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, elem) * kFwdStages;
+    if (tpr == 32) {
+      constexpr int RPB = kWarpBlock / 32;
+      const int blocks = ceil_div(a.T, RPB), most = num_sms * 4;
+      return launch_ring(norm_ring_kernel<T, true, kFwdStages, POST, PRE>,
+                         blocks < most ? blocks : most, kWarpBlock, slot * RPB, s, a, args...);
+    }
+    // (more blocks than fit at once are no loss: each takes fewer rows)
+    const int most = num_sms * blocks_per_sm(tpr) * 2;
+    return launch_ring(norm_ring_kernel<T, false, kFwdStages, POST, PRE>, a.T < most ? a.T : most,
+                       tpr, slot, s, a, args...);
   }
 };
+
 template <typename T, bool POST, bool PRE>
 struct Bwd {
-  static constexpr int kMost = 2;
-  template <int TPR, int NV>
-  static cudaError_t go(const NormArgs& a, int groups, const void* dout, const float* dn,
-                        const void* yo, const void* b, const float* w_post, const void* gate,
-                        const float* w_pre, const float* rstd_post, const float* rstd_pre,
-                        void* dx, void* db, void* dgate, float* part, cudaStream_t s) {
-    constexpr int RPB = block_of(TPR) / TPR;
-    return launch_pdl(block_norm_bwd_kernel<T, TPR, NV, POST, PRE>, dim3(groups / RPB),
-                      dim3(block_of(TPR)), 0, s, a, static_cast<const T*>(dout), dn,
-                      static_cast<const T*>(yo), static_cast<const T*>(b), w_post, gate, w_pre,
-                      rstd_post, rstd_pre, static_cast<T*>(dx), static_cast<T*>(db), dgate, part);
+  template <typename... Args>
+  static cudaError_t go(const NormArgs& a, int groups, cudaStream_t s, Args... args) {
+    const int nvec = a.d / Vec<T>::N, tpr = threads_of(nvec, a.T);
+    if (tpr == 0)
+      return launch_pdl(norm_wide_bwd_kernel<T, POST, PRE>, dim3(groups), dim3(kWideThreads), 0, s,
+                        a, args...);
+    const size_t slot = bwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement);
+    if (tpr == 32) {
+      constexpr int RPB = kWarpBlock / 32;
+      return launch_ring(norm_ring_bwd_kernel<T, true, 2, POST, PRE>, groups / RPB, kWarpBlock,
+                         slot * 2 * RPB, s, a, args...);
+    }
+    // three rows in flight where an SM's blocks have room for them
+    return slot * 3 * blocks_per_sm(tpr) <= kRingMost
+               ? launch_ring(norm_ring_bwd_kernel<T, false, 3, POST, PRE>, groups, tpr, slot * 3, s,
+                             a, args...)
+               : launch_ring(norm_ring_bwd_kernel<T, false, 2, POST, PRE>, groups, tpr, slot * 2, s,
+                             a, args...);
   }
 };
 
-template <template <typename, bool, bool> class K, typename T, bool POST, bool PRE,
-          typename... Args>
-cudaError_t by_shape(Shape sh, Args&&... args) {
-  using F = K<T, POST, PRE>;
-  switch (sh.tpr * 8 + sh.nv) {
-    case 32 * 8 + 1: return F::template go<32, 1>(args...);
-    case 32 * 8 + 2: return F::template go<32, 2>(args...);
-    case 128 * 8 + 1: return F::template go<128, 1>(args...);
-    case 128 * 8 + 2: return F::template go<128, 2>(args...);
-    case 256 * 8 + 1: return F::template go<256, 1>(args...);
-    case 256 * 8 + 2: return F::template go<256, 2>(args...);
-    case 512 * 8 + 1: return F::template go<512, 1>(args...);
-    case 512 * 8 + 2: return F::template go<512, 2>(args...);
-    case 512 * 8 + 0: return F::template go<512, 0>(args...);
-  }
-  if constexpr (F::kMost == 4) {
-    switch (sh.tpr) {
-      case 32: return F::template go<32, 4>(args...);
-      case 128: return F::template go<128, 4>(args...);
-      case 256: return F::template go<256, 4>(args...);
-      case 512: return F::template go<512, 4>(args...);
-    }
-  }
-  return cudaErrorInvalidValue;
+template <typename T, template <typename, bool, bool> class K, typename F>
+cudaError_t by_halves(bool post, bool pre, F f) {
+  if (post && pre) return f(K<T, true, true>());
+  if (post) return f(K<T, true, false>());
+  return f(K<T, false, true>());
 }
 
-template <template <typename, bool, bool> class K, typename... Args>
-cudaError_t by_kind(int dtype, bool post, bool pre, Shape sh, Args&&... args) {
-  if (dtype == 0) {
-    if (post && pre) return by_shape<K, float, true, true>(sh, args...);
-    if (post) return by_shape<K, float, true, false>(sh, args...);
-    return by_shape<K, float, false, true>(sh, args...);
-  }
-  if (post && pre) return by_shape<K, __nv_bfloat16, true, true>(sh, args...);
-  if (post) return by_shape<K, __nv_bfloat16, true, false>(sh, args...);
-  return by_shape<K, __nv_bfloat16, false, true>(sh, args...);
+template <typename T>
+cudaError_t forward_of(const NormArgs& a, int num_sms, cudaStream_t s, const void* x,
+                       const void* b, const float* w_post, const void* gate, const float* w_pre,
+                       void* out, void* n, float* rstd_post, float* rstd_pre) {
+  return by_halves<T, Fwd>(b != nullptr, w_pre != nullptr, [&](auto k) {
+    return decltype(k)::go(a, num_sms, s, static_cast<const T*>(x), static_cast<const T*>(b),
+                           w_post, gate, w_pre, static_cast<T*>(out), static_cast<T*>(n),
+                           rstd_post, rstd_pre);
+  });
 }
-
-// Backward row groups: a multiple of the rows per block, at most
-// kNormGroups(tpr), each with at least one row of its own where T allows.
-int bwd_groups(Shape sh, int T) {
-  const int rpb = block_of(sh.tpr) / sh.tpr;
-  const int most = sh.tpr == 32 ? 2432 : (sh.tpr == 128 ? 608 : (sh.nv == 0 ? 152 : 304));
-  const int g = T < most ? T : most;
-  return ceil_div(g, rpb) * rpb;
+template <typename T>
+cudaError_t backward_of(const NormArgs& a, int groups, cudaStream_t s, const void* dout,
+                        const float* dn, const void* yo, const void* b, const float* w_post,
+                        const void* gate, const float* w_pre, const float* rstd_post,
+                        const float* rstd_pre, void* dx, void* db, void* dgate, float* part) {
+  return by_halves<T, Bwd>(b != nullptr, w_pre != nullptr, [&](auto k) {
+    return decltype(k)::go(a, groups, s, static_cast<const T*>(dout), dn,
+                           static_cast<const T*>(yo), static_cast<const T*>(b), w_post, gate,
+                           w_pre, rstd_post, rstd_pre, static_cast<T*>(dx), static_cast<T*>(db),
+                           dgate, part);
+  });
 }
 
 }  // namespace
@@ -606,18 +913,16 @@ cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, 
                               int d, const void* x, const void* b, const float* w_post,
                               const void* gate, const float* w_pre, void* out, void* n,
                               float* rstd_post, float* rstd_pre, int num_sms, cudaStream_t s) {
-  const int vec = dtype == 0 ? 4 : 8;
-  const Shape sh = shape_of(d / vec, T, 4);  // Fwd::kMost
   const NormArgs a{T, d, gate_kind, eps, alpha, beta};
-  // a few rows a group, so that the channel weights stay in L1
-  const int resident = num_sms * (2048 / block_of(sh.tpr)) * (block_of(sh.tpr) / sh.tpr);
-  return by_kind<Fwd>(dtype, b != nullptr, w_pre != nullptr, sh, a, T < resident ? T : resident, x,
-                      b, w_post, gate, w_pre, out, n, rstd_post, rstd_pre, s);
+  return dtype == 0 ? forward_of<float>(a, num_sms, s, x, b, w_post, gate, w_pre, out, n,
+                                        rstd_post, rstd_pre)
+                    : forward_of<__nv_bfloat16>(a, num_sms, s, x, b, w_post, gate, w_pre, out, n,
+                                                rstd_post, rstd_pre);
 }
 
 size_t block_norm_bwd_ws(int dtype, int T, int d) {
-  const Shape sh = shape_of(d / (dtype == 0 ? 4 : 8), T, 2);
-  return static_cast<size_t>(bwd_groups(sh, T)) * 3 * d * sizeof(float);
+  const int groups = bwd_groups(threads_of(d / (dtype == 0 ? 4 : 8), T), T);
+  return static_cast<size_t>(groups) * 2 * d * sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
@@ -626,19 +931,22 @@ cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alp
                                   const float* w_pre, const float* rstd_post,
                                   const float* rstd_pre, void* dx, void* db, float* dw_post,
                                   void* dgate, float* dw_pre, float* part, cudaStream_t s) {
-  const Shape sh = shape_of(d / (dtype == 0 ? 4 : 8), T, 2);
   const NormArgs a{T, d, gate_kind, eps, alpha, beta};
-  const int groups = bwd_groups(sh, T);
+  const int groups = T > 0 ? bwd_groups(threads_of(d / (dtype == 0 ? 4 : 8), T), T) : 0;
   if (T > 0) {
     const cudaError_t e =
-        by_kind<Bwd>(dtype, b != nullptr, w_pre != nullptr, sh, a, groups, dout, dn, yo, b,
-                     w_post, gate, w_pre, rstd_post, rstd_pre, dx, db, dgate, part, s);
+        dtype == 0 ? backward_of<float>(a, groups, s, dout, dn, yo, b, w_post, gate, w_pre,
+                                        rstd_post, rstd_pre, dx, db, dgate, part)
+                   : backward_of<__nv_bfloat16>(a, groups, s, dout, dn, yo, b, w_post, gate, w_pre,
+                                                rstd_post, rstd_pre, dx, db, dgate, part);
     if (e != cudaSuccess) return e;
   }
-  float* cg = b != nullptr && gate_kind == kGateChannel ? static_cast<float*>(dgate) : nullptr;
-  return launch_pdl(reduce_columns_kernel, dim3(d / 32, 3), dim3(256), 0, s,
-                    static_cast<const float*>(part), T > 0 ? groups : 0, d,
-                    w_pre != nullptr ? dw_pre : nullptr, b != nullptr ? dw_post : nullptr, cg);
+  const bool post = b != nullptr, pre = w_pre != nullptr;
+  const bool chan = post && gate_kind == kGateChannel;
+  return launch_pdl(reduce_columns_kernel, dim3(d / 32, (post ? 1 : 0) + (pre ? 1 : 0)), dim3(256),
+                    0, s, static_cast<const float*>(part), groups, d, pre ? 0 : 1, w_post,
+                    chan ? static_cast<const float*>(gate) : nullptr, dw_pre, dw_post,
+                    chan ? static_cast<float*>(dgate) : nullptr);
 }
 
 }  // namespace moe

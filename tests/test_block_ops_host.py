@@ -80,6 +80,14 @@ def test_norm_backward_arguments(lib, gate, kw):
     assert norm_backward(lib, norm(gate=gate), **kw) == L.MOE_ERR_INVALID_ARG
 
 
+def test_norm_backward_of_no_rows_still_checks_what_it_reads(lib):
+    for kw in (dict(w_post=None), dict(gate=None, dgate=P), dict(gate=ODD, dgate=P),
+               dict(gate=P, dgate=None), dict(dw_pre=None)):
+        full = dict(gate=P, dgate=P)
+        full.update(kw)
+        assert norm_backward(lib, norm(T=0, gate=2), **full) == L.MOE_ERR_INVALID_ARG
+
+
 def test_norm_backward_workspace(lib):
     c = norm()
     need = lib.moe_block_norm_backward_workspace_size(ctypes.byref(c))
