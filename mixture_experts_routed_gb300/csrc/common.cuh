@@ -274,8 +274,6 @@ cudaError_t launch_gemm_simt(int epi, const float* A, int a_shared, int R, const
                              cudaStream_t s, float* zout = nullptr);
 
 // ---------------------------------------------------------------- norm.cu
-// Up to this many rows take the widest row groups (one wave of the SMs).
-constexpr int kNormFewRows = 152;
 // The norms around a block (b null: no post half; w_pre null: no pre half);
 // gate_kind as MOE_GATE_*.
 cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, float beta, int T,
@@ -283,7 +281,7 @@ cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, 
                               const void* gate, const float* w_pre, void* out, void* n,
                               float* rstd_post, float* rstd_pre, int num_sms, cudaStream_t s);
 // Bytes of `part` the backward's column sums take.
-size_t block_norm_bwd_ws(int dtype, int T, int d);
+size_t block_norm_bwd_ws(int dtype, int gate_kind, int T, int d);
 cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
                                   int T, int d, const void* dout, const float* dn, const void* yo,
                                   const void* b, const float* w_post, const void* gate,

@@ -918,7 +918,7 @@ int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b, c
 
 size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg) {
   if (check_norm(cfg) != MOE_OK) return 0;
-  return align_up(block_norm_bwd_ws(cfg->dtype, cfg->T > 0 ? cfg->T : 1, cfg->d), kAlign);
+  return align_up(block_norm_bwd_ws(cfg->dtype, cfg->gate, cfg->T > 0 ? cfg->T : 1, cfg->d), kAlign);
 }
 
 int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, const float* dn,

@@ -176,25 +176,36 @@ __device__ __forceinline__ void store2f(float* p, const f2 (&v)[N / 2]) {
   }
 }
 
-// Sum over the threads of a row (a warp, or the block), in a fixed order;
-// every thread gets it. `buf`: 2 x 32 floats, `turn` alternates so that one
-// barrier per sum is enough.
+// Sums of two values over the threads of a row (a warp, or the block), in a
+// fixed order; every thread gets them. `buf`: 2 x 32 pairs, `turn` alternates
+// so that one barrier is enough.
 template <bool WARP>
-__device__ __forceinline__ float row_sum(float v, float* buf, int& turn) {
+__device__ __forceinline__ float2 row_sums(float2 v, float2* buf, int& turn) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  }
   if constexpr (!WARP) {
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* b = buf + turn * 32;
+    float2* b = buf + turn * 32;
     turn ^= 1;
     if (lane == 0) b[w] = v;
     __syncthreads();
-    v = lane < (blockDim.x >> 5) ? b[lane] : 0.f;
+    v = lane < (blockDim.x >> 5) ? b[lane] : float2{0.f, 0.f};
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    v = __shfl_sync(0xffffffffu, v, 0);
+    for (int o = 8; o > 0; o >>= 1) {  // (at most 16 warps)
+      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+    }
+    v.x = __shfl_sync(0xffffffffu, v.x, 0);
+    v.y = __shfl_sync(0xffffffffu, v.y, 0);
   }
   return v;
+}
+// one value, over the block
+__device__ __forceinline__ float row_sum(float v, float2* buf, int& turn) {
+  return row_sums<false>(float2{v, 0.f}, buf, turn).x;
 }
 
 struct NormArgs {
@@ -259,7 +270,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
                      float* __restrict__ rstd_post, float* __restrict__ rstd_pre) {
   constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float buf[64];
+  __shared__ float2 buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -302,18 +313,10 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
   const f2 alpha = dup2(a.alpha);
   const bool token = POST && a.gate == kGateToken;
   float gt_next = token && t0 < a.T ? __ldg(static_cast<const float*>(gate) + t0) : 1.f;
-  int slot = 0;
-  for (int t = t0; t < a.T; t += step) {
-    // the slot that the row before this one was read from is filled again
-    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
-    ptx::cp_async_wait<S - 1>();
-    const uint4* in = mine + slot * size;
-    slot = slot + 1 == S ? 0 : slot + 1;
-    float rb = 0.f;
-    const float gt = gt_next;
-    if (token && t + step < a.T) gt_next = __ldg(static_cast<const float*>(gate) + t + step);
+  // this thread's part of a row's sum of b^2
+  auto b_square = [&](const uint4* in) {
+    f2 ss = 0;
     if constexpr (POST) {
-      f2 ss = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int i = tid + j * tpr;
@@ -324,11 +327,27 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
           for (int q = 0; q < H; ++q) ss = fma2(v[q], v[q], ss);
         }
       }
-      const float2 h = un2(ss);
-      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
-      rb = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
-      if (rstd_post != nullptr && tid == 0) rstd_post[t] = rb;
     }
+    const float2 h = un2(ss);
+    return h.x + h.y;
+  };
+  float sum_b = 0.f;
+  ptx::cp_async_wait<S - 2>();  // the first row
+  if (POST && t0 < a.T) {
+    sum_b = row_sums<WARP>(float2{b_square(mine), 0.f}, buf, turn).x;
+  }
+  int slot = 0;
+  for (int t = t0; t < a.T; t += step) {
+    // the slot that the row before this one was read from is filled again
+    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    ptx::cp_async_wait<S - 2>();  // this row and the next
+    const uint4* in = mine + slot * size;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    const uint4* in_next = mine + slot * size;
+    const float gt = gt_next;
+    if (token && t + step < a.T) gt_next = __ldg(static_cast<const float*>(gate) + t + step);
+    const float rb = POST ? 1.f / sqrtf(fmaf(sum_b, inv_d, a.eps)) : 0.f;
+    if (POST && rstd_post != nullptr && tid == 0) rstd_post[t] = rb;
     const size_t at = static_cast<size_t>(t) * d;
     const f2 scale = dup2(a.beta * gt * rb);
     f2 ss = 0;
@@ -359,10 +378,12 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
         }
       }
     }
+    const float2 h = un2(ss);
+    const float mine_b = t + step < a.T ? b_square(in_next) : 0.f;
+    const float2 sums = row_sums<WARP>(float2{mine_b, h.x + h.y}, buf, turn);
+    sum_b = sums.x;
     if constexpr (PRE) {
-      const float2 h = un2(ss);
-      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
-      const float ro = 1.f / sqrtf(fmaf(sum, inv_d, a.eps));
+      const float ro = 1.f / sqrtf(fmaf(sums.y, inv_d, a.eps));
       if (rstd_pre != nullptr && tid == 0) rstd_pre[t] = ro;
       const f2 r2 = dup2(ro);
 #pragma unroll
@@ -396,7 +417,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
   constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
   constexpr int P = N / 4;  // 16-byte pieces of dn to a vector
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float buf[64];
+  __shared__ float2 buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -469,20 +490,11 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     if (POST) rb_next = __ldg(rstd_post + t);
     if (token) gt_next = __ldg(static_cast<const float*>(gate) + t);
   };
-  fetch(group);
-  int slot = 0;
-  for (int t = group; t < a.T; t += step) {
-    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
-    ptx::cp_async_wait<S - 1>();
-    const uint4* in = mine + slot * size;
-    slot = slot + 1 == S ? 0 : slot + 1;
-    const size_t at = static_cast<size_t>(t) * d;
-    const float ro = ro_next, rb = rb_next, gt = gt_next;
-    fetch(t + step);
-    float s1 = 0.f;  // ro mean(v y)
+  // a row's part of ro mean(v y), and its terms of dw_pre
+  auto first = [&](const uint4* in, float ro) {
+    f2 ss = 0;
     if constexpr (PRE) {
       const f2 r2 = dup2(ro);
-      f2 ss = 0;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int i = tid + j * tpr;
@@ -498,9 +510,25 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
           }
         }
       }
-      const float2 h = un2(ss);
-      s1 = row_sum<WARP>(h.x + h.y, buf, turn) * inv_d;
     }
+    const float2 h = un2(ss);
+    return h.x + h.y;
+  };
+  fetch(group);
+  float s1 = 0.f;
+  ptx::cp_async_wait<S - 2>();  // the first row
+  if (PRE && group < a.T) {
+    s1 = row_sums<WARP>(float2{first(mine, ro_next), 0.f}, buf, turn).x * inv_d;
+  }
+  int slot = 0;
+  for (int t = group; t < a.T; t += step) {
+    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
+    const uint4* in = mine + slot * size;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    const uint4* in_next = mine + slot * size;
+    const size_t at = static_cast<size_t>(t) * d;
+    const float ro = ro_next, rb = rb_next, gt = gt_next;
+    fetch(t + step);
     // D = dout + ro v - ro yh mean(v yh), dx = alpha D and, of the branch, D w
     const f2 r2 = dup2(ro), c2 = dup2(-ro * ro * s1), k2 = dup2(gt * a.beta * rb);
     f2 v2[2][H], ss = 0;
@@ -543,10 +571,14 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
         }
       }
     }
+    ptx::cp_async_wait<S - 2>();  // the next row
+    const float2 h = un2(ss);
+    const float next = t + step < a.T ? first(in_next, ro_next) : 0.f;
+    const float2 sums = row_sums<WARP>(float2{next, h.x + h.y}, buf, turn);
+    s1 = sums.x * inv_d;
     if constexpr (POST) {
       // sum of D w b: beta rb of it is a token gate's gradient
-      const float2 h = un2(ss);
-      const float sum = row_sum<WARP>(h.x + h.y, buf, turn);
+      const float sum = sums.y;
       if (token && tid == 0) static_cast<float*>(dgate)[t] = a.beta * rb * sum;
       const float k = gt * a.beta * rb;
       const f2 kv = dup2(k), kb = dup2(-k * rb * rb * sum * inv_d);
@@ -585,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads)
                      const float* __restrict__ w_pre, T* __restrict__ out, T* __restrict__ n,
                      float* __restrict__ rstd_post, float* __restrict__ rstd_pre) {
   constexpr int N = Vec<T>::N, TPR = kWideThreads;
-  __shared__ float buf[64];
+  __shared__ float2 buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -602,7 +634,7 @@ __global__ void __launch_bounds__(kWideThreads)
 #pragma unroll
         for (int q = 0; q < N; ++q) ss = fmaf(v[q], v[q], ss);
       }
-      ss = row_sum<false>(ss, buf, turn);
+      ss = row_sum(ss, buf, turn);
       rb = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
       if (rstd_post != nullptr && tid == 0) rstd_post[t] = rb;
     }
@@ -627,7 +659,7 @@ __global__ void __launch_bounds__(kWideThreads)
       for (int q = 0; q < N; ++q) ss = fmaf(y[q], y[q], ss);
     }
     if constexpr (PRE) {
-      ss = row_sum<false>(ss, buf, turn);
+      ss = row_sum(ss, buf, turn);
       const float ro = 1.f / sqrtf(fmaf(ss, inv_d, a.eps));
       if (rstd_pre != nullptr && tid == 0) rstd_pre[t] = ro;
       for (int i = tid; i < nvec; i += TPR) {
@@ -653,7 +685,7 @@ __global__ void __launch_bounds__(kWideThreads)
                          T* __restrict__ dx, T* __restrict__ db, void* __restrict__ dgate,
                          float* __restrict__ part) {
   constexpr int N = Vec<T>::N, TPR = kWideThreads;
-  __shared__ float buf[64];
+  __shared__ float2 buf[64];
   int turn = 0;
   pdl_wait();
   pdl_trigger();
@@ -688,7 +720,7 @@ __global__ void __launch_bounds__(kWideThreads)
           s1 = fmaf(v[q] * w[q], yh[q], s1);
         }
       }
-      s1 = row_sum<false>(s1, buf, turn) * inv_d;
+      s1 = row_sum(s1, buf, turn) * inv_d;
     }
     auto d_at = [&](int i, float (&D)[N]) {
       widen<T>(ld_stream(dout + at + i * N), D);
@@ -737,7 +769,7 @@ __global__ void __launch_bounds__(kWideThreads)
       }
     }
     if constexpr (POST) {
-      s2 = row_sum<false>(s2, buf, turn);
+      s2 = row_sum(s2, buf, turn);
       if (token && tid == 0) static_cast<float*>(dgate)[t] = s2;
       s2 *= inv_d;
       for (int i = tid; i < nvec; i += TPR) {
@@ -789,16 +821,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // Threads to a row of nvec vectors (0: too wide for the ring): a warp for
-// short rows, else two vectors a thread, or one where the rows do not fill
-// the SMs, so that a row is as short as it can be.
-int threads_of(int nvec, int T) {
+// short rows, one vector a thread up to 512 of them, else two.
+int threads_of(int nvec) {
   if (nvec > 2 * kRowThreads) return 0;
-  const int per = T <= kNormFewRows ? 1 : 2;
-  const int n = ceil_div(ceil_div(nvec, per), 32) * 32;
-  return nvec <= 32 * per ? 32 : (n < kRowThreads ? n : kRowThreads);
+  return ceil_div(nvec <= kRowThreads ? nvec : ceil_div(nvec, 2), 32) * 32;
 }
-// Blocks an SM is to hold, at 128 registers a thread.
-int blocks_per_sm(int tpr) { return tpr == 32 ? 4 : 512 / tpr; }
 
 // Bytes of a row's tensors in the ring.
 size_t fwd_slot(int dtype, int d, bool post, bool elem) {
@@ -809,14 +836,26 @@ size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
          ((dtype == 0 ? 4 : 2) * (1 + (pre ? 1 : 0) + (post ? 1 : 0) + (post && elem ? 1 : 0)) +
           (pre ? 4 : 0));
 }
-constexpr size_t kRingMost = 220 * 1024;  // shared memory a block may take
-constexpr int kFwdStages = 3;
+constexpr size_t kRingMost = 220 * 1024;  // shared memory an SM has for its blocks
+constexpr int kStages = 3;
 
-// Backward row groups (each writes its column sums): one wave of blocks, each
-// group with a row of its own where T allows.
-int bwd_groups(int tpr, int T) {
+// Blocks an SM is to hold: what their registers (128 a thread) and rings
+// leave room for.
+int blocks_per_sm(int tpr, size_t ring) {
+  const int threads = tpr == 32 ? kWarpBlock : tpr, by_regs = 512 / threads;
+  const int by_ring = static_cast<int>(kRingMost / ring);
+  const int n = by_regs < by_ring ? by_regs : by_ring;
+  return n < 1 ? 1 : n;
+}
+
+// Backward row groups (each writes its column sums): one wave of blocks of
+// the form with both halves, each group with a row of its own where T allows.
+int bwd_groups(int dtype, int d, bool elem, int T) {
+  const int tpr = threads_of(d / (dtype == 0 ? 4 : 8));
   if (tpr == 0) return T < 152 ? T : 152;
-  const int rpb = tpr == 32 ? kWarpBlock / 32 : 1, most = 152 * blocks_per_sm(tpr) * rpb;
+  const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
+  const size_t ring = bwd_slot(dtype, d, true, true, elem) * kStages * rpb;
+  const int most = 152 * blocks_per_sm(tpr, ring) * rpb;
   return ceil_div(T < most ? T : most, rpb) * rpb;
 }
 
@@ -835,22 +874,19 @@ template <typename T, bool POST, bool PRE>
 struct Fwd {
   template <typename... Args>
   static cudaError_t go(const NormArgs& a, int num_sms, cudaStream_t s, Args... args) {
-    const int nvec = a.d / Vec<T>::N, tpr = threads_of(nvec, a.T);
+    const int tpr = threads_of(a.d / Vec<T>::N);
     if (tpr == 0)
       return launch_pdl(norm_wide_kernel<T, POST, PRE>, dim3(a.T < num_sms * 4 ? a.T : num_sms * 4),
                         dim3(kWideThreads), 0, s, a, args...);
     const bool elem = POST && a.gate == kGateElement;
-    const size_t slot = fwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, elem) * kFwdStages;
-    if (tpr == 32) {
-      constexpr int RPB = kWarpBlock / 32;
-      const int blocks = ceil_div(a.T, RPB), most = num_sms * 4;
-      return launch_ring(norm_ring_kernel<T, true, kFwdStages, POST, PRE>,
-                         blocks < most ? blocks : most, kWarpBlock, slot * RPB, s, a, args...);
-    }
-    // (more blocks than fit at once are no loss: each takes fewer rows)
-    const int most = num_sms * blocks_per_sm(tpr) * 2;
-    return launch_ring(norm_ring_kernel<T, false, kFwdStages, POST, PRE>, a.T < most ? a.T : most,
-                       tpr, slot, s, a, args...);
+    const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
+    const size_t ring = fwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, elem) * kStages * rpb;
+    const int most = num_sms * blocks_per_sm(tpr, ring), blocks = ceil_div(a.T, rpb);
+    const int grid = blocks < most ? blocks : most;
+    return tpr == 32 ? launch_ring(norm_ring_kernel<T, true, kStages, POST, PRE>, grid, kWarpBlock,
+                                   ring, s, a, args...)
+                     : launch_ring(norm_ring_kernel<T, false, kStages, POST, PRE>, grid, tpr, ring,
+                                   s, a, args...);
   }
 };
 
@@ -858,20 +894,20 @@ template <typename T, bool POST, bool PRE>
 struct Bwd {
   template <typename... Args>
   static cudaError_t go(const NormArgs& a, int groups, cudaStream_t s, Args... args) {
-    const int nvec = a.d / Vec<T>::N, tpr = threads_of(nvec, a.T);
+    const int tpr = threads_of(a.d / Vec<T>::N);
     if (tpr == 0)
       return launch_pdl(norm_wide_bwd_kernel<T, POST, PRE>, dim3(groups), dim3(kWideThreads), 0, s,
                         a, args...);
-    const size_t slot = bwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement);
-    if (tpr == 32) {
-      constexpr int RPB = kWarpBlock / 32;
-      return launch_ring(norm_ring_bwd_kernel<T, true, 2, POST, PRE>, groups / RPB, kWarpBlock,
-                         slot * 2 * RPB, s, a, args...);
-    }
-    // three rows in flight where an SM's blocks have room for them
-    return slot * 3 * blocks_per_sm(tpr) <= kRingMost
-               ? launch_ring(norm_ring_bwd_kernel<T, false, 3, POST, PRE>, groups, tpr, slot * 3, s,
-                             a, args...)
+    const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
+    const size_t slot =
+        bwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement) * rpb;
+    if (tpr == 32)
+      return launch_ring(norm_ring_bwd_kernel<T, true, kStages, POST, PRE>, groups / rpb, kWarpBlock,
+                         slot * kStages, s, a, args...);
+    // the longest rows leave room for two
+    return slot * kStages <= kRingMost
+               ? launch_ring(norm_ring_bwd_kernel<T, false, kStages, POST, PRE>, groups, tpr,
+                             slot * kStages, s, a, args...)
                : launch_ring(norm_ring_bwd_kernel<T, false, 2, POST, PRE>, groups, tpr, slot * 2, s,
                              a, args...);
   }
@@ -920,9 +956,9 @@ cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, 
                                                 rstd_post, rstd_pre);
 }
 
-size_t block_norm_bwd_ws(int dtype, int T, int d) {
-  const int groups = bwd_groups(threads_of(d / (dtype == 0 ? 4 : 8), T), T);
-  return static_cast<size_t>(groups) * 2 * d * sizeof(float);
+size_t block_norm_bwd_ws(int dtype, int gate_kind, int T, int d) {
+  return static_cast<size_t>(bwd_groups(dtype, d, gate_kind == kGateElement, T)) * 2 * d *
+         sizeof(float);
 }
 
 cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
@@ -932,7 +968,7 @@ cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alp
                                   const float* rstd_pre, void* dx, void* db, float* dw_post,
                                   void* dgate, float* dw_pre, float* part, cudaStream_t s) {
   const NormArgs a{T, d, gate_kind, eps, alpha, beta};
-  const int groups = T > 0 ? bwd_groups(threads_of(d / (dtype == 0 ? 4 : 8), T), T) : 0;
+  const int groups = T > 0 ? bwd_groups(dtype, d, gate_kind == kGateElement, T) : 0;
   if (T > 0) {
     const cudaError_t e =
         dtype == 0 ? backward_of<float>(a, groups, s, dout, dn, yo, b, w_post, gate, w_pre,
