@@ -839,10 +839,10 @@ size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
 constexpr size_t kRingMost = 220 * 1024;  // shared memory an SM has for its blocks
 constexpr int kStages = 3;
 
-// Blocks an SM is to hold: what their registers (128 a thread) and rings
-// leave room for.
-int blocks_per_sm(int tpr, size_t ring) {
-  const int threads = tpr == 32 ? kWarpBlock : tpr, by_regs = 512 / threads;
+// Blocks an SM is to hold: what their registers (96 a thread forward, 128
+// backward) and rings leave room for.
+int blocks_per_sm(int tpr, int regs, size_t ring) {
+  const int threads = tpr == 32 ? kWarpBlock : tpr, by_regs = 65536 / (regs * threads);
   const int by_ring = static_cast<int>(kRingMost / ring);
   const int n = by_regs < by_ring ? by_regs : by_ring;
   return n < 1 ? 1 : n;
@@ -855,7 +855,7 @@ int bwd_groups(int dtype, int d, bool elem, int T) {
   if (tpr == 0) return T < 152 ? T : 152;
   const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
   const size_t ring = bwd_slot(dtype, d, true, true, elem) * kStages * rpb;
-  const int most = 152 * blocks_per_sm(tpr, ring) * rpb;
+  const int most = 152 * blocks_per_sm(tpr, 128, ring) * rpb;
   return ceil_div(T < most ? T : most, rpb) * rpb;
 }
 
@@ -881,7 +881,7 @@ struct Fwd {
     const bool elem = POST && a.gate == kGateElement;
     const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
     const size_t ring = fwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, elem) * kStages * rpb;
-    const int most = num_sms * blocks_per_sm(tpr, ring), blocks = ceil_div(a.T, rpb);
+    const int most = num_sms * blocks_per_sm(tpr, 96, ring), blocks = ceil_div(a.T, rpb);
     const int grid = blocks < most ? blocks : most;
     return tpr == 32 ? launch_ring(norm_ring_kernel<T, true, kStages, POST, PRE>, grid, kWarpBlock,
                                    ring, s, a, args...)
