@@ -82,7 +82,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 def _s(stream):
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is not None and torch.cuda.is_initialized():
+    if _raw_stream is not None:  # (called once the tensors are known to be in GPU memory)
         return _raw_stream(torch._C._cuda_getDevice())
     return torch.cuda.current_stream().cuda_stream
 
@@ -257,8 +257,7 @@ def forward_few(c, x, Wg, bias, W1, W2, *, ws, out=None, noise=None, stream=None
     if out is None:
         out = torch.empty((cc.T, cc.d), dtype=torch.bfloat16, device=x.device)
     st = L.load().moe_forward_few(ctypes.byref(cc), _p(x), _p(Wg), _p(bias), _p(noise), _p(W1),
-                                  _p(W2), _p(out), _p(ws), ws.numel() * ws.element_size(),
-                                  _s(stream))
+                                  _p(W2), _p(out), _p(ws), ws.nbytes, _s(stream))
     _check(st, "moe_forward_few")
     return out
 
@@ -354,18 +353,24 @@ def alloc_norm_workspace(c, device=None) -> torch.Tensor:
 
 
 def _shaped(name, t, shape, dtype):
-    """A tensor of the call's shape and type, or None."""
+    """Device address of a tensor of the call's shape and type (None stays None)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype:
+    if t.shape != shape or t.dtype is not dtype:
         raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {tuple(t.shape)} {t.dtype}, not "
                                               f"{tuple(shape)} {dtype}")
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     return _p(t)
 
 
-def _gate_form(c):
-    return {L.MOE_GATE_TOKEN: ((c.T,), torch.float32), L.MOE_GATE_CHANNEL: ((c.d,), torch.float32),
-            L.MOE_GATE_ELEMENT: ((c.T, c.d), _ndt(c))}.get(c.gate)
+def _gate_form(kind, T, d, dt):
+    """(shape, type) of the gate, None without one."""
+    if kind == L.MOE_GATE_TOKEN:
+        return (T,), torch.float32
+    if kind == L.MOE_GATE_CHANNEL:
+        return (d,), torch.float32
+    return ((T, d), dt) if kind == L.MOE_GATE_ELEMENT else None
 
 
 def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=None,
@@ -373,23 +378,29 @@ def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=
     """out = alpha x + beta gate * norm(b) w_post and n = norm(out) w_pre; without ``b``
     out is x, without ``w_pre`` there is no n. ``want_rstd``: keep the statistics the
     backward reads."""
-    dt, td, f32 = _ndt(c), (c.T, c.d), torch.float32
+    T, d, f32 = c.T, c.d, torch.float32
+    dt, td = _ndt(c), (T, d)
     post, pre = b is not None, w_pre is not None
-    if post and out is None:
-        out = torch.empty(td, dtype=dt, device=x.device)
-    if pre and n is None:
-        n = torch.empty(td, dtype=dt, device=x.device)
+    px = _shaped("x", x, td, dt)
+    if out is not None or not post:
+        po = _shaped("out", out, td, dt)
+    else:
+        out = torch.empty_like(x)
+        po = out.data_ptr()
+    if n is not None or not pre:
+        pn = _shaped("n", n, td, dt)
+    else:
+        n = torch.empty_like(x)
+        pn = n.data_ptr()
     if want_rstd and post and rstd_post is None:
-        rstd_post = torch.empty(c.T, dtype=f32, device=x.device)
+        rstd_post = torch.empty(T, dtype=f32, device=x.device)
     if want_rstd and pre and rstd_pre is None:
-        rstd_pre = torch.empty(c.T, dtype=f32, device=x.device)
-    form = _gate_form(c) if post else None
+        rstd_pre = torch.empty(T, dtype=f32, device=x.device)
+    form = _gate_form(c.gate, T, d, dt) if post else None
     st = L.load().moe_block_norm(
-        ctypes.byref(c), _shaped("x", x, td, dt), _shaped("b", b, td, dt),
-        _shaped("w_post", w_post, (c.d,), f32),
-        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (c.d,), f32),
-        _shaped("out", out, td, dt), _shaped("n", n, td, dt),
-        _shaped("rstd_post", rstd_post, (c.T,), f32), _shaped("rstd_pre", rstd_pre, (c.T,), f32),
+        ctypes.byref(c), px, _shaped("b", b, td, dt), _shaped("w_post", w_post, (d,), f32),
+        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (d,), f32),
+        po, pn, _shaped("rstd_post", rstd_post, (T,), f32), _shaped("rstd_pre", rstd_pre, (T,), f32),
         _s(stream))
     _check(st, "moe_block_norm")
     return {"out": out, "n": n, "rstd_post": rstd_post, "rstd_pre": rstd_pre}
@@ -401,23 +412,24 @@ def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_
     ``b``), ``dout`` the gradient that reaches y by the residual, ``dn`` (fp32) the one of
     n. dx, db, an element gate's dgate in the config's type; dw_post, dw_pre and the other
     dgate fp32; None for what the forward left out."""
-    dt, td, f32, dev = _ndt(c), (c.T, c.d), torch.float32, dout.device
+    T, d, f32 = c.T, c.d, torch.float32
+    dt, td = _ndt(c), (T, d)
     post, pre = w_post is not None, w_pre is not None
-    form = _gate_form(c) if post else None
-
-    def new(on, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=dev) if on else None
-
-    g = {"dx": new(True, td, dt), "db": new(post, td, dt), "dw_post": new(post, (c.d,), f32),
-         "dgate": new(True, *form) if form else None, "dw_pre": new(pre, (c.d,), f32)}
+    form = _gate_form(c.gate, T, d, dt) if post else None
+    pd = _shaped("dout", dout, td, dt)
+    g = {"dx": torch.empty_like(dout), "db": torch.empty_like(dout) if post else None,
+         "dw_post": torch.empty_like(w_post) if post else None, "dgate": None,
+         "dw_pre": torch.empty_like(w_pre) if pre else None}
+    if form:
+        g["dgate"] = torch.empty(form[0], dtype=form[1], device=dout.device)
     st = L.load().moe_block_norm_backward(
-        ctypes.byref(c), _shaped("dout", dout, td, dt), _shaped("dn", dn, td, f32),
-        _shaped("y", y, td, dt), _shaped("b", b, td, dt), _shaped("w_post", w_post, (c.d,), f32),
-        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (c.d,), f32),
-        _shaped("rstd_post", rstd_post, (c.T,), f32) if post else None,
-        _shaped("rstd_pre", rstd_pre, (c.T,), f32) if pre else None, _p(g["dx"]), _p(g["db"]),
-        _p(g["dw_post"]), _p(g["dgate"]), _p(g["dw_pre"]), _p(ws),
-        ws.numel() * ws.element_size(), _s(stream))
+        ctypes.byref(c), pd, _shaped("dn", dn, td, f32), _shaped("y", y, td, dt),
+        _shaped("b", b, td, dt), _shaped("w_post", w_post, (d,), f32),
+        _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (d,), f32),
+        _shaped("rstd_post", rstd_post, (T,), f32) if post else None,
+        _shaped("rstd_pre", rstd_pre, (T,), f32) if pre else None,
+        *[None if t is None else t.data_ptr() for t in g.values()], _p(ws), ws.nbytes,
+        _s(stream))
     _check(st, "moe_block_norm_backward")
     return g
 
@@ -436,36 +448,34 @@ def alloc_mx4_workspace(c, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-def _scales(size, c, device):
-    n = int(size(ctypes.byref(c)))
-    if n == 0:
-        raise MoEError(L.MOE_ERR_INVALID_ARG, "mx4 config")
-    return torch.empty(n, dtype=torch.uint8, device=device)
-
-
-def _scale_p(name, size, c, t):
-    if t.dtype != torch.uint8 or t.numel() < int(size(ctypes.byref(c))):
-        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {t.numel()} {t.dtype}")
+def _scale_p(name, n, t):
+    if t.dtype is not torch.uint8 or t.numel() < n or n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {t.numel()} {t.dtype}, not {n} uint8")
     return _p(t)
 
 
 def _indices(name, t, n):
-    if t is not None and (t.dtype != torch.int32 or t.numel() != n):
+    if t is not None and (t.dtype is not torch.int32 or t.numel() != n):
         raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {t.numel()} {t.dtype}, not {n} int32")
     return _p(t)
 
 
+def _bytes(n, device):
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def mx4_quantize_weights(c, W, *, q=None, scale=None, stream=None):
     """W [E, K, N] -> (codes uint8 [E, N, K / 2], scales uint8 in the product's layout)."""
-    lib = L.load()
+    lib, r = L.load(), ctypes.byref(c)
+    E, K, N = c.E, c.K, c.N
+    n = lib.moe_mx4_weight_scale_size(r)
     if q is None:
-        q = torch.empty((c.E, c.N, c.K // 2), dtype=torch.uint8, device=W.device)
+        q = torch.empty((E, N, K // 2), dtype=torch.uint8, device=W.device)
     if scale is None:
-        scale = _scales(lib.moe_mx4_weight_scale_size, c, W.device)
-    st = lib.moe_mx4_quantize_weights(
-        ctypes.byref(c), _shaped("W", W, (c.E, c.K, c.N), _ndt(c)),
-        _shaped("q", q, (c.E, c.N, c.K // 2), torch.uint8),
-        _scale_p("scale", lib.moe_mx4_weight_scale_size, c, scale), _s(stream))
+        scale = _bytes(n, W.device)
+    st = lib.moe_mx4_quantize_weights(r, _shaped("W", W, (E, K, N), _ndt(c)),
+                                      _shaped("q", q, (E, N, K // 2), torch.uint8),
+                                      _scale_p("scale", n, scale), _s(stream))
     _check(st, "moe_mx4_quantize_weights")
     return q, scale
 
@@ -473,59 +483,63 @@ def mx4_quantize_weights(c, W, *, q=None, scale=None, stream=None):
 def mx4_quantize_rows(c, x, offsets, *, ws, src=None, q=None, scale=None, stream=None):
     """Rows x [R, K], or with ``src`` [R] the rows x[src] of x [x_rows, K] -> (codes uint8
     [R, K / 2], scales uint8 laid out for ``offsets``)."""
-    lib = L.load()
+    lib, r = L.load(), ctypes.byref(c)
+    R, K = c.R, c.K
+    n = lib.moe_mx4_row_scale_size(r)
     if q is None:
-        q = torch.empty((c.R, c.K // 2), dtype=torch.uint8, device=x.device)
+        q = torch.empty((R, K // 2), dtype=torch.uint8, device=x.device)
     if scale is None:
-        scale = _scales(lib.moe_mx4_row_scale_size, c, x.device)
+        scale = _bytes(n, x.device)
     st = lib.moe_mx4_quantize_rows(
-        ctypes.byref(c), _shaped("x", x, (c.R if src is None else c.x_rows, c.K), _ndt(c)),
-        _indices("src", src, c.R), _indices("offsets", offsets, c.E + 1),
-        _shaped("q", q, (c.R, c.K // 2), torch.uint8),
-        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale), _p(ws),
-        ws.numel() * ws.element_size(), _s(stream))
+        r, _shaped("x", x, (R if src is None else c.x_rows, K), _ndt(c)),
+        _indices("src", src, R), _indices("offsets", offsets, c.E + 1),
+        _shaped("q", q, (R, K // 2), torch.uint8), _scale_p("scale", n, scale), _p(ws), ws.nbytes,
+        _s(stream))
     _check(st, "moe_mx4_quantize_rows")
     return q, scale
 
 
 def mx4_product(c, q, scale, wq, w_scale, offsets, *, ws, out=None, stream=None):
     """out[r] = rows q[r] . weights wq[e] over each expert's segment, [R, N]."""
-    lib = L.load()
+    lib, r = L.load(), ctypes.byref(c)
+    R, K, N, E = c.R, c.K, c.N, c.E
     odt = torch.float32 if c.out_dtype == L.MOE_DTYPE_F32 else torch.bfloat16
     if out is None:
-        out = torch.empty((c.R, c.N), dtype=odt, device=q.device)
+        out = torch.empty((R, N), dtype=odt, device=q.device)
     st = lib.moe_mx4_product(
-        ctypes.byref(c), _shaped("q", q, (c.R, c.K // 2), torch.uint8),
-        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale),
-        _shaped("wq", wq, (c.E, c.N, c.K // 2), torch.uint8),
-        _scale_p("w_scale", lib.moe_mx4_weight_scale_size, c, w_scale),
-        _indices("offsets", offsets, c.E + 1), _shaped("out", out, (c.R, c.N), odt), _p(ws),
-        ws.numel() * ws.element_size(), _s(stream))
+        r, _shaped("q", q, (R, K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_row_scale_size(r), scale),
+        _shaped("wq", wq, (E, N, K // 2), torch.uint8),
+        _scale_p("w_scale", lib.moe_mx4_weight_scale_size(r), w_scale),
+        _indices("offsets", offsets, E + 1), _shaped("out", out, (R, N), odt), _p(ws), ws.nbytes,
+        _s(stream))
     _check(st, "moe_mx4_product")
     return out
 
 
 def mx4_dequantize_weights(c, wq, w_scale, *, W=None, stream=None):
     """The values of quantised weights, [E, K, N]."""
-    lib = L.load()
+    lib, r = L.load(), ctypes.byref(c)
+    E, K, N = c.E, c.K, c.N
     if W is None:
-        W = torch.empty((c.E, c.K, c.N), dtype=_ndt(c), device=wq.device)
+        W = torch.empty((E, K, N), dtype=_ndt(c), device=wq.device)
     st = lib.moe_mx4_dequantize_weights(
-        ctypes.byref(c), _shaped("wq", wq, (c.E, c.N, c.K // 2), torch.uint8),
-        _scale_p("w_scale", lib.moe_mx4_weight_scale_size, c, w_scale),
-        _shaped("W", W, (c.E, c.K, c.N), _ndt(c)), _s(stream))
+        r, _shaped("wq", wq, (E, N, K // 2), torch.uint8),
+        _scale_p("w_scale", lib.moe_mx4_weight_scale_size(r), w_scale),
+        _shaped("W", W, (E, K, N), _ndt(c)), _s(stream))
     _check(st, "moe_mx4_dequantize_weights")
     return W
 
 
 def mx4_dequantize_rows(c, q, scale, offsets, *, x=None, stream=None):
     """The values of quantised rows, [R, K] (rows outside the segments are not written)."""
-    lib = L.load()
+    lib, r = L.load(), ctypes.byref(c)
+    R, K = c.R, c.K
     if x is None:
-        x = torch.empty((c.R, c.K), dtype=_ndt(c), device=q.device)
+        x = torch.empty((R, K), dtype=_ndt(c), device=q.device)
     st = lib.moe_mx4_dequantize_rows(
-        ctypes.byref(c), _shaped("q", q, (c.R, c.K // 2), torch.uint8),
-        _scale_p("scale", lib.moe_mx4_row_scale_size, c, scale),
-        _indices("offsets", offsets, c.E + 1), _shaped("x", x, (c.R, c.K), _ndt(c)), _s(stream))
+        r, _shaped("q", q, (R, K // 2), torch.uint8),
+        _scale_p("scale", lib.moe_mx4_row_scale_size(r), scale),
+        _indices("offsets", offsets, c.E + 1), _shaped("x", x, (R, K), _ndt(c)), _s(stream))
     _check(st, "moe_mx4_dequantize_rows")
     return x

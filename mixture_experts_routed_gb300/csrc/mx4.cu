@@ -25,7 +25,6 @@
 
 #include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "ptx.cuh"
@@ -80,14 +79,13 @@ __device__ __forceinline__ uint32_t pack8(const float (&v)[8]) {
       : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
   return r;
 }
-// the values of the two codes in the low byte of c
-__device__ __forceinline__ float2 code_pair(uint32_t c) {
-  uint32_t h;
-  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t}"
-      : "=r"(h)
-      : "r"(c));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// The value of code j of the eight in w: its bits as the top of a number
+// (sign; exponent and mantissa at 24..22, so 2^-126 times the value, the code
+// .5 a subnormal) and then scaled; four instructions where the conversion
+// instruction runs at a fraction of the rate.
+__device__ __forceinline__ float code_value(uint32_t w, int j) {
+  const uint32_t t = w << (28 - 4 * j);
+  return __uint_as_float((t & 0x80000000u) | ((t >> 6) & 0x01c00000u)) * 0x1p126f;
 }
 
 // The segments' row tiles: seg[e] = offsets[e], base[e] = row tiles before
@@ -240,11 +238,7 @@ __global__ void __launch_bounds__(256)
     T* o = out + static_cast<size_t>(r) * K + k;
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const float2 f = code_pair(c >> (4 * j));
-      v[j] = f.x * s;
-      v[j + 1] = f.y * s;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = code_value(c, j) * s;
     if constexpr (sizeof(T) == 4) {
       reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -329,6 +323,8 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
       static_cast<uint16_t>(s2[0] | s2[1] << 8);
 }
 
+// And back: a thread takes one block of 32 of two neighbouring n, so that it
+// writes both values of a k at once.
 template <typename T>
 __global__ void __launch_bounds__(kWeightThreads<T>)
     mx4_weights_back_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc, int K,
@@ -338,23 +334,21 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
   pdl_wait();
   pdl_trigger();
   const int n0 = blockIdx.x * 64, k0 = blockIdx.y * KT, e = blockIdx.z;
-  const int n = threadIdx.x & 63, kt = (threadIdx.x >> 6) * 64;
+  const int n = (threadIdx.x & 31) * 2, kt = (threadIdx.x >> 5) * 32;
   if (k0 + kt < K) {
-    const uint32_t s2 =
-        __ldg(reinterpret_cast<const uint16_t*>(sc + weight_scale_at(e, n0 + n, k0 + kt, K, N)));
-    const uint4* c = reinterpret_cast<const uint4*>(
-        q + (static_cast<size_t>(e) * N + n0 + n) * (K / 2) + (k0 + kt) / 2);
-    const uint4 both[2] = {ld_once(c), ld_once(c + 1)};
+    const uint8_t* c = q + (static_cast<size_t>(e) * N + n0 + n) * (K / 2) + (k0 + kt) / 2;
+    const uint4 a4 = __ldg(reinterpret_cast<const uint4*>(c));
+    const uint4 b4 = __ldg(reinterpret_cast<const uint4*>(c + K / 2));
+    const size_t at = weight_scale_at(e, n0 + n, k0 + kt, K, N);
+    const float sa = scale_value(__ldg(sc + at)), sb = scale_value(__ldg(sc + at + 16));
+    const uint32_t wa[4] = {a4.x, a4.y, a4.z, a4.w}, wb[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 c4 = both[h];
-      const float s = scale_value((s2 >> (8 * h)) & 255u);
-      const uint32_t w[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float2 f = code_pair(w[j >> 3] >> (4 * (j & 7)));
-        tile[kt + h * 32 + j][n] = static_cast<T>(f.x * s);
-        tile[kt + h * 32 + j + 1][n] = static_cast<T>(f.y * s);
+    for (int j = 0; j < 32; ++j) {
+      const float fa = code_value(wa[j >> 3], j & 7) * sa, fb = code_value(wb[j >> 3], j & 7) * sb;
+      if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float2*>(&tile[kt + j][n]) = make_float2(fa, fb);
+      } else {
+        *reinterpret_cast<__nv_bfloat162*>(&tile[kt + j][n]) = __floats2bfloat162_rn(fa, fb);
       }
     }
   }
