@@ -12,7 +12,7 @@
 // the first W1 tile to the last W2 tile without draining.
 //
 // Products: the weights are the M operand of tcgen05.mma, 128 output
-// features x 64 contraction rows a tile, read MN-major straight from their
+// features x 128 contraction rows a step, read MN-major straight from their
 // row-major storage; the tokens are the N operand. Every token multiplies
 // every chosen expert (N = 16..64 costs the tensor core nothing here) and
 // the epilogue keeps the routed ones, so nothing is permuted or packed. For
@@ -20,7 +20,7 @@
 // (h to 2^-17 relative, so out is rounded once).
 //
 // Work split: the tiles of a phase, k innermost, are one sequence of steps
-// (64 contraction rows x 128 features), cut into equal ranges, one per CTA.
+// (128 contraction rows x 128 features), cut into equal ranges, one per CTA.
 // A feature block whose steps fall to several CTAs is joined from their fp32
 // partial sums by the last of them to arrive, in CTA order: no atomics on
 // values, so the result is bitwise reproducible on one GPU model. In phase 1
@@ -52,13 +52,13 @@ using namespace ptx;
 
 namespace fw {
 constexpr int THREADS = 256;
-constexpr int BM = 128, BK = 64;            // features, contraction rows of a step
-constexpr int BOX_BYTES = BK * 64 * 2;      // [64 k][64 features] bf16
-constexpr int A_BYTES = 2 * BOX_BYTES;
+constexpr int BM = 128, BK = 128;           // features, contraction rows of a step
+constexpr int BOX_BYTES = 64 * 64 * 2;      // [64 k][64 features] bf16
+constexpr int A_BYTES = 4 * BOX_BYTES;      // [k half][feature half]
 constexpr int GATE_E = 64;                  // experts of a gate CTA
 constexpr int GATE_ROWS = 256;              // contraction rows staged at a time
 constexpr int MAX_LOADS = 32;               // partial sums of a logit a thread adds up
-constexpr int WARM_STEPS = 24;              // W2 steps prefetched to L2: 58 MB over 152 CTAs
+constexpr int WARM_STEPS = 12;              // W2 steps prefetched to L2: 58 MB over 152 CTAs
 constexpr int TMEM_COLS = 128;              // two accumulators of 64 columns
 constexpr int MAX_ROWS = kFewMaxTokens * kMaxFanout;
 
@@ -72,7 +72,8 @@ struct Cfg {
   static constexpr int VE = TP <= 8 ? 8 : 64 / TP;
   static constexpr int LPR = GATE_E / VE, RG = THREADS / LPR;
   static constexpr int CB = 32 / TP;            // partial sums joined at a time
-  static constexpr int B_BYTES = (N1 > N2 ? N1 : N2) * 128;
+  static constexpr int B_HALF = (N1 > N2 ? N1 : N2) * 128;  // 64 k of every column
+  static constexpr int B_BYTES = 2 * B_HALF;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 200 * 1024 / STAGE;
   static constexpr int OFF_BAR = STAGES * STAGE;
@@ -440,7 +441,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int nslots = *s_nslots;
   const int FB = (f + BM - 1) / BM, DB = (d + BM - 1) / BM;
-  const Range r1(nslots * FB, d / BK, grid), r2(DB * nslots, f / BK, grid);
+  const Range r1(nslots * FB, (d + BK - 1) / BK, grid), r2(DB * nslots, (f + BK - 1) / BK, grid);
 
   if (nslots == 0) {
     for (size_t i = static_cast<size_t>(cta) * THREADS + tid; i < static_cast<size_t>(T) * d;
@@ -460,16 +461,19 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     uint32_t ph = 0;
     int used = 0;  // stages filled at least once
     bool dead = false;
-    // a step's weight boxes, rows [row, row + 64) x features [c0, c0 + 64 nb),
-    // and the byte count of all it loads
-    auto load_a = [&](const CUtensorMap* m, int row, int c0, int nb, uint32_t b_bytes) {
+    // a step's loads: weight rows [row, row + 64 nk) x features [c0, c0 + 64
+    // nb), and as much of k from column k on of box rows at b_row of the
+    // tokens' side (b_bytes a 64-wide box); nk = 1 in a last half step
+    auto load_a = [&](const CUtensorMap* m, int row, int c0, int nk, int nb, uint32_t b_bytes) {
       uint8_t* st = smem + s * C::STAGE;
-      mbar_arrive_expect_tx(&full[s], nb * BOX_BYTES + b_bytes);
-      tma_load_2d(st, m, &full[s], c0, row);
-      if (nb == 2) tma_load_2d(st + BOX_BYTES, m, &full[s], c0 + 64, row);
+      mbar_arrive_expect_tx(&full[s], nk * (nb * BOX_BYTES + b_bytes));
+      for (int h = 0; h < nk; ++h)
+        for (int b = 0; b < nb; ++b)
+          tma_load_2d(st + (2 * h + b) * BOX_BYTES, m, &full[s], c0 + b * 64, row + h * 64);
     };
-    auto load_b = [&](const CUtensorMap* m, int k, int row) {
-      tma_load_2d(smem + s * C::STAGE + A_BYTES, m, &full[s], k, row);
+    auto load_b = [&](const CUtensorMap* m, int k, int nk, int b_row) {
+      for (int h = 0; h < nk; ++h)
+        tma_load_2d(smem + s * C::STAGE + A_BYTES + h * C::B_HALF, m, &full[s], k + h * 64, b_row);
     };
     auto next = [&]() {
       if (++s == C::STAGES) {
@@ -493,9 +497,10 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         const int nb = min(2, (f - c0) / 64);
         for (int j = k0; j < k0 + n; ++j) {
           if (!claim()) break;
+          const int nk = min(2, d / 64 - 2 * j);
           if (elect_one()) {
-            load_a(&tmW1, row + j * BK, c0, nb, C::N1 * 128);
-            load_b(&tmX, j * BK, 0);
+            load_a(&tmW1, row + j * BK, c0, nk, nb, C::N1 * 128);
+            load_b(&tmX, j * BK, nk, 0);
           }
           __syncwarp();
           next();
@@ -517,9 +522,10 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
           for (int j = k0; j < k0 + n; ++j) {
             if (a && !claim()) break;
+            const int nk = min(2, f / 64 - 2 * j);
             if (elect_one()) {
-              if (a) load_a(&tmW2, row + j * BK, db * BM, nb, C::HR * 128);
-              if (b) load_b(&tmH, j * BK, slot * C::HR);
+              if (a) load_a(&tmW2, row + j * BK, db * BM, nk, nb, C::HR * 128);
+              if (b) load_b(&tmH, j * BK, nk, slot * C::HR);
             }
             __syncwarp();
             next();
@@ -535,17 +541,18 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         const int db = u / nslots, slot = u - db * nslots;
         const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
         for (int j = k0; j < k0 + n; ++j) {
-          if (elect_one()) {
-            tma_prefetch_2d(&tmW2, db * BM, row + j * BK);
-            if (nb == 2) tma_prefetch_2d(&tmW2, db * BM + 64, row + j * BK);
-          }
+          const int nk = min(2, f / 64 - 2 * j);
+          if (elect_one())
+            for (int h = 0; h < nk; ++h)
+              for (int b = 0; b < nb; ++b)
+                tma_prefetch_2d(&tmW2, db * BM + b * 64, row + j * BK + h * 64);
           __syncwarp();
         }
         i += n;
       }
       if (lane == 0 && !lost) lost = !wait_count(p.sync + SYNC_H, nslots * FB, kWaitLimitNs);
       __syncwarp();
-      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("fence.proxy.async.global;" ::: "memory");
       if (!dead) {
         s = s0;
         ph = ph0;
@@ -575,10 +582,10 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     bool dead = false;
     const uint64_t ad0 = make_sdesc_sw128(smem_u32(smem), BOX_BYTES, 1024),
                    bd0 = make_sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
-    auto phase = [&](const Range& r, uint32_t idesc) {
+    auto phase = [&](const Range& r, int k64, uint32_t idesc) {
       const int end = r.start(cta + 1);
       for (int i = r.start(cta); i < end && !dead;) {
-        const int n = min(r.len - i % r.len, end - i);
+        const int k0 = i % r.len, n = min(r.len - k0, end - i);
         if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs))) {
           dead = true;
           break;
@@ -593,11 +600,18 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           tc_fence_after();
           const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
           const uint32_t more = j > 0 ? 1u : 0u;
+          const bool both = k64 - 2 * (k0 + j) >= 2;  // both k halves
           if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
+            for (int kk = 0; kk < 4; ++kk)
               tc_mma_f16(dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
                          kk > 0 ? 1u : more);
+            if (both) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc_mma_f16(dt, ad0 + off + (2 * BOX_BYTES + kk * 2048) / 16,
+                           bd0 + off + C::B_HALF / 16 + kk * 2, idesc, 1u);
+            }
             tc_commit(&empty[s]);
           }
           __syncwarp();
@@ -615,8 +629,8 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
         i += n;
       }
     };
-    phase(r1, make_idesc_bf16_f32(BM, C::N1, true, false));
-    if (!dead) phase(r2, make_idesc_bf16_f32(BM, C::N2, true, false));
+    phase(r1, d / 64, make_idesc_bf16_f32(BM, C::N1, true, false));
+    if (!dead) phase(r2, f / 64, make_idesc_bf16_f32(BM, C::N2, true, false));
     // nothing this thread issued may still run when tensor memory is freed
     if (elect_one()) tc_commit(drain);
     __syncwarp();
@@ -717,7 +731,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
               }
           }
           // h is read by other CTAs' TMA copies
-          asm volatile("fence.proxy.async;" ::: "memory");
+          asm volatile("fence.proxy.async.global;" ::: "memory");
           bar_epi();
           if (tid == 128) add_release(p.sync + SYNC_H, 1);
         }
@@ -874,8 +888,8 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
   CUtensorMap mX, mW1, mW2, mH;
   const uint64_t Eu = static_cast<uint64_t>(E);
   if (!make_map_2d(&mX, x, T, d, 64, TP < 16 ? 16 : TP) ||
-      !make_map_2d(&mW1, W1, Eu * d, f, 64, fw::BK) ||
-      !make_map_2d(&mW2, W2, Eu * f, d, 64, fw::BK) ||
+      !make_map_2d(&mW1, W1, Eu * d, f, 64, 64) ||
+      !make_map_2d(&mW2, W2, Eu * f, d, 64, 64) ||
       !make_map_2d(&mH, p.h, L.h_rows, f, 64, 2 * TP))
     return cudaErrorInvalidValue;
   switch (TP) {
