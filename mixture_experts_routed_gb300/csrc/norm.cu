@@ -21,8 +21,8 @@
 // A channel gate keeps one sum, A = sum_t G bh: dw_post = g A, dg = w_post A.
 //
 // Both directions are bound by HBM: every tensor is read or written once.
-// A row is shared by a warp or by a block of up to 512 threads; each copies
-// the two vectors of its own columns into a ring of rows in shared memory (cp.async: a thread
+// A row is shared by a warp or by a block; each thread copies the vectors of
+// its own columns into a ring of rows in shared memory (cp.async: a thread
 // waits for its own copies only, so the ring needs no barrier) and reads
 // them as often as the sums in between require, while the next rows are on
 // their way. Loads into registers instead left too little in flight beside
@@ -194,12 +194,10 @@ __device__ __forceinline__ float2 row_sums(float2 v, float2* buf, int& turn) {
     __syncthreads();
     v = lane < (blockDim.x >> 5) ? b[lane] : float2{0.f, 0.f};
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {  // (at most 16 warps)
+    for (int o = 16; o > 0; o >>= 1) {
       v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
       v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
     }
-    v.x = __shfl_sync(0xffffffffu, v.x, 0);
-    v.y = __shfl_sync(0xffffffffu, v.y, 0);
   }
   return v;
 }
@@ -246,15 +244,19 @@ __device__ __forceinline__ void pack2(const float (&w)[N], f2 (&v)[N / 2]) {
 }
 
 // Threads of a block that takes rows by the warp; other blocks are one row's
-// threads, two vectors each.
+// threads, at most two vectors each forward, one backward (whose column sums
+// and weights are as many registers again: with two, half the warps were left
+// to hide its latencies, 166 us for 158; forward two small blocks do better
+// than one wide one, 111 us for 125 at 16384 x 5120).
 constexpr int kWarpBlock = 128;
-constexpr int kRowThreads = 512;  // at most
+constexpr int kFwdVecs = 2, kBwdVecs = 1;
+constexpr int kRowVecs = 1024;  // vectors of the longest row a ring takes
 
 // This thread's copies of one tensor's row.
-template <typename T>
+template <typename T, int V>
 __device__ __forceinline__ void ring_fill(uint4* dst, const T* row, int nvec, int tid, int tpr) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < V; ++j) {
     const int i = tid + j * tpr;
     if (i < nvec)
       ptx::cp_async16(ptx::smem_u32(dst + i), row + static_cast<size_t>(i) * Vec<T>::N);
@@ -263,7 +265,7 @@ __device__ __forceinline__ void ring_fill(uint4* dst, const T* row, int nvec, in
 
 // Forward: S rows in flight.
 template <typename T, bool WARP, int S, bool POST, bool PRE>
-__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
+__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kFwdVecs, WARP ? 4 : 1)
     norm_ring_kernel(const NormArgs a, const T* __restrict__ x, const T* __restrict__ b,
                      const float* __restrict__ w_post, const void* __restrict__ gate,
                      const float* __restrict__ w_pre, T* __restrict__ out, T* __restrict__ n,
@@ -286,17 +288,17 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     if (t < a.T) {
       uint4* dst = mine + slot * size;
       const size_t at = static_cast<size_t>(t) * d;
-      ring_fill<T>(dst, x + at, nvec, tid, tpr);
-      if (POST) ring_fill<T>(dst + nvec, b + at, nvec, tid, tpr);
-      if (elem) ring_fill<T>(dst + 2 * nvec, static_cast<const T*>(gate) + at, nvec, tid, tpr);
+      ring_fill<T, kFwdVecs>(dst, x + at, nvec, tid, tpr);
+      if (POST) ring_fill<T, kFwdVecs>(dst + nvec, b + at, nvec, tid, tpr);
+      if (elem) ring_fill<T, kFwdVecs>(dst + 2 * nvec, static_cast<const T*>(gate) + at, nvec, tid, tpr);
     }
     ptx::cp_async_commit();
   };
-  f2 wb[2][H], wn[2][H];
+  f2 wb[kFwdVecs][H], wn[kFwdVecs][H];
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fill(t0 + s * step, s);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kFwdVecs; ++j) {
     const int c = (tid + j * tpr) * N;
     if (c < d) {
       float w[N];
@@ -318,7 +320,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     f2 ss = 0;
     if constexpr (POST) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kFwdVecs; ++j) {
         const int i = tid + j * tpr;
         if (i < nvec) {
           f2 v[H];
@@ -351,9 +353,9 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     const size_t at = static_cast<size_t>(t) * d;
     const f2 scale = dup2(a.beta * gt * rb);
     f2 ss = 0;
-    f2 y[2][H];
+    f2 y[kFwdVecs][H];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kFwdVecs; ++j) {
       const int i = tid + j * tpr;
       if (i < nvec) {
         widen2<T>(in[i], y[j]);
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
       if (rstd_pre != nullptr && tid == 0) rstd_pre[t] = ro;
       const f2 r2 = dup2(ro);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kFwdVecs; ++j) {
         const int i = tid + j * tpr;
         if (i < nvec) {
 #pragma unroll
@@ -406,7 +408,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
 // order. Factors that a row shares (rstd, beta, a token gate) are taken out
 // of the per-element terms.
 template <typename T, bool WARP, int S, bool POST, bool PRE>
-__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
+__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP ? 4 : 1)
     norm_ring_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
                          const float* __restrict__ dn, const T* __restrict__ yo,
                          const T* __restrict__ b, const float* __restrict__ w_post,
@@ -436,11 +438,11 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     if (t < a.T) {
       uint4* dst = mine + slot * size;
       const size_t at = static_cast<size_t>(t) * d;
-      ring_fill<T>(dst, dout + at, nvec, tid, tpr);
+      ring_fill<T, kBwdVecs>(dst, dout + at, nvec, tid, tpr);
       if constexpr (PRE) {
-        ring_fill<T>(dst + off_y, yo + at, nvec, tid, tpr);
+        ring_fill<T, kBwdVecs>(dst + off_y, yo + at, nvec, tid, tpr);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < kBwdVecs; ++j) {
           const int i = tid + j * tpr;
           if (i < nvec)
 #pragma unroll
@@ -449,8 +451,8 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
         }
       }
       if constexpr (POST) {
-        ring_fill<T>(dst + off_b, b + at, nvec, tid, tpr);
-        if (elem) ring_fill<T>(dst + off_g, static_cast<const T*>(gate) + at, nvec, tid, tpr);
+        ring_fill<T, kBwdVecs>(dst + off_b, b + at, nvec, tid, tpr);
+        if (elem) ring_fill<T, kBwdVecs>(dst + off_g, static_cast<const T*>(gate) + at, nvec, tid, tpr);
       }
     }
     ptx::cp_async_commit();
@@ -463,11 +465,11 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
       v[2 * q + 1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
     }
   };
-  f2 wb[2][H], wn[2][H], apre[2][H] = {}, apost[2][H] = {};
+  f2 wb[kBwdVecs][H], wn[kBwdVecs][H], apre[kBwdVecs][H] = {}, apost[kBwdVecs][H] = {};
 #pragma unroll
   for (int s = 0; s < S - 1; ++s) fill(group + s * step, s);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kBwdVecs; ++j) {
     const int c = (tid + j * tpr) * N;
     if (c < d) {
       float w[N];
@@ -496,7 +498,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     if constexpr (PRE) {
       const f2 r2 = dup2(ro);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kBwdVecs; ++j) {
         const int i = tid + j * tpr;
         if (i < nvec) {
           f2 y[H], v[H];
@@ -531,9 +533,9 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
     fetch(t + step);
     // D = dout + ro v - ro yh mean(v yh), dx = alpha D and, of the branch, D w
     const f2 r2 = dup2(ro), c2 = dup2(-ro * ro * s1), k2 = dup2(gt * a.beta * rb);
-    f2 v2[2][H], ss = 0;
+    f2 v2[kBwdVecs][H], ss = 0;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kBwdVecs; ++j) {
       const int i = tid + j * tpr;
       if (i < nvec) {
         f2 D[H], o[H];
@@ -583,7 +585,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
       const float k = gt * a.beta * rb;
       const f2 kv = dup2(k), kb = dup2(-k * rb * rb * sum * inv_d);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
+      for (int j = 0; j < kBwdVecs; ++j) {
         const int i = tid + j * tpr;
         if (i < nvec) {
           f2 bb[H];
@@ -597,7 +599,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowThreads, WARP ? 4 : 1)
   }
   ptx::cp_async_wait<0>();
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
+  for (int j = 0; j < kBwdVecs; ++j) {
     const int i = tid + j * tpr;
     if (i >= nvec) continue;
     float* o = part + static_cast<size_t>(group) * 2 * d + i * N;
@@ -820,11 +822,11 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Threads to a row of nvec vectors (0: too wide for the ring): a warp for
-// short rows, one vector a thread up to 512 of them, else two.
-int threads_of(int nvec) {
-  if (nvec > 2 * kRowThreads) return 0;
-  return ceil_div(nvec <= kRowThreads ? nvec : ceil_div(nvec, 2), 32) * 32;
+// Threads to a row of nvec vectors, at most `vecs` each (0: too wide for the
+// ring): a warp for short rows, one vector a thread while those are enough.
+int threads_of(int nvec, int vecs) {
+  if (nvec > kRowVecs) return 0;
+  return ceil_div(nvec <= kRowVecs / vecs ? nvec : ceil_div(nvec, vecs), 32) * 32;
 }
 
 // Bytes of a row's tensors in the ring.
@@ -839,7 +841,7 @@ size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
 constexpr size_t kRingMost = 220 * 1024;  // shared memory an SM has for its blocks
 constexpr int kStages = 3;
 
-// Blocks an SM is to hold: what their registers (96 a thread forward, 128
+// Blocks an SM is to hold: what their registers (96 a thread forward, 64
 // backward) and rings leave room for.
 int blocks_per_sm(int tpr, int regs, size_t ring) {
   const int threads = tpr == 32 ? kWarpBlock : tpr, by_regs = 65536 / (regs * threads);
@@ -851,11 +853,11 @@ int blocks_per_sm(int tpr, int regs, size_t ring) {
 // Backward row groups (each writes its column sums): one wave of blocks of
 // the form with both halves, each group with a row of its own where T allows.
 int bwd_groups(int dtype, int d, bool elem, int T) {
-  const int tpr = threads_of(d / (dtype == 0 ? 4 : 8));
+  const int tpr = threads_of(d / (dtype == 0 ? 4 : 8), kBwdVecs);
   if (tpr == 0) return T < 152 ? T : 152;
   const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
   const size_t ring = bwd_slot(dtype, d, true, true, elem) * kStages * rpb;
-  const int most = 152 * blocks_per_sm(tpr, 128, ring) * rpb;
+  const int most = 152 * blocks_per_sm(tpr, 64, ring) * rpb;
   return ceil_div(T < most ? T : most, rpb) * rpb;
 }
 
@@ -874,7 +876,7 @@ template <typename T, bool POST, bool PRE>
 struct Fwd {
   template <typename... Args>
   static cudaError_t go(const NormArgs& a, int num_sms, cudaStream_t s, Args... args) {
-    const int tpr = threads_of(a.d / Vec<T>::N);
+    const int tpr = threads_of(a.d / Vec<T>::N, kFwdVecs);
     if (tpr == 0)
       return launch_pdl(norm_wide_kernel<T, POST, PRE>, dim3(a.T < num_sms * 4 ? a.T : num_sms * 4),
                         dim3(kWideThreads), 0, s, a, args...);
@@ -894,7 +896,7 @@ template <typename T, bool POST, bool PRE>
 struct Bwd {
   template <typename... Args>
   static cudaError_t go(const NormArgs& a, int groups, cudaStream_t s, Args... args) {
-    const int tpr = threads_of(a.d / Vec<T>::N);
+    const int tpr = threads_of(a.d / Vec<T>::N, kBwdVecs);
     if (tpr == 0)
       return launch_pdl(norm_wide_bwd_kernel<T, POST, PRE>, dim3(groups), dim3(kWideThreads), 0, s,
                         a, args...);
