@@ -436,8 +436,10 @@ MOE_API int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const vo
 
 /* Gradients of moe_block_norm's inputs, given dout [T, d] (the gradient that
  * reaches out by other ways than n: the next residual's) and dn [T, d] fp32
- * (moe_backward's dx; NULL without the pre half). y [T, d]: the forward's
- * out (x without the post half); b, weights, gate and rstd_* as there.
+ * (moe_backward's dx; NULL without the pre half). x, b, weights and gate: the
+ * forward's, unchanged; rstd_*: what it wrote. out is formed again from x and
+ * b, in fp32 (its rounding does not reach the gradients); x is not read
+ * without the pre half and may be NULL there.
  * Outputs, overwritten: dx [T, d] (of x, through the residual), db [T, d],
  * dw_post, dw_pre [d] fp32, dgate (gate's shape; fp32, or dtype for an
  * element gate); those of a half left out, and dgate without a gate, are
@@ -446,7 +448,7 @@ MOE_API int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const vo
  * atomics: bitwise reproducible. T = 0 zeroes the weights' gradients. */
 MOE_API size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg);
 MOE_API int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout,
-                   const float* dn, const void* y, const void* b, const float* w_post,
+                   const float* dn, const void* x, const void* b, const float* w_post,
                    const void* gate, const float* w_pre, const float* rstd_post,
                    const float* rstd_pre, void* dx, void* db, float* dw_post, void* dgate,
                    float* dw_pre, void* ws, size_t ws_bytes, void* stream);

@@ -12,7 +12,8 @@ from .api import (  # noqa: F401
     get_device_error,
     clear_device_error, kernel_count, check_config, backward, backward_workspace_size,
     forward_few, few_workspace_size,
-    norm_config, block_norm, block_norm_backward, block_norm_workspace_size, alloc_norm_workspace,
+    norm_config, KeptNorm, block_norm, block_norm_backward, block_norm_workspace_size,
+    alloc_norm_workspace,
     mx4_config, mx4_quantize_weights, mx4_quantize_rows, mx4_product, mx4_dequantize_weights,
     mx4_dequantize_rows, alloc_mx4_workspace,
 )

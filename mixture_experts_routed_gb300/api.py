@@ -9,6 +9,7 @@ the library is missing, importing the first call raises.
 from __future__ import annotations
 
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -18,7 +19,7 @@ __all__ = ["MoEError", "make_config", "config_from", "workspace_size", "scratch_
            "alloc_workspace", "route", "dispatch", "expert_ffn", "combine", "forward",
            "forward_views", "get_device_error", "clear_device_error", "kernel_count",
            "check_config", "backward", "backward_workspace_size", "forward_few",
-           "few_workspace_size", "norm_config", "block_norm",
+           "few_workspace_size", "norm_config", "KeptNorm", "block_norm",
            "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace",
            "mx4_config", "mx4_quantize_weights", "mx4_quantize_rows", "mx4_product",
            "mx4_dequantize_weights", "mx4_dequantize_rows", "alloc_mx4_workspace"]
@@ -373,11 +374,19 @@ def _gate_form(kind, T, d, dt):
     return ((T, d), dt) if kind == L.MOE_GATE_ELEMENT else None
 
 
+class KeptNorm(NamedTuple):
+    """What a forward with both halves keeps for the gradient through its second norm: that
+    norm's 1 / root mean square [T] and x, from which (with b) out is formed again in fp32."""
+    rstd: torch.Tensor
+    x: torch.Tensor
+
+
 def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=None,
                rstd_post=None, rstd_pre=None, want_rstd=False, stream=None) -> dict:
     """out = alpha x + beta gate * norm(b) w_post and n = norm(out) w_pre; without ``b``
-    out is x, without ``w_pre`` there is no n. ``want_rstd``: keep the statistics the
-    backward reads."""
+    out is x, without ``w_pre`` there is no n. ``want_rstd``: keep what the backward reads,
+    under "rstd_post" (fp32 [T]) and "rstd_pre" (fp32 [T]; with both halves a ``KeptNorm`` of
+    it and x, which must not change before the backward)."""
     T, d, f32 = c.T, c.d, torch.float32
     dt, td = _ndt(c), (T, d)
     post, pre = b is not None, w_pre is not None
@@ -396,6 +405,8 @@ def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=
         rstd_post = torch.empty(T, dtype=f32, device=x.device)
     if want_rstd and pre and rstd_pre is None:
         rstd_pre = torch.empty(T, dtype=f32, device=x.device)
+    if isinstance(rstd_pre, KeptNorm):  # (one to be filled again)
+        rstd_pre = rstd_pre.rstd
     form = _gate_form(c.gate, T, d, dt) if post else None
     st = L.load().moe_block_norm(
         ctypes.byref(c), px, _shaped("b", b, td, dt), _shaped("w_post", w_post, (d,), f32),
@@ -403,19 +414,28 @@ def block_norm(c, x, b=None, w_post=None, gate=None, w_pre=None, *, out=None, n=
         po, pn, _shaped("rstd_post", rstd_post, (T,), f32), _shaped("rstd_pre", rstd_pre, (T,), f32),
         _s(stream))
     _check(st, "moe_block_norm")
+    if post and rstd_pre is not None:
+        rstd_pre = KeptNorm(rstd_pre, x)
     return {"out": out, "n": n, "rstd_post": rstd_post, "rstd_pre": rstd_pre}
 
 
 def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_pre, *, ws,
                         stream=None) -> dict:
-    """Gradients after a ``block_norm`` of the same inputs: ``y`` is its out (x without
-    ``b``), ``dout`` the gradient that reaches y by the residual, ``dn`` (fp32) the one of
-    n. dx, db, an element gate's dgate in the config's type; dw_post, dw_pre and the other
-    dgate fp32; None for what the forward left out."""
+    """Gradients after a ``block_norm`` of the same inputs: ``dout`` is the gradient that
+    reaches its out by the residual, ``dn`` (fp32) the one of n, ``rstd_post`` and
+    ``rstd_pre`` what it kept. ``y``: without ``b``, the x that was normed; with it, the
+    forward's out, which is not read (``rstd_pre`` has what stands in for it). dx, db, an
+    element gate's dgate in the config's type; dw_post, dw_pre and the other dgate fp32; None
+    for what the forward left out."""
     T, d, f32 = c.T, c.d, torch.float32
     dt, td = _ndt(c), (T, d)
     post, pre = w_post is not None, w_pre is not None
     form = _gate_form(c.gate, T, d, dt) if post else None
+    if post and pre:
+        if not isinstance(rstd_pre, KeptNorm):
+            raise MoEError(L.MOE_ERR_INVALID_ARG,
+                           "rstd_pre of a forward with both halves is the KeptNorm it returned")
+        rstd_pre, y = rstd_pre
     pd = _shaped("dout", dout, td, dt)
     g = {"dx": torch.empty_like(dout), "db": torch.empty_like(dout) if post else None,
          "dw_post": torch.empty_like(w_post) if post else None, "dgate": None,
@@ -423,7 +443,7 @@ def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_
     if form:
         g["dgate"] = torch.empty(form[0], dtype=form[1], device=dout.device)
     st = L.load().moe_block_norm_backward(
-        ctypes.byref(c), pd, _shaped("dn", dn, td, f32), _shaped("y", y, td, dt),
+        ctypes.byref(c), pd, _shaped("dn", dn, td, f32), _shaped("y", y, td, dt) if pre else None,
         _shaped("b", b, td, dt), _shaped("w_post", w_post, (d,), f32),
         _shaped("gate", gate, *form) if form else None, _shaped("w_pre", w_pre, (d,), f32),
         _shaped("rstd_post", rstd_post, (T,), f32) if post else None,

@@ -283,7 +283,7 @@ cudaError_t launch_block_norm(int dtype, int gate_kind, float eps, float alpha, 
 // Bytes of `part` the backward's column sums take.
 size_t block_norm_bwd_ws(int dtype, int gate_kind, int T, int d);
 cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
-                                  int T, int d, const void* dout, const float* dn, const void* yo,
+                                  int T, int d, const void* dout, const float* dn, const void* x,
                                   const void* b, const float* w_post, const void* gate,
                                   const float* w_pre, const float* rstd_post,
                                   const float* rstd_pre, void* dx, void* db, float* dw_post,

@@ -922,7 +922,7 @@ size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg) {
 }
 
 int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, const float* dn,
-                            const void* y, const void* b, const float* w_post, const void* gate,
+                            const void* x, const void* b, const float* w_post, const void* gate,
                             const float* w_pre, const float* rstd_post, const float* rstd_pre,
                             void* dx, void* db, float* dw_post, void* dgate, float* dw_pre,
                             void* ws, size_t ws_bytes, void* stream) {
@@ -941,7 +941,7 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
   if ((post && !ok_ptr(w_post)) || (post && c.gate == MOE_GATE_CHANNEL && !ok_ptr(gate)))
     return MOE_ERR_INVALID_ARG;
   if (c.T > 0) {
-    if (!norm_args_ok(c, y, b, w_post, gate, w_pre) || !ok_ptr(dout) || !ok_ptr(dx))
+    if (!norm_args_ok(c, pre ? x : b, b, w_post, gate, w_pre) || !ok_ptr(dout) || !ok_ptr(dx))
       return MOE_ERR_INVALID_ARG;
     if ((pre ? !ok_ptr(dn) || rstd_pre == nullptr : dn != nullptr) ||
         (post ? !ok_ptr(db) || rstd_post == nullptr : db != nullptr))
@@ -951,7 +951,7 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
   // (with no rows b may be null: what is left out goes by the weights)
   const void* bp = post && b == nullptr ? static_cast<const void*>(w_post) : b;
   return status_of(launch_block_norm_bwd(c.dtype, c.gate, c.eps, c.alpha, c.beta, c.T, c.d, dout,
-                                         dn, y, bp, w_post, gate, w_pre, rstd_post, rstd_pre, dx,
+                                         dn, x, bp, w_post, gate, w_pre, rstd_post, rstd_pre, dx,
                                          db, dw_post, dgate, dw_pre, static_cast<float*>(ws),
                                          as_stream(stream)));
 }

@@ -20,6 +20,10 @@
 //
 // A channel gate keeps one sum, A = sum_t G bh: dw_post = g A, dg = w_post A.
 //
+// yh wants out as the forward had it, not as bf16 rounded it (each term of
+// dw_pre would be off by up to 2^-9): the backward reads x in its place and
+// forms out again, in fp32, from x and the b that it reads anyway.
+//
 // Both directions are bound by HBM: every tensor is read or written once.
 // A row is shared by a warp or by a block; each thread copies the vectors of
 // its own columns into a ring of rows in shared memory (cp.async: a thread
@@ -406,11 +410,13 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kFwdVecs, WARP 
 // column sums (of dw_pre; of dw_post, or A of a channel gate) in registers,
 // written once to part[group][2][d]; reduce_columns adds the groups in
 // order. Factors that a row shares (rstd, beta, a token gate) are taken out
-// of the per-element terms.
+// of the per-element terms. The first sum of a row is taken a row ahead of
+// the rest, so there are two rings: S rows of what it reads (what out is
+// formed from, and dn; the rest reads them again) and two rows of the others.
 template <typename T, bool WARP, int S, bool POST, bool PRE>
 __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP ? 4 : 1)
     norm_ring_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
-                         const float* __restrict__ dn, const T* __restrict__ yo,
+                         const float* __restrict__ dn, const T* __restrict__ x,
                          const T* __restrict__ b, const float* __restrict__ w_post,
                          const void* __restrict__ gate, const float* __restrict__ w_pre,
                          const float* __restrict__ rstd_post, const float* __restrict__ rstd_pre,
@@ -418,6 +424,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
                          float* __restrict__ part) {
   constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
   constexpr int P = N / 4;  // 16-byte pieces of dn to a vector
+  static_assert(S == 2 || S == 3, "rows in the first ring");
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float2 buf[64];
   int turn = 0;
@@ -428,46 +435,52 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
   const int d = a.d, nvec = d / N;
   const float inv_d = 1.f / static_cast<float>(d);
   const bool elem = POST && a.gate == kGateElement, token = POST && a.gate == kGateToken;
-  // a ring slot: dout, then y and dn, then b, then an element gate
-  const int off_y = nvec, off_n = 2 * nvec, off_b = PRE ? (2 + P) * nvec : nvec;
-  const int off_g = off_b + nvec;
-  const int size = off_b + (POST ? nvec : 0) + (elem ? nvec : 0);
-  uint4* mine = ring + static_cast<size_t>(sub) * S * size;
+  // slots: x and dn, then b and an element gate, in the first ring where that
+  // is in use; dout in the second, before them otherwise
+  const int branch = POST ? nvec * (1 + (elem ? 1 : 0)) : 0;
+  const int size_a = PRE ? (1 + P) * nvec + branch : 0;
+  const int size_b = nvec + (PRE ? 0 : branch);
+  uint4* ring_a = ring + static_cast<size_t>(sub) * (S * size_a + 2 * size_b);
+  uint4* ring_b = ring_a + S * size_a;
   const int group = blockIdx.x * RPB + sub, step = gridDim.x * RPB;
-  auto fill = [&](int t, int slot) {
-    if (t < a.T) {
-      uint4* dst = mine + slot * size;
-      const size_t at = static_cast<size_t>(t) * d;
-      ring_fill<T, kBwdVecs>(dst, dout + at, nvec, tid, tpr);
-      if constexpr (PRE) {
-        ring_fill<T, kBwdVecs>(dst + off_y, yo + at, nvec, tid, tpr);
-#pragma unroll
-        for (int j = 0; j < kBwdVecs; ++j) {
-          const int i = tid + j * tpr;
-          if (i < nvec)
-#pragma unroll
-            for (int q = 0; q < P; ++q)
-              ptx::cp_async16(ptx::smem_u32(dst + off_n + q * nvec + i), dn + at + i * N + q * 4);
-        }
-      }
-      if constexpr (POST) {
-        ring_fill<T, kBwdVecs>(dst + off_b, b + at, nvec, tid, tpr);
-        if (elem) ring_fill<T, kBwdVecs>(dst + off_g, static_cast<const T*>(gate) + at, nvec, tid, tpr);
-      }
+  auto fill_branch = [&](uint4* dst, size_t at) {
+    if constexpr (POST) {
+      ring_fill<T, kBwdVecs>(dst, b + at, nvec, tid, tpr);
+      if (elem) ring_fill<T, kBwdVecs>(dst + nvec, static_cast<const T*>(gate) + at, nvec, tid, tpr);
     }
-    ptx::cp_async_commit();
   };
-  auto load_dn = [&](const uint4* in, int i, f2 (&v)[H]) {
+  auto fill_a = [&](int t, int slot) {
+    if constexpr (PRE) {
+      if (t >= a.T) return;
+      uint4* dst = ring_a + slot * size_a;
+      const size_t at = static_cast<size_t>(t) * d;
+      ring_fill<T, kBwdVecs>(dst, x + at, nvec, tid, tpr);
 #pragma unroll
-    for (int q = 0; q < P; ++q) {
-      const uint4 r = in[off_n + q * nvec + i];
-      v[2 * q] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
-      v[2 * q + 1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+      for (int j = 0; j < kBwdVecs; ++j) {
+        const int i = tid + j * tpr;
+        if (i < nvec)
+#pragma unroll
+          for (int q = 0; q < P; ++q)
+            ptx::cp_async16(ptx::smem_u32(dst + (1 + q) * nvec + i), dn + at + i * N + q * 4);
+      }
+      fill_branch(dst + (1 + P) * nvec, at);
     }
+  };
+  auto fill_b = [&](int t, int slot) {
+    if (t >= a.T) return;
+    uint4* dst = ring_b + slot * size_b;
+    const size_t at = static_cast<size_t>(t) * d;
+    ring_fill<T, kBwdVecs>(dst, dout + at, nvec, tid, tpr);
+    if constexpr (!PRE) fill_branch(dst + nvec, at);
   };
   f2 wb[kBwdVecs][H], wn[kBwdVecs][H], apre[kBwdVecs][H] = {}, apost[kBwdVecs][H] = {};
-#pragma unroll
-  for (int s = 0; s < S - 1; ++s) fill(group + s * step, s);
+  fill_a(group, 0);
+  fill_b(group, 0);
+  ptx::cp_async_commit();
+  if (S == 3) {
+    fill_a(group + step, 1);
+    ptx::cp_async_commit();
+  }
 #pragma unroll
   for (int j = 0; j < kBwdVecs; ++j) {
     const int c = (tid + j * tpr) * N;
@@ -492,18 +505,41 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
     if (POST) rb_next = __ldg(rstd_post + t);
     if (token) gt_next = __ldg(static_cast<const float*>(gate) + t);
   };
+  // out (y) and dn (v) at vector i of a first-ring slot; k = beta gate rstd_post
+  auto load_y = [&](const uint4* in, int i, int j, f2 k, f2 (&y)[H], f2 (&v)[H]) {
+    widen2<T>(in[i], y);
+    if constexpr (POST) {
+      f2 u[H];
+      widen2<T>(in[(1 + P) * nvec + i], u);
+#pragma unroll
+      for (int q = 0; q < H; ++q) u[q] = mul2(u[q], wb[j][q]);
+      if (elem) {
+        f2 g[H];
+        widen2<T>(in[(2 + P) * nvec + i], g);
+#pragma unroll
+        for (int q = 0; q < H; ++q) u[q] = mul2(u[q], g[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < H; ++q) y[q] = fma2(k, u[q], mul2(al, y[q]));
+    }
+#pragma unroll
+    for (int q = 0; q < P; ++q) {
+      const uint4 r = in[(1 + q) * nvec + i];
+      v[2 * q] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+      v[2 * q + 1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+    }
+  };
   // a row's part of ro mean(v y), and its terms of dw_pre
-  auto first = [&](const uint4* in, float ro) {
+  auto first = [&](const uint4* in, float ro, float k) {
     f2 ss = 0;
     if constexpr (PRE) {
-      const f2 r2 = dup2(ro);
+      const f2 r2 = dup2(ro), kk = dup2(k);
 #pragma unroll
       for (int j = 0; j < kBwdVecs; ++j) {
         const int i = tid + j * tpr;
         if (i < nvec) {
           f2 y[H], v[H];
-          widen2<T>(in[off_y + i], y);
-          load_dn(in, i, v);
+          load_y(in, i, j, kk, y, v);
 #pragma unroll
           for (int q = 0; q < H; ++q) {
             const f2 p = mul2(mul2(v[q], r2), y[q]);
@@ -519,15 +555,20 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
   fetch(group);
   float s1 = 0.f;
   ptx::cp_async_wait<S - 2>();  // the first row
-  if (PRE && group < a.T) {
-    s1 = row_sums<WARP>(float2{first(mine, ro_next), 0.f}, buf, turn).x * inv_d;
-  }
-  int slot = 0;
-  for (int t = group; t < a.T; t += step) {
-    fill(t + (S - 1) * step, slot == 0 ? S - 1 : slot - 1);
-    const uint4* in = mine + slot * size;
-    slot = slot + 1 == S ? 0 : slot + 1;
-    const uint4* in_next = mine + slot * size;
+  if (PRE && group < a.T)
+    s1 = row_sums<WARP>(float2{first(ring_a, ro_next, gt_next * a.beta * rb_next), 0.f}, buf, turn)
+             .x *
+         inv_d;
+  int sa = 0, sb = 0;
+  for (int t = group; t < a.T; t += step, sa = sa + 1 == S ? 0 : sa + 1, sb ^= 1) {
+    const int sa_next = sa + 1 == S ? 0 : sa + 1;
+    // (into the slots that the row before this one was read from)
+    fill_a(t + (S - 1) * step, sa == 0 ? S - 1 : sa - 1);
+    fill_b(t + step, sb ^ 1);
+    ptx::cp_async_commit();
+    if (S == 3) ptx::cp_async_wait<1>();  // this row's second part, the next row's first
+    const uint4 *in_a = ring_a + sa * size_a, *in_b = ring_b + sb * size_b;
+    const uint4* in_br = PRE ? in_a + (1 + P) * nvec : in_b + nvec;  // b, element gate
     const size_t at = static_cast<size_t>(t) * d;
     const float ro = ro_next, rb = rb_next, gt = gt_next;
     fetch(t + step);
@@ -539,11 +580,10 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
       const int i = tid + j * tpr;
       if (i < nvec) {
         f2 D[H], o[H];
-        widen2<T>(in[i], D);
+        widen2<T>(in_b[i], D);
         if constexpr (PRE) {
           f2 y[H], v[H];
-          widen2<T>(in[off_y + i], y);
-          load_dn(in, i, v);
+          load_y(in_a, i, j, k2, y, v);
 #pragma unroll
           for (int q = 0; q < H; ++q)
             D[q] = fma2(mul2(v[q], wn[j][q]), r2, fma2(y[q], c2, D[q]));
@@ -553,10 +593,10 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
         store2<T>(dx + at + i * N, o);
         if constexpr (POST) {
           f2 bb[H];
-          widen2<T>(in[off_b + i], bb);
+          widen2<T>(in_br[i], bb);
           if (elem) {
             f2 g[H];
-            widen2<T>(in[off_g + i], g);
+            widen2<T>(in_br[nvec + i], g);
 #pragma unroll
             for (int q = 0; q < H; ++q) {
               o[q] = mul2(mul2(D[q], k2), mul2(bb[q], wb[j][q]));
@@ -573,9 +613,10 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
         }
       }
     }
-    ptx::cp_async_wait<S - 2>();  // the next row
+    if (S == 2) ptx::cp_async_wait<0>();  // the next row
     const float2 h = un2(ss);
-    const float next = t + step < a.T ? first(in_next, ro_next) : 0.f;
+    const float next = t + step < a.T ? first(ring_a + sa_next * size_a, ro_next, gt_next * a.beta * rb_next)
+                                        : 0.f;
     const float2 sums = row_sums<WARP>(float2{next, h.x + h.y}, buf, turn);
     s1 = sums.x * inv_d;
     if constexpr (POST) {
@@ -589,7 +630,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
         const int i = tid + j * tpr;
         if (i < nvec) {
           f2 bb[H];
-          widen2<T>(in[off_b + i], bb);
+          widen2<T>(in_br[i], bb);
 #pragma unroll
           for (int q = 0; q < H; ++q) v2[j][q] = fma2(kv, v2[j][q], mul2(kb, bb[q]));
           store2<T>(db + at + i * N, v2[j]);
@@ -680,7 +721,7 @@ __global__ void __launch_bounds__(kWideThreads)
 template <typename T, bool POST, bool PRE>
 __global__ void __launch_bounds__(kWideThreads)
     norm_wide_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
-                         const float* __restrict__ dn, const T* __restrict__ yo,
+                         const float* __restrict__ dn, const T* __restrict__ x,
                          const T* __restrict__ b, const float* __restrict__ w_post,
                          const void* __restrict__ gate, const float* __restrict__ w_pre,
                          const float* __restrict__ rstd_post, const float* __restrict__ rstd_pre,
@@ -704,7 +745,16 @@ __global__ void __launch_bounds__(kWideThreads)
     const bool token = POST && a.gate == kGateToken;
     const float gt = token ? __ldg(static_cast<const float*>(gate) + t) : 1.f;
     auto pre_at = [&](int i, float (&yh)[N], float (&v)[N], float (&w)[N]) {
-      widen<T>(ld_stream(yo + at + i * N), yh);
+      widen<T>(ld_stream(x + at + i * N), yh);
+      if constexpr (POST) {
+        float u[N], wp[N], g[N];
+        widen<T>(ld_stream(b + at + i * N), u);
+        ld_f32<N>(w_post + i * N, wp);
+        gate_at<T, N>(gate, a.gate, gt, t, d, i * N, g);
+#pragma unroll
+        for (int q = 0; q < N; ++q)
+          yh[q] = fmaf(a.alpha, yh[q], a.beta * g[q] * (u[q] * rb * wp[q]));
+      }
       ld_f32_stream<N>(dn + at + i * N, v);
       ld_f32<N>(w_pre + i * N, w);
 #pragma unroll
@@ -833,12 +883,12 @@ int threads_of(int nvec, int vecs) {
 size_t fwd_slot(int dtype, int d, bool post, bool elem) {
   return static_cast<size_t>(d) * (dtype == 0 ? 4 : 2) * (1 + (post ? 1 : 0) + (elem ? 1 : 0));
 }
-size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
-  return static_cast<size_t>(d) *
-         ((dtype == 0 ? 4 : 2) * (1 + (pre ? 1 : 0) + (post ? 1 : 0) + (post && elem ? 1 : 0)) +
-          (pre ? 4 : 0));
+size_t bwd_ring(int dtype, int d, bool post, bool pre, bool elem, int rows) {
+  const int es = dtype == 0 ? 4 : 2, branch = post ? es * (1 + (elem ? 1 : 0)) : 0;
+  const int first = pre ? es + 4 + branch : 0, second = es + (pre ? 0 : branch);
+  return static_cast<size_t>(d) * (first * rows + second * 2);
 }
-constexpr size_t kRingMost = 220 * 1024;  // shared memory an SM has for its blocks
+constexpr size_t kRingMost = 225 * 1024;  // shared memory an SM has for its blocks' rings
 constexpr int kStages = 3;
 
 // Blocks an SM is to hold: what their registers (96 a thread forward, 64
@@ -856,7 +906,7 @@ int bwd_groups(int dtype, int d, bool elem, int T) {
   const int tpr = threads_of(d / (dtype == 0 ? 4 : 8), kBwdVecs);
   if (tpr == 0) return T < 152 ? T : 152;
   const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
-  const size_t ring = bwd_slot(dtype, d, true, true, elem) * kStages * rpb;
+  const size_t ring = bwd_ring(dtype, d, true, true, elem, kStages) * rpb;
   const int most = 152 * blocks_per_sm(tpr, 64, ring) * rpb;
   return ceil_div(T < most ? T : most, rpb) * rpb;
 }
@@ -901,16 +951,18 @@ struct Bwd {
       return launch_pdl(norm_wide_bwd_kernel<T, POST, PRE>, dim3(groups), dim3(kWideThreads), 0, s,
                         a, args...);
     const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
-    const size_t slot =
-        bwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement) * rpb;
+    auto ring = [&](int rows) {
+      return bwd_ring(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement, rows) *
+             rpb;
+    };
     if (tpr == 32)
       return launch_ring(norm_ring_bwd_kernel<T, true, kStages, POST, PRE>, groups / rpb, kWarpBlock,
-                         slot * kStages, s, a, args...);
+                         ring(kStages), s, a, args...);
     // the longest rows leave room for two
-    return slot * kStages <= kRingMost
+    return ring(kStages) <= kRingMost
                ? launch_ring(norm_ring_bwd_kernel<T, false, kStages, POST, PRE>, groups, tpr,
-                             slot * kStages, s, a, args...)
-               : launch_ring(norm_ring_bwd_kernel<T, false, 2, POST, PRE>, groups, tpr, slot * 2, s,
+                             ring(kStages), s, a, args...)
+               : launch_ring(norm_ring_bwd_kernel<T, false, 2, POST, PRE>, groups, tpr, ring(2), s,
                              a, args...);
   }
 };
@@ -934,12 +986,12 @@ cudaError_t forward_of(const NormArgs& a, int num_sms, cudaStream_t s, const voi
 }
 template <typename T>
 cudaError_t backward_of(const NormArgs& a, int groups, cudaStream_t s, const void* dout,
-                        const float* dn, const void* yo, const void* b, const float* w_post,
+                        const float* dn, const void* x, const void* b, const float* w_post,
                         const void* gate, const float* w_pre, const float* rstd_post,
                         const float* rstd_pre, void* dx, void* db, void* dgate, float* part) {
   return by_halves<T, Bwd>(b != nullptr, w_pre != nullptr, [&](auto k) {
     return decltype(k)::go(a, groups, s, static_cast<const T*>(dout), dn,
-                           static_cast<const T*>(yo), static_cast<const T*>(b), w_post, gate,
+                           static_cast<const T*>(x), static_cast<const T*>(b), w_post, gate,
                            w_pre, rstd_post, rstd_pre, static_cast<T*>(dx), static_cast<T*>(db),
                            dgate, part);
   });
@@ -964,7 +1016,7 @@ size_t block_norm_bwd_ws(int dtype, int gate_kind, int T, int d) {
 }
 
 cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alpha, float beta,
-                                  int T, int d, const void* dout, const float* dn, const void* yo,
+                                  int T, int d, const void* dout, const float* dn, const void* x,
                                   const void* b, const float* w_post, const void* gate,
                                   const float* w_pre, const float* rstd_post,
                                   const float* rstd_pre, void* dx, void* db, float* dw_post,
@@ -973,9 +1025,9 @@ cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alp
   const int groups = T > 0 ? bwd_groups(dtype, d, gate_kind == kGateElement, T) : 0;
   if (T > 0) {
     const cudaError_t e =
-        dtype == 0 ? backward_of<float>(a, groups, s, dout, dn, yo, b, w_post, gate, w_pre,
+        dtype == 0 ? backward_of<float>(a, groups, s, dout, dn, x, b, w_post, gate, w_pre,
                                         rstd_post, rstd_pre, dx, db, dgate, part)
-                   : backward_of<__nv_bfloat16>(a, groups, s, dout, dn, yo, b, w_post, gate, w_pre,
+                   : backward_of<__nv_bfloat16>(a, groups, s, dout, dn, x, b, w_post, gate, w_pre,
                                                 rstd_post, rstd_pre, dx, db, dgate, part);
     if (e != cudaSuccess) return e;
   }

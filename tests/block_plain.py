@@ -31,15 +31,17 @@ def norm_forward(x, b, w_post, gate, w_pre, kind, eps, alpha, beta):
     return r
 
 
-def norm_backward(dout, dn, y, b, w_post, gate, w_pre, rb, ro, kind, alpha, beta):
-    """Of (dx, db, dw_post, dgate, dw_pre): (value, absolute terms); rb, ro [T] as kept."""
+def norm_backward(dout, dn, y, b, w_post, gate, w_pre, rb, ro, kind, alpha, beta, ay=None):
+    """Of (dx, db, dw_post, dgate, dw_pre): (value, absolute terms); rb, ro [T] as kept; ay: the
+    absolute terms y is the sum of (its errors go by them)."""
     r = {}
     D, aD = dout, dout.abs()
     if w_pre is not None:
         yh, v = y * ro[:, None], dn * w_pre
-        r["dw_pre"] = ((dn * yh).sum(0), (dn * yh).abs().sum(0))
+        ah = (y.abs() if ay is None else ay) * ro[:, None]
+        r["dw_pre"] = ((dn * yh).sum(0), (dn.abs() * ah).sum(0))
         D = D + ro[:, None] * (v - yh * (v * yh).mean(1, keepdim=True))
-        aD = aD + ro[:, None] * (v.abs() + yh.abs() * (v * yh).abs().mean(1, keepdim=True))
+        aD = aD + ro[:, None] * (v.abs() + ah * (v.abs() * ah).mean(1, keepdim=True))
     if b is None:
         r["dx"] = (D, aD)
         return r

@@ -27,9 +27,9 @@ def norm_forward(lib, c, x=P, b=P, w_post=P, gate=None, w_pre=P, out=P, n=P):
     return lib.moe_block_norm(ctypes.byref(c), x, b, w_post, gate, w_pre, out, n, None, None, None)
 
 
-def norm_backward(lib, c, dout=P, dn=P, y=P, b=P, w_post=P, gate=None, w_pre=P, rb=P, ro=P, dx=P,
+def norm_backward(lib, c, dout=P, dn=P, x=P, b=P, w_post=P, gate=None, w_pre=P, rb=P, ro=P, dx=P,
                   db=P, dw_post=P, dgate=None, dw_pre=P, ws=P, ws_bytes=1 << 40):
-    return lib.moe_block_norm_backward(ctypes.byref(c), dout, dn, y, b, w_post, gate, w_pre, rb, ro,
+    return lib.moe_block_norm_backward(ctypes.byref(c), dout, dn, x, b, w_post, gate, w_pre, rb, ro,
                                        dx, db, dw_post, dgate, dw_pre, ws, ws_bytes, None)
 
 
@@ -69,7 +69,7 @@ def test_norm_forward_arguments(lib, gate, kw):
 
 @pytest.mark.parametrize("gate,kw", [
     (0, dict(dout=None)), (0, dict(dout=ODD)), (0, dict(dn=None)), (0, dict(dn=ODD)),
-    (0, dict(y=None)), (0, dict(y=ODD)), (0, dict(b=None)), (0, dict(b=ODD)),
+    (0, dict(x=None)), (0, dict(x=ODD)), (0, dict(b=None)), (0, dict(b=ODD)),
     (0, dict(w_post=None)), (0, dict(w_pre=None)), (0, dict(rb=None)), (0, dict(ro=None)),
     (0, dict(dx=None)), (0, dict(dx=ODD)), (0, dict(db=None)), (0, dict(db=ODD)),
     (0, dict(dw_post=None)), (0, dict(dw_pre=None)), (0, dict(dw_pre=ODD)), (0, dict(dgate=P)),
@@ -226,3 +226,13 @@ def test_mx4_config_matches_the_header():
     from test_abi_host import struct_fields
     assert [(n, ctypes.c_int32) for n, t in struct_fields("moe_mx4_config")] == \
         list(L.MoeMx4Config._fields_)
+
+
+def test_norm_backward_wants_what_the_forward_kept():
+    import torch
+    import mixture_experts_routed_gb300 as moe
+    B.build()
+    c = moe.norm_config(4, 64, "f32")
+    t, w, r = torch.zeros((4, 64)), torch.ones(64), torch.ones(4)
+    with pytest.raises(moe.MoEError, match="KeptNorm"):
+        moe.block_norm_backward(c, t, t, t, t, w, None, w, r, r, ws=torch.zeros(8))

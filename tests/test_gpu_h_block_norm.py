@@ -40,15 +40,19 @@ def both(T, d, dtype, kind, post, pre, seed=0, alpha=0.75, beta=1.5, eps=1e-5, i
     w = {k: wide(v) for k, v in i.items()}
     k = kind if post else "none"
     f = norm_forward(w["x"], w["b"], w["w_post"], w["gate"], w["w_pre"], k, eps, alpha, beta)
+    kept = r["rstd_pre"]
+    if post and pre:
+        assert isinstance(kept, moe.KeptNorm) and kept.x is i["x"]
+        r = {**r, "rstd_pre": kept.rstd}
     for name, want in f.items():
         check(name, r[name], want, torch.float32 if name.startswith("rstd") else dt)
-    y = r["out"] if post else i["x"]
     ws = moe.alloc_norm_workspace(c)
     ws.fill_(0xff)  # the workspace needs no zeroing: NaN bytes must not show
-    g = moe.block_norm_backward(c, i["dout"], i["dn"], y, i["b"], i["w_post"], i["gate"],
-                                i["w_pre"], r["rstd_post"], r["rstd_pre"], ws=ws)
-    want = norm_backward(w["dout"], w["dn"], wide(y), w["b"], w["w_post"], w["gate"], w["w_pre"],
-                         wide(r["rstd_post"]), wide(r["rstd_pre"]), k, alpha, beta)
+    g = moe.block_norm_backward(c, i["dout"], i["dn"], r["out"] if post else i["x"], i["b"], i["w_post"], i["gate"],
+                                i["w_pre"], r["rstd_post"], kept, ws=ws)
+    y64, ay = f["out"] if post else (w["x"], w["x"].abs())
+    want = norm_backward(w["dout"], w["dn"], y64, w["b"], w["w_post"], w["gate"], w["w_pre"],
+                         wide(r["rstd_post"]), wide(r["rstd_pre"]), k, alpha, beta, ay)
     assert {n for n, v in g.items() if v is not None} == set(want)
     for name, val in want.items():
         full = name in ("dx", "db") or (name == "dgate" and kind == "element")
@@ -74,6 +78,29 @@ def test_lengths(cuda_ok, T, d, dtype):
     both(T, d, dtype, "channel", True, True, seed=T + d)
 
 
+@pytest.mark.parametrize("T,d,kind", [(1, 64, "token"), (300, 2048, "channel"),
+                                      (77, 7168, "element"), (9, 20480, "none")])
+def test_weights_gradients_follow_the_unrounded_forward(cuda_ok, T, d, kind):
+    # against the formula's gradients of the unrounded chain: out is formed in fp32 for them, not
+    # read as bf16, so no sum is off by 2^-16 of its terms, nor of its value
+    i = norm_problem(T, d, torch.bfloat16, kind, True, True, 4, "cuda")
+    c = moe.norm_config(T, d, gate=kind, alpha=0.75, beta=1.5)
+    r = moe.block_norm(c, i["x"], i["b"], i["w_post"], i["gate"], i["w_pre"], want_rstd=True)
+    g = moe.block_norm_backward(c, i["dout"], i["dn"], r["out"], i["b"], i["w_post"], i["gate"],
+                                i["w_pre"], r["rstd_post"], r["rstd_pre"],
+                                ws=moe.alloc_norm_workspace(c))
+    w = {k: wide(v) for k, v in i.items()}
+    f = norm_forward(w["x"], w["b"], w["w_post"], w["gate"], w["w_pre"], kind, 1e-6, 0.75, 1.5)
+    want = norm_backward(w["dout"], w["dn"], f["out"][0], w["b"], w["w_post"], w["gate"],
+                         w["w_pre"], f["rstd_post"][0], f["rstd_pre"][0], kind, 0.75, 1.5)
+    for name in ("dw_pre", "dw_post") + (("dgate",) if kind in ("token", "channel") else ()):
+        value, terms = want[name]
+        tol = (2.0 ** -16 + (TERMS + T) * U32) * terms
+        assert bool(((g[name].cpu().to(F64) - value).abs() <= tol).all()), name
+        err = float((g[name].cpu().to(F64) - value).norm() / value.norm())
+        assert err <= 2.0 ** -16, (name, err)
+
+
 def test_empty_batch(cuda_ok):
     c = moe.norm_config(0, 128, "bf16", gate="channel")
     e = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
@@ -94,7 +121,7 @@ def test_zero_rows_and_values_at_the_ends(cuda_ok):
     i["b"][1] = 0
     i = {k: None if v is None else v.cuda() for k, v in i.items()}
     r, _ = both(6, 256, "f32", "none", True, True, i=i)
-    clean = {k: v.clone() for k, v in r.items()}
+    clean = {k: v.clone() for k, v in r.items() if k in ("out", "n")}
     i["b"][3, 7] = float("nan")
     i["x"][4, 9] = float("inf")
     c = moe.norm_config(6, 256, "f32", alpha=0.75, beta=1.5, eps=1e-5)
