@@ -185,25 +185,26 @@ __device__ __forceinline__ void store2f(float* p, const f2 (&v)[N / 2]) {
 // so that one barrier is enough.
 template <bool WARP>
 __device__ __forceinline__ float2 row_sums(float2 v, float2* buf, int& turn) {
+  const int lane = threadIdx.x & 31;
+  // the lower half of the warp takes the first value, the upper the second
+  auto warp_pair = [&](float2 u) {
+    const bool up = lane >= 16;
+    const float give = up ? u.x : u.y, keep = up ? u.y : u.x;
+    float w = keep + __shfl_xor_sync(0xffffffffu, give, 16);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-    v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-  }
+    for (int o = 8; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+    return w;
+  };
+  float w = warp_pair(v);
   if constexpr (!WARP) {
-    const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float2* b = buf + turn * 32;
     turn ^= 1;
-    if (lane == 0) b[w] = v;
+    if (lane == 0) b[threadIdx.x >> 5].x = w;
+    if (lane == 16) b[threadIdx.x >> 5].y = w;
     __syncthreads();
-    v = lane < (blockDim.x >> 5) ? b[lane] : float2{0.f, 0.f};
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-      v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-    }
+    w = warp_pair(lane < (blockDim.x >> 5) ? b[lane] : float2{0.f, 0.f});
   }
-  return v;
+  return float2{__shfl_sync(0xffffffffu, w, 0), __shfl_sync(0xffffffffu, w, 16)};
 }
 // one value, over the block
 __device__ __forceinline__ float row_sum(float v, float2* buf, int& turn) {
@@ -248,10 +249,9 @@ __device__ __forceinline__ void pack2(const float (&w)[N], f2 (&v)[N / 2]) {
 }
 
 // Threads of a block that takes rows by the warp; other blocks are one row's
-// threads, at most two vectors each forward, one backward (whose column sums
-// and weights are as many registers again: with two, half the warps were left
-// to hide its latencies, 166 us for 158; forward two small blocks do better
-// than one wide one, 111 us for 125 at 16384 x 5120).
+// threads, at most two vectors each forward (two small blocks to an SM do
+// better there than one wide one, 111 us for 125 at 16384 x 5120), one
+// backward.
 constexpr int kWarpBlock = 128;
 constexpr int kFwdVecs = 2, kBwdVecs = 1;
 constexpr int kRowVecs = 1024;  // vectors of the longest row a ring takes
@@ -406,15 +406,54 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kFwdVecs, WARP 
   ptx::cp_async_wait<0>();
 }
 
+// Half a vector, in pairs, from its raw 16 bytes.
+template <typename T>
+__device__ __forceinline__ void widen_half(const uint4& r, int half, f2 (&v)[Vec<T>::N / 4]) {
+  const uint32_t lo = half == 0 ? r.x : r.z, hi = half == 0 ? r.y : r.w;
+  if constexpr (std::is_same<T, float>::value) {
+    v[0] = mk2(__uint_as_float(lo), __uint_as_float(hi));
+  } else {
+    v[0] = mk2(__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u));
+    v[1] = mk2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+  }
+}
+// ... and rounded back into them.
+template <typename T>
+__device__ __forceinline__ void round_half(uint4& r, int half, const f2 (&v)[Vec<T>::N / 4]) {
+  uint32_t w[2];
+  if constexpr (std::is_same<T, float>::value) {
+    const float2 a = un2(v[0]);
+    w[0] = __float_as_uint(a.x);
+    w[1] = __float_as_uint(a.y);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 a = un2(v[i]);
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  if (half == 0) {
+    r.x = w[0];
+    r.y = w[1];
+  } else {
+    r.z = w[0];
+    r.w = w[1];
+  }
+}
+
 // Backward. Each row group walks rows g, g + groups, ... and keeps its rows'
 // column sums (of dw_pre; of dw_post, or A of a channel gate) in registers,
 // written once to part[group][2][d]; reduce_columns adds the groups in
 // order. Factors that a row shares (rstd, beta, a token gate) are taken out
 // of the per-element terms. The first sum of a row is taken a row ahead of
-// the rest, so there are two rings: S rows of what it reads (what out is
-// formed from, and dn; the rest reads them again) and two rows of the others.
-template <typename T, bool WARP, int S, bool POST, bool PRE>
-__global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP ? 4 : 1)
+// the rest; S rows are in the ring, each part of a slot filled again as soon
+// as its row is done with it.
+// A thread takes one vector, half by half: its sums and weights are 32
+// registers, and what a half needs fits beside them at 28 warps to the SM
+// (two vectors at 14 warps: 201 us for the 8191 x 7168 backward).
+template <typename T, int MAXT, int S, bool POST, bool PRE, bool ELEM>
+__global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
     norm_ring_bwd_kernel(const NormArgs a, const T* __restrict__ dout,
                          const float* __restrict__ dn, const T* __restrict__ x,
                          const T* __restrict__ b, const float* __restrict__ w_post,
@@ -422,7 +461,8 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
                          const float* __restrict__ rstd_post, const float* __restrict__ rstd_pre,
                          T* __restrict__ dx, T* __restrict__ db, void* __restrict__ dgate,
                          float* __restrict__ part) {
-  constexpr int N = Vec<T>::N, H = N / 2, RPB = WARP ? kWarpBlock / 32 : 1;
+  constexpr bool WARP = MAXT == kWarpBlock;
+  constexpr int N = Vec<T>::N, H = N / 2, Q = N / 4, RPB = WARP ? kWarpBlock / 32 : 1;
   constexpr int P = N / 4;  // 16-byte pieces of dn to a vector
   static_assert(S == 2 || S == 3, "rows in the first ring");
   extern __shared__ __align__(16) uint4 ring[];
@@ -430,222 +470,216 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kBwdVecs, WARP 
   int turn = 0;
   pdl_wait();
   pdl_trigger();
-  const int tpr = WARP ? 32 : blockDim.x, tid = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int sub = WARP ? threadIdx.x >> 5 : 0;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, sub = WARP ? threadIdx.x >> 5 : 0;
   const int d = a.d, nvec = d / N;
+  const bool mine = tid < nvec;
   const float inv_d = 1.f / static_cast<float>(d);
-  const bool elem = POST && a.gate == kGateElement, token = POST && a.gate == kGateToken;
-  // slots: x and dn, then b and an element gate, in the first ring where that
-  // is in use; dout in the second, before them otherwise
-  const int branch = POST ? nvec * (1 + (elem ? 1 : 0)) : 0;
-  const int size_a = PRE ? (1 + P) * nvec + branch : 0;
-  const int size_b = nvec + (PRE ? 0 : branch);
-  uint4* ring_a = ring + static_cast<size_t>(sub) * (S * size_a + 2 * size_b);
-  uint4* ring_b = ring_a + S * size_a;
+  const bool token = POST && a.gate == kGateToken;
+  // a slot: dout, x and dn, b, an element gate
+  const int off_x = nvec, off_b = PRE ? (2 + P) * nvec : nvec, off_g = off_b + nvec;
+  const int size = off_b + (POST ? nvec : 0) + (ELEM ? nvec : 0);
+  uint4* slots = ring + static_cast<size_t>(sub) * S * size + tid;
   const int group = blockIdx.x * RPB + sub, step = gridDim.x * RPB;
-  auto fill_branch = [&](uint4* dst, size_t at) {
-    if constexpr (POST) {
-      ring_fill<T, kBwdVecs>(dst, b + at, nvec, tid, tpr);
-      if (elem) ring_fill<T, kBwdVecs>(dst + nvec, static_cast<const T*>(gate) + at, nvec, tid, tpr);
-    }
-  };
-  auto fill_a = [&](int t, int slot) {
-    if constexpr (PRE) {
-      if (t >= a.T) return;
-      uint4* dst = ring_a + slot * size_a;
-      const size_t at = static_cast<size_t>(t) * d;
-      ring_fill<T, kBwdVecs>(dst, x + at, nvec, tid, tpr);
-#pragma unroll
-      for (int j = 0; j < kBwdVecs; ++j) {
-        const int i = tid + j * tpr;
-        if (i < nvec)
-#pragma unroll
-          for (int q = 0; q < P; ++q)
-            ptx::cp_async16(ptx::smem_u32(dst + (1 + q) * nvec + i), dn + at + i * N + q * 4);
-      }
-      fill_branch(dst + (1 + P) * nvec, at);
-    }
-  };
-  auto fill_b = [&](int t, int slot) {
-    if (t >= a.T) return;
-    uint4* dst = ring_b + slot * size_b;
-    const size_t at = static_cast<size_t>(t) * d;
-    ring_fill<T, kBwdVecs>(dst, dout + at, nvec, tid, tpr);
-    if constexpr (!PRE) fill_branch(dst + nvec, at);
-  };
-  f2 wb[kBwdVecs][H], wn[kBwdVecs][H], apre[kBwdVecs][H] = {}, apost[kBwdVecs][H] = {};
-  fill_a(group, 0);
-  fill_b(group, 0);
-  ptx::cp_async_commit();
-  if (S == 3) {
-    fill_a(group + step, 1);
-    ptx::cp_async_commit();
-  }
-#pragma unroll
-  for (int j = 0; j < kBwdVecs; ++j) {
-    const int c = (tid + j * tpr) * N;
-    if (c < d) {
-      float w[N];
-      if constexpr (POST) {
-        branch_weight<N>(w_post, gate, a.gate, c, w);
-        pack2<N>(w, wb[j]);
-      }
+  auto copy = [&](uint4* dst, const void* src) { ptx::cp_async16(ptx::smem_u32(dst), src); };
+  // a row's copies: what a row at work is done with first, and b
+  auto fill_rest = [&](int t, uint4* dst) {
+    if (t < a.T && mine) {
+      const size_t at = static_cast<size_t>(t) * d + tid * N;
+      copy(dst, dout + at);
       if constexpr (PRE) {
-        ld_f32<N>(w_pre + c, w);
-        pack2<N>(w, wn[j]);
+        copy(dst + off_x, x + at);
+#pragma unroll
+        for (int q = 0; q < P; ++q) copy(dst + off_x + (1 + q) * nvec, dn + at + q * 4);
       }
+      if constexpr (ELEM) copy(dst + off_g, static_cast<const T*>(gate) + at);
+    }
+  };
+  auto fill_b = [&](int t, uint4* dst) {
+    if constexpr (POST)
+      if (t < a.T && mine) copy(dst + off_b, b + static_cast<size_t>(t) * d + tid * N);
+    ptx::cp_async_commit();
+  };
+  f2 wb[H], wn[H], apre[H] = {}, apost[H] = {};
+#pragma unroll
+  for (int i = 0; i < S; ++i) {
+    fill_rest(group + i * step, slots + i * size);
+    fill_b(group + i * step, slots + i * size);
+  }
+  if (mine) {
+    float w[N];
+    if constexpr (POST) {
+      branch_weight<N>(w_post, gate, a.gate, tid * N, w);
+      pack2<N>(w, wb);
+    }
+    if constexpr (PRE) {
+      ld_f32<N>(w_pre + tid * N, w);
+      pack2<N>(w, wn);
     }
   }
-  const f2 al = dup2(POST ? a.alpha : 1.f);
-  // a row's statistics and token gate, loaded while the row before is at work
-  float ro_next = 0.f, rb_next = 0.f, gt_next = 1.f;
+  // statistics and token gate of a row, the next and, on its way, the one after
+  struct Stats {
+    float ro, rb, gt;
+  };
   auto fetch = [&](int t) {
-    if (t >= a.T) return;
-    if (PRE) ro_next = __ldg(rstd_pre + t);
-    if (POST) rb_next = __ldg(rstd_post + t);
-    if (token) gt_next = __ldg(static_cast<const float*>(gate) + t);
-  };
-  // out (y) and dn (v) at vector i of a first-ring slot; k = beta gate rstd_post
-  auto load_y = [&](const uint4* in, int i, int j, f2 k, f2 (&y)[H], f2 (&v)[H]) {
-    widen2<T>(in[i], y);
-    if constexpr (POST) {
-      f2 u[H];
-      widen2<T>(in[(1 + P) * nvec + i], u);
-#pragma unroll
-      for (int q = 0; q < H; ++q) u[q] = mul2(u[q], wb[j][q]);
-      if (elem) {
-        f2 g[H];
-        widen2<T>(in[(2 + P) * nvec + i], g);
-#pragma unroll
-        for (int q = 0; q < H; ++q) u[q] = mul2(u[q], g[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < H; ++q) y[q] = fma2(k, u[q], mul2(al, y[q]));
+    Stats r{0.f, 0.f, 1.f};
+    if (t < a.T) {
+      if (PRE) r.ro = __ldg(rstd_pre + t);
+      if (POST) r.rb = __ldg(rstd_post + t);
+      if (token) r.gt = __ldg(static_cast<const float*>(gate) + t);
     }
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-      const uint4 r = in[(1 + q) * nvec + i];
-      v[2 * q] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
-      v[2 * q + 1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+    return r;
+  };
+  // half h of dn
+  auto half_dn = [&](const uint4* in, int h, f2 (&v)[Q]) {
+    if constexpr (Q == 2) {
+      const uint4 r = in[off_x + (1 + h) * nvec];
+      v[0] = mk2(__uint_as_float(r.x), __uint_as_float(r.y));
+      v[1] = mk2(__uint_as_float(r.z), __uint_as_float(r.w));
+    } else {
+      widen_half<T>(in[off_x + nvec], h, v);
     }
   };
-  // a row's part of ro mean(v y), and its terms of dw_pre
-  auto first = [&](const uint4* in, float ro, float k) {
+  const f2 al = dup2(POST ? a.alpha : 1.f);
+  // a row's part of mean(v y), and its terms of dw_pre
+  auto first = [&](const uint4* in, const Stats& st) {
     f2 ss = 0;
     if constexpr (PRE) {
-      const f2 r2 = dup2(ro), kk = dup2(k);
+      if (mine) {
+        const f2 r2 = dup2(st.ro), k = dup2(st.gt * a.beta * st.rb);
+        const uint4 xr = in[off_x];
+        uint4 br = {}, gr = {};
+        if constexpr (POST) br = in[off_b];
+        if constexpr (ELEM) gr = in[off_g];
 #pragma unroll
-      for (int j = 0; j < kBwdVecs; ++j) {
-        const int i = tid + j * tpr;
-        if (i < nvec) {
-          f2 y[H], v[H];
-          load_y(in, i, j, kk, y, v);
+        for (int h = 0; h < 2; ++h) {
+          f2 y[Q], v[Q];
+          widen_half<T>(xr, h, y);
+          if constexpr (POST) {
+            f2 u[Q], g[Q];
+            widen_half<T>(br, h, u);
+            if constexpr (ELEM) widen_half<T>(gr, h, g);
 #pragma unroll
-          for (int q = 0; q < H; ++q) {
-            const f2 p = mul2(mul2(v[q], r2), y[q]);
-            asm("add.rn.f32x2 %0, %0, %1;" : "+l"(apre[j][q]) : "l"(p));
-            ss = fma2(p, wn[j][q], ss);
+            for (int q = 0; q < Q; ++q) {
+              u[q] = mul2(u[q], wb[h * Q + q]);
+              if constexpr (ELEM) u[q] = mul2(u[q], g[q]);
+              y[q] = fma2(k, u[q], mul2(al, y[q]));
+            }
+          }
+          half_dn(in, h, v);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            const f2 p = mul2(v[q], y[q]);
+            apre[h * Q + q] = fma2(p, r2, apre[h * Q + q]);
+            ss = fma2(p, wn[h * Q + q], ss);
           }
         }
       }
     }
-    const float2 h = un2(ss);
-    return h.x + h.y;
+    const float2 f = un2(ss);
+    return f.x + f.y;
   };
-  fetch(group);
+  Stats now = fetch(group), next = fetch(group + step);
   float s1 = 0.f;
-  ptx::cp_async_wait<S - 2>();  // the first row
+  ptx::cp_async_wait<S - 1>();  // the first row
   if (PRE && group < a.T)
-    s1 = row_sums<WARP>(float2{first(ring_a, ro_next, gt_next * a.beta * rb_next), 0.f}, buf, turn)
-             .x *
-         inv_d;
-  int sa = 0, sb = 0;
-  for (int t = group; t < a.T; t += step, sa = sa + 1 == S ? 0 : sa + 1, sb ^= 1) {
-    const int sa_next = sa + 1 == S ? 0 : sa + 1;
-    // (into the slots that the row before this one was read from)
-    fill_a(t + (S - 1) * step, sa == 0 ? S - 1 : sa - 1);
-    fill_b(t + step, sb ^ 1);
-    ptx::cp_async_commit();
-    if (S == 3) ptx::cp_async_wait<1>();  // this row's second part, the next row's first
-    const uint4 *in_a = ring_a + sa * size_a, *in_b = ring_b + sb * size_b;
-    const uint4* in_br = PRE ? in_a + (1 + P) * nvec : in_b + nvec;  // b, element gate
-    const size_t at = static_cast<size_t>(t) * d;
-    const float ro = ro_next, rb = rb_next, gt = gt_next;
-    fetch(t + step);
+    s1 = row_sums<WARP>(float2{first(slots, now), 0.f}, buf, turn).x;
+  int slot = 0;
+  for (int t = group; t < a.T; t += step) {
+    uint4* in = slots + slot * size;
+    slot = slot + 1 == S ? 0 : slot + 1;
+    const uint4* in_next = slots + slot * size;
+    const size_t at = static_cast<size_t>(t) * d + tid * N;
+    const Stats after = fetch(t + 2 * step);
+    const float k = now.gt * a.beta * now.rb;
     // D = dout + ro v - ro yh mean(v yh), dx = alpha D and, of the branch, D w
-    const f2 r2 = dup2(ro), c2 = dup2(-ro * ro * s1), k2 = dup2(gt * a.beta * rb);
-    f2 v2[kBwdVecs][H], ss = 0;
+    f2 v2[H], ss = 0;
+    if (mine) {
+      const float c = now.ro * now.ro * now.ro * s1 * inv_d;
+      const f2 r2 = dup2(now.ro), cx = dup2(-c * (POST ? a.alpha : 1.f)), cu = dup2(-c * k),
+               k2 = dup2(k);
+      const uint4 dr = in[0];
+      uint4 xr = {}, brr = {}, gr = {}, od, og = {};
+      if constexpr (PRE) xr = in[off_x];
+      if constexpr (POST) brr = in[off_b];
+      if constexpr (ELEM) gr = in[off_g];
 #pragma unroll
-    for (int j = 0; j < kBwdVecs; ++j) {
-      const int i = tid + j * tpr;
-      if (i < nvec) {
-        f2 D[H], o[H];
-        widen2<T>(in_b[i], D);
-        if constexpr (PRE) {
-          f2 y[H], v[H];
-          load_y(in_a, i, j, k2, y, v);
-#pragma unroll
-          for (int q = 0; q < H; ++q)
-            D[q] = fma2(mul2(v[q], wn[j][q]), r2, fma2(y[q], c2, D[q]));
-        }
-#pragma unroll
-        for (int q = 0; q < H; ++q) o[q] = mul2(al, D[q]);
-        store2<T>(dx + at + i * N, o);
+      for (int h = 0; h < 2; ++h) {
+        f2 D[Q], u[Q], bb[Q], g[Q];
+        widen_half<T>(dr, h, D);
         if constexpr (POST) {
-          f2 bb[H];
-          widen2<T>(in_br[i], bb);
-          if (elem) {
-            f2 g[H];
-            widen2<T>(in_br[nvec + i], g);
+          widen_half<T>(brr, h, bb);
+          if constexpr (ELEM) widen_half<T>(gr, h, g);
 #pragma unroll
-            for (int q = 0; q < H; ++q) {
-              o[q] = mul2(mul2(D[q], k2), mul2(bb[q], wb[j][q]));
+          for (int q = 0; q < Q; ++q) {
+            u[q] = mul2(bb[q], wb[h * Q + q]);
+            if constexpr (ELEM) u[q] = mul2(u[q], g[q]);
+          }
+        }
+        if constexpr (PRE) {
+          f2 y[Q], v[Q];
+          widen_half<T>(xr, h, y);
+          half_dn(in, h, v);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            D[q] = fma2(y[q], cx, D[q]);
+            if constexpr (POST) D[q] = fma2(u[q], cu, D[q]);
+            D[q] = fma2(mul2(v[q], wn[h * Q + q]), r2, D[q]);
+          }
+        }
+        f2 o[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) o[q] = mul2(al, D[q]);
+        round_half<T>(od, h, o);
+        if constexpr (POST) {
+#pragma unroll
+          for (int q = 0; q < Q; ++q) {
+            ss = fma2(D[q], u[q], ss);
+            if constexpr (ELEM) {
+              o[q] = mul2(mul2(D[q], k2), mul2(bb[q], wb[h * Q + q]));
               D[q] = mul2(D[q], g[q]);
             }
-            store2<T>(static_cast<T*>(dgate) + at + i * N, o);
+            apost[h * Q + q] = fma2(mul2(D[q], k2), bb[q], apost[h * Q + q]);
+            v2[h * Q + q] = mul2(D[q], wb[h * Q + q]);
           }
-#pragma unroll
-          for (int q = 0; q < H; ++q) {
-            apost[j][q] = fma2(mul2(D[q], k2), bb[q], apost[j][q]);
-            v2[j][q] = mul2(D[q], wb[j][q]);
-            ss = fma2(v2[j][q], bb[q], ss);
-          }
+          if constexpr (ELEM) round_half<T>(og, h, o);
         }
       }
+      *reinterpret_cast<uint4*>(dx + at) = od;
+      if constexpr (ELEM) *reinterpret_cast<uint4*>(static_cast<T*>(dgate) + at) = og;
     }
-    if (S == 2) ptx::cp_async_wait<0>();  // the next row
-    const float2 h = un2(ss);
-    const float next = t + step < a.T ? first(ring_a + sa_next * size_a, ro_next, gt_next * a.beta * rb_next)
-                                        : 0.f;
-    const float2 sums = row_sums<WARP>(float2{next, h.x + h.y}, buf, turn);
-    s1 = sums.x * inv_d;
+    fill_rest(t + S * step, in);  // (of this row only b is read again)
+    ptx::cp_async_wait<S - 2>();  // the next row
+    const float2 f = un2(ss);
+    const float ahead = t + step < a.T ? first(in_next, next) : 0.f;
+    const float2 sums = row_sums<WARP>(float2{ahead, f.x + f.y}, buf, turn);
+    s1 = sums.x;
     if constexpr (POST) {
       // sum of D w b: beta rb of it is a token gate's gradient
-      const float sum = sums.y;
-      if (token && tid == 0) static_cast<float*>(dgate)[t] = a.beta * rb * sum;
-      const float k = gt * a.beta * rb;
-      const f2 kv = dup2(k), kb = dup2(-k * rb * rb * sum * inv_d);
+      if (token && tid == 0) static_cast<float*>(dgate)[t] = a.beta * now.rb * sums.y;
+      if (mine) {
+        const f2 kv = dup2(k), kb = dup2(-k * now.rb * now.rb * sums.y * inv_d);
+        const uint4 brr = in[off_b];
+        uint4 o;
 #pragma unroll
-      for (int j = 0; j < kBwdVecs; ++j) {
-        const int i = tid + j * tpr;
-        if (i < nvec) {
-          f2 bb[H];
-          widen2<T>(in_br[i], bb);
+        for (int h = 0; h < 2; ++h) {
+          f2 bb[Q];
+          widen_half<T>(brr, h, bb);
 #pragma unroll
-          for (int q = 0; q < H; ++q) v2[j][q] = fma2(kv, v2[j][q], mul2(kb, bb[q]));
-          store2<T>(db + at + i * N, v2[j]);
+          for (int q = 0; q < Q; ++q) bb[q] = fma2(kv, v2[h * Q + q], mul2(kb, bb[q]));
+          round_half<T>(o, h, bb);
         }
+        *reinterpret_cast<uint4*>(db + at) = o;
       }
     }
+    fill_b(t + S * step, in);
+    now = next;
+    next = after;
   }
   ptx::cp_async_wait<0>();
-#pragma unroll
-  for (int j = 0; j < kBwdVecs; ++j) {
-    const int i = tid + j * tpr;
-    if (i >= nvec) continue;
-    float* o = part + static_cast<size_t>(group) * 2 * d + i * N;
-    if (PRE) store2f<N>(o, apre[j]);
-    if (POST) store2f<N>(o + d, apost[j]);
+  if (mine) {
+    float* o = part + static_cast<size_t>(group) * 2 * d + tid * N;
+    if (PRE) store2f<N>(o, apre);
+    if (POST) store2f<N>(o + d, apost);
   }
 }
 
@@ -883,10 +917,10 @@ int threads_of(int nvec, int vecs) {
 size_t fwd_slot(int dtype, int d, bool post, bool elem) {
   return static_cast<size_t>(d) * (dtype == 0 ? 4 : 2) * (1 + (post ? 1 : 0) + (elem ? 1 : 0));
 }
-size_t bwd_ring(int dtype, int d, bool post, bool pre, bool elem, int rows) {
-  const int es = dtype == 0 ? 4 : 2, branch = post ? es * (1 + (elem ? 1 : 0)) : 0;
-  const int first = pre ? es + 4 + branch : 0, second = es + (pre ? 0 : branch);
-  return static_cast<size_t>(d) * (first * rows + second * 2);
+size_t bwd_slot(int dtype, int d, bool post, bool pre, bool elem) {
+  const int es = dtype == 0 ? 4 : 2;
+  return static_cast<size_t>(d) *
+         (es + (pre ? es + 4 : 0) + (post ? es * (1 + (elem ? 1 : 0)) : 0));
 }
 constexpr size_t kRingMost = 225 * 1024;  // shared memory an SM has for its blocks' rings
 constexpr int kStages = 3;
@@ -906,7 +940,7 @@ int bwd_groups(int dtype, int d, bool elem, int T) {
   const int tpr = threads_of(d / (dtype == 0 ? 4 : 8), kBwdVecs);
   if (tpr == 0) return T < 152 ? T : 152;
   const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
-  const size_t ring = bwd_ring(dtype, d, true, true, elem, kStages) * rpb;
+  const size_t ring = bwd_slot(dtype, d, true, true, elem) * kStages * rpb;
   const int most = 152 * blocks_per_sm(tpr, 64, ring) * rpb;
   return ceil_div(T < most ? T : most, rpb) * rpb;
 }
@@ -952,18 +986,21 @@ struct Bwd {
                         a, args...);
     const int rpb = tpr == 32 ? kWarpBlock / 32 : 1;
     auto ring = [&](int rows) {
-      return bwd_ring(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement, rows) *
-             rpb;
+      return bwd_slot(sizeof(T) == 4 ? 0 : 1, a.d, POST, PRE, a.gate == kGateElement) * rows * rpb;
     };
-    if (tpr == 32)
-      return launch_ring(norm_ring_bwd_kernel<T, true, kStages, POST, PRE>, groups / rpb, kWarpBlock,
-                         ring(kStages), s, a, args...);
-    // the longest rows leave room for two
-    return ring(kStages) <= kRingMost
-               ? launch_ring(norm_ring_bwd_kernel<T, false, kStages, POST, PRE>, groups, tpr,
-                             ring(kStages), s, a, args...)
-               : launch_ring(norm_ring_bwd_kernel<T, false, 2, POST, PRE>, groups, tpr, ring(2), s,
-                             a, args...);
+    auto run = [&](auto elem) {
+      constexpr bool ELEM = POST && decltype(elem)::value;
+      if (tpr == 32)
+        return launch_ring(norm_ring_bwd_kernel<T, kWarpBlock, kStages, POST, PRE, ELEM>,
+                           groups / rpb, kWarpBlock, ring(kStages), s, a, args...);
+      // the longest rows leave room for two
+      return ring(kStages) <= kRingMost
+                 ? launch_ring(norm_ring_bwd_kernel<T, kRowVecs, kStages, POST, PRE, ELEM>, groups,
+                               tpr, ring(kStages), s, a, args...)
+                 : launch_ring(norm_ring_bwd_kernel<T, kRowVecs, 2, POST, PRE, ELEM>, groups, tpr,
+                               ring(2), s, a, args...);
+    };
+    return a.gate == kGateElement ? run(std::true_type()) : run(std::false_type());
   }
 };
 
