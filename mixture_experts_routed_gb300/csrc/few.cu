@@ -75,7 +75,7 @@ struct Cfg {
   static constexpr int B_HALF = (N1 > N2 ? N1 : N2) * 128;  // 64 k of every column
   static constexpr int B_BYTES = 2 * B_HALF;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 200 * 1024 / STAGE;
+  static constexpr int STAGES = 219 * 1024 / STAGE;
   static constexpr int OFF_BAR = STAGES * STAGE;
   static constexpr int OFF_TAB = OFF_BAR + (2 * STAGES + 5) * 8;
   static constexpr int SMEM = OFF_TAB + 256 * 4 + 256 * 2 + MAX_ROWS * 4 + MAX_ROWS * 4 + 64 + 1024;
