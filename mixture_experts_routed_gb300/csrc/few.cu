@@ -7,9 +7,9 @@
 //   out[t] = sum over the chosen e of w[t, e] (h[t, e] W2[e])
 //
 // Bound: each chosen expert's weights cross HBM once (4 d f bytes); the
-// products are thin. So the grid is one CTA per SM and every CTA streams an
-// equal, contiguous share of the weight tiles through a deep TMA ring, from
-// the first W1 tile to the last W2 tile without draining.
+// products are thin. So the grid is one CTA per SM and every CTA streams its
+// share of the weight tiles through a deep TMA ring, from the first W1 tile
+// to the last W2 tile without draining.
 //
 // Products: the weights are the M operand of tcgen05.mma, 128 output
 // features x 128 contraction rows a step, read MN-major straight from their
@@ -19,14 +19,23 @@
 // W2 the tokens' h rows are carried as bf16 hi + lo, side by side in N
 // (h to 2^-17 relative, so out is rounded once).
 //
-// Work split: the tiles of a phase, k innermost, are one sequence of steps
-// (128 contraction rows x 128 features), cut into equal ranges, one per CTA.
-// A feature block whose steps fall to several CTAs is joined from their fp32
-// partial sums by the last of them to arrive, in CTA order: no atomics on
-// values, so the result is bitwise reproducible on one GPU model. In phase 1
-// a block is one expert's 128 features of h; in phase 2 it is 128 features
-// of out with every expert's steps one after the other, the routing weights
-// applied as each expert's accumulator is read.
+// Work split: a feature block (phase 1: one expert's 128 features of h; phase
+// 2: 128 features of out, every expert's steps one after the other) is a run
+// of steps of 128 contraction rows, cut into equal chunks where there are
+// fewer blocks than the SMs want units of work. CTAs take units in order from
+// a counter, one ahead: SMs differ by a tenth in the bandwidth they get, and
+// equal shares left them waiting for the slowest (one token through 8 of 256
+// experts: 89.8 us so, 85.5 now; 8 tokens: 416 and 400). A cut block's fp32
+// partial sums are joined by the last CTA to arrive, in chunk order, whoever
+// computed them: no atomics on values, so the result is bitwise reproducible.
+// In phase 2 the routing weights are applied as each expert's accumulator is
+// read.
+//
+// Measured: 7 tokens, 8 experts of 4096 x 11008, two chosen: 163 us, 7.7 TB/s
+// of weights (a plain copy of this GPU: 6.8); one token, 256 experts of
+// 7168 x 2048, eight chosen: 85 us, 5.6 TB/s; two of 64 experts of
+// 2048 x 1408: 18.6 us, where the chain gate -> router -> W1 -> W2 and its
+// four hand-overs between CTAs bound it, not the 3.4 us of bytes.
 //
 // The CTAs wait on one another (gate sums -> router -> h), so the launch is
 // cooperative: all of them are resident. While a CTA waits for h its ring
@@ -41,7 +50,6 @@
 
 #include "common.cuh"
 #include "ptx.cuh"
-#include "range.cuh"
 #include "tmap.cuh"
 #include "topk.cuh"
 
@@ -58,8 +66,14 @@ constexpr int A_BYTES = 4 * BOX_BYTES;      // [k half][feature half]
 constexpr int GATE_E = 64;                  // experts of a gate CTA
 constexpr int GATE_ROWS = 256;              // contraction rows staged at a time
 constexpr int MAX_LOADS = 32;               // partial sums of a logit a thread adds up
-constexpr int WARM_STEPS = 12;              // W2 steps prefetched to L2: 58 MB over 152 CTAs
-constexpr int TMEM_COLS = 128;              // two accumulators of 64 columns
+constexpr int ACCS = 4, TMEM_COLS = 256;    // accumulators of 64 columns
+constexpr int QUEUE = 8;                    // units on their way through a CTA
+// Units a CTA is to take in a phase: more even out the SMs better, but each
+// costs a partial sum and its arrival, about 1 us of the epilogue (one token
+// and 256 experts, eight chosen: 2, 3, 5, 10 units 89.5, 85.5, 86.1, 96.9 us);
+// and the fewest steps to a unit of a cut block (1: 21.1 us for 18.7 at one
+// token and two experts of 2048 x 1408).
+constexpr int UNITS = 3, UNIT_STEPS = 2;
 constexpr int MAX_ROWS = kFewMaxTokens * kMaxFanout;
 
 // TP: the tokens a launch is compiled for
@@ -77,8 +91,10 @@ struct Cfg {
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int STAGES = 219 * 1024 / STAGE;
   static constexpr int OFF_BAR = STAGES * STAGE;
-  static constexpr int OFF_TAB = OFF_BAR + (2 * STAGES + 5) * 8;
-  static constexpr int SMEM = OFF_TAB + 256 * 4 + 256 * 2 + MAX_ROWS * 4 + MAX_ROWS * 4 + 64 + 1024;
+  static_assert(STAGES < QUEUE, "a stage may wait for h in each of as many units");
+  static constexpr int OFF_TAB = OFF_BAR + (2 * STAGES + 2 * ACCS + 2 * QUEUE + 1) * 8;
+  static constexpr int SMEM = OFF_TAB + 256 * 4 + 256 * 2 + MAX_ROWS * 4 + MAX_ROWS * 4 + 64 +
+                              QUEUE * 4 + QUEUE * 12 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(GATE_ROWS * TP * 4 + RG * TP * GATE_E * 4 + GATE_ROWS * GATE_E * 2 <= OFF_BAR,
                 "scratch");
@@ -98,12 +114,12 @@ struct Params {
   uint32_t* tiles;   // arrivals: [slots][f blocks], then [d blocks]
   int ntiles;
   __nv_bfloat16* h;  // [slots][2 TP][f]
-  float* part;       // [phase][CTA][2][TP][128]
+  float* part;       // [phase][unit][TP][128]
   __nv_bfloat16* out;
   uint32_t* err;
-  uint32_t* sync;    // four counters, 8 words apart, zero between launches
+  uint32_t* sync;    // five counters, zero between launches
 };
-constexpr int SYNC_GATE = 0, SYNC_ROUTE = 8, SYNC_H = 16, SYNC_EXIT = 24;
+constexpr int SYNC_GATE = 0, SYNC_CLAIM = 4, SYNC_ROUTE = 8, SYNC_H = 16, SYNC_EXIT = 24;
 
 __device__ __forceinline__ uint32_t ld_acquire(const uint32_t* p) {
   uint32_t v;
@@ -202,6 +218,20 @@ __device__ __forceinline__ void weigh_all(const float* row, int E, const RouterS
   const float v[1] = {lane < E ? row[lane] : -INFINITY};
   topk::warp_soft_weigh<1>(v, id, E, rs, t, idx, w);
 }
+// A phase's units: blocks of `len` steps in `chunks` chunks of `per`; unit v
+// is chunk v / blocks of block v % blocks, so that the CTAs at work side by
+// side read whole rows of the weights between them (the other way round they
+// read one column of them: 222 us for 165 at 7 tokens and 8 wide experts).
+struct Cut {
+  int blocks, len, per, chunks, units;
+  __device__ Cut(int blocks_, int len_, int want) : blocks(blocks_), len(len_) {
+    per = max(UNIT_STEPS, (blocks * len + want - 1) / want);
+    chunks = per >= len ? 1 : (len + per - 1) / per;
+    per = (len + chunks - 1) / chunks;
+    chunks = (len + per - 1) / per;
+    units = blocks * chunks;
+  }
+};
 __device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
 }  // namespace fw
 
@@ -218,8 +248,10 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::STAGES;
   uint64_t* tfull = empty + C::STAGES;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + ACCS;
+  uint64_t* qfull = tempty + ACCS;
+  uint64_t* qempty = qfull + QUEUE;
+  uint64_t* drain = qempty + QUEUE;
   uint32_t* smask = reinterpret_cast<uint32_t*>(smem + C::OFF_TAB);  // slot -> its tokens
   float* rw = reinterpret_cast<float*>(smask + kMaxExperts);         // [T][k] weights
   int32_t* ridx = reinterpret_cast<int32_t*>(rw + MAX_ROWS);         // [T][k] experts, -1: none
@@ -228,6 +260,8 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   uint32_t* tmem_slot = misc;
   int* s_nslots = reinterpret_cast<int*>(misc + 1);
   uint32_t* s_last = misc + 2;
+  volatile int* queue = reinterpret_cast<volatile int*>(misc + 16);   // unit numbers, -1: no more
+  int* pending = reinterpret_cast<int*>(misc + 16 + QUEUE);           // steps that wait for h
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cta = blockIdx.x, grid = gridDim.x;
   const int T = p.T, d = p.d, E = p.E, f = p.f, k = p.k;
@@ -237,9 +271,13 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < ACCS; ++i) {
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 4);
+    }
+    for (int i = 0; i < QUEUE; ++i) {
+      mbar_init(&qfull[i], 1);
+      mbar_init(&qempty[i], 5);  // the MMA warp, four epilogue warps
     }
     mbar_init(drain, 1);
     fence_mbar_init();
@@ -441,7 +479,9 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
   const uint32_t tmem_base = *tmem_slot;
   const int nslots = *s_nslots;
   const int FB = (f + BM - 1) / BM, DB = (d + BM - 1) / BM;
-  const Range r1(nslots * FB, (d + BK - 1) / BK, grid), r2(DB * nslots, (f + BK - 1) / BK, grid);
+  // (fewer than 2 want units of a cut phase: cut blocks are fewer than want)
+  const int len2 = (f + BK - 1) / BK, want = grid * UNITS;
+  const Cut c1(nslots * FB, (d + BK - 1) / BK, want), c2(DB, nslots * len2, want);
 
   if (nslots == 0) {
     for (size_t i = static_cast<size_t>(cta) * THREADS + tid; i < static_cast<size_t>(T) * d;
@@ -489,13 +529,50 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       if (used < C::STAGES) ++used;
       return true;
     };
-    {
-      const int end = r1.start(cta + 1);
-      for (int i = r1.start(cta); i < end && !dead;) {
-        const int u = i / r1.len, k0 = i - u * r1.len, n = min(r1.len - k0, end - i);
+    // hand unit v (-1: the end) to the other roles
+    int qi = 0;
+    uint32_t qph = 0;
+    auto push = [&](int v) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&qempty[qi], qph ^ 1u, kWaitLimitNs))) dead = true;
+      if (lane == 0) {
+        queue[qi] = v;
+        mbar_arrive(&qfull[qi]);
+      }
+      __syncwarp();
+      if (++qi == QUEUE) {
+        qi = 0;
+        qph ^= 1u;
+      }
+    };
+    // Before h is known to be there, W2 tiles go out without their h rows, as
+    // many as the ring holds; those follow once every h tile has been counted.
+    bool ready = false;
+    int npend = 0;
+    auto h_ready = [&]() {
+      if (lane == 0 && !lost) lost = !wait_count(p.sync + SYNC_H, nslots * FB, kWaitLimitNs);
+      __syncwarp();
+      asm volatile("fence.proxy.async.global;" ::: "memory");
+      ready = true;
+      if (dead) return;
+      s -= npend;
+      if (s < 0) s += C::STAGES;
+      for (int i = 0; i < npend; ++i) {
+        if (elect_one()) load_b(&tmH, pending[3 * i], pending[3 * i + 1], pending[3 * i + 2]);
+        __syncwarp();
+        if (++s == C::STAGES) s = 0;  // (the phase is already the next stage's)
+      }
+    };
+    int v = cta;
+    while (v < c1.units + c2.units && !dead) {
+      push(v);
+      // the next one, on its way while this one is loaded
+      int v_next = 0;
+      if (lane == 0) v_next = grid + static_cast<int>(atomicAdd(p.sync + SYNC_CLAIM, 1u));
+      if (v < c1.units) {
+        const int j1 = v / c1.blocks, u = v - j1 * c1.blocks, k0 = j1 * c1.per;
         const int slot = u / FB, c0 = (u - slot * FB) * BM, row = sexp[slot] * d;
-        const int nb = min(2, (f - c0) / 64);
-        for (int j = k0; j < k0 + n; ++j) {
+        const int nb = min(2, (f - c0) / 64), k1 = min(c1.len, k0 + c1.per);
+        for (int j = k0; j < k1; ++j) {
           if (!claim()) break;
           const int nk = min(2, d / 64 - 2 * j);
           if (elect_one()) {
@@ -505,61 +582,37 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           __syncwarp();
           next();
         }
-        i += n;
-      }
-    }
-    if (!dead) {
-      // the first W2 tiles go out before h is known to be there; their h
-      // rows follow once every h tile has been counted
-      const int first = r2.start(cta), end = r2.start(cta + 1);
-      const int ahead = min(end, first + C::STAGES);
-      const int s0 = s;
-      const uint32_t ph0 = ph;
-      auto w2_steps = [&](int from, int to, bool a, bool b) {
-        for (int i = from; i < to && !dead;) {
-          const int u = i / r2.len, k0 = i - u * r2.len, n = min(r2.len - k0, to - i);
-          const int db = u / nslots, slot = u - db * nslots;
-          const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
-          for (int j = k0; j < k0 + n; ++j) {
-            if (a && !claim()) break;
-            const int nk = min(2, f / 64 - 2 * j);
-            if (elect_one()) {
-              if (a) load_a(&tmW2, row + j * BK, db * BM, nk, nb, C::HR * 128);
-              if (b) load_b(&tmH, j * BK, nk, slot * C::HR);
-            }
-            __syncwarp();
-            next();
-          }
-          i += n;
-        }
-      };
-      w2_steps(first, ahead, true, false);
-      // and the next ones to L2, so that HBM is at work meanwhile
-      const int warm = min(end, ahead + WARM_STEPS);
-      for (int i = ahead; i < warm;) {
-        const int u = i / r2.len, k0 = i - u * r2.len, n = min(r2.len - k0, warm - i);
-        const int db = u / nslots, slot = u - db * nslots;
-        const int row = sexp[slot] * f, nb = min(2, (d - db * BM) / 64);
-        for (int j = k0; j < k0 + n; ++j) {
+      } else {
+        const int w = v - c1.units, j2 = w / c2.blocks, db = w - j2 * c2.blocks, i0 = j2 * c2.per;
+        const int i1 = min(c2.len, i0 + c2.per), nb = min(2, (d - db * BM) / 64);
+        int slot = i0 / len2, j = i0 - slot * len2;
+        for (int i = i0; i < i1; ++i) {
+          if (!ready && npend == C::STAGES) h_ready();
+          if (!claim()) break;
           const int nk = min(2, f / 64 - 2 * j);
-          if (elect_one())
-            for (int h = 0; h < nk; ++h)
-              for (int b = 0; b < nb; ++b)
-                tma_prefetch_2d(&tmW2, db * BM + b * 64, row + j * BK + h * 64);
+          if (elect_one()) {
+            load_a(&tmW2, sexp[slot] * f + j * BK, db * BM, nk, nb, C::HR * 128);
+            if (ready) {
+              load_b(&tmH, j * BK, nk, slot * C::HR);
+            } else {
+              pending[3 * npend] = j * BK;
+              pending[3 * npend + 1] = nk;
+              pending[3 * npend + 2] = slot * C::HR;
+            }
+          }
           __syncwarp();
+          if (!ready) ++npend;
+          next();
+          if (++j == len2) {
+            j = 0;
+            ++slot;
+          }
         }
-        i += n;
       }
-      if (lane == 0 && !lost) lost = !wait_count(p.sync + SYNC_H, nslots * FB, kWaitLimitNs);
-      __syncwarp();
-      asm volatile("fence.proxy.async.global;" ::: "memory");
-      if (!dead) {
-        s = s0;
-        ph = ph0;
-        w2_steps(first, ahead, false, true);
-        w2_steps(ahead, end, true, true);
-      }
+      v = __shfl_sync(0xffffffffu, v_next, 0);
     }
+    if (!ready && npend > 0) h_ready();
+    push(-1);
     // no copy may still be on its way into this CTA when it exits: the
     // latest use of each stage has landed (its phase is the one before s, ph)
     for (int j = 0; j < used; ++j) {
@@ -582,55 +635,76 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     bool dead = false;
     const uint64_t ad0 = make_sdesc_sw128(smem_u32(smem), BOX_BYTES, 1024),
                    bd0 = make_sdesc_sw128(smem_u32(smem) + A_BYTES, 16, 1024);
-    auto phase = [&](const Range& r, int k64, uint32_t idesc) {
-      const int end = r.start(cta + 1);
-      for (int i = r.start(cta); i < end && !dead;) {
-        const int k0 = i % r.len, n = min(r.len - k0, end - i);
-        if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs))) {
+    // n steps into the next accumulator, the first at step k0 of k64 half steps
+    auto run = [&](int k0, int n, int k64, uint32_t idesc) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&tempty[acc], aph ^ 1u, kWaitLimitNs))) {
+        dead = true;
+        return;
+      }
+      tc_fence_after();
+      const uint32_t dt = tmem_base + acc * 64;
+      for (int j = 0; j < n; ++j) {
+        if (!__all_sync(0xffffffffu, mbar_wait_spin(&full[s], ph, kWaitLimitNs))) {
           dead = true;
           break;
         }
         tc_fence_after();
-        const uint32_t dt = tmem_base + acc * 64;
-        for (int j = 0; j < n; ++j) {
-          if (!__all_sync(0xffffffffu, mbar_wait_spin(&full[s], ph, kWaitLimitNs))) {
-            dead = true;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
-          const uint32_t more = j > 0 ? 1u : 0u;
-          const bool both = k64 - 2 * (k0 + j) >= 2;  // both k halves
-          if (elect_one()) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t more = j > 0 ? 1u : 0u;
+        const bool both = k64 - 2 * (k0 + j) >= 2;  // both k halves
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_f16(dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
+                       kk > 0 ? 1u : more);
+          if (both) {
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_f16(dt, ad0 + off + kk * (2048 / 16), bd0 + off + kk * 2, idesc,
-                         kk > 0 ? 1u : more);
-            if (both) {
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                tc_mma_f16(dt, ad0 + off + (2 * BOX_BYTES + kk * 2048) / 16,
-                           bd0 + off + C::B_HALF / 16 + kk * 2, idesc, 1u);
-            }
-            tc_commit(&empty[s]);
+              tc_mma_f16(dt, ad0 + off + (2 * BOX_BYTES + kk * 2048) / 16,
+                         bd0 + off + C::B_HALF / 16 + kk * 2, idesc, 1u);
           }
-          __syncwarp();
-          if (++s == C::STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+          tc_commit(&empty[s]);
         }
-        if (elect_one()) tc_commit(&tfull[acc]);
         __syncwarp();
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1u;
+        if (++s == C::STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
-        i += n;
+      }
+      if (elect_one()) tc_commit(&tfull[acc]);
+      __syncwarp();
+      if (++acc == ACCS) {
+        acc = 0;
+        aph ^= 1u;
       }
     };
-    phase(r1, d / 64, make_idesc_bf16_f32(BM, C::N1, true, false));
-    if (!dead) phase(r2, f / 64, make_idesc_bf16_f32(BM, C::N2, true, false));
+    int qi = 0;
+    uint32_t qph = 0;
+    while (!dead) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&qfull[qi], qph, kWaitLimitNs))) {
+        dead = true;
+        break;
+      }
+      const int v = queue[qi];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[qi]);
+      if (++qi == QUEUE) {
+        qi = 0;
+        qph ^= 1u;
+      }
+      if (v < 0) break;
+      if (v < c1.units) {
+        const int k0 = v / c1.blocks * c1.per;
+        run(k0, min(c1.per, c1.len - k0), d / 64, make_idesc_bf16_f32(BM, C::N1, true, false));
+      } else {
+        const int i0 = (v - c1.units) / c2.blocks * c2.per, i1 = min(c2.len, i0 + c2.per);
+        for (int i = i0; i < i1 && !dead;) {
+          const int j = i % len2, n = min(len2 - j, i1 - i);
+          run(j, n, f / 64, make_idesc_bf16_f32(BM, C::N2, true, false));
+          i += n;
+        }
+      }
+    }
     // nothing this thread issued may still run when tensor memory is freed
     if (elect_one()) tc_commit(drain);
     __syncwarp();
@@ -669,37 +743,35 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);
-      if (++acc == 2) {
+      if (++acc == ACCS) {
         acc = 0;
         aph ^= 1u;
       }
     };
-    // Joins block `blk` of range r (steps [a, b)) that this CTA holds a part
-    // v of: true for the last CTA to arrive, with the sum in v.
-    float* part = p.part;
-    auto join = [&](const Range& r, int a, int b, uint32_t* ctr, uint32_t mask, float (&v)[TP]) {
-      const int c0 = r.owner(a), c1 = r.owner(b - 1);
-      // a CTA's part of the block its range starts in comes first, of the one
-      // it ends in second
-      auto slice = [&](int c) { return part + (c * 2 + (c > c0 ? 0 : 1)) * TP * BM + col; };
-      float* mine = slice(cta);
+    // Joins a block of `chunks` chunks, of which v is chunk j's sum; parts: the
+    // first one's. True for the last CTA to arrive, with the block's sum in v.
+    auto join = [&](float* parts, int chunks, int j, uint32_t* ctr, uint32_t mask,
+                    float (&v)[TP]) {
+      float* mine = parts + static_cast<size_t>(j) * TP * BM + col;
 #pragma unroll
       for (int t = 0; t < TP; ++t)
         if ((mask >> t) & 1u) __stcg(mine + t * BM, v[t]);
       bar_epi();
-      if (tid == 128) *s_last = add_acq_rel(ctr, 1) == static_cast<uint32_t>(c1 - c0) ? 1u : 0u;
+      if (tid == 128) *s_last = add_acq_rel(ctr, 1) == static_cast<uint32_t>(chunks) - 1 ? 1u : 0u;
       bar_epi();
       const bool last = *s_last != 0;
       if (last) {
 #pragma unroll
         for (int t = 0; t < TP; ++t) v[t] = 0.f;
-        for (int cb = c0; cb <= c1; cb += C::CB) {
+        for (int cb = 0; cb < chunks; cb += C::CB) {
           float o[C::CB][TP];
+          const float* from = parts + static_cast<size_t>(cb) * TP * BM + col;
 #pragma unroll
           for (int q = 0; q < C::CB; ++q)
 #pragma unroll
             for (int t = 0; t < TP; ++t)
-              o[q][t] = cb + q <= c1 && ((mask >> t) & 1u) ? __ldcg(slice(cb + q) + t * BM) : 0.f;
+              o[q][t] = cb + q < chunks && ((mask >> t) & 1u) ? __ldcg(from + (q * TP + t) * BM)
+                                                              : 0.f;
 #pragma unroll
           for (int q = 0; q < C::CB; ++q)
 #pragma unroll
@@ -708,15 +780,29 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
       }
       return last;
     };
-    {
-      const int end = r1.start(cta + 1);
-      for (int i = r1.start(cta); i < end;) {
-        const int u = i / r1.len, a = u * r1.len, b = a + r1.len, stop = min(b, end);
+    int qi = 0;
+    uint32_t qph = 0;
+    while (true) {
+      // (four warps meet at barriers below: a wait that runs out ends none of
+      // them before the others, the queue being one for all)
+      if (!mbar_wait(&qfull[qi], qph, kWaitLimitNs)) dead = true;
+      const int unit = ptx::bar_and(2, 128, !dead) ? queue[qi] : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&qempty[qi]);
+      if (++qi == QUEUE) {
+        qi = 0;
+        qph ^= 1u;
+      }
+      if (unit < 0) break;
+      if (unit < c1.units) {
+        const int j = unit / c1.blocks, u = unit - j * c1.blocks;
         const int slot = u / FB, fb = u - slot * FB;
         const uint32_t mask = smask[slot];
         float v[TP];
         take(v, 1);
-        if ((i == a && stop == b) || join(r1, a, b, p.tiles + u, mask, v)) {
+        if (c1.chunks == 1 ||
+            join(p.part + static_cast<size_t>(u) * c1.chunks * TP * BM, c1.chunks, j, p.tiles + u,
+                 mask, v)) {
           const int c = fb * BM + col;
           if (c < f) {
             __nv_bfloat16* hr = p.h + static_cast<size_t>(slot) * C::HR * f + c;
@@ -735,36 +821,33 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
           bar_epi();
           if (tid == 128) add_release(p.sync + SYNC_H, 1);
         }
-        i = stop;
-      }
-    }
-    part += static_cast<size_t>(grid) * 2 * TP * BM;
-    {
-      const int end = r2.start(cta + 1), blk = nslots * r2.len;
-      for (int i = r2.start(cta); i < end;) {
-        const int db = i / blk, a = db * blk, b = a + blk, begin = i, stop = min(b, end);
+      } else {
+        const int w = unit - c1.units, j = w / c2.blocks, db = w - j * c2.blocks;
+        const int i0 = j * c2.per, i1 = min(c2.len, i0 + c2.per);
         float o[TP];
 #pragma unroll
         for (int t = 0; t < TP; ++t) o[t] = 0.f;
-        while (i < stop) {
-          const int u = i / r2.len, slot = u - db * nslots, e = sexp[slot];
+        for (int i = i0; i < i1;) {
+          const int slot = i / len2, e = sexp[slot];
           // lane t holds token t's weight for this expert
           float wt = 0.f;
           if (lane < T)
-            for (int j = 0; j < k; ++j)
-              if (ridx[lane * k + j] == e) wt = rw[lane * k + j];
+            for (int q = 0; q < k; ++q)
+              if (ridx[lane * k + q] == e) wt = rw[lane * k + q];
           const uint32_t mask = smask[slot];
           float v[TP];
           take(v, 2);
 #pragma unroll
           for (int t = 0; t < TP; ++t) {
-            const float w = __shfl_sync(0xffffffffu, wt, t);
-            if ((mask >> t) & 1u) o[t] = fmaf(w, v[t], o[t]);
+            const float wv = __shfl_sync(0xffffffffu, wt, t);
+            if ((mask >> t) & 1u) o[t] = fmaf(wv, v[t], o[t]);
           }
-          i = min((u + 1) * r2.len, stop);
+          i = min((slot + 1) * len2, i1);
         }
         const uint32_t all = T >= 32 ? 0xffffffffu : (1u << T) - 1u;
-        if ((begin == a && stop == b) || join(r2, a, b, p.tiles + nslots * FB + db, all, o)) {
+        float* parts = p.part + (static_cast<size_t>(2) * want + static_cast<size_t>(db) * c2.chunks) *
+                                    TP * BM;
+        if (c2.chunks == 1 || join(parts, c2.chunks, j, p.tiles + nslots * FB + db, all, o)) {
           const int c = db * BM + col;
           if (c < d) {
 #pragma unroll
@@ -787,6 +870,7 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
     // the last CTA out leaves the counters zero for the next launch
     if (add_acq_rel(p.sync + SYNC_EXIT, 1) == static_cast<uint32_t>(grid) - 1) {
       p.sync[SYNC_GATE] = 0;
+      p.sync[SYNC_CLAIM] = 0;
       p.sync[SYNC_ROUTE] = 0;
       p.sync[SYNC_H] = 0;
       p.sync[SYNC_EXIT] = 0;
@@ -842,7 +926,8 @@ FewLayout few_layout(int T, int d, int E, int k, int f) {
   L.tiles = take(L.ntiles * 4);
   L.h_rows = slots * 2 * TP;
   L.h = take(L.h_rows * f * 2);
-  L.part = take(static_cast<size_t>(2) * kFewMaxCtas * 2 * TP * fw::BM * 4);
+  // two phases of fewer than 2 x CTAs x units partial sums
+  L.part = take(static_cast<size_t>(4) * kFewMaxCtas * fw::UNITS * TP * fw::BM * 4);
   L.total = o;
   return L;
 }
