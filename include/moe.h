@@ -315,9 +315,10 @@ MOE_API int moe_forward(const moe_config_t* cfg, const void* x, const void* W_g,
  * else MOE_ERR_UNSUPPORTED. gemm_tile_n and x_perm_mode have no effect.
  * Arguments as moe_forward. ws: >= moe_forward_few_workspace_size bytes (0
  * for a configuration it refuses), 256-byte aligned, zeroed once before its
- * first use; calls that share one must not overlap. No atomics on values:
- * bitwise reproducible. The kernel's blocks wait on one another (a
- * cooperative launch, one block per SM). It can be captured into a graph. */
+ * first use and again after a MOE_ERR_TIMEOUT; calls that share one must not
+ * overlap. No atomics on values: bitwise reproducible. The kernel's blocks
+ * wait on one another (a cooperative launch, one block per SM). It can be
+ * captured into a graph. */
 #define MOE_FEW_MAX_TOKENS 32
 MOE_API size_t moe_forward_few_workspace_size(const moe_config_t* cfg);
 MOE_API int moe_forward_few(const moe_config_t* cfg, const void* x, const void* W_g,
@@ -482,7 +483,9 @@ typedef struct moe_mx4_config {
 
 /* Sizes in bytes (0 for an invalid configuration): the rows' scales, the
  * weights' scales, and the workspace of the two calls that take one (an
- * error word and the product's split sums; zero it once before first use). */
+ * error word and the product's split sums; 256-byte aligned; zero it once
+ * before its first use and again after a MOE_ERR_TIMEOUT; calls that share
+ * one must not overlap). */
 MOE_API size_t moe_mx4_row_scale_size(const moe_mx4_config_t* cfg);
 MOE_API size_t moe_mx4_weight_scale_size(const moe_mx4_config_t* cfg);
 MOE_API size_t moe_mx4_workspace_size(const moe_mx4_config_t* cfg);
