@@ -401,21 +401,33 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
 // rows x 256 columns on a pair of CTAs (cta_group::2: each stages its own 128
 // rows and half of the columns, so a byte staged feeds twice the products);
 // persistent. A stage of the TMA ring holds 256 values of k: the rows' and
-// the weights' codes (128-byte rows, 128-byte swizzle, both k-major) and
-// their scale chunks (of a pair's columns: all of them, on both sides). One
-// thread copies a stage's scales to tensor memory (tcgen05.cp, the 512 bytes
-// of a chunk to 4 columns of each of the four lane quarters) and issues the
-// products of 128 columns x K 64 that read them; the scales have columns of
-// their own per stage, so a stage's copy never meets a product still reading.
-// Three accumulators of 128 columns: a tile takes two, and the next tile
-// starts once the epilogue has drained one of them.
+// the weights' codes (128-byte rows, 128-byte swizzle, both k-major; a warp
+// loads each) and their scale chunks (of a pair's columns: all of them, on
+// both sides). One thread copies a stage's scales to tensor memory
+// (tcgen05.cp, the 512 bytes of a chunk to 4 columns of each of the four lane
+// quarters) and issues the products of 128 columns x K 64 that read them; the
+// scales have a ring of columns of their own, one stage shorter than the
+// data's (tensor memory's most), so a stage's copy never meets a product still
+// reading. Three accumulators of 128 columns: a tile takes two, and the next
+// tile starts once one of them is drained, with the first half's products of
+// its first stages. Eight warps drain: into registers, which frees the
+// accumulator, and then to out.
+//
+// Bound: a product takes the tensor core 64 clocks whatever its columns' split
+// (one of 256 columns: 128), so a pair's stage 514, 9.5 PFLOP/s in all. Dense
+// 8192 x 8192 x 8192 in bf16: 148 us, 7.4 PFLOP/s (171 with the accumulators
+// freed after the stores by four warps that wrote a sector of each row at a
+// time, one loading warp and five stages: of a stage's 790 clocks 100 went to
+// accumulators not yet drained and 150 to the issuing loop). 16384 skewed rows
+// of 32 experts, 7168 x 2048 to fp32: 109 us (116), where 445 MB move and 632
+// tiles over 76 pairs leave the last of nine waves two thirds empty.
 namespace mx {
 constexpr int BN = 256, HN = 128, KS = 256;  // a tile's columns, an accumulator's, a stage's k
 constexpr int B_BOX = 64 * 128;             // a box of 64 columns
 constexpr int A_BYTES = 128 * 128;
 constexpr int SF_COL = 384, SF_STAGE = 24;  // tensor memory columns: 3 x 128, then scales
 constexpr int TMEM_COLS = 512, ACCS = 3;
-constexpr int THREADS = 256;
+constexpr int EPI_THREADS = 256, THREADS = 128 + EPI_THREADS;
 
 template <bool PAIR>
 struct Cfg {
@@ -423,12 +435,13 @@ struct Cfg {
   static constexpr int B_BYTES = (PAIR ? 128 : 256) * 128;
   static constexpr int OFF_B = A_BYTES, OFF_SFA = OFF_B + B_BYTES, OFF_SFB = OFF_SFA + 2 * CHUNK;
   static constexpr int STAGE = OFF_SFB + 4 * CHUNK;
-  static constexpr int STAGES = PAIR ? 5 : 4;  // (tensor memory's and shared memory's most)
+  static constexpr int STAGES = PAIR ? 6 : 4;  // (shared memory's most)
+  static constexpr int SLOTS = STAGES < 5 ? STAGES : 5;  // of scales (tensor memory's most)
   static constexpr int OFF_BAR = STAGES * STAGE;
   static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
   static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(STAGE % 1024 == 0 && SMEM <= 227 * 1024, "shared memory");
-  static_assert(SF_COL + STAGES * SF_STAGE <= TMEM_COLS, "tensor memory");
+  static_assert(SF_COL + SLOTS * SF_STAGE <= TMEM_COLS && STAGES - SLOTS <= 1, "tensor memory");
 };
 
 struct Params {
@@ -447,42 +460,50 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int m, int n, uint32_t sf) {
   return (sf << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
          (static_cast<uint32_t>(m >> 7) << 27) | (sf << 29);
 }
+// Operand descriptors: the low word holds the address, the high one does not
+// change (128-byte swizzle, 8-row groups 1024 bytes apart, version 1).
+constexpr uint32_t AB_HI = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t SF_HI = (128 >> 4) | 1u << 14;  // no swizzle, 8-row groups 128 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+
 template <bool PAIR>
-__device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b,
-                                         uint32_t idesc, uint32_t sfa, uint32_t sfb,
-                                         uint32_t accumulate) {
+__device__ __forceinline__ void mma_mxf4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, "
         "[%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(AB_HI)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, "
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, "
         "[%4], [%5], p;\n\t}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(AB_HI)
         : "memory");
 }
 // 32 rows of 16 bytes, contiguous, to 4 columns of all four lane quarters
-// (of a pair: in each CTA from its own shared memory). The descriptor: no
-// swizzle, 8-row groups 128 bytes apart, version 1.
-__device__ __forceinline__ uint64_t scales_desc(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-         (static_cast<uint64_t>(128 >> 4) << 32) | (static_cast<uint64_t>(1) << 46);
-}
+// (of a pair: in each CTA from its own shared memory).
 template <bool PAIR>
-__device__ __forceinline__ void cp_scales(uint32_t taddr, uint64_t desc) {
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t desc) {
   if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t}\n" ::"r"(taddr),
+        "r"(desc), "r"(SF_HI)
+        : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}\n" ::"r"(taddr),
+        "r"(desc), "r"(SF_HI)
+        : "memory");
 }
 template <bool PAIR>
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -491,7 +512,9 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
   else
     tc_commit(bar);
 }
-__device__ __forceinline__ void bar_epi() { asm volatile("barrier.cta.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void bar_epi() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+}
 
 struct Tile {
   int e, row0, rows, mt, n0, n;
@@ -567,7 +590,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     }
     for (int i = 0; i < ACCS; ++i) {
       mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], PAIR ? 8 : 4);
+      mbar_init(&tempty[i], PAIR ? 16 : 8);
     }
     mbar_init(drain, 1);
     *s_wide = 0;
@@ -630,8 +653,10 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     }
   };
 
-  if (warp == 0) {
-    // (the whole warp, converged: elect_one says why)
+  if (warp == 0 || warp == 2) {
+    // the first loads the rows, the other the weights (the whole warp,
+    // converged: elect_one says why)
+    const bool a_side = warp == 0;
     if (lane == 0) {
       prefetch_tmap(&tmA);
       prefetch_tmap(&tmA32);
@@ -688,16 +713,19 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         if (used < STAGES) ++used;
         if (elect_one()) {
           uint8_t* st = smem + s * C::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
+          if (a_side) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
+            if (na > 0) {
+              load2(st, ma, kb * 128, row0);
+              load3(st + C::OFF_SFA, &tmSA, 0, kb * 2, mt);
+            }
+          } else {
 #pragma unroll
-          for (int b = 0; b < (PAIR ? 2 : 4); ++b)
-            if (b < nb)
-              load2(st + C::OFF_B + b * B_BOX, &tmB, kb * 128, col0 + b * (PAIR ? HN : 64));
-          if (na > 0) {
-            load2(st, ma, kb * 128, row0);
-            load3(st + C::OFF_SFA, &tmSA, 0, kb * 2, mt);
+            for (int b = 0; b < (PAIR ? 2 : 4); ++b)
+              if (b < nb)
+                load2(st + C::OFF_B + b * B_BOX, &tmB, kb * 128, col0 + b * (PAIR ? HN : 64));
+            load3(st + C::OFF_SFB, &tmSB, 0, kb * 2, sbt);
           }
-          load3(st + C::OFF_SFB, &tmSB, 0, kb * 2, sbt);
         }
         __syncwarp();
         if (++s == STAGES) {
@@ -709,7 +737,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     });
     // the latest use of each stage has landed before this CTA may exit (a
     // pair: the even CTA's barrier counts both, and both exit together)
-    for (int j = 0; rank == 0 && j < used; ++j) {
+    for (int j = 0; a_side && rank == 0 && j < used; ++j) {
       if (s == 0) {
         s = STAGES;
         ph ^= 1u;
@@ -722,21 +750,41 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     }
     if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
-    // (the whole warp, converged: elect_one says why)
+    // (one lane issues: elect_one says how)
     if (rank == 0) {
-      int s = 0, acc = 0;
+      int s = 0, acc = 0, slot = 0;
       uint32_t ph = 0, aph = 0;
       bool dead = false;
+      constexpr int LEAD = C::SLOTS - 1;
       const uint32_t base0 = smem_u32(smem);
-      const uint64_t ad0 = make_sdesc_sw128(base0, 16, 1024),
-                     bd0 = make_sdesc_sw128(base0 + C::OFF_B, 16, 1024),
-                     sa0 = scales_desc(base0 + C::OFF_SFA), sb0 = scales_desc(base0 + C::OFF_SFB);
+      const uint32_t ad0 = desc_lo(base0), bd0 = desc_lo(base0 + C::OFF_B),
+                     sa0 = desc_lo(base0 + C::OFF_SFA), sb0 = desc_lo(base0 + C::OFF_SFB);
       constexpr int B_HALF = (PAIR ? 1 : 2) * B_BOX;
       const uint32_t id0 = idesc_mxf4(BM, HN, 0), id2 = idesc_mxf4(BM, HN, 2);
-      // one stage's scales and products (inlined with constants for a whole one)
-      auto stage = [&](int chunks, int steps, int nj, uint32_t d0, uint32_t d1, uint32_t more) {
+      // the stage, and the slot its scales go to, whose last products were
+      // SLOTS steps ago, are there
+      auto take = [&] {
+        const bool last = s + 1 == STAGES;
+        if (mbar_wait_spin(&full[s], ph, kWaitLimitNs) &&
+            (C::SLOTS == STAGES ||
+             mbar_wait_spin(&empty[last ? 0 : s + 1], last ? ph : ph ^ 1u, kWaitLimitNs))) {
+          tc_fence_after();
+          return true;
+        }
+        return false;
+      };
+      auto next = [&] {
+        if (++slot == C::SLOTS) slot = 0;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      };
+      // a stage's scales, and its products for the halves j0..j1 of the
+      // columns (inlined with constants for whole stages)
+      auto scales = [&](int chunks, int nj) {
         const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
-        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
+        const uint32_t sf = tmem_base + SF_COL + slot * SF_STAGE;
 #pragma unroll
         for (int c = 0; c < chunks; ++c) {
           cp_scales<PAIR>(sf + c * 4, sa0 + off + c * (CHUNK / 16));
@@ -745,53 +793,79 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
             cp_scales<PAIR>(sf + 8 + c * 8 + j * 4,
                             sb0 + off + (2 * j + c) * (CHUNK / 16));
         }
+      };
+      auto products = [&](int steps, int j0, int j1, uint32_t d0, uint32_t d1, uint32_t more) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t sf = tmem_base + SF_COL + slot * SF_STAGE;
 #pragma unroll
         for (int kk = 0; kk < steps; ++kk)
 #pragma unroll
-          for (int j = 0; j < nj; ++j)
+          for (int j = j0; j < j1; ++j)
             mma_mxf4<PAIR>(j == 0 ? d0 : d1, ad0 + off + kk * 2,
                            bd0 + off + j * (B_HALF / 16) + kk * 2, (kk & 1) ? id2 : id0,
                            sf + (kk >> 1) * 4, sf + 8 + (kk >> 1) * 8 + j * 4,
                            kk > 0 ? 1u : more);
       };
-      walk([&](int t, int k0, int k1) {
+      if (elect_one()) walk([&](int t, int k0, int k1) {
         const int n = tile_at<BM>(t, seg, base, tb, E, N).n;
         const int nj = n > HN ? 2 : 1;
         const int acc1 = acc + 1 == ACCS ? 0 : acc + 1;
         const uint32_t aph1 = acc + 1 == ACCS ? aph ^ 1u : aph;
-        bool ready = mbar_wait_spin_cluster(&tempty[acc], aph ^ 1u, kWaitLimitNs);
-        if (nj == 2 && ready)
-          ready = mbar_wait_spin_cluster(&tempty[acc1], aph1 ^ 1u, kWaitLimitNs);
-        if (!__all_sync(0xffffffffu, ready)) {
+        if (!mbar_wait_spin_cluster(&tempty[acc], aph ^ 1u, kWaitLimitNs)) {
           dead = true;
           return false;
         }
         tc_fence_after();
         const uint32_t d0 = tmem_base + acc * HN, d1 = tmem_base + acc1 * HN;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!__all_sync(0xffffffffu, mbar_wait_spin(&full[s], ph, kWaitLimitNs))) {
+        const int whole = nj == 2 ? K / KS : 0;  // stages with nothing left out
+        int kb = k0;
+        if (nj == 2) {
+          // until the second accumulator is drained too: the first half's
+          // products of a few stages, and after that the second's
+          const int s0 = s, slot0 = slot, most = min(min(k1, whole), k0 + LEAD);
+          const uint32_t ph0 = ph;
+          while (kb < most && !mbar_test_wait_cluster(&tempty[acc1], aph1 ^ 1u)) {
+            if (!take()) {
+              dead = true;
+              return false;
+            }
+            scales(2, 2);
+            products(4, 0, 1, d0, d1, kb > k0 ? 1u : 0u);
+            next();
+            ++kb;
+          }
+          if (!mbar_wait_spin_cluster(&tempty[acc1], aph1 ^ 1u, kWaitLimitNs)) {
+            dead = true;
+            return false;
+          }
+          tc_fence_after();
+          s = s0;
+          ph = ph0;
+          slot = slot0;
+          for (int i = k0; i < kb; ++i) {
+            products(4, 1, 2, d0, d1, i > k0 ? 1u : 0u);
+            commit<PAIR>(&empty[s]);
+            next();
+          }
+        }
+        for (; kb < k1; ++kb) {
+          if (!take()) {
             dead = true;
             break;
           }
-          tc_fence_after();
           const uint32_t more = kb > k0 ? 1u : 0u;
-          const int left = K - kb * KS;
-          if (elect_one()) {
-            if (left >= KS && nj == 2)
-              stage(2, 4, 2, d0, d1, more);
-            else
-              stage(left > 128 ? 2 : 1, min(4, left / 64), nj, d0, d1, more);
-            commit<PAIR>(&empty[s]);
+          if (kb < whole) {
+            scales(2, 2);
+            products(4, 0, 2, d0, d1, more);
+          } else {
+            scales(K - kb * KS > 128 ? 2 : 1, nj);
+            products(min(4, K / 64 - kb * 4), 0, nj, d0, d1, more);
           }
-          __syncwarp();
-          if (++s == STAGES) {
-            s = 0;
-            ph ^= 1u;
-          }
+          commit<PAIR>(&empty[s]);
+          next();
         }
         for (int j = 0; j < nj; ++j) {
-          if (elect_one()) commit<PAIR>(&tfull[acc]);
-          __syncwarp();
+          commit<PAIR>(&tfull[acc]);
           if (++acc == ACCS) {
             acc = 0;
             aph ^= 1u;
@@ -799,6 +873,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         }
         return !dead;
       });
+      dead = __any_sync(0xffffffffu, dead);
       if (elect_one()) {
         if constexpr (PAIR)
           tc_commit_pair_mc(drain, 0x1);
@@ -809,33 +884,57 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
       if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
     }
   } else if (warp >= 4) {
-    const int w = warp & 3;
+    // two warps to a quarter of the rows, 64 of an accumulator's columns each
+    const int w = warp & 3, half = (warp - 4) >> 2;
     int acc = 0;
     uint32_t aph = 0;
     bool dead = false;
     TO* out = static_cast<TO*>(p.out);
     const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
     auto finish = [&](float v) { return p.silu ? mx_silu(v) : v; };
-    // 32 columns of a row from a lane's registers, whole sectors a store
+    // 32 columns of up to 32 rows, a row to a lane, to out: neighbouring lanes
+    // exchange 32-byte pieces first, so that a store instruction writes
+    // contiguous runs of 128 bytes (fp32; bf16: 64), not a sector of each row
     const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
-    auto put32 = [&](size_t row, int col, const uint32_t (&r)[32]) {
-      TO* o = out + row * N + col;
-      constexpr int PER = 32 / sizeof(TO);
+    auto put32 = [&](size_t row0, int rows, int col, const uint32_t (&r)[32]) {
+      constexpr int PER = 32 / sizeof(TO), NC = 32 / PER;  // a piece's columns, a row's pieces
+      uint32_t v[NC][8];
 #pragma unroll
-      for (int j = 0; j < 32; j += PER) {
-        uint32_t v[8];
+      for (int c = 0; c < NC; ++c) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           if constexpr (sizeof(TO) == 4) {
-            v[i] = __float_as_uint(finish(__uint_as_float(r[j + i])));
+            v[c][i] = __float_as_uint(finish(__uint_as_float(r[c * PER + i])));
           } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(
-                finish(__uint_as_float(r[j + 2 * i])), finish(__uint_as_float(r[j + 2 * i + 1])));
-            v[i] = *reinterpret_cast<const uint32_t*>(&h);
+            const __nv_bfloat162 h =
+                __floats2bfloat162_rn(finish(__uint_as_float(r[c * PER + 2 * i])),
+                                      finish(__uint_as_float(r[c * PER + 2 * i + 1])));
+            v[c][i] = *reinterpret_cast<const uint32_t*>(&h);
           }
         }
-        st_sector(sectors, o + j, v);
       }
+      // a transposition within groups of NC lanes: v[i] is then piece `lane %
+      // NC` of the group's row i
+#pragma unroll
+      for (int m = 1; m < NC; m <<= 1) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          if (c & m) continue;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const bool up = lane & m;
+            const uint32_t got =
+                __shfl_xor_sync(0xffffffffu, up ? v[c][i] : v[c | m][i], m);
+            v[c][i] = up ? got : v[c][i];
+            v[c | m][i] = up ? v[c | m][i] : got;
+          }
+        }
+      }
+      const int g = lane & ~(NC - 1);
+      TO* o = out + (row0 + g) * N + col + (lane - g) * PER;
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+        if (g + i < rows) st_sector(sectors, o + static_cast<size_t>(i) * N, v[i]);
     };
     walk([&](int t, int k0, int k1) {
       const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
@@ -854,29 +953,18 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         if (!dead && !mbar_wait(&tfull[acc], aph, kWaitLimitNs)) dead = true;
         dead = __any_sync(0xffffffffu, dead);
         tc_fence_after();
-        if (rows > 0) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < min(HN, tl.n - h); c0 += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(
-                tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN + c0, r);
-            tmem_ld_wait();
-            if (lane < rows) {
-              if (whole) {
-                put32(static_cast<size_t>(tl.row0 + r0 + lane), tl.n0 + h + c0, r);
-              } else {
-                // (at most kMx4SplitRows rows: the first warp's)
-                uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * BN + h + c0);
+        const int col = h + half * 64;
+        const bool some = rows > 0 && col < tl.n;
+        uint32_t r[2][32];
+        if (some) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 8) {
-                  const uint32_t v[8] = {r[j],     r[j + 1], r[j + 2], r[j + 3],
-                                         r[j + 4], r[j + 5], r[j + 6], r[j + 7]};
-                  st_sector(true, o + j, v);
-                }
-              }
-            }
-          }
+          for (int i = 0; i < 2; ++i)
+            tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN +
+                                   half * 64 + i * 32,
+                               r[i]);
+          tmem_ld_wait();
         }
+        // free before the stores: the next tile waits for this one's first half
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -884,6 +972,22 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
             mbar_arrive_remote(leader_tempty + acc * 8);
           else
             mbar_arrive(&tempty[acc]);
+        }
+        if (some && whole) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            put32(static_cast<size_t>(tl.row0 + r0), rows, tl.n0 + col + i * 32, r[i]);
+        } else if (some && lane < rows) {
+          // (at most kMx4SplitRows rows: the first quarter's)
+          uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * BN + col);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              const uint32_t v[8] = {r[i][j],     r[i][j + 1], r[i][j + 2], r[i][j + 3],
+                                     r[i][j + 4], r[i][j + 5], r[i][j + 6], r[i][j + 7]};
+              st_sector(true, o + i * 32 + j, v);
+            }
         }
         if (++acc == ACCS) {
           acc = 0;
@@ -903,7 +1007,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         if (*s_last != 0) {
           __threadfence();
           const int quads = tl.n / 4;
-          for (int i = tid - 128; i < tl.rows * quads; i += 128) {
+          for (int i = tid - 128; i < tl.rows * quads; i += EPI_THREADS) {
             const int row = i / quads, col = (i - row * quads) * 4;
             float4 v = {0.f, 0.f, 0.f, 0.f};
             for (int cb = first; cb <= last_cta; cb += 8) {

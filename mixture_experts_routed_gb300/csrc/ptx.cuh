@@ -216,11 +216,11 @@ __device__ __forceinline__ void tc_mma_f16(uint32_t d_tmem, uint64_t adesc, uint
 }
 
 // One lane of a converged warp (always the same): true for it alone. A loop
-// that issues tensor-core products or TMA copies runs converged and enters
-// the issuing branch by this election: their operands then are values of the
-// whole warp. From a loop inside a one-lane branch each product took about
-// 130 clocks to issue (the 4-bit product of 8192^3: 534 us so, 349 us with
-// lane-predicated instructions, 209 us elected).
+// that issues tensor-core products or TMA copies enters the issuing branch by
+// this election, or runs inside such a branch: the operands then are values
+// of the whole warp. From a loop inside a branch on the lane's number each
+// product took about 130 clocks to issue (the 4-bit product of 8192^3: 534 us
+// so, 349 us with lane-predicated instructions, 209 us elected).
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile(
