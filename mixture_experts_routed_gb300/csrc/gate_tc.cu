@@ -238,6 +238,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (timed_out && err != nullptr) atomicOr(err, kErrTimeout);
   __syncthreads();  // the ring is idle: reuse it for the logits tile
+  // the peer's too, before this CTA writes to it: its operands would be
+  // overwritten, or its copies land on the partial sums
+  if (ksplit == 2) cluster_sync();
   // ksplit = 2: CTA `part` finishes rows [64 part, 64 part + 64); its partial
   // sums of the other half go straight into the peer's tile at row r ^ 64
   // (the rows the peer does not finish itself) with remote stores
