@@ -1284,38 +1284,6 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
   return r == CUDA_SUCCESS;
 }
 
-// 2-D map over row-major [rows, cols] bytes, box [box_rows][128 bytes].
-bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
-                       uint32_t box_rows) {
-  auto enc = get_encode();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {cols, rows};
-  const cuuint64_t strides[1] = {cols};
-  const cuuint32_t box[2] = {128, box_rows};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
-// 3-D map over [tiles][groups] chunks of 512 bytes, box [box_tiles][2].
-bool make_map_3d_chunks(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t groups,
-                        uint32_t box_tiles) {
-  auto enc = get_encode();
-  if (!enc) return false;
-  const cuuint64_t dims[3] = {128, groups, tiles};
-  const cuuint64_t strides[2] = {512, groups * 512};
-  const cuuint32_t box[3] = {128, 2, box_tiles};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims,
-                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 // 2-D map over the row-major [rows, cols] output, box [32 rows][32 cols]:
 // fp32 (128-byte rows, 128-byte swizzle) for the fp32 pass, bf16 (64-byte
 // rows, 64-byte swizzle) for the SiLU pass, matching the staging blocks.
