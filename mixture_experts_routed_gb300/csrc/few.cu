@@ -31,9 +31,9 @@
 // In phase 2 the routing weights are applied as each expert's accumulator is
 // read.
 //
-// Measured: 7 tokens, 8 experts of 4096 x 11008, two chosen: 163 us, 7.7 TB/s
-// of weights (a plain copy of this GPU: 6.8); one token, 256 experts of
-// 7168 x 2048, eight chosen: 85 us, 5.6 TB/s; two of 64 experts of
+// Measured: 7 tokens, 8 experts of 4096 x 11008, two chosen: 179 us with the
+// weights out of L2, 7.0 TB/s (163 over and over); one token, 256 experts of
+// 7168 x 2048, eight chosen: 87 us, 5.4 TB/s; two of 64 experts of
 // 2048 x 1408: 18.6 us, where the chain gate -> router -> W1 -> W2 and its
 // four hand-overs between CTAs bound it, not the 3.4 us of bytes.
 //

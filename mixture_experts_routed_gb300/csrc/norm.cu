@@ -30,8 +30,8 @@
 // waits for its own copies only, so the ring needs no barrier) and reads
 // them as often as the sums in between require, while the next rows are on
 // their way. Loads into registers instead left too little in flight beside
-// the column sums and weights (16384 x 5120 forward: 173 us; 8191 x 7168
-// backward: 250 us).
+// the column sums and weights (16384 x 5120 forward: 173 us, now 109, 6.1
+// TB/s; 8191 x 7168 backward: 250 us, now 174, 4.7 TB/s).
 #include <cstdint>
 #include <type_traits>
 
