@@ -308,7 +308,11 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
 // Microscaled 4-bit rows and expert weights, and their grouped product.
 constexpr int kMx4MaxCtas = 160;    // the grid the product's partial sums are sized for
 constexpr int kMx4SplitRows = 32;   // a split launch's rows per expert, at most
-constexpr int kMx4PairRows = 128;   // rows per expert, on average, from which pairs of CTAs work
+// Rows per expert, on average, from which pairs of CTAs work, in tiles of 256
+// rows (one CTA: 128). One CTA and pairs at 128 rows each: 25.9 and 34.8 us (64
+// experts of 2048 x 1408), 40.6 and 44.6 (8 of 4096 x 11008); skewed, 16 of
+// 7168 x 2048, 34.8 and 30.8. At 256: 35.0 and 37.9, 49.3 and 48.0; 41.6 and 38.5.
+constexpr int kMx4PairRows = 192;
 // Row tiles (128 rows of one expert) that R rows of E experts can make.
 size_t mx4_row_tiles(int R, int E);
 cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,
