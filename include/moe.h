@@ -407,8 +407,9 @@ MOE_API int moe_backward(const moe_config_t* cfg, const void* x, const void* W_g
  *                                                   block's input)
  * Either half may be left out: b = NULL leaves out the post half (out is x;
  * alpha, beta and the gate are not used), w_pre = NULL the pre half. n is
- * taken from the fp32 out, before its rounding; sums are fp32. A row whose
- * sum of squares passes the fp32 range has rstd 0. */
+ * taken from the fp32 out, before its rounding; sums are fp32. A finite row
+ * whose sum of squares passes the fp32 range has rstd 0: its norm, and what
+ * comes back through it, is 0. */
 enum {
   MOE_GATE_NONE = 0,    /* g = 1 */
   MOE_GATE_TOKEN = 1,   /* gate [T] fp32 */

@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kFwdVecs, WARP 
           f2 v[H];
           widen2<T>(in[nvec + i], v);
 #pragma unroll
-          for (int q = 0; q < H; ++q) v[q] = mul2(v[q], wb[j][q]);
+          for (int q = 0; q < H; ++q) v[q] = mul2(v[q], scale);  // (first: scale may be 0)
           if (elem) {
             f2 g[H];
             widen2<T>(in[2 * nvec + i], g);
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(WARP ? kWarpBlock : kRowVecs / kFwdVecs, WARP 
             for (int q = 0; q < H; ++q) v[q] = mul2(v[q], g[q]);
           }
 #pragma unroll
-          for (int q = 0; q < H; ++q) y[j][q] = fma2(scale, v[q], mul2(alpha, y[j][q]));
+          for (int q = 0; q < H; ++q) y[j][q] = fma2(v[q], wb[j][q], mul2(alpha, y[j][q]));
           store2<T>(out + at + i * N, y[j]);
         }
         if constexpr (PRE) {
@@ -446,9 +446,12 @@ __device__ __forceinline__ void round_half(uint4& r, int half, const f2 (&v)[Vec
 // column sums (of dw_pre; of dw_post, or A of a channel gate) in registers,
 // written once to part[group][2][d]; reduce_columns adds the groups in
 // order. Factors that a row shares (rstd, beta, a token gate) are taken out
-// of the per-element terms. The first sum of a row is taken a row ahead of
-// the rest; S rows are in the ring, each part of a slot filled again as soon
-// as its row is done with it.
+// of the per-element terms, in an order in which no square or cube of rstd
+// stands alone: it is up to 1 / sqrt(eps) where the row is all but zero, and
+// its cube passes the range at rows of 1e13 and at an eps of 1e-26. A row with
+// rstd 0 (its sum of squares passed the range) is zeroed in the ring. The
+// first sum of a row is taken a row ahead of the rest; S rows are in the ring,
+// each part of a slot filled again as soon as its row is done with it.
 // A thread takes one vector, half by half: its sums and weights are 32
 // registers, and what a half needs fits beside them at 28 warps to the SM
 // (two vectors at 14 warps: 201 us for the 8191 x 7168 backward).
@@ -539,6 +542,15 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
       widen_half<T>(in[off_x + nvec], h, v);
     }
   };
+  // what a row with rstd 0 has in its norm counts as 0 (each thread reads its
+  // own columns only)
+  auto drop = [&](uint4* in, const Stats& st) {
+    if (POST && st.rb == 0.f && mine) in[off_b] = uint4{};
+    if (PRE && st.ro == 0.f && mine) {
+#pragma unroll
+      for (int q = 0; q <= P; ++q) in[off_x + q * nvec] = uint4{};
+    }
+  };
   const f2 al = dup2(POST ? a.alpha : 1.f);
   // a row's part of mean(v y), and its terms of dw_pre
   auto first = [&](const uint4* in, const Stats& st) {
@@ -581,20 +593,21 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
   Stats now = fetch(group), next = fetch(group + step);
   float s1 = 0.f;
   ptx::cp_async_wait<S - 1>();  // the first row
+  if (group < a.T) drop(slots, now);
   if (PRE && group < a.T)
     s1 = row_sums<WARP>(float2{first(slots, now), 0.f}, buf, turn).x;
   int slot = 0;
   for (int t = group; t < a.T; t += step) {
     uint4* in = slots + slot * size;
     slot = slot + 1 == S ? 0 : slot + 1;
-    const uint4* in_next = slots + slot * size;
+    uint4* in_next = slots + slot * size;
     const size_t at = static_cast<size_t>(t) * d + tid * N;
     const Stats after = fetch(t + 2 * step);
     const float k = now.gt * a.beta * now.rb;
-    // D = dout + ro v - ro yh mean(v yh), dx = alpha D and, of the branch, D w
+    // D = dout + ro (v - yh mean(v yh)), dx = alpha D and, of the branch, D w
     f2 v2[H], ss = 0;
     if (mine) {
-      const float c = now.ro * now.ro * now.ro * s1 * inv_d;
+      const float c = now.ro * s1 * inv_d * now.ro;  // (ro s1 / d is the mean)
       const f2 r2 = dup2(now.ro), cx = dup2(-c * (POST ? a.alpha : 1.f)), cu = dup2(-c * k),
                k2 = dup2(k);
       const uint4 dr = in[0];
@@ -621,9 +634,9 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
           half_dn(in, h, v);
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
-            D[q] = fma2(y[q], cx, D[q]);
-            if constexpr (POST) D[q] = fma2(u[q], cu, D[q]);
-            D[q] = fma2(mul2(v[q], wn[h * Q + q]), r2, D[q]);
+            v[q] = fma2(y[q], cx, mul2(v[q], wn[h * Q + q]));
+            if constexpr (POST) v[q] = fma2(u[q], cu, v[q]);
+            D[q] = fma2(v[q], r2, D[q]);
           }
         }
         f2 o[Q];
@@ -634,11 +647,12 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
 #pragma unroll
           for (int q = 0; q < Q; ++q) {
             ss = fma2(D[q], u[q], ss);
+            bb[q] = mul2(bb[q], k2);
             if constexpr (ELEM) {
-              o[q] = mul2(mul2(D[q], k2), mul2(bb[q], wb[h * Q + q]));
+              o[q] = mul2(D[q], mul2(bb[q], wb[h * Q + q]));
               D[q] = mul2(D[q], g[q]);
             }
-            apost[h * Q + q] = fma2(mul2(D[q], k2), bb[q], apost[h * Q + q]);
+            apost[h * Q + q] = fma2(D[q], bb[q], apost[h * Q + q]);
             v2[h * Q + q] = mul2(D[q], wb[h * Q + q]);
           }
           if constexpr (ELEM) round_half<T>(og, h, o);
@@ -650,6 +664,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
     fill_rest(t + S * step, in);  // (of this row only b is read again)
     ptx::cp_async_wait<S - 2>();  // the next row
     const float2 f = un2(ss);
+    if (t + step < a.T) drop(in_next, next);
     const float ahead = t + step < a.T ? first(in_next, next) : 0.f;
     const float2 sums = row_sums<WARP>(float2{ahead, f.x + f.y}, buf, turn);
     s1 = sums.x;
@@ -657,7 +672,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
       // sum of D w b: beta rb of it is a token gate's gradient
       if (token && tid == 0) static_cast<float*>(dgate)[t] = a.beta * now.rb * sums.y;
       if (mine) {
-        const f2 kv = dup2(k), kb = dup2(-k * now.rb * now.rb * sums.y * inv_d);
+        const f2 kv = dup2(k), mb = dup2(-(now.rb * sums.y * inv_d) * now.rb);
         const uint4 brr = in[off_b];
         uint4 o;
 #pragma unroll
@@ -665,7 +680,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == kWarpBlock ? 4 : 1)
           f2 bb[Q];
           widen_half<T>(brr, h, bb);
 #pragma unroll
-          for (int q = 0; q < Q; ++q) bb[q] = fma2(kv, v2[h * Q + q], mul2(kb, bb[q]));
+          for (int q = 0; q < Q; ++q) bb[q] = mul2(kv, fma2(mb, bb[q], v2[h * Q + q]));
           round_half<T>(o, h, bb);
         }
         *reinterpret_cast<uint4*>(db + at) = o;
