@@ -447,7 +447,8 @@ MOE_API int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const vo
  * element gate); those of a half left out, and dgate without a gate, are
  * NULL. ws: >= moe_block_norm_backward_workspace_size bytes (0 for an
  * invalid configuration), 256-byte aligned; no zeroing. Two kernels, no
- * atomics: bitwise reproducible. T = 0 zeroes the weights' gradients. */
+ * atomics: bitwise reproducible. T = 0 zeroes the weights' gradients; the
+ * tensors of T rows, empty then, may be NULL. */
 MOE_API size_t moe_block_norm_backward_workspace_size(const moe_norm_config_t* cfg);
 MOE_API int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout,
                    const float* dn, const void* x, const void* b, const float* w_post,

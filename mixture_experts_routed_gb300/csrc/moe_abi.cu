@@ -934,8 +934,10 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
   if (ws == nullptr || !aligned(ws, kAlign) || (!post && !pre)) return MOE_ERR_INVALID_ARG;
   if ((pre ? !ok_ptr(dw_pre) : dw_pre != nullptr) || (post ? !ok_ptr(dw_post) : dw_post != nullptr))
     return MOE_ERR_INVALID_ARG;
-  if (gated ? (dgate == nullptr || !aligned(dgate, c.gate == MOE_GATE_TOKEN ? 4 : 16))
-            : dgate != nullptr)
+  // (with no rows a token or element gate's gradient is empty, and may be null)
+  if (gated && (c.T > 0 || c.gate == MOE_GATE_CHANNEL)
+          ? (dgate == nullptr || !aligned(dgate, c.gate == MOE_GATE_TOKEN ? 4 : 16))
+          : !gated && dgate != nullptr)
     return MOE_ERR_INVALID_ARG;
   // (a channel gate's gradients read the weight and the gate, rows or none)
   if ((post && !ok_ptr(w_post)) || (post && c.gate == MOE_GATE_CHANNEL && !ok_ptr(gate)))
