@@ -255,8 +255,23 @@ def forward_few(c, x, Wg, bias, W1, W2, *, ws, out=None, noise=None, stream=None
     """The whole layer for at most MOE_FEW_MAX_TOKENS tokens, in one kernel. ``ws``: a
     "few" workspace."""
     cc = config_from(c)
+    T, d, E, f, dt = cc.T, cc.d, cc.E, cc.f, _ndt(cc)
     if out is None:
-        out = torch.empty((cc.T, cc.d), dtype=torch.bfloat16, device=x.device)
+        out = torch.empty((T, d), dtype=dt, device=x.device)
+    # every tensor of the call's shape and type (named only where one is not: a decode step's
+    # call costs what its kernel does)
+    soft = cc.router == L.MOE_ROUTER_SOFT_GUMBEL
+    if not (x.shape == out.shape == (T, d) and Wg.shape == (d, E) and W1.shape == (E, d, f)
+            and W2.shape == (E, f, d) and dt is x.dtype is Wg.dtype is W1.dtype is W2.dtype
+            and out.dtype is dt
+            and (bias is None or bias.shape == (E,) and bias.dtype is torch.float32)) or soft:
+        for name, t, shape, of in (
+                ("x", x, (T, d), dt), ("Wg", Wg, (d, E), dt), ("bias", bias, (E,), torch.float32),
+                ("W1", W1, (E, d, f), dt), ("W2", W2, (E, f, d), dt), ("out", out, (T, d), dt),
+                ("noise", noise if soft else None, (T, E), torch.float32)):
+            if t is not None and (t.shape != shape or t.dtype is not of):
+                raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {tuple(t.shape)} {t.dtype}, not "
+                                                      f"{shape} {of}")
     st = L.load().moe_forward_few(ctypes.byref(cc), _p(x), _p(Wg), _p(bias), _p(noise), _p(W1),
                                   _p(W2), _p(out), _p(ws), ws.nbytes, _s(stream))
     _check(st, "moe_forward_few")
