@@ -430,8 +430,9 @@ typedef struct moe_norm_config {
 /* x, b [T, d]; w_post, w_pre [d] fp32; gate as cfg->gate says. Outputs:
  * out [T, d] (NULL without the post half), n [T, d] (NULL without the pre
  * half), rstd_post, rstd_pre [T] fp32 (what the backward reads; nullable).
- * Outputs may not overlap inputs or one another. Every tensor pointer but
- * the [T] ones is 16-byte aligned. */
+ * Outputs may not overlap inputs or one another (MOE_ERR_INVALID_ARG; the
+ * backward's likewise). Every tensor pointer but the [T] ones is 16-byte
+ * aligned. */
 MOE_API int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b,
                    const float* w_post, const void* gate, const float* w_pre, void* out,
                    void* n, float* rstd_post, float* rstd_pre, void* stream);

@@ -583,6 +583,32 @@ int check_norm(const moe_norm_config_t* c) {
   return c->d > 65536 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// Bytes of memory that a call reads or writes (p null: none).
+struct Span {
+  const void* p;
+  size_t n;
+};
+// No output overlaps an input or another output.
+template <size_t O, size_t I>
+bool apart(const Span (&out)[O], const Span (&in)[I]) {
+  auto meet = [](const Span& a, const Span& b) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+    return a.p != nullptr && b.p != nullptr && pa < pb + b.n && pb < pa + a.n;
+  };
+  for (size_t i = 0; i < O; ++i) {
+    for (const Span& b : in)
+      if (meet(out[i], b)) return false;
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return false;
+  }
+  return true;
+}
+size_t gate_bytes(const moe_norm_config_t& c) {
+  const size_t T = c.T, d = c.d;
+  return c.gate == MOE_GATE_TOKEN ? T * 4
+                                  : (c.gate == MOE_GATE_CHANNEL ? d * 4 : T * d * elem_size(c.dtype));
+}
+
 // The halves' tensors go together.
 bool norm_args_ok(const moe_norm_config_t& c, const void* x, const void* b, const float* w_post,
                   const void* gate, const float* w_pre) {
@@ -909,6 +935,12 @@ int moe_block_norm(const moe_norm_config_t* cfg, const void* x, const void* b, c
   if (!norm_args_ok(c, x, b, w_post, gate, w_pre) || (b != nullptr ? !ok_ptr(out) : out != nullptr) ||
       (w_pre != nullptr ? !ok_ptr(n) : n != nullptr))
     return MOE_ERR_INVALID_ARG;
+  const size_t rows = static_cast<size_t>(c.T) * c.d * elem_size(c.dtype), t4 = c.T * size_t(4),
+               d4 = c.d * size_t(4);
+  const void* g = b != nullptr && c.gate != MOE_GATE_NONE ? gate : nullptr;
+  if (!apart({{out, rows}, {n, rows}, {rstd_post, t4}, {rstd_pre, t4}},
+             {{x, rows}, {b, rows}, {w_post, d4}, {w_pre, d4}, {g, gate_bytes(c)}}))
+    return MOE_ERR_INVALID_ARG;
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_block_norm(c.dtype, c.gate, c.eps, c.alpha, c.beta, c.T, c.d, x, b,
@@ -950,6 +982,15 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
       return MOE_ERR_INVALID_ARG;
   }
   if (ws_bytes < moe_block_norm_backward_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t rows = static_cast<size_t>(c.T) * c.d * elem_size(c.dtype), t4 = c.T * size_t(4),
+               d4 = c.d * size_t(4);
+  if (c.T > 0 && !apart({{dx, rows}, {db, rows}, {dw_post, d4}, {dgate, gate_bytes(c)}, {dw_pre, d4},
+                         {ws, moe_block_norm_backward_workspace_size(cfg)}},
+                        {{dout, rows}, {dn, static_cast<size_t>(c.T) * d4}, {pre ? x : nullptr, rows},
+                         {b, rows}, {w_post, d4}, {gated ? gate : nullptr, gate_bytes(c)},
+                         {w_pre, d4}, {post ? rstd_post : nullptr, t4},
+                         {pre ? rstd_pre : nullptr, t4}}))
+    return MOE_ERR_INVALID_ARG;
   // (with no rows b may be null: what is left out goes by the weights)
   const void* bp = post && b == nullptr ? static_cast<const void*>(w_post) : b;
   return status_of(launch_block_norm_bwd(c.dtype, c.gate, c.eps, c.alpha, c.beta, c.T, c.d, dout,
