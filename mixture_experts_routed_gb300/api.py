@@ -439,7 +439,7 @@ def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_
     """Gradients after a ``block_norm`` of the same inputs: ``dout`` is the gradient that
     reaches its out by the residual, ``dn`` (fp32) the one of n, ``rstd_post`` and
     ``rstd_pre`` what it kept. ``y``: without ``b``, the x that was normed; with it, the
-    forward's out, which is not read (``rstd_pre`` has what stands in for it). dx, db, an
+    forward's out or None: it is not read (``rstd_pre`` has what stands in for it). dx, db, an
     element gate's dgate in the config's type; dw_post, dw_pre and the other dgate fp32; None
     for what the forward left out."""
     T, d, f32 = c.T, c.d, torch.float32
@@ -450,6 +450,8 @@ def block_norm_backward(c, dout, dn, y, b, w_post, gate, w_pre, rstd_post, rstd_
         if not isinstance(rstd_pre, KeptNorm):
             raise MoEError(L.MOE_ERR_INVALID_ARG,
                            "rstd_pre of a forward with both halves is the KeptNorm it returned")
+        if y is not None and (y.shape != td or y.dtype is not dt):
+            raise MoEError(L.MOE_ERR_INVALID_ARG, f"y is {tuple(y.shape)} {y.dtype}, not {td} {dt}")
         rstd_pre, y = rstd_pre
     pd = _shaped("dout", dout, td, dt)
     g = {"dx": torch.empty_like(dout), "db": torch.empty_like(dout) if post else None,
