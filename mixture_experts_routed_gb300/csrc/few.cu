@@ -225,6 +225,10 @@ __device__ __forceinline__ void weigh_all(const float* row, int E, const RouterS
 struct Cut {
   int blocks, len, per, chunks, units;
   __device__ Cut(int blocks_, int len_, int want) : blocks(blocks_), len(len_) {
+    if (len == 0) {  // no token has an expert
+      per = chunks = units = 0;
+      return;
+    }
     per = max(UNIT_STEPS, (blocks * len + want - 1) / want);
     chunks = per >= len ? 1 : (len + per - 1) / per;
     per = (len + chunks - 1) / chunks;
