@@ -291,7 +291,7 @@ cudaError_t launch_block_norm_bwd(int dtype, int gate_kind, float eps, float alp
 
 // ---------------------------------------------------------------- few.cu
 // The whole layer for a few tokens (T <= kFewMaxTokens, bf16) in one
-// cooperative kernel. Its four counters live in the workspace's first block
+// cooperative kernel. Its five counters live in the workspace's first block
 // at kFewSyncOffset and are zero between launches.
 constexpr int kFewMaxTokens = 32;
 constexpr int kFewMaxCtas = 160;  // the grid the partial sums are sized for
