@@ -814,10 +814,12 @@ __global__ void __launch_bounds__(fw::THREADS, 1)
             for (int t = 0; t < TP; ++t)
               if ((mask >> t) & 1u) {
                 const float z = v[t], hv = z / (1.f + expf(-z));
-                const __nv_bfloat16 hi = __float2bfloat16_rn(hv);
+                // (past bf16's range hi is cut off, and of an infinity lo is 0)
+                __nv_bfloat16 hi = __float2bfloat16_rn(hv);
+                if (__hisinf(hi)) hi = __float2bfloat16_rz(hv);
                 hr[static_cast<size_t>(t) * f] = hi;
                 hr[static_cast<size_t>(TP + t) * f] =
-                    __float2bfloat16_rn(hv - __bfloat162float(hi));
+                    __float2bfloat16_rn(isinf(hv) ? 0.f : hv - __bfloat162float(hi));
               }
           }
           // h is read by other CTAs' TMA copies
