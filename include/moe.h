@@ -516,7 +516,8 @@ MOE_API int moe_mx4_product(const moe_mx4_config_t* cfg, const uint8_t* q, const
                    void* out, void* ws, size_t ws_bytes, void* stream);
 
 /* The values codes and scales stand for (exact in both types): W [E, K, N],
- * rows [R, K]. */
+ * rows [R, K]. Offsets that fall or leave [0, R] write no rows (and, these calls
+ * having no workspace, flag nothing: moe_mx4_quantize_rows did). */
 MOE_API int moe_mx4_dequantize_weights(const moe_mx4_config_t* cfg, const uint8_t* wq,
                    const uint8_t* w_scale, void* W, void* stream);
 MOE_API int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* q,

@@ -569,7 +569,8 @@ def mx4_dequantize_weights(c, wq, w_scale, *, W=None, stream=None):
 
 
 def mx4_dequantize_rows(c, q, scale, offsets, *, x=None, stream=None):
-    """The values of quantised rows, [R, K] (rows outside the segments are not written)."""
+    """The values of quantised rows, [R, K] (rows outside the segments are not written, and with
+    offsets that fall or leave [0, R] none is)."""
     lib, r = L.load(), ctypes.byref(c)
     R, K = c.R, c.K
     if x is None:

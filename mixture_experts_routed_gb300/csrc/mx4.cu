@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
         return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * BN;
       };
       for (int h = 0; h < tl.n; h += HN) {
-        // after a wait that ran out the loops go on, so that the four warps
+        // after a wait that ran out the loops go on, so that the eight warps
         // still meet at every barrier
         if (!dead && !mbar_wait(&tfull[acc], aph, kWaitLimitNs)) dead = true;
         dead = __any_sync(0xffffffffu, dead);
