@@ -397,6 +397,15 @@ MOE_API int moe_backward(const moe_config_t* cfg, const void* x, const void* W_g
                  float* dW_g, float* dbias, float* dW1, float* dW2, void* ws,
                  size_t ws_bytes, void* stream);
 
+/* The same with a gradient of the logits from elsewhere added to the
+ * router's, before it goes on to x, W_g and the bias: dlogits [T, E] fp32
+ * (moe_router_loss_backward's), 4-byte aligned. */
+MOE_API int moe_backward_with_dlogits(const moe_config_t* cfg, const void* x, const void* W_g,
+                 const float* bias, const float* noise, const void* W1, const void* W2,
+                 const void* fwd_ws, size_t fwd_ws_bytes, const void* dout,
+                 const float* dlogits, float* dx, float* dW_g, float* dbias, float* dW1,
+                 float* dW2, void* ws, size_t ws_bytes, void* stream);
+
 /* ---- norms around a block -----------------------------------------------
  * (No counterpart on the source pages: the expert layer's neighbours in a
  * transformer block.) Root-mean-square norms before and after a block, fused
@@ -522,6 +531,169 @@ MOE_API int moe_mx4_dequantize_weights(const moe_mx4_config_t* cfg, const uint8_
                    const uint8_t* w_scale, void* W, void* stream);
 MOE_API int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* q,
                    const uint8_t* scale, const int32_t* offsets, void* x, void* stream);
+
+/* ---- 8-bit expert products, forward and backward ------------------------------
+ * (The source pages quantise what is exchanged; here both sides of the
+ * products are, and of their gradients.) E4M3 codes (largest 448) with one
+ * power-of-two scale, a byte s, for each block of 128:
+ *   s - 127 = the least e >= -127 with amax <= 448 2^e; s = 127 for a block
+ *   of zeros, 255 (which stands for NaN) for one with an infinity or a NaN;
+ *   code = E4M3(v / 2^(s - 127)), to nearest even (nothing saturates).
+ * Rows: blocks of 128 along a row; codes [R, C], scales [R, pitch] bytes,
+ * pitch = ceil(C / 128) rounded up to 4 (the padding is not read). Columns:
+ * blocks of 128 rows of one expert, whose segment is cut into tiles of 128
+ * from its start, one expert after the other; codes [tile * 128 + row, C],
+ * zeros past a segment's end, scales [tile, C]. Weights: blocks of 128 x 128
+ * of each W[e]; codes [E, K, N] as W lies, scales [E, ceil(K / 128),
+ * ceil(N / 128)]: the one copy serves the product and its transpose. C is K
+ * (rows of x) or N (rows of dy). Code pointers are 16-byte aligned, the
+ * scales of rows and columns 4-byte. */
+typedef struct moe_fp8_config {
+  int32_t R;         /* routed rows, 0..2^24 */
+  int32_t K;         /* W's rows (the product's contraction), multiple of 64, at most 65536 */
+  int32_t N;         /* W's columns, multiple of 64, at most 65536 */
+  int32_t E;         /* experts, 1..256 (1: a plain linear layer, offsets {0, R}) */
+  int32_t dtype;     /* MOE_DTYPE_*: x, z, W and what the dequantisers write */
+  int32_t out_dtype; /* MOE_DTYPE_*: the products' output (weight gradients are fp32) */
+  int32_t silu;      /* 1: the product ends in SiLU (the W1 pass); else 0 */
+  int32_t x_rows;    /* rows of x where quantised rows are gathered, >= 0 */
+} moe_fp8_config_t;
+
+/* What is quantised, x or a function of it */
+enum {
+  MOE_ACT_NONE = 0,      /* x */
+  MOE_ACT_SILU = 1,      /* SiLU(x): the rows of the second product from the
+                          * first one's pre-activation */
+  MOE_ACT_SILU_GRAD = 2  /* x SiLU'(z): what goes back past the activation */
+};
+
+/* Sizes (0 for an invalid configuration): bytes of the scales of rows of
+ * `cols` columns; rows of a columns' code tensor (a multiple of 128; its
+ * scales have a 128th of them); bytes of the weights' scales; bytes of the
+ * workspace (an error word and split sums; 256-byte aligned; zero it once
+ * before its first use and again after a MOE_ERR_TIMEOUT; calls that share
+ * one must not overlap). */
+MOE_API size_t moe_fp8_row_scale_size(const moe_fp8_config_t* cfg, int32_t cols);
+MOE_API size_t moe_fp8_column_rows(const moe_fp8_config_t* cfg);
+MOE_API size_t moe_fp8_weight_scale_size(const moe_fp8_config_t* cfg);
+MOE_API size_t moe_fp8_workspace_size(const moe_fp8_config_t* cfg);
+
+/* Expert weights W [E, K, N] (dtype) -> wq, w_scale. */
+MOE_API int moe_fp8_quantize_weights(const moe_fp8_config_t* cfg, const void* W, uint8_t* wq,
+                   uint8_t* w_scale, void* stream);
+
+/* Rows of x (dtype, `cols` = K or N columns) -> rows (q, scale), columns (cq,
+ * cscale) or both in one pass; the form left out is NULL. Row r of the
+ * layout is x[r], or x[src[r]] with src (x then has x_rows rows), times
+ * row_weight[r] (fp32 [R]; NULL: 1) and through `act` (MOE_ACT_*; z [R, cols]
+ * with MOE_ACT_SILU_GRAD, else NULL), all in fp32. Rows outside [offsets[0],
+ * offsets[E]) are not touched. A src outside [0, x_rows) gives a row of zeros,
+ * offsets that fall or leave [0, R] give nothing, and both flag
+ * MOE_ERR_BAD_INDEX. Outputs may not overlap inputs or one another
+ * (MOE_ERR_INVALID_ARG, as in every call here). */
+MOE_API int moe_fp8_quantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const void* x,
+                   const int32_t* src, const float* row_weight, int32_t act, const void* z,
+                   const int32_t* offsets, uint8_t* q, uint8_t* scale, uint8_t* cq,
+                   uint8_t* cscale, void* ws, size_t ws_bytes, void* stream);
+
+/* transposed 0: out[r] = rows q[r] . wq[e], q of K columns, out [R, N] (then
+ * SiLU with cfg->silu); 1: out[r] = q[r] . wq[e]^T, q of N columns, out [R, K]
+ * (the gradient of the product's rows; cfg->silu must be 0:
+ * MOE_ERR_UNSUPPORTED), for the rows of each expert e's segment. fp32 sums,
+ * rounded to out_dtype. Offsets that fall or leave [0, R] write nothing and
+ * flag MOE_ERR_BAD_INDEX; rows of no segment are not written. Bitwise
+ * reproducible. */
+MOE_API int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8_t* q,
+                   const uint8_t* scale, const uint8_t* wq, const uint8_t* w_scale,
+                   const int32_t* offsets, void* out, void* ws, size_t ws_bytes,
+                   void* stream);
+
+/* dW[e] = sum over expert e's rows of x[r]^T dy[r], fp32 [E, K, N], from the
+ * columns of x and of dy made for the same offsets; zeros for an expert
+ * without rows. Bad offsets as above. Bitwise reproducible. */
+MOE_API int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq,
+                   const uint8_t* x_scale, const uint8_t* dyq, const uint8_t* dy_scale,
+                   const int32_t* offsets, float* dW, void* ws, size_t ws_bytes, void* stream);
+
+/* The values codes and scales stand for (exact in both types but for bf16's
+ * subnormal numbers): W [E, K, N], rows [R, cols]. */
+MOE_API int moe_fp8_dequantize_weights(const moe_fp8_config_t* cfg, const uint8_t* wq,
+                   const uint8_t* w_scale, void* W, void* stream);
+MOE_API int moe_fp8_dequantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const uint8_t* q,
+                   const uint8_t* scale, void* x, void* stream);
+
+/* ---- the router's losses -----------------------------------------------------
+ * (No counterpart on the source pages, which measure the experts' load and
+ * leave its training to others.) Over the tokens t of sequence s that count
+ * (n_s of them, of which c_se chose expert e):
+ *   p_t = softmax(L_t)  f_se = E c_se / (k n_s)  P_se = sum_t p_te / n_s
+ *   balance = sum_s sum_e f_se P_se / S'    over the S' sequences with n_s > 0
+ *   z       = sum_t lse_t^2 / N             lse_t = log sum_e exp(L_te)
+ *   loss    = cfg->balance * balance + cfg->z * z
+ * One sequence (S = 1) makes it the loss of the batch. The counts are
+ * constants to the gradient. */
+typedef struct moe_router_loss_config {
+  int32_t T;     /* tokens, 0..2^26 */
+  int32_t E;     /* experts, 1..256 */
+  int32_t k;     /* experts per token, 1..min(E, 16) */
+  int32_t S;     /* sequences, 1..2^20 */
+  float balance; /* coefficients, finite */
+  float z;
+} moe_router_loss_config_t;
+
+/* Workspace bytes (0 for an invalid configuration); 256-byte aligned; zero it
+ * once before its first use; calls that share one must not overlap. */
+MOE_API size_t moe_router_loss_workspace_size(const moe_router_loss_config_t* cfg);
+
+/* logits [T, E] fp32 and topk_idx [T, k] as moe_route gives them. seq_offsets
+ * [S + 1]: sequence s is the tokens [seq_offsets[s], seq_offsets[s + 1]); NULL
+ * (S = 1 only): all T. mask [T] bytes, 0 for a token that does not count;
+ * NULL: all do. Tokens of no sequence do not count, and neither their logits
+ * nor those of masked tokens are read.
+ * Outputs: loss [3] (the loss, balance, z; 0 with no token), counts [S, E]
+ * (c), tokens [S + 2] (n_s, then S' and N), lse [T] (0 where masked; not
+ * written for tokens of no sequence). Offsets that fall or leave [0, T] write
+ * nothing, an expert id outside [0, E) is not counted, and both flag
+ * MOE_ERR_BAD_INDEX. Bitwise reproducible. */
+MOE_API int moe_router_loss(const moe_router_loss_config_t* cfg, const float* logits,
+                   const int32_t* topk_idx, const int32_t* seq_offsets, const uint8_t* mask,
+                   float* loss, int32_t* counts, int32_t* tokens, float* lse, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* dlogits [T, E] fp32 = dloss * the gradient of loss[0] (dloss: one fp32 on the
+ * device; NULL: 1), 0 for tokens that do not count. logits, seq_offsets, mask:
+ * the forward's; counts, tokens, lse: what it wrote. */
+MOE_API int moe_router_loss_backward(const moe_router_loss_config_t* cfg, const float* logits,
+                   const int32_t* seq_offsets, const uint8_t* mask, const int32_t* counts,
+                   const int32_t* tokens, const float* lse, const float* dloss,
+                   float* dlogits, void* stream);
+
+/* ---- dropout of a block's branch ---------------------------------------------
+ * (No counterpart on the source pages: the block around the layer.)
+ *   out = residual + keep x / (1 - p')     dx = keep dout / (1 - p')
+ * The mask is drawn again wherever it is needed and never stored: element i
+ * (of T d) takes 16 bits of Philox 4x32 with ten rounds (Salmon et al., SC
+ * 2011), counter (i / 8 low, i / 8 high, site, step), key the 64-bit seed, word
+ * (i % 8) / 2, its low half for an even i; it is kept where those bits are at
+ * least thr = min(round(65536 p), 65535), and p' = thr / 65536. */
+typedef struct moe_dropout_config {
+  int32_t T;     /* rows, 0..2^24 */
+  int32_t d;     /* row length, multiple of 64, at most 65536 */
+  int32_t dtype; /* MOE_DTYPE_*: x, residual, out, dout, dx */
+  int32_t site;  /* which of a model's dropouts this is, >= 0 */
+  float p;       /* share that is dropped, 0 <= p < 1 */
+} moe_dropout_config_t;
+
+/* state: two int64 in device memory, the seed and the step (its low 32 bits
+ * are used), read by the kernel, so that a captured graph draws anew when
+ * they change; 8-byte aligned. residual may be NULL (none). out may be x or
+ * residual itself; other overlaps are MOE_ERR_INVALID_ARG. A dropped element
+ * is the residual alone, whatever x holds there. The residual's gradient is
+ * dout. The backward takes the forward's config and state. */
+MOE_API int moe_dropout(const moe_dropout_config_t* cfg, const void* x, const void* residual,
+                   const int64_t* state, void* out, void* stream);
+MOE_API int moe_dropout_backward(const moe_dropout_config_t* cfg, const void* dout,
+                   const int64_t* state, void* dx, void* stream);
 
 /* ---- errors --------------------------------------------------------------
  * moe_get_device_error synchronises `stream`, reads the workspace error

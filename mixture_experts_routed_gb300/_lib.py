@@ -30,6 +30,9 @@ MOE_GATE_NONE = 0
 MOE_GATE_TOKEN = 1
 MOE_GATE_CHANNEL = 2
 MOE_GATE_ELEMENT = 3
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_SILU_GRAD = 2
 
 
 class MoeConfig(ctypes.Structure):
@@ -51,6 +54,21 @@ class MoeNormConfig(ctypes.Structure):
 class MoeMx4Config(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("R", "K", "N", "E", "dtype", "out_dtype", "silu", "x_rows")]
+
+
+class MoeFp8Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("R", "K", "N", "E", "dtype", "out_dtype", "silu", "x_rows")]
+
+
+class MoeRouterLossConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "E", "k", "S")] + \
+               [(n, ctypes.c_float) for n in ("balance", "z")]
+
+
+class MoeDropoutConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("T", "d", "dtype", "site")] + \
+               [("p", ctypes.c_float)]
 
 
 class MoeForwardViews(ctypes.Structure):
@@ -105,6 +123,24 @@ PROTOTYPES = {
     "moe_block_norm": (_I, [_P] * 11),
     "moe_block_norm_backward_workspace_size": (_SZ, [_P]),
     "moe_block_norm_backward": (_I, [_P] * 16 + [_SZ, _P]),
+    "moe_backward_with_dlogits": (_I, [_CFG, _P, _P, _P, _P, _P, _P, _P, _SZ, _P, _P, _P, _P, _P,
+                                       _P, _P, _P, _SZ, _P]),
+    "moe_fp8_row_scale_size": (_SZ, [_P, ctypes.c_int32]),
+    "moe_fp8_column_rows": (_SZ, [_P]),
+    "moe_fp8_weight_scale_size": (_SZ, [_P]),
+    "moe_fp8_workspace_size": (_SZ, [_P]),
+    "moe_fp8_quantize_weights": (_I, [_P] * 5),
+    "moe_fp8_quantize_rows": (_I, [_P, ctypes.c_int32, _P, _P, _P, ctypes.c_int32] + [_P] * 7 +
+                              [_SZ, _P]),
+    "moe_fp8_product": (_I, [_P, ctypes.c_int32] + [_P] * 7 + [_SZ, _P]),
+    "moe_fp8_weight_grad": (_I, [_P] * 8 + [_SZ, _P]),
+    "moe_fp8_dequantize_weights": (_I, [_P] * 5),
+    "moe_fp8_dequantize_rows": (_I, [_P, ctypes.c_int32] + [_P] * 4),
+    "moe_router_loss_workspace_size": (_SZ, [_P]),
+    "moe_router_loss": (_I, [_P] * 10 + [_SZ, _P]),
+    "moe_router_loss_backward": (_I, [_P] * 10),
+    "moe_dropout": (_I, [_P] * 6),
+    "moe_dropout_backward": (_I, [_P] * 5),
 }
 
 _lib = None

@@ -22,7 +22,12 @@ __all__ = ["MoEError", "make_config", "config_from", "workspace_size", "scratch_
            "few_workspace_size", "norm_config", "KeptNorm", "block_norm",
            "block_norm_backward", "block_norm_workspace_size", "alloc_norm_workspace",
            "mx4_config", "mx4_quantize_weights", "mx4_quantize_rows", "mx4_product",
-           "mx4_dequantize_weights", "mx4_dequantize_rows", "alloc_mx4_workspace"]
+           "mx4_dequantize_weights", "mx4_dequantize_rows", "alloc_mx4_workspace",
+           "fp8_config", "Fp8Rows", "fp8_quantize_weights", "fp8_quantize_rows", "fp8_product",
+           "fp8_weight_grad", "fp8_dequantize_weights", "fp8_dequantize_rows",
+           "alloc_fp8_workspace", "router_loss_config", "RouterLoss", "router_loss",
+           "router_loss_backward", "alloc_router_loss_workspace", "dropout_config", "dropout",
+           "dropout_backward"]
 
 
 class MoEError(RuntimeError):
@@ -278,10 +283,12 @@ def forward_few(c, x, Wg, bias, W1, W2, *, ws, out=None, noise=None, stream=None
     return out
 
 
-def backward(c, x, Wg, bias, W1, W2, dout, *, fwd_ws, ws, noise=None, stream=None) -> dict:
+def backward(c, x, Wg, bias, W1, W2, dout, *, fwd_ws, ws, noise=None, dlogits=None,
+             stream=None) -> dict:
     """Gradients of the layer for dout = dl/dout [T, d] after a forward in
     ``fwd_ws`` on the same inputs: dx [T, d], dWg [d, E], dbias [E], dW1 [E,
-    d, f], dW2 [E, f, d], all fp32. ``ws``: a backward workspace."""
+    d, f], dW2 [E, f, d], all fp32. ``ws``: a backward workspace. ``dlogits`` (fp32 [T, E]): a
+    gradient of the logits from elsewhere (``router_loss_backward``'s), added to the router's."""
     cc = config_from(c)
     dev = x.device
     g = {"dx": torch.empty((cc.T, cc.d), dtype=torch.float32, device=dev),
@@ -289,9 +296,14 @@ def backward(c, x, Wg, bias, W1, W2, dout, *, fwd_ws, ws, noise=None, stream=Non
          "dbias": torch.empty((cc.E,), dtype=torch.float32, device=dev),
          "dW1": torch.empty((cc.E, cc.d, cc.f), dtype=torch.float32, device=dev),
          "dW2": torch.empty((cc.E, cc.f, cc.d), dtype=torch.float32, device=dev)}
-    st = L.load().moe_backward(
+    lib = L.load()
+    call, more = lib.moe_backward, ()
+    if dlogits is not None:
+        call = lib.moe_backward_with_dlogits
+        more = (_shaped("dlogits", dlogits, (cc.T, cc.E), torch.float32),)
+    st = call(
         ctypes.byref(cc), _p(x), _p(Wg), _p(bias), _p(noise), _p(W1), _p(W2), _p(fwd_ws),
-        fwd_ws.numel() * fwd_ws.element_size(), _p(dout), _p(g["dx"]), _p(g["dWg"]),
+        fwd_ws.numel() * fwd_ws.element_size(), _p(dout), *more, _p(g["dx"]), _p(g["dWg"]),
         _p(g["dbias"]), _p(g["dW1"]), _p(g["dW2"]), _p(ws), ws.numel() * ws.element_size(),
         _s(stream))
     _check(st, "moe_backward")
@@ -581,3 +593,249 @@ def mx4_dequantize_rows(c, q, scale, offsets, *, x=None, stream=None):
         _indices("offsets", offsets, c.E + 1), _shaped("x", x, (R, K), _ndt(c)), _s(stream))
     _check(st, "moe_mx4_dequantize_rows")
     return x
+
+
+# ---------------------------------------------------------------- 8-bit expert products
+_ACTS = {None: L.MOE_ACT_NONE, "silu": L.MOE_ACT_SILU, "silu_grad": L.MOE_ACT_SILU_GRAD}
+
+
+def fp8_config(R, K, N, E, dtype="bf16", out_dtype="bf16", silu=0, x_rows=0) -> L.MoeFp8Config:
+    return L.MoeFp8Config(int(R), int(K), int(N), int(E), _DTYPES[dtype], _DTYPES[out_dtype],
+                          int(silu), int(x_rows))
+
+
+def alloc_fp8_workspace(c, device=None) -> torch.Tensor:
+    """Zeroed workspace of the 8-bit calls (one serves any configuration)."""
+    n = int(L.load().moe_fp8_workspace_size(ctypes.byref(c)))
+    if n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+class Fp8Rows(NamedTuple):
+    """Quantised rows [R, C]: codes ``q`` and scales ``scale`` [R, pitch] of blocks of 128 along
+    a row, codes ``cq`` [column rows, C] and scales ``cscale`` of blocks of 128 rows of an
+    expert, all uint8; None for a form that was not asked for."""
+    q: torch.Tensor | None
+    scale: torch.Tensor | None
+    cq: torch.Tensor | None
+    cscale: torch.Tensor | None
+
+
+def _fp8_pitch(cols):
+    return (-(-cols // 128) + 3) // 4 * 4
+
+
+def fp8_quantize_weights(c, W, *, q=None, scale=None, stream=None):
+    """W [E, K, N] -> (codes uint8 [E, K, N], scales uint8 [E, ceil(K / 128), ceil(N / 128)])."""
+    E, K, N = c.E, c.K, c.N
+    blocks = (E, -(-K // 128), -(-N // 128))
+    u8 = torch.uint8
+    if q is None:
+        q = torch.empty((E, K, N), dtype=u8, device=W.device)
+    if scale is None:
+        scale = torch.empty(blocks, dtype=u8, device=W.device)
+    st = L.load().moe_fp8_quantize_weights(ctypes.byref(c), _shaped("W", W, (E, K, N), _ndt(c)),
+                                           _shaped("q", q, (E, K, N), u8),
+                                           _shaped("scale", scale, blocks, u8), _s(stream))
+    _check(st, "moe_fp8_quantize_weights")
+    return q, scale
+
+
+def fp8_quantize_rows(c, x, offsets, *, ws, rows=True, columns=False, src=None, row_weight=None,
+                      act=None, z=None, stream=None) -> Fp8Rows:
+    """Rows x [R, K] or [R, N], or with ``src`` [R] the rows x[src] of x [x_rows, ..], times
+    ``row_weight`` [R], in the forms asked for. ``act``: None, "silu" (of x) or "silu_grad" (x
+    times SiLU'(z), z [R, ..])."""
+    lib, r, u8 = L.load(), ctypes.byref(c), torch.uint8
+    R, C, dt = c.R, x.shape[-1], _ndt(c)
+    if act not in _ACTS:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"act is {act!r}")
+    if C not in (c.K, c.N):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"x has {C} columns, not {c.K} or {c.N}")
+    if not (rows or columns):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "neither rows nor columns asked for")
+    q = scale = cq = cscale = None
+    if rows:
+        q = torch.empty((R, C), dtype=u8, device=x.device)
+        scale = torch.empty((R, _fp8_pitch(C)), dtype=u8, device=x.device)
+    if columns:
+        n = int(lib.moe_fp8_column_rows(r))
+        cq = torch.empty((n, C), dtype=u8, device=x.device)
+        cscale = torch.empty((n // 128, C), dtype=u8, device=x.device)
+    st = lib.moe_fp8_quantize_rows(
+        r, C, _shaped("x", x, (R if src is None else c.x_rows, C), dt), _indices("src", src, R),
+        _shaped("row_weight", row_weight, (R,), torch.float32), _ACTS[act],
+        _shaped("z", z, (R, C), dt), _indices("offsets", offsets, c.E + 1),
+        *[None if t is None else t.data_ptr() for t in (q, scale, cq, cscale)], _p(ws), ws.nbytes,
+        _s(stream))
+    _check(st, "moe_fp8_quantize_rows")
+    return Fp8Rows(q, scale, cq, cscale)
+
+
+def _fp8_weights(c, wq, w_scale):
+    return (_shaped("wq", wq, (c.E, c.K, c.N), torch.uint8),
+            _shaped("w_scale", w_scale, (c.E, -(-c.K // 128), -(-c.N // 128)), torch.uint8))
+
+
+def _need(name, t):
+    if t is None:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} was not quantised in the form this takes")
+    return t
+
+
+def fp8_product(c, rows, wq, w_scale, offsets, *, ws, transposed=False, out=None, stream=None):
+    """out[r] = rows[r] . W[e], [R, N], from rows of K columns; ``transposed``: rows[r] . W[e]^T,
+    [R, K], from rows of N columns."""
+    R, u8 = c.R, torch.uint8
+    length, width = (c.N, c.K) if transposed else (c.K, c.N)
+    odt = torch.float32 if c.out_dtype == L.MOE_DTYPE_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty((R, width), dtype=odt, device=wq.device)
+    st = L.load().moe_fp8_product(
+        ctypes.byref(c), int(transposed), _shaped("rows.q", _need("rows", rows.q), (R, length), u8),
+        _shaped("rows.scale", rows.scale, (R, _fp8_pitch(length)), u8),
+        *_fp8_weights(c, wq, w_scale), _indices("offsets", offsets, c.E + 1),
+        _shaped("out", out, (R, width), odt), _p(ws), ws.nbytes, _s(stream))
+    _check(st, "moe_fp8_product")
+    return out
+
+
+def fp8_weight_grad(c, x, dy, offsets, *, ws, out=None, stream=None):
+    """fp32 dW [E, K, N]: the sum over each expert's rows of x[r]^T dy[r], from the columns of x
+    [R, K] and of dy [R, N]."""
+    lib, r, u8 = L.load(), ctypes.byref(c), torch.uint8
+    E, K, N = c.E, c.K, c.N
+    n = int(lib.moe_fp8_column_rows(r))
+    if out is None:
+        out = torch.empty((E, K, N), dtype=torch.float32, device=_need("x", x.cq).device)
+    st = lib.moe_fp8_weight_grad(
+        r, _shaped("x.cq", _need("x", x.cq), (n, K), u8),
+        _shaped("x.cscale", x.cscale, (n // 128, K), u8),
+        _shaped("dy.cq", _need("dy", dy.cq), (n, N), u8),
+        _shaped("dy.cscale", dy.cscale, (n // 128, N), u8), _indices("offsets", offsets, E + 1),
+        _shaped("out", out, (E, K, N), torch.float32), _p(ws), ws.nbytes, _s(stream))
+    _check(st, "moe_fp8_weight_grad")
+    return out
+
+
+def fp8_dequantize_weights(c, wq, w_scale, *, W=None, stream=None):
+    """The values of quantised weights, [E, K, N]."""
+    if W is None:
+        W = torch.empty((c.E, c.K, c.N), dtype=_ndt(c), device=wq.device)
+    st = L.load().moe_fp8_dequantize_weights(
+        ctypes.byref(c), *_fp8_weights(c, wq, w_scale),
+        _shaped("W", W, (c.E, c.K, c.N), _ndt(c)), _s(stream))
+    _check(st, "moe_fp8_dequantize_weights")
+    return W
+
+
+def fp8_dequantize_rows(c, rows, *, x=None, stream=None):
+    """The values of quantised rows, [R, C], from their ``q`` and ``scale``."""
+    q = _need("rows", rows.q)
+    R, C = c.R, q.shape[-1]
+    if x is None:
+        x = torch.empty((R, C), dtype=_ndt(c), device=q.device)
+    st = L.load().moe_fp8_dequantize_rows(
+        ctypes.byref(c), C, _shaped("rows.q", q, (R, C), torch.uint8),
+        _shaped("rows.scale", rows.scale, (R, _fp8_pitch(C)), torch.uint8),
+        _shaped("x", x, (R, C), _ndt(c)), _s(stream))
+    _check(st, "moe_fp8_dequantize_rows")
+    return x
+
+
+# ---------------------------------------------------------------- the router's losses
+def router_loss_config(T, E, k, S=1, balance=0.01, z=0.0) -> L.MoeRouterLossConfig:
+    """``balance`` and ``z``: the two losses' coefficients."""
+    return L.MoeRouterLossConfig(int(T), int(E), int(k), int(S), float(balance), float(z))
+
+
+def alloc_router_loss_workspace(c, device=None) -> torch.Tensor:
+    n = int(L.load().moe_router_loss_workspace_size(ctypes.byref(c)))
+    if n == 0:
+        raise MoEError(L.MOE_ERR_INVALID_ARG, "workspace size")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+class RouterLoss(NamedTuple):
+    """``loss`` fp32 [3]: the loss, the balance and the z loss without their coefficients;
+    ``counts`` int32 [S, E]: the experts' tokens by sequence. ``tokens`` int32 [S + 2] (by
+    sequence, sequences with any, all) and ``lse`` fp32 [T] are the backward's."""
+    loss: torch.Tensor
+    counts: torch.Tensor
+    tokens: torch.Tensor
+    lse: torch.Tensor
+
+
+def router_loss(c, logits, topk_idx, *, ws, offsets=None, mask=None, stream=None) -> RouterLoss:
+    """The router's losses of logits [T, E] and choices [T, k]. ``offsets`` int32 [S + 1]: the
+    sequences' tokens (None: one of all); ``mask`` [T], bool or uint8: the tokens that count."""
+    T, E, k, S = c.T, c.E, c.k, c.S
+    i32, dev = torch.int32, logits.device
+    r = RouterLoss(torch.empty(3, dtype=torch.float32, device=dev),
+                   torch.empty((S, E), dtype=i32, device=dev),
+                   torch.empty(S + 2, dtype=i32, device=dev),
+                   torch.empty(T, dtype=torch.float32, device=dev))
+    st = L.load().moe_router_loss(
+        ctypes.byref(c), _shaped("logits", logits, (T, E), torch.float32),
+        _shaped("topk_idx", topk_idx, (T, k), i32), _indices("offsets", offsets, S + 1),
+        _mask_p(mask, T), *[t.data_ptr() for t in r], _p(ws), ws.nbytes, _s(stream))
+    _check(st, "moe_router_loss")
+    return r
+
+
+def router_loss_backward(c, logits, kept, *, dloss=None, offsets=None, mask=None, out=None,
+                         stream=None):
+    """fp32 [T, E]: ``dloss`` (fp32 [1]; None: 1) times the gradient of loss[0] by the logits,
+    after a ``router_loss`` of the same inputs that gave ``kept``. What ``backward`` takes as
+    ``dlogits``."""
+    T, E, S, f32 = c.T, c.E, c.S, torch.float32
+    if out is None:
+        out = torch.empty_like(logits)
+    st = L.load().moe_router_loss_backward(
+        ctypes.byref(c), _shaped("logits", logits, (T, E), f32),
+        _indices("offsets", offsets, S + 1), _mask_p(mask, T),
+        _shaped("counts", kept.counts, (S, E), torch.int32),
+        _shaped("tokens", kept.tokens, (S + 2,), torch.int32),
+        _shaped("lse", kept.lse, (T,), f32), _shaped("dloss", dloss, (1,), f32),
+        _shaped("out", out, (T, E), f32), _s(stream))
+    _check(st, "moe_router_loss_backward")
+    return out
+
+
+def _mask_p(mask, T):
+    if mask is not None and (mask.shape != (T,) or mask.dtype not in (torch.bool, torch.uint8)):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"mask is {tuple(mask.shape)} {mask.dtype}, not "
+                                              f"{(T,)} bool or uint8")
+    return _p(mask)
+
+
+# ---------------------------------------------------------------- dropout of a branch
+def dropout_config(T, d, dtype="bf16", p=0.1, site=0) -> L.MoeDropoutConfig:
+    """``site``: which of a model's dropouts this is; each draws a mask of its own."""
+    return L.MoeDropoutConfig(int(T), int(d), _DTYPES[dtype], int(site), float(p))
+
+
+def dropout(c, x, state, *, residual=None, out=None, stream=None):
+    """residual + x dropped and scaled, [T, d]. ``state``: int64 [2] on the GPU, the seed and the
+    step; its values at the time the kernel runs are used. ``out`` may be x or residual."""
+    td, dt = (c.T, c.d), _ndt(c)
+    if out is None:
+        out = torch.empty_like(x)
+    st = L.load().moe_dropout(
+        ctypes.byref(c), _shaped("x", x, td, dt), _shaped("residual", residual, td, dt),
+        _shaped("state", state, (2,), torch.int64), _shaped("out", out, td, dt), _s(stream))
+    _check(st, "moe_dropout")
+    return out
+
+
+def dropout_backward(c, dout, state, *, dx=None, stream=None):
+    """dx [T, d] of a ``dropout`` with this config and state (the residual's gradient is dout)."""
+    td, dt = (c.T, c.d), _ndt(c)
+    if dx is None:
+        dx = torch.empty_like(dout)
+    st = L.load().moe_dropout_backward(
+        ctypes.byref(c), _shaped("dout", dout, td, dt), _shaped("state", state, (2,), torch.int64),
+        _shaped("dx", dx, td, dt), _s(stream))
+    _check(st, "moe_dropout_backward")
+    return dx

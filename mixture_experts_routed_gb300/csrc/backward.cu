@@ -148,7 +148,7 @@ __device__ __forceinline__ bool beats_b(float va, int ia, float vb, int ib) {
 __global__ void __launch_bounds__(256) router_bwd_kernel(
     const float* __restrict__ L, const int32_t* __restrict__ idx, const float* __restrict__ w,
     const float* __restrict__ dw, int T, int E, int k, int mode, int pre_k, float tau,
-    float* __restrict__ dL, __nv_bfloat16* __restrict__ dLs) {
+    const float* __restrict__ more, float* __restrict__ dL, __nv_bfloat16* __restrict__ dLs) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(256) router_bwd_kernel(
   for (int jj = 0; jj < kRB_NJ; ++jj) {
     const int e = lane + 32 * jj;
     if (e < E) {
+      if (more != nullptr) g[jj] += __ldg(more + static_cast<size_t>(t) * E + e);
       dL[static_cast<size_t>(t) * E + e] = g[jj];
       if (dLs != nullptr) {
         // [T][2E] = [hi | lo] for the tensor-core gate GEMMs
@@ -550,11 +551,11 @@ cudaError_t launch_combine_bwd(int dtype, const void* dout, const float* y, cons
 }
 
 cudaError_t launch_router_bwd(const float* L, const int32_t* idx, const float* w, const float* dw,
-                              int T, int E, int k, int mode, int pre_k, float tau, float* dL,
-                              void* dLs, cudaStream_t s) {
+                              int T, int E, int k, int mode, int pre_k, float tau,
+                              const float* more, float* dL, void* dLs, cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   return launch_pdl(router_bwd_kernel, dim3(ceil_div(T, 8)), dim3(256), 0, s, L, idx, w, dw, T, E,
-                    k, mode, pre_k, tau, dL, static_cast<__nv_bfloat16*>(dLs));
+                    k, mode, pre_k, tau, more, dL, static_cast<__nv_bfloat16*>(dLs));
 }
 
 cudaError_t launch_gemm_nt(int wdtype, bool silu, const float* A, const void* W, int E, int R,

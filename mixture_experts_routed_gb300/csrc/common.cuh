@@ -108,7 +108,7 @@ constexpr int kMaxGroups = 32;
 // kMaxFanout (= E) for soft gating.
 constexpr int kMaxFanout = 16;
 
-inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- route.cu
@@ -213,11 +213,11 @@ cudaError_t launch_combine_bwd(int dtype, const void* dout, const float* y, cons
                                const void* h, int f, void* hs, void* doutp, float* wr, float* dw,
                                uint32_t* err, uint32_t* zero, int nzero, int32_t* seg01,
                                int32_t* segk, int nsegk, int chunk, cudaStream_t s);
-// dL [T, E] from dw through the router's softmax Jacobian (mode as RouterSpec),
-// and, when dLs is non-null, its bf16 split [T][2E] = [hi | lo].
+// dL [T, E] from dw through the router's softmax Jacobian (mode as RouterSpec)
+// plus `more` [T, E] where that is non-null, and, when dLs is non-null, its bf16 split [T][2E] = [hi | lo].
 cudaError_t launch_router_bwd(const float* L, const int32_t* idx, const float* w, const float* dw,
-                              int T, int E, int k, int mode, int pre_k, float tau, float* dL,
-                              void* dLs, cudaStream_t s);
+                              int T, int E, int k, int mode, int pre_k, float tau,
+                              const float* more, float* dL, void* dLs, cudaStream_t s);
 // out[r] = A[r] . W[e]^T over the segments (W [E][N][K], dtype wdtype);
 // silu: out holds Z and gets acc * SiLU'(Z).
 cudaError_t launch_gemm_nt(int wdtype, bool silu, const float* A, const void* W, int E, int R,
@@ -304,6 +304,9 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
                        const void* W2, int T, int d, int E, int f, RouterSpec rs, void* out,
                        void* ws, int num_sms, cudaStream_t s);
 
+// Row tiles (128 rows of one expert) that R rows of E experts can make.
+inline size_t row_tiles(int R, int E) { return static_cast<size_t>(R / 128) + (R < E ? R : E); }
+
 // ---------------------------------------------------------------- mx4.cu
 // Microscaled 4-bit rows and expert weights, and their grouped product.
 constexpr int kMx4MaxCtas = 160;    // the grid the product's partial sums are sized for
@@ -313,8 +316,6 @@ constexpr int kMx4SplitRows = 32;   // a split launch's rows per expert, at most
 // experts of 2048 x 1408), 40.6 and 44.6 (8 of 4096 x 11008); skewed, 16 of
 // 7168 x 2048, 34.8 and 30.8. At 256: 35.0 and 37.9, 49.3 and 48.0; 41.6 and 38.5.
 constexpr int kMx4PairRows = 192;
-// Row tiles (128 rows of one expert) that R rows of E experts can make.
-size_t mx4_row_tiles(int R, int E);
 cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,
                             const int32_t* offsets, int E, int R, int K, uint8_t* q, uint8_t* sc,
                             uint32_t* err, int num_sms, cudaStream_t s);
@@ -331,5 +332,40 @@ cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8
                                const uint8_t* wsc, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,
                                uint32_t* ctr, float* part, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- fp8.cu
+// 8-bit rows (q, sc) and columns (cq, csc) of x [R, C] (either may be null),
+// and of expert weights, and back: [experts][rows][cols] codes with a scale
+// for `per` rows x 128 columns, `pitch` of them to a line.
+cudaError_t launch_fp8_rows(int dtype, int act, const void* x, const int32_t* src, int x_rows,
+                            const float* weight, const void* z, const int32_t* offsets, int E,
+                            int R, int C, uint8_t* q, uint8_t* sc, uint8_t* cq, uint8_t* csc,
+                            uint32_t* err, int num_sms, cudaStream_t s);
+cudaError_t launch_fp8_weights(int dtype, const void* W, int E, int K, int N, uint8_t* q,
+                               uint8_t* sc, cudaStream_t s);
+cudaError_t launch_fp8_back(int dtype, const uint8_t* q, const uint8_t* sc, int experts, int rows,
+                            int cols, int per, int pitch, void* out, int num_sms, cudaStream_t s);
+// mode 0: rows a [R, K] . W [E, K, N]; 1: rows a [R, N] . W^T; 2: columns a
+// [.., K]^T . columns b [.., N] to fp32 [E, K, N].
+cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, const uint8_t* b,
+                               const uint8_t* bs, const int32_t* offsets, int E, int R, int K,
+                               int N, int out_f32, int silu, void* out, uint32_t* err,
+                               cudaStream_t s);
+
+// ---------------------------------------------------------------- router_loss.cu
+size_t router_loss_ws(int T, int E, int S);
+cudaError_t launch_router_loss(const float* logits, const int32_t* idx, const int32_t* offsets,
+                               const uint8_t* mask, int T, int E, int k, int S, float balance,
+                               float z, float* loss, int32_t* counts, int32_t* tokens, float* lse,
+                               void* ws, cudaStream_t s);
+cudaError_t launch_router_loss_bwd(const float* logits, const int32_t* offsets, const uint8_t* mask,
+                                   int T, int E, int k, int S, float balance, float z,
+                                   const int32_t* counts, const int32_t* tokens, const float* lse,
+                                   const float* dloss, float* dlogits, cudaStream_t s);
+
+// ---------------------------------------------------------------- dropout.cu
+// n elements (a multiple of 8); residual may be null; out may be x or residual.
+cudaError_t launch_dropout(int dtype, const void* x, const void* residual, const int64_t* state,
+                           uint32_t site, uint32_t thr, long long n, void* out, cudaStream_t s);
 
 }  // namespace moe

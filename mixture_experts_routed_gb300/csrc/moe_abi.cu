@@ -385,7 +385,8 @@ BwdLayout bwd_layout_of(const moe_config_t& c) {
 int backward_impl(const moe_config_t* cfg, const void* x, const void* Wg, const float* bias,
                   const float* noise, const void* W1, const void* W2, const void* fwd_ws,
                   size_t fwd_ws_bytes, const void* dout, float* dx, float* dWg, float* dbias,
-                  float* dW1, float* dW2, void* bws, size_t bws_bytes, void* stream) {
+                  float* dW1, float* dW2, void* bws, size_t bws_bytes, void* stream,
+                  const float* dlogits = nullptr) {
   int st = check_cfg(cfg);
   if (st != MOE_OK) return st;
   const moe_config_t& c = *cfg;
@@ -455,7 +456,8 @@ int backward_impl(const moe_config_t* cfg, const void* x, const void* Wg, const 
                            ch.n, ch.len, s);
   void* dLs = tc ? at<void>(bws, B.dLs) : nullptr;
   if (e == cudaSuccess)
-    e = launch_router_bwd(Lr, idx, w, dw, T, E, k, c.router, c.pre_k, c.tau, dL, dLs, s);
+    e = launch_router_bwd(Lr, idx, w, dw, T, E, k, c.router, c.pre_k, c.tau, dlogits, dL, dLs,
+                          s);
   // gate: dx_gate = dL W_g^T ([T, E] x [E, d]), dW_g = x^T dL, db = sum_t dL.
   // bf16 layers put them on the tensor cores with dL split into hi + lo
   // (dx_gate: W_g read K-major, K = E a multiple of 64; dW_g: E a multiple
@@ -569,7 +571,42 @@ constexpr size_t kMx4PartOffset = kMx4CtrOffset + 1024;
 static_assert(kMx4MaxCtas * sizeof(uint32_t) <= 1024, "arrivals");
 
 size_t mx4_row_scales(const moe_mx4_config_t& c) {
-  return mx4_row_tiles(c.R, c.E) * ceil_div(c.K, 128) * 512;
+  return row_tiles(c.R, c.E) * ceil_div(c.K, 128) * 512;
+}
+
+// ---------------------------------------------------------------- 8-bit products
+int check_fp8(const moe_fp8_config_t* c) {
+  if (c == nullptr || c->R < 0 || c->K <= 0 || c->N <= 0 || c->K % 64 != 0 || c->N % 64 != 0)
+    return MOE_ERR_INVALID_ARG;
+  if (c->E < 1 || c->E > kMaxExperts || c->x_rows < 0) return MOE_ERR_INVALID_ARG;
+  for (int dt : {c->dtype, c->out_dtype})
+    if (dt != MOE_DTYPE_F32 && dt != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->silu != 0 && c->silu != 1) return MOE_ERR_INVALID_ARG;
+  if (c->K > 65536 || c->N > 65536 || c->R > 1 << 24) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+int fp8_pitch(int cols) { return ceil_div(ceil_div(cols, 128), 4) * 4; }
+bool fp8_cols_ok(const moe_fp8_config_t& c, int cols) { return cols == c.K || cols == c.N; }
+
+// ---------------------------------------------------------------- router losses
+int check_router_loss(const moe_router_loss_config_t* c) {
+  if (c == nullptr || c->T < 0 || c->E < 1 || c->E > kMaxExperts || c->k < 1 || c->k > c->E ||
+      c->k > kMaxFanout || c->S < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (!(fabsf(c->balance) <= FLT_MAX) || !(fabsf(c->z) <= FLT_MAX)) return MOE_ERR_INVALID_ARG;
+  if (c->T > 1 << 26 || c->S > 1 << 20) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+bool words(const void* p) { return aligned(p, 4); }  // (null too)
+
+// ---------------------------------------------------------------- dropout
+int check_dropout(const moe_dropout_config_t* c) {
+  if (c == nullptr || c->T < 0 || c->d <= 0 || c->d % 64 != 0 || c->site < 0)
+    return MOE_ERR_INVALID_ARG;
+  if (c->dtype != MOE_DTYPE_F32 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!(c->p >= 0.f && c->p < 1.f)) return MOE_ERR_INVALID_ARG;
+  if (c->d > 65536 || c->T > 1 << 24) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
 }
 
 // ---------------------------------------------------------------- block norms
@@ -997,6 +1034,246 @@ int moe_block_norm_backward(const moe_norm_config_t* cfg, const void* dout, cons
                                          dn, x, bp, w_post, gate, w_pre, rstd_post, rstd_pre, dx,
                                          db, dw_post, dgate, dw_pre, static_cast<float*>(ws),
                                          as_stream(stream)));
+}
+
+int moe_backward_with_dlogits(const moe_config_t* cfg, const void* x, const void* W_g,
+                              const float* bias, const float* noise, const void* W1,
+                              const void* W2, const void* fwd_ws, size_t fwd_ws_bytes,
+                              const void* dout, const float* dlogits, float* dx, float* dW_g,
+                              float* dbias, float* dW1, float* dW2, void* ws, size_t ws_bytes,
+                              void* stream) {
+  if (dlogits == nullptr && check_cfg(cfg) == MOE_OK && cfg->T > 0) return MOE_ERR_INVALID_ARG;
+  return backward_impl(cfg, x, W_g, bias, noise, W1, W2, fwd_ws, fwd_ws_bytes, dout, dx, dW_g,
+                       dbias, dW1, dW2, ws, ws_bytes, stream, dlogits);
+}
+
+size_t moe_fp8_row_scale_size(const moe_fp8_config_t* cfg, int32_t cols) {
+  if (check_fp8(cfg) != MOE_OK || !fp8_cols_ok(*cfg, cols)) return 0;
+  return static_cast<size_t>(cfg->R > 0 ? cfg->R : 1) * fp8_pitch(cols);
+}
+
+size_t moe_fp8_column_rows(const moe_fp8_config_t* cfg) {
+  if (check_fp8(cfg) != MOE_OK) return 0;
+  return 128 * (cfg->R > 0 ? row_tiles(cfg->R, cfg->E) : 1);
+}
+
+size_t moe_fp8_weight_scale_size(const moe_fp8_config_t* cfg) {
+  if (check_fp8(cfg) != MOE_OK) return 0;
+  return static_cast<size_t>(cfg->E) * ceil_div(cfg->N, 128) * ceil_div(cfg->K, 128);
+}
+
+size_t moe_fp8_workspace_size(const moe_fp8_config_t* cfg) {
+  if (check_fp8(cfg) != MOE_OK) return 0;
+  return kMx4PartOffset + static_cast<size_t>(kMx4MaxCtas) * 2 * kMx4SplitRows * 256 * 4;
+}
+
+int moe_fp8_quantize_weights(const moe_fp8_config_t* cfg, const void* W, uint8_t* wq,
+                             uint8_t* w_scale, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (!ok_ptr(W) || !ok_ptr(wq) || w_scale == nullptr) return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(c.E) * c.K * c.N;
+  if (!apart({{wq, n}, {w_scale, moe_fp8_weight_scale_size(cfg)}}, {{W, n * elem_size(c.dtype)}}))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(launch_fp8_weights(c.dtype, W, c.E, c.K, c.N, wq, w_scale, as_stream(stream)));
+}
+
+int moe_fp8_quantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const void* x,
+                          const int32_t* src, const float* row_weight, int32_t act, const void* z,
+                          const int32_t* offsets, uint8_t* q, uint8_t* scale, uint8_t* cq,
+                          uint8_t* cscale, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (!fp8_cols_ok(c, cols) || act < MOE_ACT_NONE || act > MOE_ACT_SILU_GRAD)
+    return MOE_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if ((q == nullptr) != (scale == nullptr) || (cq == nullptr) != (cscale == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (c.R > 0 && (!ok_ptr(x) || offsets == nullptr || (q == nullptr && cq == nullptr) ||
+                  (q != nullptr && (!ok_ptr(q) || !aligned(scale, 4))) ||
+                  (cq != nullptr && (!ok_ptr(cq) || !aligned(cscale, 4))) ||
+                  (act == MOE_ACT_SILU_GRAD ? !ok_ptr(z) : z != nullptr)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_fp8_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.R == 0) return MOE_OK;
+  const size_t es = elem_size(c.dtype), R = c.R, C = cols, cr = moe_fp8_column_rows(cfg);
+  const int xr = src != nullptr ? c.x_rows : c.R;
+  if (!apart({{q, R * C}, {scale, R * fp8_pitch(cols)}, {cq, cr * C}, {cscale, cr / 128 * C},
+              {ws, moe_fp8_workspace_size(cfg)}},
+             {{x, xr * C * es}, {src, R * 4}, {row_weight, R * 4}, {z, R * C * es},
+              {offsets, (c.E + size_t(1)) * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_fp8_rows(c.dtype, act, x, src, xr, row_weight, z, offsets, c.E, c.R,
+                                   cols, q, scale, cq, cscale, static_cast<uint32_t*>(ws), sms,
+                                   as_stream(stream)));
+}
+
+int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8_t* q,
+                    const uint8_t* scale, const uint8_t* wq, const uint8_t* w_scale,
+                    const int32_t* offsets, void* out, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (transposed != 0 && transposed != 1) return MOE_ERR_INVALID_ARG;
+  if (transposed && c.silu) return MOE_ERR_UNSUPPORTED;
+  if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
+  if (c.R > 0 && (!ok_ptr(q) || scale == nullptr || !aligned(scale, 4) || !ok_ptr(wq) ||
+                  w_scale == nullptr || offsets == nullptr || !ok_ptr(out)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_fp8_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (c.R == 0) return MOE_OK;
+  const size_t R = c.R, len = transposed ? c.N : c.K, width = transposed ? c.K : c.N;
+  if (!apart({{out, R * width * elem_size(c.out_dtype)}, {ws, moe_fp8_workspace_size(cfg)}},
+             {{q, R * len}, {scale, R * fp8_pitch(static_cast<int>(len))},
+              {wq, static_cast<size_t>(c.E) * c.K * c.N}, {w_scale, moe_fp8_weight_scale_size(cfg)},
+              {offsets, (c.E + size_t(1)) * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_fp8_product(transposed, q, scale, wq, w_scale, offsets, c.E, c.R, c.K,
+                                      c.N, c.out_dtype == MOE_DTYPE_F32 ? 1 : 0, c.silu, out,
+                                      static_cast<uint32_t*>(ws), as_stream(stream)));
+}
+
+int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const uint8_t* x_scale,
+                        const uint8_t* dyq, const uint8_t* dy_scale, const int32_t* offsets,
+                        float* dW, void* ws, size_t ws_bytes, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (ws == nullptr || !aligned(ws, kAlign) || !ok_ptr(dW)) return MOE_ERR_INVALID_ARG;
+  if (c.R > 0 && (!ok_ptr(xq) || x_scale == nullptr || !aligned(x_scale, 4) || !ok_ptr(dyq) ||
+                  dy_scale == nullptr || !aligned(dy_scale, 4) || offsets == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_fp8_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t n = static_cast<size_t>(c.E) * c.K * c.N * 4;
+  if (c.R == 0) return status_of(cudaMemsetAsync(dW, 0, n, as_stream(stream)));
+  const size_t cr = moe_fp8_column_rows(cfg);
+  if (!apart({{dW, n}, {ws, moe_fp8_workspace_size(cfg)}},
+             {{xq, cr * c.K}, {x_scale, cr / 128 * c.K}, {dyq, cr * c.N}, {dy_scale, cr / 128 * c.N},
+              {offsets, (c.E + size_t(1)) * 4}}))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_fp8_product(2, xq, x_scale, dyq, dy_scale, offsets, c.E, c.R, c.K, c.N,
+                                      1, 0, dW, static_cast<uint32_t*>(ws), as_stream(stream)));
+}
+
+int moe_fp8_dequantize_weights(const moe_fp8_config_t* cfg, const uint8_t* wq,
+                               const uint8_t* w_scale, void* W, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (!ok_ptr(W) || !ok_ptr(wq) || w_scale == nullptr) return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(c.E) * c.K * c.N;
+  if (!apart({{W, n * elem_size(c.dtype)}},
+             {{wq, n}, {w_scale, moe_fp8_weight_scale_size(cfg)}}))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_fp8_back(c.dtype, wq, w_scale, c.E, c.K, c.N, 128, ceil_div(c.N, 128), W,
+                                   sms, as_stream(stream)));
+}
+
+int moe_fp8_dequantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const uint8_t* q,
+                            const uint8_t* scale, void* x, void* stream) {
+  const int st = check_fp8(cfg);
+  if (st != MOE_OK) return st;
+  const moe_fp8_config_t& c = *cfg;
+  if (!fp8_cols_ok(c, cols)) return MOE_ERR_INVALID_ARG;
+  if (c.R == 0) return MOE_OK;
+  if (!ok_ptr(q) || scale == nullptr || !ok_ptr(x)) return MOE_ERR_INVALID_ARG;
+  const size_t n = static_cast<size_t>(c.R) * cols;
+  if (!apart({{x, n * elem_size(c.dtype)}},
+             {{q, n}, {scale, static_cast<size_t>(c.R) * fp8_pitch(cols)}}))
+    return MOE_ERR_INVALID_ARG;
+  const int sms = num_sms();
+  if (sms <= 0) return MOE_ERR_LAUNCH;
+  return status_of(launch_fp8_back(c.dtype, q, scale, 1, c.R, cols, 1, fp8_pitch(cols), x, sms,
+                                   as_stream(stream)));
+}
+
+size_t moe_router_loss_workspace_size(const moe_router_loss_config_t* cfg) {
+  if (check_router_loss(cfg) != MOE_OK) return 0;
+  return router_loss_ws(cfg->T, cfg->E, cfg->S);
+}
+
+int moe_router_loss(const moe_router_loss_config_t* cfg, const float* logits,
+                    const int32_t* topk_idx, const int32_t* seq_offsets, const uint8_t* mask,
+                    float* loss, int32_t* counts, int32_t* tokens, float* lse, void* ws,
+                    size_t ws_bytes, void* stream) {
+  const int st = check_router_loss(cfg);
+  if (st != MOE_OK) return st;
+  const moe_router_loss_config_t& c = *cfg;
+  if (ws == nullptr || !aligned(ws, kAlign) || !words(loss) || loss == nullptr ||
+      counts == nullptr || !words(counts) || tokens == nullptr || !words(tokens) ||
+      !words(seq_offsets) || (c.S > 1 && seq_offsets == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (c.T > 0 && (logits == nullptr || !words(logits) || topk_idx == nullptr || !words(topk_idx) ||
+                  lse == nullptr || !words(lse)))
+    return MOE_ERR_INVALID_ARG;
+  if (ws_bytes < moe_router_loss_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t T = c.T, E = c.E, S = c.S;
+  if (!apart({{loss, 12}, {counts, S * E * 4}, {tokens, (S + 2) * 4}, {lse, T * 4},
+              {ws, moe_router_loss_workspace_size(cfg)}},
+             {{logits, T * E * 4}, {topk_idx, T * c.k * 4}, {seq_offsets, (S + 1) * 4}, {mask, T}}))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(launch_router_loss(logits, topk_idx, seq_offsets, mask, c.T, c.E, c.k, c.S,
+                                      c.balance, c.z, loss, counts, tokens, lse, ws,
+                                      as_stream(stream)));
+}
+
+int moe_router_loss_backward(const moe_router_loss_config_t* cfg, const float* logits,
+                             const int32_t* seq_offsets, const uint8_t* mask,
+                             const int32_t* counts, const int32_t* tokens, const float* lse,
+                             const float* dloss, float* dlogits, void* stream) {
+  const int st = check_router_loss(cfg);
+  if (st != MOE_OK) return st;
+  const moe_router_loss_config_t& c = *cfg;
+  if ((c.S > 1 && seq_offsets == nullptr) || !words(seq_offsets)) return MOE_ERR_INVALID_ARG;
+  if (c.T == 0) return MOE_OK;
+  if (logits == nullptr || counts == nullptr || tokens == nullptr || lse == nullptr ||
+      dlogits == nullptr || !words(logits) || !words(counts) || !words(tokens) || !words(lse) ||
+      !words(dloss) || !words(dlogits))
+    return MOE_ERR_INVALID_ARG;
+  const size_t T = c.T, E = c.E, S = c.S;
+  if (!apart({{dlogits, T * E * 4}},
+             {{logits, T * E * 4}, {seq_offsets, (S + 1) * 4}, {mask, T}, {counts, S * E * 4},
+              {tokens, (S + 2) * 4}, {lse, T * 4}, {dloss, 4}}))
+    return MOE_ERR_INVALID_ARG;
+  return status_of(launch_router_loss_bwd(logits, seq_offsets, mask, c.T, c.E, c.k, c.S, c.balance,
+                                          c.z, counts, tokens, lse, dloss, dlogits,
+                                          as_stream(stream)));
+}
+
+int moe_dropout(const moe_dropout_config_t* cfg, const void* x, const void* residual,
+                const int64_t* state, void* out, void* stream) {
+  const int st = check_dropout(cfg);
+  if (st != MOE_OK) return st;
+  const moe_dropout_config_t& c = *cfg;
+  if (c.T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(out) || (residual != nullptr && !ok_ptr(residual)) ||
+      state == nullptr || !aligned(state, 8))
+    return MOE_ERR_INVALID_ARG;
+  // in place, element for element, is fine; any other overlap is not
+  const long long n = static_cast<long long>(c.T) * c.d;
+  const size_t bytes = static_cast<size_t>(n) * elem_size(c.dtype);
+  if (!apart({{out, bytes}}, {{x != out ? x : nullptr, bytes},
+                              {residual != out ? residual : nullptr, bytes}, {state, 16}}))
+    return MOE_ERR_INVALID_ARG;
+  const long r = lroundf(c.p * 65536.f);
+  return status_of(launch_dropout(c.dtype, x, residual, state, static_cast<uint32_t>(c.site),
+                                  static_cast<uint32_t>(r < 65535 ? r : 65535), n, out,
+                                  as_stream(stream)));
+}
+
+int moe_dropout_backward(const moe_dropout_config_t* cfg, const void* dout, const int64_t* state,
+                         void* dx, void* stream) {
+  return moe_dropout(cfg, dout, nullptr, state, dx, stream);
 }
 
 int moe_forward_kernel_count(const moe_config_t* cfg) {

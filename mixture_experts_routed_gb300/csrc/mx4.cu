@@ -27,6 +27,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "grouped.cuh"
 #include "ptx.cuh"
 #include "range.cuh"
 #include "tmap.cuh"
@@ -37,8 +38,6 @@ namespace {
 using namespace ptx;
 
 constexpr int CHUNK = 512;  // bytes of scales of 128 rows x 128 values
-
-__host__ __device__ constexpr int up_div(int a, int b) { return (a + b - 1) / b; }
 
 __device__ __forceinline__ uint32_t scale_code(uint32_t amax_bits) {
   if (amax_bits >= 0x7f800000u) return 255u;
@@ -55,15 +54,6 @@ __device__ __forceinline__ float inv_scale(uint32_t s) {
 // the scale 2^(s - 127) (s = 0: 2^-127, subnormal)
 __device__ __forceinline__ float scale_value(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7fc00000u : (s == 0u ? 0x00400000u : s << 23));
-}
-
-// 16 bytes that are read once
-__device__ __forceinline__ uint4 ld_once(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
 }
 
 // 8 scaled values to 8 codes, v[0] lowest
@@ -88,51 +78,6 @@ __device__ __forceinline__ float code_value(uint32_t w, int j) {
   return __uint_as_float((t & 0x80000000u) | ((t >> 6) & 0x01c00000u)) * 0x1p126f;
 }
 
-// The segments' row tiles: seg[e] = offsets[e], base[e] = row tiles before
-// expert e. Every thread of the block takes part; false (and the error
-// flagged) when the offsets leave [0, R] or fall.
-__device__ bool load_segments(const int32_t* __restrict__ offsets, int E, int R, int* seg,
-                              int* base, int* ok, uint32_t* err) {
-  const int tid = threadIdx.x;
-  if (tid == 0) *ok = 1;
-  for (int e = tid; e <= E; e += blockDim.x) seg[e] = __ldg(offsets + e);
-  __syncthreads();
-  for (int e = tid; e <= E; e += blockDim.x)
-    if (seg[e] < 0 || seg[e] > R || (e > 0 && seg[e] < seg[e - 1])) *ok = 0;
-  __syncthreads();
-  if (tid < 32) {
-    int run = 0;
-    for (int e0 = 0; e0 < E; e0 += 32) {
-      const int e = e0 + tid;
-      int n = *ok && e < E ? up_div(seg[e + 1] - seg[e], 128) : 0;
-      int inc = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (tid >= o) inc += v;
-      }
-      if (e < E) base[e] = run + inc - n;
-      run += __shfl_sync(0xffffffffu, inc, 31);
-    }
-    if (tid == 0) base[E] = run;
-  }
-  __syncthreads();
-  if (!*ok && tid == 0 && blockIdx.x == 0 && blockIdx.y == 0 && err != nullptr)
-    atomicOr(err, kErrBadIndex);
-  return *ok != 0;
-}
-// the last i of v[0..n] with v[i] <= x (v rising, v[0] <= x)
-__device__ __forceinline__ int last_at_most(const int* v, int n, int x) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (v[mid] <= x)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
-  return lo;
-}
 // first byte of row r's scales of 128-value group 0 (groups CHUNK apart)
 __device__ __forceinline__ size_t row_scale_at(int r, const int* seg, const int* base, int E,
                                                int kc) {
@@ -424,7 +369,7 @@ __global__ void __launch_bounds__(kWeightThreads<T>)
 // of 32 experts, 7168 x 2048 to fp32: 109 us (116), where 445 MB move and 632
 // tiles over 76 pairs leave the last of nine waves two thirds empty.
 namespace mx {
-constexpr int BN = 256, HN = 128, KS = 256;  // a tile's columns, an accumulator's, a stage's k
+constexpr int BN = kTileCols, HN = 128, KS = 256;  // a tile's columns, an accumulator's, a stage's k
 constexpr int B_BOX = 64 * 128;             // a box of 64 columns
 constexpr int A_BYTES = 128 * 128;
 constexpr int SF_COL = 384, SF_STAGE = 24;  // tensor memory columns: 3 x 128, then scales
@@ -518,58 +463,7 @@ __device__ __forceinline__ void bar_epi() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
 }
 
-struct Tile {
-  int e, row0, rows, mt, n0, n;
-};
-// Tile t: expert by expert, column blocks outside, row tiles inside, so that
-// the CTAs at work side by side share a column block's weights. tb: tiles of
-// BM rows before each expert; base: tiles of 128 rows (scale chunks).
-template <int BM>
-__device__ __forceinline__ Tile tile_at(int t, const int* seg, const int* base, const int* tb,
-                                        int E, int N) {
-  const int nt = up_div(N, BN);
-  Tile r;
-  r.e = last_at_most(tb, E - 1, t / nt);
-  const int l = t - tb[r.e] * nt, m = tb[r.e + 1] - tb[r.e];
-  const int nb = l / m, mt = l - nb * m;
-  r.mt = base[r.e] + mt * (BM / 128);
-  r.row0 = seg[r.e] + mt * BM;
-  r.rows = min(BM, seg[r.e + 1] - r.row0);
-  r.n0 = nb * BN;
-  r.n = min(BN, N - r.n0);
-  return r;
-}
 }  // namespace mx
-
-// 32 bytes: one store where they are 32-byte aligned, else two of 16
-__device__ __forceinline__ void st_sector(bool whole, void* p, const uint32_t (&v)[8]) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-// SiLU of an fp32 sum. Where fp32 is stored: with t = exp(-|z|) (2 units of the
-// last place), z / (1 + t), or z t / (1 + t) below 0, so that nothing overflows;
-// the denominator is in [1, 2], its approximate reciprocal y needs no special
-// cases, and one correction of q = n y by its residual (P. Markstein, IBM J.
-// Res. Dev. 34(1), 1990) leaves the quotient's own rounding: 7 half steps in
-// all (2047 rows of 64 experts of 2048 x 1408 30.3 us, with a plain division 53.5).
-// Where bf16 is stored: approximate exponential and quotient, whose error (some
-// 60 half steps of fp32) is a thousandth of the rounding that follows; below
-// z = -87.3 they give 0 for at most 1.1e-36.
-template <typename TO>
-__device__ __forceinline__ float mx_silu(float z) {
-  if constexpr (sizeof(TO) == 4) {
-    const float t = expf(-fabsf(z)), d = 1.f + t, n = z < 0.f ? z * t : z;
-    const float y = __fdividef(1.f, d), q = n * y;
-    return isinf(q) ? q : fmaf(fmaf(-q, d, n), y, q);
-  }
-  return __fdividef(z, 1.f + __expf(-z));
-}
 
 // TO: the output type
 template <bool PAIR, typename TO>
@@ -910,50 +804,10 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
     bool dead = false;
     TO* out = static_cast<TO*>(p.out);
     const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
-    auto finish = [&](float v) { return p.silu ? mx_silu<TO>(v) : v; };
-    // 32 columns of up to 32 rows, a row to a lane, to out: neighbouring lanes
-    // exchange 32-byte pieces first, so that a store instruction writes
-    // contiguous runs of 128 bytes (fp32; bf16: 64), not a sector of each row
+    auto finish = [&](float v) { return p.silu ? silu_of<TO>(v) : v; };
     const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
     auto put32 = [&](size_t row0, int rows, int col, const uint32_t (&r)[32]) {
-      constexpr int PER = 32 / sizeof(TO), NC = 32 / PER;  // a piece's columns, a row's pieces
-      uint32_t v[NC][8];
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if constexpr (sizeof(TO) == 4) {
-            v[c][i] = __float_as_uint(finish(__uint_as_float(r[c * PER + i])));
-          } else {
-            const __nv_bfloat162 h =
-                __floats2bfloat162_rn(finish(__uint_as_float(r[c * PER + 2 * i])),
-                                      finish(__uint_as_float(r[c * PER + 2 * i + 1])));
-            v[c][i] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-        }
-      }
-      // a transposition within groups of NC lanes: v[i] is then piece `lane %
-      // NC` of the group's row i
-#pragma unroll
-      for (int m = 1; m < NC; m <<= 1) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          if (c & m) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const bool up = lane & m;
-            const uint32_t got =
-                __shfl_xor_sync(0xffffffffu, up ? v[c][i] : v[c | m][i], m);
-            v[c][i] = up ? got : v[c][i];
-            v[c | m][i] = up ? v[c | m][i] : got;
-          }
-        }
-      }
-      const int g = lane & ~(NC - 1);
-      TO* o = out + (row0 + g) * N + col + (lane - g) * PER;
-#pragma unroll
-      for (int i = 0; i < NC; ++i)
-        if (g + i < rows) st_sector(sectors, o + static_cast<size_t>(i) * N, v[i]);
+      put_rows32(out, sectors, row0, rows, N, col, r, finish);
     };
     walk([&](int t, int k0, int k1) {
       const Tile tl = tile_at<BM>(t, seg, base, tb, E, N);
@@ -1100,8 +954,6 @@ int blocks_for(long long items, int per_block, int most) {
 
 }  // namespace
 
-size_t mx4_row_tiles(int R, int E) { return static_cast<size_t>(R / 128) + (R < E ? R : E); }
-
 cudaError_t launch_mx4_rows(int dtype, const void* x, const int32_t* src, int x_rows,
                             const int32_t* offsets, int E, int R, int K, uint8_t* q, uint8_t* sc,
                             uint32_t* err, int num_sms, cudaStream_t s) {
@@ -1151,7 +1003,7 @@ cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8
   const uint64_t kc = up_div(K, 128);
   if (!make_map_2d_bytes(&mA, aq, R, K / 2, 128) || !make_map_2d_bytes(&mA32, aq, R, K / 2, 32) ||
       !make_map_2d_bytes(&mB, wq, static_cast<uint64_t>(E) * N, K / 2, 64) ||
-      !make_map_3d_chunks(&mSA, as, mx4_row_tiles(R, E), kc, 1) ||
+      !make_map_3d_chunks(&mSA, as, row_tiles(R, E), kc, 1) ||
       !make_map_3d_chunks(&mSB, wsc, static_cast<uint64_t>(E) * up_div(N, 128), kc, 2))
     return cudaErrorInvalidValue;
   const mx::Params p{offsets, out, err, ctr, part, E, R, K, N, silu};

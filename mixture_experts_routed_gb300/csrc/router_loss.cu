@@ -1,0 +1,379 @@
+// router_loss.cu - the router's balance loss, by sequence or over the batch,
+// its z loss and the experts' counts, and the gradient of the logits.
+//
+// Over the tokens t of sequence s that count (n_s of them; c_se chose e):
+//   p_t = softmax(L_t)   f_se = E c_se / (k n_s)   P_se = sum_t p_te / n_s
+//   balance = 1/S' sum_s sum_e f_se P_se          S' sequences with n_s > 0
+//   z       = 1/N sum_t lse_t^2                   N = sum_s n_s
+//   loss    = a balance + b z
+//   dL_te   = a / (S' n_s) p_te (f_se - sum_j p_tj f_sj) + 2 b / N lse_t p_te
+// (the counts are constants to the gradient).
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kNJ = kMaxExperts / 32;  // a lane's experts
+constexpr int kWarps = 8;
+
+// Tokens are cut into chunks of `len` of one sequence. Chunk j of sequence s
+// has the slot offsets[s] / len + s + j, which no other chunk has (a sequence
+// begins at most one slot behind the one before it, plus its own chunks).
+struct Seqs {
+  const int32_t* offsets;  // null: one sequence of all T
+  int T, S, len;
+  __device__ int at(int s) const { return offsets != nullptr ? __ldg(offsets + s) : (s ? T : 0); }
+  __device__ int slot(int s) const { return at(s) / len + s; }
+  // the last s whose value is at most x, 0 if none
+  template <typename F>
+  __device__ int last(int x, F value) const {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (value(mid) <= x)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    return lo;
+  }
+  // Every thread of the block takes part: do the offsets rise within [0, T]?
+  __device__ bool good() const {
+    int bad = 0;
+    if (offsets != nullptr)
+      for (int s = threadIdx.x; s <= S; s += blockDim.x) {
+        const int o = at(s);
+        if (o < 0 || o > T || (s > 0 && o < at(s - 1))) bad = 1;
+      }
+    return __syncthreads_or(bad) == 0;
+  }
+};
+
+// what a token's row is to its lanes: values at lane + 32 j
+struct Row {
+  float v[kNJ];
+  __device__ void load(const float* p, int E, int lane) {
+#pragma unroll
+    for (int j = 0; j < kNJ; ++j) v[j] = lane + 32 * j < E ? __ldg(p + lane + 32 * j) : -INFINITY;
+  }
+};
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// A block sums one chunk, a token to a warp at a time.
+__global__ void __launch_bounds__(kWarps * 32)
+    router_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                       const Seqs q, const uint8_t* __restrict__ mask, int E, int k,
+                       float* __restrict__ lse, float* __restrict__ psum, int32_t* __restrict__ cnt,
+                       float2* __restrict__ tail, uint32_t* err) {
+  __shared__ float ps[kWarps][kMaxExperts];
+  __shared__ int cs[kMaxExperts];
+  __shared__ float zs[kWarps];
+  __shared__ int ns[kWarps];
+  pdl_wait();
+  pdl_trigger();
+  if (!q.good()) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kErrBadIndex);
+    return;
+  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int s = q.last(blockIdx.x, [&](int i) { return q.slot(i); });
+  const int t0 = q.at(s) + (static_cast<int>(blockIdx.x) - q.slot(s)) * q.len;
+  const int t1 = min(t0 + q.len, q.at(s + 1));
+  if (t0 >= t1 || t0 < q.at(s)) return;
+  for (int e = tid; e < E; e += kWarps * 32) cs[e] = 0;
+  __syncthreads();
+  Row sum;
+#pragma unroll
+  for (int j = 0; j < kNJ; ++j) sum.v[j] = 0.f;
+  float zsum = 0.f;
+  int n = 0;
+  for (int t = t0 + warp; t < t1; t += kWarps) {
+    if (mask != nullptr && __ldg(mask + t) == 0) {
+      if (lane == 0) lse[t] = 0.f;
+      continue;
+    }
+    Row L;
+    L.load(logits + static_cast<size_t>(t) * E, E, lane);
+    if (lane < k) {
+      const int e = __ldg(idx + static_cast<size_t>(t) * k + lane);
+      if (e >= 0 && e < E)
+        atomicAdd(&cs[e], 1);
+      else
+        atomicOr(err, kErrBadIndex);
+    }
+    float top = L.v[0];
+#pragma unroll
+    for (int j = 1; j < kNJ; ++j) top = fmaxf(top, L.v[j]);
+    top = warp_max(top);
+    float den = 0.f;
+#pragma unroll
+    for (int j = 0; j < kNJ; ++j) {
+      L.v[j] = lane + 32 * j < E ? expf(L.v[j] - top) : 0.f;
+      den += L.v[j];
+    }
+    den = warp_sum(den);
+    const float inv = 1.f / den, l = top + logf(den);
+#pragma unroll
+    for (int j = 0; j < kNJ; ++j) sum.v[j] = fmaf(L.v[j], inv, sum.v[j]);
+    zsum = fmaf(l, l, zsum);
+    ++n;
+    if (lane == 0) lse[t] = l;
+  }
+#pragma unroll
+  for (int j = 0; j < kNJ; ++j)
+    if (lane + 32 * j < E) ps[warp][lane + 32 * j] = sum.v[j];
+  if (lane == 0) {
+    zs[warp] = zsum;
+    ns[warp] = n;
+  }
+  __syncthreads();
+  const size_t at = static_cast<size_t>(blockIdx.x) * E;
+  for (int e = tid; e < E; e += kWarps * 32) {
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += ps[w][e];
+    psum[at + e] = v;
+    cnt[at + e] = cs[e];
+  }
+  if (tid == 0) {
+    float v = 0.f;
+    int m = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      v += zs[w];
+      m += ns[w];
+    }
+    tail[blockIdx.x] = make_float2(v, __int_as_float(m));
+  }
+}
+
+// A block joins the chunks of one sequence for 32 experts, in chunk order by
+// eight warps and then over the warps; the last block to be done adds up the
+// sequences, in order.
+__global__ void __launch_bounds__(kWarps * 32)
+    router_loss_join_kernel(const Seqs q, int E, int k, float balance, float zcoef,
+                            const float* __restrict__ psum, const int32_t* __restrict__ cnt,
+                            const float2* __restrict__ tail, float* term, uint32_t* done,
+                            float* __restrict__ loss, int32_t* __restrict__ counts,
+                            int32_t* tokens) {
+  __shared__ float ps[kWarps][32], zs[kWarps][32];
+  __shared__ int cs[kWarps][32], ns[kWarps][32];
+  __shared__ double fin[kWarps][2];
+  __shared__ int fn[kWarps][2], last;
+  pdl_wait();
+  pdl_trigger();
+  if (!q.good()) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int parts = ceil_div(E, 32);
+  const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, e = part * 32 + lane;
+  const int first = q.slot(s), chunks = ceil_div(q.at(s + 1) - q.at(s), q.len);
+  float p = 0.f, z = 0.f;
+  int c = 0, n = 0;
+  for (int j = warp; j < chunks; j += kWarps) {
+    if (e < E) {
+      const size_t at = static_cast<size_t>(first + j) * E + e;
+      p += __ldcg(psum + at);
+      c += __ldcg(cnt + at);
+    }
+  }
+  for (int j = tid; j < chunks; j += kWarps * 32) {
+    const float2 v = __ldcg(tail + first + j);
+    z += v.x;
+    n += __float_as_int(v.y);
+  }
+  ps[warp][lane] = p;
+  cs[warp][lane] = c;
+  zs[warp][lane] = z;
+  ns[warp][lane] = n;
+  __syncthreads();
+  if (warp == 0) {
+    p = z = 0.f;
+    c = n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      p += ps[w][lane];
+      c += cs[w][lane];
+      z += zs[w][lane];
+      n += ns[w][lane];
+    }
+    z = warp_sum(z);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (e < E) counts[static_cast<size_t>(s) * E + e] = c;
+    // f P = E c / (k n) p / n
+    const float fn_ = static_cast<float>(n);
+    const float v = warp_sum(
+        n > 0 && e < E ? static_cast<float>(E) * static_cast<float>(c) / (static_cast<float>(k) * fn_) * (p / fn_)
+                       : 0.f);
+    if (lane == 0) {
+      term[2 * blockIdx.x] = v;
+      term[2 * blockIdx.x + 1] = part == 0 ? z : 0.f;
+      if (part == 0) tokens[s] = n;
+      __threadfence();
+      last = atomicAdd(done, 1u) == gridDim.x - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  double bal = 0, zz = 0;
+  int used = 0, all = 0;
+  for (int i = tid; i < static_cast<int>(gridDim.x); i += kWarps * 32) {
+    bal += __ldcg(term + 2 * i);
+    zz += __ldcg(term + 2 * i + 1);
+  }
+  for (int i = tid; i < q.S; i += kWarps * 32) {
+    const int m = __ldcg(tokens + i);
+    used += m > 0;
+    all += m;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    bal += __shfl_xor_sync(0xffffffffu, bal, o);
+    zz += __shfl_xor_sync(0xffffffffu, zz, o);
+  }
+  used = __reduce_add_sync(0xffffffffu, used);
+  all = __reduce_add_sync(0xffffffffu, all);
+  if (lane == 0) {
+    fin[warp][0] = bal;
+    fin[warp][1] = zz;
+    fn[warp][0] = used;
+    fn[warp][1] = all;
+  }
+  __syncthreads();
+  if (tid != 0) return;
+  bal = zz = 0;
+  used = all = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    bal += fin[w][0];
+    zz += fin[w][1];
+    used += fn[w][0];
+    all += fn[w][1];
+  }
+  if (used > 0) bal /= used;
+  if (all > 0) zz /= all;
+  loss[0] = static_cast<float>(balance * bal + zcoef * zz);
+  loss[1] = static_cast<float>(bal);
+  loss[2] = static_cast<float>(zz);
+  tokens[q.S] = used;
+  tokens[q.S + 1] = all;
+  *done = 0;
+}
+
+// A token to a warp.
+__global__ void __launch_bounds__(kWarps * 32)
+    router_loss_bwd_kernel(const float* __restrict__ logits, const Seqs q,
+                           const uint8_t* __restrict__ mask, int E, int k, float balance,
+                           float zcoef, const int32_t* __restrict__ counts,
+                           const int32_t* __restrict__ tokens, const float* __restrict__ lse,
+                           const float* __restrict__ dloss, float* __restrict__ dlogits) {
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (t >= q.T) return;
+  float* out = dlogits + static_cast<size_t>(t) * E;
+  const int s = q.last(t, [&](int i) { return q.at(i); });
+  const int n = __ldg(tokens + s), used = __ldg(tokens + q.S), all = __ldg(tokens + q.S + 1);
+  const bool on = t >= q.at(s) && t < q.at(s + 1) && n > 0 && used > 0 && all > 0 &&
+                  (mask == nullptr || __ldg(mask + t) != 0);
+  if (!on) {
+    for (int e = lane; e < E; e += 32) out[e] = 0.f;
+    return;
+  }
+  const float g = dloss != nullptr ? __ldg(dloss) : 1.f, l = __ldg(lse + t);
+  const float fs = static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(n));
+  Row L;
+  L.load(logits + static_cast<size_t>(t) * E, E, lane);
+  float f[kNJ], dot = 0.f;
+#pragma unroll
+  for (int j = 0; j < kNJ; ++j) {
+    const int e = lane + 32 * j;
+    f[j] = e < E ? fs * static_cast<float>(__ldg(counts + static_cast<size_t>(s) * E + e)) : 0.f;
+    L.v[j] = e < E ? expf(L.v[j] - l) : 0.f;
+    dot = fmaf(L.v[j], f[j], dot);
+  }
+  dot = warp_sum(dot);
+  const float cb = g * balance / (static_cast<float>(used) * static_cast<float>(n));
+  const float cz = g * 2.f * zcoef / static_cast<float>(all) * l;
+#pragma unroll
+  for (int j = 0; j < kNJ; ++j) {
+    const int e = lane + 32 * j;
+    if (e < E) out[e] = L.v[j] * fmaf(cb, f[j] - dot, cz);
+  }
+}
+
+// Chunks of a warp's token or more, about two blocks to an SM.
+int chunk_len(int T) {
+  const int len = ceil_div(ceil_div(T, 304), kWarps) * kWarps;
+  return len < kWarps ? kWarps : len;
+}
+int slots_of(int T, int S) { return T / chunk_len(T) + S; }
+
+struct Layout {
+  size_t done, psum, cnt, tail, term, total;
+};
+Layout layout(int T, int E, int S) {
+  Layout L;
+  const size_t slots = slots_of(T, S);
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o = align_up(o + bytes, 256);
+    return at;
+  };
+  take(4);  // the error word
+  L.done = 64;
+  L.psum = take(slots * E * 4);
+  L.cnt = take(slots * E * 4);
+  L.tail = take(slots * 8);
+  L.term = take(static_cast<size_t>(S) * ceil_div(E, 32) * 8);
+  L.total = o;
+  return L;
+}
+
+}  // namespace
+
+size_t router_loss_ws(int T, int E, int S) { return layout(T, E, S).total; }
+
+cudaError_t launch_router_loss(const float* logits, const int32_t* idx, const int32_t* offsets,
+                               const uint8_t* mask, int T, int E, int k, int S, float balance,
+                               float z, float* loss, int32_t* counts, int32_t* tokens, float* lse,
+                               void* ws, cudaStream_t s) {
+  const Layout L = layout(T, E, S);
+  char* w = static_cast<char*>(ws);
+  const Seqs q{offsets, T, S, chunk_len(T)};
+  float* psum = reinterpret_cast<float*>(w + L.psum);
+  int32_t* cnt = reinterpret_cast<int32_t*>(w + L.cnt);
+  float2* tail = reinterpret_cast<float2*>(w + L.tail);
+  const cudaError_t e =
+      launch_pdl(router_loss_kernel, dim3(slots_of(T, S)), dim3(kWarps * 32), 0, s, logits, idx, q,
+                 mask, E, k, lse, psum, cnt, tail, reinterpret_cast<uint32_t*>(w));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(router_loss_join_kernel, dim3(S * ceil_div(E, 32)), dim3(kWarps * 32), 0, s, q,
+                    E, k, balance, z, static_cast<const float*>(psum),
+                    static_cast<const int32_t*>(cnt), static_cast<const float2*>(tail),
+                    reinterpret_cast<float*>(w + L.term), reinterpret_cast<uint32_t*>(w + L.done),
+                    loss, counts, tokens);
+}
+
+cudaError_t launch_router_loss_bwd(const float* logits, const int32_t* offsets, const uint8_t* mask,
+                                   int T, int E, int k, int S, float balance, float z,
+                                   const int32_t* counts, const int32_t* tokens, const float* lse,
+                                   const float* dloss, float* dlogits, cudaStream_t s) {
+  const Seqs q{offsets, T, S, chunk_len(T)};
+  return launch_pdl(router_loss_bwd_kernel, dim3(ceil_div(T, kWarps)), dim3(kWarps * 32), 0, s,
+                    logits, q, mask, E, k, balance, z, counts, tokens, lse, dloss, dlogits);
+}
+
+}  // namespace moe
