@@ -346,11 +346,12 @@ cudaError_t launch_fp8_weights(int dtype, const void* W, int E, int K, int N, ui
 cudaError_t launch_fp8_back(int dtype, const uint8_t* q, const uint8_t* sc, int experts, int rows,
                             int cols, int per, int pitch, void* out, int num_sms, cudaStream_t s);
 // mode 0: rows a [R, K] . W [E, K, N]; 1: rows a [R, N] . W^T; 2: columns a
-// [.., K]^T . columns b [.., N] to fp32 [E, K, N].
+// [.., K]^T . columns b [.., N] to fp32 [E, K, N]. ctr and part as for the 4-bit
+// product.
 cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, const uint8_t* b,
                                const uint8_t* bs, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,
-                               cudaStream_t s);
+                               uint32_t* ctr, float* part, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- router_loss.cu
 size_t router_loss_ws(int T, int E, int S);

@@ -23,12 +23,16 @@
 //   dW[e] = sum_r x[r]^T dy[r]             columns, columns
 #include <cstdint>
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "common.cuh"
 #include "grouped.cuh"
 #include "moe.h"
+#include "ptx.cuh"
+#include "range.cuh"
+#include "tmap.cuh"
 
 namespace moe {
 namespace {
@@ -340,101 +344,743 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- products
-// MODE 0: Y, 1: dX, 2: dW. 64 x 64 outputs a block, 4 x 4 a thread, fp32 FMA
-// over 16 steps of the contraction at a time.
+// MODE 0: Y = rows . W[e], 1: dX = rows . W[e]^T, 2: dW[e] = columns^T . columns.
+//
+// Tiles of 128 rows x up to 256 columns on one CTA, or of 256 x 256 on a pair
+// of CTAs (cta_group::2: each stages its own 128 rows and 128 of the columns,
+// so a byte staged feeds twice the products); persistent. A stage of the ring
+// holds 128 steps of the contraction, which is one block of scales: codes by
+// TMA in boxes of 128 x 128 bytes (128-byte swizzle; a warp loads each side)
+// as they lie in memory, k- or row-major as the mode has it (the tensor core
+// takes 8-bit operands either way, so the one copy of W serves both
+// products); a warp spreads the stage's scale bytes to chunks of 512, in the
+// order the tensor core reads them. One thread copies a stage's chunks to
+// tensor memory (tcgen05.cp) and issues the products of 128 columns x 32
+// steps (kind::mxf8f6f4) that read them. A pair's product takes 64 columns of
+// each CTA's 128, so its two accumulators hold columns 0..63 with 128..191, and
+// 64..127 with 192..255. Three accumulators of 128 columns: a tile takes two,
+// and the next tile starts once one of them is drained, with the first half's
+// products of its first stages. Eight warps drain: into registers, which
+// frees the accumulator, and then to out.
+namespace f8 {
+using namespace ptx;
+constexpr int HN = 128, KS = 128;  // an accumulator's columns, a stage's steps
+constexpr int BOX = 128 * 128, CHUNK = 512;
+constexpr int SF_COL = 384, SF_STAGE = 12;  // tensor memory columns: 3 x 128, then scales
+constexpr int TMEM_COLS = 512, ACCS = 3;
+constexpr int EPI_THREADS = 256, THREADS = 128 + EPI_THREADS;
+
+template <bool PAIR>
+struct Cfg {
+  static constexpr int BM = PAIR ? 256 : 128;
+  static constexpr int B_BOXES = PAIR ? 1 : 2;
+  static constexpr int OFF_B = BOX, OFF_SFA = OFF_B + B_BOXES * BOX, OFF_SFB = OFF_SFA + CHUNK;
+  static constexpr int STAGE = (OFF_SFB + 2 * CHUNK + 1023) / 1024 * 1024;
+  static constexpr int STAGES = PAIR ? 6 : 4;  // (shared memory's most)
+  static constexpr int OFF_BAR = STAGES * STAGE;
+  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
+  static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
+  static_assert(SMEM <= 227 * 1024, "shared memory");
+  static_assert(SF_COL + STAGES * SF_STAGE <= TMEM_COLS, "tensor memory");
+};
+
 struct Params {
-  const uint8_t *a, *as, *b, *bs;
+  const uint8_t *as, *bs;  // scales
   const int32_t* offsets;
   void* out;
   uint32_t* err;
-  int E, R, K, N, silu;
+  uint32_t* ctr;  // arrivals per tile of a split launch, zero between launches
+  float* part;    // [CTA][2][kMx4SplitRows][256]
+  int E, R, K, N;
+  int silu;
 };
-__device__ __forceinline__ float value_of(uint32_t code, uint32_t s) {
-  return code_values(code).x * scale_value(s);
+
+// kind::mxf8f6f4, E4M3 both sides, E8M0 scales, fp32 accumulator, K = 32; an
+// operand whose rows are the contraction's steps is "transposed"
+constexpr uint32_t idesc(int m, int n, bool a_steps, bool b_steps) {
+  return (a_steps ? 1u << 15 : 0u) | (b_steps ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 7) << 27);
+}
+// Operand descriptors: the low word holds the address (and, not used by
+// operands of one 128-byte column, the distance of the next), the high one
+// does not change (128-byte swizzle, groups of 8 rows 1024 bytes apart,
+// version 1).
+constexpr uint32_t AB_HI = (1024 >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t SF_HI = (128 >> 4) | 1u << 14;  // no swizzle, 8-row groups 128 bytes apart
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+  return (saddr & 0x3FFFFu) >> 4 | (BOX >> 4) << 16;
+}
+__device__ __forceinline__ uint32_t sf_lo(uint32_t saddr) { return (saddr & 0x3FFFFu) >> 4; }
+
+template <bool PAIR>
+__device__ __forceinline__ void mma(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t sfa,
+                                    uint32_t sfb, uint32_t accumulate) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(AB_HI)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], a, b, %3, "
+        "[%4], [%5], p;\n\t}\n" ::"r"(d),
+        "r"(a), "r"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(AB_HI)
+        : "memory");
+}
+// 32 rows of 16 bytes, contiguous, to 4 columns of all four lane quarters
+// (of a pair: in each CTA from its own shared memory).
+template <bool PAIR>
+__device__ __forceinline__ void cp_scales(uint32_t taddr, uint32_t desc) {
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], a;\n\t}\n" ::"r"(taddr),
+        "r"(desc), "r"(SF_HI)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .b64 a;\n\tmov.b64 a, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], a;\n\t}\n" ::"r"(taddr),
+        "r"(desc), "r"(SF_HI)
+        : "memory");
+}
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR)
+    tc_commit_pair_mc(bar, 0x3);
+  else
+    tc_commit(bar);
+}
+__device__ __forceinline__ void bar_epi() {
+  asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+}
+__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                           uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
+}
+__device__ __forceinline__ void st_shared1(uint32_t addr, uint32_t a) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 
-template <int MODE, typename TO>
-__global__ void __launch_bounds__(256) fp8_product_kernel(const Params p) {
-  __shared__ int seg[kMaxExperts + 1], base[kMaxExperts + 1], ok;
-  __shared__ float As[16][65], Bs[16][65];
+// Tile t of a weight gradient: expert by expert, its rows (of K) inside
+template <int BM>
+__device__ __forceinline__ Tile grad_tile(int t, int K, int N) {
+  const int mt = up_div(K, BM), each = mt * up_div(N, kTileCols);
+  Tile r;
+  r.e = t / each;
+  const int l = t - r.e * each, nb = l / mt;
+  r.mt = 0;
+  r.row0 = (l - nb * mt) * BM;
+  r.rows = min(BM, K - r.row0);
+  r.n0 = nb * kTileCols;
+  r.n = min(kTileCols, N - r.n0);
+  return r;
+}
+}  // namespace f8
+
+template <int MODE, bool PAIR, typename TO>
+__global__ void __launch_bounds__(f8::THREADS, 1)
+    fp8_product_kernel(const __grid_constant__ CUtensorMap tmA,
+                       const __grid_constant__ CUtensorMap tmA32,
+                       const __grid_constant__ CUtensorMap tmB, const f8::Params p) {
+  using namespace f8;
+  using C = Cfg<PAIR>;
+  constexpr int STAGES = C::STAGES, BM = C::BM;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // pair: the even CTA's
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + ACCS;  // pair: the even CTA's
+  uint64_t* drain = tempty + ACCS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  int* s_ok = reinterpret_cast<int*>(tmem_slot + 1);
+  uint32_t* s_last = tmem_slot + 2;
+  int* s_wide = reinterpret_cast<int*>(tmem_slot + 3);
+  int* seg = reinterpret_cast<int*>(smem + C::OFF_SEG);
+  int* base = seg + kMaxExperts + 1;
+  int* tb = PAIR ? base + kMaxExperts + 1 : base;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const int cta = PAIR ? blockIdx.x >> 1 : blockIdx.x, grid = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int E = p.E, K = p.K, N = p.N;
+  const int width = MODE == 1 ? K : N, len = MODE == 1 ? N : K;  // (len: of the rows' modes)
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], PAIR ? 3 : 2);
+      mbar_init(&empty[i], 1);
+    }
+    for (int i = 0; i < ACCS; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], PAIR ? 16 : 8);
+    }
+    mbar_init(drain, 1);
+    *s_wide = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    if constexpr (PAIR) {
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
   pdl_wait();
   pdl_trigger();
-  if (!load_segments(p.offsets, p.E, p.R, seg, base, &ok, p.err)) return;
-  const int tid = threadIdx.x, K = p.K, N = p.N;
-  const int width = MODE == 1 ? K : N;  // of the output
-  const int c0 = blockIdx.x * 64;
-  int e, row0, rows, len, tile0 = 0;  // output rows; the contraction
-  size_t out0;
-  if constexpr (MODE == 2) {
-    const int mt = up_div(K, 64);
-    e = blockIdx.y / mt;
-    row0 = (blockIdx.y - e * mt) * 64;
-    rows = K - row0;
-    len = (base[e + 1] - base[e]) * 128;
-    tile0 = base[e];
-    out0 = static_cast<size_t>(e) * K + row0;
-  } else {
-    const int rt = blockIdx.y >> 1;
-    if (rt >= base[p.E]) return;
-    e = last_at_most(base, p.E - 1, rt);
-    row0 = seg[e] + (rt - base[e]) * 128 + (blockIdx.y & 1) * 64;
-    rows = seg[e + 1] - row0;
-    len = MODE == 1 ? N : K;
-    out0 = row0;
-  }
-  if (rows <= 0) return;
-  rows = min(rows, 64);
-  const int nbk = up_div(K, 128), nbn = up_div(N, 128), pitch = (up_div(len, 128) + 3) & ~3;
-  float acc[4][4] = {};
-  const int ty = tid / 16, tx = tid % 16;
-  for (int k0 = 0; k0 < len; k0 += 16) {
-    for (int i = tid; i < 1024; i += 256) {
-      const int r = i / 16, k = k0 + i % 16;
-      float a = 0.f, b = 0.f;
-      if (MODE != 2 && r < rows)
-        a = value_of(p.a[static_cast<size_t>(row0 + r) * len + k],
-                     p.as[static_cast<size_t>(row0 + r) * pitch + k / 128]);
-      if (MODE == 2 && r < rows)
-        a = value_of(p.a[(static_cast<size_t>(tile0) * 128 + k) * K + row0 + r],
-                     p.as[(static_cast<size_t>(tile0) + k / 128) * K + row0 + r]);
-      const int c = c0 + r;
-      if (MODE == 0 && c < N)
-        b = value_of(p.b[(static_cast<size_t>(e) * K + k) * N + c],
-                     p.bs[(static_cast<size_t>(e) * nbk + k / 128) * nbn + c / 128]);
-      if (MODE == 1 && c < K)
-        b = value_of(p.b[(static_cast<size_t>(e) * K + c) * N + k],
-                     p.bs[(static_cast<size_t>(e) * nbk + c / 128) * nbn + k / 128]);
-      if (MODE == 2 && c < N)
-        b = value_of(p.b[(static_cast<size_t>(tile0) * 128 + k) * N + c],
-                     p.bs[(static_cast<size_t>(tile0) + k / 128) * N + c]);
-      As[i % 16][r] = a;
-      Bs[i % 16][r] = b;
+  const bool ok = load_segments(p.offsets, E, p.R, seg, base, s_ok, p.err);
+  for (int e = tid; ok && e < E; e += THREADS)
+    if (seg[e + 1] - seg[e] > kMx4SplitRows) *s_wide = 1;
+  if (MODE != 2 && PAIR && warp == 0) {
+    // tiles of 256 rows before each expert
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane, n = e < E ? (base[e + 1] - base[e] + 1) / 2 : 0;
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      if (e < E) tb[e] = run + inc - n;
+      run += __shfl_sync(0xffffffffu, inc, 31);
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][ty * 4 + i], Bs[k][tx * 4 + j], acc[i][j]);
-    __syncthreads();
+    if (lane == 0) tb[E] = run;
   }
-  TO* out = static_cast<TO*>(p.out);
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = ty * 4 + i, c = c0 + tx * 4 + j;
-      if (r < rows && c < width)
-        out[(out0 + r) * width + c] = static_cast<TO>(p.silu ? silu_of<TO>(acc[i][j]) : acc[i][j]);
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers exist before anyone signals them
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const int kst = up_div(len, KS);
+  const int tiles = !ok         ? 0
+                    : MODE == 2 ? E * up_div(K, BM) * up_div(N, kTileCols)
+                                : tb[E] * up_div(width, kTileCols);
+  auto tile = [&](int t) {
+    if constexpr (MODE == 2)
+      return grad_tile<BM>(t, K, N);
+    else
+      return tile_at<BM>(t, seg, base, tb, E, width);
+  };
+  // Few rows everywhere and fewer tiles than CTAs: the tiles' stages are one
+  // sequence cut into equal ranges, and a tile's partial sums are joined by
+  // the last CTA to arrive, in CTA order. Otherwise whole tiles in turn.
+  const bool split = MODE != 2 && !PAIR && tiles < grid && *s_wide == 0;
+  const Range rg(split ? tiles : 0, kst, grid);
+  // Walk this CTA's pieces: f(tile, first stage, end stage)
+  auto walk = [&](auto f) {
+    if (split) {
+      const int end = rg.start(cta + 1);
+      for (int i = rg.start(cta); i < end;) {
+        const int t = i / kst, k0 = i - t * kst, k1 = min(kst, k0 + end - i);
+        if (!f(t, k0, k1)) return;
+        i += k1 - k0;
+      }
+    } else {
+      for (int t = cta; t < tiles; t += grid) {
+        int k1 = kst;
+        if constexpr (MODE == 2) {
+          const int e = tile(t).e;
+          k1 = base[e + 1] - base[e];
+        }
+        if (!f(t, 0, k1)) return;
+      }
     }
+  };
+
+  if (warp == 0 || warp == 2) {
+    // the first loads the A side, the other the B side (the whole warp,
+    // converged: elect_one says why)
+    const bool a_side = warp == 0;
+    if (lane == 0) {
+      prefetch_tmap(&tmA);
+      prefetch_tmap(&tmA32);
+      prefetch_tmap(&tmB);
+    }
+    __syncwarp();
+    int s = 0, used = 0;
+    uint32_t ph = 0;
+    bool dead = false;
+    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
+    auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
+      if constexpr (PAIR)
+        tma_load_2d_pair(dst, m, bar0 + s * 8, c0, c1);
+      else
+        tma_load_2d(dst, m, &full[s], c0, c1);
+    };
+    auto load3 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1, int c2) {
+      if constexpr (PAIR)
+        tma_load_3d_pair(dst, m, bar0 + s * 8, c0, c1, c2);
+      else
+        tma_load_3d(dst, m, &full[s], c0, c1, c2);
+    };
+    walk([&](int t, int k0, int k1) {
+      const Tile tl = tile(t);
+      // CTA r's rows come in one box of 128 or, few, of 32, its columns in
+      // boxes of 128; what is not loaded feeds only sums that are not stored
+      auto a_bytes = [&](int r) {
+        const int left = tl.rows - r * 128;
+        return left <= 0 ? 0 : (MODE != 2 && left <= 32 ? BOX / 4 : BOX);
+      };
+      auto b_boxes = [&](int r) {
+        const int left = tl.n - r * 128;
+        return PAIR ? (left > 0 ? 1 : 0) : (left > 128 ? 2 : 1);
+      };
+      auto bytes = [&](int r) { return a_bytes(r) + b_boxes(r) * BOX; };
+      const int na = a_bytes(rank), nb = b_boxes(rank);
+      const uint32_t expect = PAIR ? bytes(0) + bytes(1) : bytes(0);
+      const CUtensorMap* ma = na == BOX ? &tmA : &tmA32;
+      const int row0 = tl.row0 + rank * 128, col0 = tl.n0 + rank * 128;
+      const int first = MODE == 2 ? base[tl.e] * 128 : 0;
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
+          dead = true;
+          return false;
+        }
+        if (used < STAGES) ++used;
+        if (elect_one()) {
+          uint8_t* st = smem + s * C::STAGE;
+          if (a_side) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
+            if (na > 0) {
+              if constexpr (MODE == 2)
+                load2(st, &tmA, row0, first + kb * KS);
+              else
+                load2(st, ma, kb * KS, row0);
+            }
+          } else {
+#pragma unroll
+            for (int b = 0; b < C::B_BOXES; ++b)
+              if (b < nb) {
+                uint8_t* dst = st + C::OFF_B + b * BOX;
+                if constexpr (MODE == 2)
+                  load2(dst, &tmB, col0 + b * 128, first + kb * KS);
+                else if constexpr (MODE == 1)
+                  load3(dst, &tmB, kb * KS, col0 + b * 128, tl.e);
+                else
+                  load3(dst, &tmB, col0 + b * 128, kb * KS, tl.e);
+              }
+          }
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      return true;
+    });
+    // the latest use of each stage has landed before this CTA may exit (a
+    // pair: the even CTA's barrier counts both, and both exit together)
+    for (int j = 0; a_side && rank == 0 && j < used; ++j) {
+      if (s == 0) {
+        s = STAGES;
+        ph ^= 1u;
+      }
+      --s;
+      if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
+        dead = true;
+        break;
+      }
+    }
+    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
+  } else if (warp == 3) {
+    // a stage's scales, as chunks: row i's byte four times at (i % 32) 16 + (i
+    // / 32) 4. Loaded four stages at a time, four stages ahead.
+    int s = 0;
+    uint32_t ph = 0;
+    bool dead = false;
+    const uint32_t base0 = smem_u32(smem);
+    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
+    const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
+    constexpr uint32_t ONE = 0x7f7f7f7fu;
+    walk([&](int t, int k0, int k1) {
+      const Tile tl = tile(t);
+      const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
+      struct Quad {
+        uint32_t w[MODE == 2 ? 12 : 5];
+      } cur, nxt;
+      auto load = [&](int q) {
+        Quad r;
+        if constexpr (MODE == 2) {
+          // a lane's four neighbouring rows (of K) and columns
+          const int m = tl.row0 + static_cast<int>(rank) * 128 + 4 * lane;
+          const int c = PAIR ? tl.n0 + (lane < 16 ? 0 : 64) + 4 * lane : tl.n0 + 4 * lane;
+          constexpr int NEXT = PAIR ? 64 : 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kb = min(q * 4 + i, k1 - 1);
+            const uint8_t* a = p.as + static_cast<size_t>(base[tl.e] + kb) * K;
+            const uint8_t* b = p.bs + static_cast<size_t>(base[tl.e] + kb) * N;
+            r.w[i * 3] = m < K ? __ldg(reinterpret_cast<const uint32_t*>(a + m)) : ONE;
+            r.w[i * 3 + 1] = c < N ? __ldg(reinterpret_cast<const uint32_t*>(b + c)) : ONE;
+            r.w[i * 3 + 2] =
+                c + NEXT < N ? __ldg(reinterpret_cast<const uint32_t*>(b + c + NEXT)) : ONE;
+          }
+        } else {
+          // rows lane + 32 i, four blocks each; lanes 0..7: a block of the two
+          // blocks of columns each
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = tl.row0 + static_cast<int>(rank) * 128 + min(lane + 32 * i, rows - 1);
+            r.w[i] = rows > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
+                                    p.as + static_cast<size_t>(row) * pitch + q * 4))
+                              : ONE;
+          }
+          const int nb = min(tl.n0 / 128 + (lane & 1), up_div(width, 128) - 1);
+          const int kb = min(q * 4 + (lane >> 1 & 3), kst - 1);
+          const int at = MODE == 1 ? nb * nbn + kb : kb * nbn + nb;
+          r.w[4] = __ldg(p.bs + static_cast<size_t>(tl.e) * nbk * nbn + at);
+        }
+        return r;
+      };
+      if (k0 < k1) nxt = load(k0 >> 2);
+      for (int kb = k0; kb < k1; ++kb) {
+        const int i = kb & 3;
+        if (kb == k0 || i == 0) {
+          cur = nxt;
+          if ((kb >> 2) * 4 + 4 < k1) nxt = load((kb >> 2) + 1);
+        }
+        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
+          dead = true;
+          return false;
+        }
+        const uint32_t sfa = base0 + s * C::STAGE + C::OFF_SFA;
+        if constexpr (MODE == 2) {
+          const uint32_t at = (lane & 7) * 64 + (lane >> 3) * 4;
+#pragma unroll
+          for (int c = 0; c < 3; ++c) {
+            const uint32_t w = i == 0 ? cur.w[c] : i == 1 ? cur.w[3 + c]
+                               : i == 2 ? cur.w[6 + c] : cur.w[9 + c];
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              st_shared1(sfa + c * CHUNK + at + b * 16, __byte_perm(w, 0, 0x1111 * b));
+          }
+        } else {
+          const uint32_t sel = 0x1111u * i;
+          st_shared4(sfa + lane * 16, __byte_perm(cur.w[0], 0, sel), __byte_perm(cur.w[1], 0, sel),
+                     __byte_perm(cur.w[2], 0, sel), __byte_perm(cur.w[3], 0, sel));
+          const uint32_t s0 = __shfl_sync(0xffffffffu, cur.w[4], i * 2) * 0x01010101u;
+          const uint32_t s1 = __shfl_sync(0xffffffffu, cur.w[4], i * 2 + 1) * 0x01010101u;
+          const uint32_t sfb = sfa + CHUNK + lane * 16;
+          if constexpr (PAIR) {
+            st_shared4(sfb, s0, s0, s1, s1);
+            st_shared4(sfb + CHUNK, s0, s0, s1, s1);
+          } else {
+            st_shared4(sfb, s0, s0, s0, s0);
+            st_shared4(sfb + CHUNK, s1, s1, s1, s1);
+          }
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && rank != 0)
+            mbar_arrive_remote(bar0 + s * 8);
+          else
+            mbar_arrive(&full[s]);
+        }
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      return true;
+    });
+    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
+  } else if (warp == 1) {
+    // (one lane issues: elect_one says how)
+    if (rank == 0) {
+      int s = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool dead = false;
+      constexpr bool A_STEPS = MODE == 2, B_STEPS = MODE != 1;
+      constexpr uint32_t id = idesc(BM, HN, A_STEPS, B_STEPS);
+      // 32 steps on: 32 rows of 128 bytes, or 32 bytes of a row
+      constexpr uint32_t A_ON = A_STEPS ? 4096 >> 4 : 32 >> 4, B_ON = B_STEPS ? 4096 >> 4 : 32 >> 4;
+      // the other 128 (pair: 64) columns
+      constexpr uint32_t B_HALF = !PAIR ? BOX >> 4 : B_STEPS ? 64 >> 4 : (64 * 128) >> 4;
+      const uint32_t base0 = smem_u32(smem);
+      const uint32_t ad0 = desc_lo(base0), bd0 = desc_lo(base0 + C::OFF_B),
+                     sa0 = sf_lo(base0 + C::OFF_SFA);
+      auto take = [&] {
+        const bool there = PAIR ? mbar_wait_spin_cluster(&full[s], ph, kWaitLimitNs)
+                                : mbar_wait_spin(&full[s], ph, kWaitLimitNs);
+        if (there) tc_fence_after();
+        return there;
+      };
+      auto next = [&] {
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
+        }
+      };
+      // a stage's scales, and its products for the halves j0..j1 of the
+      // columns (inlined with constants for whole stages)
+      auto scales = [&](int nj) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
+        cp_scales<PAIR>(sf, sa0 + off);
+#pragma unroll
+        for (int j = 0; j < nj; ++j)
+          cp_scales<PAIR>(sf + 4 + j * 4, sa0 + off + (j + 1) * (CHUNK / 16));
+      };
+      auto products = [&](int steps, int j0, int j1, uint32_t d0, uint32_t d1, uint32_t more) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
+#pragma unroll
+        for (int kk = 0; kk < steps; ++kk)
+#pragma unroll
+          for (int j = j0; j < j1; ++j)
+            mma<PAIR>(j == 0 ? d0 : d1, ad0 + off + kk * A_ON, bd0 + off + j * B_HALF + kk * B_ON,
+                      id, sf, sf + 4 + j * 4, kk > 0 ? 1u : more);
+      };
+      if (elect_one()) walk([&](int t, int k0, int k1) {
+        if (k0 == k1) return true;
+        const int n = tile(t).n;
+        const int nj = n > (PAIR ? 64 : HN) ? 2 : 1;
+        const int acc1 = acc + 1 == ACCS ? 0 : acc + 1;
+        const uint32_t aph1 = acc + 1 == ACCS ? aph ^ 1u : aph;
+        if (!mbar_wait_spin_cluster(&tempty[acc], aph ^ 1u, kWaitLimitNs)) {
+          dead = true;
+          return false;
+        }
+        tc_fence_after();
+        const uint32_t d0 = tmem_base + acc * HN, d1 = tmem_base + acc1 * HN;
+        // stages with nothing left out
+        const int whole = nj == 2 ? (MODE == 2 ? k1 : len / KS) : 0;
+        int kb = k0;
+        if (nj == 2) {
+          // until the second accumulator is drained too: the first half's
+          // products of a few stages, and after that the second's
+          const int s0 = s, most = min(min(k1, whole), k0 + STAGES - 1);
+          const uint32_t ph0 = ph;
+          while (kb < most && !mbar_test_wait_cluster(&tempty[acc1], aph1 ^ 1u)) {
+            if (!take()) {
+              dead = true;
+              return false;
+            }
+            scales(2);
+            products(4, 0, 1, d0, d1, kb > k0 ? 1u : 0u);
+            next();
+            ++kb;
+          }
+          if (!mbar_wait_spin_cluster(&tempty[acc1], aph1 ^ 1u, kWaitLimitNs)) {
+            dead = true;
+            return false;
+          }
+          tc_fence_after();
+          s = s0;
+          ph = ph0;
+          for (int i = k0; i < kb; ++i) {
+            products(4, 1, 2, d0, d1, i > k0 ? 1u : 0u);
+            commit<PAIR>(&empty[s]);
+            next();
+          }
+        }
+        for (; kb < k1; ++kb) {
+          if (!take()) {
+            dead = true;
+            break;
+          }
+          const uint32_t more = kb > k0 ? 1u : 0u;
+          if (kb < whole) {
+            scales(2);
+            products(4, 0, 2, d0, d1, more);
+          } else {
+            scales(nj);
+            products(MODE == 2 ? 4 : min(4, (len - kb * KS) / 32), 0, nj, d0, d1, more);
+          }
+          commit<PAIR>(&empty[s]);
+          next();
+        }
+        for (int j = 0; j < nj; ++j) {
+          commit<PAIR>(&tfull[acc]);
+          if (++acc == ACCS) {
+            acc = 0;
+            aph ^= 1u;
+          }
+        }
+        return !dead;
+      });
+      dead = __any_sync(0xffffffffu, dead);
+      if (elect_one()) {
+        if constexpr (PAIR)
+          tc_commit_pair_mc(drain, 0x1);
+        else
+          tc_commit(drain);
+      }
+      __syncwarp();
+      if ((!mbar_wait(drain, 0, kWaitLimitNs) || dead) && lane == 0) atomicOr(p.err, kErrTimeout);
+    }
+  } else if (warp >= 4) {
+    // two warps to a quarter of the rows, 64 of an accumulator's columns each
+    const int w = warp & 3, half = (warp - 4) >> 2;
+    int acc = 0;
+    uint32_t aph = 0;
+    bool dead = false;
+    TO* out = static_cast<TO*>(p.out);
+    const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
+    auto finish = [&](float v) { return MODE == 0 && p.silu ? silu_of<TO>(v) : v; };
+    const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
+    walk([&](int t, int k0, int k1) {
+      const Tile tl = tile(t);
+      const bool whole = MODE == 2 || (k0 == 0 && k1 == kst);
+      // rows of this warp's 32 lanes
+      const int r0 = static_cast<int>(rank) * 128 + w * 32, rows = min(32, tl.rows - r0);
+      const size_t out_row = (MODE == 2 ? static_cast<size_t>(tl.e) * K : 0) + tl.row0 + r0;
+      const int first = split ? rg.owner(t * kst) : 0;
+      // a CTA's part of the tile its range starts in comes first, of the one
+      // it ends in second
+      auto slice = [&](int c) {
+        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * kTileCols;
+      };
+      const int nj = tl.n > (PAIR ? 64 : HN) ? 2 : 1;
+      for (int j = 0; j < nj; ++j) {
+        const int col = PAIR ? half * 128 + j * 64 : j * 128 + half * 64;
+        const bool some = rows > 0 && col < tl.n;
+        uint32_t r[2][32];
+        if (MODE == 2 && k0 == k1) {
+          // an expert without rows
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) r[i][c] = 0;
+        } else {
+          // after a wait that ran out the loops go on, so that the eight warps
+          // still meet at every barrier
+          if (!dead && !mbar_wait(&tfull[acc], aph, kWaitLimitNs)) dead = true;
+          dead = __any_sync(0xffffffffu, dead);
+          tc_fence_after();
+          if (some) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+              tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN +
+                                     half * 64 + i * 32,
+                                 r[i]);
+            tmem_ld_wait();
+          }
+          // free before the stores: the next tile waits for this one's first half
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR)
+              mbar_arrive_remote(leader_tempty + acc * 8);
+            else
+              mbar_arrive(&tempty[acc]);
+          }
+          if (++acc == ACCS) {
+            acc = 0;
+            aph ^= 1u;
+          }
+        }
+        if (some && whole) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            put_rows32(out, sectors, out_row, rows, width, tl.n0 + col + i * 32, r[i], finish);
+        } else if (some && lane < rows) {
+          // (at most kMx4SplitRows rows: the first quarter's)
+          uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * kTileCols + col);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+              const uint32_t v[8] = {r[i][c],     r[i][c + 1], r[i][c + 2], r[i][c + 3],
+                                     r[i][c + 4], r[i][c + 5], r[i][c + 6], r[i][c + 7]};
+              st_sector(true, o + i * 32 + c, v);
+            }
+        }
+      }
+      if (!whole) {
+        const int last_cta = rg.owner((t + 1) * kst - 1);
+        __threadfence();
+        bar_epi();
+        if (tid == 128) {
+          const bool last = atomicAdd(p.ctr + t, 1u) == static_cast<uint32_t>(last_cta - first);
+          if (last) p.ctr[t] = 0;
+          *s_last = last ? 1u : 0u;
+        }
+        bar_epi();
+        if (*s_last != 0) {
+          __threadfence();
+          const int quads = tl.n / 4;
+          for (int i = tid - 128; i < tl.rows * quads; i += EPI_THREADS) {
+            const int row = i / quads, col = (i - row * quads) * 4;
+            float4 v = {0.f, 0.f, 0.f, 0.f};
+            for (int cb = first; cb <= last_cta; cb += 8) {
+              float4 o[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                o[j] = cb + j <= last_cta
+                           ? __ldcg(reinterpret_cast<const float4*>(slice(cb + j) +
+                                                                    row * kTileCols + col))
+                           : float4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                v.x += o[j].x;
+                v.y += o[j].y;
+                v.z += o[j].z;
+                v.w += o[j].w;
+              }
+            }
+            TO* o = out + static_cast<size_t>(tl.row0 + row) * width + tl.n0 + col;
+            o[0] = static_cast<TO>(finish(v.x));
+            o[1] = static_cast<TO>(finish(v.y));
+            o[2] = static_cast<TO>(finish(v.z));
+            o[3] = static_cast<TO>(finish(v.w));
+          }
+        }
+      }
+      return true;
+    });
+    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if constexpr (PAIR) cluster_sync();
+  tc_fence_after();
+  if (warp == 1) {
+    if constexpr (PAIR)
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, TMEM_COLS);
+  }
 }
 
-template <int MODE, typename TO>
-cudaError_t launch_mode(const Params& p, cudaStream_t s) {
-  const int width = MODE == 1 ? p.K : p.N;
-  const int tall = MODE == 2 ? p.E * up_div(p.K, 64) : 2 * static_cast<int>(row_tiles(p.R, p.E));
-  return launch_pdl(fp8_product_kernel<MODE, TO>, dim3(up_div(width, 64), tall), dim3(256), 0, s, p);
+template <int MODE, bool PAIR, typename TO>
+cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mA32, const CUtensorMap& mB,
+                           const f8::Params& p, int grid, cudaStream_t s) {
+  using C = f8::Cfg<PAIR>;
+  auto* kernel = fp8_product_kernel<MODE, PAIR, TO>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3(PAIR ? grid / 2 * 2 : grid);
+  lc.blockDim = dim3(f8::THREADS);
+  lc.dynamicSmemBytes = C::SMEM;
+  lc.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  lc.attrs = attr;
+  lc.numAttrs = PAIR ? 2 : 1;
+  return cudaLaunchKernelEx(&lc, kernel, mA, mA32, mB, p);
 }
 
 template <typename T, int ACT>
@@ -509,12 +1155,30 @@ cudaError_t launch_fp8_back(int dtype, const uint8_t* q, const uint8_t* sc, int 
 cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, const uint8_t* b,
                                const uint8_t* bs, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,
-                               cudaStream_t s) {
-  const Params p{a, as, b, bs, offsets, out, err, E, R, K, N, silu};
-  if (mode == 2) return launch_mode<2, float>(p, s);
+                               uint32_t* ctr, float* part, int num_sms, cudaStream_t s) {
+  CUtensorMap mA, mA32, mB;
+  const uint64_t cr = row_tiles(R, E) * 128;
+  const uint64_t len = mode == 1 ? N : K;
+  if (mode == 2 ? !make_map_2d_bytes(&mA, a, cr, K, 128) || !make_map_2d_bytes(&mB, b, cr, N, 128)
+                : !make_map_2d_bytes(&mA, a, R, len, 128) ||
+                      !make_map_2d_bytes(&mA32, a, R, len, 32) ||
+                      !make_map_3d_bytes(&mB, b, E, K, N))
+    return cudaErrorInvalidValue;
+  if (mode == 2) mA32 = mA;
+  const f8::Params p{as, bs, offsets, out, err, ctr, part, E, R, K, N, silu};
+  const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
+  if (mode == 2) return launch_product<2, true, float>(mA, mA32, mB, p, grid, s);
+  const bool pair = R >= kMx4PairRows * E;
+  auto go = [&](auto kernel) { return kernel(mA, mA32, mB, p, grid, s); };
   if (mode == 1)
-    return out_f32 ? launch_mode<1, float>(p, s) : launch_mode<1, __nv_bfloat16>(p, s);
-  return out_f32 ? launch_mode<0, float>(p, s) : launch_mode<0, __nv_bfloat16>(p, s);
+    return pair ? (out_f32 ? go(launch_product<1, true, float>)
+                           : go(launch_product<1, true, __nv_bfloat16>))
+                : (out_f32 ? go(launch_product<1, false, float>)
+                           : go(launch_product<1, false, __nv_bfloat16>));
+  return pair ? (out_f32 ? go(launch_product<0, true, float>)
+                         : go(launch_product<0, true, __nv_bfloat16>))
+              : (out_f32 ? go(launch_product<0, false, float>)
+                         : go(launch_product<0, false, __nv_bfloat16>));
 }
 
 }  // namespace moe

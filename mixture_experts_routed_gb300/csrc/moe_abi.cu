@@ -1136,7 +1136,8 @@ int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_fp8_product(transposed, q, scale, wq, w_scale, offsets, c.E, c.R, c.K,
                                       c.N, c.out_dtype == MOE_DTYPE_F32 ? 1 : 0, c.silu, out,
-                                      static_cast<uint32_t*>(ws), as_stream(stream)));
+                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kMx4CtrOffset),
+                                      at<float>(ws, kMx4PartOffset), sms, as_stream(stream)));
 }
 
 int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const uint8_t* x_scale,
@@ -1160,7 +1161,9 @@ int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const ui
   const int sms = num_sms();
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_fp8_product(2, xq, x_scale, dyq, dy_scale, offsets, c.E, c.R, c.K, c.N,
-                                      1, 0, dW, static_cast<uint32_t*>(ws), as_stream(stream)));
+                                      1, 0, dW, static_cast<uint32_t*>(ws),
+                                      at<uint32_t>(ws, kMx4CtrOffset), at<float>(ws, kMx4PartOffset),
+                                      sms, as_stream(stream)));
 }
 
 int moe_fp8_dequantize_weights(const moe_fp8_config_t* cfg, const uint8_t* wq,

@@ -1,5 +1,5 @@
-// tmap.cu - TMA tensor maps of bytes and of scale chunks, for the 4-bit
-// products (tmap.cuh).
+// tmap.cu - TMA tensor maps of bytes and of scale chunks, for the 4- and
+// 8-bit products (tmap.cuh).
 #include "tmap.cuh"
 
 #include <cuda_runtime.h>
@@ -35,6 +35,20 @@ bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t
   const cuuint32_t box[2] = {128, box_rows};
   const cuuint32_t estr[2] = {1, 1};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_3d_bytes(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows,
+                       uint64_t cols) {
+  const auto enc = encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {cols, rows, mats};
+  const cuuint64_t strides[2] = {cols, rows * cols};
+  const cuuint32_t box[3] = {128, 128, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

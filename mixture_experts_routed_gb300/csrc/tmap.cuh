@@ -19,6 +19,11 @@ bool make_map_2d(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
 bool make_map_2d_bytes(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
                        uint32_t box_rows);
 
+// 3-D map over row-major [mats, rows, cols] bytes (cols a multiple of 16), box
+// [128 rows][128 bytes] of one of them, 128-byte swizzle, zero fill outside.
+bool make_map_3d_bytes(CUtensorMap* m, const void* base, uint64_t mats, uint64_t rows,
+                       uint64_t cols);
+
 // 3-D map over [tiles][groups] chunks of 512 bytes (128 words), box of
 // box_tiles x two chunks, no swizzle, zero fill outside.
 bool make_map_3d_chunks(CUtensorMap* m, const void* base, uint64_t tiles, uint64_t groups,
