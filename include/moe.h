@@ -543,7 +543,9 @@ MOE_API int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* 
  * pitch = ceil(C / 128) rounded up to 4 (the padding is not read). Columns:
  * blocks of 128 rows of one expert, whose segment is cut into tiles of 128
  * from its start, one expert after the other; codes [tile * 128 + row, C],
- * zeros past a segment's end, scales [tile, C]. Weights: blocks of 128 x 128
+ * zeros past a segment's end, scales [tile, ceil(C / 128), 128], those of 128
+ * columns in the order the tensor core reads them: column i at (i % 32) * 4 +
+ * i / 32 (127 past C). Weights: blocks of 128 x 128
  * of each W[e]; codes [E, K, N] as W lies, scales [E, ceil(K / 128),
  * ceil(N / 128)]: the one copy serves the product and its transpose. C is K
  * (rows of x) or N (rows of dy). Code pointers are 16-byte aligned, the
@@ -568,8 +570,8 @@ enum {
 };
 
 /* Sizes (0 for an invalid configuration): bytes of the scales of rows of
- * `cols` columns; rows of a columns' code tensor (a multiple of 128; its
- * scales have a 128th of them); bytes of the weights' scales; bytes of the
+ * `cols` columns; rows of a columns' code tensor (a multiple of 128; a
+ * 128th of them are tiles); bytes of the weights' scales; bytes of the
  * workspace (an error word and split sums; 256-byte aligned; zero it once
  * before its first use and again after a MOE_ERR_TIMEOUT; calls that share
  * one must not overlap). */

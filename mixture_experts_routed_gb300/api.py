@@ -614,8 +614,8 @@ def alloc_fp8_workspace(c, device=None) -> torch.Tensor:
 
 class Fp8Rows(NamedTuple):
     """Quantised rows [R, C]: codes ``q`` and scales ``scale`` [R, pitch] of blocks of 128 along
-    a row, codes ``cq`` [column rows, C] and scales ``cscale`` of blocks of 128 rows of an
-    expert, all uint8; None for a form that was not asked for."""
+    a row, codes ``cq`` [column rows, C] and scales ``cscale`` [tiles, ceil(C / 128), 128] of
+    blocks of 128 rows of an expert, all uint8; None for a form that was not asked for."""
     q: torch.Tensor | None
     scale: torch.Tensor | None
     cq: torch.Tensor | None
@@ -662,7 +662,7 @@ def fp8_quantize_rows(c, x, offsets, *, ws, rows=True, columns=False, src=None, 
     if columns:
         n = int(lib.moe_fp8_column_rows(r))
         cq = torch.empty((n, C), dtype=u8, device=x.device)
-        cscale = torch.empty((n // 128, C), dtype=u8, device=x.device)
+        cscale = torch.empty((n // 128, -(-C // 128), 128), dtype=u8, device=x.device)
     st = lib.moe_fp8_quantize_rows(
         r, C, _shaped("x", x, (R if src is None else c.x_rows, C), dt), _indices("src", src, R),
         _shaped("row_weight", row_weight, (R,), torch.float32), _ACTS[act],
@@ -711,9 +711,10 @@ def fp8_weight_grad(c, x, dy, offsets, *, ws, out=None, stream=None):
         out = torch.empty((E, K, N), dtype=torch.float32, device=_need("x", x.cq).device)
     st = lib.moe_fp8_weight_grad(
         r, _shaped("x.cq", _need("x", x.cq), (n, K), u8),
-        _shaped("x.cscale", x.cscale, (n // 128, K), u8),
+        _shaped("x.cscale", x.cscale, (n // 128, -(-K // 128), 128), u8),
         _shaped("dy.cq", _need("dy", dy.cq), (n, N), u8),
-        _shaped("dy.cscale", dy.cscale, (n // 128, N), u8), _indices("offsets", offsets, E + 1),
+        _shaped("dy.cscale", dy.cscale, (n // 128, -(-N // 128), 128), u8),
+        _indices("offsets", offsets, E + 1),
         _shaped("out", out, (E, K, N), torch.float32), _p(ws), ws.nbytes, _s(stream))
     _check(st, "moe_fp8_weight_grad")
     return out

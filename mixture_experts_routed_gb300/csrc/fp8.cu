@@ -14,7 +14,7 @@
 //             pitch = ceil(C / 128) rounded up to 4 (padding: any bytes)
 //   columns   blocks of 128 rows of one expert, its segment cut into tiles:
 //             codes [tile * 128 + row][C] (zeros past a segment's end), scales
-//             [tile][C]
+//             [tile][ceil(C / 128)][128], column i of 128 at (i % 32) 4 + i / 32
 //   weights   blocks of 128 x 128 of W[e]: codes [E][K][N] as W lies, scales
 //             [E][ceil(K / 128)][ceil(N / 128)]
 //
@@ -229,8 +229,8 @@ __global__ void __launch_bounds__(kRowThreads)
         for (int k = 0; k < kRowThreads / 32; ++k) m = max(m, top[k][tid]);
         const uint32_t s = scale_code(m);
         inv[tid] = inv_scale(s);
-        if (cb * 128 + tid < C)
-          csc[static_cast<size_t>(rt) * C + cb * 128 + tid] = static_cast<uint8_t>(s);
+        csc[(static_cast<size_t>(rt) * nb + cb) * 128 + (tid & 31) * 4 + (tid >> 5)] =
+            static_cast<uint8_t>(s);
       }
       __syncthreads();
       if (in) {
@@ -353,10 +353,14 @@ __global__ void __launch_bounds__(256)
 // TMA in boxes of 128 x 128 bytes (128-byte swizzle; a warp loads each side)
 // as they lie in memory, k- or row-major as the mode has it (the tensor core
 // takes 8-bit operands either way, so the one copy of W serves both
-// products); a warp spreads the stage's scale bytes to chunks of 512, in the
-// order the tensor core reads them. One thread copies a stage's chunks to
-// tensor memory (tcgen05.cp) and issues the products of 128 columns x 32
-// steps (kind::mxf8f6f4) that read them. A pair's product takes 64 columns of
+// products). The warp that loads the columns' side first spreads the stage's
+// scale bytes to chunks of 512, in the order the tensor core reads them: its
+// copy is issued after they are written, so they are there when the copy's
+// bytes are, and a pair's odd CTA needs no arrival of its own at the even
+// one's barrier (a release at cluster scope, which took 1 us a stage: 8192 x
+// 8192 x 8192 in 1131 us). One thread copies a stage's chunks to tensor memory
+// (tcgen05.cp) and issues the products of 128 columns x 32 steps
+// (kind::mxf8f6f4) that read them. A pair's product takes 64 columns of
 // each CTA's 128, so its two accumulators hold columns 0..63 with 128..191, and
 // 64..127 with 192..255. Three accumulators of 128 columns: a tile takes two,
 // and the next tile starts once one of them is drained, with the first half's
@@ -461,14 +465,10 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
 __device__ __forceinline__ void bar_epi() {
   asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
 }
-__device__ __forceinline__ void st_shared4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                           uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-               "r"(d)
+__device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
                : "memory");
-}
-__device__ __forceinline__ void st_shared1(uint32_t addr, uint32_t a) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(a) : "memory");
 }
 
 // Tile t of a weight gradient: expert by expert, its rows (of K) inside
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
 
   if (tid == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], PAIR ? 3 : 2);
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < ACCS; ++i) {
@@ -601,8 +601,8 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   };
 
   if (warp == 0 || warp == 2) {
-    // the first loads the A side, the other the B side (the whole warp,
-    // converged: elect_one says why)
+    // the first loads the A side, the other the scales and the B side (the
+    // whole warp, converged: elect_one says why)
     const bool a_side = warp == 0;
     if (lane == 0) {
       prefetch_tmap(&tmA);
@@ -613,6 +613,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     int s = 0, used = 0;
     uint32_t ph = 0;
     bool dead = false;
+    const uint32_t base0 = smem_u32(smem);
     const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
     auto load2 = [&](uint8_t* dst, const CUtensorMap* m, int c0, int c1) {
       if constexpr (PAIR)
@@ -626,33 +627,40 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       else
         tma_load_3d(dst, m, &full[s], c0, c1, c2);
     };
-    walk([&](int t, int k0, int k1) {
-      const Tile tl = tile(t);
-      // CTA r's rows come in one box of 128 or, few, of 32, its columns in
-      // boxes of 128; what is not loaded feeds only sums that are not stored
-      auto a_bytes = [&](int r) {
-        const int left = tl.rows - r * 128;
-        return left <= 0 ? 0 : (MODE != 2 && left <= 32 ? BOX / 4 : BOX);
-      };
-      auto b_boxes = [&](int r) {
-        const int left = tl.n - r * 128;
-        return PAIR ? (left > 0 ? 1 : 0) : (left > 128 ? 2 : 1);
-      };
-      auto bytes = [&](int r) { return a_bytes(r) + b_boxes(r) * BOX; };
-      const int na = a_bytes(rank), nb = b_boxes(rank);
-      const uint32_t expect = PAIR ? bytes(0) + bytes(1) : bytes(0);
-      const CUtensorMap* ma = na == BOX ? &tmA : &tmA32;
-      const int row0 = tl.row0 + rank * 128, col0 = tl.n0 + rank * 128;
-      const int first = MODE == 2 ? base[tl.e] * 128 : 0;
-      for (int kb = k0; kb < k1; ++kb) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
-          dead = true;
-          return false;
-        }
-        if (used < STAGES) ++used;
-        if (elect_one()) {
-          uint8_t* st = smem + s * C::STAGE;
-          if (a_side) {
+    // the next stage, once it is free
+    auto take = [&] {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
+        dead = true;
+        return false;
+      }
+      return true;
+    };
+    auto next = [&] {
+      if (++s == STAGES) {
+        s = 0;
+        ph ^= 1u;
+      }
+    };
+    // CTA r's rows come in one box of 128 or, few, of 32, its columns in
+    // boxes of 128; rows that are not loaded feed only sums that are not stored
+    auto a_bytes = [](const Tile& tl, int r) {
+      const int left = tl.rows - r * 128;
+      return left <= 0 ? 0 : (MODE != 2 && left <= 32 ? BOX / 4 : BOX);
+    };
+    auto b_boxes = [](const Tile& tl) { return !PAIR && tl.n > 128 ? 2 : 1; };
+    if (a_side) {
+      walk([&](int t, int k0, int k1) {
+        const Tile tl = tile(t);
+        const int na = a_bytes(tl, rank), both = a_bytes(tl, 0) + (PAIR ? a_bytes(tl, 1) : 0);
+        const uint32_t expect = both + (PAIR ? 2 : b_boxes(tl)) * BOX;
+        const CUtensorMap* ma = na == BOX ? &tmA : &tmA32;
+        const int row0 = tl.row0 + rank * 128;
+        const int first = MODE == 2 ? base[tl.e] * 128 : 0;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!take()) return false;
+          if (used < STAGES) ++used;
+          if (elect_one()) {
+            uint8_t* st = smem + s * C::STAGE;
             if (rank == 0) mbar_arrive_expect_tx(&full[s], expect);
             if (na > 0) {
               if constexpr (MODE == 2)
@@ -660,144 +668,132 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
               else
                 load2(st, ma, kb * KS, row0);
             }
+          }
+          __syncwarp();
+          next();
+        }
+        return true;
+      });
+      // the latest use of each stage has landed before this CTA may exit (a
+      // pair: the even CTA's barrier counts both, and both exit together)
+      for (int j = 0; rank == 0 && j < used; ++j) {
+        if (s == 0) {
+          s = STAGES;
+          ph ^= 1u;
+        }
+        --s;
+        if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
+          dead = true;
+          break;
+        }
+      }
+    } else {
+      // a stage's scales, as chunks: row i's byte at (i % 32) 16 + (i / 32) 4
+      // (four times: any may be read). Loaded four stages at a time, four
+      // stages ahead.
+      const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
+      constexpr uint32_t ONE = 0x7f7f7f7fu;
+      walk([&](int t, int k0, int k1) {
+        const Tile tl = tile(t);
+        const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
+        const int first = MODE == 2 ? base[tl.e] : 0;
+        struct Quad {
+          uint32_t w[MODE == 2 ? 12 : 5];
+        } cur, nxt;
+        auto load = [&](int q) {
+          Quad r;
+          if constexpr (MODE == 2) {
+            // a word is rows lane + 32 i of one block: of A's and of the two of columns
+            const int m = tl.row0 / 128 + rank, n = tl.n0 / 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int kb = first + min(q * 4 + i, k1 - 1);
+              const uint32_t* a = reinterpret_cast<const uint32_t*>(p.as) +
+                                  (static_cast<size_t>(kb) * nbk + m) * 32 + lane;
+              const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bs) +
+                                  (static_cast<size_t>(kb) * nbn + n) * 32 + lane;
+              r.w[i * 3] = m < nbk ? __ldg(a) : ONE;
+              r.w[i * 3 + 1] = __ldg(b);
+              r.w[i * 3 + 2] = n + 1 < nbn ? __ldg(b + 32) : ONE;
+            }
           } else {
+            // rows lane + 32 i, four blocks each; lanes 0..7: a block of the
+            // two blocks of columns each
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = tl.row0 + static_cast<int>(rank) * 128 + min(lane + 32 * i, rows - 1);
+              r.w[i] = rows > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
+                                      p.as + static_cast<size_t>(row) * pitch + q * 4))
+                                : ONE;
+            }
+            const int nb = min(tl.n0 / 128 + (lane & 1), up_div(width, 128) - 1);
+            const int kb = min(q * 4 + (lane >> 1 & 3), kst - 1);
+            const int at = MODE == 1 ? nb * nbn + kb : kb * nbn + nb;
+            r.w[4] = __ldg(p.bs + static_cast<size_t>(tl.e) * nbk * nbn + at);
+          }
+          return r;
+        };
+        const int nb = b_boxes(tl), col0 = tl.n0 + rank * 128;
+        if (k0 < k1) nxt = load(k0 >> 2);
+        for (int kb = k0; kb < k1; ++kb) {
+          const int i = kb & 3;
+          if (kb == k0 || i == 0) {
+            cur = nxt;
+            if ((kb >> 2) * 4 + 4 < k1) nxt = load((kb >> 2) + 1);
+          }
+          uint4 a, b0, b1;
+          if constexpr (MODE == 2) {
+            uint32_t w[3];
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              w[c] = i == 0 ? cur.w[c] : i == 1 ? cur.w[3 + c] : i == 2 ? cur.w[6 + c] : cur.w[9 + c];
+            auto four = [](uint32_t x) {
+              return make_uint4(__byte_perm(x, 0, 0x0000), __byte_perm(x, 0, 0x1111),
+                                __byte_perm(x, 0, 0x2222), __byte_perm(x, 0, 0x3333));
+            };
+            a = four(w[0]);
+            b0 = four(w[1]);
+            b1 = four(w[2]);
+            if constexpr (PAIR) {
+              const uint4 c0 = b0, c1 = b1;
+              b0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
+              b1 = make_uint4(c0.z, c0.w, c1.z, c1.w);
+            }
+          } else {
+            const uint32_t sel = 0x1111u * i;
+            a = make_uint4(__byte_perm(cur.w[0], 0, sel), __byte_perm(cur.w[1], 0, sel),
+                           __byte_perm(cur.w[2], 0, sel), __byte_perm(cur.w[3], 0, sel));
+            const uint32_t s0 = __shfl_sync(0xffffffffu, cur.w[4], i * 2) * 0x01010101u;
+            const uint32_t s1 = __shfl_sync(0xffffffffu, cur.w[4], i * 2 + 1) * 0x01010101u;
+            b0 = PAIR ? make_uint4(s0, s0, s1, s1) : make_uint4(s0, s0, s0, s0);
+            b1 = PAIR ? b0 : make_uint4(s1, s1, s1, s1);
+          }
+          if (!take()) return false;
+          const uint32_t sf = base0 + s * C::STAGE + C::OFF_SFA + lane * 16;
+          st_shared(sf, a);
+          st_shared(sf + CHUNK, b0);
+          st_shared(sf + 2 * CHUNK, b1);
+          fence_proxy_async_shared();
+          __syncwarp();
+          if (elect_one()) {
+            uint8_t* dst = smem + s * C::STAGE + C::OFF_B;
 #pragma unroll
             for (int b = 0; b < C::B_BOXES; ++b)
               if (b < nb) {
-                uint8_t* dst = st + C::OFF_B + b * BOX;
                 if constexpr (MODE == 2)
-                  load2(dst, &tmB, col0 + b * 128, first + kb * KS);
+                  load2(dst + b * BOX, &tmB, col0 + b * 128, (first + kb) * KS);
                 else if constexpr (MODE == 1)
-                  load3(dst, &tmB, kb * KS, col0 + b * 128, tl.e);
+                  load3(dst + b * BOX, &tmB, kb * KS, col0 + b * 128, tl.e);
                 else
-                  load3(dst, &tmB, col0 + b * 128, kb * KS, tl.e);
+                  load3(dst + b * BOX, &tmB, col0 + b * 128, kb * KS, tl.e);
               }
           }
+          __syncwarp();
+          next();
         }
-        __syncwarp();
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      return true;
-    });
-    // the latest use of each stage has landed before this CTA may exit (a
-    // pair: the even CTA's barrier counts both, and both exit together)
-    for (int j = 0; a_side && rank == 0 && j < used; ++j) {
-      if (s == 0) {
-        s = STAGES;
-        ph ^= 1u;
-      }
-      --s;
-      if (!mbar_wait(&full[s], ph, kWaitLimitNs)) {
-        dead = true;
-        break;
-      }
+        return true;
+      });
     }
-    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
-  } else if (warp == 3) {
-    // a stage's scales, as chunks: row i's byte four times at (i % 32) 16 + (i
-    // / 32) 4. Loaded four stages at a time, four stages ahead.
-    int s = 0;
-    uint32_t ph = 0;
-    bool dead = false;
-    const uint32_t base0 = smem_u32(smem);
-    const uint32_t bar0 = PAIR ? mapa_shared(smem_u32(full), 0) : 0;
-    const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
-    constexpr uint32_t ONE = 0x7f7f7f7fu;
-    walk([&](int t, int k0, int k1) {
-      const Tile tl = tile(t);
-      const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
-      struct Quad {
-        uint32_t w[MODE == 2 ? 12 : 5];
-      } cur, nxt;
-      auto load = [&](int q) {
-        Quad r;
-        if constexpr (MODE == 2) {
-          // a lane's four neighbouring rows (of K) and columns
-          const int m = tl.row0 + static_cast<int>(rank) * 128 + 4 * lane;
-          const int c = PAIR ? tl.n0 + (lane < 16 ? 0 : 64) + 4 * lane : tl.n0 + 4 * lane;
-          constexpr int NEXT = PAIR ? 64 : 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int kb = min(q * 4 + i, k1 - 1);
-            const uint8_t* a = p.as + static_cast<size_t>(base[tl.e] + kb) * K;
-            const uint8_t* b = p.bs + static_cast<size_t>(base[tl.e] + kb) * N;
-            r.w[i * 3] = m < K ? __ldg(reinterpret_cast<const uint32_t*>(a + m)) : ONE;
-            r.w[i * 3 + 1] = c < N ? __ldg(reinterpret_cast<const uint32_t*>(b + c)) : ONE;
-            r.w[i * 3 + 2] =
-                c + NEXT < N ? __ldg(reinterpret_cast<const uint32_t*>(b + c + NEXT)) : ONE;
-          }
-        } else {
-          // rows lane + 32 i, four blocks each; lanes 0..7: a block of the two
-          // blocks of columns each
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = tl.row0 + static_cast<int>(rank) * 128 + min(lane + 32 * i, rows - 1);
-            r.w[i] = rows > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
-                                    p.as + static_cast<size_t>(row) * pitch + q * 4))
-                              : ONE;
-          }
-          const int nb = min(tl.n0 / 128 + (lane & 1), up_div(width, 128) - 1);
-          const int kb = min(q * 4 + (lane >> 1 & 3), kst - 1);
-          const int at = MODE == 1 ? nb * nbn + kb : kb * nbn + nb;
-          r.w[4] = __ldg(p.bs + static_cast<size_t>(tl.e) * nbk * nbn + at);
-        }
-        return r;
-      };
-      if (k0 < k1) nxt = load(k0 >> 2);
-      for (int kb = k0; kb < k1; ++kb) {
-        const int i = kb & 3;
-        if (kb == k0 || i == 0) {
-          cur = nxt;
-          if ((kb >> 2) * 4 + 4 < k1) nxt = load((kb >> 2) + 1);
-        }
-        if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1u, kWaitLimitNs))) {
-          dead = true;
-          return false;
-        }
-        const uint32_t sfa = base0 + s * C::STAGE + C::OFF_SFA;
-        if constexpr (MODE == 2) {
-          const uint32_t at = (lane & 7) * 64 + (lane >> 3) * 4;
-#pragma unroll
-          for (int c = 0; c < 3; ++c) {
-            const uint32_t w = i == 0 ? cur.w[c] : i == 1 ? cur.w[3 + c]
-                               : i == 2 ? cur.w[6 + c] : cur.w[9 + c];
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-              st_shared1(sfa + c * CHUNK + at + b * 16, __byte_perm(w, 0, 0x1111 * b));
-          }
-        } else {
-          const uint32_t sel = 0x1111u * i;
-          st_shared4(sfa + lane * 16, __byte_perm(cur.w[0], 0, sel), __byte_perm(cur.w[1], 0, sel),
-                     __byte_perm(cur.w[2], 0, sel), __byte_perm(cur.w[3], 0, sel));
-          const uint32_t s0 = __shfl_sync(0xffffffffu, cur.w[4], i * 2) * 0x01010101u;
-          const uint32_t s1 = __shfl_sync(0xffffffffu, cur.w[4], i * 2 + 1) * 0x01010101u;
-          const uint32_t sfb = sfa + CHUNK + lane * 16;
-          if constexpr (PAIR) {
-            st_shared4(sfb, s0, s0, s1, s1);
-            st_shared4(sfb + CHUNK, s0, s0, s1, s1);
-          } else {
-            st_shared4(sfb, s0, s0, s0, s0);
-            st_shared4(sfb + CHUNK, s1, s1, s1, s1);
-          }
-        }
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR && rank != 0)
-            mbar_arrive_remote(bar0 + s * 8);
-          else
-            mbar_arrive(&full[s]);
-        }
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      return true;
-    });
     if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
     // (one lane issues: elect_one says how)
@@ -815,8 +811,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       const uint32_t ad0 = desc_lo(base0), bd0 = desc_lo(base0 + C::OFF_B),
                      sa0 = sf_lo(base0 + C::OFF_SFA);
       auto take = [&] {
-        const bool there = PAIR ? mbar_wait_spin_cluster(&full[s], ph, kWaitLimitNs)
-                                : mbar_wait_spin(&full[s], ph, kWaitLimitNs);
+        const bool there = mbar_wait_spin(&full[s], ph, kWaitLimitNs);
         if (there) tc_fence_after();
         return there;
       };

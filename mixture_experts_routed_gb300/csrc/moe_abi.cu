@@ -1100,7 +1100,7 @@ int moe_fp8_quantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const void*
   if (c.R == 0) return MOE_OK;
   const size_t es = elem_size(c.dtype), R = c.R, C = cols, cr = moe_fp8_column_rows(cfg);
   const int xr = src != nullptr ? c.x_rows : c.R;
-  if (!apart({{q, R * C}, {scale, R * fp8_pitch(cols)}, {cq, cr * C}, {cscale, cr / 128 * C},
+  if (!apart({{q, R * C}, {scale, R * fp8_pitch(cols)}, {cq, cr * C}, {cscale, cr * ceil_div(cols, 128)},
               {ws, moe_fp8_workspace_size(cfg)}},
              {{x, xr * C * es}, {src, R * 4}, {row_weight, R * 4}, {z, R * C * es},
               {offsets, (c.E + size_t(1)) * 4}}))
@@ -1155,7 +1155,8 @@ int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const ui
   if (c.R == 0) return status_of(cudaMemsetAsync(dW, 0, n, as_stream(stream)));
   const size_t cr = moe_fp8_column_rows(cfg);
   if (!apart({{dW, n}, {ws, moe_fp8_workspace_size(cfg)}},
-             {{xq, cr * c.K}, {x_scale, cr / 128 * c.K}, {dyq, cr * c.N}, {dy_scale, cr / 128 * c.N},
+             {{xq, cr * c.K}, {x_scale, cr * ceil_div(c.K, 128)}, {dyq, cr * c.N},
+              {dy_scale, cr * ceil_div(c.N, 128)},
               {offsets, (c.E + size_t(1)) * 4}}))
     return MOE_ERR_INVALID_ARG;
   const int sms = num_sms();

@@ -54,6 +54,12 @@ def column_form(v, counts):
     return torch.cat(values), torch.cat(scales)
 
 
+def columns_of(cscale, C):
+    """The scales [tile, C] of a columns' form, in the columns' order."""
+    n = len(cscale)
+    return cscale.view(n, -1, 32, 4).transpose(2, 3).reshape(n, -1)[:, :C].contiguous()
+
+
 def same(a, b):
     return torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
 
@@ -68,8 +74,9 @@ def check_rows(r, v, counts):
     if r.cq is not None:
         want, s = column_form(v, counts)
         n = len(s)
-        assert torch.equal(r.cscale[:n], s)
-        assert same(decode(r.cq[:n * 128], r.cscale[:n], 128, 1), want)
+        got = columns_of(r.cscale, C)[:n]
+        assert torch.equal(got, s)
+        assert same(decode(r.cq[:n * 128], got, 128, 1), want)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -158,11 +165,11 @@ def test_activations(cuda_ok, dtype, act):
         v = torch.where(far, v, torch.zeros_like(v))
     r = moe.fp8_quantize_rows(c, x, off, ws=ws, row_weight=w, columns=True, act=act, z=zz)
     near_codes(r.q, r.scale[:, :3].contiguous(), v, 1, 128)
-    at, lo, tile = 0, 0, 0
+    lo, tile, cs = 0, 0, columns_of(r.cscale, C)
     for n in counts:
         tiles = -(-n // 128)
         if n:
-            near_codes(r.cq[tile * 128:tile * 128 + n], r.cscale[tile:tile + tiles], v[lo:lo + n],
+            near_codes(r.cq[tile * 128:tile * 128 + n], cs[tile:tile + tiles], v[lo:lo + n],
                        128, 1)
         lo, tile = lo + n, tile + tiles
     assert moe.get_device_error(ws) == moe.MOE_OK
@@ -287,14 +294,15 @@ def run_product(p, transposed):
 
 def check_grad(p, dW):
     c, tile = p["c"], 0
+    xs, ds = columns_of(p["x"].cscale, c.K), columns_of(p["dy"].cscale, c.N)
     for e, n in enumerate(p["counts"]):
         tiles = -(-n // 128)
         if not n:
             assert not bool(dW[e].any())
             continue
         t = slice(tile * 128, (tile + tiles) * 128)
-        a = decode(p["x"].cq[t], p["x"].cscale[tile:tile + tiles], 128, 1)
-        b = decode(p["dy"].cq[t], p["dy"].cscale[tile:tile + tiles], 128, 1)
+        a = decode(p["x"].cq[t], xs[tile:tile + tiles], 128, 1)
+        b = decode(p["dy"].cq[t], ds[tile:tile + tiles], 128, 1)
         within(dW[e], a.t() @ b, a.abs().t() @ b.abs(), n, torch.float32)
         tile += tiles
 
@@ -398,7 +406,7 @@ def test_nan_blocks_reach_their_rows_and_columns_only(cuda_ok):
         p["x"].scale[1, 0] = 255          # row 1, k below 128
         p["dy"].scale[0, 2] = 255         # row 0, n of 256 and more
         p["wsc"][1, 1, 0] = 255           # expert 1, k of 128 and more, n below 128
-        p["x"].cscale[0, 9] = 255         # expert 0, k = 9
+        p["x"].cscale[0, 1, 4 * 9] = 255  # expert 0, k = 128 + 9
         y2, dx2, dW2 = run_product(p, False), run_product(p, True), run_grad(p)
         bad = torch.zeros_like(y, dtype=torch.bool)
         bad[1] = True
@@ -409,7 +417,7 @@ def test_nan_blocks_reach_their_rows_and_columns_only(cuda_ok):
         bad[counts[0]:, 128:] = True
         assert torch.equal(dx2.isnan(), bad) and torch.equal(dx2[~bad], dx[~bad])
         bad = torch.zeros_like(dW, dtype=torch.bool)
-        bad[0, 9] = True
+        bad[0, 137] = True
         assert torch.equal(dW2.isnan(), bad) and torch.equal(dW2[~bad], dW[~bad])
 
 
