@@ -344,7 +344,7 @@ cudaError_t launch_fp8_rows(int dtype, int act, const void* x, const int32_t* sr
 cudaError_t launch_fp8_weights(int dtype, const void* W, int E, int K, int N, uint8_t* q,
                                uint8_t* sc, cudaStream_t s);
 cudaError_t launch_fp8_back(int dtype, const uint8_t* q, const uint8_t* sc, int experts, int rows,
-                            int cols, int per, int pitch, void* out, int num_sms, cudaStream_t s);
+                            int cols, int per, int pitch, void* out, cudaStream_t s);
 // mode 0: rows a [R, K] . W [E, K, N]; 1: rows a [R, N] . W^T; 2: columns a
 // [.., K]^T . columns b [.., N] to fp32 [E, K, N]. ctr and part as for the 4-bit
 // product.

@@ -106,24 +106,170 @@ __device__ __forceinline__ void st_codes(uint8_t* p, const float (&v)[V]) {
 }
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// ---------------------------------------------------------------- rows
-// A block takes tiles of 128 rows of one expert x 128 columns, a thread 16
-// bytes of every 16th (fp32: 8th) row, all loaded before the first is used; a
-// row's lanes agree on its amax by shuffles, the columns' amax goes through
-// shared memory. Both forms come out of the one read.
-// Bound by HBM: bf16 in, one byte a form out.
-constexpr int kRowThreads = 256;
+// What is quantised: 16 bytes of x (and of z) through the activation, times a
+// row's weight.
+template <typename T, int ACT>
+__device__ __forceinline__ void input(const uint4& x, const uint4& z, float w,
+                                      float (&v)[16 / sizeof(T)]) {
+  constexpr int V = 16 / sizeof(T);
+  unpack<T>(x, v);
+  float zv[V];
+  if constexpr (ACT == MOE_ACT_SILU_GRAD) unpack<T>(z, zv);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if constexpr (ACT == MOE_ACT_NONE)
+      v[i] *= w;
+    else if constexpr (ACT == MOE_ACT_SILU)
+      v[i] = silu_of<float>(v[i]) * w;
+    else
+      v[i] *= silu_slope(zv[i]) * w;
+  }
+}
 
-template <typename T, int ACT, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kRowThreads)
+// ---------------------------------------------------------------- rows
+// A warp quantises groups of four spans (256 bf16 or 128 fp32 values each) of
+// a row: a lane loads 16 bytes of a span, a block's 16 (32) lanes agree on its
+// amax. The groups of all rows are shared out evenly, each warp's one after
+// the other, and a group is loaded while the one before it is quantised.
+// Bound by HBM: the row is read once, a byte a value written.
+constexpr int kRowBlocks = 4;  // blocks of 256 threads an SM holds at once
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(256)
     fp8_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
                     const float* __restrict__ weight, const T* __restrict__ z,
                     const int32_t* __restrict__ offsets, int E, int R, int C,
-                    uint8_t* __restrict__ q, uint8_t* __restrict__ sc, uint8_t* __restrict__ cq,
-                    uint8_t* __restrict__ csc, uint32_t* err) {
-  constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kRowThreads / LPR, PASS = 128 / RPP;
+                    uint8_t* __restrict__ q, uint8_t* __restrict__ sc, uint32_t* err) {
+  constexpr int V = 16 / sizeof(T), LPB = 128 / V, SPAN = 32 * V, F = 4;
+  constexpr bool Z = ACT == MOE_ACT_SILU_GRAD;
+  __shared__ int bad;
+  pdl_wait();
+  pdl_trigger();
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e <= E; e += 256) {
+    const int o = __ldg(offsets + e);
+    if (o < 0 || o > R || (e > 0 && o < __ldg(offsets + e - 1))) bad = 1;
+  }
+  __syncthreads();
+  if (bad) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kErrBadIndex);
+    return;
+  }
+  const int first = __ldg(offsets), end = __ldg(offsets + E);
+  const int lane = threadIdx.x & 31;
+  const int groups = up_div(C, F * SPAN), pitch = up_div(up_div(C, 128), 4) * 4;
+  // (at most 2^24 rows of 128 groups)
+  const uint32_t warp = blockIdx.x * 8 + (threadIdx.x >> 5), warps = gridDim.x * 8;
+  const uint32_t total = static_cast<uint32_t>(end - first) * groups;
+  const uint32_t share = total / warps, more = total - share * warps;
+  const uint32_t g0 = share * warp + min(warp, more);
+  int left = share + (warp < more ? 1 : 0);
+  if (left == 0) return;
+  int r = first + static_cast<int>(g0 / groups), g = static_cast<int>(g0 % groups);
+  const T *row, *zrow;
+  bool in;
+  float w;
+  auto find = [&](int r) {
+    const int xr = src != nullptr ? __ldg(src + r) : r;
+    in = xr >= 0 && xr < x_rows;
+    if (!in && lane == 0) atomicOr(err, kErrBadIndex);
+    row = x + static_cast<size_t>(in ? xr : 0) * C;
+    if constexpr (Z) zrow = z + static_cast<size_t>(r) * C;
+    w = weight != nullptr ? __ldg(weight + r) : 1.f;
+  };
+  uint4 raw[F], zr[Z ? F : 1];
+  auto load = [&](int kb) {
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const bool some = in && kb + f * SPAN < C;
+      raw[f] = some ? ld_once(row + kb + f * SPAN) : uint4{0, 0, 0, 0};
+      if constexpr (Z) zr[f] = some ? ld_once(zrow + kb + f * SPAN) : uint4{0, 0, 0, 0};
+    }
+  };
+  find(r);
+  load(g * F * SPAN + lane * V);
+  while (true) {
+    uint8_t* qr = q + static_cast<size_t>(r) * C;
+    uint8_t* sr = sc + static_cast<size_t>(r) * pitch;
+    const int kb = g * F * SPAN + lane * V;
+    uint4 now[F], znow[Z ? F : 1];
+    const float wnow = w;
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      now[f] = raw[f];
+      if constexpr (Z) znow[f] = zr[f];
+    }
+    if (--left > 0) {
+      if (++g == groups) {
+        g = 0;
+        find(++r);
+      }
+      load(g * F * SPAN + lane * V);
+    }
+    uint32_t word = 0;  // four blocks' scales
+#pragma unroll
+    for (int f = 0; f < F; ++f) {
+      const int k = kb + f * SPAN;
+      float v[V];
+      input<T, ACT>(now[f], znow[Z ? f : 0], wnow, v);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = max(m, mag(v[i]));
+#pragma unroll
+      for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+      const uint32_t s = scale_code(m);
+      const float inv = inv_scale(s);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= inv;
+      if (k < C) st_codes(qr + k, v);
+      // (the scales' lines are padded to four)
+      if constexpr (V == 8) {
+        word |= (s | __shfl_sync(0xffffffffu, s, 16) << 8) << (f & 1) * 16;
+        if ((f & 1) && lane == 0 && k - SPAN < C)
+          *reinterpret_cast<uint32_t*>(sr + ((k - SPAN) >> 7)) = word;
+        if (f & 1) word = 0;
+      } else {
+        word |= s << f * 8;
+        if (f == F - 1 && lane == 0 && kb < C) *reinterpret_cast<uint32_t*>(sr + (kb >> 7)) = word;
+      }
+    }
+    if (left == 0) return;
+  }
+}
+
+// ---------------------------------------------------------------- columns
+// A block takes tiles of 128 rows of one expert x 128 columns, a thread 16
+// bytes of every 16th (fp32: 8th) row, which it copies to a place of its own in
+// shared memory (cp.async) DEPTH tiles ahead. The columns' amax goes over
+// shared memory, a row's (where the rows' form is wanted too) by shuffles:
+// both forms come out of the one read. Bound by HBM.
+constexpr int kColThreads = 256, kTileBytes = 128 * 128;
+
+template <typename T, int ACT>
+struct ColCfg {
+  static constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kColThreads / LPR,
+                       PASS = 128 / RPP;
+  static constexpr bool Z = ACT == MOE_ACT_SILU_GRAD;
+  static constexpr int TENSORS = Z ? 2 : 1;
+  static constexpr int BYTES = kTileBytes * sizeof(T) * TENSORS;  // of one tile
+  static constexpr int BUFS = BYTES <= 32768 ? 3 : BYTES <= 65536 ? 2 : 1, DEPTH = BUFS - 1;
+  static constexpr int SMEM = BUFS * BYTES;
+  static_assert(SMEM <= 200 * 1024, "shared memory");
+};
+
+template <typename T, int ACT, bool ROWS>
+__global__ void __launch_bounds__(kColThreads)
+    fp8_columns_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
+                       const float* __restrict__ weight, const T* __restrict__ z,
+                       const int32_t* __restrict__ offsets, int E, int R, int C,
+                       uint8_t* __restrict__ q, uint8_t* __restrict__ sc, uint8_t* __restrict__ cq,
+                       uint8_t* __restrict__ csc, uint32_t* err) {
+  using K = ColCfg<T, ACT>;
+  constexpr int V = K::V, LPR = K::LPR, RPP = K::RPP, PASS = K::PASS, WARPS = kColThreads / 32;
+  extern __shared__ __align__(16) uint8_t buf[];  // [BUFS][TENSORS][PASS][threads] 16 bytes
   __shared__ int seg[kMaxExperts + 1], base[kMaxExperts + 1], ok;
-  __shared__ uint32_t top[COLS ? kRowThreads / 32 : 1][128];
+  __shared__ __align__(16) uint32_t top[WARPS][128];
   __shared__ float inv[128];
   pdl_wait();
   pdl_trigger();
@@ -133,74 +279,95 @@ __global__ void __launch_bounds__(kRowThreads)
   const int c0 = tid % LPR * V, r0 = tid / LPR;
   // (at most 2^17 + 256 row tiles of 512 blocks)
   const int tiles = base[E] * nb;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int rt = t / nb, cb = t - rt * nb;
-    const int e = last_at_most(base, E - 1, rt);
-    const int row0 = seg[e] + (rt - base[e]) * 128, rows = min(128, seg[e + 1] - row0);
-    const int col = cb * 128 + c0;
-    const bool in = col < C;
-    uint4 raw[PASS];
-    uint4 zr[ACT == MOE_ACT_SILU_GRAD ? PASS : 1];
-    float w[PASS];
+  struct At {
+    int rt, cb, row0, rows;
+  };
+  auto place = [&](int t) {
+    At a;
+    a.rt = t / nb;
+    a.cb = t - a.rt * nb;
+    const int e = last_at_most(base, E - 1, a.rt);
+    a.row0 = seg[e] + (a.rt - base[e]) * 128;
+    a.rows = min(128, seg[e + 1] - a.row0);
+    return a;
+  };
+  auto piece = [&](int b, int h, int j) {
+    return reinterpret_cast<uint4*>(buf) +
+           ((b * K::TENSORS + h) * PASS + j) * kColThreads + tid;
+  };
+  auto fetch = [&](int t, int b) {
+    if (t < tiles) {
+      const At a = place(t);
+      const int col = a.cb * 128 + c0;
 #pragma unroll
-    for (int j = 0; j < PASS; ++j) {
-      const int r = r0 + j * RPP;
-      raw[j] = uint4{0, 0, 0, 0};
-      w[j] = 1.f;
-      if constexpr (ACT == MOE_ACT_SILU_GRAD) zr[j] = uint4{0, 0, 0, 0};
-      if (r >= rows || !in) continue;
-      int xr = row0 + r;
-      if (src != nullptr) {
-        xr = __ldg(src + xr);
-        if (xr < 0 || xr >= x_rows) {
-          atomicOr(err, kErrBadIndex);
-          continue;
+      for (int j = 0; j < PASS; ++j) {
+        const int r = a.row0 + r0 + j * RPP;
+        bool some = r0 + j * RPP < a.rows && col < C;
+        int xr = r;
+        if (some && src != nullptr) {
+          xr = __ldg(src + r);
+          if (xr < 0 || xr >= x_rows) {
+            atomicOr(err, kErrBadIndex);
+            some = false;
+          }
+        }
+        if (some) {
+          ptx::cp_async16(ptx::smem_u32(piece(b, 0, j)), x + static_cast<size_t>(xr) * C + col);
+          if constexpr (K::Z)
+            ptx::cp_async16(ptx::smem_u32(piece(b, 1, j)), z + static_cast<size_t>(r) * C + col);
+        } else {
+          *piece(b, 0, j) = uint4{0, 0, 0, 0};
+          if constexpr (K::Z) *piece(b, 1, j) = uint4{0, 0, 0, 0};
         }
       }
-      raw[j] = ld_once(x + static_cast<size_t>(xr) * C + col);
-      if (weight != nullptr) w[j] = __ldg(weight + row0 + r);
-      if constexpr (ACT == MOE_ACT_SILU_GRAD)
-        zr[j] = ld_once(z + static_cast<size_t>(row0 + r) * C + col);
     }
-    // (a form that takes long to compute is kept in fp32; else the raw words are)
-    float held[ACT != MOE_ACT_NONE ? PASS : 1][V];
+    ptx::cp_async_commit();
+  };
+  // (a thread reads only what it copied: no barrier, and a buffer is free
+  // once its thread is through with it)
+#pragma unroll
+  for (int i = 0; i < K::DEPTH; ++i) fetch(blockIdx.x + i * gridDim.x, i);
+  int b = 0;
+  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+    const At a = place(t);
+    const int col = a.cb * 128 + c0;
+    const bool in = col < C;
+    float w[PASS];
+#pragma unroll
+    for (int j = 0; j < PASS; ++j)
+      w[j] = weight != nullptr && r0 + j * RPP < a.rows ? __ldg(weight + a.row0 + r0 + j * RPP) : 1.f;
+    int ahead = b + K::DEPTH;
+    if (ahead >= K::BUFS) ahead -= K::BUFS;
+    fetch(t + K::DEPTH * gridDim.x, ahead);
+    ptx::cp_async_wait<K::DEPTH>();
+    // (a form that takes long to compute is kept in fp32; else the words are)
+    constexpr bool HELD = ACT != MOE_ACT_NONE;
+    float held[HELD ? PASS : 1][V];
+    uint4 raw[HELD ? 1 : PASS];
     auto value = [&](int j, float (&v)[V]) {
-      if constexpr (ACT != MOE_ACT_NONE) {
+      if constexpr (HELD) {
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = held[j][i];
       } else {
-        unpack<T>(raw[j], v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= w[j];
+        input<T, ACT>(raw[j], raw[j], w[j], v);
       }
     };
-    if constexpr (ACT != MOE_ACT_NONE) {
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        float zv[V];
-        unpack<T>(raw[j], held[j]);
-        if constexpr (ACT == MOE_ACT_SILU_GRAD) unpack<T>(zr[j], zv);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          if constexpr (ACT == MOE_ACT_SILU)
-            held[j][i] = silu_of<float>(held[j][i]) * w[j];
-          else
-            held[j][i] *= silu_slope(zv[i]) * w[j];
-        }
-      }
-    }
-    uint32_t cm[COLS ? V : 1] = {};
+    uint32_t cm[V] = {};
 #pragma unroll
     for (int j = 0; j < PASS; ++j) {
+      if constexpr (HELD)
+        input<T, ACT>(*piece(b, 0, j), *piece(b, K::TENSORS - 1, j), w[j], held[j]);
+      else
+        raw[j] = *piece(b, 0, j);
       const int r = r0 + j * RPP;
       float v[V];
       value(j, v);
       uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint32_t a = mag(v[i]);
-        if constexpr (ROWS) m = max(m, a);
-        if constexpr (COLS) cm[i] = max(cm[i], a);
+        const uint32_t g = mag(v[i]);
+        if constexpr (ROWS) m = max(m, g);
+        cm[i] = max(cm[i], g);
       }
       if constexpr (ROWS) {
 #pragma unroll
@@ -209,57 +376,61 @@ __global__ void __launch_bounds__(kRowThreads)
         const float f = inv_scale(s);
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] *= f;
-        if (r < rows && in) {
-          st_codes(q + static_cast<size_t>(row0 + r) * C + col, v);
-          if (c0 == 0) sc[static_cast<size_t>(row0 + r) * pitch + cb] = static_cast<uint8_t>(s);
+        if (r < a.rows && in) {
+          st_codes(q + static_cast<size_t>(a.row0 + r) * C + col, v);
+          if (c0 == 0) sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
         }
       }
     }
-    if constexpr (COLS) {
+    if constexpr (LPR == 16) {
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if constexpr (LPR == 16) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
-      if (lane < LPR)
+      for (int i = 0; i < V; ++i) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+    }
+    if (lane < LPR) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) top[warp][c0 + i] = cm[i];
-      __syncthreads();
-      if (tid < 128) {
-        uint32_t m = 0;
+      for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<uint4*>(&top[warp][c0 + i]) =
+            make_uint4(cm[i], cm[i + 1], cm[i + 2], cm[i + 3]);
+    }
+    __syncthreads();
+    if (tid < 128) {
+      uint32_t m = 0;
 #pragma unroll
-        for (int k = 0; k < kRowThreads / 32; ++k) m = max(m, top[k][tid]);
-        const uint32_t s = scale_code(m);
-        inv[tid] = inv_scale(s);
-        csc[(static_cast<size_t>(rt) * nb + cb) * 128 + (tid & 31) * 4 + (tid >> 5)] =
-            static_cast<uint8_t>(s);
-      }
-      __syncthreads();
-      if (in) {
-        float f[V];
+      for (int k = 0; k < WARPS; ++k) m = max(m, top[k][tid]);
+      const uint32_t s = scale_code(m);
+      inv[tid] = inv_scale(s);
+      csc[(static_cast<size_t>(a.rt) * nb + a.cb) * 128 + (tid & 31) * 4 + (tid >> 5)] =
+          static_cast<uint8_t>(s);
+    }
+    __syncthreads();
+    if (in) {
+      float f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) f[i] = inv[c0 + i];
+      for (int i = 0; i < V; ++i) f[i] = inv[c0 + i];
 #pragma unroll
-        for (int j = 0; j < PASS; ++j) {
-          const int r = r0 + j * RPP;
-          float v[V];
-          value(j, v);
-          // (past the segment: zeros, also in a column whose scale is NaN)
+      for (int j = 0; j < PASS; ++j) {
+        const int r = r0 + j * RPP;
+        float v[V];
+        value(j, v);
+        // (past the segment: zeros, also in a column whose scale is NaN)
 #pragma unroll
-          for (int i = 0; i < V; ++i) v[i] = r < rows ? v[i] * f[i] : 0.f;
-          st_codes(cq + (static_cast<size_t>(rt) * 128 + r) * C + col, v);
-        }
+        for (int i = 0; i < V; ++i) v[i] = r < a.rows ? v[i] * f[i] : 0.f;
+        st_codes(cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col, v);
       }
     }
+    if (++b == K::BUFS) b = 0;
   }
+  ptx::cp_async_wait<0>();
 }
 
 // ---------------------------------------------------------------- weights
 // A block takes 128 x 128 of one expert. Bound by HBM.
 template <typename T>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kColThreads)
     fp8_weights_kernel(const T* __restrict__ W, int K, int N, uint8_t* __restrict__ q,
                        uint8_t* __restrict__ sc) {
-  constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kRowThreads / LPR, PASS = 128 / RPP;
-  __shared__ uint32_t top[kRowThreads / 32];
+  constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kColThreads / LPR, PASS = 128 / RPP;
+  __shared__ uint32_t top[kColThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, e = blockIdx.z;
@@ -283,7 +454,7 @@ __global__ void __launch_bounds__(kRowThreads)
   if ((tid & 31) == 0) top[tid >> 5] = m;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kRowThreads / 32; ++i) m = max(m, top[i]);
+  for (int i = 0; i < kColThreads / 32; ++i) m = max(m, top[i]);
   const uint32_t s = scale_code(m);
   const float f = inv_scale(s);
   if (tid == 0)
@@ -301,42 +472,51 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 // ---------------------------------------------------------------- and back
-// [rows][cols] codes whose scale lies at sc[(row / per) * pitch + col / 128]
-// (rows: per 1; weights: 128, each expert's K rows by themselves), 8 codes a
-// thread and step.
+// [experts][rows][cols] codes with a scale for `per` (1 or 128) rows x 128
+// columns, `pitch` of them to a line. A block takes 128 x 128, a thread 8
+// codes of every 16th row, all loaded before the first is written. Bound by
+// the writes: a plain fill of as much memory takes as long.
 template <typename T>
-__global__ void __launch_bounds__(256)
-    fp8_back_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc, int experts,
-                    int rows, int cols, int per, int pitch, T* __restrict__ out) {
+__global__ void __launch_bounds__(kColThreads)
+    fp8_back_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc, int rows,
+                    int cols, int per, int pitch, T* __restrict__ out) {
+  constexpr int PASS = 8;
   pdl_wait();
   pdl_trigger();
-  const int words = cols / 8, high = up_div(rows, per);
-  const long long all = static_cast<long long>(experts) * rows * words;
-  for (long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x; i < all;
-       i += static_cast<long long>(gridDim.x) * 256) {
-    const long long row = i / words;
-    const int c = static_cast<int>(i - row * words) * 8;
-    const int e = static_cast<int>(row / rows), r = static_cast<int>(row - static_cast<long long>(e) * rows);
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(q + i * 8));
-    const float s = scale_value(
-        __ldg(sc + (static_cast<size_t>(e) * high + r / per) * pitch + (c >> 7)));
+  const int c = blockIdx.y * 128 + threadIdx.x % 16 * 8, r0 = blockIdx.x * 128 + threadIdx.x / 16;
+  if (c >= cols) return;
+  const size_t e = blockIdx.z;
+  const uint8_t* s0 = sc + e * up_div(rows, per) * pitch + blockIdx.y;
+  uint2 w[PASS];
+  uint8_t s[PASS];
+#pragma unroll
+  for (int j = 0; j < PASS; ++j) {
+    const int r = min(r0 + j * 16, rows - 1);
+    w[j] = __ldg(reinterpret_cast<const uint2*>(q + (e * rows + r) * cols + c));
+    s[j] = __ldg(s0 + static_cast<size_t>(r / per) * pitch);
+  }
+#pragma unroll
+  for (int j = 0; j < PASS; ++j) {
+    const int r = r0 + j * 16;
+    if (r >= rows) return;
+    const float f = scale_value(s[j]);
     float v[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 f = code_values((j < 2 ? w.x : w.y) >> (j & 1) * 16);
-      v[2 * j] = f.x * s;
-      v[2 * j + 1] = f.y * s;
+    for (int i = 0; i < 4; ++i) {
+      const float2 two = code_values((i < 2 ? w[j].x : w[j].y) >> (i & 1) * 16);
+      v[2 * i] = two.x * f;
+      v[2 * i + 1] = two.y * f;
     }
-    T* o = out + i * 8;
+    T* o = out + (e * rows + r) * cols + c;
     if constexpr (sizeof(T) == 4) {
       reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
       reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
       uint32_t p[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-        p[j] = *reinterpret_cast<const uint32_t*>(&h);
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        p[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
       *reinterpret_cast<uint4*>(o) = make_uint4(p[0], p[1], p[2], p[3]);
     }
@@ -1083,16 +1263,27 @@ cudaError_t launch_rows(const void* x, const int32_t* src, int x_rows, const flo
                         const void* z, const int32_t* offsets, int E, int R, int C, uint8_t* q,
                         uint8_t* sc, uint8_t* cq, uint8_t* csc, uint32_t* err, int num_sms,
                         cudaStream_t s) {
-  const long long tiles = static_cast<long long>(row_tiles(R, E)) * up_div(C, 128);
-  const long long most = static_cast<long long>(num_sms) * 4;
-  const dim3 grid(static_cast<unsigned>(tiles < most ? tiles : most)), block(kRowThreads);
-  auto go = [&](auto kernel) {
-    return launch_pdl(kernel, grid, block, 0, s, static_cast<const T*>(x), src, x_rows, weight,
-                      static_cast<const T*>(z), offsets, E, R, C, q, sc, cq, csc, err);
+  const T *xt = static_cast<const T*>(x), *zt = static_cast<const T*>(z);
+  auto grid = [](long long items, long long most) {
+    return dim3(static_cast<unsigned>(items < most ? items : most));
   };
-  if (cq == nullptr) return go(fp8_rows_kernel<T, ACT, true, false>);
-  return q == nullptr ? go(fp8_rows_kernel<T, ACT, false, true>)
-                      : go(fp8_rows_kernel<T, ACT, true, true>);
+  if (cq == nullptr) {
+    const long long groups = static_cast<long long>(R) * up_div(C, sizeof(T) == 4 ? 512 : 1024);
+    return launch_pdl(fp8_rows_kernel<T, ACT>,
+                      grid((groups + 7) / 8, static_cast<long long>(num_sms) * kRowBlocks),
+                      dim3(256), 0, s, xt, src, x_rows, weight, zt, offsets, E, R, C, q, sc, err);
+  }
+  using K = ColCfg<T, ACT>;
+  const long long tiles = static_cast<long long>(row_tiles(R, E)) * up_div(C, 128);
+  const dim3 blocks = grid(tiles, static_cast<long long>(num_sms) * (K::SMEM <= 100 * 1024 ? 2 : 1));
+  auto go = [&](auto kernel) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kernel, blocks, dim3(kColThreads), K::SMEM, s, xt, src, x_rows, weight, zt,
+                      offsets, E, R, C, q, sc, cq, csc, err);
+  };
+  return q == nullptr ? go(fp8_columns_kernel<T, ACT, false>) : go(fp8_columns_kernel<T, ACT, true>);
 }
 
 template <typename T>
@@ -1112,11 +1303,9 @@ cudaError_t launch_rows_act(int act, const void* x, const int32_t* src, int x_ro
 
 template <typename T>
 cudaError_t launch_back(const uint8_t* q, const uint8_t* sc, int experts, int rows, int cols,
-                        int per, int pitch, void* out, int num_sms, cudaStream_t s) {
-  const long long blocks = (static_cast<long long>(experts) * rows * (cols / 8) + 255) / 256;
-  const long long most = static_cast<long long>(num_sms) * 8;
-  return launch_pdl(fp8_back_kernel<T>, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                    dim3(256), 0, s, q, sc, experts, rows, cols, per, pitch, static_cast<T*>(out));
+                        int per, int pitch, void* out, cudaStream_t s) {
+  return launch_pdl(fp8_back_kernel<T>, dim3(up_div(rows, 128), up_div(cols, 128), experts),
+                    dim3(kColThreads), 0, s, q, sc, rows, cols, per, pitch, static_cast<T*>(out));
 }
 
 }  // namespace
@@ -1133,7 +1322,7 @@ cudaError_t launch_fp8_rows(int dtype, int act, const void* x, const int32_t* sr
 
 cudaError_t launch_fp8_weights(int dtype, const void* W, int E, int K, int N, uint8_t* q,
                                uint8_t* sc, cudaStream_t s) {
-  const dim3 grid(up_div(N, 128), up_div(K, 128), E), block(kRowThreads);
+  const dim3 grid(up_div(N, 128), up_div(K, 128), E), block(kColThreads);
   return dtype == 0 ? launch_pdl(fp8_weights_kernel<float>, grid, block, 0, s,
                                  static_cast<const float*>(W), K, N, q, sc)
                     : launch_pdl(fp8_weights_kernel<__nv_bfloat16>, grid, block, 0, s,
@@ -1141,10 +1330,9 @@ cudaError_t launch_fp8_weights(int dtype, const void* W, int E, int K, int N, ui
 }
 
 cudaError_t launch_fp8_back(int dtype, const uint8_t* q, const uint8_t* sc, int experts, int rows,
-                            int cols, int per, int pitch, void* out, int num_sms, cudaStream_t s) {
-  return dtype == 0
-             ? launch_back<float>(q, sc, experts, rows, cols, per, pitch, out, num_sms, s)
-             : launch_back<__nv_bfloat16>(q, sc, experts, rows, cols, per, pitch, out, num_sms, s);
+                            int cols, int per, int pitch, void* out, cudaStream_t s) {
+  return dtype == 0 ? launch_back<float>(q, sc, experts, rows, cols, per, pitch, out, s)
+                    : launch_back<__nv_bfloat16>(q, sc, experts, rows, cols, per, pitch, out, s);
 }
 
 cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, const uint8_t* b,

@@ -1177,10 +1177,8 @@ int moe_fp8_dequantize_weights(const moe_fp8_config_t* cfg, const uint8_t* wq,
   if (!apart({{W, n * elem_size(c.dtype)}},
              {{wq, n}, {w_scale, moe_fp8_weight_scale_size(cfg)}}))
     return MOE_ERR_INVALID_ARG;
-  const int sms = num_sms();
-  if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_fp8_back(c.dtype, wq, w_scale, c.E, c.K, c.N, 128, ceil_div(c.N, 128), W,
-                                   sms, as_stream(stream)));
+                                   as_stream(stream)));
 }
 
 int moe_fp8_dequantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const uint8_t* q,
@@ -1195,9 +1193,7 @@ int moe_fp8_dequantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const uin
   if (!apart({{x, n * elem_size(c.dtype)}},
              {{q, n}, {scale, static_cast<size_t>(c.R) * fp8_pitch(cols)}}))
     return MOE_ERR_INVALID_ARG;
-  const int sms = num_sms();
-  if (sms <= 0) return MOE_ERR_LAUNCH;
-  return status_of(launch_fp8_back(c.dtype, q, scale, 1, c.R, cols, 1, fp8_pitch(cols), x, sms,
+  return status_of(launch_fp8_back(c.dtype, q, scale, 1, c.R, cols, 1, fp8_pitch(cols), x,
                                    as_stream(stream)));
 }
 

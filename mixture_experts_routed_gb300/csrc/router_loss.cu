@@ -9,14 +9,14 @@
 //   dL_te   = a / (S' n_s) p_te (f_se - sum_j p_tj f_sj) + 2 b / N lse_t p_te
 // (the counts are constants to the gradient).
 #include <cstdint>
+#include <type_traits>
 
 #include "common.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kNJ = kMaxExperts / 32;  // a lane's experts
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kJoinWarps = 32;
 
 // Tokens are cut into chunks of `len` of one sequence. Chunk j of sequence s
 // has the slot offsets[s] / len + s + j, which no other chunk has (a sequence
@@ -51,12 +51,13 @@ struct Seqs {
   }
 };
 
-// what a token's row is to its lanes: values at lane + 32 j
+// what a token's row is to its lanes: values at lane + 32 j, NJ of them
+template <int NJ>
 struct Row {
-  float v[kNJ];
+  float v[NJ];
   __device__ void load(const float* p, int E, int lane) {
 #pragma unroll
-    for (int j = 0; j < kNJ; ++j) v[j] = lane + 32 * j < E ? __ldg(p + lane + 32 * j) : -INFINITY;
+    for (int j = 0; j < NJ; ++j) v[j] = lane + 32 * j < E ? __ldg(p + lane + 32 * j) : -INFINITY;
   }
 };
 __device__ __forceinline__ float warp_sum(float v) {
@@ -70,14 +71,16 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A block sums one chunk, a token to a warp at a time.
+// A block sums one chunk, a token to a warp at a time, the next one's logits
+// loaded meanwhile.
+template <int NJ>
 __global__ void __launch_bounds__(kWarps * 32)
     router_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                        const Seqs q, const uint8_t* __restrict__ mask, int E, int k,
                        float* __restrict__ lse, float* __restrict__ psum, int32_t* __restrict__ cnt,
                        float2* __restrict__ tail, uint32_t* err) {
-  __shared__ float ps[kWarps][kMaxExperts];
-  __shared__ int cs[kMaxExperts];
+  __shared__ float ps[kWarps][NJ * 32];
+  __shared__ int cs[NJ * 32];
   __shared__ float zs[kWarps];
   __shared__ int ns[kWarps];
   pdl_wait();
@@ -93,58 +96,68 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (t0 >= t1 || t0 < q.at(s)) return;
   for (int e = tid; e < E; e += kWarps * 32) cs[e] = 0;
   __syncthreads();
-  Row sum;
+  Row<NJ> sum, L, ahead;
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j) sum.v[j] = 0.f;
+  for (int j = 0; j < NJ; ++j) sum.v[j] = 0.f;
   float zsum = 0.f;
   int n = 0;
+  bool on = false;
+  int e = 0;
+  // (a masked token's row is not read)
+  auto load = [&](int t) {
+    on = t < t1 && (mask == nullptr || __ldg(mask + t) != 0);
+    if (!on) return;
+    ahead.load(logits + static_cast<size_t>(t) * E, E, lane);
+    if (lane < k) e = __ldg(idx + static_cast<size_t>(t) * k + lane);
+  };
+  load(t0 + warp);
   for (int t = t0 + warp; t < t1; t += kWarps) {
-    if (mask != nullptr && __ldg(mask + t) == 0) {
+    const bool now = on;
+    const int chosen = e;
+    L = ahead;
+    load(t + kWarps);
+    if (!now) {
       if (lane == 0) lse[t] = 0.f;
       continue;
     }
-    Row L;
-    L.load(logits + static_cast<size_t>(t) * E, E, lane);
     if (lane < k) {
-      const int e = __ldg(idx + static_cast<size_t>(t) * k + lane);
-      if (e >= 0 && e < E)
-        atomicAdd(&cs[e], 1);
+      if (chosen >= 0 && chosen < E)
+        atomicAdd(&cs[chosen], 1);
       else
         atomicOr(err, kErrBadIndex);
     }
     float top = L.v[0];
 #pragma unroll
-    for (int j = 1; j < kNJ; ++j) top = fmaxf(top, L.v[j]);
+    for (int j = 1; j < NJ; ++j) top = fmaxf(top, L.v[j]);
     top = warp_max(top);
     float den = 0.f;
 #pragma unroll
-    for (int j = 0; j < kNJ; ++j) {
+    for (int j = 0; j < NJ; ++j) {
       L.v[j] = lane + 32 * j < E ? expf(L.v[j] - top) : 0.f;
       den += L.v[j];
     }
     den = warp_sum(den);
     const float inv = 1.f / den, l = top + logf(den);
 #pragma unroll
-    for (int j = 0; j < kNJ; ++j) sum.v[j] = fmaf(L.v[j], inv, sum.v[j]);
+    for (int j = 0; j < NJ; ++j) sum.v[j] = fmaf(L.v[j], inv, sum.v[j]);
     zsum = fmaf(l, l, zsum);
     ++n;
     if (lane == 0) lse[t] = l;
   }
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j)
-    if (lane + 32 * j < E) ps[warp][lane + 32 * j] = sum.v[j];
+  for (int j = 0; j < NJ; ++j) ps[warp][lane + 32 * j] = sum.v[j];
   if (lane == 0) {
     zs[warp] = zsum;
     ns[warp] = n;
   }
   __syncthreads();
   const size_t at = static_cast<size_t>(blockIdx.x) * E;
-  for (int e = tid; e < E; e += kWarps * 32) {
+  for (int i = tid; i < E; i += kWarps * 32) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += ps[w][e];
-    psum[at + e] = v;
-    cnt[at + e] = cs[e];
+    for (int w = 0; w < kWarps; ++w) v += ps[w][i];
+    psum[at + i] = v;
+    cnt[at + i] = cs[i];
   }
   if (tid == 0) {
     float v = 0.f;
@@ -159,18 +172,18 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // A block joins the chunks of one sequence for 32 experts, in chunk order by
-// eight warps and then over the warps; the last block to be done adds up the
+// its warps and then over the warps; the last block to be done adds up the
 // sequences, in order.
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kJoinWarps * 32)
     router_loss_join_kernel(const Seqs q, int E, int k, float balance, float zcoef,
                             const float* __restrict__ psum, const int32_t* __restrict__ cnt,
                             const float2* __restrict__ tail, float* term, uint32_t* done,
                             float* __restrict__ loss, int32_t* __restrict__ counts,
                             int32_t* tokens) {
-  __shared__ float ps[kWarps][32], zs[kWarps][32];
-  __shared__ int cs[kWarps][32], ns[kWarps][32];
-  __shared__ double fin[kWarps][2];
-  __shared__ int fn[kWarps][2], last;
+  __shared__ float ps[kJoinWarps][32], zs[kJoinWarps][32];
+  __shared__ int cs[kJoinWarps][32], ns[kJoinWarps][32];
+  __shared__ double fin[kJoinWarps][2];
+  __shared__ int fn[kJoinWarps][2], last;
   pdl_wait();
   pdl_trigger();
   if (!q.good()) return;
@@ -180,14 +193,24 @@ __global__ void __launch_bounds__(kWarps * 32)
   const int first = q.slot(s), chunks = ceil_div(q.at(s + 1) - q.at(s), q.len);
   float p = 0.f, z = 0.f;
   int c = 0, n = 0;
-  for (int j = warp; j < chunks; j += kWarps) {
-    if (e < E) {
-      const size_t at = static_cast<size_t>(first + j) * E + e;
-      p += __ldcg(psum + at);
-      c += __ldcg(cnt + at);
+  // (eight chunks' loads under way at a time)
+  for (int j = warp; j < chunks; j += kJoinWarps * 8) {
+    float pv[8];
+    int cv[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool some = e < E && j + i * kJoinWarps < chunks;
+      const size_t at = static_cast<size_t>(first + j + i * kJoinWarps) * E + e;
+      pv[i] = some ? __ldcg(psum + at) : 0.f;
+      cv[i] = some ? __ldcg(cnt + at) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p += pv[i];
+      c += cv[i];
     }
   }
-  for (int j = tid; j < chunks; j += kWarps * 32) {
+  for (int j = tid; j < chunks; j += kJoinWarps * 32) {
     const float2 v = __ldcg(tail + first + j);
     z += v.x;
     n += __float_as_int(v.y);
@@ -201,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     p = z = 0.f;
     c = n = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kJoinWarps; ++w) {
       p += ps[w][lane];
       c += cs[w][lane];
       z += zs[w][lane];
@@ -228,11 +251,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   __threadfence();
   double bal = 0, zz = 0;
   int used = 0, all = 0;
-  for (int i = tid; i < static_cast<int>(gridDim.x); i += kWarps * 32) {
+  for (int i = tid; i < static_cast<int>(gridDim.x); i += kJoinWarps * 32) {
     bal += __ldcg(term + 2 * i);
     zz += __ldcg(term + 2 * i + 1);
   }
-  for (int i = tid; i < q.S; i += kWarps * 32) {
+  for (int i = tid; i < q.S; i += kJoinWarps * 32) {
     const int m = __ldcg(tokens + i);
     used += m > 0;
     all += m;
@@ -254,7 +277,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (tid != 0) return;
   bal = zz = 0;
   used = all = 0;
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kJoinWarps; ++w) {
     bal += fin[w][0];
     zz += fin[w][1];
     used += fn[w][0];
@@ -271,6 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 }
 
 // A token to a warp.
+template <int NJ>
 __global__ void __launch_bounds__(kWarps * 32)
     router_loss_bwd_kernel(const float* __restrict__ logits, const Seqs q,
                            const uint8_t* __restrict__ mask, int E, int k, float balance,
@@ -293,11 +317,11 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
   const float g = dloss != nullptr ? __ldg(dloss) : 1.f, l = __ldg(lse + t);
   const float fs = static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(n));
-  Row L;
+  Row<NJ> L;
   L.load(logits + static_cast<size_t>(t) * E, E, lane);
-  float f[kNJ], dot = 0.f;
+  float f[NJ], dot = 0.f;
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     const int e = lane + 32 * j;
     f[j] = e < E ? fs * static_cast<float>(__ldg(counts + static_cast<size_t>(s) * E + e)) : 0.f;
     L.v[j] = e < E ? expf(L.v[j] - l) : 0.f;
@@ -307,10 +331,18 @@ __global__ void __launch_bounds__(kWarps * 32)
   const float cb = g * balance / (static_cast<float>(used) * static_cast<float>(n));
   const float cz = g * 2.f * zcoef / static_cast<float>(all) * l;
 #pragma unroll
-  for (int j = 0; j < kNJ; ++j) {
+  for (int j = 0; j < NJ; ++j) {
     const int e = lane + 32 * j;
     if (e < E) out[e] = L.v[j] * fmaf(cb, f[j] - dot, cz);
   }
+}
+
+// f with the number of experts a lane takes: 1, 2, 4 or 8
+template <typename F>
+cudaError_t by_experts(int E, F f) {
+  if (E <= 32) return f(std::integral_constant<int, 1>());
+  if (E <= 64) return f(std::integral_constant<int, 2>());
+  return E <= 128 ? f(std::integral_constant<int, 4>()) : f(std::integral_constant<int, 8>());
 }
 
 // Chunks of a warp's token or more, about two blocks to an SM.
@@ -356,11 +388,13 @@ cudaError_t launch_router_loss(const float* logits, const int32_t* idx, const in
   float* psum = reinterpret_cast<float*>(w + L.psum);
   int32_t* cnt = reinterpret_cast<int32_t*>(w + L.cnt);
   float2* tail = reinterpret_cast<float2*>(w + L.tail);
-  const cudaError_t e =
-      launch_pdl(router_loss_kernel, dim3(slots_of(T, S)), dim3(kWarps * 32), 0, s, logits, idx, q,
-                 mask, E, k, lse, psum, cnt, tail, reinterpret_cast<uint32_t*>(w));
+  const cudaError_t e = by_experts(E, [&](auto nj) {
+    return launch_pdl(router_loss_kernel<decltype(nj)::value>, dim3(slots_of(T, S)),
+                      dim3(kWarps * 32), 0, s, logits, idx, q, mask, E, k, lse, psum, cnt, tail,
+                      reinterpret_cast<uint32_t*>(w));
+  });
   if (e != cudaSuccess) return e;
-  return launch_pdl(router_loss_join_kernel, dim3(S * ceil_div(E, 32)), dim3(kWarps * 32), 0, s, q,
+  return launch_pdl(router_loss_join_kernel, dim3(S * ceil_div(E, 32)), dim3(kJoinWarps * 32), 0, s, q,
                     E, k, balance, z, static_cast<const float*>(psum),
                     static_cast<const int32_t*>(cnt), static_cast<const float2*>(tail),
                     reinterpret_cast<float*>(w + L.term), reinterpret_cast<uint32_t*>(w + L.done),
@@ -372,8 +406,11 @@ cudaError_t launch_router_loss_bwd(const float* logits, const int32_t* offsets, 
                                    const int32_t* counts, const int32_t* tokens, const float* lse,
                                    const float* dloss, float* dlogits, cudaStream_t s) {
   const Seqs q{offsets, T, S, chunk_len(T)};
-  return launch_pdl(router_loss_bwd_kernel, dim3(ceil_div(T, kWarps)), dim3(kWarps * 32), 0, s,
-                    logits, q, mask, E, k, balance, z, counts, tokens, lse, dloss, dlogits);
+  return by_experts(E, [&](auto nj) {
+    return launch_pdl(router_loss_bwd_kernel<decltype(nj)::value>, dim3(ceil_div(T, kWarps)),
+                      dim3(kWarps * 32), 0, s, logits, q, mask, E, k, balance, z, counts, tokens,
+                      lse, dloss, dlogits);
+  });
 }
 
 }  // namespace moe
