@@ -258,7 +258,24 @@ struct ColCfg {
   static_assert(SMEM <= 200 * 1024, "shared memory");
 };
 
-template <typename T, int ACT, bool ROWS>
+// 8 bf16 values in words, scaled by a power of two a pair (exact, but for
+// results below 2^-126, whose code is 0 either way), to codes.
+__device__ __forceinline__ uint2 scaled_codes(const uint4& u, const uint32_t (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(f[i]));
+    v[2 * i] = __uint_as_float(r << 16);
+    v[2 * i + 1] = __uint_as_float(r & 0xffff0000u);
+  }
+  return make_uint2(pack4(v[0], v[1], v[2], v[3]), pack4(v[4], v[5], v[6], v[7]));
+}
+
+// PLAIN: bf16 values as they are (no activation, no weights): amax and scaling
+// two values to an instruction
+template <typename T, int ACT, bool ROWS, bool PLAIN>
 __global__ void __launch_bounds__(kColThreads)
     fp8_columns_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
                        const float* __restrict__ weight, const T* __restrict__ z,
@@ -332,9 +349,9 @@ __global__ void __launch_bounds__(kColThreads)
     const At a = place(t);
     const int col = a.cb * 128 + c0;
     const bool in = col < C;
-    float w[PASS];
+    float w[PLAIN ? 1 : PASS];
 #pragma unroll
-    for (int j = 0; j < PASS; ++j)
+    for (int j = 0; !PLAIN && j < PASS; ++j)
       w[j] = weight != nullptr && r0 + j * RPP < a.rows ? __ldg(weight + a.row0 + r0 + j * RPP) : 1.f;
     int ahead = b + K::DEPTH;
     if (ahead >= K::BUFS) ahead -= K::BUFS;
@@ -349,42 +366,75 @@ __global__ void __launch_bounds__(kColThreads)
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = held[j][i];
       } else {
-        input<T, ACT>(raw[j], raw[j], w[j], v);
+        input<T, ACT>(raw[j], raw[j], w[PLAIN ? 0 : j], v);
       }
     };
     uint32_t cm[V] = {};
+    if constexpr (PLAIN) {
+      uint32_t c2[4] = {};
 #pragma unroll
-    for (int j = 0; j < PASS; ++j) {
-      if constexpr (HELD)
-        input<T, ACT>(*piece(b, 0, j), *piece(b, K::TENSORS - 1, j), w[j], held[j]);
-      else
+      for (int j = 0; j < PASS; ++j) {
         raw[j] = *piece(b, 0, j);
-      const int r = r0 + j * RPP;
-      float v[V];
-      value(j, v);
-      uint32_t m = 0;
+        const uint32_t u[4] = {raw[j].x & 0x7fff7fffu, raw[j].y & 0x7fff7fffu,
+                               raw[j].z & 0x7fff7fffu, raw[j].w & 0x7fff7fffu};
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const uint32_t g = mag(v[i]);
-        if constexpr (ROWS) m = max(m, g);
-        cm[i] = max(cm[i], g);
-      }
-      if constexpr (ROWS) {
+        for (int i = 0; i < 4; ++i) c2[i] = __vmaxu2(c2[i], u[i]);
+        if constexpr (ROWS) {
+          const int r = r0 + j * RPP;
+          uint32_t m = __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3]));
 #pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t s = scale_code(m);
-        const float f = inv_scale(s);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] *= f;
-        if (r < a.rows && in) {
-          st_codes(q + static_cast<size_t>(a.row0 + r) * C + col, v);
-          if (c0 == 0) sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
+          for (int o = 1; o < LPR; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t s = scale_code(max(m << 16, m & 0xffff0000u));
+          const uint32_t f = __byte_perm(__float_as_uint(inv_scale(s)), 0, 0x3232);
+          const uint32_t f4[4] = {f, f, f, f};
+          if (r < a.rows && in) {
+            *reinterpret_cast<uint2*>(q + static_cast<size_t>(a.row0 + r) * C + col) =
+                scaled_codes(raw[j], f4);
+            if (c0 == 0)
+              sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
+          }
         }
       }
-    }
-    if constexpr (LPR == 16) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+      for (int i = 0; i < 4; ++i) {
+        c2[i] = __vmaxu2(c2[i], __shfl_xor_sync(0xffffffffu, c2[i], 16));
+        cm[2 * i] = c2[i] << 16;
+        cm[2 * i + 1] = c2[i] & 0xffff0000u;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < PASS; ++j) {
+        if constexpr (HELD)
+          input<T, ACT>(*piece(b, 0, j), *piece(b, K::TENSORS - 1, j), w[j], held[j]);
+        else
+          raw[j] = *piece(b, 0, j);
+        const int r = r0 + j * RPP;
+        float v[V];
+        value(j, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint32_t g = mag(v[i]);
+          if constexpr (ROWS) m = max(m, g);
+          cm[i] = max(cm[i], g);
+        }
+        if constexpr (ROWS) {
+#pragma unroll
+          for (int o = 1; o < LPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          const uint32_t s = scale_code(m);
+          const float f = inv_scale(s);
+#pragma unroll
+          for (int i = 0; i < V; ++i) v[i] *= f;
+          if (r < a.rows && in) {
+            st_codes(q + static_cast<size_t>(a.row0 + r) * C + col, v);
+            if (c0 == 0) sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
+          }
+        }
+      }
+      if constexpr (LPR == 16) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+      }
     }
     if (lane < LPR) {
 #pragma unroll
@@ -403,7 +453,20 @@ __global__ void __launch_bounds__(kColThreads)
           static_cast<uint8_t>(s);
     }
     __syncthreads();
-    if (in) {
+    if (PLAIN && in) {
+      uint32_t f[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        f[i] = __byte_perm(__float_as_uint(inv[c0 + 2 * i]), __float_as_uint(inv[c0 + 2 * i + 1]),
+                           0x7632);
+#pragma unroll
+      for (int j = 0; j < PASS; ++j) {
+        const int r = r0 + j * RPP;
+        // (past the segment: zeros, also in a column whose scale is NaN)
+        *reinterpret_cast<uint2*>(cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col) =
+            r < a.rows ? scaled_codes(raw[j], f) : make_uint2(0, 0);
+      }
+    } else if (in) {
       float f[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) f[i] = inv[c0 + i];
@@ -412,7 +475,6 @@ __global__ void __launch_bounds__(kColThreads)
         const int r = r0 + j * RPP;
         float v[V];
         value(j, v);
-        // (past the segment: zeros, also in a column whose scale is NaN)
 #pragma unroll
         for (int i = 0; i < V; ++i) v[i] = r < a.rows ? v[i] * f[i] : 0.f;
         st_codes(cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col, v);
@@ -533,13 +595,15 @@ __global__ void __launch_bounds__(kColThreads)
 // TMA in boxes of 128 x 128 bytes (128-byte swizzle; a warp loads each side)
 // as they lie in memory, k- or row-major as the mode has it (the tensor core
 // takes 8-bit operands either way, so the one copy of W serves both
-// products). The warp that loads the columns' side first spreads the stage's
-// scale bytes to chunks of 512, in the order the tensor core reads them: its
-// copy is issued after they are written, so they are there when the copy's
-// bytes are, and a pair's odd CTA needs no arrival of its own at the even
-// one's barrier (a release at cluster scope, which took 1 us a stage: 8192 x
-// 8192 x 8192 in 1131 us). One thread copies a stage's chunks to tensor memory
-// (tcgen05.cp) and issues the products of 128 columns x 32 steps
+// products). A chunk of scales is 512 bytes, four for each of 128 rows, and a
+// product names the one of the four it takes: those of four stages. The warp
+// that loads the columns' side writes the chunks of four stages before the
+// first one's codes: its copy is issued after they are written, so they are
+// there when the copy's bytes are, and a pair's odd CTA needs no arrival of
+// its own at the even one's barrier (a release at cluster scope, which took 1
+// us a stage: 8192 x 8192 x 8192 in 1131 us). One thread copies the chunks to
+// tensor memory (tcgen05.cp; in the tensor core's way, so every stage its own
+// took 11 to 15 % more) and issues the products of 128 columns x 32 steps
 // (kind::mxf8f6f4) that read them. A pair's product takes 64 columns of
 // each CTA's 128, so its two accumulators hold columns 0..63 with 128..191, and
 // 64..127 with 192..255. Three accumulators of 128 columns: a tile takes two,
@@ -550,7 +614,10 @@ namespace f8 {
 using namespace ptx;
 constexpr int HN = 128, KS = 128;  // an accumulator's columns, a stage's steps
 constexpr int BOX = 128 * 128, CHUNK = 512;
-constexpr int SF_COL = 384, SF_STAGE = 12;  // tensor memory columns: 3 x 128, then scales
+// tensor memory columns: 3 x 128, then scales. A slot of scales is written
+// again SLOTS uses later, of a stage or more each, so after products that a
+// ring of fewer stages has seen the end of.
+constexpr int SF_COL = 384, SF_SLOT = 12, SLOTS = 10;
 constexpr int TMEM_COLS = 512, ACCS = 3;
 constexpr int EPI_THREADS = 256, THREADS = 128 + EPI_THREADS;
 
@@ -565,7 +632,7 @@ struct Cfg {
   static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
   static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
-  static_assert(SF_COL + STAGES * SF_STAGE <= TMEM_COLS, "tensor memory");
+  static_assert(SF_COL + SLOTS * SF_SLOT <= TMEM_COLS && SLOTS > STAGES, "tensor memory");
 };
 
 struct Params {
@@ -580,7 +647,9 @@ struct Params {
 };
 
 // kind::mxf8f6f4, E4M3 both sides, E8M0 scales, fp32 accumulator, K = 32; an
-// operand whose rows are the contraction's steps is "transposed"
+// operand whose rows are the contraction's steps is "transposed"; sf_byte:
+// which of the four bytes, for both sides
+__device__ __forceinline__ uint32_t sf_byte(uint32_t i) { return i << 4 | i << 29; }
 constexpr uint32_t idesc(int m, int n, bool a_steps, bool b_steps) {
   return (a_steps ? 1u << 15 : 0u) | (b_steps ? 1u << 16 : 0u) |
          (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) | (static_cast<uint32_t>(m >> 7) << 27);
@@ -868,9 +937,8 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         }
       }
     } else {
-      // a stage's scales, as chunks: row i's byte at (i % 32) 16 + (i / 32) 4
-      // (four times: any may be read). Loaded four stages at a time, four
-      // stages ahead.
+      // four stages' scales, as chunks: row i's four bytes at (i % 32) 16 + (i
+      // / 32) 4. Loaded four stages ahead.
       const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
       constexpr uint32_t ONE = 0x7f7f7f7fu;
       walk([&](int t, int k0, int k1) {
@@ -892,9 +960,9 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
                                   (static_cast<size_t>(kb) * nbk + m) * 32 + lane;
               const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bs) +
                                   (static_cast<size_t>(kb) * nbn + n) * 32 + lane;
-              r.w[i * 3] = m < nbk ? __ldg(a) : ONE;
-              r.w[i * 3 + 1] = __ldg(b);
-              r.w[i * 3 + 2] = n + 1 < nbn ? __ldg(b + 32) : ONE;
+              r.w[i] = m < nbk ? __ldg(a) : ONE;
+              r.w[4 + i] = __ldg(b);
+              r.w[8 + i] = n + 1 < nbn ? __ldg(b + 32) : ONE;
             }
           } else {
             // rows lane + 32 i, four blocks each; lanes 0..7: a block of the
@@ -913,48 +981,50 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           }
           return r;
         };
+        // the four bytes of each of four words, by byte
+        auto turn = [](const uint32_t* t) {
+          const uint32_t a = __byte_perm(t[0], t[1], 0x5140), b = __byte_perm(t[2], t[3], 0x5140);
+          const uint32_t c = __byte_perm(t[0], t[1], 0x7362), d = __byte_perm(t[2], t[3], 0x7362);
+          return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                            __byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632));
+        };
         const int nb = b_boxes(tl), col0 = tl.n0 + rank * 128;
         if (k0 < k1) nxt = load(k0 >> 2);
         for (int kb = k0; kb < k1; ++kb) {
-          const int i = kb & 3;
-          if (kb == k0 || i == 0) {
+          const bool four = kb == k0 || (kb & 3) == 0;
+          uint4 a, b0, b1;
+          if (four) {
             cur = nxt;
             if ((kb >> 2) * 4 + 4 < k1) nxt = load((kb >> 2) + 1);
-          }
-          uint4 a, b0, b1;
-          if constexpr (MODE == 2) {
-            uint32_t w[3];
+            if constexpr (MODE == 2) {
+              a = turn(cur.w);
+              b0 = turn(cur.w + 4);
+              b1 = turn(cur.w + 8);
+              if constexpr (PAIR) {
+                const uint4 c0 = b0, c1 = b1;
+                b0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
+                b1 = make_uint4(c0.z, c0.w, c1.z, c1.w);
+              }
+            } else {
+              a = make_uint4(cur.w[0], cur.w[1], cur.w[2], cur.w[3]);
+              uint32_t s[2] = {0, 0};
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              w[c] = i == 0 ? cur.w[c] : i == 1 ? cur.w[3 + c] : i == 2 ? cur.w[6 + c] : cur.w[9 + c];
-            auto four = [](uint32_t x) {
-              return make_uint4(__byte_perm(x, 0, 0x0000), __byte_perm(x, 0, 0x1111),
-                                __byte_perm(x, 0, 0x2222), __byte_perm(x, 0, 0x3333));
-            };
-            a = four(w[0]);
-            b0 = four(w[1]);
-            b1 = four(w[2]);
-            if constexpr (PAIR) {
-              const uint4 c0 = b0, c1 = b1;
-              b0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
-              b1 = make_uint4(c0.z, c0.w, c1.z, c1.w);
+              for (int i = 0; i < 8; ++i)
+                s[i & 1] |= __shfl_sync(0xffffffffu, cur.w[4], i) << (i >> 1) * 8;
+              // (a pair's accumulators have the same two blocks of columns)
+              b0 = PAIR ? make_uint4(s[0], s[0], s[1], s[1]) : make_uint4(s[0], s[0], s[0], s[0]);
+              b1 = make_uint4(s[1], s[1], s[1], s[1]);
             }
-          } else {
-            const uint32_t sel = 0x1111u * i;
-            a = make_uint4(__byte_perm(cur.w[0], 0, sel), __byte_perm(cur.w[1], 0, sel),
-                           __byte_perm(cur.w[2], 0, sel), __byte_perm(cur.w[3], 0, sel));
-            const uint32_t s0 = __shfl_sync(0xffffffffu, cur.w[4], i * 2) * 0x01010101u;
-            const uint32_t s1 = __shfl_sync(0xffffffffu, cur.w[4], i * 2 + 1) * 0x01010101u;
-            b0 = PAIR ? make_uint4(s0, s0, s1, s1) : make_uint4(s0, s0, s0, s0);
-            b1 = PAIR ? b0 : make_uint4(s1, s1, s1, s1);
           }
           if (!take()) return false;
-          const uint32_t sf = base0 + s * C::STAGE + C::OFF_SFA + lane * 16;
-          st_shared(sf, a);
-          st_shared(sf + CHUNK, b0);
-          st_shared(sf + 2 * CHUNK, b1);
-          fence_proxy_async_shared();
-          __syncwarp();
+          if (four) {
+            const uint32_t sf = base0 + s * C::STAGE + C::OFF_SFA + lane * 16;
+            st_shared(sf, a);
+            st_shared(sf + CHUNK, b0);
+            if constexpr (MODE == 2 || !PAIR) st_shared(sf + 2 * CHUNK, b1);
+            fence_proxy_async_shared();
+            __syncwarp();
+          }
           if (elect_one()) {
             uint8_t* dst = smem + s * C::STAGE + C::OFF_B;
 #pragma unroll
@@ -1001,25 +1071,33 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           ph ^= 1u;
         }
       };
-      // a stage's scales, and its products for the halves j0..j1 of the
-      // columns (inlined with constants for whole stages)
-      auto scales = [&](int nj) {
-        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
-        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
-        cp_scales<PAIR>(sf, sa0 + off);
-#pragma unroll
-        for (int j = 0; j < nj; ++j)
-          cp_scales<PAIR>(sf + 4 + j * 4, sa0 + off + (j + 1) * (CHUNK / 16));
+      // the next slot for scales, with four stages' where stage kb brings them
+      int slot = SLOTS - 1;
+      constexpr int B_CHUNKS = MODE == 2 || !PAIR ? 2 : 1;
+      auto on = [&](int kb, int k0) {
+        const bool four = kb == k0 || (kb & 3) == 0;
+        if (four && ++slot == SLOTS) slot = 0;
+        return four;
       };
-      auto products = [&](int steps, int j0, int j1, uint32_t d0, uint32_t d1, uint32_t more) {
+      auto scales = [&] {
         const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
-        const uint32_t sf = tmem_base + SF_COL + s * SF_STAGE;
+        const uint32_t sf = tmem_base + SF_COL + slot * SF_SLOT;
+#pragma unroll
+        for (int c = 0; c <= B_CHUNKS; ++c) cp_scales<PAIR>(sf + c * 4, sa0 + off + c * (CHUNK / 16));
+      };
+      // a stage's products for the halves j0..j1 of the columns (inlined with
+      // constants for whole stages)
+      auto products = [&](int kb, int steps, int j0, int j1, uint32_t d0, uint32_t d1,
+                          uint32_t more) {
+        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+        const uint32_t sf = tmem_base + SF_COL + slot * SF_SLOT;
+        const uint32_t idk = id | sf_byte(kb & 3);
 #pragma unroll
         for (int kk = 0; kk < steps; ++kk)
 #pragma unroll
           for (int j = j0; j < j1; ++j)
             mma<PAIR>(j == 0 ? d0 : d1, ad0 + off + kk * A_ON, bd0 + off + j * B_HALF + kk * B_ON,
-                      id, sf, sf + 4 + j * 4, kk > 0 ? 1u : more);
+                      idk, sf, sf + 4 + (B_CHUNKS > 1 ? j * 4 : 0), kk > 0 ? 1u : more);
       };
       if (elect_one()) walk([&](int t, int k0, int k1) {
         if (k0 == k1) return true;
@@ -1039,15 +1117,15 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         if (nj == 2) {
           // until the second accumulator is drained too: the first half's
           // products of a few stages, and after that the second's
-          const int s0 = s, most = min(min(k1, whole), k0 + STAGES - 1);
+          const int s0 = s, slot0 = slot, most = min(min(k1, whole), k0 + STAGES - 1);
           const uint32_t ph0 = ph;
           while (kb < most && !mbar_test_wait_cluster(&tempty[acc1], aph1 ^ 1u)) {
             if (!take()) {
               dead = true;
               return false;
             }
-            scales(2);
-            products(4, 0, 1, d0, d1, kb > k0 ? 1u : 0u);
+            if (on(kb, k0)) scales();
+            products(kb, 4, 0, 1, d0, d1, kb > k0 ? 1u : 0u);
             next();
             ++kb;
           }
@@ -1058,8 +1136,10 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           tc_fence_after();
           s = s0;
           ph = ph0;
+          slot = slot0;
           for (int i = k0; i < kb; ++i) {
-            products(4, 1, 2, d0, d1, i > k0 ? 1u : 0u);
+            on(i, k0);
+            products(i, 4, 1, 2, d0, d1, i > k0 ? 1u : 0u);
             commit<PAIR>(&empty[s]);
             next();
           }
@@ -1070,13 +1150,11 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
             break;
           }
           const uint32_t more = kb > k0 ? 1u : 0u;
-          if (kb < whole) {
-            scales(2);
-            products(4, 0, 2, d0, d1, more);
-          } else {
-            scales(nj);
-            products(MODE == 2 ? 4 : min(4, (len - kb * KS) / 32), 0, nj, d0, d1, more);
-          }
+          if (on(kb, k0)) scales();
+          if (kb < whole)
+            products(kb, 4, 0, 2, d0, d1, more);
+          else
+            products(kb, MODE == 2 ? 4 : min(4, (len - kb * KS) / 32), 0, nj, d0, d1, more);
           commit<PAIR>(&empty[s]);
           next();
         }
@@ -1283,7 +1361,12 @@ cudaError_t launch_rows(const void* x, const int32_t* src, int x_rows, const flo
     return launch_pdl(kernel, blocks, dim3(kColThreads), K::SMEM, s, xt, src, x_rows, weight, zt,
                       offsets, E, R, C, q, sc, cq, csc, err);
   };
-  return q == nullptr ? go(fp8_columns_kernel<T, ACT, false>) : go(fp8_columns_kernel<T, ACT, true>);
+  if constexpr (sizeof(T) == 2 && ACT == MOE_ACT_NONE)
+    if (weight == nullptr)
+      return q == nullptr ? go(fp8_columns_kernel<T, ACT, false, true>)
+                          : go(fp8_columns_kernel<T, ACT, true, true>);
+  return q == nullptr ? go(fp8_columns_kernel<T, ACT, false, false>)
+                      : go(fp8_columns_kernel<T, ACT, true, false>);
 }
 
 template <typename T>

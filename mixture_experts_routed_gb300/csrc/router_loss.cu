@@ -182,8 +182,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                             int32_t* tokens) {
   __shared__ float ps[kJoinWarps][32], zs[kJoinWarps][32];
   __shared__ int cs[kJoinWarps][32], ns[kJoinWarps][32];
-  __shared__ double fin[kJoinWarps][2];
-  __shared__ int fn[kJoinWarps][2], last;
+  __shared__ int last;
   pdl_wait();
   pdl_trigger();
   if (!q.good()) return;
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __syncthreads();
   if (!last) return;
   __threadfence();
-  double bal = 0, zz = 0;
+  float bal = 0.f, zz = 0.f;
   int used = 0, all = 0;
   for (int i = tid; i < static_cast<int>(gridDim.x); i += kJoinWarps * 32) {
     bal += __ldcg(term + 2 * i);
@@ -260,34 +259,28 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     used += m > 0;
     all += m;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    bal += __shfl_xor_sync(0xffffffffu, bal, o);
-    zz += __shfl_xor_sync(0xffffffffu, zz, o);
-  }
+  bal = warp_sum(bal);
+  zz = warp_sum(zz);
   used = __reduce_add_sync(0xffffffffu, used);
   all = __reduce_add_sync(0xffffffffu, all);
   if (lane == 0) {
-    fin[warp][0] = bal;
-    fin[warp][1] = zz;
-    fn[warp][0] = used;
-    fn[warp][1] = all;
+    ps[warp][0] = bal;
+    zs[warp][0] = zz;
+    cs[warp][0] = used;
+    ns[warp][0] = all;
   }
   __syncthreads();
-  if (tid != 0) return;
-  bal = zz = 0;
-  used = all = 0;
-  for (int w = 0; w < kJoinWarps; ++w) {
-    bal += fin[w][0];
-    zz += fin[w][1];
-    used += fn[w][0];
-    all += fn[w][1];
-  }
-  if (used > 0) bal /= used;
-  if (all > 0) zz /= all;
-  loss[0] = static_cast<float>(balance * bal + zcoef * zz);
-  loss[1] = static_cast<float>(bal);
-  loss[2] = static_cast<float>(zz);
+  if (warp != 0) return;
+  bal = warp_sum(ps[lane][0]);
+  zz = warp_sum(zs[lane][0]);
+  used = __reduce_add_sync(0xffffffffu, cs[lane][0]);
+  all = __reduce_add_sync(0xffffffffu, ns[lane][0]);
+  if (lane != 0) return;
+  if (used > 0) bal /= static_cast<float>(used);
+  if (all > 0) zz /= static_cast<float>(all);
+  loss[0] = fmaf(balance, bal, zcoef * zz);
+  loss[1] = bal;
+  loss[2] = zz;
   tokens[q.S] = used;
   tokens[q.S + 1] = all;
   *done = 0;
