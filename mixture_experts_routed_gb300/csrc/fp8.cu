@@ -244,22 +244,201 @@ __global__ void __launch_bounds__(256)
 // shared memory (cp.async) DEPTH tiles ahead. The columns' amax goes over
 // shared memory, a row's (where the rows' form is wanted too) by shuffles:
 // both forms come out of the one read. Bound by HBM.
-constexpr int kColThreads = 256, kTileBytes = 128 * 128;
+constexpr int kColThreads = 256, kColWarps = kColThreads / 32, kTileBytes = 128 * 128;
 
-template <typename T, int ACT>
-struct ColCfg {
+// T's tiles, TENSORS of them (x, or x and z), in at most BUFS buffers
+template <typename T, int TENSORS, int MOST>
+struct ColRing {
   static constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kColThreads / LPR,
                        PASS = 128 / RPP;
-  static constexpr bool Z = ACT == MOE_ACT_SILU_GRAD;
-  static constexpr int TENSORS = Z ? 2 : 1;
-  static constexpr int BYTES = kTileBytes * sizeof(T) * TENSORS;  // of one tile
-  static constexpr int BUFS = BYTES <= 32768 ? 3 : BYTES <= 65536 ? 2 : 1, DEPTH = BUFS - 1;
-  static constexpr int SMEM = BUFS * BYTES;
+  static constexpr int BYTES = kTileBytes * sizeof(T) * TENSORS;
+  static constexpr int FIT = BYTES <= 32768 ? 3 : BYTES <= 65536 ? 2 : 1;
+  static constexpr int BUFS = FIT < MOST ? FIT : MOST, DEPTH = BUFS - 1, SMEM = BUFS * BYTES;
   static_assert(SMEM <= 200 * 1024, "shared memory");
+  struct At {
+    int rt, cb, row0, rows;  // (rows 0: no such tile)
+  };
+  const T *x, *z;
+  const int32_t* src;
+  int x_rows, E, C, nb, tiles;
+  const int *seg, *base;
+  uint4* buf;  // [BUFS][TENSORS][PASS][threads]
+  uint32_t* err;
+  int c0, r0;
+
+  __device__ uint4* piece(int b, int h, int j) const {
+    return buf + ((b * TENSORS + h) * PASS + j) * kColThreads + threadIdx.x;
+  }
+  // Tile t's place, its values on their way to buffer b. A thread reads only
+  // what it copied: no barrier, and a buffer is free once its thread is
+  // through with it.
+  __device__ At fetch(int t, int b) const {
+    At a{0, 0, 0, 0};
+    if (t < tiles) {
+      a.rt = t / nb;
+      a.cb = t - a.rt * nb;
+      const int e = last_at_most(base, E - 1, a.rt);
+      a.row0 = seg[e] + (a.rt - base[e]) * 128;
+      a.rows = min(128, seg[e + 1] - a.row0);
+      const int col = a.cb * 128 + c0;
+      const size_t at = static_cast<size_t>(a.row0 + r0) * C + col;
+      if (a.rows == 128 && a.cb * 128 + 128 <= C && src == nullptr) {
+#pragma unroll
+        for (int j = 0; j < PASS; ++j) {
+          const size_t on = at + static_cast<size_t>(j) * RPP * C;
+          ptx::cp_async16(ptx::smem_u32(piece(b, 0, j)), x + on);
+          if constexpr (TENSORS > 1) ptx::cp_async16(ptx::smem_u32(piece(b, 1, j)), z + on);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < PASS; ++j) {
+          const int r = a.row0 + r0 + j * RPP;
+          bool some = r0 + j * RPP < a.rows && col < C;
+          int xr = r;
+          if (some && src != nullptr) {
+            xr = __ldg(src + r);
+            if (xr < 0 || xr >= x_rows) {
+              atomicOr(err, kErrBadIndex);
+              some = false;
+            }
+          }
+          if (some) {
+            ptx::cp_async16(ptx::smem_u32(piece(b, 0, j)), x + static_cast<size_t>(xr) * C + col);
+            if constexpr (TENSORS > 1)
+              ptx::cp_async16(ptx::smem_u32(piece(b, 1, j)), z + static_cast<size_t>(r) * C + col);
+          } else {
+            *piece(b, 0, j) = uint4{0, 0, 0, 0};
+            if constexpr (TENSORS > 1) *piece(b, 1, j) = uint4{0, 0, 0, 0};
+          }
+        }
+      }
+    }
+    ptx::cp_async_commit();
+    return a;
+  }
+  // f(tile's place, its buffer) for every tile of this block, in turn; all its
+  // threads take part
+  template <typename F>
+  __device__ void walk(F f) const {
+    At at[DEPTH + 1];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) at[i] = fetch(blockIdx.x + i * gridDim.x, i);
+    int b = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const int ahead = b + DEPTH >= BUFS ? b + DEPTH - BUFS : b + DEPTH;
+      at[DEPTH] = fetch(t + DEPTH * gridDim.x, ahead);
+      ptx::cp_async_wait<DEPTH>();
+      f(at[0], b);
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i) at[i] = at[i + 1];
+      if (++b == BUFS) b = 0;
+    }
+    ptx::cp_async_wait<0>();
+  }
 };
 
-// 8 bf16 values in words, scaled by a power of two a pair (exact, but for
-// results below 2^-126, whose code is 0 either way), to codes.
+struct ColOut {
+  uint8_t *q, *sc, *cq, *csc;
+};
+
+template <typename T, int ACT, bool ROWS>
+__global__ void __launch_bounds__(kColThreads)
+    fp8_columns_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
+                       const float* __restrict__ weight, const T* __restrict__ z,
+                       const int32_t* __restrict__ offsets, int E, int R, int C, const ColOut o,
+                       uint32_t* err) {
+  constexpr bool Z = ACT == MOE_ACT_SILU_GRAD;
+  using K = ColRing<T, Z ? 2 : 1, 3>;
+  constexpr int V = K::V, LPR = K::LPR, RPP = K::RPP, PASS = K::PASS;
+  extern __shared__ __align__(16) uint8_t buf[];
+  __shared__ int seg[kMaxExperts + 1], base[kMaxExperts + 1], ok;
+  __shared__ __align__(16) uint32_t top[kColWarps][128];
+  __shared__ float inv[128];
+  pdl_wait();
+  pdl_trigger();
+  if (!load_segments(offsets, E, R, seg, base, &ok, err)) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nb = up_div(C, 128), pitch = (nb + 3) & ~3;
+  const int c0 = tid % LPR * V, r0 = tid / LPR;
+  // (at most 2^17 + 256 row tiles of 512 blocks)
+  const K ring{x, z, src, x_rows, E, C, nb, base[E] * nb, seg, base,
+               reinterpret_cast<uint4*>(buf), err, c0, r0};
+  ring.walk([&](const typename K::At& a, int b) {
+    const int col = a.cb * 128 + c0;
+    const bool in = col < C;
+    float held[PASS][V];
+    uint32_t cm[V] = {};
+#pragma unroll
+    for (int j = 0; j < PASS; ++j) {
+      const int r = r0 + j * RPP;
+      const float w = weight != nullptr && r < a.rows ? __ldg(weight + a.row0 + r) : 1.f;
+      input<T, ACT>(*ring.piece(b, 0, j), *ring.piece(b, Z ? 1 : 0, j), w, held[j]);
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t g = mag(held[j][i]);
+        if constexpr (ROWS) m = max(m, g);
+        cm[i] = max(cm[i], g);
+      }
+      if constexpr (ROWS) {
+#pragma unroll
+        for (int k = 1; k < LPR; k <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, k));
+        const uint32_t s = scale_code(m);
+        const float f = inv_scale(s);
+        float v[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = held[j][i] * f;
+        if (r < a.rows && in) {
+          st_codes(o.q + static_cast<size_t>(a.row0 + r) * C + col, v);
+          if (c0 == 0)
+            o.sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
+        }
+      }
+    }
+    if constexpr (LPR == 16) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+    }
+    if (lane < LPR) {
+#pragma unroll
+      for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<uint4*>(&top[warp][c0 + i]) =
+            make_uint4(cm[i], cm[i + 1], cm[i + 2], cm[i + 3]);
+    }
+    __syncthreads();
+    if (tid < 128) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < kColWarps; ++k) m = max(m, top[k][tid]);
+      const uint32_t s = scale_code(m);
+      inv[tid] = inv_scale(s);
+      o.csc[(static_cast<size_t>(a.rt) * nb + a.cb) * 128 + (tid & 31) * 4 + (tid >> 5)] =
+          static_cast<uint8_t>(s);
+    }
+    __syncthreads();
+    if (in) {
+      float f[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = inv[c0 + i];
+#pragma unroll
+      for (int j = 0; j < PASS; ++j) {
+        const int r = r0 + j * RPP;
+        float v[V];
+        // (past the segment: zeros, also in a column whose scale is NaN)
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = r < a.rows ? held[j][i] * f[i] : 0.f;
+        st_codes(o.cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col, v);
+      }
+    }
+  });
+}
+
+// The same for bf16 values as they are (no activation, no weights), two values
+// to an instruction: their amax as 16-bit whole numbers, their scaling in bf16
+// (exact, but for results below 2^-126, whose code is 0 either way). The eight
+// rows' amax of a thread are reduced together, two to a word: a lane gives away
+// half of its words at each step, ends with two rows', makes their scales, and
+// hands the factors back.
 __device__ __forceinline__ uint2 scaled_codes(const uint4& u, const uint32_t (&f)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
   float v[8];
@@ -272,217 +451,106 @@ __device__ __forceinline__ uint2 scaled_codes(const uint4& u, const uint32_t (&f
   }
   return make_uint2(pack4(v[0], v[1], v[2], v[3]), pack4(v[4], v[5], v[6], v[7]));
 }
+// the bf16 factors of two scales, and the scales of two amax, in one word
+__device__ __forceinline__ uint32_t inv_pair(uint32_t lo, uint32_t hi) {
+  return __byte_perm(__float_as_uint(inv_scale(lo)), __float_as_uint(inv_scale(hi)), 0x7632);
+}
 
-// PLAIN: bf16 values as they are (no activation, no weights): amax and scaling
-// two values to an instruction
-template <typename T, int ACT, bool ROWS, bool PLAIN>
-__global__ void __launch_bounds__(kColThreads)
-    fp8_columns_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
-                       const float* __restrict__ weight, const T* __restrict__ z,
-                       const int32_t* __restrict__ offsets, int E, int R, int C,
-                       uint8_t* __restrict__ q, uint8_t* __restrict__ sc, uint8_t* __restrict__ cq,
-                       uint8_t* __restrict__ csc, uint32_t* err) {
-  using K = ColCfg<T, ACT>;
-  constexpr int V = K::V, LPR = K::LPR, RPP = K::RPP, PASS = K::PASS, WARPS = kColThreads / 32;
-  extern __shared__ __align__(16) uint8_t buf[];  // [BUFS][TENSORS][PASS][threads] 16 bytes
+template <bool ROWS>
+__global__ void __launch_bounds__(kColThreads, 3)
+    fp8_columns_bf16_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ src,
+                            int x_rows, const int32_t* __restrict__ offsets, int E, int R, int C,
+                            const ColOut o, uint32_t* err) {
+  using K = ColRing<__nv_bfloat16, 1, 2>;
+  static_assert(K::PASS == 8 && K::LPR == 16, "a thread's rows");
+  extern __shared__ __align__(16) uint8_t buf[];
   __shared__ int seg[kMaxExperts + 1], base[kMaxExperts + 1], ok;
-  __shared__ __align__(16) uint32_t top[WARPS][128];
-  __shared__ float inv[128];
+  __shared__ __align__(16) uint32_t top[kColWarps][64], inv[64];
   pdl_wait();
   pdl_trigger();
   if (!load_segments(offsets, E, R, seg, base, &ok, err)) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int nb = up_div(C, 128), pitch = (nb + 3) & ~3;
-  const int c0 = tid % LPR * V, r0 = tid / LPR;
+  const int c0 = tid % 16 * 8, r0 = tid / 16;
   // (at most 2^17 + 256 row tiles of 512 blocks)
-  const int tiles = base[E] * nb;
-  struct At {
-    int rt, cb, row0, rows;
-  };
-  auto place = [&](int t) {
-    At a;
-    a.rt = t / nb;
-    a.cb = t - a.rt * nb;
-    const int e = last_at_most(base, E - 1, a.rt);
-    a.row0 = seg[e] + (a.rt - base[e]) * 128;
-    a.rows = min(128, seg[e + 1] - a.row0);
-    return a;
-  };
-  auto piece = [&](int b, int h, int j) {
-    return reinterpret_cast<uint4*>(buf) +
-           ((b * K::TENSORS + h) * PASS + j) * kColThreads + tid;
-  };
-  auto fetch = [&](int t, int b) {
-    if (t < tiles) {
-      const At a = place(t);
-      const int col = a.cb * 128 + c0;
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        const int r = a.row0 + r0 + j * RPP;
-        bool some = r0 + j * RPP < a.rows && col < C;
-        int xr = r;
-        if (some && src != nullptr) {
-          xr = __ldg(src + r);
-          if (xr < 0 || xr >= x_rows) {
-            atomicOr(err, kErrBadIndex);
-            some = false;
-          }
-        }
-        if (some) {
-          ptx::cp_async16(ptx::smem_u32(piece(b, 0, j)), x + static_cast<size_t>(xr) * C + col);
-          if constexpr (K::Z)
-            ptx::cp_async16(ptx::smem_u32(piece(b, 1, j)), z + static_cast<size_t>(r) * C + col);
-        } else {
-          *piece(b, 0, j) = uint4{0, 0, 0, 0};
-          if constexpr (K::Z) *piece(b, 1, j) = uint4{0, 0, 0, 0};
-        }
-      }
-    }
-    ptx::cp_async_commit();
-  };
-  // (a thread reads only what it copied: no barrier, and a buffer is free
-  // once its thread is through with it)
-#pragma unroll
-  for (int i = 0; i < K::DEPTH; ++i) fetch(blockIdx.x + i * gridDim.x, i);
-  int b = 0;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const At a = place(t);
+  const K ring{x, nullptr, src, x_rows, E, C, nb, base[E] * nb, seg, base,
+               reinterpret_cast<uint4*>(buf), err, c0, r0};
+  ring.walk([&](const typename K::At& a, int b) {
     const int col = a.cb * 128 + c0;
     const bool in = col < C;
-    float w[PLAIN ? 1 : PASS];
+    uint4 raw[8];
+    uint32_t cm[4] = {}, rm[8];
 #pragma unroll
-    for (int j = 0; !PLAIN && j < PASS; ++j)
-      w[j] = weight != nullptr && r0 + j * RPP < a.rows ? __ldg(weight + a.row0 + r0 + j * RPP) : 1.f;
-    int ahead = b + K::DEPTH;
-    if (ahead >= K::BUFS) ahead -= K::BUFS;
-    fetch(t + K::DEPTH * gridDim.x, ahead);
-    ptx::cp_async_wait<K::DEPTH>();
-    // (a form that takes long to compute is kept in fp32; else the words are)
-    constexpr bool HELD = ACT != MOE_ACT_NONE;
-    float held[HELD ? PASS : 1][V];
-    uint4 raw[HELD ? 1 : PASS];
-    auto value = [&](int j, float (&v)[V]) {
-      if constexpr (HELD) {
+    for (int j = 0; j < 8; ++j) {
+      raw[j] = *ring.piece(b, 0, j);
+      const uint32_t u[4] = {raw[j].x & 0x7fff7fffu, raw[j].y & 0x7fff7fffu,
+                             raw[j].z & 0x7fff7fffu, raw[j].w & 0x7fff7fffu};
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = held[j][i];
-      } else {
-        input<T, ACT>(raw[j], raw[j], w[PLAIN ? 0 : j], v);
-      }
-    };
-    uint32_t cm[V] = {};
-    if constexpr (PLAIN) {
-      uint32_t c2[4] = {};
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        raw[j] = *piece(b, 0, j);
-        const uint32_t u[4] = {raw[j].x & 0x7fff7fffu, raw[j].y & 0x7fff7fffu,
-                               raw[j].z & 0x7fff7fffu, raw[j].w & 0x7fff7fffu};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) c2[i] = __vmaxu2(c2[i], u[i]);
-        if constexpr (ROWS) {
-          const int r = r0 + j * RPP;
-          uint32_t m = __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3]));
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t s = scale_code(max(m << 16, m & 0xffff0000u));
-          const uint32_t f = __byte_perm(__float_as_uint(inv_scale(s)), 0, 0x3232);
-          const uint32_t f4[4] = {f, f, f, f};
-          if (r < a.rows && in) {
-            *reinterpret_cast<uint2*>(q + static_cast<size_t>(a.row0 + r) * C + col) =
-                scaled_codes(raw[j], f4);
-            if (c0 == 0)
-              sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        c2[i] = __vmaxu2(c2[i], __shfl_xor_sync(0xffffffffu, c2[i], 16));
-        cm[2 * i] = c2[i] << 16;
-        cm[2 * i + 1] = c2[i] & 0xffff0000u;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        if constexpr (HELD)
-          input<T, ACT>(*piece(b, 0, j), *piece(b, K::TENSORS - 1, j), w[j], held[j]);
-        else
-          raw[j] = *piece(b, 0, j);
-        const int r = r0 + j * RPP;
-        float v[V];
-        value(j, v);
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const uint32_t g = mag(v[i]);
-          if constexpr (ROWS) m = max(m, g);
-          cm[i] = max(cm[i], g);
-        }
-        if constexpr (ROWS) {
-#pragma unroll
-          for (int o = 1; o < LPR; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          const uint32_t s = scale_code(m);
-          const float f = inv_scale(s);
-#pragma unroll
-          for (int i = 0; i < V; ++i) v[i] *= f;
-          if (r < a.rows && in) {
-            st_codes(q + static_cast<size_t>(a.row0 + r) * C + col, v);
-            if (c0 == 0) sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] = static_cast<uint8_t>(s);
-          }
-        }
-      }
-      if constexpr (LPR == 16) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) cm[i] = max(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
-      }
+      for (int i = 0; i < 4; ++i) cm[i] = __vmaxu2(cm[i], u[i]);
+      rm[j] = __vmaxu2(__vmaxu2(u[0], u[1]), __vmaxu2(u[2], u[3]));
     }
-    if (lane < LPR) {
 #pragma unroll
-      for (int i = 0; i < V; i += 4)
-        *reinterpret_cast<uint4*>(&top[warp][c0 + i]) =
-            make_uint4(cm[i], cm[i + 1], cm[i + 2], cm[i + 3]);
+    for (int i = 0; i < 4; ++i) cm[i] = __vmaxu2(cm[i], __shfl_xor_sync(0xffffffffu, cm[i], 16));
+    if (lane < 16)
+      *reinterpret_cast<uint4*>(&top[warp][c0 / 2]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+    if constexpr (ROWS) {
+      uint32_t p[4];  // rows j and j + 4
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        p[j] = __vmaxu2(__byte_perm(rm[j], rm[j + 4], 0x5410), __byte_perm(rm[j], rm[j + 4], 0x7632));
+      const bool up8 = lane & 8, up4 = lane & 4;
+      uint32_t m0 = up8 ? p[2] : p[0], m1 = up8 ? p[3] : p[1];
+      m0 = __vmaxu2(m0, __shfl_xor_sync(0xffffffffu, up8 ? p[0] : p[2], 8));
+      m1 = __vmaxu2(m1, __shfl_xor_sync(0xffffffffu, up8 ? p[1] : p[3], 8));
+      uint32_t m = __vmaxu2(up4 ? m1 : m0, __shfl_xor_sync(0xffffffffu, up4 ? m0 : m1, 4));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      const uint32_t lo = scale_code(m << 16), hi = scale_code(m & 0xffff0000u);
+      const uint32_t both = inv_pair(lo, hi);
+      // (two of the four lanes that hold a pair of rows write its scales)
+      const int r = r0 + ((lane >> 2 & 3) >> 1) * 32 + (lane >> 2 & 1) * 16 + (lane & 1) * 64;
+      if ((lane & 2) == 0 && r < a.rows)
+        o.sc[static_cast<size_t>(a.row0 + r) * pitch + a.cb] =
+            static_cast<uint8_t>(lane & 1 ? hi : lo);
+      uint8_t* to = o.q + static_cast<size_t>(a.row0 + r0) * C + col;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t f = __shfl_sync(0xffffffffu, both, (lane & 16) | j << 2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t g = __byte_perm(f, 0, h ? 0x3232 : 0x1010);
+          const uint32_t f4[4] = {g, g, g, g};
+          const int i = j + h * 4;
+          if (r0 + i * 16 < a.rows && in)
+            *reinterpret_cast<uint2*>(to + static_cast<size_t>(i) * 16 * C) =
+                scaled_codes(raw[i], f4);
+        }
+      }
     }
     __syncthreads();
-    if (tid < 128) {
+    if (tid < 64) {
       uint32_t m = 0;
 #pragma unroll
-      for (int k = 0; k < WARPS; ++k) m = max(m, top[k][tid]);
-      const uint32_t s = scale_code(m);
-      inv[tid] = inv_scale(s);
-      csc[(static_cast<size_t>(a.rt) * nb + a.cb) * 128 + (tid & 31) * 4 + (tid >> 5)] =
-          static_cast<uint8_t>(s);
+      for (int k = 0; k < kColWarps; ++k) m = __vmaxu2(m, top[k][tid]);
+      const uint32_t lo = scale_code(m << 16), hi = scale_code(m & 0xffff0000u);
+      inv[tid] = inv_pair(lo, hi);
+      // columns 2 tid and 2 tid + 1 of the block
+      uint8_t* to = o.csc + (static_cast<size_t>(a.rt) * nb + a.cb) * 128 + (tid & 15) * 8 + (tid >> 4);
+      to[0] = static_cast<uint8_t>(lo);
+      to[4] = static_cast<uint8_t>(hi);
     }
     __syncthreads();
-    if (PLAIN && in) {
-      uint32_t f[4];
+    if (in) {
+      const uint4 f = *reinterpret_cast<const uint4*>(&inv[c0 / 2]);
+      const uint32_t f4[4] = {f.x, f.y, f.z, f.w};
+      uint8_t* to = o.cq + (static_cast<size_t>(a.rt) * 128 + r0) * C + col;
+      // (past the segment: zeros, also in a column whose scale is NaN)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        f[i] = __byte_perm(__float_as_uint(inv[c0 + 2 * i]), __float_as_uint(inv[c0 + 2 * i + 1]),
-                           0x7632);
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        const int r = r0 + j * RPP;
-        // (past the segment: zeros, also in a column whose scale is NaN)
-        *reinterpret_cast<uint2*>(cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col) =
-            r < a.rows ? scaled_codes(raw[j], f) : make_uint2(0, 0);
-      }
-    } else if (in) {
-      float f[V];
-#pragma unroll
-      for (int i = 0; i < V; ++i) f[i] = inv[c0 + i];
-#pragma unroll
-      for (int j = 0; j < PASS; ++j) {
-        const int r = r0 + j * RPP;
-        float v[V];
-        value(j, v);
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[i] = r < a.rows ? v[i] * f[i] : 0.f;
-        st_codes(cq + (static_cast<size_t>(a.rt) * 128 + r) * C + col, v);
-      }
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint2*>(to + static_cast<size_t>(j) * 16 * C) =
+            r0 + j * 16 < a.rows ? scaled_codes(raw[j], f4) : make_uint2(0, 0);
     }
-    if (++b == K::BUFS) b = 0;
-  }
-  ptx::cp_async_wait<0>();
+  });
 }
 
 // ---------------------------------------------------------------- weights
@@ -1351,22 +1419,26 @@ cudaError_t launch_rows(const void* x, const int32_t* src, int x_rows, const flo
                       grid((groups + 7) / 8, static_cast<long long>(num_sms) * kRowBlocks),
                       dim3(256), 0, s, xt, src, x_rows, weight, zt, offsets, E, R, C, q, sc, err);
   }
-  using K = ColCfg<T, ACT>;
   const long long tiles = static_cast<long long>(row_tiles(R, E)) * up_div(C, 128);
-  const dim3 blocks = grid(tiles, static_cast<long long>(num_sms) * (K::SMEM <= 100 * 1024 ? 2 : 1));
-  auto go = [&](auto kernel) {
+  const ColOut o{q, sc, cq, csc};
+  auto go = [&](auto kernel, int smem, auto... args) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K::SMEM);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, blocks, dim3(kColThreads), K::SMEM, s, xt, src, x_rows, weight, zt,
-                      offsets, E, R, C, q, sc, cq, csc, err);
+    const int each = smem <= 64 * 1024 ? 3 : smem <= 96 * 1024 ? 2 : 1;  // blocks on an SM
+    return launch_pdl(kernel, grid(tiles, static_cast<long long>(num_sms) * each),
+                      dim3(kColThreads), smem, s, xt, src, x_rows, args..., offsets, E, R, C, o,
+                      err);
   };
   if constexpr (sizeof(T) == 2 && ACT == MOE_ACT_NONE)
-    if (weight == nullptr)
-      return q == nullptr ? go(fp8_columns_kernel<T, ACT, false, true>)
-                          : go(fp8_columns_kernel<T, ACT, true, true>);
-  return q == nullptr ? go(fp8_columns_kernel<T, ACT, false, false>)
-                      : go(fp8_columns_kernel<T, ACT, true, false>);
+    if (weight == nullptr) {
+      constexpr int SMEM = ColRing<T, 1, 2>::SMEM;
+      return q == nullptr ? go(fp8_columns_bf16_kernel<false>, SMEM)
+                          : go(fp8_columns_bf16_kernel<true>, SMEM);
+    }
+  constexpr int SMEM = ColRing<T, ACT == MOE_ACT_SILU_GRAD ? 2 : 1, 3>::SMEM;
+  return q == nullptr ? go(fp8_columns_kernel<T, ACT, false>, SMEM, weight, zt)
+                      : go(fp8_columns_kernel<T, ACT, true>, SMEM, weight, zt);
 }
 
 template <typename T>
