@@ -71,7 +71,7 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
-// A block sums one chunk, a token to a warp at a time, the next one's logits
+// A block sums one chunk, a token to a warp at a time, the next two's logits
 // loaded meanwhile.
 template <int NJ>
 __global__ void __launch_bounds__(kWarps * 32)
@@ -96,36 +96,34 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (t0 >= t1 || t0 < q.at(s)) return;
   for (int e = tid; e < E; e += kWarps * 32) cs[e] = 0;
   __syncthreads();
-  Row<NJ> sum, L, ahead;
+  Row<NJ> sum;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) sum.v[j] = 0.f;
   float zsum = 0.f;
   int n = 0;
-  bool on = false;
-  int e = 0;
-  // (a masked token's row is not read)
-  auto load = [&](int t) {
-    on = t < t1 && (mask == nullptr || __ldg(mask + t) != 0);
-    if (!on) return;
-    ahead.load(logits + static_cast<size_t>(t) * E, E, lane);
-    if (lane < k) e = __ldg(idx + static_cast<size_t>(t) * k + lane);
+  struct Token {
+    Row<NJ> L;
+    int e;    // this lane's choice
+    bool on;  // (a masked token's row is not read)
+  } ahead[2];
+  auto load = [&](Token& k0, int t) {
+    k0.on = t < t1 && (mask == nullptr || __ldg(mask + t) != 0);
+    if (!k0.on) return;
+    k0.L.load(logits + static_cast<size_t>(t) * E, E, lane);
+    if (lane < k) k0.e = __ldg(idx + static_cast<size_t>(t) * k + lane);
   };
-  load(t0 + warp);
-  for (int t = t0 + warp; t < t1; t += kWarps) {
-    const bool now = on;
-    const int chosen = e;
-    L = ahead;
-    load(t + kWarps);
-    if (!now) {
-      if (lane == 0) lse[t] = 0.f;
-      continue;
+  auto add = [&](Token& k0, int t) {
+    if (!k0.on) {
+      if (t < t1 && lane == 0) lse[t] = 0.f;
+      return;
     }
     if (lane < k) {
-      if (chosen >= 0 && chosen < E)
-        atomicAdd(&cs[chosen], 1);
+      if (k0.e >= 0 && k0.e < E)
+        atomicAdd(&cs[k0.e], 1);
       else
         atomicOr(err, kErrBadIndex);
     }
+    Row<NJ>& L = k0.L;
     float top = L.v[0];
 #pragma unroll
     for (int j = 1; j < NJ; ++j) top = fmaxf(top, L.v[j]);
@@ -143,6 +141,15 @@ __global__ void __launch_bounds__(kWarps * 32)
     zsum = fmaf(l, l, zsum);
     ++n;
     if (lane == 0) lse[t] = l;
+  };
+  load(ahead[0], t0 + warp);
+  load(ahead[1], t0 + warp + kWarps);
+  for (int t = t0 + warp; t < t1; t += 2 * kWarps) {
+    Token now[2] = {ahead[0], ahead[1]};
+    load(ahead[0], t + 2 * kWarps);
+    load(ahead[1], t + 3 * kWarps);
+    add(now[0], t);
+    add(now[1], t + kWarps);
   }
 #pragma unroll
   for (int j = 0; j < NJ; ++j) ps[warp][lane + 32 * j] = sum.v[j];
@@ -171,8 +178,8 @@ __global__ void __launch_bounds__(kWarps * 32)
   }
 }
 
-// A block joins the chunks of one sequence for 32 experts, in chunk order by
-// its warps and then over the warps; the last block to be done adds up the
+// A block joins the chunks of one sequence for 32 experts, every 32nd to a
+// warp, in order, and then over the warps; the last block to be done adds up the
 // sequences, in order.
 __global__ void __launch_bounds__(kJoinWarps * 32)
     router_loss_join_kernel(const Seqs q, int E, int k, float balance, float zcoef,
@@ -180,8 +187,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
                             const float2* __restrict__ tail, float* term, uint32_t* done,
                             float* __restrict__ loss, int32_t* __restrict__ counts,
                             int32_t* tokens) {
-  __shared__ float ps[kJoinWarps][32], zs[kJoinWarps][32];
-  __shared__ int cs[kJoinWarps][32], ns[kJoinWarps][32];
+  // (a warp writes a row and reads a column)
+  __shared__ float ps[kJoinWarps][33], zs[kJoinWarps], vs[32];
+  __shared__ int cs[kJoinWarps][33], ns[kJoinWarps];
   __shared__ int last;
   pdl_wait();
   pdl_trigger();
@@ -216,27 +224,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   }
   ps[warp][lane] = p;
   cs[warp][lane] = c;
-  zs[warp][lane] = z;
-  ns[warp][lane] = n;
+  z = warp_sum(z);
+  n = __reduce_add_sync(0xffffffffu, n);
+  if (lane == 0) {
+    zs[warp] = z;
+    ns[warp] = n;
+  }
+  __syncthreads();
+  // warp w: expert part * 32 + w
+  n = __reduce_add_sync(0xffffffffu, ns[lane]);
+  p = warp_sum(ps[lane][warp]);
+  c = __reduce_add_sync(0xffffffffu, cs[lane][warp]);
+  if (lane == 0) {
+    const int mine = part * 32 + warp;
+    const float tokens_f = static_cast<float>(n);
+    if (mine < E) counts[static_cast<size_t>(s) * E + mine] = c;
+    // f P = E c / (k n) p / n
+    vs[warp] = n > 0 && mine < E ? static_cast<float>(E) * static_cast<float>(c) /
+                                       (static_cast<float>(k) * tokens_f) * (p / tokens_f)
+                                 : 0.f;
+  }
   __syncthreads();
   if (warp == 0) {
-    p = z = 0.f;
-    c = n = 0;
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) {
-      p += ps[w][lane];
-      c += cs[w][lane];
-      z += zs[w][lane];
-      n += ns[w][lane];
-    }
-    z = warp_sum(z);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (e < E) counts[static_cast<size_t>(s) * E + e] = c;
-    // f P = E c / (k n) p / n
-    const float fn_ = static_cast<float>(n);
-    const float v = warp_sum(
-        n > 0 && e < E ? static_cast<float>(E) * static_cast<float>(c) / (static_cast<float>(k) * fn_) * (p / fn_)
-                       : 0.f);
+    const float v = warp_sum(vs[lane]);
+    z = warp_sum(zs[lane]);
     if (lane == 0) {
       term[2 * blockIdx.x] = v;
       term[2 * blockIdx.x + 1] = part == 0 ? z : 0.f;
@@ -264,17 +275,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   used = __reduce_add_sync(0xffffffffu, used);
   all = __reduce_add_sync(0xffffffffu, all);
   if (lane == 0) {
-    ps[warp][0] = bal;
-    zs[warp][0] = zz;
+    vs[warp] = bal;
+    zs[warp] = zz;
     cs[warp][0] = used;
-    ns[warp][0] = all;
+    ns[warp] = all;
   }
   __syncthreads();
   if (warp != 0) return;
-  bal = warp_sum(ps[lane][0]);
-  zz = warp_sum(zs[lane][0]);
+  bal = warp_sum(vs[lane]);
+  zz = warp_sum(zs[lane]);
   used = __reduce_add_sync(0xffffffffu, cs[lane][0]);
-  all = __reduce_add_sync(0xffffffffu, ns[lane][0]);
+  all = __reduce_add_sync(0xffffffffu, ns[lane]);
   if (lane != 0) return;
   if (used > 0) bal /= static_cast<float>(used);
   if (all > 0) zz /= static_cast<float>(all);
@@ -338,9 +349,9 @@ cudaError_t by_experts(int E, F f) {
   return E <= 128 ? f(std::integral_constant<int, 4>()) : f(std::integral_constant<int, 8>());
 }
 
-// Chunks of a warp's token or more, about two blocks to an SM.
+// Chunks of a warp's token or more, about three blocks to an SM.
 int chunk_len(int T) {
-  const int len = ceil_div(ceil_div(T, 304), kWarps) * kWarps;
+  const int len = ceil_div(ceil_div(T, 456), kWarps) * kWarps;
   return len < kWarps ? kWarps : len;
 }
 int slots_of(int T, int S) { return T / chunk_len(T) + S; }
