@@ -1042,7 +1042,8 @@ int moe_backward_with_dlogits(const moe_config_t* cfg, const void* x, const void
                               const void* dout, const float* dlogits, float* dx, float* dW_g,
                               float* dbias, float* dW1, float* dW2, void* ws, size_t ws_bytes,
                               void* stream) {
-  if (dlogits == nullptr && check_cfg(cfg) == MOE_OK && cfg->T > 0) return MOE_ERR_INVALID_ARG;
+  if (!words(dlogits) || (dlogits == nullptr && check_cfg(cfg) == MOE_OK && cfg->T > 0))
+    return MOE_ERR_INVALID_ARG;
   return backward_impl(cfg, x, W_g, bias, noise, W1, W2, fwd_ws, fwd_ws_bytes, dout, dx, dW_g,
                        dbias, dW1, dW2, ws, ws_bytes, stream, dlogits);
 }

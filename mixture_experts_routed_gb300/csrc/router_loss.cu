@@ -39,15 +39,10 @@ struct Seqs {
     }
     return lo;
   }
-  // Every thread of the block takes part: do the offsets rise within [0, T]?
-  __device__ bool good() const {
-    int bad = 0;
-    if (offsets != nullptr)
-      for (int s = threadIdx.x; s <= S; s += blockDim.x) {
-        const int o = at(s);
-        if (o < 0 || o > T || (s > 0 && o < at(s - 1))) bad = 1;
-      }
-    return __syncthreads_or(bad) == 0;
+  // sequence s begins and ends within [0, T], in this order
+  __device__ bool good(int s) const {
+    const int a = at(s), b = at(s + 1);
+    return a >= 0 && a <= b && b <= T;
   }
 };
 
@@ -78,19 +73,21 @@ __global__ void __launch_bounds__(kWarps * 32)
     router_loss_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                        const Seqs q, const uint8_t* __restrict__ mask, int E, int k,
                        float* __restrict__ lse, float* __restrict__ psum, int32_t* __restrict__ cnt,
-                       float2* __restrict__ tail, uint32_t* err) {
+                       float2* __restrict__ tail, uint32_t* __restrict__ bad, uint32_t* err) {
   __shared__ float ps[kWarps][NJ * 32];
   __shared__ int cs[NJ * 32];
   __shared__ float zs[kWarps];
   __shared__ int ns[kWarps];
   pdl_wait();
   pdl_trigger();
-  if (!q.good()) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(err, kErrBadIndex);
-    return;
+  // (a sequence a block is checked for all; each block's own, before it reads)
+  if (threadIdx.x == 0 && static_cast<int>(blockIdx.x) < q.S && !q.good(blockIdx.x)) {
+    *bad = 1;
+    atomicOr(err, kErrBadIndex);
   }
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = q.last(blockIdx.x, [&](int i) { return q.slot(i); });
+  if (!q.good(s)) return;
   const int t0 = q.at(s) + (static_cast<int>(blockIdx.x) - q.slot(s)) * q.len;
   const int t1 = min(t0 + q.len, q.at(s + 1));
   if (t0 >= t1 || t0 < q.at(s)) return;
@@ -184,7 +181,7 @@ __global__ void __launch_bounds__(kWarps * 32)
 __global__ void __launch_bounds__(kJoinWarps * 32)
     router_loss_join_kernel(const Seqs q, int E, int k, float balance, float zcoef,
                             const float* __restrict__ psum, const int32_t* __restrict__ cnt,
-                            const float2* __restrict__ tail, float* term, uint32_t* done,
+                            const float2* __restrict__ tail, float* term, uint32_t* bad, uint32_t* done,
                             float* __restrict__ loss, int32_t* __restrict__ counts,
                             int32_t* tokens) {
   // (a warp writes a row and reads a column)
@@ -193,11 +190,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   __shared__ int last;
   pdl_wait();
   pdl_trigger();
-  if (!q.good()) return;
+  const bool fine = __ldcg(bad) == 0;  // (else nothing is written)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int parts = ceil_div(E, 32);
   const int s = blockIdx.x / parts, part = blockIdx.x - s * parts, e = part * 32 + lane;
-  const int first = q.slot(s), chunks = ceil_div(q.at(s + 1) - q.at(s), q.len);
+  const int first = fine ? q.slot(s) : 0,
+            chunks = fine ? ceil_div(q.at(s + 1) - q.at(s), q.len) : 0;
   float p = 0.f, z = 0.f;
   int c = 0, n = 0;
   // (eight chunks' loads under way at a time)
@@ -238,7 +236,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
   if (lane == 0) {
     const int mine = part * 32 + warp;
     const float tokens_f = static_cast<float>(n);
-    if (mine < E) counts[static_cast<size_t>(s) * E + mine] = c;
+    if (mine < E && fine) counts[static_cast<size_t>(s) * E + mine] = c;
     // f P = E c / (k n) p / n
     vs[warp] = n > 0 && mine < E ? static_cast<float>(E) * static_cast<float>(c) /
                                        (static_cast<float>(k) * tokens_f) * (p / tokens_f)
@@ -251,13 +249,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32)
     if (lane == 0) {
       term[2 * blockIdx.x] = v;
       term[2 * blockIdx.x + 1] = part == 0 ? z : 0.f;
-      if (part == 0) tokens[s] = n;
+      if (part == 0 && fine) tokens[s] = n;
       __threadfence();
       last = atomicAdd(done, 1u) == gridDim.x - 1;
     }
   }
   __syncthreads();
   if (!last) return;
+  if (!fine) {
+    if (tid == 0) *bad = *done = 0;
+    return;
+  }
   __threadfence();
   float bal = 0.f, zz = 0.f;
   int used = 0, all = 0;
@@ -357,7 +359,7 @@ int chunk_len(int T) {
 int slots_of(int T, int S) { return T / chunk_len(T) + S; }
 
 struct Layout {
-  size_t done, psum, cnt, tail, term, total;
+  size_t bad, done, psum, cnt, tail, term, total;
 };
 Layout layout(int T, int E, int S) {
   Layout L;
@@ -368,8 +370,9 @@ Layout layout(int T, int E, int S) {
     o = align_up(o + bytes, 256);
     return at;
   };
-  take(4);  // the error word
-  L.done = 64;
+  take(4);  // the error word, and two of the kernels'
+  L.bad = 64;
+  L.done = 128;
   L.psum = take(slots * E * 4);
   L.cnt = take(slots * E * 4);
   L.tail = take(slots * 8);
@@ -395,14 +398,14 @@ cudaError_t launch_router_loss(const float* logits, const int32_t* idx, const in
   const cudaError_t e = by_experts(E, [&](auto nj) {
     return launch_pdl(router_loss_kernel<decltype(nj)::value>, dim3(slots_of(T, S)),
                       dim3(kWarps * 32), 0, s, logits, idx, q, mask, E, k, lse, psum, cnt, tail,
-                      reinterpret_cast<uint32_t*>(w));
+                      reinterpret_cast<uint32_t*>(w + L.bad), reinterpret_cast<uint32_t*>(w));
   });
   if (e != cudaSuccess) return e;
   return launch_pdl(router_loss_join_kernel, dim3(S * ceil_div(E, 32)), dim3(kJoinWarps * 32), 0, s, q,
                     E, k, balance, z, static_cast<const float*>(psum),
                     static_cast<const int32_t*>(cnt), static_cast<const float2*>(tail),
-                    reinterpret_cast<float*>(w + L.term), reinterpret_cast<uint32_t*>(w + L.done),
-                    loss, counts, tokens);
+                    reinterpret_cast<float*>(w + L.term), reinterpret_cast<uint32_t*>(w + L.bad),
+                    reinterpret_cast<uint32_t*>(w + L.done), loss, counts, tokens);
 }
 
 cudaError_t launch_router_loss_bwd(const float* logits, const int32_t* offsets, const uint8_t* mask,

@@ -95,6 +95,22 @@ def test_many_sequences(cuda_ok):
     check(L, idx, [0] + cut.tolist() + [5000])
 
 
+def test_more_sequences_than_tokens(cuda_ok):
+    L, idx = problem(50, 16, 2, seed=12)
+    cut = torch.sort(torch.randint(0, 51, (69998,), generator=gen(5), device="cuda")).values
+    c = moe.router_loss_config(50, 16, 2, S=69999, balance=0.5, z=0.1)
+    off = torch.cat([cut.new_zeros(1), cut, cut.new_full((1,), 50)]).to(torch.int32)
+    r = moe.router_loss(c, L, idx, ws=moe.alloc_router_loss_workspace(c), offsets=off)
+    # the sequences of none do not matter
+    some = torch.unique(off)
+    c2 = moe.router_loss_config(50, 16, 2, S=len(some) - 1, balance=0.5, z=0.1)
+    r2 = moe.router_loss(c2, L, idx, ws=moe.alloc_router_loss_workspace(c2), offsets=some)
+    assert torch.allclose(r.loss, r2.loss, rtol=1e-5)
+    assert r.tokens[-2:].tolist() == r2.tokens[-2:].tolist()
+    g = moe.router_loss_backward(c, L, r, offsets=off)
+    assert torch.allclose(g, moe.router_loss_backward(c2, L, r2, offsets=some), rtol=1e-5, atol=1e-9)
+
+
 def test_long_batch(cuda_ok):
     check(*problem(70000, 64, 6, seed=5))
 
@@ -157,8 +173,17 @@ def test_bad_offsets(cuda_ok, offs):
     c = moe.router_loss_config(64, 8, 2, S=3)
     ws = moe.alloc_router_loss_workspace(c)
     off = torch.tensor(offs, dtype=torch.int32, device="cuda")
-    moe.router_loss(c, L, idx, ws=ws, offsets=off)
+    good = torch.tensor([0, 5, 5, 64], dtype=torch.int32, device="cuda")
+    r = moe.router_loss(c, L, idx, ws=ws, offsets=good)
+    kept = [t.clone() for t in r[:3]]
+    ptrs = [t.data_ptr() for t in r]
+    st = moe._lib.load().moe_router_loss(
+        moe.api.ctypes.byref(c), L.data_ptr(), idx.data_ptr(), off.data_ptr(), None, *ptrs,
+        ws.data_ptr(), ws.nbytes, torch.cuda.current_stream().cuda_stream)
+    assert st == moe.MOE_OK
     assert moe.get_device_error(ws) == moe.MOE_ERR_BAD_INDEX
+    assert all(torch.equal(a, b) for a, b in zip(r[:3], kept))
+    # the workspace is as good as before
     check(L, idx, [0, 5, 5, 64], ws=ws)
 
 

@@ -198,9 +198,10 @@ def test_backward_with_dlogits_needs_them(lib):
     from test_abi_host import cfg
     c = cfg(T=8)
     a = [at(i) for i in range(20)]
-    st = lib.moe_backward_with_dlogits(ctypes.byref(c), *a[:3], None, *a[3:6], BIG, a[6], None,
-                                       *a[7:13], BIG, None)
-    assert st == INVALID
+    for dlogits in (None, ODD):
+        st = lib.moe_backward_with_dlogits(ctypes.byref(c), *a[:3], None, *a[3:6], BIG, a[6],
+                                           dlogits, *a[7:13], BIG, None)
+        assert st == INVALID
 
 
 # ---------------------------------------------------------------- dropout
