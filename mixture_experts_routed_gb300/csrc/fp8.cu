@@ -126,6 +126,31 @@ __device__ __forceinline__ void input(const uint4& x, const uint4& z, float w,
   }
 }
 
+// Eight bf16 values as they are, two to an instruction: their scaling by powers
+// of two in bf16 (exact, but for results below 2^-126, whose code is 0 either
+// way), their amax as 16-bit whole numbers.
+__device__ __forceinline__ uint2 scaled_codes(const uint4& u, const uint32_t (&f)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(f[i]));
+    v[2 * i] = __uint_as_float(r << 16);
+    v[2 * i + 1] = __uint_as_float(r & 0xffff0000u);
+  }
+  return make_uint2(pack4(v[0], v[1], v[2], v[3]), pack4(v[4], v[5], v[6], v[7]));
+}
+__device__ __forceinline__ uint32_t amax2(const uint4& u) {
+  return __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                  __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+}
+__device__ __forceinline__ uint32_t of_two(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
+// the bf16 factors of two scales in one word
+__device__ __forceinline__ uint32_t inv_pair(uint32_t lo, uint32_t hi) {
+  return __byte_perm(__float_as_uint(inv_scale(lo)), __float_as_uint(inv_scale(hi)), 0x7632);
+}
+
 // ---------------------------------------------------------------- rows
 // A warp quantises groups of four spans (256 bf16 or 128 fp32 values each) of
 // a row: a lane loads 16 bytes of a span, a block's 16 (32) lanes agree on its
@@ -134,7 +159,8 @@ __device__ __forceinline__ void input(const uint4& x, const uint4& z, float w,
 // Bound by HBM: the row is read once, a byte a value written.
 constexpr int kRowBlocks = 4;  // blocks of 256 threads an SM holds at once
 
-template <typename T, int ACT>
+// PLAIN: bf16 values as they are (no activation, no weights)
+template <typename T, int ACT, bool PLAIN>
 __global__ void __launch_bounds__(256)
     fp8_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ src, int x_rows,
                     const float* __restrict__ weight, const T* __restrict__ z,
@@ -211,18 +237,28 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
     for (int f = 0; f < F; ++f) {
       const int k = kb + f * SPAN;
-      float v[V];
-      input<T, ACT>(now[f], znow[Z ? f : 0], wnow, v);
-      uint32_t m = 0;
+      uint32_t s;
+      if constexpr (PLAIN) {
+        uint32_t m = amax2(now[f]);
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = max(m, mag(v[i]));
+        for (int o = 1; o < LPB; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = scale_code(of_two(m));
+        const uint32_t inv = inv_pair(s, s), f4[4] = {inv, inv, inv, inv};
+        if (k < C) *reinterpret_cast<uint2*>(qr + k) = scaled_codes(now[f], f4);
+      } else {
+        float v[V];
+        input<T, ACT>(now[f], znow[Z ? f : 0], wnow, v);
+        uint32_t m = 0;
 #pragma unroll
-      for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const uint32_t s = scale_code(m);
-      const float inv = inv_scale(s);
+        for (int i = 0; i < V; ++i) m = max(m, mag(v[i]));
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] *= inv;
-      if (k < C) st_codes(qr + k, v);
+        for (int o = 1; o < LPB; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        s = scale_code(m);
+        const float inv = inv_scale(s);
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] *= inv;
+        if (k < C) st_codes(qr + k, v);
+      }
       // (the scales' lines are padded to four)
       if constexpr (V == 8) {
         word |= (s | __shfl_sync(0xffffffffu, s, 16) << 8) << (f & 1) * 16;
@@ -433,29 +469,10 @@ __global__ void __launch_bounds__(kColThreads)
   });
 }
 
-// The same for bf16 values as they are (no activation, no weights), two values
-// to an instruction: their amax as 16-bit whole numbers, their scaling in bf16
-// (exact, but for results below 2^-126, whose code is 0 either way). The eight
+// The same for bf16 values as they are (no activation, no weights). The eight
 // rows' amax of a thread are reduced together, two to a word: a lane gives away
 // half of its words at each step, ends with two rows', makes their scales, and
 // hands the factors back.
-__device__ __forceinline__ uint2 scaled_codes(const uint4& u, const uint32_t (&f)[4]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t r;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(w[i]), "r"(f[i]));
-    v[2 * i] = __uint_as_float(r << 16);
-    v[2 * i + 1] = __uint_as_float(r & 0xffff0000u);
-  }
-  return make_uint2(pack4(v[0], v[1], v[2], v[3]), pack4(v[4], v[5], v[6], v[7]));
-}
-// the bf16 factors of two scales, and the scales of two amax, in one word
-__device__ __forceinline__ uint32_t inv_pair(uint32_t lo, uint32_t hi) {
-  return __byte_perm(__float_as_uint(inv_scale(lo)), __float_as_uint(inv_scale(hi)), 0x7632);
-}
-
 template <bool ROWS>
 __global__ void __launch_bounds__(kColThreads, 3)
     fp8_columns_bf16_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ src,
@@ -575,11 +592,14 @@ __global__ void __launch_bounds__(kColThreads)
   uint32_t m = 0;
 #pragma unroll
   for (int j = 0; j < PASS; ++j) {
-    float v[V];
-    unpack<T>(raw[j], v);
-#pragma unroll
-    for (int i = 0; i < V; ++i) m = max(m, mag(v[i]));
+    if constexpr (V == 8) {
+      m = __vmaxu2(m, amax2(raw[j]));
+    } else {
+      m = max(m, max(max(raw[j].x & 0x7fffffffu, raw[j].y & 0x7fffffffu),
+                     max(raw[j].z & 0x7fffffffu, raw[j].w & 0x7fffffffu)));
+    }
   }
+  if constexpr (V == 8) m = of_two(m);
   m = __reduce_max_sync(0xffffffffu, m);
   if ((tid & 31) == 0) top[tid >> 5] = m;
   __syncthreads();
@@ -593,11 +613,18 @@ __global__ void __launch_bounds__(kColThreads)
 #pragma unroll
   for (int j = 0; j < PASS; ++j) {
     const int k = k0 + j * RPP;
-    float v[V];
-    unpack<T>(raw[j], v);
+    if (n >= N || k >= K) continue;
+    uint8_t* to = q + at + static_cast<size_t>(k) * N + n;
+    if constexpr (V == 8) {
+      const uint32_t inv = inv_pair(s, s), f4[4] = {inv, inv, inv, inv};
+      *reinterpret_cast<uint2*>(to) = scaled_codes(raw[j], f4);
+    } else {
+      float v[V];
+      unpack<T>(raw[j], v);
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= f;
-    if (n < N && k < K) st_codes(q + at + static_cast<size_t>(k) * N + n, v);
+      for (int i = 0; i < V; ++i) v[i] *= f;
+      st_codes(to, v);
+    }
   }
 }
 
@@ -1379,6 +1406,12 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   }
 }
 
+// Rows per expert, on average, from which pairs of CTAs work on Y and dX (dW:
+// always). One CTA and pairs at 384 rows each: 68 and 81 us (64 experts of 2048
+// x 1408), 106 and 126 (8 of 4096 x 11008), 76 and 83 (16 of 7168 x 2048); at 512:
+// 90 and 86, 143 and 130, and 193 and 168 (32 of 7168 x 2048).
+constexpr int kPairRows = 448;
+
 template <int MODE, bool PAIR, typename TO>
 cudaError_t launch_product(const CUtensorMap& mA, const CUtensorMap& mA32, const CUtensorMap& mB,
                            const f8::Params& p, int grid, cudaStream_t s) {
@@ -1415,9 +1448,13 @@ cudaError_t launch_rows(const void* x, const int32_t* src, int x_rows, const flo
   };
   if (cq == nullptr) {
     const long long groups = static_cast<long long>(R) * up_div(C, sizeof(T) == 4 ? 512 : 1024);
-    return launch_pdl(fp8_rows_kernel<T, ACT>,
-                      grid((groups + 7) / 8, static_cast<long long>(num_sms) * kRowBlocks),
-                      dim3(256), 0, s, xt, src, x_rows, weight, zt, offsets, E, R, C, q, sc, err);
+    auto go = [&](auto kernel) {
+      return launch_pdl(kernel, grid((groups + 7) / 8, static_cast<long long>(num_sms) * kRowBlocks),
+                        dim3(256), 0, s, xt, src, x_rows, weight, zt, offsets, E, R, C, q, sc, err);
+    };
+    if constexpr (sizeof(T) == 2 && ACT == MOE_ACT_NONE)
+      if (weight == nullptr) return go(fp8_rows_kernel<T, ACT, true>);
+    return go(fp8_rows_kernel<T, ACT, false>);
   }
   const long long tiles = static_cast<long long>(row_tiles(R, E)) * up_div(C, 128);
   const ColOut o{q, sc, cq, csc};
@@ -1506,7 +1543,7 @@ cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, co
   const f8::Params p{as, bs, offsets, out, err, ctr, part, E, R, K, N, silu};
   const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
   if (mode == 2) return launch_product<2, true, float>(mA, mA32, mB, p, grid, s);
-  const bool pair = R >= kMx4PairRows * E;
+  const bool pair = R >= kPairRows * E;
   auto go = [&](auto kernel) { return kernel(mA, mA32, mB, p, grid, s); };
   if (mode == 1)
     return pair ? (out_f32 ? go(launch_product<1, true, float>)
