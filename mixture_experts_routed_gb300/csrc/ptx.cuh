@@ -335,6 +335,13 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// The same without ordering any memory access (a release at cluster scope
+// takes about 1 us): to hand back tensor memory whose reads are complete.
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
+}
+
 // Store a 32-bit value to another CTA's shared memory (a shared::cluster
 // address from mapa); a following release-arrive orders it for the reader.
 __device__ __forceinline__ void st_shared_cluster_s32(uint32_t cluster_addr, int v) {
