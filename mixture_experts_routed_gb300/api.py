@@ -655,20 +655,23 @@ def fp8_quantize_rows(c, x, offsets, *, ws, rows=True, columns=False, src=None, 
         raise MoEError(L.MOE_ERR_INVALID_ARG, f"x has {C} columns, not {c.K} or {c.N}")
     if not (rows or columns):
         raise MoEError(L.MOE_ERR_INVALID_ARG, "neither rows nor columns asked for")
+    px = _shaped("x", x, (R if src is None else c.x_rows, C), dt)
     q = scale = cq = cscale = None
+    dev = x.device
     if rows:
-        q = torch.empty((R, C), dtype=u8, device=x.device)
-        scale = torch.empty((R, _fp8_pitch(C)), dtype=u8, device=x.device)
+        q = torch.empty((R, C), dtype=u8, device=dev)
+        scale = torch.empty((R, _fp8_pitch(C)), dtype=u8, device=dev)
     if columns:
         n = int(lib.moe_fp8_column_rows(r))
-        cq = torch.empty((n, C), dtype=u8, device=x.device)
-        cscale = torch.empty((n // 128, -(-C // 128), 128), dtype=u8, device=x.device)
+        cq = torch.empty((n, C), dtype=u8, device=dev)
+        cscale = torch.empty((n // 128, -(-C // 128), 128), dtype=u8, device=dev)
     st = lib.moe_fp8_quantize_rows(
-        r, C, _shaped("x", x, (R if src is None else c.x_rows, C), dt), _indices("src", src, R),
-        _shaped("row_weight", row_weight, (R,), torch.float32), _ACTS[act],
-        _shaped("z", z, (R, C), dt), _indices("offsets", offsets, c.E + 1),
-        *[None if t is None else t.data_ptr() for t in (q, scale, cq, cscale)], _p(ws), ws.nbytes,
-        _s(stream))
+        r, C, px, None if src is None else _indices("src", src, R),
+        None if row_weight is None else _shaped("row_weight", row_weight, (R,), torch.float32),
+        _ACTS[act], None if z is None else _shaped("z", z, (R, C), dt),
+        _indices("offsets", offsets, c.E + 1), q.data_ptr() if rows else None,
+        scale.data_ptr() if rows else None, cq.data_ptr() if columns else None,
+        cscale.data_ptr() if columns else None, _p(ws), ws.nbytes, _s(stream))
     _check(st, "moe_fp8_quantize_rows")
     return Fp8Rows(q, scale, cq, cscale)
 
@@ -690,13 +693,17 @@ def fp8_product(c, rows, wq, w_scale, offsets, *, ws, transposed=False, out=None
     R, u8 = c.R, torch.uint8
     length, width = (c.N, c.K) if transposed else (c.K, c.N)
     odt = torch.float32 if c.out_dtype == L.MOE_DTYPE_F32 else torch.bfloat16
+    pq = _shaped("rows.q", _need("rows", rows.q), (R, length), u8)
+    ps = _shaped("rows.scale", rows.scale, (R, _fp8_pitch(length)), u8)
+    pw, pws = _fp8_weights(c, wq, w_scale)
     if out is None:
         out = torch.empty((R, width), dtype=odt, device=wq.device)
-    st = L.load().moe_fp8_product(
-        ctypes.byref(c), int(transposed), _shaped("rows.q", _need("rows", rows.q), (R, length), u8),
-        _shaped("rows.scale", rows.scale, (R, _fp8_pitch(length)), u8),
-        *_fp8_weights(c, wq, w_scale), _indices("offsets", offsets, c.E + 1),
-        _shaped("out", out, (R, width), odt), _p(ws), ws.nbytes, _s(stream))
+        po = out.data_ptr()
+    else:
+        po = _shaped("out", out, (R, width), odt)
+    st = L.load().moe_fp8_product(ctypes.byref(c), int(transposed), pq, ps, pw, pws,
+                                  _indices("offsets", offsets, c.E + 1), po, _p(ws), ws.nbytes,
+                                  _s(stream))
     _check(st, "moe_fp8_product")
     return out
 
@@ -758,30 +765,53 @@ def alloc_router_loss_workspace(c, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-class RouterLoss(NamedTuple):
-    """``loss`` fp32 [3]: the loss, the balance and the z loss without their coefficients;
-    ``counts`` int32 [S, E]: the experts' tokens by sequence. ``tokens`` int32 [S + 2] (by
-    sequence, sequences with any, all) and ``lse`` fp32 [T] are the backward's."""
-    loss: torch.Tensor
-    counts: torch.Tensor
-    tokens: torch.Tensor
-    lse: torch.Tensor
+class RouterLoss:
+    """What ``router_loss`` gives: ``loss`` fp32 [3], the loss, the balance and the z loss without
+    their coefficients; ``counts`` int32 [S, E], the experts' tokens by sequence; and for the
+    backward ``tokens`` int32 [S + 2] (by sequence, sequences with any, all) and ``lse`` fp32 [T].
+    Views of one buffer, made where they are asked for (an allocation costs a call what a view
+    does, and a call costs more than its kernels)."""
+    __slots__ = ("buf", "T", "E", "S")
+
+    def __init__(self, T, E, S, device):
+        self.T, self.E, self.S = T, E, S
+        self.buf = torch.empty(4 + T + S * E + S + 2, dtype=torch.int32, device=device)
+
+    def pointers(self):
+        """Device addresses of loss, counts, tokens and lse."""
+        at = self.buf.data_ptr()
+        counts = at + 4 * (4 + self.T)
+        return at, counts, counts + 4 * self.S * self.E, at + 16
+
+    @property
+    def loss(self):
+        return self.buf[:3].view(torch.float32)
+
+    @property
+    def counts(self):
+        at = 4 + self.T
+        return self.buf[at:at + self.S * self.E].view(self.S, self.E)
+
+    @property
+    def tokens(self):
+        return self.buf[4 + self.T + self.S * self.E:]
+
+    @property
+    def lse(self):
+        return self.buf[4:4 + self.T].view(torch.float32)
 
 
 def router_loss(c, logits, topk_idx, *, ws, offsets=None, mask=None, stream=None) -> RouterLoss:
     """The router's losses of logits [T, E] and choices [T, k]. ``offsets`` int32 [S + 1]: the
     sequences' tokens (None: one of all); ``mask`` [T], bool or uint8: the tokens that count."""
-    T, E, k, S = c.T, c.E, c.k, c.S
-    i32, dev = torch.int32, logits.device
-    r = RouterLoss(torch.empty(3, dtype=torch.float32, device=dev),
-                   torch.empty((S, E), dtype=i32, device=dev),
-                   torch.empty(S + 2, dtype=i32, device=dev),
-                   torch.empty(T, dtype=torch.float32, device=dev))
-    st = L.load().moe_router_loss(
-        ctypes.byref(c), _shaped("logits", logits, (T, E), torch.float32),
-        _shaped("topk_idx", topk_idx, (T, k), i32), _indices("offsets", offsets, S + 1),
-        _mask_p(mask, T), *[t.data_ptr() for t in r], _p(ws), ws.nbytes, _s(stream))
-    _check(st, "moe_router_loss")
+    T, E, S = c.T, c.E, c.S
+    px = _shaped("logits", logits, (T, E), torch.float32)
+    pi = _shaped("topk_idx", topk_idx, (T, c.k), torch.int32)
+    po = None if offsets is None else _indices("offsets", offsets, S + 1)
+    pm = None if mask is None else _mask_p(mask, T)
+    r = RouterLoss(T, E, S, logits.device)
+    _check(L.load().moe_router_loss(ctypes.byref(c), px, pi, po, pm, *r.pointers(), _p(ws),
+                                    ws.nbytes, _s(stream)), "moe_router_loss")
     return r
 
 
@@ -791,15 +821,20 @@ def router_loss_backward(c, logits, kept, *, dloss=None, offsets=None, mask=None
     after a ``router_loss`` of the same inputs that gave ``kept``. What ``backward`` takes as
     ``dlogits``."""
     T, E, S, f32 = c.T, c.E, c.S, torch.float32
+    if (kept.T, kept.E, kept.S) != (T, E, S):
+        raise MoEError(L.MOE_ERR_INVALID_ARG, f"kept is of T, E, S = {kept.T}, {kept.E}, {kept.S}, "
+                                              f"not {T}, {E}, {S}")
+    px = _shaped("logits", logits, (T, E), f32)
     if out is None:
         out = torch.empty_like(logits)
+        pout = out.data_ptr()
+    else:
+        pout = _shaped("out", out, (T, E), f32)
+    _, counts, tokens, lse = kept.pointers()
     st = L.load().moe_router_loss_backward(
-        ctypes.byref(c), _shaped("logits", logits, (T, E), f32),
-        _indices("offsets", offsets, S + 1), _mask_p(mask, T),
-        _shaped("counts", kept.counts, (S, E), torch.int32),
-        _shaped("tokens", kept.tokens, (S + 2,), torch.int32),
-        _shaped("lse", kept.lse, (T,), f32), _shaped("dloss", dloss, (1,), f32),
-        _shaped("out", out, (T, E), f32), _s(stream))
+        ctypes.byref(c), px, None if offsets is None else _indices("offsets", offsets, S + 1),
+        None if mask is None else _mask_p(mask, T), counts, tokens, lse,
+        None if dloss is None else _shaped("dloss", dloss, (1,), f32), pout, _s(stream))
     _check(st, "moe_router_loss_backward")
     return out
 
@@ -821,22 +856,28 @@ def dropout(c, x, state, *, residual=None, out=None, stream=None):
     """residual + x dropped and scaled, [T, d]. ``state``: int64 [2] on the GPU, the seed and the
     step; its values at the time the kernel runs are used. ``out`` may be x or residual."""
     td, dt = (c.T, c.d), _ndt(c)
+    px = _shaped("x", x, td, dt)
+    pr = None if residual is None else _shaped("residual", residual, td, dt)
+    ps = _shaped("state", state, (2,), torch.int64)
     if out is None:
         out = torch.empty_like(x)
-    st = L.load().moe_dropout(
-        ctypes.byref(c), _shaped("x", x, td, dt), _shaped("residual", residual, td, dt),
-        _shaped("state", state, (2,), torch.int64), _shaped("out", out, td, dt), _s(stream))
-    _check(st, "moe_dropout")
+        po = out.data_ptr()
+    else:
+        po = _shaped("out", out, td, dt)
+    _check(L.load().moe_dropout(ctypes.byref(c), px, pr, ps, po, _s(stream)), "moe_dropout")
     return out
 
 
 def dropout_backward(c, dout, state, *, dx=None, stream=None):
     """dx [T, d] of a ``dropout`` with this config and state (the residual's gradient is dout)."""
     td, dt = (c.T, c.d), _ndt(c)
+    pd = _shaped("dout", dout, td, dt)
+    ps = _shaped("state", state, (2,), torch.int64)
     if dx is None:
         dx = torch.empty_like(dout)
-    st = L.load().moe_dropout_backward(
-        ctypes.byref(c), _shaped("dout", dout, td, dt), _shaped("state", state, (2,), torch.int64),
-        _shaped("dx", dx, td, dt), _s(stream))
-    _check(st, "moe_dropout_backward")
+        px = dx.data_ptr()
+    else:
+        px = _shaped("dx", dx, td, dt)
+    _check(L.load().moe_dropout_backward(ctypes.byref(c), pd, ps, px, _s(stream)),
+           "moe_dropout_backward")
     return dx

@@ -286,6 +286,8 @@ def test_binding_refuses_wrong_shapes_types_and_forms():
     idx = torch.zeros((4, 2), dtype=i32)
     refused(lambda: moe.router_loss(c, torch.zeros((4, 8), dtype=bf), idx, ws=ws))
     refused(lambda: moe.router_loss(c, torch.zeros((4, 8)), idx.long(), ws=ws))
+    kept = moe.RouterLoss(4, 8, 2, "cpu")
+    refused(lambda: moe.router_loss_backward(c, torch.zeros((4, 8)), kept))
     c = moe.dropout_config(4, 64)
     x = torch.zeros((4, 64), dtype=bf)
     refused(lambda: moe.dropout(c, x.float(), torch.zeros(2, dtype=torch.int64)))
