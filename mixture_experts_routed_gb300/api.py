@@ -612,18 +612,57 @@ def alloc_fp8_workspace(c, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-class Fp8Rows(NamedTuple):
-    """Quantised rows [R, C]: codes ``q`` and scales ``scale`` [R, pitch] of blocks of 128 along
-    a row, codes ``cq`` [column rows, C] and scales ``cscale`` [tiles, ceil(C / 128), 128] of
-    blocks of 128 rows of an expert, all uint8; None for a form that was not asked for."""
-    q: torch.Tensor | None
-    scale: torch.Tensor | None
-    cq: torch.Tensor | None
-    cscale: torch.Tensor | None
-
-
 def _fp8_pitch(cols):
     return (-(-cols // 128) + 3) // 4 * 4
+
+
+class Fp8Rows:
+    """Quantised rows [R, C], uint8: codes ``q`` and scales ``scale`` [R, pitch] of blocks of 128
+    along a row, codes ``cq`` [128 tiles, C] and scales ``cscale`` [tiles, ceil(C / 128), 128] of
+    blocks of 128 rows of an expert; None for a form that was not asked for. Views of one buffer,
+    made where they are asked for."""
+    __slots__ = ("buf", "R", "C", "rows", "columns", "tiles", "at")
+
+    def __init__(self, R, C, rows, columns, tiles, device):
+        self.R, self.C, self.rows, self.columns, self.tiles = R, C, rows, columns, tiles
+        # where q, scale, cq and cscale begin, and the end
+        q = R * C if rows else 0
+        s = q + ((R * _fp8_pitch(C) + 255) // 256 * 256 if rows else 0)
+        c = s + (tiles * 128 * C if columns else 0)
+        self.at = (0, q, s, c, c + (tiles * -(-C // 128) * 128 if columns else 0))
+        self.buf = torch.empty(self.at[4], dtype=torch.uint8, device=device)
+
+    def _view(self, i, *shape):
+        return self.buf[self.at[i]:self.at[i + 1]][:shape[0] * shape[1]].view(shape[0], shape[1])
+
+    @property
+    def q(self):
+        return self._view(0, self.R, self.C) if self.rows else None
+
+    @property
+    def scale(self):
+        return self._view(1, self.R, _fp8_pitch(self.C)) if self.rows else None
+
+    @property
+    def cq(self):
+        return self._view(2, self.tiles * 128, self.C) if self.columns else None
+
+    @property
+    def cscale(self):
+        n = -(-self.C // 128)
+        return self._view(3, self.tiles, n * 128).view(-1, n, 128) if self.columns else None
+
+    def pointers(self, form, name, R, C, tiles=None):
+        """Device addresses of a form's codes and scales, if it has that and the call's sizes."""
+        if not (self.rows if form == 0 else self.columns):
+            raise MoEError(L.MOE_ERR_INVALID_ARG,
+                           f"{name} was not quantised in the form this takes")
+        if (self.R, self.C) != (R, C) or tiles not in (None, self.tiles):
+            raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is {(self.R, self.C)}, not {(R, C)}")
+        if not self.buf.is_cuda:
+            raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} is not in GPU memory")
+        base = self.buf.data_ptr()
+        return base + self.at[2 * form], base + self.at[2 * form + 1]
 
 
 def fp8_quantize_weights(c, W, *, q=None, scale=None, stream=None):
@@ -647,7 +686,7 @@ def fp8_quantize_rows(c, x, offsets, *, ws, rows=True, columns=False, src=None, 
     """Rows x [R, K] or [R, N], or with ``src`` [R] the rows x[src] of x [x_rows, ..], times
     ``row_weight`` [R], in the forms asked for. ``act``: None, "silu" (of x) or "silu_grad" (x
     times SiLU'(z), z [R, ..])."""
-    lib, r, u8 = L.load(), ctypes.byref(c), torch.uint8
+    lib, r = L.load(), ctypes.byref(c)
     R, C, dt = c.R, x.shape[-1], _ndt(c)
     if act not in _ACTS:
         raise MoEError(L.MOE_ERR_INVALID_ARG, f"act is {act!r}")
@@ -656,24 +695,17 @@ def fp8_quantize_rows(c, x, offsets, *, ws, rows=True, columns=False, src=None, 
     if not (rows or columns):
         raise MoEError(L.MOE_ERR_INVALID_ARG, "neither rows nor columns asked for")
     px = _shaped("x", x, (R if src is None else c.x_rows, C), dt)
-    q = scale = cq = cscale = None
-    dev = x.device
-    if rows:
-        q = torch.empty((R, C), dtype=u8, device=dev)
-        scale = torch.empty((R, _fp8_pitch(C)), dtype=u8, device=dev)
-    if columns:
-        n = int(lib.moe_fp8_column_rows(r))
-        cq = torch.empty((n, C), dtype=u8, device=dev)
-        cscale = torch.empty((n // 128, -(-C // 128), 128), dtype=u8, device=dev)
+    out = Fp8Rows(R, C, rows, columns, int(lib.moe_fp8_column_rows(r)) // 128 if columns else 0,
+                  x.device)
+    at, (_, o1, o2, o3, _) = out.buf.data_ptr(), out.at
     st = lib.moe_fp8_quantize_rows(
         r, C, px, None if src is None else _indices("src", src, R),
         None if row_weight is None else _shaped("row_weight", row_weight, (R,), torch.float32),
         _ACTS[act], None if z is None else _shaped("z", z, (R, C), dt),
-        _indices("offsets", offsets, c.E + 1), q.data_ptr() if rows else None,
-        scale.data_ptr() if rows else None, cq.data_ptr() if columns else None,
-        cscale.data_ptr() if columns else None, _p(ws), ws.nbytes, _s(stream))
+        _indices("offsets", offsets, c.E + 1), at if rows else None, at + o1 if rows else None,
+        at + o2 if columns else None, at + o3 if columns else None, _p(ws), ws.nbytes, _s(stream))
     _check(st, "moe_fp8_quantize_rows")
-    return Fp8Rows(q, scale, cq, cscale)
+    return out
 
 
 def _fp8_weights(c, wq, w_scale):
@@ -681,20 +713,13 @@ def _fp8_weights(c, wq, w_scale):
             _shaped("w_scale", w_scale, (c.E, -(-c.K // 128), -(-c.N // 128)), torch.uint8))
 
 
-def _need(name, t):
-    if t is None:
-        raise MoEError(L.MOE_ERR_INVALID_ARG, f"{name} was not quantised in the form this takes")
-    return t
-
-
 def fp8_product(c, rows, wq, w_scale, offsets, *, ws, transposed=False, out=None, stream=None):
     """out[r] = rows[r] . W[e], [R, N], from rows of K columns; ``transposed``: rows[r] . W[e]^T,
     [R, K], from rows of N columns."""
-    R, u8 = c.R, torch.uint8
+    R = c.R
     length, width = (c.N, c.K) if transposed else (c.K, c.N)
     odt = torch.float32 if c.out_dtype == L.MOE_DTYPE_F32 else torch.bfloat16
-    pq = _shaped("rows.q", _need("rows", rows.q), (R, length), u8)
-    ps = _shaped("rows.scale", rows.scale, (R, _fp8_pitch(length)), u8)
+    pq, ps = rows.pointers(0, "rows", R, length)
     pw, pws = _fp8_weights(c, wq, w_scale)
     if out is None:
         out = torch.empty((R, width), dtype=odt, device=wq.device)
@@ -711,18 +736,16 @@ def fp8_product(c, rows, wq, w_scale, offsets, *, ws, transposed=False, out=None
 def fp8_weight_grad(c, x, dy, offsets, *, ws, out=None, stream=None):
     """fp32 dW [E, K, N]: the sum over each expert's rows of x[r]^T dy[r], from the columns of x
     [R, K] and of dy [R, N]."""
-    lib, r, u8 = L.load(), ctypes.byref(c), torch.uint8
-    E, K, N = c.E, c.K, c.N
-    n = int(lib.moe_fp8_column_rows(r))
+    lib, r = L.load(), ctypes.byref(c)
+    R, E, K, N = c.R, c.E, c.K, c.N
+    tiles = int(lib.moe_fp8_column_rows(r)) // 128
+    px, pxs = x.pointers(1, "x", R, K, tiles)
+    pd, pds = dy.pointers(1, "dy", R, N, tiles)
     if out is None:
-        out = torch.empty((E, K, N), dtype=torch.float32, device=_need("x", x.cq).device)
-    st = lib.moe_fp8_weight_grad(
-        r, _shaped("x.cq", _need("x", x.cq), (n, K), u8),
-        _shaped("x.cscale", x.cscale, (n // 128, -(-K // 128), 128), u8),
-        _shaped("dy.cq", _need("dy", dy.cq), (n, N), u8),
-        _shaped("dy.cscale", dy.cscale, (n // 128, -(-N // 128), 128), u8),
-        _indices("offsets", offsets, E + 1),
-        _shaped("out", out, (E, K, N), torch.float32), _p(ws), ws.nbytes, _s(stream))
+        out = torch.empty((E, K, N), dtype=torch.float32, device=x.buf.device)
+    st = lib.moe_fp8_weight_grad(r, px, pxs, pd, pds, _indices("offsets", offsets, E + 1),
+                                 _shaped("out", out, (E, K, N), torch.float32), _p(ws), ws.nbytes,
+                                 _s(stream))
     _check(st, "moe_fp8_weight_grad")
     return out
 
@@ -740,14 +763,12 @@ def fp8_dequantize_weights(c, wq, w_scale, *, W=None, stream=None):
 
 def fp8_dequantize_rows(c, rows, *, x=None, stream=None):
     """The values of quantised rows, [R, C], from their ``q`` and ``scale``."""
-    q = _need("rows", rows.q)
-    R, C = c.R, q.shape[-1]
+    R, C = c.R, rows.C
+    pq, ps = rows.pointers(0, "rows", R, C)
     if x is None:
-        x = torch.empty((R, C), dtype=_ndt(c), device=q.device)
-    st = L.load().moe_fp8_dequantize_rows(
-        ctypes.byref(c), C, _shaped("rows.q", q, (R, C), torch.uint8),
-        _shaped("rows.scale", rows.scale, (R, _fp8_pitch(C)), torch.uint8),
-        _shaped("x", x, (R, C), _ndt(c)), _s(stream))
+        x = torch.empty((R, C), dtype=_ndt(c), device=rows.buf.device)
+    st = L.load().moe_fp8_dequantize_rows(ctypes.byref(c), C, pq, ps,
+                                          _shaped("x", x, (R, C), _ndt(c)), _s(stream))
     _check(st, "moe_fp8_dequantize_rows")
     return x
 
@@ -765,53 +786,32 @@ def alloc_router_loss_workspace(c, device=None) -> torch.Tensor:
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 
 
-class RouterLoss:
-    """What ``router_loss`` gives: ``loss`` fp32 [3], the loss, the balance and the z loss without
-    their coefficients; ``counts`` int32 [S, E], the experts' tokens by sequence; and for the
-    backward ``tokens`` int32 [S + 2] (by sequence, sequences with any, all) and ``lse`` fp32 [T].
-    Views of one buffer, made where they are asked for (an allocation costs a call what a view
-    does, and a call costs more than its kernels)."""
-    __slots__ = ("buf", "T", "E", "S")
-
-    def __init__(self, T, E, S, device):
-        self.T, self.E, self.S = T, E, S
-        self.buf = torch.empty(4 + T + S * E + S + 2, dtype=torch.int32, device=device)
-
-    def pointers(self):
-        """Device addresses of loss, counts, tokens and lse."""
-        at = self.buf.data_ptr()
-        counts = at + 4 * (4 + self.T)
-        return at, counts, counts + 4 * self.S * self.E, at + 16
-
-    @property
-    def loss(self):
-        return self.buf[:3].view(torch.float32)
-
-    @property
-    def counts(self):
-        at = 4 + self.T
-        return self.buf[at:at + self.S * self.E].view(self.S, self.E)
-
-    @property
-    def tokens(self):
-        return self.buf[4 + self.T + self.S * self.E:]
-
-    @property
-    def lse(self):
-        return self.buf[4:4 + self.T].view(torch.float32)
+class RouterLoss(NamedTuple):
+    """``loss`` fp32 [3]: the loss, the balance and the z loss without their coefficients;
+    ``counts`` int32 [S, E]: the experts' tokens by sequence. ``tokens`` int32 [S + 2] (by
+    sequence, sequences with any, all) and ``lse`` fp32 [T] are the backward's."""
+    loss: torch.Tensor
+    counts: torch.Tensor
+    tokens: torch.Tensor
+    lse: torch.Tensor
 
 
 def router_loss(c, logits, topk_idx, *, ws, offsets=None, mask=None, stream=None) -> RouterLoss:
     """The router's losses of logits [T, E] and choices [T, k]. ``offsets`` int32 [S + 1]: the
     sequences' tokens (None: one of all); ``mask`` [T], bool or uint8: the tokens that count."""
-    T, E, S = c.T, c.E, c.S
-    px = _shaped("logits", logits, (T, E), torch.float32)
-    pi = _shaped("topk_idx", topk_idx, (T, c.k), torch.int32)
-    po = None if offsets is None else _indices("offsets", offsets, S + 1)
-    pm = None if mask is None else _mask_p(mask, T)
-    r = RouterLoss(T, E, S, logits.device)
-    _check(L.load().moe_router_loss(ctypes.byref(c), px, pi, po, pm, *r.pointers(), _p(ws),
-                                    ws.nbytes, _s(stream)), "moe_router_loss")
+    T, E, k, S = c.T, c.E, c.k, c.S
+    i32, dev = torch.int32, logits.device
+    r = RouterLoss(torch.empty(3, dtype=torch.float32, device=dev),
+                   torch.empty((S, E), dtype=i32, device=dev),
+                   torch.empty(S + 2, dtype=i32, device=dev),
+                   torch.empty(T, dtype=torch.float32, device=dev))
+    st = L.load().moe_router_loss(
+        ctypes.byref(c), _shaped("logits", logits, (T, E), torch.float32),
+        _shaped("topk_idx", topk_idx, (T, k), i32),
+        None if offsets is None else _indices("offsets", offsets, S + 1),
+        None if mask is None else _mask_p(mask, T), r.loss.data_ptr(), r.counts.data_ptr(),
+        r.tokens.data_ptr(), r.lse.data_ptr(), _p(ws), ws.nbytes, _s(stream))
+    _check(st, "moe_router_loss")
     return r
 
 
@@ -821,19 +821,18 @@ def router_loss_backward(c, logits, kept, *, dloss=None, offsets=None, mask=None
     after a ``router_loss`` of the same inputs that gave ``kept``. What ``backward`` takes as
     ``dlogits``."""
     T, E, S, f32 = c.T, c.E, c.S, torch.float32
-    if (kept.T, kept.E, kept.S) != (T, E, S):
-        raise MoEError(L.MOE_ERR_INVALID_ARG, f"kept is of T, E, S = {kept.T}, {kept.E}, {kept.S}, "
-                                              f"not {T}, {E}, {S}")
     px = _shaped("logits", logits, (T, E), f32)
     if out is None:
         out = torch.empty_like(logits)
         pout = out.data_ptr()
     else:
         pout = _shaped("out", out, (T, E), f32)
-    _, counts, tokens, lse = kept.pointers()
     st = L.load().moe_router_loss_backward(
         ctypes.byref(c), px, None if offsets is None else _indices("offsets", offsets, S + 1),
-        None if mask is None else _mask_p(mask, T), counts, tokens, lse,
+        None if mask is None else _mask_p(mask, T),
+        _shaped("counts", kept.counts, (S, E), torch.int32),
+        _shaped("tokens", kept.tokens, (S + 2,), torch.int32),
+        _shaped("lse", kept.lse, (T,), f32),
         None if dloss is None else _shaped("dloss", dloss, (1,), f32), pout, _s(stream))
     _check(st, "moe_router_loss_backward")
     return out

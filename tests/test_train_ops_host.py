@@ -275,18 +275,21 @@ def test_binding_refuses_wrong_shapes_types_and_forms():
                                           act="relu"), "act")
     refused(lambda: moe.fp8_quantize_rows(c, torch.zeros((4, 128), dtype=bf), off, ws=ws,
                                           rows=False), "neither")
-    r = moe.Fp8Rows(torch.zeros((4, 128), dtype=u8), torch.zeros((4, 4), dtype=u8), None, None)
+    r = moe.Fp8Rows(4, 128, True, False, 0, "cpu")
     wq, wsc = torch.zeros((2, 128, 192), dtype=u8), torch.zeros((2, 1, 2), dtype=u8)
     refused(lambda: moe.fp8_product(c, r, wq, wsc, off, ws=ws, transposed=True))
     refused(lambda: moe.fp8_product(c, r, wq, wsc[:, :, :1], off, ws=ws))
     refused(lambda: moe.fp8_weight_grad(c, r, r, off, ws=ws), "form")
-    refused(lambda: moe.fp8_product(c, moe.Fp8Rows(None, None, None, None), wq, wsc, off, ws=ws),
-            "form")
+    refused(lambda: moe.fp8_product(c, moe.Fp8Rows(4, 128, False, True, 2, "cpu"), wq, wsc, off,
+                                    ws=ws), "form")
+    refused(lambda: moe.fp8_product(c, r, wq, wsc, off, ws=ws), "GPU memory")
+    refused(lambda: moe.fp8_dequantize_rows(moe.fp8_config(5, 128, 192, 2), r))
     c = moe.router_loss_config(4, 8, 2)
     idx = torch.zeros((4, 2), dtype=i32)
     refused(lambda: moe.router_loss(c, torch.zeros((4, 8), dtype=bf), idx, ws=ws))
     refused(lambda: moe.router_loss(c, torch.zeros((4, 8)), idx.long(), ws=ws))
-    kept = moe.RouterLoss(4, 8, 2, "cpu")
+    kept = moe.RouterLoss(torch.zeros(3), torch.zeros((2, 8), dtype=i32),
+                          torch.zeros(4, dtype=i32), torch.zeros(4))
     refused(lambda: moe.router_loss_backward(c, torch.zeros((4, 8)), kept))
     c = moe.dropout_config(4, 64)
     x = torch.zeros((4, 64), dtype=bf)
