@@ -43,6 +43,9 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
 // A thread takes kGroups groups of 8 elements, 256 groups apart; their loads
 // are under way while the draws are computed. A product and a select for
 // each element, the sum in one rounding with the product (fma).
+// Bound by HBM: 16384 x 5120 bf16 with a residual 72.5 us, 6.9 TB/s, without
+// 50.5, 6.6 TB/s (16 bits an element: a generator call for 8 of them, some 70
+// instructions, a third of what the SMs issue meanwhile).
 constexpr int kThreads = 256, kGroups = 2;
 
 template <typename T, bool RES>
