@@ -549,7 +549,7 @@ MOE_API int moe_mx4_dequantize_rows(const moe_mx4_config_t* cfg, const uint8_t* 
  * of each W[e]; codes [E, K, N] as W lies, scales [E, ceil(K / 128),
  * ceil(N / 128)]: the one copy serves the product and its transpose. C is K
  * (rows of x) or N (rows of dy). Code pointers are 16-byte aligned, the
- * scales of rows and columns 4-byte. */
+ * scales of rows and columns, src, row_weight and offsets 4-byte. */
 typedef struct moe_fp8_config {
   int32_t R;         /* routed rows, 0..2^24 */
   int32_t K;         /* W's rows (the product's contraction), multiple of 64, at most 65536 */

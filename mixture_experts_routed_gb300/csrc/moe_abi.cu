@@ -18,6 +18,7 @@ namespace {
 constexpr size_t kAlign = 256;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool words(const void* p) { return aligned(p, 4); }  // (null too)
 
 int check_cfg(const moe_config_t* c) {
   if (c == nullptr) return MOE_ERR_INVALID_ARG;
@@ -597,7 +598,6 @@ int check_router_loss(const moe_router_loss_config_t* c) {
   if (c->T > 1 << 26 || c->S > 1 << 20) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
-bool words(const void* p) { return aligned(p, 4); }  // (null too)
 
 // ---------------------------------------------------------------- dropout
 int check_dropout(const moe_dropout_config_t* c) {
@@ -1090,7 +1090,8 @@ int moe_fp8_quantize_rows(const moe_fp8_config_t* cfg, int32_t cols, const void*
   if (!fp8_cols_ok(c, cols) || act < MOE_ACT_NONE || act > MOE_ACT_SILU_GRAD)
     return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
-  if ((q == nullptr) != (scale == nullptr) || (cq == nullptr) != (cscale == nullptr))
+  if ((q == nullptr) != (scale == nullptr) || (cq == nullptr) != (cscale == nullptr) ||
+      !words(src) || !words(row_weight) || !words(offsets))
     return MOE_ERR_INVALID_ARG;
   if (c.R > 0 && (!ok_ptr(x) || offsets == nullptr || (q == nullptr && cq == nullptr) ||
                   (q != nullptr && (!ok_ptr(q) || !aligned(scale, 4))) ||
@@ -1123,7 +1124,7 @@ int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8
   if (transposed && c.silu) return MOE_ERR_UNSUPPORTED;
   if (ws == nullptr || !aligned(ws, kAlign)) return MOE_ERR_INVALID_ARG;
   if (c.R > 0 && (!ok_ptr(q) || scale == nullptr || !aligned(scale, 4) || !ok_ptr(wq) ||
-                  w_scale == nullptr || offsets == nullptr || !ok_ptr(out)))
+                  w_scale == nullptr || offsets == nullptr || !words(offsets) || !ok_ptr(out)))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_fp8_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   if (c.R == 0) return MOE_OK;
@@ -1149,7 +1150,8 @@ int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const ui
   const moe_fp8_config_t& c = *cfg;
   if (ws == nullptr || !aligned(ws, kAlign) || !ok_ptr(dW)) return MOE_ERR_INVALID_ARG;
   if (c.R > 0 && (!ok_ptr(xq) || x_scale == nullptr || !aligned(x_scale, 4) || !ok_ptr(dyq) ||
-                  dy_scale == nullptr || !aligned(dy_scale, 4) || offsets == nullptr))
+                  dy_scale == nullptr || !aligned(dy_scale, 4) || offsets == nullptr ||
+                  !words(offsets)))
     return MOE_ERR_INVALID_ARG;
   if (ws_bytes < moe_fp8_workspace_size(cfg)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   const size_t n = static_cast<size_t>(c.E) * c.K * c.N * 4;

@@ -360,6 +360,15 @@ def test_long_contractions(cuda_ok):
         check_grad(p, run_grad(p))
 
 
+def test_the_largest_contractions_and_widths(cuda_ok):
+    for counts, K, N in (([3], 65536, 64), ([130, 2], 65536, 64), ([500], 64, 65536),
+                         ([1, 2], 64, 65536)):
+        p = problem(counts, K, N, "bf16", seed=K)
+        check_products(p, False, run_product(p, False))
+        check_products(p, True, run_product(p, True))
+        check_grad(p, run_grad(p))
+
+
 @pytest.mark.parametrize("counts", [[2, 0, 3], [150, 40, 300]])
 def test_rows_of_no_segment(cuda_ok, counts):
     # before the first and behind the last: not quantised, not written, no part of any sum

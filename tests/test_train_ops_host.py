@@ -102,7 +102,8 @@ def test_fp8_configs(lib, kw, status):
     (rows, dict(q=ODD)), (rows, dict(scale=ODD)), (rows, dict(cq=None)), (rows, dict(cq=ODD)),
     (rows, dict(cscale=ODD)), (rows, dict(q=None, scale=None, cq=None, cscale=None)),
     (rows, dict(ws=None)), (rows, dict(ws=ODD)), (rows, dict(q=at(0))), (rows, dict(cq=at(2))),
-    (rows, dict(weight=at(3))),
+    (rows, dict(weight=at(3))), (rows, dict(weight=ODD)), (rows, dict(src=ODD)),
+    (rows, dict(offsets=ODD)), (product, dict(offsets=ODD)), (grad, dict(offsets=ODD)),
     (weights, dict(W=None)), (weights, dict(W=ODD)), (weights, dict(q=None)),
     (weights, dict(q=ODD)), (weights, dict(scale=None)), (weights, dict(q=at(0))),
     (product, dict(transposed=2)), (product, dict(q=None)), (product, dict(q=ODD)),
