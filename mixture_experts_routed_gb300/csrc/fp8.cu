@@ -705,35 +705,35 @@ __global__ void __launch_bounds__(kColThreads)
 // us a stage: 8192 x 8192 x 8192 in 1131 us). One thread copies the chunks to
 // tensor memory (tcgen05.cp, in line with the products: a copy every stage
 // took 323, 362 and 423 us for Y, dX and dW of 8192 cubed, 319, 355 and 376
-// since) and issues the products of 128 columns x 32 steps (kind::mxf8f6f4)
-// that read them. A pair's product takes 64 columns of
-// each CTA's 128, so its two accumulators hold columns 0..63 with 128..191, and
-// 64..127 with 192..255. Three accumulators of 128 columns: a tile takes two,
-// and the next tile starts once one of them is drained, with the first half's
-// products of its first stages. Eight warps drain: into registers, which
+// since) and issues the products of all the columns x 32 steps
+// (kind::mxf8f6f4) that read them. Three accumulators of 128 columns: tiles
+// take the first two and the last two in turn, and the next tile starts once
+// the middle one is drained, which is drained first. (Products of half the
+// columns, a tile on any two accumulators and the next on the third, read the
+// rows' side twice: 1 to 4 % slower.) Eight warps drain: into registers, which
 // frees the accumulator, and then to out.
 //
-// Bound: a pair's stage is 64 KB, 32 KB into each SM, which takes what its eight
-// products take, 512 clocks (64 bytes a clock; 256 x 128 x 32 in 64 clocks), and
-// neither hides the other whole. 8192 x 8192 x 8192 to bf16 305 us, 3.6 PFLOP/s;
-// dX 345 (both sides k-major), dW to fp32 366. With a quarter of the products
-// 267, 232 and 263. After seconds of it the power cap leaves 1350 MHz and 2.9
-// PFLOP/s. 16384 skewed rows of 32 experts, 7168 x 2048: 178 us for 481 GFLOP,
-// 9 rounds of tiles of which 6.7 are rows that exist (rows as the products'
-// columns, 32 at a time, did away with the others: 184 us, for the loads
-// stay). Copies to L2 ahead of the ring: 305 -> 354 us. dW of 16 x 5120 x 1536
-// from 16384 rows 123 us, 4.1 TB/s written beside its loads; of 64 x 1408 x
-// 2048 from 8191 rows 139 us, 5.3 TB/s. Two rows of 8 experts of 4096 x 11008:
-// 22 us, 7 TB/s and 9 us of start and join.
+// Bound, of many rows: power. 8192 x 8192 x 8192 in short runs 318, 320 and 334
+// us for Y, dX and dW (3.4 PFLOP/s), with operands of zeros or ones 276, 269 and
+// 291; after seconds the cap leaves 1350 MHz and 2.9 PFLOP/s. Behind it a pair's
+// stage: 32 KB into each SM, which at 64 bytes a clock take what its four
+// products take, 512 clocks (with a quarter of the products 267, 232 and 263
+// us). Copies to L2 ahead of the ring: Y 305 -> 354 us. 16384 skewed rows of 32
+// experts, 7168 x 2048: 181 us for 481 GFLOP, nine rounds of tiles of which 6.7
+// are rows that exist (rows as the products' columns, 32 at a time, did away
+// with the others: 184 us, for the loads stay). dW of 16 x 5120 x 1536 from
+// 16384 rows 123 us, 4.1 TB/s written beside its loads; of 64 x 1408 x 2048 from
+// 8191 rows 135 us, 5.5 TB/s. Two rows of 8 experts of 4096 x 11008: 22 us, 7
+// TB/s and 9 us of start and join.
 namespace f8 {
 using namespace ptx;
-constexpr int HN = 128, KS = 128;  // an accumulator's columns, a stage's steps
+constexpr int HN = 128, KS = 128;  // half a tile's columns, a stage's steps
 constexpr int BOX = 128 * 128, CHUNK = 512;
 // tensor memory columns: 3 x 128, then scales. A slot of scales is written
 // again SLOTS uses later, of a stage or more each, so after products that a
 // ring of fewer stages has seen the end of.
 constexpr int SF_COL = 384, SF_SLOT = 12, SLOTS = 10;
-constexpr int TMEM_COLS = 512, ACCS = 3;
+constexpr int TMEM_COLS = 512;
 constexpr int EPI_THREADS = 256, THREADS = 128 + EPI_THREADS;
 
 template <bool PAIR>
@@ -744,7 +744,7 @@ struct Cfg {
   static constexpr int STAGE = (OFF_SFB + 2 * CHUNK + 1023) / 1024 * 1024;
   static constexpr int STAGES = PAIR ? 6 : 4;  // (shared memory's most)
   static constexpr int OFF_BAR = STAGES * STAGE;
-  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 2 * ACCS + 1) * 8 + 24;
+  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 6) * 8 + 24;
   static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(SF_COL + SLOTS * SF_SLOT <= TMEM_COLS && SLOTS > STAGES, "tensor memory");
@@ -864,9 +864,9 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);  // pair: the even CTA's
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;
-  uint64_t* tempty = tfull + ACCS;  // pair: the even CTA's
-  uint64_t* drain = tempty + ACCS;
+  uint64_t* tfull = empty + STAGES;  // by a tile's parity
+  uint64_t* tfree = tfull + 2;       // accumulators 0, 1 and 2; pair: the even CTA's
+  uint64_t* drain = tfree + 3;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   int* s_ok = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* s_last = tmem_slot + 2;
@@ -885,10 +885,8 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < ACCS; ++i) {
-      mbar_init(&tfull[i], 1);
-      mbar_init(&tempty[i], PAIR ? 16 : 8);
-    }
+    for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1);
+    for (int i = 0; i < 3; ++i) mbar_init(&tfree[i], PAIR ? 16 : 8);
     mbar_init(drain, 1);
     *s_wide = 0;
     fence_mbar_init();
@@ -1115,19 +1113,13 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
               a = turn(cur.w);
               b0 = turn(cur.w + 4);
               b1 = turn(cur.w + 8);
-              if constexpr (PAIR) {
-                const uint4 c0 = b0, c1 = b1;
-                b0 = make_uint4(c0.x, c0.y, c1.x, c1.y);
-                b1 = make_uint4(c0.z, c0.w, c1.z, c1.w);
-              }
             } else {
               a = make_uint4(cur.w[0], cur.w[1], cur.w[2], cur.w[3]);
               uint32_t s[2] = {0, 0};
 #pragma unroll
               for (int i = 0; i < 8; ++i)
                 s[i & 1] |= __shfl_sync(0xffffffffu, cur.w[4], i) << (i >> 1) * 8;
-              // (a pair's accumulators have the same two blocks of columns)
-              b0 = PAIR ? make_uint4(s[0], s[0], s[1], s[1]) : make_uint4(s[0], s[0], s[0], s[0]);
+              b0 = make_uint4(s[0], s[0], s[0], s[0]);
               b1 = make_uint4(s[1], s[1], s[1], s[1]);
             }
           }
@@ -1136,7 +1128,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
             const uint32_t sf = base0 + s * C::STAGE + C::OFF_SFA + lane * 16;
             st_shared(sf, a);
             st_shared(sf + CHUNK, b0);
-            if constexpr (MODE == 2 || !PAIR) st_shared(sf + 2 * CHUNK, b1);
+            st_shared(sf + 2 * CHUNK, b1);
             fence_proxy_async_shared();
             __syncwarp();
           }
@@ -1163,123 +1155,69 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   } else if (warp == 1) {
     // (one lane issues: elect_one says how)
     if (rank == 0) {
-      int s = 0, acc = 0;
-      uint32_t ph = 0, aph = 0;
+      int s = 0;
+      uint32_t ph = 0, tiles_done = 0;
       bool dead = false;
       constexpr bool A_STEPS = MODE == 2, B_STEPS = MODE != 1;
-      constexpr uint32_t id = idesc(BM, HN, A_STEPS, B_STEPS);
+      constexpr uint32_t id_all = idesc(BM, kTileCols, A_STEPS, B_STEPS),
+                         id_half = idesc(BM, HN, A_STEPS, B_STEPS);
       // 32 steps on: 32 rows of 128 bytes, or 32 bytes of a row
       constexpr uint32_t A_ON = A_STEPS ? 4096 >> 4 : 32 >> 4, B_ON = B_STEPS ? 4096 >> 4 : 32 >> 4;
-      // the other 128 (pair: 64) columns
-      constexpr uint32_t B_HALF = !PAIR ? BOX >> 4 : B_STEPS ? 64 >> 4 : (64 * 128) >> 4;
       const uint32_t base0 = smem_u32(smem);
       const uint32_t ad0 = desc_lo(base0), bd0 = desc_lo(base0 + C::OFF_B),
                      sa0 = sf_lo(base0 + C::OFF_SFA);
-      auto take = [&] {
-        const bool there = mbar_wait_spin(&full[s], ph, kWaitLimitNs);
-        if (there) tc_fence_after();
-        return there;
-      };
-      auto next = [&] {
-        if (++s == STAGES) {
-          s = 0;
-          ph ^= 1u;
-        }
-      };
-      // the next slot for scales, with four stages' where stage kb brings them
       int slot = SLOTS - 1;
-      constexpr int B_CHUNKS = MODE == 2 || !PAIR ? 2 : 1;
-      auto on = [&](int kb, int k0) {
-        const bool four = kb == k0 || (kb & 3) == 0;
-        if (four && ++slot == SLOTS) slot = 0;
-        return four;
-      };
-      auto scales = [&] {
-        const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
-        const uint32_t sf = tmem_base + SF_COL + slot * SF_SLOT;
-#pragma unroll
-        for (int c = 0; c <= B_CHUNKS; ++c) cp_scales<PAIR>(sf + c * 4, sa0 + off + c * (CHUNK / 16));
-      };
-      // a stage's products for the halves j0..j1 of the columns (inlined with
-      // constants for whole stages)
-      auto products = [&](int kb, int steps, int j0, int j1, uint32_t d0, uint32_t d1,
-                          uint32_t more) {
+      // a stage's products of `steps` x 32 (inlined with a constant for whole ones)
+      auto products = [&](int kb, int steps, uint32_t id, uint32_t d, uint32_t more) {
         const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
         const uint32_t sf = tmem_base + SF_COL + slot * SF_SLOT;
         const uint32_t idk = id | sf_byte(kb & 3);
 #pragma unroll
         for (int kk = 0; kk < steps; ++kk)
-#pragma unroll
-          for (int j = j0; j < j1; ++j)
-            mma<PAIR>(j == 0 ? d0 : d1, ad0 + off + kk * A_ON, bd0 + off + j * B_HALF + kk * B_ON,
-                      idk, sf, sf + 4 + (B_CHUNKS > 1 ? j * 4 : 0), kk > 0 ? 1u : more);
+          mma<PAIR>(d, ad0 + off + kk * A_ON, bd0 + off + kk * B_ON, idk, sf, sf + 4,
+                    kk > 0 ? 1u : more);
       };
       if (elect_one()) walk([&](int t, int k0, int k1) {
         if (k0 == k1) return true;
-        const int n = tile(t).n;
-        const int nj = n > (PAIR ? 64 : HN) ? 2 : 1;
-        const int acc1 = acc + 1 == ACCS ? 0 : acc + 1;
-        const uint32_t aph1 = acc + 1 == ACCS ? aph ^ 1u : aph;
-        if (!mbar_wait_spin_cluster(&tempty[acc], aph ^ 1u, kWaitLimitNs)) {
+        // the middle accumulator, free of the tile before, and this tile's
+        // other one, free of the tile before that
+        const uint32_t odd = tiles_done & 1, use = tiles_done >> 1 & 1;
+        ++tiles_done;
+        if (!mbar_wait_spin_cluster(&tfree[odd * 2], use ^ 1u, kWaitLimitNs) ||
+            !mbar_wait_spin_cluster(&tfree[1], odd ^ 1u, kWaitLimitNs)) {
           dead = true;
           return false;
         }
         tc_fence_after();
-        const uint32_t d0 = tmem_base + acc * HN, d1 = tmem_base + acc1 * HN;
-        // stages with nothing left out
-        const int whole = nj == 2 ? (MODE == 2 ? k1 : len / KS) : 0;
-        int kb = k0;
-        if (nj == 2) {
-          // until the second accumulator is drained too: the first half's
-          // products of a few stages, and after that the second's
-          const int s0 = s, slot0 = slot, most = min(min(k1, whole), k0 + STAGES - 1);
-          const uint32_t ph0 = ph;
-          while (kb < most && !mbar_test_wait_cluster(&tempty[acc1], aph1 ^ 1u)) {
-            if (!take()) {
-              dead = true;
-              return false;
-            }
-            if (on(kb, k0)) scales();
-            products(kb, 4, 0, 1, d0, d1, kb > k0 ? 1u : 0u);
-            next();
-            ++kb;
-          }
-          if (!mbar_wait_spin_cluster(&tempty[acc1], aph1 ^ 1u, kWaitLimitNs)) {
-            dead = true;
-            return false;
-          }
-          tc_fence_after();
-          s = s0;
-          ph = ph0;
-          slot = slot0;
-          for (int i = k0; i < kb; ++i) {
-            on(i, k0);
-            products(i, 4, 1, 2, d0, d1, i > k0 ? 1u : 0u);
-            commit<PAIR>(&empty[s]);
-            next();
-          }
-        }
-        for (; kb < k1; ++kb) {
-          if (!take()) {
+        const uint32_t d = tmem_base + odd * HN;
+        const uint32_t id = !PAIR && tile(t).n <= HN ? id_half : id_all;
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!mbar_wait_spin(&full[s], ph, kWaitLimitNs)) {
             dead = true;
             break;
           }
+          tc_fence_after();
+          if (kb == k0 || (kb & 3) == 0) {
+            // four stages' scales, to the next slot
+            if (++slot == SLOTS) slot = 0;
+            const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              cp_scales<PAIR>(tmem_base + SF_COL + slot * SF_SLOT + c * 4,
+                              sa0 + off + c * (CHUNK / 16));
+          }
           const uint32_t more = kb > k0 ? 1u : 0u;
-          if (on(kb, k0)) scales();
-          if (kb < whole)
-            products(kb, 4, 0, 2, d0, d1, more);
+          if (MODE == 2 || kb < len / KS)
+            products(kb, 4, id, d, more);
           else
-            products(kb, MODE == 2 ? 4 : min(4, (len - kb * KS) / 32), 0, nj, d0, d1, more);
+            products(kb, (len - kb * KS) / 32, id, d, more);
           commit<PAIR>(&empty[s]);
-          next();
-        }
-        for (int j = 0; j < nj; ++j) {
-          commit<PAIR>(&tfull[acc]);
-          if (++acc == ACCS) {
-            acc = 0;
-            aph ^= 1u;
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
           }
         }
+        commit<PAIR>(&tfull[odd]);
         return !dead;
       });
       dead = __any_sync(0xffffffffu, dead);
@@ -1295,11 +1233,10 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   } else if (warp >= 4) {
     // two warps to a quarter of the rows, 64 of an accumulator's columns each
     const int w = warp & 3, half = (warp - 4) >> 2;
-    int acc = 0;
-    uint32_t aph = 0;
+    uint32_t tiles_done = 0;
     bool dead = false;
     TO* out = static_cast<TO*>(p.out);
-    const uint32_t leader_tempty = PAIR ? mapa_shared(smem_u32(tempty), 0) : 0;
+    const uint32_t leader_tfree = PAIR ? mapa_shared(smem_u32(tfree), 0) : 0;
     auto finish = [&](float v) { return MODE == 0 && p.silu ? silu_of<TO>(v) : v; };
     const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
     walk([&](int t, int k0, int k1) {
@@ -1314,47 +1251,50 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       auto slice = [&](int c) {
         return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * kTileCols;
       };
-      const int nj = tl.n > (PAIR ? 64 : HN) ? 2 : 1;
-      for (int j = 0; j < nj; ++j) {
-        const int col = PAIR ? half * 128 + j * 64 : j * 128 + half * 64;
+      if (MODE == 2 && k0 == k1) {
+        // an expert without rows
+        for (int i = lane; i < rows * 32; i += 32) {
+          const int col = (i >> 4 & 1) * HN + half * 64 + (i & 15) * 4;
+          if (col < tl.n)
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out) +
+                                       (out_row + (i >> 5)) * width + tl.n0 + col) =
+                float4{0.f, 0.f, 0.f, 0.f};
+        }
+        return true;
+      }
+      const uint32_t odd = tiles_done & 1;
+      // after a wait that ran out the loops go on, so that the eight warps
+      // still meet at every barrier
+      if (!dead && !mbar_wait(&tfull[odd], tiles_done >> 1 & 1, kWaitLimitNs)) dead = true;
+      dead = __any_sync(0xffffffffu, dead);
+      tc_fence_after();
+      ++tiles_done;
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        // the middle accumulator first: an even tile's second half
+        const int j = i ^ static_cast<int>(odd) ^ 1;
+        const int col = j * HN + half * 64;
         const bool some = rows > 0 && col < tl.n;
         uint32_t r[2][32];
-        if (MODE == 2 && k0 == k1) {
-          // an expert without rows
+        if (some) {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 32; ++c) r[i][c] = 0;
-        } else {
-          // after a wait that ran out the loops go on, so that the eight warps
-          // still meet at every barrier
-          if (!dead && !mbar_wait(&tfull[acc], aph, kWaitLimitNs)) dead = true;
-          dead = __any_sync(0xffffffffu, dead);
-          tc_fence_after();
-          if (some) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-              tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(w * 32) << 16) + acc * HN +
-                                     half * 64 + i * 32,
-                                 r[i]);
-            tmem_ld_wait();
-          }
-          // free before the stores: the next tile waits for this one's first
-          // half. (What was read is in registers, so there is nothing to
-          // release: as a release at cluster scope the two arrivals took a
-          // third of a weight gradient's time, 200 us where it now takes 139.)
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              mbar_arrive_remote_relaxed(leader_tempty + acc * 8);
-            else
-              mbar_arrive(&tempty[acc]);
-          }
-          if (++acc == ACCS) {
-            acc = 0;
-            aph ^= 1u;
-          }
+            tmem_ld_32x32b_x32(tmem_base + (static_cast<uint32_t>(w * 32) << 16) + (odd + j) * HN +
+                                   half * 64 + i * 32,
+                               r[i]);
+          tmem_ld_wait();
+        }
+        // free before the stores: the next tile waits for the middle one.
+        // (What was read is in registers, so there is nothing to release: as
+        // releases at cluster scope the two arrivals took a third of a weight
+        // gradient's time, 200 us where it then took 139.)
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            mbar_arrive_remote_relaxed(leader_tfree + (odd + j) * 8);
+          else
+            mbar_arrive(&tfree[odd + j]);
         }
         if (some && whole) {
 #pragma unroll
