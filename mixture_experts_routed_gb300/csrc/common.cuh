@@ -304,13 +304,14 @@ cudaError_t launch_few(const void* x, const void* Wg, const float* bias, const v
                        const void* W2, int T, int d, int E, int f, RouterSpec rs, void* out,
                        void* ws, int num_sms, cudaStream_t s);
 
+// ---------------------------------------------------------------- mx4.cu and fp8.cu
+constexpr int kProductCtas = 160;  // the grid the products' split sums are sized for
+constexpr int kSplitRows = 32;     // a split launch's rows per expert, at most
 // Row tiles (128 rows of one expert) that R rows of E experts can make.
 inline size_t row_tiles(int R, int E) { return static_cast<size_t>(R / 128) + (R < E ? R : E); }
 
 // ---------------------------------------------------------------- mx4.cu
 // Microscaled 4-bit rows and expert weights, and their grouped product.
-constexpr int kMx4MaxCtas = 160;    // the grid the product's partial sums are sized for
-constexpr int kMx4SplitRows = 32;   // a split launch's rows per expert, at most
 // Rows per expert, on average, from which pairs of CTAs work, in tiles of 256
 // rows (one CTA: 128). One CTA and pairs at 128 rows each: 25.9 and 34.8 us (64
 // experts of 2048 x 1408), 40.6 and 44.6 (8 of 4096 x 11008); skewed, 16 of
@@ -326,8 +327,8 @@ cudaError_t launch_mx4_weights(int dtype, const void* W, int E, int K, int N, ui
                                uint8_t* sc, cudaStream_t s);
 cudaError_t launch_mx4_weights_back(int dtype, const uint8_t* q, const uint8_t* sc, int E, int K,
                                     int N, void* W, cudaStream_t s);
-// `ctr`: kMx4MaxCtas words, zero between launches; `part`: [kMx4MaxCtas][2]
-// [kMx4SplitRows][256] fp32.
+// `ctr`: kProductCtas words, zero between launches; `part`: [kProductCtas][2]
+// [kSplitRows][256] fp32.
 cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8_t* wq,
                                const uint8_t* wsc, const int32_t* offsets, int E, int R, int K,
                                int N, int out_f32, int silu, void* out, uint32_t* err,

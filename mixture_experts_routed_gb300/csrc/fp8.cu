@@ -756,7 +756,7 @@ struct Params {
   void* out;
   uint32_t* err;
   uint32_t* ctr;  // arrivals per tile of a split launch, zero between launches
-  float* part;    // [CTA][2][kMx4SplitRows][256]
+  float* part;    // [CTA][2][kSplitRows][256]
   int E, R, K, N;
   int silu;
 };
@@ -904,7 +904,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   pdl_trigger();
   const bool ok = load_segments(p.offsets, E, p.R, seg, base, s_ok, p.err);
   for (int e = tid; ok && e < E; e += THREADS)
-    if (seg[e + 1] - seg[e] > kMx4SplitRows) *s_wide = 1;
+    if (seg[e + 1] - seg[e] > kSplitRows) *s_wide = 1;
   if (MODE != 2 && PAIR && warp == 0) {
     // tiles of 256 rows before each expert
     int run = 0;
@@ -1249,7 +1249,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       // a CTA's part of the tile its range starts in comes first, of the one
       // it ends in second
       auto slice = [&](int c) {
-        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * kTileCols;
+        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kSplitRows * kTileCols;
       };
       if (MODE == 2 && k0 == k1) {
         // an expert without rows
@@ -1301,7 +1301,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           for (int i = 0; i < 2; ++i)
             put_rows32(out, sectors, out_row, rows, width, tl.n0 + col + i * 32, r[i], finish);
         } else if (some && lane < rows) {
-          // (at most kMx4SplitRows rows: the first quarter's)
+          // (at most kSplitRows rows: the first quarter's)
           uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * kTileCols + col);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -1504,7 +1504,7 @@ cudaError_t launch_fp8_product(int mode, const uint8_t* a, const uint8_t* as, co
     return cudaErrorInvalidValue;
   if (mode == 2) mA32 = mA;
   const f8::Params p{as, bs, offsets, out, err, ctr, part, E, R, K, N, silu};
-  const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
+  const int grid = num_sms < kProductCtas ? num_sms : kProductCtas;
   if (mode == 2) return launch_product<2, true, float>(mA, mA32, mB, p, grid, s);
   const bool pair = R >= kPairRows * E;
   auto go = [&](auto kernel) { return kernel(mA, mA32, mB, p, grid, s); };

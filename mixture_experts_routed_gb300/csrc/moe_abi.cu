@@ -566,10 +566,11 @@ int check_mx4(const moe_mx4_config_t* c) {
   return MOE_OK;
 }
 
-// The workspace: the error word, the product's tile arrivals, its split sums.
-constexpr size_t kMx4CtrOffset = kAlign;
-constexpr size_t kMx4PartOffset = kMx4CtrOffset + 1024;
-static_assert(kMx4MaxCtas * sizeof(uint32_t) <= 1024, "arrivals");
+// The 4- and 8-bit products' workspace: the error word, tile arrivals, split
+// sums.
+constexpr size_t kProductCtrOffset = kAlign;
+constexpr size_t kProductPartOffset = kProductCtrOffset + 1024;
+static_assert(kProductCtas * sizeof(uint32_t) <= 1024, "arrivals");
 
 size_t mx4_row_scales(const moe_mx4_config_t& c) {
   return row_tiles(c.R, c.E) * ceil_div(c.K, 128) * 512;
@@ -890,7 +891,7 @@ size_t moe_mx4_weight_scale_size(const moe_mx4_config_t* cfg) {
 
 size_t moe_mx4_workspace_size(const moe_mx4_config_t* cfg) {
   if (check_mx4(cfg) != MOE_OK) return 0;
-  return kMx4PartOffset + static_cast<size_t>(kMx4MaxCtas) * 2 * kMx4SplitRows * 256 * 4;
+  return kProductPartOffset + static_cast<size_t>(kProductCtas) * 2 * kSplitRows * 256 * 4;
 }
 
 int moe_mx4_quantize_weights(const moe_mx4_config_t* cfg, const void* W, uint8_t* wq,
@@ -936,8 +937,8 @@ int moe_mx4_product(const moe_mx4_config_t* cfg, const uint8_t* q, const uint8_t
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_mx4_product(q, scale, wq, w_scale, offsets, c.E, c.R, c.K, c.N,
                                       c.out_dtype == MOE_DTYPE_F32 ? 1 : 0, c.silu, out,
-                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kMx4CtrOffset),
-                                      at<float>(ws, kMx4PartOffset), sms, as_stream(stream)));
+                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kProductCtrOffset),
+                                      at<float>(ws, kProductPartOffset), sms, as_stream(stream)));
 }
 
 int moe_mx4_dequantize_weights(const moe_mx4_config_t* cfg, const uint8_t* wq,
@@ -1065,7 +1066,7 @@ size_t moe_fp8_weight_scale_size(const moe_fp8_config_t* cfg) {
 
 size_t moe_fp8_workspace_size(const moe_fp8_config_t* cfg) {
   if (check_fp8(cfg) != MOE_OK) return 0;
-  return kMx4PartOffset + static_cast<size_t>(kMx4MaxCtas) * 2 * kMx4SplitRows * 256 * 4;
+  return kProductPartOffset + static_cast<size_t>(kProductCtas) * 2 * kSplitRows * 256 * 4;
 }
 
 int moe_fp8_quantize_weights(const moe_fp8_config_t* cfg, const void* W, uint8_t* wq,
@@ -1138,8 +1139,8 @@ int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_fp8_product(transposed, q, scale, wq, w_scale, offsets, c.E, c.R, c.K,
                                       c.N, c.out_dtype == MOE_DTYPE_F32 ? 1 : 0, c.silu, out,
-                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kMx4CtrOffset),
-                                      at<float>(ws, kMx4PartOffset), sms, as_stream(stream)));
+                                      static_cast<uint32_t*>(ws), at<uint32_t>(ws, kProductCtrOffset),
+                                      at<float>(ws, kProductPartOffset), sms, as_stream(stream)));
 }
 
 int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const uint8_t* x_scale,
@@ -1166,7 +1167,7 @@ int moe_fp8_weight_grad(const moe_fp8_config_t* cfg, const uint8_t* xq, const ui
   if (sms <= 0) return MOE_ERR_LAUNCH;
   return status_of(launch_fp8_product(2, xq, x_scale, dyq, dy_scale, offsets, c.E, c.R, c.K, c.N,
                                       1, 0, dW, static_cast<uint32_t*>(ws),
-                                      at<uint32_t>(ws, kMx4CtrOffset), at<float>(ws, kMx4PartOffset),
+                                      at<uint32_t>(ws, kProductCtrOffset), at<float>(ws, kProductPartOffset),
                                       sms, as_stream(stream)));
 }
 

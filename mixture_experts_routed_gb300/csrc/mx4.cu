@@ -396,7 +396,7 @@ struct Params {
   void* out;
   uint32_t* err;
   uint32_t* ctr;  // arrivals per tile of a split launch, zero between launches
-  float* part;    // [CTA][2][kMx4SplitRows][256]
+  float* part;    // [CTA][2][kSplitRows][256]
   int E, R, K, N;
   int silu;
 };
@@ -522,7 +522,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
   pdl_trigger();
   const bool ok = load_segments(p.offsets, E, p.R, seg, base, s_ok, p.err);
   for (int e = tid; ok && e < E; e += THREADS)
-    if (seg[e + 1] - seg[e] > kMx4SplitRows) *s_wide = 1;
+    if (seg[e + 1] - seg[e] > kSplitRows) *s_wide = 1;
   if (PAIR && warp == 0) {
     // tiles of 256 rows before each expert
     int run = 0;
@@ -818,7 +818,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
       // a CTA's part of the tile its range starts in comes first, of the one
       // it ends in second
       auto slice = [&](int c) {
-        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kMx4SplitRows * BN;
+        return p.part + static_cast<size_t>(c * 2 + (c > first ? 0 : 1)) * kSplitRows * BN;
       };
       for (int h = 0; h < tl.n; h += HN) {
         // after a wait that ran out the loops go on, so that the eight warps
@@ -851,7 +851,7 @@ __global__ void __launch_bounds__(mx::THREADS, 1)
           for (int i = 0; i < 2; ++i)
             put32(static_cast<size_t>(tl.row0 + r0), rows, tl.n0 + col + i * 32, r[i]);
         } else if (some && lane < rows) {
-          // (at most kMx4SplitRows rows: the first quarter's)
+          // (at most kSplitRows rows: the first quarter's)
           uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * BN + col);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -1007,7 +1007,7 @@ cudaError_t launch_mx4_product(const uint8_t* aq, const uint8_t* as, const uint8
       !make_map_3d_chunks(&mSB, wsc, static_cast<uint64_t>(E) * up_div(N, 128), kc, 2))
     return cudaErrorInvalidValue;
   const mx::Params p{offsets, out, err, ctr, part, E, R, K, N, silu};
-  const int grid = num_sms < kMx4MaxCtas ? num_sms : kMx4MaxCtas;
+  const int grid = num_sms < kProductCtas ? num_sms : kProductCtas;
   const bool pair = R >= kMx4PairRows * E;
   if (pair)
     return out_f32 ? launch_product<true, float>(mA, mA32, mB, mSA, mSB, p, grid, s)
