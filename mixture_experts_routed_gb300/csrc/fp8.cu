@@ -1370,9 +1370,12 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
 }
 
 // Rows per expert, on average, from which pairs of CTAs work on Y and dX (dW:
-// always). One CTA and pairs at 384 rows each: 68 and 81 us (64 experts of 2048
-// x 1408), 106 and 126 (8 of 4096 x 11008), 76 and 83 (16 of 7168 x 2048); at 512:
-// 90 and 86, 143 and 130, and 193 and 168 (32 of 7168 x 2048).
+// always). One CTA and pairs, Y, us: at 128 rows each 40 and 46 (64 experts of
+// 2048 x 1408), 67 and 71 (8 of 4096 x 11008), 79 and 95 (32 of 7168 x 2048); at
+// 448 85 and 78, 146 and 125, 178 and 161; skewed 84 and 83, 147 and 132, 176 and
+// 172. Between, tiles of 256 rows decide: at 256 each 55 and 50, 83 and 75, 110
+// and 105; at 384 67 and 74, 105 and 120, 147 and 147; skewed at 320 69 and 69,
+// 111 and 107, 139 and 163.
 constexpr int kPairRows = 448;
 
 template <int MODE, bool PAIR, typename TO>
