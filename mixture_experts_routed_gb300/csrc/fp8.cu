@@ -157,9 +157,11 @@ __device__ __forceinline__ uint32_t inv_pair(uint32_t lo, uint32_t hi) {
 // amax. The groups of all rows are shared out evenly, each warp's one after
 // the other, and a group is loaded while the one before it is quantised.
 // Bound by HBM: the row is read once, a byte a value written. 16384 rows of
-// 7168 bf16 values: 61 us, 5.8 TB/s; 2047 rows of 2048 of 64 experts 3.9 us (by
-// tiles of one expert's rows, as below, 97 and 12 us).
-constexpr int kRowBlocks = 4;  // blocks of 256 threads an SM holds at once
+// 7168 bf16 values: 59 us, 6.0 TB/s; 2047 rows of 2048 of 64 experts 3.9 us (by
+// tiles of one expert's rows, as below, 97 and 12 us). kRowBlocks: blocks of 256
+// threads for each SM, which holds four at once (3, 4, 5 held at once, 8: 64.0,
+// 60.3, 65.3, 58.7 us).
+constexpr int kRowBlocks = 8;
 
 // PLAIN: bf16 values as they are (no activation, no weights)
 template <typename T, int ACT, bool PLAIN>
