@@ -837,6 +837,21 @@ __device__ __forceinline__ void st_shared(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+// v += what this thread wrote at p before
+__device__ __forceinline__ void add_sector(uint32_t (&v)[8], const float* p) {
+  float o[8];
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3])
+               : "l"(p)
+               : "memory");
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+               : "l"(p + 4)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __float_as_uint(o[i] + __uint_as_float(v[i]));
+}
+
 // Tile t of a weight gradient: expert by expert, its rows (of K) inside
 template <int BM>
 __device__ __forceinline__ Tile grad_tile(int t, int K, int N) {
@@ -943,13 +958,32 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   // the last CTA to arrive, in CTA order. Otherwise whole tiles in turn.
   const bool split = MODE != 2 && !PAIR && tiles < grid && *s_wide == 0;
   const Range rg(split ? tiles : 0, kst, grid);
-  // Walk this CTA's pieces: f(tile, first stage, end stage)
+  // Chains: the tensor core drops what is below its accumulator's last place,
+  // which adds up over a long contraction: the relative error of dW after 16,
+  // 32, 64 and 128 stages was 5.2e-7, 1.3e-6, 2.7e-6 and 6.2e-6, of Y 1.2e-7 to
+  // 1.3e-6. Where fp32 is stored (bf16's own rounding is 2^-9), the accumulator
+  // therefore starts anew after at most CHAIN stages, and the epilogue adds the
+  // chains, rounded to nearest, where they lie: 6e-7 and 2.4e-7 at any length.
+  // Longer for Y and dX, whose products the epilogue's traffic slows more: of
+  // 8192 cubed 340, 338 and 420 us in one chain, 371, 369 and 455 us so, with 16
+  // for all 467, 456 and 445. (By reductions instead of reading back: 458, 454,
+  // 542; with the sums kept in 128 registers a thread, which the other warps
+  // give up: 359, 360, 438, but 183 us for ragged dW in one chain, here 140.)
+  constexpr int CHAIN = sizeof(TO) == 2 ? 0 : MODE == 2 ? 16 : 32;
+  auto chains = [&](auto& f, int t, int p0, int p1) {
+    const int n = CHAIN ? max(1, up_div(p1 - p0, max(CHAIN, 1))) : 1, each = up_div(p1 - p0, n);
+    for (int i = 0, k0 = p0; i < n; ++i, k0 += each)
+      if (!f(t, k0, min(k0 + each, p1), p0, p1)) return false;
+    return true;
+  };
+  // Walk this CTA's pieces: f(tile, first stage, end stage, the piece's first
+  // and end)
   auto walk = [&](auto f) {
     if (split) {
       const int end = rg.start(cta + 1);
       for (int i = rg.start(cta); i < end;) {
         const int t = i / kst, k0 = i - t * kst, k1 = min(kst, k0 + end - i);
-        if (!f(t, k0, k1)) return;
+        if (!chains(f, t, k0, k1)) return;
         i += k1 - k0;
       }
     } else {
@@ -959,7 +993,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           const int e = tile(t).e;
           k1 = base[e + 1] - base[e];
         }
-        if (!f(t, 0, k1)) return;
+        if (!chains(f, t, 0, k1)) return;
       }
     }
   };
@@ -1013,7 +1047,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     };
     auto b_boxes = [](const Tile& tl) { return !PAIR && tl.n > 128 ? 2 : 1; };
     if (a_side) {
-      walk([&](int t, int k0, int k1) {
+      walk([&](int t, int k0, int k1, int, int) {
         const Tile tl = tile(t);
         const int na = a_bytes(tl, rank), both = a_bytes(tl, 0) + (PAIR ? a_bytes(tl, 1) : 0);
         const uint32_t expect = both + (PAIR ? 2 : b_boxes(tl)) * BOX;
@@ -1056,7 +1090,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       // / 32) 4. Loaded four stages ahead.
       const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
       constexpr uint32_t ONE = 0x7f7f7f7fu;
-      walk([&](int t, int k0, int k1) {
+      walk([&](int t, int k0, int k1, int, int) {
         const Tile tl = tile(t);
         const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
         const int first = MODE == 2 ? base[tl.e] : 0;
@@ -1179,7 +1213,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           mma<PAIR>(d, ad0 + off + kk * A_ON, bd0 + off + kk * B_ON, idk, sf, sf + 4,
                     kk > 0 ? 1u : more);
       };
-      if (elect_one()) walk([&](int t, int k0, int k1) {
+      if (elect_one()) walk([&](int t, int k0, int k1, int, int) {
         if (k0 == k1) return true;
         // the middle accumulator, free of the tile before, and this tile's
         // other one, free of the tile before that
@@ -1241,9 +1275,10 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     const uint32_t leader_tfree = PAIR ? mapa_shared(smem_u32(tfree), 0) : 0;
     auto finish = [&](float v) { return MODE == 0 && p.silu ? silu_of<TO>(v) : v; };
     const bool sectors = reinterpret_cast<uintptr_t>(p.out) % 32 == 0;  // (rows are multiples of 128)
-    walk([&](int t, int k0, int k1) {
+    walk([&](int t, int k0, int k1, int p0, int p1) {
       const Tile tl = tile(t);
-      const bool whole = MODE == 2 || (k0 == 0 && k1 == kst);
+      const bool whole = MODE == 2 || (p0 == 0 && p1 == kst);
+      const bool more = k0 > p0, last_chain = k1 == p1;
       // rows of this warp's 32 lanes
       const int r0 = static_cast<int>(rank) * 128 + w * 32, rows = min(32, tl.rows - r0);
       const size_t out_row = (MODE == 2 ? static_cast<size_t>(tl.e) * K : 0) + tl.row0 + r0;
@@ -1300,8 +1335,21 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         }
         if (some && whole) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            put_rows32(out, sectors, out_row, rows, width, tl.n0 + col + i * 32, r[i], finish);
+          for (int i = 0; i < 2; ++i) {
+            if constexpr (CHAIN == 0)
+              put_rows32(out, sectors, out_row, rows, width, tl.n0 + col + i * 32, r[i], finish);
+            else
+              put_rows32_by(out, out_row, rows, width, tl.n0 + col + i * 32, r[i],
+                            [](float v) { return v; }, [&](TO* to, uint32_t (&v)[8]) {
+                              if (more) add_sector(v, to);
+                              if (MODE == 0 && last_chain && p.silu) {
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                  v[c] = __float_as_uint(finish(__uint_as_float(v[c])));
+                              }
+                              st_sector(sectors, to, v);
+                            });
+          }
         } else if (some && lane < rows) {
           // (at most kSplitRows rows: the first quarter's)
           uint32_t* o = reinterpret_cast<uint32_t*>(slice(cta) + lane * kTileCols + col);
@@ -1309,13 +1357,14 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int c = 0; c < 32; c += 8) {
-              const uint32_t v[8] = {r[i][c],     r[i][c + 1], r[i][c + 2], r[i][c + 3],
-                                     r[i][c + 4], r[i][c + 5], r[i][c + 6], r[i][c + 7]};
+              uint32_t v[8] = {r[i][c],     r[i][c + 1], r[i][c + 2], r[i][c + 3],
+                               r[i][c + 4], r[i][c + 5], r[i][c + 6], r[i][c + 7]};
+              if (CHAIN != 0 && more) add_sector(v, reinterpret_cast<float*>(o + i * 32 + c));
               st_sector(true, o + i * 32 + c, v);
             }
         }
       }
-      if (!whole) {
+      if (!whole && last_chain) {
         const int last_cta = rg.owner((t + 1) * kst - 1);
         __threadfence();
         bar_epi();

@@ -125,11 +125,10 @@ __device__ __forceinline__ float silu_of(float z) {
 // 32 columns of up to 32 rows, a row to a lane, through `finish` to out [..][N]:
 // neighbouring lanes exchange 32-byte pieces first, so that a store
 // instruction writes contiguous runs of 128 bytes (fp32; bf16: 64), not a
-// sector of each row. sectors: out is 32-byte aligned (rows are multiples of
-// 128 bytes).
-template <typename TO, typename F>
-__device__ __forceinline__ void put_rows32(TO* out, bool sectors, size_t row0, int rows, int N,
-                                           int col, const uint32_t (&r)[32], F finish) {
+// sector of each row. store(address, piece) writes one.
+template <typename TO, typename F, typename S>
+__device__ __forceinline__ void put_rows32_by(TO* out, size_t row0, int rows, int N, int col,
+                                              const uint32_t (&r)[32], F finish, S store) {
   constexpr int PER = 32 / sizeof(TO), NC = 32 / PER;  // a piece's columns, a row's pieces
   const int lane = threadIdx.x & 31;
   uint32_t v[NC][8];
@@ -166,7 +165,14 @@ __device__ __forceinline__ void put_rows32(TO* out, bool sectors, size_t row0, i
   TO* o = out + (row0 + g) * N + col + (lane - g) * PER;
 #pragma unroll
   for (int i = 0; i < NC; ++i)
-    if (g + i < rows) st_sector(sectors, o + static_cast<size_t>(i) * N, v[i]);
+    if (g + i < rows) store(o + static_cast<size_t>(i) * N, v[i]);
+}
+// sectors: out is 32-byte aligned (rows are multiples of 128 bytes)
+template <typename TO, typename F>
+__device__ __forceinline__ void put_rows32(TO* out, bool sectors, size_t row0, int rows, int N,
+                                           int col, const uint32_t (&r)[32], F finish) {
+  put_rows32_by(out, row0, rows, N, col, r, finish,
+                [&](TO* p, const uint32_t (&v)[8]) { st_sector(sectors, p, v); });
 }
 
 }  // namespace

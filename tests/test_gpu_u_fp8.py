@@ -369,6 +369,42 @@ def test_the_largest_contractions_and_widths(cuda_ok):
         check_grad(p, run_grad(p))
 
 
+# Long sums keep fp32's precision: an accumulator that drops what is below its
+# last place loses half a step on average with each of its additions, four to 128
+# steps of the contraction, so the norm of the error has to stay below that of a
+# chain of 2048 steps, 64 additions (Y and dX: 4096, 128).
+@pytest.mark.parametrize("counts,K,N", [([16384], 256, 320), ([20000, 0, 5, 2049], 192, 256)])
+def test_precision_of_long_weight_gradients(cuda_ok, counts, K, N):
+    p = problem(counts, K, N, seed=K)
+    dW, tile = run_grad(p), 0
+    check_grad(p, dW)
+    xs, ds = columns_of(p["x"].cscale, K), columns_of(p["dy"].cscale, N)
+    for e, n in enumerate(counts):
+        t = slice(tile, tile + -(-n // 128))
+        a, b = (decode(r.cq[t.start * 128:t.stop * 128], s[t], 128, 1)
+                for r, s in ((p["x"], xs), (p["dy"], ds)))
+        y = a.t() @ b
+        assert float((dW[e].to(F64) - y).norm()) <= 64 * U32 * float(y.norm())
+        tile = t.stop
+
+
+# One tile cut among all blocks; as many tiles as blocks almost, so that a block's part
+# is long; few and many rows
+@pytest.mark.parametrize("counts,K,N", [([3], 65536, 64), ([2], 16384, 25600), ([300, 1], 16640, 320),
+                                        ([1000], 16384, 256)])
+@pytest.mark.parametrize("silu", [0, 1])
+def test_precision_of_long_products(cuda_ok, counts, K, N, silu):
+    p = problem(counts, K, N, silu=silu, seed=K)
+    out = run_product(p, False)
+    check_products(p, False, out)
+    if not silu:
+        a, lo = decode(p["x"].q, p["x"].scale[:, :K // 128].contiguous(), 1, 128), 0
+        for e, n in enumerate(counts):
+            y = a[lo:lo + n] @ decode(p["wq"][e], p["wsc"][e], 128, 128)
+            assert float((out[lo:lo + n].to(F64) - y).norm()) <= 128 * U32 * float(y.norm())
+            lo += n
+
+
 @pytest.mark.parametrize("counts", [[2, 0, 3], [150, 40, 300]])
 def test_rows_of_no_segment(cuda_ok, counts):
     # before the first and behind the last: not quantised, not written, no part of any sum
