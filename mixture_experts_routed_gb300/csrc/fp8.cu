@@ -715,8 +715,8 @@ __global__ void __launch_bounds__(kColThreads)
 // rows' side twice: 1 to 4 % slower.) Eight warps drain: into registers, which
 // frees the accumulator, and then to out.
 //
-// Bound, of many rows: power. 8192 x 8192 x 8192 in short runs 318, 320 and 334
-// us for Y, dX and dW (3.4 PFLOP/s), with operands of zeros or ones 276, 269 and
+// Bound, of many rows: power. 8192 x 8192 x 8192 in short runs 318, 320 and 460
+// us for Y, dX and dW (3.4 PFLOP/s), with operands of zeros or ones, dW in one chain, 276, 269 and
 // 291; after seconds the cap leaves 1350 MHz and 2.9 PFLOP/s. Behind it a pair's
 // stage: 32 KB into each SM, which at 64 bytes a clock take what its four
 // products take, 512 clocks (with a quarter of the products 267, 232 and 263
@@ -724,8 +724,8 @@ __global__ void __launch_bounds__(kColThreads)
 // experts, 7168 x 2048: 181 us for 481 GFLOP, nine rounds of tiles of which 6.7
 // are rows that exist (rows as the products' columns, 32 at a time, did away
 // with the others: 184 us, for the loads stay). dW of 16 x 5120 x 1536 from
-// 16384 rows 123 us, 4.1 TB/s written beside its loads; of 64 x 1408 x 2048 from
-// 8191 rows 135 us, 5.5 TB/s. Two rows of 8 experts of 4096 x 11008: 22 us, 7
+// 16384 rows 138 us, 3.6 TB/s written beside its loads; of 64 x 1408 x 2048 from
+// 8191 rows 140 us, 5.3 TB/s. Two rows of 8 experts of 4096 x 11008: 22 us, 7
 // TB/s and 9 us of start and join.
 namespace f8 {
 using namespace ptx;
@@ -965,7 +965,7 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   // therefore starts anew after at most CHAIN stages, and the epilogue adds the
   // chains, rounded to nearest, where they lie: 6e-7 and 2.4e-7 at any length.
   // Longer for Y and dX, whose products the epilogue's traffic slows more: of
-  // 8192 cubed 340, 338 and 420 us in one chain, 371, 369 and 455 us so, with 16
+  // 8192 cubed 331, 327 and 350 us in one chain, 371, 369 and 460 us so, with 16
   // for all 467, 456 and 445. (By reductions instead of reading back: 458, 454,
   // 542; with the sums kept in 128 registers a thread, which the other warps
   // give up: 359, 360, 438, but 183 us for ragged dW in one chain, here 140.)
