@@ -10,7 +10,7 @@
 // (the counts are constants to the gradient). Bound by latency: two launches
 // of a few dependent loads, sums and a hand-over each. 256 tokens of 8 experts
 // 7.1 us, 8192 of 64 in 17 sequences 10.8, 16384 of 256 (17 MB) 14.8; the
-// gradients 1.5, 3.5 and 6.9 us, the last at 4.9 TB/s.
+// gradients 1.6, 3.8 and 7.6 us, the last at 4.4 TB/s.
 #include <cstdint>
 #include <type_traits>
 
@@ -328,21 +328,42 @@ __global__ void __launch_bounds__(kWarps * 32)
   const float fs = static_cast<float>(E) / (static_cast<float>(k) * static_cast<float>(n));
   Row<NJ> L;
   L.load(logits + static_cast<size_t>(t) * E, E, lane);
-  float f[NJ], dot = 0.f;
+  float f[NJ], den, dot;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int e = lane + 32 * j;
     f[j] = e < E ? fs * static_cast<float>(__ldg(counts + static_cast<size_t>(s) * E + e)) : 0.f;
-    L.v[j] = e < E ? expf(L.v[j] - l) : 0.f;
-    dot = fmaf(L.v[j], f[j], dot);
   }
-  dot = warp_sum(dot);
+  // p = exp(L - shift) over its own sum, whatever the shift: exp(L - lse) alone would be off by half
+  // a step of |lse|, which is many of p's where logits share an offset. The lse is at hand before a
+  // maximum is (16384 x 256: 7.9 us with one); past some 2^24 its half step is too wide for a shift.
+  auto weigh = [&](float shift) {
+    den = dot = 0.f;
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) {
+      L.v[j] = lane + 32 * j < E ? expf(L.v[j] - shift) : 0.f;
+      den += L.v[j];
+      dot = fmaf(L.v[j], f[j], dot);
+    }
+    den = warp_sum(den);
+    dot = warp_sum(dot);
+  };
+  weigh(l);
+  if (!(den > 0.25f && den < 4.f)) {
+    L.load(logits + static_cast<size_t>(t) * E, E, lane);
+    float top = L.v[0];
+#pragma unroll
+    for (int j = 1; j < NJ; ++j) top = fmaxf(top, L.v[j]);
+    weigh(warp_max(top));
+  }
+  const float inv = 1.f / den;
+  dot *= inv;
   const float cb = g * balance / (static_cast<float>(used) * static_cast<float>(n));
   const float cz = g * 2.f * zcoef / static_cast<float>(all) * l;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int e = lane + 32 * j;
-    if (e < E) out[e] = L.v[j] * fmaf(cb, f[j] - dot, cz);
+    if (e < E) out[e] = L.v[j] * inv * fmaf(cb, f[j] - dot, cz);
   }
 }
 
