@@ -206,7 +206,8 @@ __global__ void __launch_bounds__(256)
     if (!in && lane == 0) atomicOr(err, kErrBadIndex);
     row = x + static_cast<size_t>(in ? xr : 0) * C;
     if constexpr (Z) zrow = z + static_cast<size_t>(r) * C;
-    w = weight != nullptr ? __ldg(weight + r) : 1.f;
+    // (no row: zeros, whatever its weight)
+    w = weight != nullptr && in ? __ldg(weight + r) : 1.f;
   };
   uint4 raw[F], zr[Z ? F : 1];
   auto load = [&](int kb) {
@@ -293,12 +294,14 @@ template <typename T, int TENSORS, int MOST>
 struct ColRing {
   static constexpr int V = 16 / sizeof(T), LPR = 128 / V, RPP = kColThreads / LPR,
                        PASS = 128 / RPP;
+  static_assert(PASS <= 32, "a bit for each row of a thread");
   static constexpr int BYTES = kTileBytes * sizeof(T) * TENSORS;
   static constexpr int FIT = BYTES <= 32768 ? 3 : BYTES <= 65536 ? 2 : 1;
   static constexpr int BUFS = FIT < MOST ? FIT : MOST, DEPTH = BUFS - 1, SMEM = BUFS * BYTES;
   static_assert(SMEM <= 200 * 1024, "shared memory");
   struct At {
     int rt, cb, row0, rows;  // (rows 0: no such tile)
+    uint32_t none;           // bit j: this thread's row j has no source
   };
   const T *x, *z;
   const int32_t* src;
@@ -315,7 +318,7 @@ struct ColRing {
   // what it copied: no barrier, and a buffer is free once its thread is
   // through with it.
   __device__ At fetch(int t, int b) const {
-    At a{0, 0, 0, 0};
+    At a{0, 0, 0, 0, 0u};
     if (t < tiles) {
       a.rt = t / nb;
       a.cb = t - a.rt * nb;
@@ -335,16 +338,17 @@ struct ColRing {
 #pragma unroll
         for (int j = 0; j < PASS; ++j) {
           const int r = a.row0 + r0 + j * RPP;
-          bool some = r0 + j * RPP < a.rows && col < C;
+          bool some = r0 + j * RPP < a.rows;
           int xr = r;
           if (some && src != nullptr) {
             xr = __ldg(src + r);
             if (xr < 0 || xr >= x_rows) {
               atomicOr(err, kErrBadIndex);
+              a.none |= 1u << j;
               some = false;
             }
           }
-          if (some) {
+          if (some && col < C) {
             ptx::cp_async16(ptx::smem_u32(piece(b, 0, j)), x + static_cast<size_t>(xr) * C + col);
             if constexpr (TENSORS > 1)
               ptx::cp_async16(ptx::smem_u32(piece(b, 1, j)), z + static_cast<size_t>(r) * C + col);
@@ -413,7 +417,9 @@ __global__ void __launch_bounds__(kColThreads)
 #pragma unroll
     for (int j = 0; j < PASS; ++j) {
       const int r = r0 + j * RPP;
-      const float w = weight != nullptr && r < a.rows ? __ldg(weight + a.row0 + r) : 1.f;
+      // (no source: zeros, whatever its weight)
+      const bool weighed = weight != nullptr && r < a.rows && (a.none >> j & 1) == 0;
+      const float w = weighed ? __ldg(weight + a.row0 + r) : 1.f;
       input<T, ACT>(*ring.piece(b, 0, j), *ring.piece(b, Z ? 1 : 0, j), w, held[j]);
       uint32_t m = 0;
 #pragma unroll
