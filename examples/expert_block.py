@@ -96,8 +96,8 @@ class ExpertBlock:
 
     # ------------------------------------------------------------ training
     def train_step(self, x, dout, dnext):
-        """Outputs and every gradient, given dout (of out, by the residual) and dnext (fp32,
-        of the next block's input)."""
+        """Outputs, every gradient and the workspaces that hold an error word (the norms' does
+        not), given dout (of out, by the residual) and dnext (fp32, of the next block's input)."""
         T = x.shape[0]
         c, nc = self.config(T, keep_z=1), self.norms(T)
         ws, bws = moe.alloc_workspace(c), moe.alloc_workspace(c, "backward")
@@ -125,7 +125,7 @@ class ExpertBlock:
     def train_step_fp8(self, x, dout, dnext, state, p=0.1, balance=0.01, z_loss=0.001):
         """The same with the experts in 8 bits, dropout (state: int64 [2], seed and step) of
         their output and the router's losses, whose gradient joins the router's: outputs, the
-        losses, every gradient."""
+        losses, every gradient, the workspaces with an error word."""
         T, d, f, E, k = x.shape[0], self.d, self.f, self.E, self.k
         R = T * k
         c, nc = self.config(T), self.norms(T)
@@ -178,16 +178,18 @@ class ExpertBlock:
 
 
 def timed(name, f, reps=20):
+    """Prints a call's time; the last call's result."""
     for _ in range(3):
         f()
     torch.cuda.synchronize()
     a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
     a.record()
     for _ in range(reps):
-        f()
+        r = f()
     b.record()
     torch.cuda.synchronize()
     print(f"{name:40s} {a.elapsed_time(b) / reps * 1e3:10.1f} us")
+    return r
 
 
 def main():
@@ -206,11 +208,13 @@ def main():
     timed(f"decode {a.decode} tokens", lambda: block.decode(few, fws))
     timed(f"prefill {a.tokens} tokens, 4-bit experts", lambda: block.prefill(x, sws, mws))
     dout, dnext = torch.randn_like(x), torch.randn((a.tokens, a.d), device="cuda")
-    timed(f"train step, {a.tokens} tokens", lambda: block.train_step(x, dout, dnext), reps=3)
+    *_, step = timed(f"train step, {a.tokens} tokens", lambda: block.train_step(x, dout, dnext),
+                     reps=3)
     state = torch.tensor([1, 0], dtype=torch.int64, device="cuda")
-    timed(f"train step, {a.tokens} tokens, 8-bit experts",
-          lambda: block.train_step_fp8(x, dout, dnext, state, p=a.dropout), reps=3)
-    for ws in (fws, sws, mws):
+    *_, step8 = timed(f"train step, {a.tokens} tokens, 8-bit experts",
+                      lambda: block.train_step_fp8(x, dout, dnext, state, p=a.dropout), reps=3)
+    # every workspace with an error word; a training step makes its own and returns them
+    for ws in (fws, sws, mws, *step, *step8):
         if moe.get_device_error(ws) != moe.MOE_OK:
             raise SystemExit("device error")
 
