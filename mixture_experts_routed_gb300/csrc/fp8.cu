@@ -705,15 +705,17 @@ __global__ void __launch_bounds__(kColThreads)
 // as they lie in memory, k- or row-major as the mode has it (the tensor core
 // takes 8-bit operands either way, so the one copy of W serves both
 // products). A chunk of scales is 512 bytes, four for each of 128 rows, and a
-// product names the one of the four it takes: those of four stages. The warp
-// that loads the columns' side writes the chunks of four stages before the
-// first one's codes: its copy is issued after they are written, so they are
-// there when the copy's bytes are, and a pair's odd CTA needs no arrival of
-// its own at the even one's barrier (a release at cluster scope, which took 1
-// us a stage: 8192 x 8192 x 8192 in 1131 us). One thread copies the chunks to
-// tensor memory (tcgen05.cp, in line with the products: a copy every stage
-// took 323, 362 and 423 us for Y, dX and dW of 8192 cubed, 319, 355 and 376
-// since) and issues the products of all the columns x 32 steps
+// product names the one of the four it takes: those of four stages. A warp of
+// its own writes the chunks, those of GROUP x 4 stages to a slot of a ring, and
+// hands the slot over with an arrival that releases them: to the issuing thread
+// in its CTA; a pair's odd CTA first, at cluster scope, to the even CTA's warp,
+// which passes both on. That release takes about 1 us, so it is made once for
+// eight stages, ahead of the products (for every four 363, 374 and 488 us for
+// Y, dX and dW of 8192 cubed, for eight 315, 350 and 487; by the warp that loads
+// the columns' side, in its ring, 522, 542 and 662). One thread copies the
+// chunks to tensor memory (tcgen05.cp, in line with the products: a copy every
+// stage took 323, 362 and 423 us, every four 319, 355 and 376, dW in one chain)
+// and issues the products of all the columns x 32 steps
 // (kind::mxf8f6f4) that read them. Three accumulators of 128 columns: tiles
 // take the first two and the last two in turn, and the next tile starts once
 // the middle one is drained, which is drained first. (Products of half the
@@ -741,6 +743,9 @@ constexpr int BOX = 128 * 128, CHUNK = 512;
 // again SLOTS uses later, of a stage or more each, so after products that a
 // ring of fewer stages has seen the end of.
 constexpr int SF_COL = 384, SF_SLOT = 12, SLOTS = 10;
+// Scales in shared memory: a ring of their own, of GROUP chunks of four stages
+constexpr int GROUP = 2, GROUP_STAGES = 4 * GROUP, SF_RING = 8 / GROUP;
+constexpr int GROUP_BYTES = GROUP * 3 * CHUNK;
 constexpr int TMEM_COLS = 512;
 constexpr int EPI_THREADS = 256, THREADS = 128 + EPI_THREADS;
 
@@ -748,11 +753,11 @@ template <bool PAIR>
 struct Cfg {
   static constexpr int BM = PAIR ? 256 : 128;
   static constexpr int B_BOXES = PAIR ? 1 : 2;
-  static constexpr int OFF_B = BOX, OFF_SFA = OFF_B + B_BOXES * BOX, OFF_SFB = OFF_SFA + CHUNK;
-  static constexpr int STAGE = (OFF_SFB + 2 * CHUNK + 1023) / 1024 * 1024;
+  static constexpr int OFF_B = BOX, STAGE = OFF_B + B_BOXES * BOX;
   static constexpr int STAGES = PAIR ? 6 : 4;  // (shared memory's most)
-  static constexpr int OFF_BAR = STAGES * STAGE;
-  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 6) * 8 + 24;
+  static constexpr int OFF_SF = STAGES * STAGE;
+  static constexpr int OFF_BAR = OFF_SF + SF_RING * GROUP_BYTES;
+  static constexpr int OFF_SEG = OFF_BAR + (2 * STAGES + 6 + 3 * SF_RING) * 8 + 24;
   static constexpr int SMEM = OFF_SEG + 3 * (kMaxExperts + 1) * 4 + 1024;
   static_assert(SMEM <= 227 * 1024, "shared memory");
   static_assert(SF_COL + SLOTS * SF_SLOT <= TMEM_COLS && SLOTS > STAGES, "tensor memory");
@@ -890,7 +895,10 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   uint64_t* tfull = empty + STAGES;  // by a tile's parity
   uint64_t* tfree = tfull + 2;       // accumulators 0, 1 and 2; pair: the even CTA's
   uint64_t* drain = tfree + 3;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* sfull = drain + 1;  // of the scales' ring; pair: the even CTA's
+  uint64_t* sodd = sfull + SF_RING;  // the odd CTA's are written (the even CTA's barriers)
+  uint64_t* sempty = sodd + SF_RING;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + SF_RING);
   int* s_ok = reinterpret_cast<int*>(tmem_slot + 1);
   uint32_t* s_last = tmem_slot + 2;
   int* s_wide = reinterpret_cast<int*>(tmem_slot + 3);
@@ -911,6 +919,11 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
     for (int i = 0; i < 2; ++i) mbar_init(&tfull[i], 1);
     for (int i = 0; i < 3; ++i) mbar_init(&tfree[i], PAIR ? 16 : 8);
     mbar_init(drain, 1);
+    for (int i = 0; i < SF_RING; ++i) {
+      mbar_init(&sfull[i], 1);
+      mbar_init(&sodd[i], 1);
+      mbar_init(&sempty[i], 1);
+    }
     *s_wide = 0;
     fence_mbar_init();
   }
@@ -1092,88 +1105,12 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
         }
       }
     } else {
-      // four stages' scales, as chunks: row i's four bytes at (i % 32) 16 + (i
-      // / 32) 4. Loaded four stages ahead.
-      const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
-      constexpr uint32_t ONE = 0x7f7f7f7fu;
       walk([&](int t, int k0, int k1, int, int) {
         const Tile tl = tile(t);
-        const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
         const int first = MODE == 2 ? base[tl.e] : 0;
-        struct Quad {
-          uint32_t w[MODE == 2 ? 12 : 5];
-        } cur, nxt;
-        auto load = [&](int q) {
-          Quad r;
-          if constexpr (MODE == 2) {
-            // a word is rows lane + 32 i of one block: of A's and of the two of columns
-            const int m = tl.row0 / 128 + rank, n = tl.n0 / 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int kb = first + min(q * 4 + i, k1 - 1);
-              const uint32_t* a = reinterpret_cast<const uint32_t*>(p.as) +
-                                  (static_cast<size_t>(kb) * nbk + m) * 32 + lane;
-              const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bs) +
-                                  (static_cast<size_t>(kb) * nbn + n) * 32 + lane;
-              r.w[i] = m < nbk ? __ldg(a) : ONE;
-              r.w[4 + i] = __ldg(b);
-              r.w[8 + i] = n + 1 < nbn ? __ldg(b + 32) : ONE;
-            }
-          } else {
-            // rows lane + 32 i, four blocks each; lanes 0..7: a block of the
-            // two blocks of columns each
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int row = tl.row0 + static_cast<int>(rank) * 128 + min(lane + 32 * i, rows - 1);
-              r.w[i] = rows > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
-                                      p.as + static_cast<size_t>(row) * pitch + q * 4))
-                                : ONE;
-            }
-            const int nb = min(tl.n0 / 128 + (lane & 1), up_div(width, 128) - 1);
-            const int kb = min(q * 4 + (lane >> 1 & 3), kst - 1);
-            const int at = MODE == 1 ? nb * nbn + kb : kb * nbn + nb;
-            r.w[4] = __ldg(p.bs + static_cast<size_t>(tl.e) * nbk * nbn + at);
-          }
-          return r;
-        };
-        // the four bytes of each of four words, by byte
-        auto turn = [](const uint32_t* t) {
-          const uint32_t a = __byte_perm(t[0], t[1], 0x5140), b = __byte_perm(t[2], t[3], 0x5140);
-          const uint32_t c = __byte_perm(t[0], t[1], 0x7362), d = __byte_perm(t[2], t[3], 0x7362);
-          return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
-                            __byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632));
-        };
         const int nb = b_boxes(tl), col0 = tl.n0 + rank * 128;
-        if (k0 < k1) nxt = load(k0 >> 2);
         for (int kb = k0; kb < k1; ++kb) {
-          const bool four = kb == k0 || (kb & 3) == 0;
-          uint4 a, b0, b1;
-          if (four) {
-            cur = nxt;
-            if ((kb >> 2) * 4 + 4 < k1) nxt = load((kb >> 2) + 1);
-            if constexpr (MODE == 2) {
-              a = turn(cur.w);
-              b0 = turn(cur.w + 4);
-              b1 = turn(cur.w + 8);
-            } else {
-              a = make_uint4(cur.w[0], cur.w[1], cur.w[2], cur.w[3]);
-              uint32_t s[2] = {0, 0};
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                s[i & 1] |= __shfl_sync(0xffffffffu, cur.w[4], i) << (i >> 1) * 8;
-              b0 = make_uint4(s[0], s[0], s[0], s[0]);
-              b1 = make_uint4(s[1], s[1], s[1], s[1]);
-            }
-          }
           if (!take()) return false;
-          if (four) {
-            const uint32_t sf = base0 + s * C::STAGE + C::OFF_SFA + lane * 16;
-            st_shared(sf, a);
-            st_shared(sf + CHUNK, b0);
-            st_shared(sf + 2 * CHUNK, b1);
-            fence_proxy_async_shared();
-            __syncwarp();
-          }
           if (elect_one()) {
             uint8_t* dst = smem + s * C::STAGE + C::OFF_B;
 #pragma unroll
@@ -1194,6 +1131,126 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       });
     }
     if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
+  } else if (warp == 3) {
+    // four stages' scales, as chunks: row i's four bytes at (i % 32) 16 + (i
+    // / 32) 4. Loaded a group ahead.
+    int sl = 0;
+    uint32_t ph = 0;
+    bool dead = false;
+    const uint32_t sf0 = smem_u32(smem + C::OFF_SF) + lane * 16;
+    const uint32_t odd0 = PAIR ? mapa_shared(smem_u32(sodd), 0) : 0;
+    const int pitch = up_div(kst, 4) * 4, nbk = up_div(K, 128), nbn = up_div(N, 128);
+    constexpr uint32_t ONE = 0x7f7f7f7fu;
+    walk([&](int t, int k0, int k1, int, int) {
+      const Tile tl = tile(t);
+      const int rows = min(128, tl.rows - static_cast<int>(rank) * 128);
+      const int first = MODE == 2 ? base[tl.e] : 0;
+      struct Quad {
+        uint32_t w[MODE == 2 ? 12 : 5];
+      } quad[GROUP];
+      auto load = [&](int q) {
+        Quad r;
+        if constexpr (MODE == 2) {
+          // a word is rows lane + 32 i of one block: of A's and of the two of columns
+          const int m = tl.row0 / 128 + rank, n = tl.n0 / 128;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int kb = first + min(q * 4 + i, k1 - 1);
+            const uint32_t* a = reinterpret_cast<const uint32_t*>(p.as) +
+                                (static_cast<size_t>(kb) * nbk + m) * 32 + lane;
+            const uint32_t* b = reinterpret_cast<const uint32_t*>(p.bs) +
+                                (static_cast<size_t>(kb) * nbn + n) * 32 + lane;
+            r.w[i] = m < nbk ? __ldg(a) : ONE;
+            r.w[4 + i] = __ldg(b);
+            r.w[8 + i] = n + 1 < nbn ? __ldg(b + 32) : ONE;
+          }
+        } else {
+          // rows lane + 32 i, four blocks each; lanes 0..7: a block of the
+          // two blocks of columns each
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = tl.row0 + static_cast<int>(rank) * 128 + min(lane + 32 * i, rows - 1);
+            r.w[i] = rows > 0 ? __ldg(reinterpret_cast<const uint32_t*>(
+                                    p.as + static_cast<size_t>(row) * pitch + q * 4))
+                              : ONE;
+          }
+          const int nb = min(tl.n0 / 128 + (lane & 1), up_div(width, 128) - 1);
+          const int kb = min(q * 4 + (lane >> 1 & 3), kst - 1);
+          const int at = MODE == 1 ? nb * nbn + kb : kb * nbn + nb;
+          r.w[4] = __ldg(p.bs + static_cast<size_t>(tl.e) * nbk * nbn + at);
+        }
+        return r;
+      };
+      // the four bytes of each of four words, by byte
+      auto turn = [](const uint32_t* t) {
+        const uint32_t a = __byte_perm(t[0], t[1], 0x5140), b = __byte_perm(t[2], t[3], 0x5140);
+        const uint32_t c = __byte_perm(t[0], t[1], 0x7362), d = __byte_perm(t[2], t[3], 0x7362);
+        return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632),
+                          __byte_perm(c, d, 0x5410), __byte_perm(c, d, 0x7632));
+      };
+      // the chunks of the group that stage g is in, from g on
+      auto some = [&](int g, int i) {
+        const int k = (g & ~(GROUP_STAGES - 1)) + i * 4;
+        return k + 3 >= g && k < k1;
+      };
+      auto fetch = [&](int g) {
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i)
+          if (some(g, i)) quad[i] = load((g / GROUP_STAGES) * GROUP + i);
+      };
+      if (k0 < k1) fetch(k0);
+      for (int g = k0; g < k1;) {
+        const int after = (g | (GROUP_STAGES - 1)) + 1;
+        const bool in_time = mbar_wait(&sempty[sl], ph ^ 1u, kWaitLimitNs);
+        if (!__all_sync(0xffffffffu, in_time)) {
+          dead = true;
+          return false;
+        }
+#pragma unroll
+        for (int i = 0; i < GROUP; ++i) {
+          if (!some(g, i)) continue;
+          uint4 a, b0, b1;
+          if constexpr (MODE == 2) {
+            a = turn(quad[i].w);
+            b0 = turn(quad[i].w + 4);
+            b1 = turn(quad[i].w + 8);
+          } else {
+            a = make_uint4(quad[i].w[0], quad[i].w[1], quad[i].w[2], quad[i].w[3]);
+            uint32_t s[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              s[j & 1] |= __shfl_sync(0xffffffffu, quad[i].w[4], j) << (j >> 1) * 8;
+            b0 = make_uint4(s[0], s[0], s[0], s[0]);
+            b1 = make_uint4(s[1], s[1], s[1], s[1]);
+          }
+          const uint32_t sf = sf0 + sl * GROUP_BYTES + i * 3 * CHUNK;
+          st_shared(sf, a);
+          st_shared(sf + CHUNK, b0);
+          st_shared(sf + 2 * CHUNK, b1);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (rank != 0) {
+          if (lane == 0) mbar_arrive_remote(odd0 + sl * 8);
+        } else {
+          if constexpr (PAIR)
+            if (!__all_sync(0xffffffffu, mbar_wait_spin_cluster(&sodd[sl], ph, kWaitLimitNs))) {
+              dead = true;
+              return false;
+            }
+          if (lane == 0) mbar_arrive(&sfull[sl]);
+        }
+        __syncwarp();
+        if (after < k1) fetch(after);  // (behind the release, which would wait for it)
+        g = after;
+        if (++sl == SF_RING) {
+          sl = 0;
+          ph ^= 1u;
+        }
+      }
+      return true;
+    });
+    if (dead && lane == 0) atomicOr(p.err, kErrTimeout);
   } else if (warp == 1) {
     // (one lane issues: elect_one says how)
     if (rank == 0) {
@@ -1207,8 +1264,9 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
       constexpr uint32_t A_ON = A_STEPS ? 4096 >> 4 : 32 >> 4, B_ON = B_STEPS ? 4096 >> 4 : 32 >> 4;
       const uint32_t base0 = smem_u32(smem);
       const uint32_t ad0 = desc_lo(base0), bd0 = desc_lo(base0 + C::OFF_B),
-                     sa0 = sf_lo(base0 + C::OFF_SFA);
-      int slot = SLOTS - 1;
+                     sa0 = sf_lo(base0 + C::OFF_SF);
+      int slot = SLOTS - 1, sl = 0;
+      uint32_t sph = 0;
       // a stage's products of `steps` x 32 (inlined with a constant for whole ones)
       auto products = [&](int kb, int steps, uint32_t id, uint32_t d, uint32_t more) {
         const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
@@ -1241,12 +1299,27 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
           tc_fence_after();
           if (kb == k0 || (kb & 3) == 0) {
             // four stages' scales, to the next slot
+            if (kb == k0 || kb % GROUP_STAGES == 0) {
+              if (!mbar_wait_spin(&sfull[sl], sph, kWaitLimitNs)) {
+                dead = true;
+                break;
+              }
+              tc_fence_after();
+            }
             if (++slot == SLOTS) slot = 0;
-            const uint32_t off = static_cast<uint32_t>(s) * (C::STAGE / 16);
+            const uint32_t off = (sl * GROUP + (kb >> 2) % GROUP) * (3 * CHUNK / 16);
 #pragma unroll
             for (int c = 0; c < 3; ++c)
               cp_scales<PAIR>(tmem_base + SF_COL + slot * SF_SLOT + c * 4,
                               sa0 + off + c * (CHUNK / 16));
+            const int after = (kb | 3) + 1;
+            if (after >= k1 || after % GROUP_STAGES == 0) {
+              commit<PAIR>(&sempty[sl]);
+              if (++sl == SF_RING) {
+                sl = 0;
+                sph ^= 1u;
+              }
+            }
           }
           const uint32_t more = kb > k0 ? 1u : 0u;
           if (MODE == 2 || kb < len / KS)
