@@ -978,16 +978,22 @@ __global__ void __launch_bounds__(f8::THREADS, 1)
   const bool split = MODE != 2 && !PAIR && tiles < grid && *s_wide == 0;
   const Range rg(split ? tiles : 0, kst, grid);
   // Chains: the tensor core drops what is below its accumulator's last place,
-  // which adds up over a long contraction: the relative error of dW after 16,
-  // 32, 64 and 128 stages was 5.2e-7, 1.3e-6, 2.7e-6 and 6.2e-6, of Y 1.2e-7 to
-  // 1.3e-6. Where fp32 is stored (bf16's own rounding is 2^-9), the accumulator
-  // therefore starts anew after at most CHAIN stages, and the epilogue adds the
-  // chains, rounded to nearest, where they lie: 6e-7 and 2.4e-7 at any length.
-  // Longer for Y and dX, whose products the epilogue's traffic slows more: of
-  // 8192 cubed 331, 327 and 350 us in one chain, 371, 369 and 460 us so, with 16
-  // for all 467, 456 and 445. (By reductions instead of reading back: 458, 454,
-  // 542; with the sums kept in 128 registers a thread, which the other warps
-  // give up: 359, 360, 438, but 183 us for ragged dW in one chain, here 140.)
+  // always towards zero, which adds up over a long contraction: the norm of the
+  // error, of the sum's, after 8, 32, 128 and 512 stages was 5.8e-8, 2.2e-7,
+  // 1.2e-6 and 7.3e-6 for normal values, 1.9e-7, 1.4e-6, 9.7e-6 and 5.9e-5 for
+  // values of one sign, and 8.7e-7, 2.8e-6, 1.1e-5 and 3.9e-5 where rows and
+  // blocks differ by powers of two up to 2^18 (plain fp32 sums of the same: at
+  // most 1.4e-7, 1.1e-7 and 7.1e-7). Where fp32 is stored (bf16's own rounding
+  // is 2^-9), the accumulator therefore starts anew after at most CHAIN stages,
+  // and the epilogue adds the chains, rounded to nearest, one after the other
+  // where they lie: Y and dX 2.3e-7, 1.4e-6 and 2.8e-6, dW 1.5e-7, 5.0e-7 and
+  // 1.3e-6 at any of these lengths; rounding over more chains adds at most half
+  // a step for each. Longer for Y and dX, whose products the epilogue's traffic
+  // slows more: of 8192 cubed 331, 327 and 350 us in one chain, 371, 369 and 460
+  // us so, with 16 for all 467, 456 and 445. (By reductions instead of reading
+  // back: 458, 454, 542; with the sums kept in 128 registers a thread, which
+  // the other warps give up: 359, 360, 438, but 183 us for ragged dW in one
+  // chain, here 140. All with scales in the stages' ring, on one box.)
   constexpr int CHAIN = sizeof(TO) == 2 ? 0 : MODE == 2 ? 16 : 32;
   auto chains = [&](auto& f, int t, int p0, int p1) {
     const int n = CHAIN ? max(1, up_div(p1 - p0, max(CHAIN, 1))) : 1, each = up_div(p1 - p0, n);
