@@ -657,8 +657,11 @@ MOE_API size_t moe_router_loss_workspace_size(const moe_router_loss_config_t* cf
  * nor those of masked tokens are read.
  * Outputs: loss [3] (the loss, balance, z; 0 with no token), counts [S, E]
  * (c), tokens [S + 2] (n_s, then S' and N), lse [T] (0 where masked; not
- * written for tokens of no sequence). Offsets that fall or leave [0, T] write
- * nothing but values of lse, an expert id outside [0, E) is not counted, and both flag
+ * written for tokens of no sequence). Logits of -infinity are experts that a
+ * token may not take (p = 0); a token with nothing else, a +infinity or a NaN
+ * has no softmax: the losses are NaN, and so is its own gradient, unless it is
+ * masked. Offsets that fall or leave [0, T] write nothing but values of lse,
+ * an expert id outside [0, E) is not counted, and both flag
  * MOE_ERR_BAD_INDEX. Bitwise reproducible. */
 MOE_API int moe_router_loss(const moe_router_loss_config_t* cfg, const float* logits,
                    const int32_t* topk_idx, const int32_t* seq_offsets, const uint8_t* mask,
