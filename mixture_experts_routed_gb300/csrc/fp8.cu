@@ -160,7 +160,9 @@ __device__ __forceinline__ uint32_t inv_pair(uint32_t lo, uint32_t hi) {
 // 7168 bf16 values: 59 us, 6.0 TB/s; 2047 rows of 2048 of 64 experts 3.9 us (by
 // tiles of one expert's rows, as below, 97 and 12 us). kRowBlocks: blocks of 256
 // threads for each SM, which holds four at once (3, 4, 5 held at once, 8: 64.0,
-// 60.3, 65.3, 58.7 us).
+// 60.3, 65.3, 58.7 us). 16384 rows of 5120 bf16 values, 6.0 TB/s as they are,
+// gathered or weighted (42 us), 88 us as SiLU and 165 as SiLU' of two tensors
+// (2.9 and 2.6 TB/s); of fp32 67, 101 and 184 us.
 constexpr int kRowBlocks = 8;
 
 // PLAIN: bf16 values as they are (no activation, no weights)
@@ -284,9 +286,14 @@ __global__ void __launch_bounds__(256)
 // bytes of every 16th (fp32: 8th) row, which it copies to a place of its own in
 // shared memory (cp.async) DEPTH tiles ahead. The columns' amax goes over
 // shared memory, a row's (where the rows' form is wanted too) by shuffles:
-// both forms come out of the one read. Bound by HBM: 16384 x 5120 bf16 values to
-// both forms in 59 us, 5.7 TB/s (88 with the loads into registers and every
-// row's amax reduced by itself, 83 with two values an instruction).
+// both forms come out of the one read. (What this cost for bf16 as they are,
+// before the kernel below took them: 88 us for 16384 x 5120.) Both forms of as
+// many bf16 values: weighted and gathered 117 us, SiLU 128, SiLU' 316 (2.9, 2.6
+// and 1.6 TB/s); of fp32, as they are, 168, with a weight and gathered 389, SiLU
+// 212, SiLU' 436. Bound by latency, SiLU near issue (0.7 of the slots, SiLU'
+// 0.36): each row's amax takes shuffles of its own,
+// and 128 registers, or the ring of two tensors or of fp32, leave two blocks or
+// one to an SM.
 constexpr int kColThreads = 256, kColWarps = kColThreads / 32, kTileBytes = 128 * 128;
 
 // T's tiles, TENSORS of them (x, or x and z), in at most BUFS buffers
@@ -484,7 +491,8 @@ __global__ void __launch_bounds__(kColThreads)
 // The same for bf16 values as they are (no activation, no weights). The eight
 // rows' amax of a thread are reduced together, two to a word: a lane gives away
 // half of its words at each step, ends with two rows', makes their scales, and
-// hands the factors back.
+// hands the factors back. Bound by HBM: 16384 x 5120 values to both forms in 59
+// us, 5.7 TB/s (with every row's amax reduced by itself 83); gathered 74.
 template <bool ROWS>
 __global__ void __launch_bounds__(kColThreads, 3)
     fp8_columns_bf16_kernel(const __nv_bfloat16* __restrict__ x, const int32_t* __restrict__ src,
@@ -584,7 +592,7 @@ __global__ void __launch_bounds__(kColThreads, 3)
 
 // ---------------------------------------------------------------- weights
 // A block takes 128 x 128 of one expert. Bound by HBM: 16 x 1536 x 5120 bf16
-// values in 55 us, 6.9 TB/s.
+// values in 55 us, 6.9 TB/s, fp32 96 us, 6.5 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kColThreads)
     fp8_weights_kernel(const T* __restrict__ W, int K, int N, uint8_t* __restrict__ q,
@@ -646,7 +654,7 @@ __global__ void __launch_bounds__(kColThreads)
 // columns, `pitch` of them to a line. A block takes 128 x 128, a thread 8
 // codes of every 16th row, all loaded before the first is written. Bound by
 // HBM: the same weights back in 57 us, 6.6 TB/s (83 with 8 codes a thread at a
-// time).
+// time), to fp32 120 us, 5.2 TB/s.
 template <typename T>
 __global__ void __launch_bounds__(kColThreads)
     fp8_back_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sc, int rows,
@@ -723,18 +731,21 @@ __global__ void __launch_bounds__(kColThreads)
 // rows' side twice: 1 to 4 % slower.) Eight warps drain: into registers, which
 // frees the accumulator, and then to out.
 //
-// Bound, of many rows: power. 8192 x 8192 x 8192 in short runs 318, 320 and 460
-// us for Y, dX and dW (3.4 PFLOP/s), with operands of zeros or ones, dW in one chain, 276, 269 and
-// 291; after seconds the cap leaves 1350 MHz and 2.9 PFLOP/s. Behind it a pair's
+// Bound, of many rows: power. 8192 x 8192 x 8192 of random numbers takes 317 to
+// 340 us for Y and 335 to 357 for dX, as the power state has it (3.2 to 3.5
+// PFLOP/s), of zeros or ones 276 and 272; after seconds the cap leaves 1350 MHz
+// and 2.9 PFLOP/s. dW, fp32 in chains, 464 to 500 us (2.2 to 2.4 PFLOP/s), of
+// zeros 440: behind power the epilogue's traffic. Behind both a pair's
 // stage: 32 KB into each SM, which at 64 bytes a clock take what its four
-// products take, 512 clocks (with a quarter of the products 267, 232 and 263
-// us). Copies to L2 ahead of the ring: Y 305 -> 354 us. 16384 skewed rows of 32
-// experts, 7168 x 2048: 181 us for 481 GFLOP, nine rounds of tiles of which 6.7
-// are rows that exist (rows as the products' columns, 32 at a time, did away
-// with the others: 184 us, for the loads stay). dW of 16 x 5120 x 1536 from
-// 16384 rows 138 us, 3.6 TB/s written beside its loads; of 64 x 1408 x 2048 from
-// 8191 rows 140 us, 5.3 TB/s. Two rows of 8 experts of 4096 x 11008: 22 us, 7
-// TB/s and 9 us of start and join.
+// products take, 512 clocks (with a quarter of the products, dW in one chain,
+// 267, 232 and 263 us). Copies to L2 ahead of the ring: Y 16 % longer. 16384
+// skewed rows of 32 experts, 7168 x 2048: 181 to 186 us for 481 GFLOP, nine
+// rounds of tiles of which 6.7 are rows that exist (rows as the products'
+// columns, 32 at a time, did away with the others: no faster, for the loads
+// stay). dW of 16 x 5120 x 1536 from 16384 rows 123 us, 4.1 TB/s written beside
+// its loads; of 64 x 1408 x 2048 from 8191 rows 143 us, 5.2 TB/s. Two rows of 8
+// experts of 4096 x 11008: 22 us, 7 TB/s and 9 us of start and join. Y of 16 x
+// 5120 x 1536 from 16384 rows ending in SiLU: bf16 85 -> 89 us, fp32 118 -> 146.
 namespace f8 {
 using namespace ptx;
 constexpr int HN = 128, KS = 128;  // half a tile's columns, a stage's steps
