@@ -602,12 +602,13 @@ MOE_API int moe_fp8_quantize_rows(const moe_fp8_config_t* cfg, int32_t cols, con
  * SiLU with cfg->silu); 1: out[r] = q[r] . wq[e]^T, q of N columns, out [R, K]
  * (the gradient of the product's rows; cfg->silu must be 0:
  * MOE_ERR_UNSUPPORTED), for the rows of each expert e's segment. fp32 sums,
- * rounded to out_dtype; the tensor cores' additions drop what is below the last
- * place, up to 128 of them in a row where out_dtype is fp32 (64 for weight
- * gradients), then rounded to nearest: the norm of the error is up to 64 (32)
- * half steps of fp32 of the sum's, typically 4. Offsets that fall or leave [0, R] write nothing and
- * flag MOE_ERR_BAD_INDEX; rows of no segment are not written. Bitwise
- * reproducible. */
+ * rounded to out_dtype. The tensor cores' additions drop what is below the last
+ * place: up to 128 of them in a row where out_dtype is fp32 (64 for weight
+ * gradients; the whole contraction where it is bf16), the parts then added to
+ * nearest. Of random values, the norm of an fp32 result's error stays below 64
+ * (32) half steps of fp32 of the result's, typically 4. Offsets that fall or
+ * leave [0, R] write nothing and flag MOE_ERR_BAD_INDEX; rows of no segment are
+ * not written. Bitwise reproducible. */
 MOE_API int moe_fp8_product(const moe_fp8_config_t* cfg, int32_t transposed, const uint8_t* q,
                    const uint8_t* scale, const uint8_t* wq, const uint8_t* w_scale,
                    const int32_t* offsets, void* out, void* ws, size_t ws_bytes,
