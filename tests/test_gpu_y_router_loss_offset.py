@@ -42,7 +42,8 @@ def test_the_gradient_of_an_even_load_with_an_offset(cuda_ok):
 
 
 @pytest.mark.parametrize("offset", [1e8, -3e9, 1e12])
-def test_logits_of_any_size(cuda_ok, offset):
+@pytest.mark.parametrize("E", [8, 40, 100, 256])
+def test_logits_of_any_size(cuda_ok, offset, E):
     # steps of 8, 256 and 65536 apart: each token has one expert or some equal ones
-    L, idx = problem(200, 40, 3, seed=9)
+    L, idx = problem(200, E, 3, seed=9)
     check(L * abs(offset) * 2.0 ** -22 + offset, idx, balance=0.7, z=0.0)
